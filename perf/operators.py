@@ -265,7 +265,7 @@ def _plain_attend(s, c):
 
 
 # A row's tokens weigh w = exp((logit - largest) / temperature) in 32 bits, held as whole
-# multiples of 2^-32; all sums and shares of sums are whole numbers, so that no order of
+# multiples of 2^-31; all sums and shares of sums are whole numbers, so that no order of
 # summation changes a draw. The shares are in steps of 2^-24.
 def _share(total, part):
     """floor(total * part), part = n * 2^-24, without leaving 63 bits."""
@@ -280,7 +280,7 @@ def _plain_sample(s, c):
     order = torch.sort(x, dim=1, descending=True, stable=True)
     z = (order.values - order.values[:, :1]) * (1 / torch.where(greedy, 1.0, s["temperature"]))[:, None]
     w = torch.exp(z)
-    n = (w * 2.0 ** 32).long()
+    n = (w * 2.0 ** 31).long()
     rank = torch.arange(V, device=DEV)
     k = torch.where((s["top_k"] <= 0) | (s["top_k"] > V), V, s["top_k"])
     k = torch.where(greedy, 1, k)
@@ -371,11 +371,11 @@ def _exact_sample(s, c):
         order = torch.argsort(x, descending=True, stable=True)
         if one["top_k"][t] > 0:
             order = order[:one["top_k"][t]]
-        n = torch.floor(w[order] * 2 ** 32)
+        n = torch.floor(w[order] * 2 ** 31)
         if one["top_p"][t] < 1:
             order = order[:int((torch.cumsum(n, 0) < one["top_p"][t] * n.sum()).sum()) + 1]
         order = order[w[order] >= one["min_p"][t]].sort().values
-        n = torch.floor(w[order] * 2 ** 32)
+        n = torch.floor(w[order] * 2 ** 31)
         n = n[n > 0]
         i = min(int((torch.cumsum(n, 0) <= one["u"][t] * n.sum()).sum()), len(n) - 1)
         got[t] = torch.log(n[i] / n.sum())
