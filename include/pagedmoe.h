@@ -395,6 +395,131 @@ PMOE_API int moe_decode_forward_noalloc(const void* experts, size_t stride, int 
                                         const int32_t* ids, const float* w, const void* residual, void* y,
                                         int32_t* err_out, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Attention and sampling around the MoE layer. The article's stack leaves attention out
+ * and has no counterpart of these calls; they are what a decode step needs next to it:
+ * append the step's keys and values, attend to the cache, draw the next token.
+ *
+ * They keep no state: the caller owns the cache and every buffer, and a call enqueues its
+ * kernels on `stream` without waiting (all three can be recorded into a CUDA graph).
+ * err_out (device int32, or NULL) has error bits ORed in by the kernels, in stream order;
+ * the caller clears it. */
+
+typedef enum { PMOE_KV_BF16 = 0, PMOE_KV_E4M3 = 1 } pmoe_kv_dtype;
+
+/* A paged K/V cache of one layer: key row `slot` = page * page_size + i of head h lies at
+ * element page * page_stride + (h * page_size + i) * head_dim of k, its value at the same
+ * element of v. */
+typedef struct {
+  void* k;               /* device, 16-byte aligned                                        */
+  void* v;               /* device, 16-byte aligned                                        */
+  int64_t page_stride;   /* elements from page to page (of k and of v): at least           */
+                         /* kv_heads * page_size * head_dim, a multiple of 16 bytes        */
+  const float* k_scale;  /* PMOE_KV_E4M3: device fp32 [kv_heads], key = code * scale       */
+  const float* v_scale;  /* the same for values; both unused for PMOE_KV_BF16              */
+  int32_t num_pages;     /* num_pages * page_size < 2^31                                   */
+  int32_t page_size;     /* 16, 32, 64, 128 or 256                                         */
+  int32_t kv_heads;      /* 1..1024                                                        */
+  int32_t head_dim;      /* 64 or 128                                                      */
+  int32_t dtype;         /* pmoe_kv_dtype                                                  */
+} pmoe_kv_desc;
+
+/*
+ * moe_kv_append - head norm, rotation and append of T tokens.
+ * For each head x of q and k: where its norm weight is given, x <- x * rsqrt(mean(x^2) +
+ * eps) * norm; then each rotated pair (a, b) <- (a cos p - b sin p, b cos p + a sin p) with
+ * p = positions[axis][t] * inv_freq[i]. Pair i of rotary_dim / 2 is (x[i], x[i +
+ * rotary_dim / 2]), or (x[2i], x[2i + 1]) when interleaved != 0; elements from rotary_dim on
+ * are not rotated. The rotated q goes to q_out, the rotated k and v as it is to cache row
+ * slots[t]. fp32 throughout, one rounding (e4m3: of value / scale, to nearest even,
+ * saturating at 448).
+ *   q, k, v    device bf16 [T][q_heads | kv_heads | kv_heads][head_dim], tokens q_stride,
+ *              k_stride, v_stride elements apart (views of one projection's output), heads
+ *              contiguous; 16-byte aligned, strides multiples of 8
+ *   positions  device int32 [axes][T] (several axes: time, height, width of image and
+ *              video tokens); pair_axis device int32 [rotary_dim / 2], the axis of each
+ *              pair, or NULL for axis 0 (required when axes > 1). An axis outside
+ *              [0, axes) counts as 0 and sets error bit 32
+ *   inv_freq   device fp32 [rotary_dim / 2]; rotary_dim a multiple of 16, 0..head_dim
+ *   q_norm, k_norm  device bf16 [head_dim], 16-byte aligned, or NULL
+ *   slots      device int32 [T]; -1: the token's k and v are not stored. Any other slot
+ *              outside the cache is skipped and sets error bit 4. Two tokens of one call
+ *              must not share a slot
+ *   q_out      device bf16 [T][q_heads][head_dim], 16-byte aligned, not overlapping q, k, v
+ * T = 0 enqueues nothing. Axes 1..8, q_heads 1..1024. Returns PMOE_EINVAL on bad arguments,
+ * PMOE_EUNSUPPORTED for another page size, head size or cache type.
+ */
+PMOE_API int moe_kv_append(const pmoe_kv_desc* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, int T, int q_heads, const int32_t* positions, int axes,
+                           const int32_t* pair_axis, const float* inv_freq, int rotary_dim, int interleaved,
+                           const void* q_norm, const void* k_norm, float eps, const int32_t* slots, void* q_out,
+                           int32_t* err_out, void* stream);
+
+/*
+ * moe_prefix_attention - attention of T query rows over a paged cache, for a batch whose
+ * sequences share their first prefix_len tokens: the prefix's keys and values are read once
+ * for all rows, each row's own keys after it.
+ * Row t sees the first prefix_len rows of prefix_pages, then the first suffix_len[t] rows of
+ * the pages page_table[row_seq[t]][..]. For query head h (kv head h / (q_heads /
+ * kv_heads)): out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j, lse[t][h] = log sum_j
+ * exp(scale * q[t][h] . k_j). A row that sees no key gets out = 0, lse = -inf. What the cache
+ * holds in rows that a query does not see is never used, whatever it is.
+ * Statistics and sums are fp32; the weights are rounded to 16 bits before they meet the
+ * values (bf16, or fp16 with an e4m3 cache).
+ *   q            device bf16 [T][q_heads][head_dim], tokens q_stride elements apart; 16-byte
+ *                aligned, q_stride a multiple of 8
+ *   prefix_pages device int32 [ceil(prefix_len / page_size)] (NULL when prefix_len = 0)
+ *   page_table   device int32 [sequences][table_stride], at least ceil(max_suffix /
+ *                page_size) entries a row (NULL when max_suffix = 0)
+ *   row_seq      device int32 [T], the table row of each query row, in [0, sequences), or
+ *                NULL: row t. Several query rows may share one
+ *   suffix_len   device int32 [T], each 0..max_suffix (a length outside counts as the
+ *                nearer bound and sets error bit 128; NULL when max_suffix = 0)
+ *   out          device bf16 [T][q_heads][head_dim], 16-byte aligned
+ *   lse          device fp32 [T][q_heads], or NULL
+ *   scratch      device, 16-byte aligned, moe_prefix_attention_scratch_bytes(...) bytes
+ * A page outside [0, num_pages) or a row_seq outside [0, sequences) sets error bit 64; such
+ * keys read as zeros. Error bit 16: a bounded wait expired, outputs are undefined.
+ * T = 0 enqueues nothing. q_heads a multiple of kv_heads, at most 64 query heads to a kv
+ * head (else PMOE_EUNSUPPORTED), T * q_heads < 2^24. PMOE_EINVAL on bad arguments.
+ */
+PMOE_API int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64_t q_stride, int T, int q_heads,
+                                  float scale, const int32_t* prefix_pages, int prefix_len, const int32_t* page_table,
+                                  int table_stride, int sequences, const int32_t* row_seq, const int32_t* suffix_len,
+                                  int max_suffix, void* out, float* lse, void* scratch, size_t scratch_bytes,
+                                  int32_t* err_out, void* stream);
+/* Bytes of scratch moe_prefix_attention needs on the current device (0 for bad arguments). */
+PMOE_API size_t moe_prefix_attention_scratch_bytes(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len,
+                                                   int max_suffix);
+
+/*
+ * moe_sample_tokens - draw one token id per row of logits, from given random numbers.
+ * With m the row's largest logit, token i weighs n_i = floor(exp((x_i - m) / temperature) *
+ * 2^31), exp and its argument in fp32 ((x_i - m) * (1 / temperature)); from there on every
+ * sum and comparison is in whole numbers, so a draw depends on no order of summation. The
+ * tokens in descending order of their logits, ties to the lower id, are cut to
+ *   the first top_k                                          (top_k <= 0 or >= V: all),
+ *   of these the shortest head whose weights reach floor(total * top_p)   (top_p >= 1: all;
+ *   at least one token), and
+ *   of these the ones with exp(..) >= min_p                   (min_p <= 0: all).
+ * The draw is the first id, ascending, at which the running sum of the kept weights exceeds
+ * floor(S * u), S their sum. top_p and u count in steps of 2^-24. A token below 2^-31 of
+ * the most likely one has weight 0 and is never drawn. temperature <= 0: the largest logit,
+ * lowest id first. NaN logits count as -inf; a row without a logit above -inf gives id -1.
+ * With +inf logits, those share the row.
+ *   logits   device, fp32 (is_bf16 = 0) or bf16 (is_bf16 != 0) [T][V], rows row_stride
+ *            elements apart; aligned to its element
+ *   u        device fp32 [T], in [0, 1)
+ *   temperature, top_p, min_p  device fp32 [T], top_k device int32 [T]; NULL: 1, 1, 0, 0
+ *   ids_out  device int32 [T]
+ *   logprob_out  device fp32 [T], log(n_id / S) (0 for temperature <= 0, -inf for id -1),
+ *            or NULL
+ * V in 1..262144. T = 0 enqueues nothing. PMOE_EINVAL on bad arguments.
+ */
+PMOE_API int moe_sample_tokens(const void* logits, int is_bf16, int T, int V, int64_t row_stride,
+                               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                               const float* u, int32_t* ids_out, float* logprob_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,9 +20,11 @@ Modules
   permute    token->expert histogram, exclusive scan and stable grouping
   lru        brute-force per-layer K-slot LRU / wave simulator
   preflight  the article's sizing arithmetic (slot cost, batch cap, miss bounds)
+  attention  head norm, rotation, cache append and attention over a paged cache
+  sampling   the draw of a token with temperature, top-k, top-p and min-p
 
 Every function names the passage it follows. Points where the pages are silent
 are stated in the docstrings of the functions that take a reading.
 """
 
-from . import router, formats, moe, permute, lru, preflight  # noqa: F401
+from . import router, formats, moe, permute, lru, preflight, attention, sampling  # noqa: F401

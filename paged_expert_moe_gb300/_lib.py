@@ -18,6 +18,7 @@ PMOE_OK, PMOE_EINVAL, PMOE_ENOMEM, PMOE_EHOSTALLOC, PMOE_ECUDA, PMOE_EUNSUPPORTE
     0, -1, -2, -3, -4, -5, -6, -7
 PMOE_BF16, PMOE_FP8_BLOCK128, PMOE_INT4_GPTQ_G128, PMOE_MXFP4, PMOE_NVFP4 = 0, 1, 2, 3, 4
 PMOE_PAGEIN_COPY_ENGINE, PMOE_PAGEIN_SM_PULL = 0, 1
+PMOE_KV_BF16, PMOE_KV_E4M3 = 0, 1
 
 
 class PmoeError(RuntimeError):
@@ -35,6 +36,12 @@ class pmoe_cache_desc(ctypes.Structure):
         "max_tokens", "pagein_mode", "device")]
 
 
+class pmoe_kv_desc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "dtype")]
+
+
 class pmoe_stats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in ("steps", "hits", "misses", "waves", "bytes_paged")]
 
@@ -49,6 +56,7 @@ _LIB = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SIGS = {
     "pmoe_version": ([], _I),
     "pmoe_status_string": ([_I], ctypes.c_char_p),
@@ -73,6 +81,12 @@ _SIGS = {
     "expert_cache_kernel_times": ([_P, ctypes.POINTER(pmoe_kernel_times)], _I),
     "moe_decode_forward_noalloc": ([_P, ctypes.c_size_t, _I, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P,
                                     _P], _I),
+    "moe_kv_append": ([ctypes.POINTER(pmoe_kv_desc), _P, _L, _P, _L, _P, _L, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P,
+                       ctypes.c_float, _P, _P, _P, _P], _I),
+    "moe_prefix_attention": ([ctypes.POINTER(pmoe_kv_desc), _P, _L, _I, _I, ctypes.c_float, _P, _I, _P, _I, _I, _P, _P,
+                              _I, _P, _P, _P, ctypes.c_size_t, _P, _P], _I),
+    "moe_prefix_attention_scratch_bytes": ([ctypes.POINTER(pmoe_kv_desc), _I, _I, _I, _I], ctypes.c_size_t),
+    "moe_sample_tokens": ([_P, _I, _I, _I, _L, _P, _P, _P, _P, _P, _P, _P, _P], _I),
     "moe_paged_stack_forward": ([_P, _P, _I, _P, _P, _P, _P, _P], _I),
 }
 EXPORTED = tuple(_SIGS)
@@ -200,6 +214,143 @@ def moe_decode_forward_noalloc(experts, stride, E, top_k, H, I, fmt, x, ids, w, 
                                              _ptr(x), T, _ptr(ids), _ptr(w), _ptr(residual), _ptr(y), _ptr(err_out),
                                              _stream_handle(stream)), "moe_decode_forward_noalloc")
     return y
+
+
+def _kv_desc(k_cache, v_cache, k_scale, v_scale):
+    """pmoe_kv_desc of a paged cache: CUDA bf16 or float8_e4m3fn [num_pages, kv_heads,
+    page_size, head_dim] tensors of the same strides, contiguous but for the page stride."""
+    import torch
+    pages, heads, page, dim = k_cache.shape
+    assert k_cache.is_cuda and v_cache.is_cuda and k_cache.dtype == v_cache.dtype and v_cache.shape == k_cache.shape
+    stride = k_cache.stride()
+    assert stride == v_cache.stride() and stride[1:] == (page * dim, dim, 1)
+    if k_cache.dtype == torch.float8_e4m3fn:
+        dtype = PMOE_KV_E4M3
+        assert k_scale.dtype == v_scale.dtype == torch.float32 and k_scale.is_cuda and v_scale.is_cuda
+        assert k_scale.is_contiguous() and v_scale.is_contiguous() and k_scale.numel() == v_scale.numel() == heads
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    else:
+        dtype, ks, vs = PMOE_KV_BF16, None, None
+        assert k_cache.dtype == torch.bfloat16
+    return pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride[0], ks, vs, pages, page, heads, dim, dtype)
+
+
+def _heads_ok(x, T, dim):
+    """x [T, heads, dim] bf16 with contiguous heads; its token stride is free."""
+    import torch
+    return x.is_cuda and x.dtype == torch.bfloat16 and x.shape[0] == T and x.shape[2] == dim and \
+        x.stride(2) == 1 and (x.stride(1) == dim or x.shape[1] == 1)
+
+
+def _vec_ok(x, dtype, n):
+    return x is None or (x.is_cuda and x.dtype == dtype and x.is_contiguous() and x.numel() == n)
+
+
+def _empty(shape, dtype, like, stream):
+    """A new tensor on the device of `like`, owned by `stream` (None: the current one)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _token_stride(x):
+    """Elements from token to token of x [T, heads, dim] (one token has no stride of its own)."""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def moe_kv_append(k_cache, v_cache, q, k, v, positions, slots, inv_freq, pair_axis=None, interleaved=False, q_norm=None,
+                  k_norm=None, eps=1e-6, k_scale=None, v_scale=None, q_out=None, err_out=None, stream=None):
+    """Head norm, rotation and append of T tokens' keys and values to a paged cache.
+    k_cache, v_cache: bf16 or float8_e4m3fn [num_pages, kv_heads, page_size, head_dim];
+    q: bf16 [T, q_heads, head_dim], k, v: bf16 [T, kv_heads, head_dim] (views of one
+    projection will do); positions: int32 [axes, T] or [T]; slots: int32 [T], page *
+    page_size + row, -1 = not stored; inv_freq: fp32 [rotary_dim / 2] or None; pair_axis:
+    int32 [rotary_dim / 2]; q_norm, k_norm: bf16 [head_dim]. Returns the rotated q (q_out)."""
+    import torch
+    T, q_heads, dim = q.shape
+    desc = _kv_desc(k_cache, v_cache, k_scale, v_scale)
+    axes = positions.shape[0] if positions is not None and positions.dim() == 2 else 1
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    assert dim == desc.head_dim and k.shape[1] == v.shape[1] == desc.kv_heads
+    assert _heads_ok(q, T, dim) and _heads_ok(k, T, dim) and _heads_ok(v, T, dim)
+    assert _vec_ok(positions, torch.int32, axes * T) and _vec_ok(slots, torch.int32, T)
+    assert _vec_ok(inv_freq, torch.float32, rot // 2) and _vec_ok(pair_axis, torch.int32, rot // 2)
+    assert _vec_ok(q_norm, torch.bfloat16, dim) and _vec_ok(k_norm, torch.bfloat16, dim)
+    assert _vec_ok(err_out, torch.int32, 1)
+    if q_out is None:
+        q_out = _empty((T, q_heads, dim), torch.bfloat16, q, stream)
+    assert _vec_ok(q_out, torch.bfloat16, T * q_heads * dim)
+    _check(load().moe_kv_append(desc, _ptr(q), _token_stride(q), _ptr(k), _token_stride(k), _ptr(v), _token_stride(v),
+                                T, q_heads, _ptr(positions), axes, _ptr(pair_axis), _ptr(inv_freq), rot,
+                                1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), eps, _ptr(slots), _ptr(q_out),
+                                _ptr(err_out), _stream_handle(stream)), "moe_kv_append")
+    return q_out
+
+
+def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len, max_suffix, k_scale=None, v_scale=None):
+    """Bytes of scratch a moe_prefix_attention call of these sizes needs."""
+    return int(load().moe_prefix_attention_scratch_bytes(_kv_desc(k_cache, v_cache, k_scale, v_scale), T, q_heads,
+                                                         prefix_len, max_suffix))
+
+
+def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_table, suffix_len, max_suffix, scale=None,
+                         row_seq=None, k_scale=None, v_scale=None, out=None, lse_out=None, scratch=None, err_out=None,
+                         stream=None):
+    """Attention of q (bf16 [T, q_heads, head_dim]) over a paged cache (as moe_kv_append's).
+    Row t sees the first prefix_len keys of prefix_pages (int32), which all rows share, then
+    the first suffix_len[t] (int32 [T], at most max_suffix) of page_table[row_seq[t]] (int32
+    [sequences, pages]; row_seq int32 [T], default t). scale defaults to head_dim ** -0.5.
+    lse_out: fp32 [T, q_heads] or None; scratch: uint8, allocated here when not given.
+    Returns out (bf16 [T, q_heads, head_dim])."""
+    import torch
+    T, q_heads, dim = q.shape
+    desc = _kv_desc(k_cache, v_cache, k_scale, v_scale)
+    page = desc.page_size
+    assert dim == desc.head_dim and _heads_ok(q, T, dim)
+    assert prefix_len <= 0 or (_vec_ok(prefix_pages, torch.int32, prefix_pages.numel()) and
+                               prefix_pages.numel() * page >= prefix_len)
+    sequences = width = 0
+    if max_suffix > 0:
+        sequences, width = page_table.shape
+        assert _vec_ok(page_table, torch.int32, sequences * width) and _vec_ok(suffix_len, torch.int32, T)
+    assert _vec_ok(row_seq, torch.int32, T) and _vec_ok(lse_out, torch.float32, T * q_heads)
+    assert _vec_ok(err_out, torch.int32, 1)
+    lib = load()
+    if out is None:
+        out = _empty((T, q_heads, dim), torch.bfloat16, q, stream)
+    assert _vec_ok(out, torch.bfloat16, T * q_heads * dim)
+    if scratch is None:
+        nbytes = lib.moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix)
+        scratch = _empty(nbytes, torch.uint8, q, stream)
+    assert scratch.is_cuda and scratch.dtype == torch.uint8 and scratch.is_contiguous()
+    _check(lib.moe_prefix_attention(desc, _ptr(q), _token_stride(q), T, q_heads, dim ** -0.5 if scale is None else scale,
+                                    _ptr(prefix_pages), prefix_len, _ptr(page_table), width, sequences, _ptr(row_seq),
+                                    _ptr(suffix_len), max_suffix, _ptr(out), _ptr(lse_out), _ptr(scratch),
+                                    scratch.numel(), _ptr(err_out), _stream_handle(stream)), "moe_prefix_attention")
+    return out
+
+
+def moe_sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, ids_out=None, logprob_out=None,
+                      stream=None):
+    """Draw one token id per row of logits (CUDA fp32 or bf16 [T, V], rows contiguous) from
+    u (fp32 [T], in [0, 1)). temperature, top_p, min_p: fp32 [T], top_k: int32 [T], or None
+    (1, 1, 0 and 0: no cut); temperature 0 takes the largest logit. logprob_out: fp32 [T],
+    the drawn token's log probability among the kept ones. Returns ids (int32 [T])."""
+    import torch
+    T, V = logits.shape
+    assert logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16) and (V == 1 or logits.stride(1) == 1)
+    assert u is not None and _vec_ok(u, torch.float32, T) and _vec_ok(temperature, torch.float32, T)
+    assert _vec_ok(top_k, torch.int32, T) and _vec_ok(top_p, torch.float32, T) and _vec_ok(min_p, torch.float32, T)
+    if ids_out is None:
+        ids_out = _empty(T, torch.int32, logits, stream)
+    assert _vec_ok(ids_out, torch.int32, T) and _vec_ok(logprob_out, torch.float32, T)
+    _check(load().moe_sample_tokens(_ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0, T, V,
+                                    logits.stride(0) if T > 1 else V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                                    _ptr(min_p), _ptr(u), _ptr(ids_out), _ptr(logprob_out), _stream_handle(stream)),
+           "moe_sample_tokens")
+    return ids_out
 
 
 class ExpertCache:

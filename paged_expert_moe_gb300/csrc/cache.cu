@@ -286,6 +286,15 @@ int max_waves(const pmoe_cache* c, int n_ids) {
 
 }  // namespace
 
+namespace pmoe {
+int cuda_status(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return PMOE_OK;
+  set_cuda_error(e, what);
+  return PMOE_ECUDA;
+}
+int launch_status(const char* what) { return cuda_status(cudaGetLastError(), what); }
+}  // namespace pmoe
+
 extern "C" {
 
 int pmoe_version(void) { return 100; }

@@ -1,0 +1,269 @@
+// moe_kv_append: head norm, rotary positions and the append to a paged cache, in one pass.
+//
+// For token t and head h of q and k (x the head's D values):
+//   x <- x * rsqrt(mean(x^2) + eps) * norm_w            (where a norm weight is given)
+//   (a, b) <- (a cos - b sin, b cos + a sin)             for each of the R/2 rotated pairs,
+//   angle_i = positions[axis(i)][t] * inv_freq[i]
+// then q -> q_out (bf16) and k, v -> the cache row that slots[t] names (bf16, or e4m3 of
+// x / scale[kv head]). All of it is fp32 with one rounding at the end.
+//
+// The angle keeps the rounding error of its product (one fma), since at position 10^5 that
+// error alone would be up to 4e-3 rad, more than a bf16 output's own rounding; the sine and
+// cosine of the rounded angle are corrected by it to second order.
+//
+// Bound: HBM (every input read once, every output written once); one token is launch
+// latency. A block takes a few tokens, computes their sines and cosines once into shared
+// memory while the first heads' values are in flight, and gives each head D/16 threads of
+// 16 elements, arranged so that a thread holds both halves of its 8 pairs: no exchange
+// between threads but the norm's sum.
+#include "pmoe_internal.h"
+
+#include <cuda_fp8.h>
+#include <math.h>
+
+namespace pmoe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTok = 4;     // tokens of a block
+constexpr int kMaxPairs = 64;  // R / 2 <= D / 2
+
+struct AppendArgs {
+  pmoe_kv_desc kv;
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  int T, q_heads;
+  const int32_t* positions;
+  int axes;
+  const int32_t* pair_axis;
+  const float* inv_freq;
+  int rot, interleaved;
+  const __nv_bfloat16 *q_norm, *k_norm;
+  float eps;
+  const int32_t* slots;
+  __nv_bfloat16* q_out;
+  int32_t* err;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 values as e4m3 of f / s: round to nearest even, saturating at +-448 (NaN stays NaN)
+__device__ __forceinline__ uint2 pack8_e4m3(const float* f, float s) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] / s, f[4 * i + 1] / s), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi =
+        __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] / s, f[4 * i + 3] / s), __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | (hi << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a, int tok) {
+  constexpr int LPH = D / 16;              // threads of a head
+  constexpr int UNITS = kThreads / LPH;    // heads at once
+  __shared__ __align__(16) float cs[kMaxTok][2][kMaxPairs];
+  const int t0 = blockIdx.x * tok;
+  const int nt = min(tok, a.T - t0);
+  const int hk = a.kv.kv_heads, heads = a.q_heads + 2 * hk;
+  const int j = threadIdx.x % LPH;
+  // the two 8-element runs of this thread: for half-split pairs one in each half of the
+  // rotated part, else the 16 elements from 16 j on
+  const int half = a.rot >> 1;
+  const bool split = !a.interleaved && j * 16 < a.rot;
+  const int e0 = split ? j * 8 : j * 16, e1 = split ? half + j * 8 : j * 16 + 8;
+  const bool turn = j * 16 < a.rot;
+
+  uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+  auto load = [&](int u) {
+    const int t = t0 + u / heads, h = u % heads;
+    const __nv_bfloat16* p = h < a.q_heads      ? a.q + t * a.q_stride + h * D
+                             : h < a.q_heads + hk ? a.k + t * a.k_stride + (h - a.q_heads) * D
+                                                  : a.v + t * a.v_stride + (h - a.q_heads - hk) * D;
+    x0 = __ldg(reinterpret_cast<const uint4*>(p + e0));
+    x1 = __ldg(reinterpret_cast<const uint4*>(p + e1));
+  };
+  const int total = nt * heads;
+  int u = threadIdx.x / LPH;
+  if (u < total) load(u);
+
+  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+    const int tt = i / half, pr = i - tt * half;
+    int ax = 0;
+    if (a.pair_axis != nullptr) {
+      ax = a.pair_axis[pr];
+      if ((unsigned)ax >= (unsigned)a.axes) {
+        if (a.err != nullptr) atomicOr(a.err, kErrBadAxis);
+        ax = 0;
+      }
+    }
+    const float p = (float)a.positions[(size_t)ax * a.T + t0 + tt], f = a.inv_freq[pr];
+    const float hi = p * f, lo = fmaf(p, f, -hi);
+    float s, c;
+    sincosf(hi, &s, &c);
+    const float l2 = 0.5f * lo * lo;
+    cs[tt][0][pr] = c - lo * s - l2 * c;
+    cs[tt][1][pr] = s + lo * c - l2 * s;
+  }
+  __syncthreads();
+
+  // The loop count is the same for all threads of a warp: the norm's shuffles need them.
+  for (int base = 0; base < total; base += UNITS) {
+    const bool live = u < total;
+    const int tt = live ? u / heads : 0, t = t0 + tt, h = live ? u % heads : 0;
+    float f[16];
+    unpack8(x0, f);
+    unpack8(x1, f + 8);
+    const bool is_q = h < a.q_heads, is_k = !is_q && h < a.q_heads + hk;
+    const __nv_bfloat16* nw = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
+    if (a.q_norm != nullptr || a.k_norm != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (nw != nullptr) {
+        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+        float w[16];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(nw + e0)), w);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(nw + e1)), w + 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = f[i] * r * w[i];
+      }
+    }
+    if (turn && (is_q || is_k)) {
+      const float* c = &cs[tt][0][j * 8];
+      const float* s = &cs[tt][1][j * 8];
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = f[2 * i], y = f[2 * i + 1];
+          f[2 * i] = x * c[i] - y * s[i];
+          f[2 * i + 1] = y * c[i] + x * s[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = f[i], y = f[i + 8];
+          f[i] = x * c[i] - y * s[i];
+          f[i + 8] = y * c[i] + x * s[i];
+        }
+      }
+    }
+    // the next unit's loads go out before this one's stores
+    const int un = u + UNITS;
+    const bool more = un < total;
+    if (more) load(un);
+    if (live && is_q) {
+      __nv_bfloat16* p = a.q_out + ((size_t)t * a.q_heads + h) * D;
+      *reinterpret_cast<uint4*>(p + e0) = pack8(f);
+      *reinterpret_cast<uint4*>(p + e1) = pack8(f + 8);
+    } else if (live) {
+      const int kh = h - a.q_heads - (is_k ? 0 : hk);
+      const int slot = a.slots[t];
+      const int page = slot / a.kv.page_size;
+      if (slot >= 0 && page < a.kv.num_pages) {
+        const size_t row = (size_t)page * a.kv.page_stride +
+                           ((size_t)kh * a.kv.page_size + (slot - page * a.kv.page_size)) * D;
+        void* cache = is_k ? a.kv.k : a.kv.v;
+        if (a.kv.dtype == PMOE_KV_BF16) {
+          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(cache) + row;
+          *reinterpret_cast<uint4*>(p + e0) = pack8(f);
+          *reinterpret_cast<uint4*>(p + e1) = pack8(f + 8);
+        } else {
+          uint8_t* p = static_cast<uint8_t*>(cache) + row;
+          const float sc = (is_k ? a.kv.k_scale : a.kv.v_scale)[kh];
+          *reinterpret_cast<uint2*>(p + e0) = pack8_e4m3(f, sc);
+          *reinterpret_cast<uint2*>(p + e1) = pack8_e4m3(f + 8, sc);
+        }
+      } else if (slot != -1 && j == 0 && a.err != nullptr) {
+        atomicOr(a.err, kErrBadSlot);
+      }
+    }
+    u = un;
+  }
+}
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace
+
+int check_kv(const pmoe_kv_desc* kv) {
+  if (kv == nullptr || kv->k == nullptr || kv->v == nullptr) return PMOE_EINVAL;
+  if (kv->dtype != PMOE_KV_BF16 && kv->dtype != PMOE_KV_E4M3) return PMOE_EUNSUPPORTED;
+  if (kv->head_dim != 64 && kv->head_dim != 128) return PMOE_EUNSUPPORTED;
+  if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1)) != 0) return PMOE_EUNSUPPORTED;
+  if (kv->num_pages < 1 || kv->kv_heads < 1 || kv->kv_heads > 1024) return PMOE_EINVAL;
+  if ((int64_t)kv->num_pages * kv->page_size > INT32_MAX) return PMOE_EINVAL;
+  if (kv->dtype == PMOE_KV_E4M3 && (kv->k_scale == nullptr || kv->v_scale == nullptr || !aligned(kv->k_scale, 4) ||
+                                    !aligned(kv->v_scale, 4)))
+    return PMOE_EINVAL;
+  const int64_t eb = kv->dtype == PMOE_KV_BF16 ? 2 : 1;
+  if (kv->page_stride < (int64_t)kv->kv_heads * kv->page_size * kv->head_dim || kv->page_stride * eb % 16 != 0)
+    return PMOE_EINVAL;
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return PMOE_EINVAL;
+  return PMOE_OK;
+}
+
+}  // namespace pmoe
+
+using namespace pmoe;
+
+extern "C" int moe_kv_append(const pmoe_kv_desc* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, int T, int q_heads, const int32_t* positions, int axes,
+                             const int32_t* pair_axis, const float* inv_freq, int rotary_dim, int interleaved,
+                             const void* q_norm, const void* k_norm, float eps, const int32_t* slots, void* q_out,
+                             int32_t* err_out, void* stream) {
+  const int r = check_kv(kv);
+  if (r != PMOE_OK) return r;
+  const int D = kv->head_dim, hk = kv->kv_heads;
+  if (T < 0 || q_heads < 1 || q_heads > 1024) return PMOE_EINVAL;
+  if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16 != 0) return PMOE_EINVAL;
+  if (axes < 1 || axes > 8 || (axes > 1 && rotary_dim > 0 && pair_axis == nullptr)) return PMOE_EINVAL;
+  if (!(eps >= 0.f)) return PMOE_EINVAL;
+  if (q_stride < (int64_t)q_heads * D || k_stride < (int64_t)hk * D || v_stride < (int64_t)hk * D) return PMOE_EINVAL;
+  if (T == 0) return PMOE_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || slots == nullptr || q_out == nullptr ||
+      q == q_out)
+    return PMOE_EINVAL;
+  if (rotary_dim > 0 && (positions == nullptr || inv_freq == nullptr)) return PMOE_EINVAL;
+  // heads move in 16-byte vectors
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || q_stride % 8 != 0 ||
+      k_stride % 8 != 0 || v_stride % 8 != 0 || (q_norm != nullptr && !aligned(q_norm, 16)) ||
+      (k_norm != nullptr && !aligned(k_norm, 16)))
+    return PMOE_EINVAL;
+  if (!aligned(positions, 4) || !aligned(pair_axis, 4) || !aligned(inv_freq, 4) || !aligned(slots, 4) ||
+      !aligned(err_out, 4))
+    return PMOE_EINVAL;
+  const AppendArgs a{*kv,       static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                     static_cast<const __nv_bfloat16*>(v), q_stride, k_stride, v_stride, T, q_heads, positions, axes,
+                     pair_axis, inv_freq, rotary_dim, interleaved != 0, static_cast<const __nv_bfloat16*>(q_norm),
+                     static_cast<const __nv_bfloat16*>(k_norm), eps, slots, static_cast<__nv_bfloat16*>(q_out), err_out};
+  const int tok = T >= 2048 ? 2 : 1;
+  const int blocks = (T + tok - 1) / tok;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (D == 128)
+    kv_append_kernel<128><<<blocks, kThreads, 0, s>>>(a, tok);
+  else
+    kv_append_kernel<64><<<blocks, kThreads, 0, s>>>(a, tok);
+  return launch_status("moe_kv_append");
+}

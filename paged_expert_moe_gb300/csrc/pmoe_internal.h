@@ -25,7 +25,9 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Device error word bits.
-enum : int32_t { kErrBadExpertId = 1, kErrPlanOverflow = 2, kErrBadSlot = 4, kErrPullTimeout = 8 };
+// (16: a bounded wait of a tensor-core kernel expired)
+enum : int32_t { kErrBadExpertId = 1, kErrPlanOverflow = 2, kErrBadSlot = 4, kErrPullTimeout = 8, kErrTcWait = 16,
+                 kErrBadAxis = 32, kErrBadPage = 64, kErrBadLength = 128 };
 
 // Layout of a layer's residency plan (int32 words), written by the residency kernel
 // and mirrored to pinned host memory in copy-engine mode.
@@ -151,5 +153,11 @@ struct ExpertLayout {
   size_t gu_w, d_w, gu_s, d_s, bytes;
 };
 ExpertLayout expert_layout(int fmt, int H, int I);
+
+// PMOE_OK, or PMOE_ECUDA with the launch's error text kept for pmoe_last_error.
+int launch_status(const char* what);
+int cuda_status(cudaError_t e, const char* what);
+// A cache descriptor's checks (PMOE_OK, PMOE_EINVAL or PMOE_EUNSUPPORTED).
+int check_kv(const pmoe_kv_desc* kv);
 
 }  // namespace pmoe
