@@ -3,6 +3,8 @@
 
 #include "pmoe_internal.h"
 
+#include <cuda_fp16.h>
+
 namespace pmoe {
 namespace attn {
 
@@ -32,7 +34,58 @@ struct Args {
   int prefix_parts, prefix_chunk;  // keys per prefix part (a multiple of 64)
   int suffix_parts, suffix_chunk;
   int row_tiles;    // row tiles of the prefix
+  // The tensor-core prefix kernel (tc_ctas > 0): units of one 128-key tile for one (256-row
+  // tile, kv head) group, tc_tiles units to a group, in group order; CTA c takes units
+  // [c * U / tc_ctas, (c + 1) * U / tc_ctas). A group's parts are numbered from its first CTA.
+  int tc_ctas, tc_tiles;
 };
+
+constexpr int kTcRows = 256;  // query rows of a group
+constexpr int kTcKeys = 128;  // keys of a tile
+
+__host__ __device__ inline int64_t tc_units(const Args& a) { return (int64_t)a.row_tiles * a.kv.kv_heads * a.tc_tiles; }
+// the CTA that takes unit u: the largest c with c * U / C <= u
+__host__ __device__ inline int tc_cta_of(int64_t u, int64_t units, int ctas) { return (int)(((u + 1) * ctas - 1) / units); }
+// prefix parts of query row r (of T * group) and kv head h
+__host__ __device__ inline int tc_parts(const Args& a, int r, int h) {
+  const int64_t units = tc_units(a), u = ((int64_t)(r / kTcRows) * a.kv.kv_heads + h) * a.tc_tiles;
+  return tc_cta_of(u + a.tc_tiles - 1, units, a.tc_ctas) - tc_cta_of(u, units, a.tc_ctas) + 1;
+}
+
+void plan_prefix_tc(Args* a, int sms);
+int launch_prefix_tc(const Args& a, cudaStream_t s);
+
+constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+// two e4m3 codes (low 16 bits) -> fp16 pair, exact
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)v));
+  return r;
+}
+// The power of two a query row is divided by on its way to fp16: that of its largest
+// element. What lies within 2^-14 of that one is exact. Zero, infinite and NaN rows: 2^0.
+__device__ __forceinline__ int row_exponent(float largest) {
+  const int e = (int)(__float_as_uint(largest) >> 23) - 127;
+  return e < -126 || e > 127 ? 0 : min(e, 126);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 __device__ __forceinline__ int suffix_keys(const Args& a, int t) {
   if (a.max_suffix == 0) return 0;

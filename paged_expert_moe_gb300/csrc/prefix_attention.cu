@@ -13,7 +13,6 @@ constexpr int kTile = 64;       // keys of a tile
 constexpr int kStages = 3;
 constexpr int kThreads = 128;
 constexpr int kMaxChunk = 4096; // keys of a part: its page ids lie in shared memory
-constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -49,28 +48,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-// two e4m3 codes (low 16 bits) -> fp16 pair, exact
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t v) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)v));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Where 16-byte chunk c of key row r lies in a tile, so that the 8 rows (or the 2 rows x 4
@@ -143,7 +120,7 @@ __device__ void stream_part(const Args& a, uint8_t* smem, const int32_t* pages, 
     } else {
       // Slots of step k = 4 i + s hold elements 64 i + 16 c + 4 s + .. (the order in which a
       // thread reads 16 key bytes at once). q goes to fp16 divided by the power of two of
-      // its row's largest element: exact but for what lies 2^-14 below that.
+      // its row's largest element.
       uint2 raw[2][D / 16];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -159,10 +136,9 @@ __device__ void stream_part(const Args& a, uint8_t* smem, const int32_t* pages, 
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int ex = (int)(__float_as_uint(mx) >> 23) - 127;
-        ex = ex < -126 || ex > 127 ? 0 : min(ex, 126);  // zero, infinite or NaN rows as they are
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-        qmul[e] = a.scale * a.kv.k_scale[h] * up;
+        const int ex = row_exponent(mx);
+        const float down = pow2(-ex);
+        qmul[e] = a.scale * a.kv.k_scale[h] * pow2(ex);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t w[2] = {raw[e][k].x, raw[e][k].y};
@@ -385,10 +361,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const Args a) {
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (i >= rh) return;
   const int lane = threadIdx.x & 31;
-  const int n = suffix_keys(a, (int)(i / a.q_heads));
-  const int parts = a.prefix_parts + (n + a.suffix_chunk - 1) / a.suffix_chunk;
+  const int t = (int)(i / a.q_heads), hq = (int)(i % a.q_heads);
+  const int n = suffix_keys(a, t);
+  // the row's prefix parts, then (from part prefix_parts on) its suffix parts
+  const int pre = a.tc_ctas > 0 ? tc_parts(a, t * a.group + hq % a.group, hq / a.group) : a.prefix_parts;
+  const int parts = pre + (n + a.suffix_chunk - 1) / a.suffix_chunk;
+  const int skip = a.prefix_parts - pre;
+  auto slot = [&](int p) { return (int64_t)(p < pre ? p : p + skip) * rh + i; };
   float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.ml_part[p * rh + i].x);
+  for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.ml_part[slot(p)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float base = m == -INFINITY ? 0.f : m;
@@ -396,11 +377,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const Args a) {
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) acc[d] = 0.f;
   for (int p = 0; p < parts; ++p) {
-    const float2 ml = a.ml_part[p * rh + i];
+    const int64_t at = slot(p);
+    const float2 ml = a.ml_part[at];
     const float f = ex2(ml.x - base);
     l = fmaf(ml.y, f, l);
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(a.o_part[(p * rh + i) * D + d * 32 + lane], f, acc[d]);
+    for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(a.o_part[at * D + d * 32 + lane], f, acc[d]);
   }
   const float inv = parts == 0 ? 0.f : 1.f / l;
 #pragma unroll
@@ -430,8 +412,13 @@ void plan_parts(Args* a, int wm, int sms) {
     *chunk = (int)c;
     *parts = (int)((keys + c - 1) / c);
   };
-  a->row_tiles = (a->T * a->group + 16 * wm - 1) / (16 * wm);
-  split(a->prefix_len, (int64_t)a->row_tiles * a->kv.kv_heads, &a->prefix_parts, &a->prefix_chunk);
+  a->tc_ctas = 0;
+  if (a->prefix_len > 0 && a->T * a->group > 16 * wm) {
+    plan_prefix_tc(a, sms);
+  } else {
+    a->row_tiles = (a->T * a->group + 16 * wm - 1) / (16 * wm);
+    split(a->prefix_len, (int64_t)a->row_tiles * a->kv.kv_heads, &a->prefix_parts, &a->prefix_chunk);
+  }
   split(a->max_suffix, (int64_t)a->T * a->kv.kv_heads, &a->suffix_parts, &a->suffix_chunk);
 }
 
@@ -449,7 +436,7 @@ int launch_stream(const Args& a, cudaStream_t s) {
   const int r = cuda_status(cudaFuncSetAttribute(stream_kernel<D, F8, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                             "moe_prefix_attention");
   if (r != PMOE_OK) return r;
-  const int64_t pb = (int64_t)a.prefix_parts * a.kv.kv_heads * a.row_tiles;
+  const int64_t pb = a.tc_ctas > 0 ? 0 : (int64_t)a.prefix_parts * a.kv.kv_heads * a.row_tiles;
   const int64_t sb = (int64_t)a.suffix_parts * a.kv.kv_heads * a.T;
   if (pb + sb > INT32_MAX) return PMOE_EUNSUPPORTED;
   if (pb + sb > 0) stream_kernel<D, F8, WM><<<(unsigned)(pb + sb), kThreads, smem, s>>>(a, (int)pb);
@@ -459,7 +446,9 @@ int launch_stream(const Args& a, cudaStream_t s) {
 template <int D, bool F8>
 int launch_all(const Args& a, cudaStream_t s) {
   const int wm = wm_of(a.group);
-  const int r = wm == 1 ? launch_stream<D, F8, 1>(a, s) : wm == 2 ? launch_stream<D, F8, 2>(a, s) : launch_stream<D, F8, 4>(a, s);
+  int r = a.tc_ctas > 0 ? launch_prefix_tc(a, s) : PMOE_OK;
+  if (r != PMOE_OK) return r;
+  r = wm == 1 ? launch_stream<D, F8, 1>(a, s) : wm == 2 ? launch_stream<D, F8, 2>(a, s) : launch_stream<D, F8, 4>(a, s);
   if (r != PMOE_OK) return r;
   const int64_t rh = (int64_t)a.T * a.q_heads;
   combine_kernel<D><<<(unsigned)((rh + 3) / 4), 128, 0, s>>>(a);
@@ -528,7 +517,7 @@ extern "C" int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64
   if (need > 0 && (scratch == nullptr || scratch_bytes < need)) return PMOE_EINVAL;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
-  a.scale = scale * attn::kLog2e;
+  a.scale = scale != 0.f ? scale * attn::kLog2e : 1e-30f;  // not 0: masked scores are -inf times it
   a.prefix_pages = prefix_pages;
   a.page_table = page_table;
   a.table_stride = table_stride;

@@ -1,0 +1,517 @@
+// The shared prefix of moe_prefix_attention on the tensor cores.
+//
+// All rows of a kv head (T tokens x its query heads) attend to the same keys, so the prefix
+// is two matrix products a tile of 128 keys: S = Q K^T and O += P V, P the softmax weights.
+// A CTA takes 256 rows (two 128-row query tiles, the M of an MMA) of one kv head and a range
+// of key tiles; both query tiles share each K and V tile.
+//
+// Warps: 0-3 and 4-7 own one query tile each, a thread one row (a TMEM lane): scores from
+// TMEM, weights back to TMEM in their place as the 16-bit A operand of the second product.
+// Warp 8 issues the MMAs, in the order O0 += P0 V, S0 of the next tile, O1 += P1 V, S1 of
+// the next tile, so that one query tile's softmax runs under the other's products. Warp 9
+// loads K and V tiles by TMA, one box a page and 64 columns, into a ring of five 128-key
+// tiles; with an e4m3 cache warps 9-12 read them, convert to fp16 (exact) and write the
+// same layout.
+//
+// The running maximum of a row moves only when a score exceeds it by 2^8 (any base gives the
+// same quotient; weights up to 2^8 are far from overflow), so the accumulators in TMEM are
+// rarely rescaled. Sums are fp32 of the unrounded weights.
+//
+// Work is split into equal runs of (group, key tile) units, one run per SM: a group's parts
+// are joined by the combine kernel.
+#include "attn.cuh"
+#include "tc_gemm.h"
+#include "tc_ptx.cuh"
+
+#include <algorithm>
+
+namespace pmoe {
+namespace attn {
+namespace {
+
+using namespace tc;
+
+template <int D, bool F8>
+struct TcCfg {
+  static constexpr int kTileBytes = kTcKeys * D * 2;      // one K or V tile, 16-bit operands
+  static constexpr int kQBytes = 128 * D * 2;             // one query tile
+  static constexpr int kSlots = D == 128 ? 5 : 8;         // ring of K and V tiles
+  static constexpr int kLoaders = F8 ? 4 : 1;             // loading warps
+  static constexpr int kThreads = (9 + kLoaders) * 32;
+  static constexpr int kRing = kSlots * kTileBytes;
+  static constexpr int kSmem = kRing + 2 * kQBytes + 1024 /* alignment */ + 1024 /* row factors */ + 512;
+  static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
+};
+
+// V as the B operand: [D / 64][128 keys][64 values of 128 bytes], N (the values) contiguous.
+// 8-key groups lie 1024 bytes apart, the next 64 values 128 keys further.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((kTcKeys * 128) >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  uint64_t sfull[2], pready[2], odone[2], qfull[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+// One segment of a CTA's run: key tiles [t0, t1) of one group.
+struct Segment {
+  int h, row0, rows, nq, t0, t1, part;
+};
+__device__ __forceinline__ bool segment(const Args& a, int64_t* u, int64_t end, Segment* s) {
+  if (*u >= end) return false;
+  const int g = (int)(*u / a.tc_tiles);
+  s->t0 = (int)(*u - (int64_t)g * a.tc_tiles);
+  s->t1 = (int)min((int64_t)a.tc_tiles, s->t0 + (end - *u));
+  s->h = g % a.kv.kv_heads;
+  s->row0 = g / a.kv.kv_heads * kTcRows;
+  s->rows = min(kTcRows, a.T * a.group - s->row0);
+  s->nq = s->rows > 128 ? 2 : 1;
+  s->part = (int)blockIdx.x - tc_cta_of((int64_t)g * a.tc_tiles, tc_units(a), a.tc_ctas);
+  *u += s->t1 - s->t0;
+  return true;
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a) {
+  using C = TcCfg<D, F8>;
+  constexpr int kSlots = C::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = smem + C::kRing;
+  float* qmul = reinterpret_cast<float*>(qs + 2 * C::kQBytes);  // [256]
+  Bars& b = *reinterpret_cast<Bars*>(qmul + 256);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &b.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&b.full[i], F8 ? 128 : 1);
+      mbar_init(&b.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.sfull[i], 1);
+      mbar_init(&b.pready[i], 128);
+      mbar_init(&b.odone[i], 1);
+      mbar_init(&b.qfull[i], 128);
+    }
+    mbar_init(&b.drain, 1);
+    b.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (!F8) {
+      prefetch_map(&map_k);
+      prefetch_map(&map_v);
+    }
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)),
+                 "r"(C::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = b.tmem;
+  const int64_t units = tc_units(a);
+  int64_t u = (int64_t)blockIdx.x * units / a.tc_ctas;
+  const int64_t end = (int64_t)(blockIdx.x + 1) * units / a.tc_ctas;
+  const int psh = 31 - __clz(a.kv.page_size);
+  Segment sg;
+
+  if (warp < 8) {
+    // ---------------- softmax: one thread a row
+    const int q = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + q * 128, to = lanes + 256 + q * 128;
+    constexpr int LPR = D / 8;  // threads of a row while Q is loaded
+    uint32_t n = 0, segs = 0;   // tiles and segments so far
+    bool ok = true;
+    while (ok && segment(a, &u, end, &sg)) {
+      if (q >= sg.nq) continue;
+      // the query tile, K-major with the 128-byte swizzle; rows beyond the last are zero.
+      // A negative scale goes into the sign of Q, so that the largest score stays the largest.
+      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+      const int c = row % LPR;
+      for (int r = row / LPR; r < 128; r += 128 / LPR) {
+        const int i = q * 128 + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < sg.rows) {
+          const int rr = sg.row0 + i;
+          v = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(rr / a.group) * a.q_stride +
+                                                   (sg.h * a.group + rr % a.group) * D + c * 8));
+        }
+        uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+        if (F8) {
+          float mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int e = row_exponent(mx);
+          const float down = pow2(-e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+          if (c == 0) qmul[i] = fabsf(a.scale) * a.kv.k_scale[sg.h] * pow2(e);
+        }
+        *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_async();
+      mbar_arrive(&b.qfull[q]);
+      // the row factors of all threads
+      if (!__all_sync(0xffffffffu, mbar_wait(&b.qfull[q], segs++ & 1, abort_flag, a.err))) break;
+      const float mul = F8 ? qmul[q * 128 + row] : fabsf(a.scale);
+
+      float m = -INFINITY, l = 0.f;
+      for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&b.sfull[q], n & 1, abort_flag, a.err))) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        // scores of 32 keys; -inf beyond the prefix. A bf16 cache's kernel has the registers
+        // to keep all 128, with the e4m3 loaders in the CTA they are read twice.
+        const int valid = a.prefix_len - t * kTcKeys;
+        auto fetch = [&](int i, float* s) {
+          tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s));
+          tmem_wait_ld();
+          if (valid < kTcKeys) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * i + k >= valid) s[k] = -INFINITY;
+          }
+        };
+        float s[F8 ? 32 : 128];
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (!F8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+          tmem_wait_ld();
+          if (valid < kTcKeys) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= valid) s[i] = -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i & 3] = fmaxf(x[i & 3], s[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            fetch(i, s);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k & 3] = fmaxf(x[k & 3], s[k]);
+          }
+        }
+        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
+        if (t == sg.t0) {
+          m = mx;
+        } else {
+          const bool grow = mx > m + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            // the products so far have to be done before their sums are rescaled
+            if (!__all_sync(0xffffffffu, mbar_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err))) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            const float f = grow ? ex2(m - mx) : 1.f;
+            if (grow) m = mx;
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(to + i, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16];
+          if constexpr (F8) fetch(i, s);
+          const float* sc = F8 ? s : s + 32 * i;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float y = ex2(fmaf(sc[2 * k], mul, -base)), z = ex2(fmaf(sc[2 * k + 1], mul, -base));
+            sum[2 * (k & 1)] += y;
+            sum[2 * (k & 1) + 1] += z;
+            p[k] = pack2<F8>(y, z);
+          }
+          tmem_st16(ts + 16 * i, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        fence_before();
+        mbar_arrive(&b.pready[q]);
+      }
+      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err))) break;
+      fence_after();
+      const int i = q * 128 + row, rr = sg.row0 + i;
+      const int64_t at = (int64_t)sg.part * a.T * a.q_heads + (int64_t)(rr / a.group) * a.q_heads + sg.h * a.group + rr % a.group;
+      const float vs = F8 ? a.kv.v_scale[sg.h] : 1.f;
+#pragma unroll 1
+      for (int k = 0; k < D; k += 16) {
+        uint32_t o[16];
+        tmem_ld16(to + k, o);
+        tmem_wait_ld();
+        if (i < sg.rows) {
+          float* dst = a.o_part + at * D + k;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(dst + e) = make_float4(__uint_as_float(o[e]) * vs, __uint_as_float(o[e + 1]) * vs,
+                                                              __uint_as_float(o[e + 2]) * vs, __uint_as_float(o[e + 3]) * vs);
+        }
+      }
+      if (i < sg.rows) a.ml_part[at] = make_float2(m, l);
+      fence_before();
+    }
+  } else if (warp == 8) {
+    // ---------------- MMA issuer
+    const uint32_t is = idesc_bf16(128, kTcKeys) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u);
+    const uint32_t io = (idesc_bf16(128, D) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u)) | (1u << 16);  // B: N contiguous
+    const uint32_t ring = smem_u32(smem), qa = smem_u32(qs);
+    uint32_t kv = 0;               // K and V tiles so far
+    uint32_t seg[2] = {0, 0};      // segments of each query tile so far
+    uint32_t pn[2] = {0, 0};       // products with V of each query tile so far
+    bool ok = true;
+    auto wait_kv = [&](uint32_t i) {
+      return __all_sync(0xffffffffu, mbar_wait(&b.full[i % kSlots], (i / kSlots) & 1, abort_flag, a.err));
+    };
+    auto scores = [&](int q, uint32_t slot) {
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
+          mma_bf16(tmem + q * 128, sw128_desc(qa + q * C::kQBytes + off), sw128_desc(ring + slot * C::kTileBytes + off), is,
+                   k > 0);
+        }
+        mma_commit(&b.sfull[q]);
+      }
+      __syncwarp();
+    };
+    while (ok && segment(a, &u, end, &sg)) {
+      for (int q = 0; q < sg.nq && ok; ++q) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&b.qfull[q], seg[q] & 1, abort_flag, a.err));
+        ++seg[q];
+      }
+      if (!ok || !wait_kv(kv)) break;
+      fence_after();
+      for (int q = 0; q < sg.nq; ++q) scores(q, kv % kSlots);
+      if (lane == 0) mma_commit(&b.empty[kv % kSlots]);
+      __syncwarp();
+      for (int t = sg.t0; t < sg.t1; ++t, kv += 2) {
+        const uint32_t vslot = (kv + 1) % kSlots;
+        const bool more = t + 1 < sg.t1;
+        if (!wait_kv(kv + 1)) {
+          ok = false;
+          break;
+        }
+        const int valid = a.prefix_len - t * kTcKeys;
+        if (!F8 && valid < kTcKeys) {
+          // values beyond the prefix may be anything, and 0 x NaN is NaN
+          for (int i = valid * 8 + lane; i < kTcKeys * 8; i += 32)
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              *reinterpret_cast<uint4*>(smem + vslot * C::kTileBytes + hf * (kTcKeys * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_async();
+          __syncwarp();
+        }
+        for (int q = 0; q < sg.nq; ++q) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&b.pready[q], pn[q] & 1, abort_flag, a.err))) {
+            ok = false;
+            break;
+          }
+          ++pn[q];
+          fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < kTcKeys / 16; ++k)
+              mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
+                         t > sg.t0 || k > 0);
+            mma_commit(&b.odone[q]);
+          }
+          __syncwarp();
+          if (more) {
+            if (q == 0 && !wait_kv(kv + 2)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            scores(q, (kv + 2) % kSlots);
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          mma_commit(&b.empty[vslot]);
+          if (more) mma_commit(&b.empty[(kv + 2) % kSlots]);
+        }
+        __syncwarp();
+      }
+    }
+    // every MMA and its arrival are done before the CTA leaves
+    if (lane == 0) {
+      mma_commit(&b.drain);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&b.drain, 0) && clock64() - t0 < kWaitLimit) {
+      }
+    }
+    __syncwarp();
+  } else if constexpr (!F8) {
+    // ---------------- TMA loader: lane i issues box i % boxes of page box i / halves
+    constexpr int kHalves = D / 64;
+    const int box = min(a.kv.page_size, kTcKeys), boxes = kTcKeys / box;
+    uint32_t kv = 0;
+    bool ok = true;
+    while (ok && segment(a, &u, end, &sg)) {
+      for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+        const int used = min(boxes, (a.prefix_len - t * kTcKeys + box - 1) / box);
+        const int pb = lane / kHalves, hf = lane % kHalves;
+        const int key = t * kTcKeys + pb * box;
+        int id = 0;
+        if (pb < used) {
+          id = __ldg(a.prefix_pages + (key >> psh));
+          if ((unsigned)id >= (unsigned)a.kv.num_pages) {
+            if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
+            id = a.kv.num_pages;  // out of the map's range: reads as zeros
+          }
+        }
+        for (int v = 0; v < 2; ++v, ++kv) {
+          const uint32_t slot = kv % kSlots;
+          if (!__all_sync(0xffffffffu, mbar_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&b.full[slot], used * box * D * 2);
+          __syncwarp();
+          if (pb < used)
+            tma_load_4d(smem + slot * C::kTileBytes + hf * (kTcKeys * 128) + pb * box * 128, v ? &map_v : &map_k,
+                        &b.full[slot], hf * 64, key & (a.kv.page_size - 1), sg.h, id);
+        }
+      }
+    }
+    // copies in flight land before the CTA leaves, even where another role gave up
+    for (uint32_t i = kv > kSlots ? kv - kSlots : 0; i < kv; ++i) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&b.full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kWaitLimit) {
+      }
+    }
+  } else {
+    // ---------------- e4m3 loaders: 16 codes a thread and step, to fp16
+    constexpr int CH = D / 16;  // 16-code chunks of a row
+    constexpr int N = kTcKeys * CH / 128;
+    const int tid = threadIdx.x - 9 * 32, ch = tid % CH;
+    uint32_t kv = 0;
+    bool ok = true;
+    while (ok && segment(a, &u, end, &sg)) {
+      for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+        int64_t off[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int key = t * kTcKeys + tid / CH + i * (128 / CH);
+          off[i] = -1;
+          if (key < a.prefix_len) {
+            const int id = __ldg(a.prefix_pages + (key >> psh));
+            if ((unsigned)id < (unsigned)a.kv.num_pages)
+              off[i] = (int64_t)id * a.kv.page_stride + ((int64_t)sg.h * a.kv.page_size + (key & (a.kv.page_size - 1))) * D + ch * 16;
+            else if (a.err != nullptr)
+              atomicOr(a.err, kErrBadPage);
+          }
+        }
+        for (int v = 0; v < 2; ++v, ++kv) {
+          const uint8_t* src = static_cast<const uint8_t*>(v ? a.kv.v : a.kv.k);
+          uint4 raw[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            raw[i] = off[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + off[i])) : make_uint4(0, 0, 0, 0);
+          const uint32_t slot = kv % kSlots;
+          if (!__all_sync(0xffffffffu, mbar_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err))) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int r = tid / CH + i * (128 / CH);
+            uint8_t* dst = smem + slot * C::kTileBytes + (ch / 4) * (kTcKeys * 128) + r * 128;
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[2 * k] = e4m3x2(w[k] & 0xffffu), f[2 * k + 1] = e4m3x2(w[k] >> 16);
+            // 8 threads hold a row of 128: the upper four write their halves the other way
+            // round, so that the two 64-value blocks meet on different banks
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int kk = k ^ (ch / 4 & 1);
+              *reinterpret_cast<uint4*>(dst + (((2 * (ch % 4) + kk) ^ (r & 7)) << 4)) =
+                  kk ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
+            }
+          }
+          fence_async();
+          mbar_arrive(&b.full[slot]);
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
+}
+
+int make_map(const Args& a, void* base, CUtensorMap* m) {
+  const uint64_t D = a.kv.head_dim, page = a.kv.page_size;
+  const uint64_t dims[4] = {D, page, (uint64_t)a.kv.kv_heads, (uint64_t)a.kv.num_pages};
+  const uint64_t strides[3] = {D * 2, page * D * 2, (uint64_t)a.kv.page_stride * 2};
+  const uint32_t box[4] = {64, (uint32_t)std::min<uint64_t>(page, kTcKeys), 1, 1};
+  return tc_encode_bf16_map(m, base, 4, dims, strides, box);
+}
+
+template <int D, bool F8>
+int launch(const Args& a, cudaStream_t s) {
+  using C = TcCfg<D, F8>;
+  CUtensorMap mk{}, mv{};
+  if (!F8) {
+    int r = make_map(a, a.kv.k, &mk);
+    if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
+    if (r != PMOE_OK) return r;
+  }
+  const int r = cuda_status(cudaFuncSetAttribute(prefix_tc_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem),
+                            "moe_prefix_attention");
+  if (r != PMOE_OK) return r;
+  prefix_tc_kernel<D, F8><<<a.tc_ctas, C::kThreads, C::kSmem, s>>>(mk, mv, a);
+  return launch_status("moe_prefix_attention");
+}
+
+}  // namespace
+
+void plan_prefix_tc(Args* a, int sms) {
+  a->row_tiles = (a->T * a->group + kTcRows - 1) / kTcRows;
+  a->tc_tiles = (a->prefix_len + kTcKeys - 1) / kTcKeys;
+  const int64_t units = tc_units(*a);
+  a->tc_ctas = (int)std::min<int64_t>(sms, units);
+  a->prefix_parts = 0;
+  for (int64_t u = 0; u < units; u += a->tc_tiles)
+    a->prefix_parts = std::max(a->prefix_parts, tc_cta_of(u + a->tc_tiles - 1, units, a->tc_ctas) - tc_cta_of(u, units, a->tc_ctas) + 1);
+}
+
+int launch_prefix_tc(const Args& a, cudaStream_t s) {
+  const bool f8 = a.kv.dtype == PMOE_KV_E4M3;
+  if (a.kv.head_dim == 128) return f8 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+  return f8 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+}
+
+}  // namespace attn
+}  // namespace pmoe

@@ -126,6 +126,7 @@ SIZES = [
     (33, 16, 2, 64, 16, True, 257, 20),
     (47, 40, 8, 64, 32, True, 345, 77),
     (40, 8, 1, 128, 64, False, 1000, 64),
+    (130, 8, 1, 128, 16, False, 3000, 5),
     (70, 8, 2, 128, 16, True, 640, 16),
     (64, 16, 1, 64, 128, False, 999, 0),
     (131, 4, 2, 128, 32, False, 385, 40),
