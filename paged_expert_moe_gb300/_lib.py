@@ -216,34 +216,20 @@ def moe_decode_forward_noalloc(experts, stride, E, top_k, H, I, fmt, x, ids, w, 
     return y
 
 
-def _kv_desc(k_cache, v_cache, k_scale, v_scale):
-    """pmoe_kv_desc of a paged cache: CUDA bf16 or float8_e4m3fn [num_pages, kv_heads,
-    page_size, head_dim] tensors of the same strides, contiguous but for the page stride."""
+# The calls of a decode step take a few microseconds on the GPU, so their binding is kept
+# lean: pointers go to ctypes as plain integers and the stream as its raw handle.
+
+def _raw_stream(stream, like):
     import torch
-    pages, heads, page, dim = k_cache.shape
-    assert k_cache.is_cuda and v_cache.is_cuda and k_cache.dtype == v_cache.dtype and v_cache.shape == k_cache.shape
-    stride = k_cache.stride()
-    assert stride == v_cache.stride() and stride[1:] == (page * dim, dim, 1)
-    if k_cache.dtype == torch.float8_e4m3fn:
-        dtype = PMOE_KV_E4M3
-        assert k_scale.dtype == v_scale.dtype == torch.float32 and k_scale.is_cuda and v_scale.is_cuda
-        assert k_scale.is_contiguous() and v_scale.is_contiguous() and k_scale.numel() == v_scale.numel() == heads
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    else:
-        dtype, ks, vs = PMOE_KV_BF16, None, None
-        assert k_cache.dtype == torch.bfloat16
-    return pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride[0], ks, vs, pages, page, heads, dim, dtype)
+    return torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
 
 
-def _heads_ok(x, T, dim):
-    """x [T, heads, dim] bf16 with contiguous heads; its token stride is free."""
-    import torch
-    return x.is_cuda and x.dtype == torch.bfloat16 and x.shape[0] == T and x.shape[2] == dim and \
-        x.stride(2) == 1 and (x.stride(1) == dim or x.shape[1] == 1)
-
-
-def _vec_ok(x, dtype, n):
-    return x is None or (x.is_cuda and x.dtype == dtype and x.is_contiguous() and x.numel() == n)
+def _opt(x, dtype, n):
+    """The address of a contiguous CUDA tensor of n elements, None for None."""
+    if x is None:
+        return None
+    assert x.dtype is dtype and x.is_cuda and x.numel() == n and x.is_contiguous(), (x.dtype, x.shape, dtype, n)
+    return x.data_ptr()
 
 
 def _empty(shape, dtype, like, stream):
@@ -255,9 +241,31 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _token_stride(x):
-    """Elements from token to token of x [T, heads, dim] (one token has no stride of its own)."""
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+def _kv_desc(k_cache, v_cache, k_scale, v_scale):
+    """pmoe_kv_desc of a paged cache: CUDA bf16 or float8_e4m3fn [num_pages, kv_heads,
+    page_size, head_dim] tensors of the same strides, contiguous but for the page stride."""
+    import torch
+    pages, heads, page, dim = shape = k_cache.shape
+    stride = k_cache.stride()
+    dt = k_cache.dtype
+    assert k_cache.is_cuda and v_cache.is_cuda and v_cache.dtype is dt and v_cache.shape == shape
+    assert v_cache.stride() == stride and stride[1:] == (page * dim, dim, 1)
+    if dt is torch.bfloat16:
+        return pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride[0], None, None, pages, page, heads, dim,
+                            PMOE_KV_BF16)
+    assert dt is torch.float8_e4m3fn
+    return pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride[0], _opt(k_scale, torch.float32, heads),
+                        _opt(v_scale, torch.float32, heads), pages, page, heads, dim, PMOE_KV_E4M3)
+
+
+def _heads(x, T, heads, dim):
+    """(address, elements from token to token) of bf16 x [T, heads, dim] whose heads are
+    contiguous; one token or head has no stride of its own."""
+    import torch
+    st, sh, sd = x.stride()
+    assert x.dtype is torch.bfloat16 and x.is_cuda and x.shape == (T, heads, dim)
+    assert sd == 1 and (sh == dim or heads == 1)
+    return x.data_ptr(), st if T > 1 else heads * dim
 
 
 def moe_kv_append(k_cache, v_cache, q, k, v, positions, slots, inv_freq, pair_axis=None, interleaved=False, q_norm=None,
@@ -271,21 +279,19 @@ def moe_kv_append(k_cache, v_cache, q, k, v, positions, slots, inv_freq, pair_ax
     import torch
     T, q_heads, dim = q.shape
     desc = _kv_desc(k_cache, v_cache, k_scale, v_scale)
+    hk = desc.kv_heads
+    assert dim == desc.head_dim
+    i32, bf16 = torch.int32, torch.bfloat16
     axes = positions.shape[0] if positions is not None and positions.dim() == 2 else 1
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    assert dim == desc.head_dim and k.shape[1] == v.shape[1] == desc.kv_heads
-    assert _heads_ok(q, T, dim) and _heads_ok(k, T, dim) and _heads_ok(v, T, dim)
-    assert _vec_ok(positions, torch.int32, axes * T) and _vec_ok(slots, torch.int32, T)
-    assert _vec_ok(inv_freq, torch.float32, rot // 2) and _vec_ok(pair_axis, torch.int32, rot // 2)
-    assert _vec_ok(q_norm, torch.bfloat16, dim) and _vec_ok(k_norm, torch.bfloat16, dim)
-    assert _vec_ok(err_out, torch.int32, 1)
+    pairs = 0 if inv_freq is None else inv_freq.numel()
     if q_out is None:
-        q_out = _empty((T, q_heads, dim), torch.bfloat16, q, stream)
-    assert _vec_ok(q_out, torch.bfloat16, T * q_heads * dim)
-    _check(load().moe_kv_append(desc, _ptr(q), _token_stride(q), _ptr(k), _token_stride(k), _ptr(v), _token_stride(v),
-                                T, q_heads, _ptr(positions), axes, _ptr(pair_axis), _ptr(inv_freq), rot,
-                                1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), eps, _ptr(slots), _ptr(q_out),
-                                _ptr(err_out), _stream_handle(stream)), "moe_kv_append")
+        q_out = _empty((T, q_heads, dim), bf16, q, stream)
+    _check(load().moe_kv_append(desc, *_heads(q, T, q_heads, dim), *_heads(k, T, hk, dim), *_heads(v, T, hk, dim), T,
+                                q_heads, _opt(positions, i32, axes * T), axes, _opt(pair_axis, i32, pairs),
+                                _opt(inv_freq, torch.float32, pairs), 2 * pairs, 1 if interleaved else 0,
+                                _opt(q_norm, bf16, dim), _opt(k_norm, bf16, dim), eps, _opt(slots, i32, T),
+                                _opt(q_out, bf16, T * q_heads * dim), _opt(err_out, i32, 1), _raw_stream(stream, q)),
+           "moe_kv_append")
     return q_out
 
 
@@ -307,28 +313,31 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
     import torch
     T, q_heads, dim = q.shape
     desc = _kv_desc(k_cache, v_cache, k_scale, v_scale)
-    page = desc.page_size
-    assert dim == desc.head_dim and _heads_ok(q, T, dim)
-    assert prefix_len <= 0 or (_vec_ok(prefix_pages, torch.int32, prefix_pages.numel()) and
-                               prefix_pages.numel() * page >= prefix_len)
+    i32 = torch.int32
+    assert dim == desc.head_dim
+    pages = None
+    if prefix_len > 0:
+        n = prefix_pages.numel()
+        assert n * desc.page_size >= prefix_len
+        pages = _opt(prefix_pages, i32, n)
+    table = lens = None
     sequences = width = 0
     if max_suffix > 0:
         sequences, width = page_table.shape
-        assert _vec_ok(page_table, torch.int32, sequences * width) and _vec_ok(suffix_len, torch.int32, T)
-    assert _vec_ok(row_seq, torch.int32, T) and _vec_ok(lse_out, torch.float32, T * q_heads)
-    assert _vec_ok(err_out, torch.int32, 1)
+        table, lens = _opt(page_table, i32, sequences * width), _opt(suffix_len, i32, T)
     lib = load()
     if out is None:
         out = _empty((T, q_heads, dim), torch.bfloat16, q, stream)
-    assert _vec_ok(out, torch.bfloat16, T * q_heads * dim)
     if scratch is None:
         nbytes = lib.moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix)
-        scratch = _empty(nbytes, torch.uint8, q, stream)
-    assert scratch.is_cuda and scratch.dtype == torch.uint8 and scratch.is_contiguous()
-    _check(lib.moe_prefix_attention(desc, _ptr(q), _token_stride(q), T, q_heads, dim ** -0.5 if scale is None else scale,
-                                    _ptr(prefix_pages), prefix_len, _ptr(page_table), width, sequences, _ptr(row_seq),
-                                    _ptr(suffix_len), max_suffix, _ptr(out), _ptr(lse_out), _ptr(scratch),
-                                    scratch.numel(), _ptr(err_out), _stream_handle(stream)), "moe_prefix_attention")
+        if nbytes:
+            scratch = _empty(nbytes, torch.uint8, q, stream)
+    nbytes = 0 if scratch is None else scratch.numel()
+    _check(lib.moe_prefix_attention(desc, *_heads(q, T, q_heads, dim), T, q_heads, dim ** -0.5 if scale is None else scale,
+                                    pages, prefix_len, table, width, sequences, _opt(row_seq, i32, T), lens, max_suffix,
+                                    _opt(out, torch.bfloat16, T * q_heads * dim), _opt(lse_out, torch.float32, T * q_heads),
+                                    _opt(scratch, torch.uint8, nbytes), nbytes, _opt(err_out, i32, 1),
+                                    _raw_stream(stream, q)), "moe_prefix_attention")
     return out
 
 
@@ -340,16 +349,15 @@ def moe_sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p
     the drawn token's log probability among the kept ones. Returns ids (int32 [T])."""
     import torch
     T, V = logits.shape
-    assert logits.is_cuda and logits.dtype in (torch.float32, torch.bfloat16) and (V == 1 or logits.stride(1) == 1)
-    assert u is not None and _vec_ok(u, torch.float32, T) and _vec_ok(temperature, torch.float32, T)
-    assert _vec_ok(top_k, torch.int32, T) and _vec_ok(top_p, torch.float32, T) and _vec_ok(min_p, torch.float32, T)
+    dt, f32 = logits.dtype, torch.float32
+    st, sv = logits.stride()
+    assert logits.is_cuda and (dt is f32 or dt is torch.bfloat16) and (V == 1 or sv == 1)
     if ids_out is None:
         ids_out = _empty(T, torch.int32, logits, stream)
-    assert _vec_ok(ids_out, torch.int32, T) and _vec_ok(logprob_out, torch.float32, T)
-    _check(load().moe_sample_tokens(_ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0, T, V,
-                                    logits.stride(0) if T > 1 else V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
-                                    _ptr(min_p), _ptr(u), _ptr(ids_out), _ptr(logprob_out), _stream_handle(stream)),
-           "moe_sample_tokens")
+    _check(load().moe_sample_tokens(logits.data_ptr(), 0 if dt is f32 else 1, T, V, st if T > 1 else V,
+                                    _opt(temperature, f32, T), _opt(top_k, torch.int32, T), _opt(top_p, f32, T),
+                                    _opt(min_p, f32, T), _opt(u, f32, T), _opt(ids_out, torch.int32, T),
+                                    _opt(logprob_out, f32, T), _raw_stream(stream, logits)), "moe_sample_tokens")
     return ids_out
 
 

@@ -293,6 +293,16 @@ int cuda_status(cudaError_t e, const char* what) {
   return PMOE_ECUDA;
 }
 int launch_status(const char* what) { return cuda_status(cudaGetLastError(), what); }
+int SmemLimit::set(const void* kernel, int bytes, const char* what) {
+  int dev = 0;
+  int r = cuda_status(cudaGetDevice(&dev), what);
+  if (r != PMOE_OK) return r;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return PMOE_OK;
+  r = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), what);
+  if (r == PMOE_OK) done.fetch_or(bit, std::memory_order_relaxed);
+  return r;
+}
 }  // namespace pmoe
 
 extern "C" {

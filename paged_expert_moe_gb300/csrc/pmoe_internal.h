@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "../../include/pagedmoe.h"
 
 namespace pmoe {
@@ -157,6 +159,12 @@ ExpertLayout expert_layout(int fmt, int H, int I);
 // PMOE_OK, or PMOE_ECUDA with the launch's error text kept for pmoe_last_error.
 int launch_status(const char* what);
 int cuda_status(cudaError_t e, const char* what);
+// A kernel's dynamic shared memory limit, raised once per device (the call costs more than
+// some launches).
+struct SmemLimit {
+  std::atomic<uint64_t> done{0};  // one bit per device
+  int set(const void* kernel, int bytes, const char* what);
+};
 // A cache descriptor's checks (PMOE_OK, PMOE_EINVAL or PMOE_EUNSUPPORTED).
 int check_kv(const pmoe_kv_desc* kv);
 

@@ -433,8 +433,8 @@ int wm_of(int group) { return group <= 16 ? 1 : group <= 32 ? 2 : 4; }
 template <int D, bool F8, int WM>
 int launch_stream(const Args& a, cudaStream_t s) {
   const int smem = StreamCfg<D, F8>::kSmem;
-  const int r = cuda_status(cudaFuncSetAttribute(stream_kernel<D, F8, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                            "moe_prefix_attention");
+  static SmemLimit limit;
+  const int r = limit.set(reinterpret_cast<const void*>(stream_kernel<D, F8, WM>), smem, "moe_prefix_attention");
   if (r != PMOE_OK) return r;
   const int64_t pb = a.tc_ctas > 0 ? 0 : (int64_t)a.prefix_parts * a.kv.kv_heads * a.row_tiles;
   const int64_t sb = (int64_t)a.suffix_parts * a.kv.kv_heads * a.T;

@@ -137,31 +137,41 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       // A negative scale goes into the sign of Q, so that the largest score stays the largest.
       const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
       const int c = row % LPR;
-      for (int r = row / LPR; r < 128; r += 128 / LPR) {
-        const int i = q * 128 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < sg.rows) {
-          const int rr = sg.row0 + i;
-          v = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(rr / a.group) * a.q_stride +
-                                                   (sg.h * a.group + rr % a.group) * D + c * 8));
+      constexpr int kPasses = LPR, kAhead = 8;  // rows of a thread, and how many it has in flight
+#pragma unroll
+      for (int p0 = 0; p0 < kPasses; p0 += kAhead) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) {
+          const int i = q * 128 + row / LPR + (p0 + p) * (128 / LPR);
+          v[p] = make_uint4(0, 0, 0, 0);
+          if (i < sg.rows) {
+            const int rr = sg.row0 + i;
+            v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(rr / a.group) * a.q_stride +
+                                                        (sg.h * a.group + rr % a.group) * D + c * 8));
+          }
         }
-        uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
-        if (F8) {
-          float mx = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+        for (int p = 0; p < kAhead; ++p) {
+          const int r = row / LPR + (p0 + p) * (128 / LPR);
+          uint32_t w[4] = {v[p].x ^ flip, v[p].y ^ flip, v[p].z ^ flip, v[p].w ^ flip};
+          if (F8) {
+            float mx = 0.f;
 #pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int e = row_exponent(mx);
-          const float down = pow2(-e);
+            for (int k = 0; k < 4; ++k)
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-          if (c == 0) qmul[i] = fabsf(a.scale) * a.kv.k_scale[sg.h] * pow2(e);
+            for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e = row_exponent(mx);
+            const float down = pow2(-e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+            if (c == 0) qmul[q * 128 + r] = fabsf(a.scale) * a.kv.k_scale[sg.h] * pow2(e);
+          }
+          *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_async();
       mbar_arrive(&b.qfull[q]);
@@ -488,8 +498,8 @@ int launch(const Args& a, cudaStream_t s) {
     if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
     if (r != PMOE_OK) return r;
   }
-  const int r = cuda_status(cudaFuncSetAttribute(prefix_tc_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem),
-                            "moe_prefix_attention");
+  static SmemLimit limit;
+  const int r = limit.set(reinterpret_cast<const void*>(prefix_tc_kernel<D, F8>), C::kSmem, "moe_prefix_attention");
   if (r != PMOE_OK) return r;
   prefix_tc_kernel<D, F8><<<a.tc_ctas, C::kThreads, C::kSmem, s>>>(mk, mv, a);
   return launch_status("moe_prefix_attention");
