@@ -6,21 +6,23 @@
 // Bound: HBM for many rows (each logit read once), the chain of dependent steps for few. A
 // cluster of up to 8 CTAs takes a row; each CTA keeps its slice in shared memory and the
 // CTAs exchange statistics through distributed shared memory.
-//   1. Load the slice; the largest logit of the row and of each thread.
-//   2. Rows that are cut by top-k or top-p: of the threads' largest logits, the bin (1/16
-//      wide, by distance from the row's largest) that holds the K-th, K = top_k or 512. At
-//      least K logits lie in it or above it, and seldom many more: these candidates go to
-//      the row's first CTA, which sorts them, cuts them and draws. Rows with more than 2,048
-//      candidates, or whose candidates do not reach top_p, go on with step 3.
-//   3. A histogram of all logits over the same bins, count and weight; the bin that holds
-//      the top_k-th token or in which the weight reaches top_p; inside it four passes over
-//      8 bits of the ordered logit find the threshold itself.
+//   1. Load the slice; its largest logit, and each thread's. For rows that are cut by top-k
+//      or top-p a lower bound of the K-th largest logit (K = top_k, or 384): with K / CTAs
+//      of the threads' largest logits at or above a bound in every CTA, K logits are at or
+//      above the least of these bounds, and seldom many more.
+//   2. These candidates go to the row's first CTA, which orders them, cuts them and draws.
+//      Rows with more than 2,048 candidates, or whose candidates do not reach top_p, go on
+//      with step 3.
+//   3. A histogram of all logits by distance from the largest, count and weight; the bin that holds
+//      the top_k-th token or in which the weight reaches top_p. Its logits (again up to
+//      2,048; else four passes over 8 bits of the ordered logit) give the threshold itself.
 //   4. Sums of the kept tokens in id order (ties of the threshold in id order), the segment
 //      that holds floor(S * u), and its token.
 // Uncut rows take steps 1 and 4.
 #include "pmoe_internal.h"
 
 #include <cooperative_groups.h>
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -39,9 +41,8 @@ constexpr int kMaxSmem = (kMaxVocab / kMaxCluster + 8) * 4;
 constexpr int kList = 1024;         // candidates of a CTA
 constexpr int kMerged = 2048;       // and of a row
 constexpr int kMaxK = 1200;         // top_k up to which rows are cut by their candidates
-constexpr int kCutP = 512;          // K for rows that only top-p cuts
-// exp(z) 2^31 < 1 for z below -21.487...
-constexpr float kZeroBelow = -21.6f;
+constexpr int kCutP = 384;          // K for rows that only top-p cuts
+constexpr int kPairs = 256;         // elements up to which all pairs are compared
 
 typedef unsigned long long u64;
 
@@ -65,19 +66,26 @@ struct Histogram {        // weights as two 16-bit halves: a slice holds at most
   uint32_t hi[kBins];
 };
 
+struct Threshold {        // kept: key > this key, and the first `ties` ids that have it
+  uint32_t key, ties;
+  u64 total;              // weight of the kept tokens
+};
+
 struct Shared {
+  Histogram hist;
   union {
-    Histogram hist[2];
-    struct {
-      u64 merged[kMerged];
-      u64 list[kList];
-    };
+    Histogram level;      // step 3's passes over the key's bits
+    u64 list[kList];      // candidates of this CTA: ~key << 32 | id
   };
-  float best;             // this CTA's largest logit
-  int arg;                // and, for greedy rows, the lowest id that has it
+  u64 merged[kMerged];    // and, in the row's first CTA, of all
+  float best, bound;      // this CTA's largest logit, and its bound of the K-th
+  uint32_t bound_key;
+  int arg;                // in the first CTA, of greedy rows: the lowest id that has it
   int listed;             // candidates found
-  int done;               // the row's first CTA has drawn
-  u64 sum;                // all weights of the slice
+  u64 sum, list_sum;      // all weights of the slice, and its candidates'
+  Threshold thr;
+  int members;            // select: elements of the bin it looks into
+  u64 sel, sel_upto;      // and what it found
   u64 scan[kWarps];
   uint32_t scan_cnt[kWarps];
   u64 pick_above;         // the bin found by a scan: weight above it,
@@ -100,6 +108,10 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 __device__ __forceinline__ u64 share(u64 total, float part) {
   const u64 n = (u64)(part * 16777216.f);
   return (total >> 24) * n + (((total & 0xffffffull) * n) >> 24);
+}
+
+__device__ __forceinline__ u64 least_weight(u64 total, float top_p) {
+  return max((u64)1, share(total, top_p > 0.f ? top_p : 0.f));
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -138,10 +150,7 @@ struct Row {
   __device__ __forceinline__ float weight(float x) const { return x == m ? 1.f : expf((x - m) * r); }
   // NaN gives 0, as -inf does
   __device__ __forceinline__ static uint32_t units(float w) { return (uint32_t)(w * 2147483648.f); }
-  __device__ __forceinline__ uint32_t units_of(float x) const {
-    const float z = (x - m) * r;
-    return x == m ? 0x80000000u : z > kZeroBelow ? units(expf(z)) : 0u;
-  }
+  __device__ __forceinline__ uint32_t units_of(float x) const { return units(expf(x == m ? 0.f : (x - m) * r)); }
   __device__ __forceinline__ int bin(float x) const {
     const float d = (m - x) * kBinsPerUnit;
     return d < (float)(kBins - 1) ? (int)d : (x == m ? 0 : kBins - 1);
@@ -166,39 +175,74 @@ struct Vec {
   }
 };
 
-// Sorts a[0, n) ascending, n a power of two from 64 to kMerged. A barrier is only needed
-// where a pair lies further apart than the 64 elements that a warp covers.
-__device__ void sort_up(u64* a, int n) {
-  for (int k = 2; k <= n; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int t = threadIdx.x; t < n / 2; t += kThreads) {
-        const int i = 2 * t - (t & (j - 1));
-        const u64 x = a[i], y = a[i + j];
-        if ((x > y) == ((i & k) == 0)) a[i] = y, a[i + j] = x;
-      }
-      if (j > 32 || (j == 1 && 2 * k > 64))
+constexpr int kEach = kMerged / kThreads;  // sorted elements of a thread
+
+// Sorts the block's kMerged elements ascending: thread t has elements t * kEach .. of `buf`
+// on entry (read after a barrier) and of the sorted sequence in c on return. Bitonic: pairs
+// within a thread, within a warp by shuffles, further apart through `buf`.
+__device__ void sort_up(u64* buf, u64 (&c)[kEach]) {
+  static_assert(kEach == 4, "element pairs below");
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) c[e] = buf[t * kEach + e];
+  auto order = [](u64& x, u64& y, bool up) {
+    const u64 lo = min(x, y), hi = max(x, y);
+    x = up ? lo : hi;
+    y = up ? hi : lo;
+  };
+  for (int k = 2; k <= kMerged; k <<= 1) {
+    for (int j = k >> 1; j >= kEach; j >>= 1) {
+      const int d = j / kEach;  // the partner's distance in threads
+      const bool low = ((t & d) == 0) == ((t * kEach & k) == 0);
+      u64 o[kEach];
+      if (d < 32) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) o[e] = __shfl_xor_sync(0xffffffffu, c[e], d);
+      } else {
         __syncthreads();
-      else
-        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) buf[e * kThreads + t] = c[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) o[e] = buf[e * kThreads + (t ^ d)];
+      }
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) c[e] = low ? min(c[e], o[e]) : max(c[e], o[e]);
     }
+    if (k == 2) {
+      order(c[0], c[1], true);
+      order(c[2], c[3], false);
+    } else {
+      const bool up = (t * kEach & k) == 0;
+      order(c[0], c[2], up);
+      order(c[1], c[3], up);
+      order(c[0], c[1], up);
+      order(c[2], c[3], up);
+    }
+  }
+  __syncthreads();  // buf is free
 }
 
 __device__ __forceinline__ int pow2_above(int n) { return n <= 64 ? 64 : 1 << (32 - __clz(n - 1)); }
 
-// Adds up bin `threadIdx.x` of all CTAs' histogram `b`; finds the first bin, ascending, at
-// which the running count (by_count) or weight reaches `target` (> 0). Every CTA of the
-// cluster calls it; the result is in sh.pick_* (bin kBins where it is not reached).
-// Returns the total weight.
-__device__ u64 find_bin(cg::cluster_group& cluster, Shared& sh, int b, bool by_count, u64 target) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Adds up bin `threadIdx.x` of all CTAs' histograms (`h`: this CTA's); finds the first bin,
+// ascending, at which the running count (by_count) or weight reaches `target` (> 0). Every
+// CTA of the cluster calls it; the result is in sh.pick_* (bin kBins where it is not
+// reached). Returns the total weight.
+__device__ u64 find_bin(cg::cluster_group& cluster, Shared& sh, Histogram* h, bool by_count, u64 target) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = (int)cluster.num_blocks();
   cluster.sync();
+  uint32_t v[kMaxCluster][3];  // all remote loads in flight at once
+#pragma unroll
+  for (int i = 0; i < kMaxCluster; ++i) {
+    const Histogram* o = cluster.map_shared_rank(h, i < nb ? i : 0);
+    v[i][0] = o->cnt[tid], v[i][1] = o->lo[tid], v[i][2] = o->hi[tid];
+  }
   uint32_t c = 0;
   u64 w = 0;
-  for (unsigned i = 0; i < cluster.num_blocks(); ++i) {
-    const Histogram& o = cluster.map_shared_rank(&sh, i)->hist[b];
-    c += o.cnt[tid];
-    if (!by_count || b == 1) w += ((u64)o.hi[tid] << 16) + o.lo[tid];
-  }
+#pragma unroll
+  for (int i = 0; i < kMaxCluster; ++i)
+    if (i < nb) c += v[i][0], w += ((u64)v[i][2] << 16) + v[i][1];
   u64 wi = w;
   uint32_t ci = c;
 #pragma unroll
@@ -212,6 +256,7 @@ __device__ u64 find_bin(cg::cluster_group& cluster, Shared& sh, int b, bool by_c
   __syncthreads();
   u64 wb = 0, total = 0;
   uint32_t cb = 0;
+#pragma unroll
   for (int i = 0; i < kWarps; ++i) {
     if (i < warp) wb += sh.scan[i], cb += sh.scan_cnt[i];
     total += sh.scan[i];
@@ -226,87 +271,269 @@ __device__ u64 find_bin(cg::cluster_group& cluster, Shared& sh, int b, bool by_c
   return total;
 }
 
-// Step 2's end, in the row's first CTA: sh.merged holds n candidates as (~key << 32 | id).
-// false: the kept tokens are not all among them.
-__device__ bool cut_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, int row, int n, int top_k, bool use_k,
-                             float top_p, bool use_p, float min_p, u64 all_weights) {
-  const int tid = threadIdx.x;
-  constexpr int E = kMerged / kThreads;
-  int n2 = pow2_above(n);
-  for (int i = n + tid; i < n2; i += kThreads) sh.merged[i] = ~0ull;
-  __syncthreads();
-  sort_up(sh.merged, n2);
-  __syncthreads();
-  // thread t takes candidates t * e .. t * e + e - 1
-  const int e = n2 <= kThreads ? 1 : n2 / kThreads;
-  u64 c[E], w[E], mine = 0;
-  float wt[E];
+// What each CTA listed, read by one lane per CTA: whether all of it fits, and the sums.
+struct Listed {
+  int mine, before, total;  // lane's CTA: candidates, those of the CTAs before it; all
+  bool fits;
+  u64 sum, list_sum;        // of all CTAs
+};
+__device__ Listed read_listed(cg::cluster_group& cluster, Shared& sh) {
+  const int lane = threadIdx.x & 31, nb = (int)cluster.num_blocks();
+  const Shared* o = cluster.map_shared_rank(&sh, lane < nb ? lane : 0);
+  Listed l;
+  l.mine = lane < nb ? o->listed : 0;
+  l.sum = warp_sum(lane < nb ? o->sum : 0);
+  l.list_sum = warp_sum(lane < nb ? o->list_sum : 0);
+  int upto = l.mine;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int at = tid * e + i;
-    w[i] = 0;
-    if (i < e && at < n && (!use_k || at < top_k)) {
-      c[i] = sh.merged[at];
-      wt[i] = rw.weight(of_key(~(uint32_t)(c[i] >> 32)));
-      w[i] = Row::units(wt[i]);
-      mine += w[i];
-    }
+  for (int d = 1; d < kMaxCluster; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
   }
-  u64 total;
-  u64 run = block_scan(sh, mine, &total) - mine;
-  u64 least = ~0ull;
-  if (use_p) {
-    least = max((u64)1, share(use_k ? total : all_weights, top_p > 0.f ? top_p : 0.f));
-    if (total < least) return false;
+  l.before = upto - l.mine;
+  l.total = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
+  l.fits = l.total <= kMerged && __all_sync(0xffffffffu, l.mine <= kList);
+  return l;
+}
+// All CTAs' candidates to sh.merged, two warps to a CTA, padded with
+// ~0 to a power of two; ends with a barrier.
+__device__ void merge_lists(cg::cluster_group& cluster, Shared& sh, const Listed& l) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kWarps >= 2 * kMaxCluster, "two warps a CTA");
+  const int from = warp >> 1, n = __shfl_sync(0xffffffffu, l.mine, from), at = __shfl_sync(0xffffffffu, l.before, from);
+  if (from < (int)cluster.num_blocks()) {
+    const Shared* o = cluster.map_shared_rank(&sh, from);
+    for (int i = (warp & 1) * 32 + lane; i < n; i += 64) sh.merged[at + i] = o->list[i];
   }
-  u64 kept = 0;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const bool k = w[i] > 0 && run < least && !(wt[i] < min_p);
-    run += w[i];
-    if (!k) w[i] = 0;
-    kept += k;
-  }
-  u64 r;
-  block_scan(sh, kept, &r);  // the kept tokens are the first r
-  n2 = pow2_above((int)r);
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int at = tid * e + i;
-    if (i < e && at < n2) sh.merged[at] = w[i] > 0 ? (c[i] << 32) | w[i] : ~0ull;
-  }
-  for (int i = kThreads * e + tid; i < n2; i += kThreads) sh.merged[i] = ~0ull;
+  for (int i = l.total + threadIdx.x; i < pow2_above(l.total); i += kThreads) sh.merged[i] = ~0ull;
   __syncthreads();
-  sort_up(sh.merged, n2);
+}
+
+// Sum over the G consecutive lanes that share a candidate.
+__device__ __forceinline__ u64 group_sum(u64 v, int G) {
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Step 2's end for up to kPairs candidates: sh.merged holds n of them (padded with ~0 to a
+// power of two from 64). A candidate's place and the weight before it come from comparing it
+// with all others, twice: in the order of the logits for the cuts, in the order of the ids
+// for the draw. kThreads / n2 threads share a candidate.
+__device__ void compare_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, int row, int n, int top_k, bool use_k,
+                                 float top_p, bool use_p, float min_p, u64 all_weights) {
+  const int tid = threadIdx.x, n2 = pow2_above(n), G = kThreads / n2, i = tid / G, part = tid % G;
+  uint32_t* weights = reinterpret_cast<uint32_t*>(sh.list);  // the list is in sh.merged by now
+  const u64 c = sh.merged[i];
+  const uint32_t id = (uint32_t)c;
+  const float wt = rw.weight(of_key(~(uint32_t)(c >> 32)));
+  const uint32_t w = i < n ? Row::units(wt) : 0;
+  if (part == 0) weights[i] = w;
   __syncthreads();
-  const int e2 = n2 <= kThreads ? 1 : n2 / kThreads;
-  mine = 0;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int at = tid * e2 + i;
-    w[i] = 0;
-    if (i < e2 && at < (int)r) {
-      c[i] = sh.merged[at];
-      w[i] = c[i] & 0xffffffffull;
-      mine += w[i];
-    }
+  u64 place = 0, before = 0;
+#pragma unroll 4
+  for (int j = part; j < n; j += G) {
+    const bool ahead = sh.merged[j] < c;
+    place += ahead;
+    before += ahead ? weights[j] : 0;
   }
-  run = block_scan(sh, mine, &total) - mine;
+  place = group_sum(place, G);
+  before = group_sum(before, G);
+  const bool in_k = i < n && (!use_k || place < (u64)top_k);
+  u64 total = all_weights;
+  if (use_k) block_scan(sh, in_k && part == 0 ? w : 0, &total);
+  const u64 least = use_p ? least_weight(total, top_p) : ~0ull;
+  const uint32_t kept = in_k && before < least && !(wt < min_p) ? w : 0;
+  u64 S;
+  block_scan(sh, part == 0 ? kept : 0, &S);
+  if (part == 0) weights[i] = kept;
+  __syncthreads();
+  u64 run = 0;
+#pragma unroll 4
+  for (int j = part; j < n; j += G) run += (uint32_t)sh.merged[j] < id ? weights[j] : 0;
+  run = group_sum(run, G);
   const float uu = a.u[row];
-  const u64 target = share(total, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if (run <= target && target < run + w[i]) {
-      a.ids[row] = (int32_t)(c[i] >> 32);
-      if (a.logprob != nullptr) a.logprob[row] = logf((float)w[i] / (float)total);
-    }
-    run += w[i];
+  const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
+  if (part == 0 && run <= target && target < run + kept) {
+    a.ids[row] = (int32_t)id;
+    if (a.logprob != nullptr) a.logprob[row] = logf((float)kept / (float)S);
   }
-  return true;
+}
+
+// Of the block's elements c (kEach a thread, ~0 for none; ascending order), finds the one at
+// which the running count (by_count) or weight reaches `target`, into sh.sel; the running
+// weight up to it goes to sh.sel_upto. `bin` maps an element to 0 .. kBins - 1 without
+// disturbing the order, `weight` to its weight. One histogram finds the bin, comparing all
+// pairs inside it the element; a bin of more than kPairs elements is sorted instead.
+template <class Bin, class Weight>
+__device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool by_count, u64 target) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t* weights = reinterpret_cast<uint32_t*>(sh.merged + kPairs);
+  sh.level.cnt[tid] = sh.level.lo[tid] = sh.level.hi[tid] = 0;
+  if (tid == 0) sh.members = 0;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (c[e] != ~0ull) {
+      const int b = bin(c[e]);
+      const uint32_t w = weight(c[e]);
+      atomicAdd(&sh.level.cnt[b], 1u);
+      atomicAdd(&sh.level.lo[b], w & 0xffffu);
+      atomicAdd(&sh.level.hi[b], w >> 16);
+    }
+  __syncthreads();
+  const uint32_t own_c = sh.level.cnt[tid];
+  const u64 own_w = ((u64)sh.level.hi[tid] << 16) + sh.level.lo[tid];
+  uint32_t ci = own_c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t d = __shfl_up_sync(0xffffffffu, ci, o);
+    if (lane >= o) ci += d;
+  }
+  if (lane == 31) sh.scan_cnt[warp] = ci;
+  u64 total;
+  const u64 wi = block_scan(sh, own_w, &total);
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i)
+    if (i < warp) ci += sh.scan_cnt[i];
+  if (by_count ? (ci >= target && ci - own_c < target) : (wi >= target && wi - own_w < target)) {
+    sh.pick_bin = tid;
+    sh.pick_cnt = ci - own_c;
+    sh.pick_above = wi - own_w;
+  }
+  __syncthreads();
+  const int pick = sh.pick_bin;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (c[e] != ~0ull && bin(c[e]) == pick) {
+      const int at = atomicAdd(&sh.members, 1);
+      if (at < kPairs) sh.merged[at] = c[e], weights[at] = weight(c[e]);
+    }
+  __syncthreads();
+  const int m = sh.members;
+  if (m <= kPairs) {
+    const int n2 = pow2_above(m), G = kThreads / n2, i = tid / G, part = tid % G;
+    const u64 x = i < m ? sh.merged[i] : ~0ull;
+    u64 place = 0, before = 0;
+#pragma unroll 4
+    for (int j = part; j < m; j += G) {
+      const bool ahead = sh.merged[j] < x;
+      place += ahead;
+      before += ahead ? weights[j] : 0;
+    }
+    place = group_sum(place, G) + sh.pick_cnt;
+    before = group_sum(before, G) + sh.pick_above;
+    const uint32_t w = i < m ? weights[i] : 0;
+    if (part == 0 && i < m && (by_count ? place + 1 == target : before < target && target <= before + w)) {
+      sh.sel = x;
+      sh.sel_upto = before + w;
+    }
+    __syncthreads();
+    return;
+  }
+  // every element of this or another bin may be sorted along; the caller keeps its own
+  u64 s[kEach];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) sh.merged[tid * kEach + e] = c[e];
+  __syncthreads();
+  sort_up(sh.merged, s);
+  u64 mine = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) mine += s[e] != ~0ull ? weight(s[e]) : 0;
+  u64 run = block_scan(sh, mine, &total) - mine;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const uint32_t w = s[e] != ~0ull ? weight(s[e]) : 0;
+    if (s[e] != ~0ull && (by_count ? (u64)(tid * kEach + e) + 1 == target : run < target && target <= run + w)) {
+      sh.sel = s[e];
+      sh.sel_upto = run + w;
+    }
+    run += w;
+  }
+  __syncthreads();
+}
+
+// sh.merged's n elements to registers, kEach a thread; ends with a barrier.
+__device__ void take_merged(const Shared& sh, int n, u64 (&c)[kEach]) {
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = e * kThreads + threadIdx.x;
+    c[e] = i < n ? sh.merged[i] : ~0ull;
+  }
+  __syncthreads();
+}
+
+// The same for more candidates: the cuts and the draw are selections.
+__device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, int row, int n, int top_k, bool use_k,
+                                float top_p, bool use_p, float min_p, u64 all_weights) {
+  u64 c[kEach];
+  take_merged(sh, n, c);
+  const auto logit = [](u64 x) { return of_key(~(uint32_t)(x >> 32)); };
+  const auto by_logit = [&](u64 x) { return rw.bin(logit(x)); };
+  const auto weight = [&](u64 x) { return rw.units_of(logit(x)); };
+  u64 last = ~0ull - 1, total = all_weights;  // the last candidate that is kept
+  if (use_k) {
+    if (n > top_k) {
+      select(sh, c, by_logit, weight, true, (u64)top_k);
+      last = sh.sel, total = sh.sel_upto;
+    } else {
+      u64 mine = 0;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) mine += c[e] != ~0ull ? weight(c[e]) : 0;
+      block_scan(sh, mine, &total);
+    }
+    __syncthreads();
+  }
+  if (use_p) {
+    select(sh, c, by_logit, weight, false, least_weight(total, top_p));
+    last = min(last, sh.sel);
+  }
+  // in the order of the ids: id << 32 | weight
+  u64 mine = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const float wt = c[e] <= last ? rw.weight(logit(c[e])) : 0.f;
+    const uint32_t w = wt < min_p ? 0 : Row::units(wt);
+    c[e] = w > 0 ? (c[e] << 32) | w : ~0ull;
+    mine += w;
+  }
+  u64 S;
+  block_scan(sh, mine, &S);
+  const float uu = a.u[row];
+  const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
+  select(sh, c, [&](u64 x) { return (int)((x >> 32) * kBins / (uint32_t)a.V); }, [](u64 x) { return (uint32_t)x; }, false,
+         target + 1);
+  if (threadIdx.x == 0) {
+    a.ids[row] = (int32_t)(sh.sel >> 32);
+    if (a.logprob != nullptr) a.logprob[row] = logf((float)(uint32_t)sh.sel / (float)S);
+  }
+}
+
+// Step 3's end, in the row's first CTA: sh.merged holds the n logits of bin `bin`; the one at
+// which their running count (by_count) or weight reaches `target` is the threshold.
+__device__ void find_in_bin(Shared& sh, const Row& rw, int n, int bin, bool by_count, u64 target, u64 above) {
+  const int tid = threadIdx.x;
+  u64 c[kEach];
+  take_merged(sh, n, c);
+  const auto logit = [](u64 x) { return of_key(~(uint32_t)(x >> 32)); };
+  // the bin, cut into kBins again (the last one reaches to -inf)
+  const auto inner = [&](u64 x) {
+    const float d = ((rw.m - logit(x)) * kBinsPerUnit - (float)bin) * (float)kBins;
+    return d < (float)(kBins - 1) ? max((int)d, 0) : kBins - 1;
+  };
+  select(sh, c, inner, [&](u64 x) { return rw.units_of(logit(x)); }, by_count, target);
+  if (tid == 0) sh.thr.ties = 0;
+  const u64 sel = sh.sel;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (c[e] <= sel && c[e] >> 32 == sel >> 32) atomicAdd(&sh.thr.ties, 1u);
+  if (tid == 0) sh.thr.key = ~(uint32_t)(sel >> 32), sh.thr.total = above + sh.sel_upto;
+  __syncthreads();
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
   using V = Vec<BF16>;
   constexpr int N = V::N, EB = BF16 ? 2 : 4;
   extern __shared__ __align__(16) uint4 xs[];
@@ -324,62 +551,93 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   const int nv = (n + N - 1) / N;            // its vectors
 
   // ---- 1. load; elements outside the row are -inf
-  float mine = -INFINITY;  // fmaxf leaves NaN out
-  {
-    constexpr int U = 4;
-    for (int i0 = tid; i0 < nv; i0 += kThreads * U) {
-      uint4 v[U];
+  for (int i = tid; i < nv; i += kThreads) {
+    const int id = first + i * N;
+    if (id >= 0 && (i + 1) * N <= n) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(xs + i)),
+                   "l"(base + (int64_t)id * EB)
+                   : "memory");
+    } else {
+      uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int i = i0 + k * kThreads, id = first + i * N;
-        if (i < nv && id >= 0 && (i + 1) * N <= n) {
-          v[k] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)id * EB));
-        } else {
-          uint32_t w[4];
+      for (int q = 0; q < 4; ++q) {
+        if (BF16) {
+          uint32_t h[2];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (BF16) {
-              uint32_t h[2];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int e = id + 2 * q + z;
-                h[z] = i < nv && e >= 0 && e < a.V && i * N + 2 * q + z < n ? reinterpret_cast<const uint16_t*>(base)[e] : 0xff80u;
-              }
-              w[q] = h[0] | (h[1] << 16);
-            } else {
-              const int e = id + q;
-              w[q] = i < nv && e >= 0 && e < a.V && i * N + q < n ? reinterpret_cast<const uint32_t*>(base)[e] : 0xff800000u;
-            }
+          for (int z = 0; z < 2; ++z) {
+            const int e = id + 2 * q + z;
+            h[z] = e >= 0 && i * N + 2 * q + z < n ? reinterpret_cast<const uint16_t*>(base)[e] : 0xff80u;
           }
-          v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          w[q] = h[0] | (h[1] << 16);
+        } else {
+          w[q] = id + q >= 0 && i * N + q < n ? reinterpret_cast<const uint32_t*>(base)[id + q] : 0xff800000u;
         }
       }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int i = i0 + k * kThreads;
-        if (i < nv) xs[i] = v[k];
-        const V x(v[k]);
-#pragma unroll
-        for (int q = 0; q < N; ++q) mine = fmaxf(mine, x.f[q]);
-      }
+      xs[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+  }
+  sh.hist.cnt[tid] = sh.hist.lo[tid] = sh.hist.hi[tid] = 0;
+  if (tid == 0) sh.arg = INT_MAX, sh.listed = 0, sh.sum = 0, sh.list_sum = 0;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  float mine = -INFINITY;  // of the vectors this thread loaded; fmaxf leaves NaN out
+  for (int i = tid; i < nv; i += kThreads) {
+    const V x(xs[i]);
+#pragma unroll
+    for (int q = 0; q < N; ++q) mine = fmaxf(mine, x.f[q]);
   }
   float best = mine;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if (lane == 0) sh.seg_sum[warp] = __float_as_uint(best);
-  sh.hist[0].cnt[tid] = 0;
-  if (tid == 0) sh.arg = INT_MAX, sh.listed = 0, sh.done = 0;
+  if (lane == 0) sh.seg_tie[warp] = __float_as_uint(best);
+  const float temp = a.temperature != nullptr ? a.temperature[row] : 1.f;
+  const int top_k = a.top_k != nullptr ? a.top_k[row] : 0;
+  const float top_p = a.top_p != nullptr ? a.top_p[row] : 1.f;
+  const float min_p = a.min_p != nullptr ? fminf(a.min_p[row], 1.f) : 0.f;
+  const bool use_k = top_k > 0 && top_k < a.V, use_p = top_p < 1.f;
+  const bool listing = temp > 0.f && (use_k ? top_k <= kMaxK : use_p);
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 0; i < kWarps; ++i) best = fmaxf(best, __uint_as_float((uint32_t)sh.seg_sum[i]));
-    sh.best = best;
+  best = __uint_as_float(sh.seg_tie[lane % kWarps]);
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (tid == 0) sh.best = best;
+  if (listing) {
+    // the bin of the threads' largest logits, by distance from the CTA's, that holds the
+    // K / nb-th; the bound is the least of those in it or above it
+    const uint32_t want = ((use_k ? top_k : kCutP) + nb - 1) / nb;
+    const int mybin = Row{best, 1.f}.bin(mine);
+    if (mine > -INFINITY) atomicAdd(&sh.hist.cnt[mybin], 1u);
+    if (tid == 0) sh.pick_bin = kBins, sh.bound_key = 0xffffffffu;
+    __syncthreads();
+    uint32_t upto = sh.hist.cnt[tid];
+    const uint32_t own = upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t d = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += d;
+    }
+    if (lane == 31) sh.scan_cnt[warp] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i)
+      if (i < warp) upto += sh.scan_cnt[i];
+    if (upto >= want && upto - own < want) sh.pick_bin = tid;
+    __syncthreads();
+    if (mine > -INFINITY && mybin <= sh.pick_bin) atomicMin(&sh.bound_key, key_of(mine));
+    __syncthreads();
+    // fewer threads with a logit than that: every logit is a candidate
+    if (tid == 0) sh.bound = sh.pick_bin == kBins ? -FLT_MAX : of_key(sh.bound_key);
   }
   cluster.sync();
-  best = -INFINITY;
-  for (int i = 0; i < nb; ++i) best = fmaxf(best, cluster.map_shared_rank(&sh, i)->best);
+  best = cluster.map_shared_rank(&sh, lane < nb ? lane : 0)->best;
+  float bound = listing ? cluster.map_shared_rank(&sh, lane < nb ? lane : 0)->bound : 0.f;
+#pragma unroll
+  for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    bound = fminf(bound, __shfl_xor_sync(0xffffffffu, bound, o));
+  }
+  best = __shfl_sync(0xffffffffu, best, 0);
+  bound = __shfl_sync(0xffffffffu, bound, 0);
 
-  const float temp = a.temperature != nullptr ? a.temperature[row] : 1.f;
   const Row rw{best, 1.f / temp};
   if (best == -INFINITY || !(temp > 0.f)) {  // the same for every CTA of the row
     if (best != -INFINITY && sh.best == best) {
@@ -391,75 +649,61 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
           if (x.f[q] == best) low = min(low, first + i * N + q);
       }
       low = __reduce_min_sync(0xffffffffu, low);
-      if (lane == 0) atomicMin(&sh.arg, low);
+      if (lane == 0 && low != INT_MAX) atomicMin(&cluster.map_shared_rank(&sh, 0)->arg, low);
     }
     cluster.sync();
     if (rank == 0 && tid == 0) {
-      int low = INT_MAX;
-      for (int i = 0; i < nb; ++i) low = min(low, cluster.map_shared_rank(&sh, i)->arg);
-      a.ids[row] = best == -INFINITY ? -1 : low;
+      a.ids[row] = best == -INFINITY ? -1 : sh.arg;
       if (a.logprob != nullptr) a.logprob[row] = best == -INFINITY ? -INFINITY : 0.f;
     }
-    cluster.sync();
     return;
   }
 
-  const int top_k = a.top_k != nullptr ? a.top_k[row] : 0;
-  const float top_p = a.top_p != nullptr ? a.top_p[row] : 1.f;
-  const float min_p = a.min_p != nullptr ? fminf(a.min_p[row], 1.f) : 0.f;
-  const bool use_k = top_k > 0 && top_k < a.V, use_p = top_p < 1.f;
-
   // ---- 2. candidates
-  if ((use_k && top_k <= kMaxK) || (!use_k && use_p)) {
-    if (mine > -INFINITY) atomicAdd(&sh.hist[0].cnt[rw.bin(mine)], 1u);
-    __syncthreads();
-    find_bin(cluster, sh, 0, true, use_k ? (u64)top_k : (u64)kCutP);
-    // candidates: bin at most pick_bin; everything where the threads are fewer than K
-    const float below = sh.pick_bin >= kBins - 1 ? INFINITY : (float)(sh.pick_bin + 1);
-    cluster.sync();  // every CTA has read the counts: the list may take their place
-    u64 sum = 0;
+  if (listing) {
+    u64 sum = 0, list_sum = 0;
     const bool totals = !use_k;
     for (int i = tid; i < nv; i += kThreads) {
       const V x(xs[i]);
+      uint32_t w[N];
+      if (totals) {
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        if (totals) sum += rw.units_of(x.f[q]);
-        if ((rw.m - x.f[q]) * kBinsPerUnit < below || x.f[q] == rw.m) {
-          const int at = atomicAdd(&sh.listed, 1);
-          if (at < kList) sh.list[at] = ((u64)~key_of(x.f[q]) << 32) | (uint32_t)(first + i * N + q);
-        }
+        for (int q = 0; q < N; ++q) w[q] = rw.units_of(x.f[q]);
+#pragma unroll
+        for (int q = 0; q < N; ++q) sum += w[q];
+      }
+      bool in[N], any = false;
+#pragma unroll
+      for (int q = 0; q < N; ++q) any |= in[q] = x.f[q] >= bound;
+      if (any) {
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          if (in[q]) {
+            if (totals) list_sum += w[q];
+            const int at = atomicAdd(&sh.listed, 1);
+            if (at < kList) sh.list[at] = ((u64)~key_of(x.f[q]) << 32) | (uint32_t)(first + i * N + q);
+          }
       }
     }
     if (totals) {
       sum = warp_sum(sum);
-      if (lane == 0) sh.seg_sum[warp] = sum;
-      __syncthreads();
-      if (tid == 0) {
-        for (int i = 1; i < kWarps; ++i) sum += sh.seg_sum[i];
-        sh.sum = sum;
-      }
+      list_sum = warp_sum(list_sum);
+      if (lane == 0) atomicAdd(&sh.sum, sum), atomicAdd(&sh.list_sum, list_sum);
     }
     cluster.sync();
-    if (rank == 0) {
-      int total = 0;
-      bool fits = true;
-      u64 weights = 0;
-      for (int i = 0; i < nb; ++i) {
-        const Shared* o = cluster.map_shared_rank(&sh, i);
-        const int c = o->listed;
-        fits = fits && c <= kList && total + c <= kMerged;
-        if (fits)
-          for (int k = tid; k < c; k += kThreads) sh.merged[total + k] = o->list[k];
-        total += c;
-        if (totals) weights += o->sum;
+    const Listed l = read_listed(cluster, sh);  // the same in every CTA
+    if (l.fits && (use_k || l.list_sum >= least_weight(l.sum, top_p))) {
+      if (rank == 0) merge_lists(cluster, sh, l);
+      cluster.sync();  // the other CTAs are done
+      if (rank == 0) {
+        if (l.total <= kPairs)
+          compare_and_draw(sh, a, rw, row, l.total, top_k, use_k, top_p, use_p, min_p, l.sum);
+        else
+          select_and_draw(sh, a, rw, row, l.total, top_k, use_k, top_p, use_p, min_p, l.sum);
       }
-      __syncthreads();
-      if (fits && cut_and_draw(sh, a, rw, row, total, top_k, use_k, top_p, use_p, min_p, weights) && tid == 0) sh.done = 1;
+      return;
     }
-    cluster.sync();
-    const bool done = cluster.map_shared_rank(&sh, 0)->done != 0;
-    cluster.sync();
-    if (done) return;
+    cluster.sync();  // every CTA has read the lists' sizes
   }
 
   // ---- 3. histogram over the distance from the largest
@@ -473,76 +717,80 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         if (x.f[q] > -INFINITY) f(x.f[q]);
     }
   };
-  auto add = [&](int b, int bin, float x) {
-    const uint32_t w = rw.units_of(x);
-    atomicAdd(&sh.hist[b].cnt[bin], 1u);
+  auto add = [&](Histogram& h, int bin, float x, bool weigh) {
+    atomicAdd(&h.cnt[bin], 1u);
+    const uint32_t w = weigh ? rw.units_of(x) : 0;
     if (w) {
-      atomicAdd(&sh.hist[b].lo[bin], w & 0xffffu);
-      atomicAdd(&sh.hist[b].hi[bin], w >> 16);
+      atomicAdd(&h.lo[bin], w & 0xffffu);
+      atomicAdd(&h.hi[bin], w >> 16);
     }
   };
   if (use_k || use_p) {
-    sh.hist[0].cnt[tid] = sh.hist[0].lo[tid] = sh.hist[0].hi[tid] = 0;
+    sh.hist.cnt[tid] = sh.hist.lo[tid] = sh.hist.hi[tid] = 0;
     __syncthreads();
-    elements([&](float x) { add(0, rw.bin(x), x); });
-    __syncthreads();
+    elements([&](float x) { add(sh.hist, rw.bin(x), x, use_p); });
     u64 total = 0;
     for (int mode = use_k ? 0 : 1; mode <= (use_p ? 1 : 0); ++mode) {
       // mode 0: the top_k-th token; mode 1: the token at which the weight reaches top_p
-      u64 target;
-      if (mode == 0) {
-        target = (u64)top_k;
-      } else {
-        if (!use_k) total = find_bin(cluster, sh, 0, false, 1);
-        target = max((u64)1, share(total, top_p > 0.f ? top_p : 0.f));
-      }
-      const u64 all = find_bin(cluster, sh, 0, false, mode == 0 ? 1 : target);
-      if (mode == 0) find_bin(cluster, sh, 0, true, target);
+      if (mode == 1 && !use_k) total = find_bin(cluster, sh, &sh.hist, false, 1);
+      const u64 target = mode == 0 ? (u64)top_k : least_weight(total, top_p);
+      const u64 all = find_bin(cluster, sh, &sh.hist, mode == 0, target);
       if (sh.pick_bin == kBins) {  // top_k exceeds the logits above -inf: none is cut
         total = all;
         continue;
       }
       const int bin = sh.pick_bin;
-      u64 above = 0;
-      uint32_t above_cnt = sh.pick_cnt;
-      if (mode == 1) above = sh.pick_above;
+      const u64 above = sh.pick_above;
+      const uint32_t above_cnt = sh.pick_cnt;
+      const u64 inside = target - (mode == 0 ? above_cnt : above);
+      if (tid == 0) sh.listed = 0;
+      __syncthreads();
+      for (int i = tid; i < nv; i += kThreads) {
+        const V x(xs[i]);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          if (x.f[q] > -INFINITY && rw.bin(x.f[q]) == bin) {
+            const int at = atomicAdd(&sh.listed, 1);
+            if (at < kList) sh.list[at] = ((u64)~key_of(x.f[q]) << 32) | (uint32_t)(first + i * N + q);
+          }
+      }
+      cluster.sync();
+      const Listed l = read_listed(cluster, sh);
+      if (l.fits) {
+        if (rank == 0) {
+          merge_lists(cluster, sh, l);
+          find_in_bin(sh, rw, l.total, bin, mode == 0, inside, above);
+          if (tid > 0 && tid < nb) cluster.map_shared_rank(&sh, tid)->thr = sh.thr;
+        }
+        cluster.sync();
+        key_t = sh.thr.key, ties = sh.thr.ties;
+        total = sh.thr.total;
+        continue;
+      }
       // inside the bin, 8 bits of the key at a time
       uint32_t prefix = 0;
+      u64 over = above;
+      uint32_t over_cnt = above_cnt;
       for (int level = 0; level < 4; ++level) {
         const int sft = 24 - 8 * level;
-        __syncthreads();
-        cluster.sync();  // every CTA has read histogram 1 of the level before
-        sh.hist[1].cnt[tid] = sh.hist[1].lo[tid] = sh.hist[1].hi[tid] = 0;
+        cluster.sync();  // every CTA has read the list, or the level before
+        sh.level.cnt[tid] = sh.level.lo[tid] = sh.level.hi[tid] = 0;
         __syncthreads();
         elements([&](float x) {
           if (rw.bin(x) != bin) return;
           const uint32_t k = key_of(x);
-          if (level == 0 || (k >> (sft + 8)) == prefix) add(1, 255 - ((k >> sft) & 255), x);  // descending
+          if (level == 0 || (k >> (sft + 8)) == prefix) add(sh.level, 255 - ((k >> sft) & 255), x, use_p);  // descending
         });
-        __syncthreads();
-        find_bin(cluster, sh, 1, mode == 0, mode == 0 ? target - above_cnt : target - above);
-        above += sh.pick_above;
-        above_cnt += sh.pick_cnt;
+        find_bin(cluster, sh, &sh.level, mode == 0, target - (mode == 0 ? over_cnt : over));
+        over += sh.pick_above;
+        over_cnt += sh.pick_cnt;
         prefix = (prefix << 8) | (255 - sh.pick_bin);
       }
       key_t = prefix;
       const u64 each = rw.units_of(of_key(key_t));
-      if (mode == 0) {
-        ties = (uint32_t)(target - above_cnt);
-        // the weight above the bin, which the search by count does not add up
-        __syncthreads();
-        cluster.sync();
-        u64 w = 0;
-        if (tid < bin)
-          for (int i = 0; i < nb; ++i) {
-            const Histogram& o = cluster.map_shared_rank(&sh, i)->hist[0];
-            w += ((u64)o.hi[tid] << 16) + o.lo[tid];
-          }
-        block_scan(sh, w, &total);
-        total += above + each * ties;
-      } else {
-        ties = (uint32_t)((target - above + each - 1) / each);
-      }
+      ties = (uint32_t)(mode == 0 ? target - over_cnt : (target - over + each - 1) / each);
+      total = over + each * ties;
+      cluster.sync();  // before the list takes the level's place
     }
   }
 
@@ -555,20 +803,36 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   const bool tie_ok = !all_keys && !(rw.weight(x_t) < min_p);
   // an element's weight if it lies above the threshold (ties are counted apart)
   auto kept = [&](float x) -> uint32_t {
-    const float z = (x - rw.m) * rw.r;
-    if (x == rw.m) return x > x_t ? 0x80000000u : 0u;
-    if (!(x > x_t && z > kZeroBelow)) return 0;
-    const float w = expf(z);
-    return w < min_p ? 0u : Row::units(w);
+    const float w = expf(x == rw.m ? 0.f : (x - rw.m) * rw.r);
+    return x > x_t && !(w < min_p) ? Row::units(w) : 0u;
   };
   u64 sum = 0;
   uint32_t nt = 0;
-  for (int i = s0 + lane; i < s1; i += 32) {
-    const V x(xs[i]);
+  if (all_keys && !(min_p > 0.f)) {
+    for (int i = s0 + lane; i < s1; i += 32) {
+      const V x(xs[i]);
+      uint32_t w[N];
 #pragma unroll
-    for (int q = 0; q < N; ++q) {
-      sum += kept(x.f[q]);
-      nt += x.f[q] == x_t;  // -inf where nothing is cut: tie_ok is false then
+      for (int q = 0; q < N; ++q) w[q] = rw.units_of(x.f[q]);
+#pragma unroll
+      for (int q = 0; q < N; ++q) sum += w[q];
+    }
+  } else {
+    // a vector whose elements are all cut needs no weights: none above the threshold, or all
+    // safely below min_p (z below log(min_p) by more than logf and expf can be off)
+    const float z_cut = min_p > 0.f ? logf(min_p) - 0.01f : -INFINITY;
+    for (int i = s0 + lane; i < s1; i += 32) {
+      const V x(xs[i]);
+      bool any = false;
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        any |= x.f[q] > x_t && ((x.f[q] - rw.m) * rw.r > z_cut || x.f[q] == rw.m);
+        nt += x.f[q] == x_t;  // -inf where nothing is cut: tie_ok is false then
+      }
+      if (any) {
+#pragma unroll
+        for (int q = 0; q < N; ++q) sum += kept(x.f[q]);
+      }
     }
   }
   sum = warp_sum(sum);
@@ -578,27 +842,29 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   const int segs = nb * kWarps;
   if (warp == 0) {
     // every CTA: running ties and sums over all segments
-    u64 run = 0;
-    uint32_t run_t = 0;
-    for (int s = lane; s < ((segs + 31) & ~31); s += 32) {
-      u64 v = 0;
-      uint32_t t = 0;
-      if (s < segs) {
-        const Shared* o = cluster.map_shared_rank(&sh, s / kWarps);
-        v = o->seg_sum[s % kWarps];
-        t = o->seg_tie[s % kWarps];
-      }
-      uint32_t ti = t;
+    constexpr int R = kMaxCluster * kWarps / 32;
+    u64 sums[R], run = 0;
+    uint32_t tied[R], run_t = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int s = i * 32 + lane;
+      const Shared* o = cluster.map_shared_rank(&sh, s < segs ? s / kWarps : 0);
+      sums[i] = s < segs ? o->seg_sum[s % kWarps] : 0;
+      tied[i] = s < segs ? o->seg_tie[s % kWarps] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int s = i * 32 + lane;
+      uint32_t ti = tied[i];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t d = __shfl_up_sync(0xffffffffu, ti, o);
         if (lane >= o) ti += d;
       }
-      const uint32_t before = run_t + ti - t;
+      const uint32_t before = run_t + ti - tied[i];
       run_t += __shfl_sync(0xffffffffu, ti, 31);
-      const uint32_t in = before >= ties ? 0 : min(t, ties - before);
-      if (tie_ok) v += (u64)in * unit_t;
-      const u64 vi = warp_scan(v, lane) + run;
+      const uint32_t in = before >= ties ? 0 : min(tied[i], ties - before);
+      const u64 vi = warp_scan(sums[i] + (tie_ok ? (u64)in * unit_t : 0), lane) + run;
       run = __shfl_sync(0xffffffffu, vi, 31);
       if (s < segs) sh.all_sum[s] = vi;
       if (s >= rank * kWarps && s < (rank + 1) * kWarps) sh.scan_cnt[s - rank * kWarps] = before;
@@ -679,7 +945,7 @@ extern "C" int moe_sample_tokens(const void* logits, int is_bf16, int T, int V, 
       off(ids_out, 4) || off(logprob_out, 4))
     return PMOE_EINVAL;
   int cluster = 1;
-  while (cluster < kMaxCluster && V > cluster * 2048) cluster *= 2;
+  while (cluster < kMaxCluster && V > cluster * 4096) cluster *= 2;
   if ((int64_t)T * cluster > INT32_MAX) return PMOE_EINVAL;
   SampleArgs a{logits, T, V, row_stride, temperature, top_k, top_p, min_p, u, ids_out, logprob_out, 0};
   // 7: the most elements by which a row can start after its first 16-byte vector
