@@ -38,6 +38,7 @@ struct Args {
   // tile, kv head) group, tc_tiles units to a group, in group order; CTA c takes units
   // [c * U / tc_ctas, (c + 1) * U / tc_ctas). A group's parts are numbered from its first CTA.
   int tc_ctas, tc_tiles;
+  uint32_t group_magic;  // 2^32 / group + 1
 };
 
 constexpr int kTcRows = 256;  // query rows of a group

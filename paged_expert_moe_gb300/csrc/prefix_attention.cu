@@ -467,6 +467,7 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   a->T = T;
   a->q_heads = q_heads;
   a->group = q_heads / kv->kv_heads;
+  a->group_magic = (uint32_t)((1ull << 32) / a->group + 1);  // of no use for 1
   a->prefix_len = prefix_len;
   a->max_suffix = max_suffix;
   if (a->group > kMaxGroup) return PMOE_EUNSUPPORTED;

@@ -50,12 +50,27 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// r / group for r < 2^24 and group <= 64: magic = 2^32 / group + 1
+__device__ __forceinline__ int row_token(const Args& a, int r) { return a.group == 1 ? r : (int)__umulhi((uint32_t)r, a.group_magic); }
+
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t sfull[2], pready[2], odone[2], qfull[2], drain;
+  uint64_t sfull[2], pready[2], odone[2], qfull[2], staged[2], drain;
   uint32_t tmem;
   int abort;
 };
+
+// One lane waits and one lane arrives for its warp: 128 threads that poll or arrive at the
+// same barrier hold one another up for longer than a tile's products take.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 // One segment of a CTA's run: key tiles [t0, t1) of one group.
 struct Segment {
@@ -90,14 +105,15 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&b.full[i], F8 ? 128 : 1);
+      mbar_init(&b.full[i], F8 ? 4 : 1);
       mbar_init(&b.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.sfull[i], 1);
-      mbar_init(&b.pready[i], 128);
+      mbar_init(&b.pready[i], 4);
       mbar_init(&b.odone[i], 1);
-      mbar_init(&b.qfull[i], 128);
+      mbar_init(&b.qfull[i], 4);
+      mbar_init(&b.staged[i], 4);
     }
     mbar_init(&b.drain, 1);
     b.abort = 0;
@@ -137,7 +153,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       // A negative scale goes into the sign of Q, so that the largest score stays the largest.
       const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
       const int c = row % LPR;
-      constexpr int kPasses = LPR, kAhead = 8;  // rows of a thread, and how many it has in flight
+      constexpr int kPasses = LPR, kAhead = F8 ? 8 : LPR;  // rows of a thread, and how many it has in flight
 #pragma unroll
       for (int p0 = 0; p0 < kPasses; p0 += kAhead) {
         uint4 v[kAhead];
@@ -146,9 +162,9 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           const int i = q * 128 + row / LPR + (p0 + p) * (128 / LPR);
           v[p] = make_uint4(0, 0, 0, 0);
           if (i < sg.rows) {
-            const int rr = sg.row0 + i;
-            v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(rr / a.group) * a.q_stride +
-                                                        (sg.h * a.group + rr % a.group) * D + c * 8));
+            const int rr = sg.row0 + i, t = row_token(a, rr);
+            v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)t * a.q_stride +
+                                                        (sg.h * a.group + rr - t * a.group) * D + c * 8));
           }
         }
 #pragma unroll
@@ -174,14 +190,14 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
         }
       }
       fence_async();
-      mbar_arrive(&b.qfull[q]);
+      warp_arrive(&b.qfull[q]);
       // the row factors of all threads
-      if (!__all_sync(0xffffffffu, mbar_wait(&b.qfull[q], segs++ & 1, abort_flag, a.err))) break;
+      if (!warp_wait(&b.qfull[q], segs++ & 1, abort_flag, a.err)) break;
       const float mul = F8 ? qmul[q * 128 + row] : fabsf(a.scale);
 
       float m = -INFINITY, l = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++n) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&b.sfull[q], n & 1, abort_flag, a.err))) {
+        if (!warp_wait(&b.sfull[q], n & 1, abort_flag, a.err)) {
           ok = false;
           break;
         }
@@ -226,7 +242,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           const bool grow = mx > m + 8.f;
           if (__any_sync(0xffffffffu, grow)) {
             // the products so far have to be done before their sums are rescaled
-            if (!__all_sync(0xffffffffu, mbar_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err))) {
+            if (!warp_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err)) {
               ok = false;
               break;
             }
@@ -264,28 +280,51 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         fence_before();
-        mbar_arrive(&b.pready[q]);
+        warp_arrive(&b.pready[q]);
       }
       if (!ok) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err))) break;
+      if (!warp_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err)) break;
       fence_after();
-      const int i = q * 128 + row, rr = sg.row0 + i;
-      const int64_t at = (int64_t)sg.part * a.T * a.q_heads + (int64_t)(rr / a.group) * a.q_heads + sg.h * a.group + rr % a.group;
+      // 32 columns at a time through shared memory (the query tile's, which is done with), so
+      // that a store covers whole lines: 8 threads a row of 128 bytes, whose 16-byte chunks
+      // are swizzled by the row
       const float vs = F8 ? a.kv.v_scale[sg.h] : 1.f;
-#pragma unroll 1
-      for (int k = 0; k < D; k += 16) {
-        uint32_t o[16];
-        tmem_ld16(to + k, o);
-        tmem_wait_ld();
-        if (i < sg.rows) {
-          float* dst = a.o_part + at * D + k;
+      const int64_t part0 = (int64_t)sg.part * a.T * a.q_heads;
+      uint8_t* stage = qs + q * C::kQBytes + (warp & 3) * (C::kQBytes / 4);
+      float* dst[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(dst + e) = make_float4(__uint_as_float(o[e]) * vs, __uint_as_float(o[e + 1]) * vs,
-                                                              __uint_as_float(o[e + 2]) * vs, __uint_as_float(o[e + 3]) * vs);
-        }
+      for (int k = 0; k < 8; ++k) {
+        const int i = q * 128 + (warp & 3) * 32 + 4 * k + (lane >> 3), rr = sg.row0 + i, tok = row_token(a, rr);
+        dst[k] = i < sg.rows ? a.o_part + (part0 + (int64_t)tok * a.q_heads + sg.h * a.group + rr - tok * a.group) * D + (lane & 7) * 4
+                             : nullptr;
       }
-      if (i < sg.rows) a.ml_part[at] = make_float2(m, l);
+#pragma unroll
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(to + d, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+              make_float4(__uint_as_float(o[4 * k]) * vs, __uint_as_float(o[4 * k + 1]) * vs,
+                          __uint_as_float(o[4 * k + 2]) * vs, __uint_as_float(o[4 * k + 3]) * vs);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3);
+          const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (dst[k] != nullptr) *reinterpret_cast<float4*>(dst[k] + d) = v;
+        }
+        __syncwarp();
+      }
+      const int i = q * 128 + row;
+      if (i < sg.rows) {
+        const int rr = sg.row0 + i, tok = row_token(a, rr);
+        a.ml_part[part0 + (int64_t)tok * a.q_heads + sg.h * a.group + rr - tok * a.group] = make_float2(m, l);
+      }
+      // every warp is done with its stage before Q is written again
+      warp_arrive(&b.staged[q]);
+      if (!warp_wait(&b.staged[q], (segs - 1) & 1, abort_flag, a.err)) break;
       fence_before();
     }
   } else if (warp == 8) {
@@ -298,10 +337,10 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     uint32_t pn[2] = {0, 0};       // products with V of each query tile so far
     bool ok = true;
     auto wait_kv = [&](uint32_t i) {
-      return __all_sync(0xffffffffu, mbar_wait(&b.full[i % kSlots], (i / kSlots) & 1, abort_flag, a.err));
+      return warp_wait(&b.full[i % kSlots], (i / kSlots) & 1, abort_flag, a.err);
     };
     auto scores = [&](int q, uint32_t slot) {
-      if (lane == 0) {
+      if (converged_lane()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
@@ -314,13 +353,13 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     };
     while (ok && segment(a, &u, end, &sg)) {
       for (int q = 0; q < sg.nq && ok; ++q) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&b.qfull[q], seg[q] & 1, abort_flag, a.err));
+        ok = warp_wait(&b.qfull[q], seg[q] & 1, abort_flag, a.err);
         ++seg[q];
       }
       if (!ok || !wait_kv(kv)) break;
       fence_after();
       for (int q = 0; q < sg.nq; ++q) scores(q, kv % kSlots);
-      if (lane == 0) mma_commit(&b.empty[kv % kSlots]);
+      if (converged_lane()) mma_commit(&b.empty[kv % kSlots]);
       __syncwarp();
       for (int t = sg.t0; t < sg.t1; ++t, kv += 2) {
         const uint32_t vslot = (kv + 1) % kSlots;
@@ -340,13 +379,13 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           __syncwarp();
         }
         for (int q = 0; q < sg.nq; ++q) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&b.pready[q], pn[q] & 1, abort_flag, a.err))) {
+          if (!warp_wait(&b.pready[q], pn[q] & 1, abort_flag, a.err)) {
             ok = false;
             break;
           }
           ++pn[q];
           fence_after();
-          if (lane == 0) {
+          if (converged_lane()) {
 #pragma unroll
             for (int k = 0; k < kTcKeys / 16; ++k)
               mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
@@ -364,7 +403,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           }
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (converged_lane()) {
           mma_commit(&b.empty[vslot]);
           if (more) mma_commit(&b.empty[(kv + 2) % kSlots]);
         }
@@ -372,7 +411,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       }
     }
     // every MMA and its arrival are done before the CTA leaves
-    if (lane == 0) {
+    if (converged_lane()) {
       mma_commit(&b.drain);
       const long long t0 = clock64();
       while (!mbar_try_wait(&b.drain, 0) && clock64() - t0 < kWaitLimit) {
@@ -400,7 +439,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
         }
         for (int v = 0; v < 2; ++v, ++kv) {
           const uint32_t slot = kv % kSlots;
-          if (!__all_sync(0xffffffffu, mbar_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err))) {
+          if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) {
             ok = false;
             break;
           }
@@ -447,7 +486,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           for (int i = 0; i < N; ++i)
             raw[i] = off[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + off[i])) : make_uint4(0, 0, 0, 0);
           const uint32_t slot = kv % kSlots;
-          if (!__all_sync(0xffffffffu, mbar_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err))) {
+          if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) {
             ok = false;
             break;
           }
@@ -469,7 +508,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
             }
           }
           fence_async();
-          mbar_arrive(&b.full[slot]);
+          warp_arrive(&b.full[slot]);
         }
       }
     }
