@@ -55,21 +55,41 @@ __device__ __forceinline__ int row_token(const Args& a, int r) { return a.group 
 
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t sfull[2], pready[2], odone[2], qfull[2], staged[2], drain;
+  uint64_t sfull[2], pready[2][2], odone[2], qfull[2], staged[2], drain;
   uint32_t tmem;
   int abort;
 };
 
-// One lane waits and one lane arrives for its warp: 128 threads that poll or arrive at the
-// same barrier hold one another up for longer than a tile's products take.
+// Waits by all lanes of a warp, the same answer for all; arrivals by one lane a warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+// pairs of floats in one 64-bit register
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // One segment of a CTA's run: key tiles [t0, t1) of one group.
@@ -110,7 +130,8 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.sfull[i], 1);
-      mbar_init(&b.pready[i], 4);
+      mbar_init(&b.pready[i][0], 4);
+      mbar_init(&b.pready[i][1], 4);
       mbar_init(&b.odone[i], 1);
       mbar_init(&b.qfull[i], 4);
       mbar_init(&b.staged[i], 4);
@@ -226,13 +247,13 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
               if (i >= valid) s[i] = -INFINITY;
           }
 #pragma unroll
-          for (int i = 0; i < 128; ++i) x[i & 3] = fmaxf(x[i & 3], s[i]);
+          for (int i = 0; i < 128; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             fetch(i, s);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k & 3] = fmaxf(x[k & 3], s[k]);
+            for (int k = 0; k < 32; k += 2) x[(k >> 1) & 3] = max3(x[(k >> 1) & 3], s[k], s[k + 1]);
           }
         }
         const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
@@ -262,7 +283,8 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t mul2 = pair(mul, mul), base2 = pair(-base, -base);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t p[16];
@@ -270,17 +292,22 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           const float* sc = F8 ? s : s + 32 * i;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float y = ex2(fmaf(sc[2 * k], mul, -base)), z = ex2(fmaf(sc[2 * k + 1], mul, -base));
-            sum[2 * (k & 1)] += y;
-            sum[2 * (k & 1) + 1] += z;
+            float y, z;
+            unpair(fma2(pair(sc[2 * k], sc[2 * k + 1]), mul2, base2), y, z);
+            y = ex2(y), z = ex2(z);
+            sum[k & 1] = add2(sum[k & 1], pair(y, z));
             p[k] = pack2<F8>(y, z);
           }
           tmem_st16(ts + 16 * i, p);
+          if (i & 1) {  // the products start on the first 64 keys
+            tmem_wait_st();
+            fence_before();
+            warp_arrive(&b.pready[q][i >> 1]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        fence_before();
-        warp_arrive(&b.pready[q]);
+        float y, z;
+        unpair(add2(sum[0], sum[1]), y, z);
+        l += y + z;
       }
       if (!ok) break;
       if (!warp_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err)) break;
@@ -364,7 +391,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       for (int t = sg.t0; t < sg.t1; ++t, kv += 2) {
         const uint32_t vslot = (kv + 1) % kSlots;
         const bool more = t + 1 < sg.t1;
-        if (!wait_kv(kv + 1)) {
+        if (!wait_kv(kv + 1) || (more && !wait_kv(kv + 2))) {
           ok = false;
           break;
         }
@@ -379,28 +406,25 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           __syncwarp();
         }
         for (int q = 0; q < sg.nq; ++q) {
-          if (!warp_wait(&b.pready[q], pn[q] & 1, abort_flag, a.err)) {
-            ok = false;
-            break;
-          }
-          ++pn[q];
-          fence_after();
-          if (converged_lane()) {
 #pragma unroll
-            for (int k = 0; k < kTcKeys / 16; ++k)
-              mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
-                         t > sg.t0 || k > 0);
-            mma_commit(&b.odone[q]);
-          }
-          __syncwarp();
-          if (more) {
-            if (q == 0 && !wait_kv(kv + 2)) {
+          for (int half = 0; half < 2; ++half) {
+            if (!warp_wait(&b.pready[q][half], pn[q] & 1, abort_flag, a.err)) {
               ok = false;
               break;
             }
             fence_after();
-            scores(q, (kv + 2) % kSlots);
+            if (converged_lane()) {
+#pragma unroll
+              for (int k = half * (kTcKeys / 32); k < (half + 1) * (kTcKeys / 32); ++k)
+                mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
+                           t > sg.t0 || k > 0);
+              if (half == 1) mma_commit(&b.odone[q]);
+            }
+            __syncwarp();
           }
+          if (!ok) break;
+          ++pn[q];
+          if (more) scores(q, (kv + 2) % kSlots);
         }
         if (!ok) break;
         if (converged_lane()) {
