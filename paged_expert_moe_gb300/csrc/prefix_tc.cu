@@ -262,12 +262,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
         } else {
           const bool grow = mx > m + 8.f;
           if (__any_sync(0xffffffffu, grow)) {
-            // the products so far have to be done before their sums are rescaled
-            if (!warp_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err)) {
-              ok = false;
-              break;
-            }
-            fence_after();
+            // the products so far are done: these scores were issued after them
             const float f = grow ? ex2(m - mx) : 1.f;
             if (grow) m = mx;
             l *= f;
@@ -310,7 +305,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
         l += y + z;
       }
       if (!ok) break;
-      if (!warp_wait(&b.odone[q], (n - 1) & 1, abort_flag, a.err)) break;
+      if (!warp_wait(&b.odone[q], (segs - 1) & 1, abort_flag, a.err)) break;
       fence_after();
       // 32 columns at a time through shared memory (the query tile's, which is done with), so
       // that a store covers whole lines: 8 threads a row of 128 bytes, whose 16-byte chunks
@@ -366,7 +361,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     auto wait_kv = [&](uint32_t i) {
       return warp_wait(&b.full[i % kSlots], (i / kSlots) & 1, abort_flag, a.err);
     };
-    auto scores = [&](int q, uint32_t slot) {
+    auto scores = [&](int q, uint32_t slot, bool last) {  // last: of the query tiles on this slot
       if (converged_lane()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -375,6 +370,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
                    k > 0);
         }
         mma_commit(&b.sfull[q]);
+        if (last) mma_commit(&b.empty[slot]);
       }
       __syncwarp();
     };
@@ -385,9 +381,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       }
       if (!ok || !wait_kv(kv)) break;
       fence_after();
-      for (int q = 0; q < sg.nq; ++q) scores(q, kv % kSlots);
-      if (converged_lane()) mma_commit(&b.empty[kv % kSlots]);
-      __syncwarp();
+      for (int q = 0; q < sg.nq; ++q) scores(q, kv % kSlots, q + 1 == sg.nq);
       for (int t = sg.t0; t < sg.t1; ++t, kv += 2) {
         const uint32_t vslot = (kv + 1) % kSlots;
         const bool more = t + 1 < sg.t1;
@@ -418,20 +412,18 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
               for (int k = half * (kTcKeys / 32); k < (half + 1) * (kTcKeys / 32); ++k)
                 mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
                            t > sg.t0 || k > 0);
-              if (half == 1) mma_commit(&b.odone[q]);
+              if (half == 1) {
+                if (!more) mma_commit(&b.odone[q]);
+                if (q + 1 == sg.nq) mma_commit(&b.empty[vslot]);
+              }
             }
             __syncwarp();
           }
           if (!ok) break;
           ++pn[q];
-          if (more) scores(q, (kv + 2) % kSlots);
+          if (more) scores(q, (kv + 2) % kSlots, q + 1 == sg.nq);
         }
         if (!ok) break;
-        if (converged_lane()) {
-          mma_commit(&b.empty[vslot]);
-          if (more) mma_commit(&b.empty[(kv + 2) % kSlots]);
-        }
-        __syncwarp();
       }
     }
     // every MMA and its arrival are done before the CTA leaves
