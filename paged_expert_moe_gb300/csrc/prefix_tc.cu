@@ -10,7 +10,7 @@
 // Warp 8 issues the MMAs, in the order O0 += P0 V, S0 of the next tile, O1 += P1 V, S1 of
 // the next tile, so that one query tile's softmax runs under the other's products. Warp 9
 // loads K and V tiles by TMA, one box a page and 64 columns, into a ring of five 128-key
-// tiles; with an e4m3 cache warps 9-12 read them, convert to fp16 (exact) and write the
+// tiles; with an e4m3 cache warps 12-15 read them, convert to fp16 (exact) and write the
 // same layout.
 //
 // The running maximum of a row moves only when a score exceeds it by 2^8 (any base gives the
@@ -36,8 +36,12 @@ struct TcCfg {
   static constexpr int kTileBytes = kTcKeys * D * 2;      // one K or V tile, 16-bit operands
   static constexpr int kQBytes = 128 * D * 2;             // one query tile
   static constexpr int kSlots = D == 128 ? 5 : 8;         // ring of K and V tiles
-  static constexpr int kLoaders = F8 ? 4 : 1;             // loading warps
-  static constexpr int kThreads = (9 + kLoaders) * 32;
+  static constexpr int kThreads = F8 ? 512 : 384;         // whole warpgroups
+  // Registers a thread, by warpgroup: what the other roles give up the softmax takes. The
+  // launch has 168 x 384 = 64,512 (bf16) or 128 x 512 = 65,536 (e4m3) of them; the shares add
+  // up to 200 x 256 + 104 x 128 = 64,512 and 160 x 256 + 88 x 128 + 104 x 128 = 65,536.
+  static constexpr int kSoftmaxRegs = F8 ? 160 : 200, kMmaRegs = F8 ? 88 : 104;
+  static constexpr int kLoaderRegs = F8 ? 104 : 0;
   static constexpr int kRing = kSlots * kTileBytes;
   static constexpr int kSmem = kRing + 2 * kQBytes + 1024 /* alignment */ + 1024 /* row factors */ + 512;
   static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
@@ -55,7 +59,7 @@ __device__ __forceinline__ int row_token(const Args& a, int r) { return a.group 
 
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t sfull[2], pready[2][2], odone[2], qfull[2], staged[2], drain;
+  uint64_t sfull[2], pready[2], odone[2], qfull[2], staged[2], drain;
   uint32_t tmem;
   int abort;
 };
@@ -130,8 +134,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.sfull[i], 1);
-      mbar_init(&b.pready[i][0], 4);
-      mbar_init(&b.pready[i][1], 4);
+      mbar_init(&b.pready[i], 4);
       mbar_init(&b.odone[i], 1);
       mbar_init(&b.qfull[i], 4);
       mbar_init(&b.staged[i], 4);
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
 
   if (warp < 8) {
     // ---------------- softmax: one thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     const int q = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + q * 128, to = lanes + 256 + q * 128;
@@ -294,12 +298,10 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
             p[k] = pack2<F8>(y, z);
           }
           tmem_st16(ts + 16 * i, p);
-          if (i & 1) {  // the products start on the first 64 keys
-            tmem_wait_st();
-            fence_before();
-            warp_arrive(&b.pready[q][i >> 1]);
-          }
         }
+        tmem_wait_st();
+        fence_before();
+        warp_arrive(&b.pready[q]);
         float y, z;
         unpair(add2(sum[0], sum[1]), y, z);
         l += y + z;
@@ -349,7 +351,9 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       if (!warp_wait(&b.staged[q], (segs - 1) & 1, abort_flag, a.err)) break;
       fence_before();
     }
-  } else if (warp == 8) {
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
+    if (warp == 8) {
     // ---------------- MMA issuer
     const uint32_t is = idesc_bf16(128, kTcKeys) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u);
     const uint32_t io = (idesc_bf16(128, D) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u)) | (1u << 16);  // B: N contiguous
@@ -400,27 +404,21 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           __syncwarp();
         }
         for (int q = 0; q < sg.nq; ++q) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!warp_wait(&b.pready[q][half], pn[q] & 1, abort_flag, a.err)) {
-              ok = false;
-              break;
-            }
-            fence_after();
-            if (converged_lane()) {
-#pragma unroll
-              for (int k = half * (kTcKeys / 32); k < (half + 1) * (kTcKeys / 32); ++k)
-                mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
-                           t > sg.t0 || k > 0);
-              if (half == 1) {
-                if (!more) mma_commit(&b.odone[q]);
-                if (q + 1 == sg.nq) mma_commit(&b.empty[vslot]);
-              }
-            }
-            __syncwarp();
+          if (!warp_wait(&b.pready[q], pn[q] & 1, abort_flag, a.err)) {
+            ok = false;
+            break;
           }
-          if (!ok) break;
           ++pn[q];
+          fence_after();
+          if (converged_lane()) {
+#pragma unroll
+            for (int k = 0; k < kTcKeys / 16; ++k)
+              mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
+                         t > sg.t0 || k > 0);
+            if (!more) mma_commit(&b.odone[q]);
+            if (q + 1 == sg.nq) mma_commit(&b.empty[vslot]);
+          }
+          __syncwarp();
           if (more) scores(q, (kv + 2) % kSlots, q + 1 == sg.nq);
         }
         if (!ok) break;
@@ -434,7 +432,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if constexpr (!F8) {
+    } else if (!F8 && warp == 9) {
     // ---------------- TMA loader: lane i issues box i % boxes of page box i / halves
     constexpr int kHalves = D / 64;
     const int box = min(a.kv.page_size, kTcKeys), boxes = kTcKeys / box;
@@ -473,11 +471,13 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       while (!mbar_try_wait(&b.full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kWaitLimit) {
       }
     }
-  } else {
+    }
+  } else if constexpr (F8) {
     // ---------------- e4m3 loaders: 16 codes a thread and step, to fp16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoaderRegs));
     constexpr int CH = D / 16;  // 16-code chunks of a row
     constexpr int N = kTcKeys * CH / 128;
-    const int tid = threadIdx.x - 9 * 32, ch = tid % CH;
+    const int tid = threadIdx.x - 12 * 32, ch = tid % CH;
     uint32_t kv = 0;
     bool ok = true;
     while (ok && segment(a, &u, end, &sg)) {
