@@ -10,11 +10,14 @@ namespace attn {
 
 constexpr int kMaxGroup = 64;  // query heads of a kv head
 
+constexpr int kRowBlock = 2048;  // query rows whose suffixes one stream launch takes
+
 struct Args {
   pmoe_kv_desc kv;
   const __nv_bfloat16* q;
   int64_t q_stride;
   int T, q_heads, group;   // group = q_heads / kv_heads
+  uint32_t group_magic;    // 2^32 / group + 1
   float scale;             // scores are in units of log 2: softmax scale * log2(e)
   const int32_t* prefix_pages;
   int prefix_len;
@@ -27,18 +30,20 @@ struct Args {
   float* lse;
   int32_t* err;
   // Partial results: part p of row-head i = t * q_heads + h. o: sum of weights x values
-  // (not normalised), ml: (largest score, sum of weights). Parts 0 .. prefix_parts - 1 hold
-  // the prefix, the next ceil(suffix_len / chunk) the suffix.
-  float* o_part;    // [parts][T * q_heads][head_dim]
-  float2* ml_part;  // [parts][T * q_heads]
-  int prefix_parts, prefix_chunk;  // keys per prefix part (a multiple of 64)
-  int suffix_parts, suffix_chunk;
-  int row_tiles;    // row tiles of the prefix
+  // (not normalised), ml: (base of the weights' exponents, sum of weights). Parts 0 ..
+  // prefix_parts - 1 hold the prefix, the others the suffix.
+  float* o_part;    // [prefix_parts + suffix_parts][T * q_heads][head_dim]
+  float2* ml_part;  // [prefix_parts + suffix_parts][T * q_heads]
+  int prefix_parts, suffix_parts;  // at most
   // The tensor-core prefix kernel (tc_ctas > 0): units of one 128-key tile for one (256-row
   // tile, kv head) group, tc_tiles units to a group, in group order; CTA c takes units
   // [c * U / tc_ctas, (c + 1) * U / tc_ctas). A group's parts are numbered from its first CTA.
-  int tc_ctas, tc_tiles;
-  uint32_t group_magic;  // 2^32 / group + 1
+  int row_tiles, tc_ctas, tc_tiles;
+  // The stream kernel: units of one 16-key tile for one (up to 16 query rows, kv head) item;
+  // see prefix_attention.cu. pre_tiles: its tiles of the prefix (0: the tensor-core kernel's),
+  // pre_items its items.
+  int warps, min_share, pre_tiles, pre_items, head_items;
+  int64_t* base;    // [row blocks][kRowBlock + 1] first unit of each row; last: all units
 };
 
 constexpr int kTcRows = 256;  // query rows of a group
@@ -87,6 +92,11 @@ __device__ __forceinline__ int row_exponent(float largest) {
   return e < -126 || e > 127 ? 0 : min(e, 126);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// r / group for r < 2^24 and group <= 64
+__device__ __forceinline__ int row_token(const Args& a, int r) {
+  return a.group == 1 ? r : (int)__umulhi((uint32_t)r, a.group_magic);
+}
 
 __device__ __forceinline__ int suffix_keys(const Args& a, int t) {
   if (a.max_suffix == 0) return 0;

@@ -1,29 +1,32 @@
 // moe_prefix_attention: attention over a paged cache for a batch that shares a prefix.
+//
+// Three kernels. The prefix is read once for all rows of a kv head: on the tensor cores as
+// two matrix products a tile (prefix_tc.cu). The stream kernel here takes each row's own
+// keys, and the prefix too where few rows share it; the combine kernel joins the parts.
+//
+// The stream kernel is bound by HBM: a key and its value are used by the at most 16 query
+// heads of an item only, 4 to 16 operations a byte. Every warp runs for itself, without a
+// barrier of the block: a ring of 16-key tiles of its own that TMA fills (a tile lies inside
+// one page; one box for K, one for V), mma.sync on 16 query rows, softmax in registers. The
+// (item, tile) units of all items, in order, are cut into equal runs, one a warp of every
+// SM, whatever the lengths; a warp whose run ends inside an item leaves a part of it.
 #include "attn.cuh"
+#include "tc_gemm.h"
+#include "tc_ptx.cuh"
 
 #include <algorithm>
-#include <cuda_fp16.h>
 #include <math.h>
 
 namespace pmoe {
 namespace attn {
 namespace {
 
-constexpr int kTile = 64;       // keys of a tile
-constexpr int kStages = 3;
-constexpr int kThreads = 128;
-constexpr int kMaxChunk = 4096; // keys of a part: its page ids lie in shared memory
+using namespace tc;
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// 16 bytes to shared memory; nothing is read and zeros are written where !live
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+constexpr int kTile = 16;       // keys of a unit
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int64_t kStreamTraffic = 24 << 20;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -50,212 +53,335 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Where 16-byte chunk c of key row r lies in a tile, so that the 8 rows (or the 2 rows x 4
-// chunks) of one shared-memory access phase fall on distinct banks.
-template <int ROWB, bool F8>
-__device__ __forceinline__ uint32_t place(int r, int c) {
-  int x;
-  if (ROWB == 64) x = (r >> 1) & 3;
-  else if (F8) x = ((r & 1) << 2) | ((r >> 1) & 3);
-  else x = r & 7;
-  return (uint32_t)(r * ROWB + ((c ^ x) << 4));
+template <int D, bool F8>
+struct StreamCfg {
+  static constexpr int kTileBytes = kTile * D * (F8 ? 1 : 2);  // of K, and of V
+  static constexpr int kStage = 2 * kTileBytes;
+  // 24 KB a warp and 192 KB an SM in flight; HBM's share of an SM over its latency is 50 KB
+  static constexpr int kFit = 24576 / kStage, kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kSmem = 1024 /* alignment */ + kRing + kWarps * kStages * 8 + (kRowBlock + 1) * 8 + 64 * 8;
+  // Where 16-byte chunk c of row r lies in a K or V tile (as the TMA swizzle puts it)
+  static __device__ __forceinline__ uint32_t place(int r, int c) {
+    if (!F8) return (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    if (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+    return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  }
+  // The key row of column j of an 8-key group. With e4m3 rows of 128 bytes a phase of a
+  // 16-byte access covers rows 2i and 2i + 1: the order lets them differ in bit 2, which the
+  // swizzle turns into distinct banks.
+  static __device__ __forceinline__ int key_row(int j) { return F8 && D == 128 ? (j >> 1) | ((j & 1) << 2) : j; }
+};
+
+// An item: up to 16 query rows of one kv head and the keys they attend to.
+struct Item {
+  int64_t first, end;    // its units
+  const int32_t* pages;  // its page list
+  int keys, h;
+  int t, row0, rows;     // rows: heads row0.. of token t's group; t < 0: rows row0.. of all T * group
+};
+
+__device__ __forceinline__ Item find_item(const Args& a, const int64_t* base, int nrows, int t0, int64_t pre, int64_t u) {
+  Item it;
+  if (u < pre) {
+    const int i = (int)(u / a.pre_tiles), rt = i / a.kv.kv_heads;
+    it.first = (int64_t)i * a.pre_tiles;
+    it.end = it.first + a.pre_tiles;
+    it.pages = a.prefix_pages;
+    it.keys = a.prefix_len;
+    it.h = i - rt * a.kv.kv_heads;
+    it.t = -1;
+    it.row0 = rt * 16;
+    it.rows = min(16, a.T * a.group - it.row0);
+    return it;
+  }
+  int lo = 0, hi = nrows;  // base[lo] <= u < base[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (base[mid] <= u)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int64_t b = base[lo], n = base[lo + 1] - b;
+  const int nt = (int)(n / a.head_items), i = (int)((u - b) / nt), rts = a.head_items / a.kv.kv_heads;
+  it.first = b + (int64_t)i * nt;
+  it.end = it.first + nt;
+  it.t = t0 + lo;
+  const int seq = a.row_seq != nullptr ? a.row_seq[it.t] : it.t;
+  const bool ok = (unsigned)seq < (unsigned)a.sequences;
+  if (!ok && a.err != nullptr) atomicOr(a.err, kErrBadPage);
+  // an invalid row reads row 0 of the table: in bounds, and its output is undefined
+  it.pages = a.page_table + (int64_t)(ok ? seq : 0) * a.table_stride;
+  it.keys = suffix_keys(a, it.t);
+  it.h = i / rts;
+  it.row0 = (i - it.h * rts) * 16;
+  it.rows = min(16, a.group - it.row0);
+  return it;
+}
+
+// Units of a row's suffix, and the share of a warp.
+__device__ __forceinline__ int64_t row_units(const Args& a, int keys) {
+  return (int64_t)((keys + kTile - 1) / kTile) * a.head_items;
+}
+__device__ __forceinline__ int64_t share_of(const Args& a, int64_t units) {
+  return max((int64_t)a.min_share, (units + a.warps - 1) / a.warps);
 }
 
 template <int D, bool F8>
-struct StreamCfg {
-  static constexpr int kRow = D * (F8 ? 1 : 2);         // bytes of a key row
-  static constexpr int kTileBytes = kTile * kRow;       // of K, and of V
-  static constexpr int kRing = kStages * 2 * kTileBytes;
-  static constexpr int kMerge = 4 * 16 * (D + 4) * 4;   // the warps' sums at the end
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + (kMaxChunk / 16) * 4;
-};
-
-// One CTA: up to 16 * WM query rows of one kv head against the keys [k0, k1) of one page
-// list. The 4 warps are WM row tiles x 4 / WM key groups; each keeps its own running
-// maximum and sum, joined at the end.
-// rows: row i is head `h * group + i % group` of token t0 + i / group.
-template <int D, bool F8, int WM>
-__device__ void stream_part(const Args& a, uint8_t* smem, const int32_t* pages, int h, int row0, int rows, int k0,
-                            int k1, int part) {
+__global__ void __launch_bounds__(kThreads, 1)
+    stream_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a,
+                  int block) {
   using C = StreamCfg<D, F8>;
-  constexpr int WK = 4 / WM, KW = kTile / WK, NT = KW / 8;  // keys of a warp, its 8-key tiles
-  constexpr int CH = C::kRow / 16;                          // 16-byte chunks of a row
-  int32_t* ids = reinterpret_cast<int32_t*>(smem + (C::kRing > C::kMerge ? C::kRing : C::kMerge));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wm = warp % WM, wk = warp / WM, g = lane >> 2, c = lane & 3;
-  const int psh = 31 - __clz(a.kv.page_size);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::kRing);
+  int64_t* base = reinterpret_cast<int64_t*>(bars + kWarps * C::kStages);  // [nrows + 1]
+  int64_t* sums = base + kRowBlock + 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sums + kWarps);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int t0 = block * kRowBlock, nrows = a.max_suffix > 0 ? min(kRowBlock, a.T - t0) : 0;
+  const int64_t pre = block == 0 ? (int64_t)a.pre_items * a.pre_tiles : 0;
+  pdl_trigger();
 
-  const int p0 = k0 >> psh, np = ((k1 - 1) >> psh) - p0 + 1;
-  for (int i = tid; i < np; i += kThreads) {
-    int id = pages[p0 + i];
-    if ((unsigned)id >= (unsigned)a.kv.num_pages) {
-      if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
-      id = -1;
-    }
-    ids[i] = id;
+  // ---- the first unit of every row: thread i sums 8 rows
+  int64_t mine[8], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = tid * 8 + i;
+    mine[i] = r < nrows ? row_units(a, suffix_keys(a, t0 + r)) : 0;
+    sum += mine[i];
   }
-
-  // query fragments; rows beyond the last are zero
-  uint32_t qf[D / 16][4];
-  float qmul[2];  // what a score of rows g and g + 8 is multiplied by
-  {
-    const __nv_bfloat16* qp[2];
-    bool live[2];
+  int64_t upto = sum;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = wm * 16 + g + 8 * e;
-      live[e] = i < rows;
-      const int r = row0 + (live[e] ? i : 0);
-      qp[e] = a.q + (int64_t)(r / a.group) * a.q_stride + (h * a.group + r % a.group) * D;
-      qmul[e] = a.scale;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t d = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += d;
+  }
+  if (lane == 31) sums[warp] = upto;
+  if (tid == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&bars[warp * C::kStages + i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (warp == 0) prefetch_map(&map_k), prefetch_map(&map_v);
+  }
+  __syncthreads();
+  int64_t at = pre + upto - sum, units = pre;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) at += sums[i];
+    units += sums[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = tid * 8 + i;
+    if (r < nrows) {
+      base[r] = at;
+      if (blockIdx.x == 0) a.base[(int64_t)block * (kRowBlock + 1) + r] = at;  // for the combine kernel
     }
-    if constexpr (!F8) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          qf[k][e] = live[e] ? __ldg(reinterpret_cast<const uint32_t*>(qp[e] + k * 16 + 2 * c)) : 0;
-          qf[k][2 + e] = live[e] ? __ldg(reinterpret_cast<const uint32_t*>(qp[e] + k * 16 + 2 * c + 8)) : 0;
+    at += mine[i];
+  }
+  if (tid == 0) {
+    base[nrows] = units;
+    if (blockIdx.x == 0) a.base[(int64_t)block * (kRowBlock + 1) + nrows] = units;
+  }
+  __syncthreads();
+
+  // ---- this warp's run of units; neighbouring runs on different SMs
+  const int64_t share = share_of(a, units);
+  const int64_t w = (int64_t)warp * gridDim.x + blockIdx.x;
+  const int64_t u0 = w * share, u1 = min(units, u0 + share);
+  const int psh = 31 - __clz(a.kv.page_size);
+  uint8_t* mystage = ring + warp * C::kStages * C::kStage;
+  uint64_t* bar = bars + warp * C::kStages;
+
+  // the loading side: item and page ids of the next unit to load
+  Item li{};
+  int64_t lu = u0, lids = -1;
+  int ids = 0;
+  auto load = [&]() {
+    if (lu >= u1) return;
+    if (lu >= li.end) {
+      li = find_item(a, base, nrows, t0, pre, lu);
+      lids = -1;
+    }
+    const int tile = (int)(lu - li.first);
+    if (lids < 0 || tile >= lids + 32) {  // the next 32 tiles' pages, one a lane
+      lids = tile;
+      const int key = (tile + lane) * kTile;
+      ids = 0;
+      if (key < li.keys && lu + lane < u1) {
+        ids = __ldg(li.pages + (key >> psh));
+        if ((unsigned)ids >= (unsigned)a.kv.num_pages) {
+          if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
+          ids = a.kv.num_pages;  // out of the map's range: reads as zeros
         }
-    } else {
-      // Slots of step k = 4 i + s hold elements 64 i + 16 c + 4 s + .. (the order in which a
-      // thread reads 16 key bytes at once). q goes to fp16 divided by the power of two of
-      // its row's largest element.
-      uint2 raw[2][D / 16];
+      }
+    }
+    const int id = __shfl_sync(0xffffffffu, ids, tile - (int)lids);
+    if (lane == 0) {
+      const int s = (int)((lu - u0) % C::kStages), row = (tile * kTile) & (a.kv.page_size - 1);
+      mbar_arrive_expect_tx(&bar[s], C::kStage);
+      tma_load_5d(mystage + s * C::kStage, &map_k, &bar[s], 0, row, 0, li.h, id);
+      tma_load_5d(mystage + s * C::kStage + C::kTileBytes, &map_v, &bar[s], 0, row, 0, li.h, id);
+    }
+    ++lu;
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::kStages; ++i) load();
+
+  bool ok = true;
+  int64_t u = u0;
+  while (u < u1 && ok) {
+    const Item it = find_item(a, base, nrows, t0, pre, u);
+    const int64_t stop = min(it.end, u1);
+    // ---- query fragments; rows beyond the last are zero
+    uint32_t qf[D / 16][4];
+    float qmul[2];  // what a score of rows g and g + 8 is multiplied by
+    int64_t rowhead[2];
+    bool live[2];
+    {
+      const __nv_bfloat16* qp[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          raw[e][k] = live[e] ? __ldg(reinterpret_cast<const uint2*>(qp[e] + (k >> 2) * 64 + 16 * c + (k & 3) * 4))
-                              : make_uint2(0, 0);
-          const uint32_t w[2] = {raw[e][k].x, raw[e][k].y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int ex = row_exponent(mx);
-        const float down = pow2(-ex);
-        qmul[e] = a.scale * a.kv.k_scale[h] * pow2(ex);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t w[2] = {raw[e][k].x, raw[e][k].y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qf[k][2 * i + e] = pack2<true>(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
-        }
+        const int i = g + 8 * e;
+        live[e] = i < it.rows;
+        const int r = it.row0 + (live[e] ? i : 0), tok = it.t < 0 ? row_token(a, r) : it.t;
+        const int head = it.h * a.group + (it.t < 0 ? r - tok * a.group : r);
+        qp[e] = a.q + (int64_t)tok * a.q_stride + head * D;
+        rowhead[e] = (int64_t)tok * a.q_heads + head;
+        qmul[e] = a.scale;
       }
-    }
-  }
-  __syncthreads();  // ids
-
-  const uint8_t* kb = static_cast<const uint8_t*>(a.kv.k);
-  const uint8_t* vb = static_cast<const uint8_t*>(a.kv.v);
-  const int64_t page_bytes = a.kv.page_stride * (F8 ? 1 : 2);
-  const int64_t head_off = (int64_t)h * a.kv.page_size * C::kRow;
-  const int tiles = (k1 - k0 + kTile - 1) / kTile;
-  const uint32_t ring = smem_u32(smem);
-  auto load = [&](int tile) {
-    if (tile < tiles) {
-      const uint32_t ks = ring + (tile % kStages) * 2 * C::kTileBytes, vs = ks + C::kTileBytes;
-      const int ch = tid % CH;
-#pragma unroll
-      for (int r = tid / CH; r < kTile; r += kThreads / CH) {
-        const int key = k0 + tile * kTile + r;
-        int id = -1;
-        if (key < k1) id = ids[(key >> psh) - p0];
-        const int64_t off = id < 0 ? 0 : (int64_t)id * page_bytes + head_off + (int64_t)(key & (a.kv.page_size - 1)) * C::kRow + ch * 16;
-        const uint32_t at = place<C::kRow, F8>(r, ch);
-        cp16(ks + at, kb + off, id >= 0);
-        cp16(vs + at, vb + off, id >= 0);
-      }
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) load(i);
-
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  for (int tile = 0; tile < tiles; ++tile) {
-    cp_wait<kStages - 2>();
-    __syncthreads();  // the tile has landed, and every warp is done with the one before it
-    load(tile + kStages - 1);
-    const uint32_t ks = ring + (tile % kStages) * 2 * C::kTileBytes, vs = ks + C::kTileBytes;
-
-    float s[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
       if constexpr (!F8) {
-        const int r = wk * KW + n * 8 + (lane & 7);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t b[4];
-          ldsm4(b, ks + place<C::kRow, F8>(r, k * 4 + (lane >> 3)));
-          mma<false>(s[n], qf[2 * k], b[0], b[1]);
-          mma<false>(s[n], qf[2 * k + 1], b[2], b[3]);
-        }
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            qf[k][e] = live[e] ? __ldg(reinterpret_cast<const uint32_t*>(qp[e] + k * 16 + 2 * c)) : 0;
+            qf[k][2 + e] = live[e] ? __ldg(reinterpret_cast<const uint32_t*>(qp[e] + k * 16 + 2 * c + 8)) : 0;
+          }
       } else {
-        const int r = wk * KW + n * 8 + g;
+        // Slots of step k = 4 i + s hold elements 64 i + 16 c + 4 s + .. (the order in which a
+        // thread reads 16 key bytes at once). q goes to fp16 divided by the power of two of
+        // its row's largest element.
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          uint32_t b[4];
-          lds128(b, ks + place<C::kRow, F8>(r, i * 4 + c));
+        for (int e = 0; e < 2; ++e) {
+          uint2 raw[D / 16];
+          float mx = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma<true>(s[n], qf[4 * i + k], e4m3x2(b[k] & 0xffffu), e4m3x2(b[k] >> 16));
+          for (int k = 0; k < D / 16; ++k) {
+            raw[k] = live[e] ? __ldg(reinterpret_cast<const uint2*>(qp[e] + (k >> 2) * 64 + 16 * c + (k & 3) * 4))
+                             : make_uint2(0, 0);
+            const uint32_t v[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v[i] << 16)), fabsf(__uint_as_float(v[i] & 0xffff0000u))));
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int ex = row_exponent(mx);
+          const float down = pow2(-ex);
+          qmul[e] = a.scale * a.kv.k_scale[it.h] * pow2(ex);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t v[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              qf[k][2 * i + e] = pack2<true>(__uint_as_float(v[i] << 16) * down, __uint_as_float(v[i] & 0xffff0000u) * down);
+          }
         }
       }
     }
-    // keys beyond the part; then the running maximum and the weights
-    const int kw = k0 + tile * kTile + wk * KW;
-    float mx[2] = {m[0], m[1]};
+
+    float o[D / 8][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[n][i] = kw + n * 8 + 2 * c + (i & 1) < k1 ? s[n][i] * qmul[i >> 1] : -INFINITY;
-        mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    // m: what the exponents of the weights count from; it moves only when a score exceeds it
+    // by 2^8 (any base gives the same quotient), so the sums are seldom rescaled
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (; u < stop; ++u) {
+      const int n = (int)(u - u0), s = n % C::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar[s], (n / C::kStages) & 1, abort_flag, a.err))) {
+        ok = false;
+        break;
       }
-    float base[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-      base[e] = mx[e] == -INFINITY ? 0.f : mx[e];
-      const float f = ex2(m[e] - base[e]);
-      m[e] = mx[e];
-      l[e] *= f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][2 * e] *= f, o[i][2 * e + 1] *= f;
-    }
-    uint32_t pf[NT / 2][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = ex2(s[n][i] - base[i >> 1]);
-        l[i >> 1] += p[i];
+      const uint32_t ks = smem_u32(mystage + s * C::kStage), vs = ks + C::kTileBytes;
+      const int valid = it.keys - (int)(u - it.first) * kTile;
+      if (valid < kTile) {
+        // values beyond the last key may be anything, and 0 x NaN is NaN
+        constexpr int CH = C::kTileBytes / kTile / 16;  // 16-byte chunks of a row
+        for (int i = valid * CH + lane; i < kTile * CH; i += 32)
+          *reinterpret_cast<uint4*>(mystage + s * C::kStage + C::kTileBytes + C::place(i / CH, i % CH)) = make_uint4(0, 0, 0, 0);
+        fence_async();
+        __syncwarp();
       }
-      pf[n / 2][(n & 1) * 2] = pack2<F8>(p[0], p[1]);
-      pf[n / 2][(n & 1) * 2 + 1] = pack2<F8>(p[2], p[3]);
-    }
+      float sc[2][4];
 #pragma unroll
-    for (int n = 0; n < NT / 2; ++n) {
-      const int r = wk * KW + n * 16 + (lane & 15);
+      for (int j = 0; j < 2; ++j) {
+        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+        if constexpr (!F8) {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t b[4];
+            ldsm4(b, ks + C::place(j * 8 + (lane & 7), k * 4 + (lane >> 3)));
+            mma<false>(sc[j], qf[2 * k], b[0], b[1]);
+            mma<false>(sc[j], qf[2 * k + 1], b[2], b[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            uint32_t b[4];
+            lds128(b, ks + C::place(j * 8 + C::key_row(g), i * 4 + c));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma<true>(sc[j], qf[4 * i + k], e4m3x2(b[k] & 0xffffu), e4m3x2(b[k] >> 16));
+          }
+        }
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sc[j][i] = j * 8 + C::key_row(2 * c + (i & 1)) < valid ? sc[j][i] * qmul[i >> 1] : -INFINITY;
+          mx[i >> 1] = fmaxf(mx[i >> 1], sc[j][i]);
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+      }
+      if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool grow = mx[e] > m[e] + 8.f;
+          const float f = grow ? ex2(m[e] - mx[e]) : 1.f;
+          if (grow) m[e] = mx[e];
+          l[e] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) o[i][2 * e] *= f, o[i][2 * e + 1] *= f;
+        }
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = ex2(sc[j][i] - (m[i >> 1] == -INFINITY ? 0.f : m[i >> 1]));
+          l[i >> 1] += p[i];
+        }
+        pf[j * 2] = pack2<F8>(p[0], p[1]);
+        pf[j * 2 + 1] = pack2<F8>(p[2], p[3]);
+      }
+      const int r = (lane & 8) | C::key_row(lane & 7);
       if constexpr (!F8) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t b[4];
-          ldsm4t(b, vs + place<C::kRow, F8>(r, i * 2 + (lane >> 4)));
-          mma<false>(o[2 * i], pf[n], b[0], b[1]);
-          mma<false>(o[2 * i + 1], pf[n], b[2], b[3]);
+          ldsm4t(b, vs + C::place(r, i * 2 + (lane >> 4)));
+          mma<false>(o[2 * i], pf, b[0], b[1]);
+          mma<false>(o[2 * i + 1], pf, b[2], b[3]);
         }
       } else {
         // a 16-bit element of the transposed load is 2 values of one key: the even and the
@@ -263,200 +389,237 @@ __device__ void stream_part(const Args& a, uint8_t* smem, const int32_t* pages, 
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint32_t b[4];
-          ldsm4t(b, vs + place<C::kRow, F8>(r, i * 2 + (lane >> 4)));
+          ldsm4t(b, vs + C::place(r, i * 2 + (lane >> 4)));
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            mma<true>(o[4 * i + 2 * j], pf[n], e4m3x2(__byte_perm(b[2 * j], 0, 0x4420)),
+            mma<true>(o[4 * i + 2 * j], pf, e4m3x2(__byte_perm(b[2 * j], 0, 0x4420)),
                       e4m3x2(__byte_perm(b[2 * j + 1], 0, 0x4420)));
-            mma<true>(o[4 * i + 2 * j + 1], pf[n], e4m3x2(__byte_perm(b[2 * j], 0, 0x4431)),
+            mma<true>(o[4 * i + 2 * j + 1], pf, e4m3x2(__byte_perm(b[2 * j], 0, 0x4431)),
                       e4m3x2(__byte_perm(b[2 * j + 1], 0, 0x4431)));
           }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      load();
+    }
+    if (!ok) break;
+
+    // ---- the part
+    const int part = (int)(w - it.first / share) + (it.t < 0 ? 0 : a.prefix_parts);
+    const float vscale = F8 ? a.kv.v_scale[it.h] : 1.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (!live[e]) continue;
+      const int64_t i = (int64_t)part * a.T * a.q_heads + rowhead[e];
+      float* dst = a.o_part + i * D;
+      if constexpr (!F8) {
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) *reinterpret_cast<float2*>(dst + k * 8 + 2 * c) = make_float2(o[k][2 * e], o[k][2 * e + 1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          *reinterpret_cast<float4*>(dst + k * 16 + 4 * c) =
+              make_float4(o[2 * k][2 * e] * vscale, o[2 * k + 1][2 * e] * vscale, o[2 * k][2 * e + 1] * vscale,
+                          o[2 * k + 1][2 * e + 1] * vscale);
+      }
+      if (c == 0) a.ml_part[i] = make_float2(m[e], l[e]);
+    }
+  }
+  // copies in flight land before the CTA leaves, even after a wait that gave up
+  if (!ok)
+    for (int64_t i = max(u, lu - C::kStages); i < lu; ++i) {
+      const int n = (int)(i - u0);
+      const long long c0 = clock64();
+      while (!mbar_try_wait(&bar[n % C::kStages], (n / C::kStages) & 1) && clock64() - c0 < kWaitLimit) {
+      }
+    }
+  pdl_wait();  // the combine kernel follows this one only: the tensor-core kernel is done then too
+}
+
+// Joins the parts of one row-head: W warps share its parts.
+template <int D, int W>
+__global__ void __launch_bounds__(W * 32 < 128 ? 128 : W * 32) combine_kernel(const Args a) {
+  constexpr int kRowHeads = W < 4 ? 4 / W : 1, V = D / 32;
+  __shared__ float red[W > 1 ? W : 1][D];
+  const int64_t rh = (int64_t)a.T * a.q_heads;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % W;
+  const int64_t i = (int64_t)blockIdx.x * kRowHeads + (threadIdx.x >> 5) / W;
+  pdl_wait();
+  if (W == 1 && i >= rh) return;
+  const int t = (int)(i / a.q_heads), hq = (int)(i % a.q_heads), h = hq / a.group, r = hq - h * a.group;
+  // the row's parts of the prefix, then those of its own keys
+  int pre = 0, suf = 0;
+  if (a.tc_ctas > 0) pre = tc_parts(a, t * a.group + r, h);
+  const int64_t* base = a.base + (int64_t)(t / kRowBlock) * (kRowBlock + 1);
+  if (a.pre_tiles > 0) {
+    const int64_t share = share_of(a, a.base[a.max_suffix > 0 ? min(kRowBlock, a.T) : 0]);
+    const int64_t f = ((int64_t)((t * a.group + r) / 16) * a.kv.kv_heads + h) * a.pre_tiles;
+    pre = (int)((f + a.pre_tiles - 1) / share - f / share) + 1;
+  }
+  if (a.max_suffix > 0) {
+    const int nt = (suffix_keys(a, t) + kTile - 1) / kTile;
+    if (nt > 0) {
+      const int64_t share = share_of(a, base[min(kRowBlock, a.T - t / kRowBlock * kRowBlock)]);
+      const int64_t f = base[t % kRowBlock] + (int64_t)(h * (a.head_items / a.kv.kv_heads) + r / 16) * nt;
+      suf = (int)((f + nt - 1) / share - f / share) + 1;
+    }
+  }
+  const int parts = pre + suf, skip = a.prefix_parts - pre;
+  auto slot = [&](int p) { return (int64_t)(p < pre ? p : p + skip) * rh + i; };
+
+  float m = -INFINITY;
+  for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.ml_part[slot(p)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float top = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[V];
+#pragma unroll
+  for (int d = 0; d < V; ++d) acc[d] = 0.f;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    float f = 0.f;
+    if (p0 + lane < parts) {
+      const float2 ml = a.ml_part[slot(p0 + lane)];
+      f = ex2(ml.x - top);
+      l = fmaf(ml.y, f, l);
+    }
+    const int n = min(32, parts - p0);
+    constexpr int U = 4;  // parts in flight
+    for (int j0 = w; j0 < n; j0 += U * W) {
+      float v[U][V];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int j = j0 + k * W;
+#pragma unroll
+        for (int d = 0; d < V; ++d) v[k][d] = 0.f;
+        if (j < n) {
+          const float* src = a.o_part + slot(p0 + j) * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[k][0] = x.x, v[k][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int j = j0 + k * W;
+        const float fj = __shfl_sync(0xffffffffu, f, j < n ? j : 0);
+        if (j < n) {
+#pragma unroll
+          for (int d = 0; d < V; ++d) acc[d] = fmaf(v[k][d], fj, acc[d]);
         }
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-  }
-  cp_wait<0>();
-  __syncthreads();  // the ring becomes the merge buffer
-
-  // join the key groups of each row tile: buf[warp][16][D + 4], (m, l) after each row
-  float* buf = reinterpret_cast<float*>(smem) + warp * 16 * (D + 4);
-  const float vscale = F8 ? a.kv.v_scale[h] : 1.f;
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if constexpr (W > 1) {
+    const int set = (threadIdx.x >> 5) / W;  // 0 but for several row-heads a block
+    static_assert(kRowHeads == 1, "one row-head a block");
+    (void)set;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float* row = buf + (g + 8 * e) * (D + 4);
-    if constexpr (!F8) {
+    for (int d = 0; d < V; ++d) red[w][lane * V + d] = acc[d];
+    __syncthreads();
+    if (w != 0) return;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(row + i * 8 + 2 * c) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
-    } else {
+    for (int d = 0; d < V; ++d) {
+      float x = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        *reinterpret_cast<float4*>(row + i * 16 + 4 * c) =
-            make_float4(o[2 * i][2 * e], o[2 * i + 1][2 * e], o[2 * i][2 * e + 1], o[2 * i + 1][2 * e + 1]);
+      for (int k = 0; k < W; ++k) x += red[k][lane * V + d];
+      acc[d] = x;
     }
-    if (c == 0) row[D] = m[e], row[D + 1] = l[e];
-  }
-  __syncthreads();
-  const int64_t rh = (int64_t)a.T * a.q_heads;
-  for (int i = warp; i < rows; i += 4) {
-    const float* src = reinterpret_cast<float*>(smem) + ((i / 16) * 16 + (i % 16)) * (D + 4);  // key group 0
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WK; ++w) mm = fmaxf(mm, src[w * WM * 16 * (D + 4) + D]);
-    const float bb = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f, acc[D / 32];
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) acc[d] = 0.f;
-#pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      const float* s2 = src + w * WM * 16 * (D + 4);
-      const float f = ex2(s2[D] - bb);
-      ll = fmaf(s2[D + 1], f, ll);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(s2[d * 32 + lane], f, acc[d]);
-    }
-    const int r = row0 + i;
-    const int64_t at = (int64_t)part * rh + (int64_t)(r / a.group) * a.q_heads + h * a.group + r % a.group;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) a.o_part[at * D + d * 32 + lane] = acc[d] * vscale;
-    if (lane == 0) a.ml_part[at] = make_float2(mm, ll);
-  }
-}
-
-template <int D, bool F8, int WM>
-__global__ void __launch_bounds__(kThreads) stream_kernel(const Args a, int prefix_blocks) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  int b = blockIdx.x;
-  if (b < prefix_blocks) {
-    const int part = b % a.prefix_parts;
-    b /= a.prefix_parts;
-    const int h = b % a.kv.kv_heads, tile = b / a.kv.kv_heads;
-    const int row0 = tile * 16 * WM, rows = min(16 * WM, a.T * a.group - row0);
-    const int k0 = part * a.prefix_chunk, k1 = min(a.prefix_len, k0 + a.prefix_chunk);
-    stream_part<D, F8, WM>(a, smem, a.prefix_pages, h, row0, rows, k0, k1, part);
-    return;
-  }
-  b -= prefix_blocks;
-  const int part = b % a.suffix_parts;
-  b /= a.suffix_parts;
-  const int h = b % a.kv.kv_heads, t = b / a.kv.kv_heads;
-  const int n = suffix_keys(a, t), k0 = part * a.suffix_chunk;
-  if (k0 >= n) return;
-  const int seq = a.row_seq != nullptr ? a.row_seq[t] : t;
-  const bool ok = (unsigned)seq < (unsigned)a.sequences;
-  if (!ok && a.err != nullptr) atomicOr(a.err, kErrBadPage);
-  // an invalid row reads row 0 of the table: in bounds, and its output is undefined
-  stream_part<D, F8, WM>(a, smem, a.page_table + (int64_t)(ok ? seq : 0) * a.table_stride, h, t * a.group, a.group, k0,
-                         min(n, k0 + a.suffix_chunk), a.prefix_parts + part);
-}
-
-// Joins the parts of one row-head; one warp each.
-template <int D>
-__global__ void __launch_bounds__(128) combine_kernel(const Args a) {
-  const int64_t rh = (int64_t)a.T * a.q_heads;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (i >= rh) return;
-  const int lane = threadIdx.x & 31;
-  const int t = (int)(i / a.q_heads), hq = (int)(i % a.q_heads);
-  const int n = suffix_keys(a, t);
-  // the row's prefix parts, then (from part prefix_parts on) its suffix parts
-  const int pre = a.tc_ctas > 0 ? tc_parts(a, t * a.group + hq % a.group, hq / a.group) : a.prefix_parts;
-  const int parts = pre + (n + a.suffix_chunk - 1) / a.suffix_chunk;
-  const int skip = a.prefix_parts - pre;
-  auto slot = [&](int p) { return (int64_t)(p < pre ? p : p + skip) * rh + i; };
-  float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.ml_part[slot(p)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[D / 32];
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d) acc[d] = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    const int64_t at = slot(p);
-    const float2 ml = a.ml_part[at];
-    const float f = ex2(ml.x - base);
-    l = fmaf(ml.y, f, l);
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(a.o_part[at * D + d * 32 + lane], f, acc[d]);
   }
   const float inv = parts == 0 ? 0.f : 1.f / l;
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) a.out[i * D + d * 32 + lane] = __float2bfloat16(acc[d] * inv);
+  for (int d = 0; d < V; d += 2)
+    *reinterpret_cast<__nv_bfloat162*>(a.out + i * D + lane * V + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
   if (a.lse != nullptr && lane == 0) a.lse[i] = parts == 0 ? -INFINITY : m * kLn2 + logf(l);
 }
 
+// ---------------------------------------------------------------- host side
+
 int sm_count() {
+  static std::atomic<int> count[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = count[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) count[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
-// Parts of the prefix and the suffix: enough CTAs for every SM to hold a few, no part
-// shorter than 128 keys.
-void plan_parts(Args* a, int wm, int sms) {
-  const int want = sms * 3;
-  auto split = [&](int keys, int64_t others, int* parts, int* chunk) {
-    *parts = 0;
-    *chunk = kTile;
-    if (keys == 0) return;
-    int64_t n = (want + others - 1) / others;
-    n = std::max<int64_t>(1, std::min<int64_t>(n, (keys + 127) / 128));
-    int64_t c = (keys + n - 1) / n;
-    c = std::min<int64_t>(kMaxChunk, (c + kTile - 1) / kTile * kTile);
-    *chunk = (int)c;
-    *parts = (int)((keys + c - 1) / c);
-  };
-  a->tc_ctas = 0;
-  if (a->prefix_len > 0 && a->T * a->group > 16 * wm) {
-    plan_prefix_tc(a, sms);
-  } else {
-    a->row_tiles = (a->T * a->group + 16 * wm - 1) / (16 * wm);
-    split(a->prefix_len, (int64_t)a->row_tiles * a->kv.kv_heads, &a->prefix_parts, &a->prefix_chunk);
-  }
-  split(a->max_suffix, (int64_t)a->T * a->kv.kv_heads, &a->suffix_parts, &a->suffix_chunk);
+int make_map(const Args& a, void* base, CUtensorMap* m) {
+  const bool f8 = a.kv.dtype == PMOE_KV_E4M3;
+  const uint64_t eb = f8 ? 1 : 2, row = a.kv.head_dim * eb, page = a.kv.page_size;
+  const uint64_t inner = f8 ? a.kv.head_dim : 64, blocks = a.kv.head_dim / inner;  // elements of a swizzled row
+  const uint64_t dims[5] = {inner, page, blocks, (uint64_t)a.kv.kv_heads, (uint64_t)a.kv.num_pages};
+  const uint64_t strides[4] = {row, inner * eb, page * row, (uint64_t)a.kv.page_stride * eb};
+  const uint32_t box[5] = {(uint32_t)inner, kTile, (uint32_t)blocks, 1, 1};
+  return tc_encode_map(m, base, 5, dims, strides, box,
+                       !f8 ? kTcMapBf16Sw128 : a.kv.head_dim == 128 ? kTcMapBytesSw128 : kTcMapBytesSw64);
 }
 
-size_t scratch_layout(const Args& a, size_t* ml_at) {
-  const size_t n = (size_t)(a.prefix_parts + a.suffix_parts) * a.T * a.q_heads;
-  *ml_at = n * a.kv.head_dim * 4;
-  return *ml_at + n * 8;
-}
-
-int wm_of(int group) { return group <= 16 ? 1 : group <= 32 ? 2 : 4; }
-
-template <int D, bool F8, int WM>
-int launch_stream(const Args& a, cudaStream_t s) {
-  const int smem = StreamCfg<D, F8>::kSmem;
-  static SmemLimit limit;
-  const int r = limit.set(reinterpret_cast<const void*>(stream_kernel<D, F8, WM>), smem, "moe_prefix_attention");
-  if (r != PMOE_OK) return r;
-  const int64_t pb = a.tc_ctas > 0 ? 0 : (int64_t)a.prefix_parts * a.kv.kv_heads * a.row_tiles;
-  const int64_t sb = (int64_t)a.suffix_parts * a.kv.kv_heads * a.T;
-  if (pb + sb > INT32_MAX) return PMOE_EUNSUPPORTED;
-  if (pb + sb > 0) stream_kernel<D, F8, WM><<<(unsigned)(pb + sb), kThreads, smem, s>>>(a, (int)pb);
-  return launch_status("moe_prefix_attention");
+template <class... P, class... A>
+int launch_after(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s, bool early, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...), "moe_prefix_attention");
 }
 
 template <int D, bool F8>
-int launch_all(const Args& a, cudaStream_t s) {
-  const int wm = wm_of(a.group);
+int launch_all(const Args& a, int sms, cudaStream_t s) {
+  using C = StreamCfg<D, F8>;
   int r = a.tc_ctas > 0 ? launch_prefix_tc(a, s) : PMOE_OK;
   if (r != PMOE_OK) return r;
-  r = wm == 1 ? launch_stream<D, F8, 1>(a, s) : wm == 2 ? launch_stream<D, F8, 2>(a, s) : launch_stream<D, F8, 4>(a, s);
-  if (r != PMOE_OK) return r;
+  bool early = a.tc_ctas > 0;  // may start while the kernel before it, one of this call, still runs
+  if (a.pre_tiles > 0 || a.max_suffix > 0) {
+    static SmemLimit limit;
+    CUtensorMap mk, mv;
+    r = limit.set(reinterpret_cast<const void*>(stream_kernel<D, F8>), C::kSmem, "moe_prefix_attention");
+    if (r == PMOE_OK) r = make_map(a, a.kv.k, &mk);
+    if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
+    if (r != PMOE_OK) return r;
+    const int blocks = a.max_suffix > 0 ? (a.T + kRowBlock - 1) / kRowBlock : 1;
+    for (int b = 0; b < blocks; ++b) {
+      // a later block's launch may not overtake the one before it: only the first is early
+      r = launch_after(stream_kernel<D, F8>, sms, kThreads, C::kSmem, s, early && b == 0, mk, mv, a, b);
+      if (r != PMOE_OK) return r;
+    }
+    early = true;
+  }
   const int64_t rh = (int64_t)a.T * a.q_heads;
-  combine_kernel<D><<<(unsigned)((rh + 3) / 4), 128, 0, s>>>(a);
-  return launch_status("moe_prefix_attention");
+  const int parts = a.prefix_parts + a.suffix_parts;
+  if (parts <= 12 && rh >= 4096) return launch_after(combine_kernel<D, 1>, (unsigned)((rh + 3) / 4), 128, 0, s, early, a);
+  if (parts <= 64) return launch_after(combine_kernel<D, 4>, (unsigned)rh, 128, 0, s, early, a);
+  return launch_after(combine_kernel<D, 16>, (unsigned)rh, 512, 0, s, early, a);
+}
+
+struct Layout {
+  size_t ml, base, bytes;
+};
+Layout scratch_layout(const Args& a) {
+  const size_t n = (size_t)(a.prefix_parts + a.suffix_parts) * a.T * a.q_heads;
+  Layout l;
+  l.ml = n * a.kv.head_dim * 4;
+  l.base = l.ml + n * 8;
+  l.bytes = l.base + (size_t)((a.T + kRowBlock - 1) / kRowBlock) * (kRowBlock + 1) * 8;
+  return l;
 }
 
 // Checks shared by the call and its scratch size; fills the part plan.
-int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suffix, Args* a) {
+int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suffix, Args* a, int* sms) {
   const int r = check_kv(kv);
   if (r != PMOE_OK) return r;
   if (T < 0 || q_heads < 1 || q_heads % kv->kv_heads != 0 || prefix_len < 0 || max_suffix < 0) return PMOE_EINVAL;
@@ -467,14 +630,37 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   a->T = T;
   a->q_heads = q_heads;
   a->group = q_heads / kv->kv_heads;
-  a->group_magic = (uint32_t)((1ull << 32) / a->group + 1);  // of no use for 1
+  a->group_magic = (uint32_t)((1ull << 32) / a->group + 1);
   a->prefix_len = prefix_len;
   a->max_suffix = max_suffix;
   if (a->group > kMaxGroup) return PMOE_EUNSUPPORTED;
   if (T == 0) return PMOE_OK;
-  const int sms = sm_count();
-  if (sms == 0) return PMOE_ECUDA;
-  plan_parts(a, wm_of(a->group), sms);
+  *sms = sm_count();
+  if (*sms == 0) return PMOE_ECUDA;
+
+  const int rows = T * a->group, rts = (a->group + 15) / 16;
+  a->head_items = kv->kv_heads * rts;
+  a->warps = *sms * kWarps;
+  const int64_t tiles = ((int64_t)max_suffix + kTile - 1) / kTile;
+  // A warp's run: 64 keys at least, and long enough that an item has few parts
+  const int64_t items = (int64_t)T * a->head_items;
+  const int64_t most = std::min<int64_t>(512, std::max<int64_t>(4, 4ll * a->warps / items));
+  a->min_share = (int)std::max<int64_t>(4, (tiles + most - 1) / most);
+  a->suffix_parts = tiles > 0 ? (int)((tiles - 1) / a->min_share + 2) : 0;
+  a->prefix_parts = 0;
+  if (prefix_len > 0) {
+    const int64_t pre_rts = (rows + 15) / 16;
+    const int64_t traffic = pre_rts * kv->kv_heads * prefix_len * kv->head_dim * (kv->dtype == PMOE_KV_E4M3 ? 2 : 4);
+    if (pre_rts == 1 || traffic <= kStreamTraffic) {
+      a->pre_tiles = (prefix_len + kTile - 1) / kTile;
+      a->pre_items = (int)(pre_rts * kv->kv_heads);
+      const int64_t units = (int64_t)a->pre_tiles * a->pre_items;
+      const int64_t share = std::max<int64_t>(a->min_share, (units + a->warps - 1) / a->warps);
+      a->prefix_parts = (int)((a->pre_tiles - 1) / share + 2);
+    } else {
+      plan_prefix_tc(a, *sms);
+    }
+  }
   return PMOE_OK;
 }
 
@@ -487,9 +673,9 @@ using namespace pmoe;
 extern "C" size_t moe_prefix_attention_scratch_bytes(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len,
                                                      int max_suffix) {
   attn::Args a{};
-  size_t ml = 0;
-  if (attn::plan(kv, T, q_heads, prefix_len, max_suffix, &a) != PMOE_OK || T == 0) return 0;
-  return attn::scratch_layout(a, &ml);
+  int sms = 0;
+  if (attn::plan(kv, T, q_heads, prefix_len, max_suffix, &a, &sms) != PMOE_OK || T == 0) return 0;
+  return attn::scratch_layout(a).bytes;
 }
 
 extern "C" int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64_t q_stride, int T, int q_heads,
@@ -511,11 +697,11 @@ extern "C" int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64
       return PMOE_EINVAL;
     if (off(lse, 4) || off(err_out, 4) || off(scratch, 16)) return PMOE_EINVAL;
   }
-  int r = attn::plan(kv, T, q_heads, prefix_len, max_suffix, &a);
+  int sms = 0;
+  const int r = attn::plan(kv, T, q_heads, prefix_len, max_suffix, &a, &sms);
   if (r != PMOE_OK || T == 0) return r;
-  size_t ml = 0;
-  const size_t need = attn::scratch_layout(a, &ml);
-  if (need > 0 && (scratch == nullptr || scratch_bytes < need)) return PMOE_EINVAL;
+  const attn::Layout lay = attn::scratch_layout(a);
+  if (scratch == nullptr || scratch_bytes < lay.bytes) return PMOE_EINVAL;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
   a.scale = scale != 0.f ? scale * attn::kLog2e : 1e-30f;  // not 0: masked scores are -inf times it
@@ -529,9 +715,10 @@ extern "C" int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64
   a.lse = lse;
   a.err = err_out;
   a.o_part = static_cast<float*>(scratch);
-  a.ml_part = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + ml);
+  a.ml_part = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + lay.ml);
+  a.base = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(scratch) + lay.base);
   cudaStream_t s = (cudaStream_t)stream;
   const bool f8 = kv->dtype == PMOE_KV_E4M3;
-  if (kv->head_dim == 128) return f8 ? attn::launch_all<128, true>(a, s) : attn::launch_all<128, false>(a, s);
-  return f8 ? attn::launch_all<64, true>(a, s) : attn::launch_all<64, false>(a, s);
+  if (kv->head_dim == 128) return f8 ? attn::launch_all<128, true>(a, sms, s) : attn::launch_all<128, false>(a, sms, s);
+  return f8 ? attn::launch_all<64, true>(a, sms, s) : attn::launch_all<64, false>(a, sms, s);
 }

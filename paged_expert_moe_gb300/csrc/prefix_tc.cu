@@ -54,9 +54,6 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// r / group for r < 2^24 and group <= 64: magic = 2^32 / group + 1
-__device__ __forceinline__ int row_token(const Args& a, int r) { return a.group == 1 ? r : (int)__umulhi((uint32_t)r, a.group_magic); }
-
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t sfull[2], pready[2], odone[2], qfull[2], staged[2], drain;
@@ -153,6 +150,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_trigger();  // the stream kernel may take the SMs that this one is done with
   fence_before();
   __syncthreads();
   fence_after();
@@ -541,7 +539,7 @@ int make_map(const Args& a, void* base, CUtensorMap* m) {
   const uint64_t dims[4] = {D, page, (uint64_t)a.kv.kv_heads, (uint64_t)a.kv.num_pages};
   const uint64_t strides[3] = {D * 2, page * D * 2, (uint64_t)a.kv.page_stride * 2};
   const uint32_t box[4] = {64, (uint32_t)std::min<uint64_t>(page, kTcKeys), 1, 1};
-  return tc_encode_bf16_map(m, base, 4, dims, strides, box);
+  return tc_encode_map(m, base, 4, dims, strides, box, kTcMapBf16Sw128);
 }
 
 template <int D, bool F8>

@@ -1068,8 +1068,8 @@ int encode(CUtensorMap* m, void* base, int rank, const cuuint64_t* dims, const c
 
 }  // namespace
 
-int tc_encode_bf16_map(CUtensorMap* m, void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-                       const uint32_t* box) {
+int tc_encode_map(CUtensorMap* m, void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                  const uint32_t* box, TcMapKind kind) {
   cuuint64_t d[5], st[4];
   cuuint32_t bx[5];
   for (int i = 0; i < rank; ++i) {
@@ -1077,7 +1077,8 @@ int tc_encode_bf16_map(CUtensorMap* m, void* base, int rank, const uint64_t* dim
     bx[i] = box[i];
     if (i + 1 < rank) st[i] = strides_bytes[i];
   }
-  return encode(m, base, rank, d, st, bx);
+  return encode(m, base, rank, d, st, bx,
+                kind == kTcMapBf16Sw128 ? kMapBf16Sw128 : kind == kTcMapBytesSw128 ? kMapBytesSw128 : kMapBytesSw64);
 }
 
 namespace {

@@ -27,9 +27,11 @@ struct TcMaps {
   CUtensorMap gu4;
 };
 
-// Tensor map of bf16 elements with the 128-byte swizzle (PMOE_OK or PMOE_ECUDA).
-int tc_encode_bf16_map(CUtensorMap* m, void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-                       const uint32_t* box);
+// Tensor map of bf16 elements with the 128-byte swizzle, or of bytes with the 128- or 64-byte
+// one (PMOE_OK or PMOE_ECUDA).
+enum TcMapKind { kTcMapBf16Sw128, kTcMapBytesSw128, kTcMapBytesSw64 };
+int tc_encode_map(CUtensorMap* m, void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                  const uint32_t* box, TcMapKind kind);
 bool tc_supported(int H, int I);
 // Weight tensor maps over one layer's slot arena: bf16 rows (128-byte swizzle) or the raw
 // quantised bytes (dequantised in shared memory); block-FP8 also as 128-byte swizzled

@@ -132,6 +132,15 @@ SIZES = [
     (131, 4, 2, 128, 32, False, 385, 40),
     (9, 32, 4, 128, 16, False, 0, 50),
     (130, 7, 7, 64, 16, False, 130, 3),
+    # enough rows and keys for the tensor-core kernel
+    (300, 16, 2, 128, 16, False, 1000, 20),
+    (300, 16, 2, 64, 32, True, 1100, 20),
+    (257, 8, 1, 128, 64, True, 900, 0),
+    (520, 4, 2, 64, 128, False, 900, 33),
+    (1100, 2, 1, 128, 256, False, 641, 17),
+    (290, 10, 1, 128, 16, True, 1281, 9),
+    # rows beyond one block of the stream kernel
+    (2050, 1, 1, 64, 16, False, 5, 3),
 ]
 
 
@@ -150,7 +159,7 @@ def test_attention_matches_oracle(pm, T, Hq, Hkv, D, page, e4m3, prefix, suffix)
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("T,Hq", [(2, 8), (40, 16)])
+@pytest.mark.parametrize("T,Hq", [(2, 8), (40, 16), (300, 16)])
 def test_peaked_and_shifted_scores(pm, e4m3, T, Hq):
     """Large scores of either sign: the running maximum moves far between tiles."""
     c = make(77, T, Hq, 2, 128, 16, e4m3, 900, 200, qscale=30.0)
@@ -160,8 +169,9 @@ def test_peaked_and_shifted_scores(pm, e4m3, T, Hq):
     check(c, out, lse, scale=-0.05)
 
 
-def test_rows_share_sequences_and_padded_layouts(pm):
-    c = make(5, 12, 8, 2, 64, 16, False, 100, 90, seqs=3, page_gap=128, q_gap=24)
+@pytest.mark.parametrize("T,prefix", [(12, 100), (400, 1300)])
+def test_rows_share_sequences_and_padded_layouts(pm, T, prefix):
+    c = make(5, T, 8, 2, 64, 16, False, prefix, 90, seqs=3, page_gap=128, q_gap=24)
     out, lse = run(pm, c)
     check(c, out, lse)
 
@@ -215,8 +225,9 @@ def test_bad_pages_lengths_and_rows_are_reported(pm, T):
     check(good, out, lse, rows=[i for i in range(T) if i != 1])
 
 
-def test_same_bits_twice_on_another_stream_and_in_a_graph(pm):
-    c = make(9, 40, 16, 2, 128, 16, False, 2000, 100)
+@pytest.mark.parametrize("prefix", [300, 8000])
+def test_same_bits_twice_on_another_stream_and_in_a_graph(pm, prefix):
+    c = make(9, 40, 16, 2, 128, 16, False, prefix, 100)
     out, lse = run(pm, c)
     again, _ = run(pm, c)
     assert torch.equal(out, again)
@@ -227,7 +238,7 @@ def test_same_bits_twice_on_another_stream_and_in_a_graph(pm):
     other = pm.moe_prefix_attention(*args, stream=s)
     s.synchronize()
     assert torch.equal(out, other)
-    scratch = torch.empty(pm.moe_prefix_attention_scratch_bytes(c["k"], c["v"], 40, 16, 2000, 100), dtype=torch.uint8,
+    scratch = torch.empty(pm.moe_prefix_attention_scratch_bytes(c["k"], c["v"], 40, 16, prefix, 100), dtype=torch.uint8,
                           device="cuda")
     held = torch.zeros_like(out)
     g = torch.cuda.CUDAGraph()
@@ -238,11 +249,12 @@ def test_same_bits_twice_on_another_stream_and_in_a_graph(pm):
     assert torch.equal(out, held)
 
 
-def test_offsets_past_32_bits(pm):
+@pytest.mark.parametrize("T", [40, 160])
+def test_offsets_past_32_bits(pm, T):
     """Pages beyond 2^32 elements into the cache, in the prefix and the suffix."""
     page, D, Hkv = 256, 128, 8
     pages = 2 ** 32 // (page * D * Hkv) + 3
-    c = make(10, 40, 32, 8, 128, 256, True, 256, 256, lens=[200] * 40, seqs=2)
+    c = make(10, T, 32, 8, 128, 256, True, 256, 256, lens=[200] * T, seqs=2)
     k = torch.zeros((pages, Hkv, page, D), dtype=torch.float8_e4m3fn, device="cuda")
     v = torch.zeros_like(k)
     far = {}
@@ -253,6 +265,15 @@ def test_offsets_past_32_bits(pm):
            "pt": np.array([[far[int(x[0])]] for x in c["pt"]], np.int32)}
     out, lse = run(pm, big)
     check(c, out, lse)
+
+
+def test_a_bad_prefix_page_is_reported_by_the_tensor_core_kernel(pm):
+    for e4m3 in (False, True):
+        c = make(12, 300, 16, 2, 128, 16, e4m3, 1000, 20)
+        c["pp"][7] = c["k"].shape[0]
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        run(pm, c, err_out=err)
+        assert int(err) == 64
 
 
 def test_attention_refusals(pm):
