@@ -9,7 +9,8 @@
 // barrier of the block: a ring of 16-key tiles of its own that TMA fills (a tile lies inside
 // one page; one box for K, one for V), mma.sync on 16 query rows, softmax in registers. The
 // (item, tile) units of all items, in order, are cut into equal runs, one a warp of every
-// SM, whatever the lengths; a warp whose run ends inside an item leaves a part of it.
+// SM, whatever the lengths; a warp whose run ends inside an item leaves a part of it. An item
+// counts for kHead units more than its tiles: short ones cost more than their keys.
 #include "attn.cuh"
 #include "tc_gemm.h"
 #include "tc_ptx.cuh"
@@ -24,6 +25,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 16;       // keys of a unit
+constexpr int kHead = 1;        // empty units at the start of an item
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int64_t kStreamTraffic = 24 << 20;
@@ -53,6 +55,15 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// What a warp has to know of a unit, noted in shared memory beside its stage.
+struct Unit {
+  int tile, tiles;  // of the item
+  int valid;        // keys of this tile that the item sees, up to kTile
+  int h;            // kv head
+  int t;            // token; < 0: the prefix, whose rows are all T * group of them
+  int row0;         // first query row of the item, in the token's group or in all rows
+};
+
 template <int D, bool F8>
 struct StreamCfg {
   static constexpr int kTileBytes = kTile * D * (F8 ? 1 : 2);  // of K, and of V
@@ -60,7 +71,8 @@ struct StreamCfg {
   // 24 KB a warp and 192 KB an SM in flight; HBM's share of an SM over its latency is 50 KB
   static constexpr int kFit = 24576 / kStage, kStages = kFit < 8 ? kFit : 8;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kSmem = 1024 /* alignment */ + kRing + kWarps * kStages * 8 + (kRowBlock + 1) * 8 + 64 * 8;
+  static constexpr int kSmem = 1024 /* alignment */ + kRing + kWarps * kStages * (8 + (int)sizeof(Unit)) +
+                               (kRowBlock + 1) * 8 + kRowBlock * 4 + 64 * 8;
   // Where 16-byte chunk c of row r lies in a K or V tile (as the TMA swizzle puts it)
   static __device__ __forceinline__ uint32_t place(int r, int c) {
     if (!F8) return (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -73,56 +85,13 @@ struct StreamCfg {
   static __device__ __forceinline__ int key_row(int j) { return F8 && D == 128 ? (j >> 1) | ((j & 1) << 2) : j; }
 };
 
-// An item: up to 16 query rows of one kv head and the keys they attend to.
-struct Item {
-  int64_t first, end;    // its units
-  const int32_t* pages;  // its page list
-  int keys, h;
-  int t, row0, rows;     // rows: heads row0.. of token t's group; t < 0: rows row0.. of all T * group
-};
-
-__device__ __forceinline__ Item find_item(const Args& a, const int64_t* base, int nrows, int t0, int64_t pre, int64_t u) {
-  Item it;
-  if (u < pre) {
-    const int i = (int)(u / a.pre_tiles), rt = i / a.kv.kv_heads;
-    it.first = (int64_t)i * a.pre_tiles;
-    it.end = it.first + a.pre_tiles;
-    it.pages = a.prefix_pages;
-    it.keys = a.prefix_len;
-    it.h = i - rt * a.kv.kv_heads;
-    it.t = -1;
-    it.row0 = rt * 16;
-    it.rows = min(16, a.T * a.group - it.row0);
-    return it;
-  }
-  int lo = 0, hi = nrows;  // base[lo] <= u < base[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (base[mid] <= u)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int64_t b = base[lo], n = base[lo + 1] - b;
-  const int nt = (int)(n / a.head_items), i = (int)((u - b) / nt), rts = a.head_items / a.kv.kv_heads;
-  it.first = b + (int64_t)i * nt;
-  it.end = it.first + nt;
-  it.t = t0 + lo;
-  const int seq = a.row_seq != nullptr ? a.row_seq[it.t] : it.t;
-  const bool ok = (unsigned)seq < (unsigned)a.sequences;
-  if (!ok && a.err != nullptr) atomicOr(a.err, kErrBadPage);
-  // an invalid row reads row 0 of the table: in bounds, and its output is undefined
-  it.pages = a.page_table + (int64_t)(ok ? seq : 0) * a.table_stride;
-  it.keys = suffix_keys(a, it.t);
-  it.h = i / rts;
-  it.row0 = (i - it.h * rts) * 16;
-  it.rows = min(16, a.group - it.row0);
-  return it;
-}
-
 // Units of a row's suffix, and the share of a warp.
 __device__ __forceinline__ int64_t row_units(const Args& a, int keys) {
-  return (int64_t)((keys + kTile - 1) / kTile) * a.head_items;
+  return keys > 0 ? (int64_t)((keys + kTile - 1) / kTile + kHead) * a.head_items : 0;
+}
+// The first unit with keys of an item, `origin` the first of its row's (or the prefix's) units.
+__device__ __forceinline__ int64_t first_unit(int64_t origin, int item, int tiles) {
+  return origin + (int64_t)item * (tiles + kHead) + kHead;
 }
 __device__ __forceinline__ int64_t share_of(const Args& a, int64_t units) {
   return max((int64_t)a.min_share, (units + a.warps - 1) / a.warps);
@@ -139,9 +108,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* base = reinterpret_cast<int64_t*>(bars + kWarps * C::kStages);  // [nrows + 1]
   int64_t* sums = base + kRowBlock + 1;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sums + kWarps);
+  int32_t* keys = reinterpret_cast<int32_t*>(sums + 64);  // [nrows]
+  Unit* notes = reinterpret_cast<Unit*>(keys + kRowBlock);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int t0 = block * kRowBlock, nrows = a.max_suffix > 0 ? min(kRowBlock, a.T - t0) : 0;
-  const int64_t pre = block == 0 ? (int64_t)a.pre_items * a.pre_tiles : 0;
+  const int64_t pre = block == 0 && a.pre_tiles > 0 ? (int64_t)a.pre_items * (a.pre_tiles + kHead) : 0;
   pdl_trigger();
 
   // ---- the first unit of every row: thread i sums 8 rows
@@ -149,7 +120,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = tid * 8 + i;
-    mine[i] = r < nrows ? row_units(a, suffix_keys(a, t0 + r)) : 0;
+    const int n = r < nrows ? suffix_keys(a, t0 + r) : 0;
+    if (r < nrows) keys[r] = n;
+    mine[i] = row_units(a, n);
     sum += mine[i];
   }
   int64_t upto = sum;
@@ -195,46 +168,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* mystage = ring + warp * C::kStages * C::kStage;
   uint64_t* bar = bars + warp * C::kStages;
 
-  // the loading side: item and page ids of the next unit to load
-  Item li{};
-  int64_t lu = u0, lids = -1;
-  int ids = 0;
+  Unit* note = notes + warp * C::kStages;
+
+  // ---- the loading side: lane i works out unit `batch` + i of the run, with its page id
+  int64_t batch = u0 - 32;
+  Unit mu{};
+  int id = 0, row = 0, loaded = 0;
+  uint32_t todo = 0;  // lanes whose units are still to be loaded
   auto load = [&]() {
-    if (lu >= u1) return;
-    if (lu >= li.end) {
-      li = find_item(a, base, nrows, t0, pre, lu);
-      lids = -1;
-    }
-    const int tile = (int)(lu - li.first);
-    if (lids < 0 || tile >= lids + 32) {  // the next 32 tiles' pages, one a lane
-      lids = tile;
-      const int key = (tile + lane) * kTile;
-      ids = 0;
-      if (key < li.keys && lu + lane < u1) {
-        ids = __ldg(li.pages + (key >> psh));
-        if ((unsigned)ids >= (unsigned)a.kv.num_pages) {
-          if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
-          ids = a.kv.num_pages;  // out of the map's range: reads as zeros
+    while (todo == 0) {
+      batch += 32;
+      if (batch >= u1) return;
+      const int64_t v = batch + lane;
+      bool live = v < u1;
+      if (live) {
+        int64_t r;  // unit of its row, or of the prefix
+        const int32_t* pages;
+        int n;
+        if (v < pre) {
+          r = v;
+          n = a.prefix_len;
+          pages = a.prefix_pages;
+          mu.t = -1;
+        } else {
+          int lo = 0, hi = nrows;  // base[lo] <= v < base[hi]
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (base[mid] <= v)
+              lo = mid;
+            else
+              hi = mid;
+          }
+          r = v - base[lo];
+          n = keys[lo];
+          mu.t = t0 + lo;
+          const int seq = a.row_seq != nullptr ? a.row_seq[mu.t] : mu.t;
+          const bool ok = (unsigned)seq < (unsigned)a.sequences;
+          if (!ok && a.err != nullptr) atomicOr(a.err, kErrBadPage);
+          // an invalid row reads row 0 of the table: in bounds, and its output is undefined
+          pages = a.page_table + (int64_t)(ok ? seq : 0) * a.table_stride;
+        }
+        mu.tiles = (n + kTile - 1) / kTile;
+        const int span = mu.tiles + kHead;
+        const int item = r >> 32 ? (int)(r / span) : (int)((uint32_t)r / (uint32_t)span);
+        mu.tile = (int)(r - (int64_t)item * span) - kHead;
+        live = mu.tile >= 0;
+        if (mu.t < 0) {
+          const int rt = item / a.kv.kv_heads;
+          mu.h = item - rt * a.kv.kv_heads;
+          mu.row0 = rt * 16;
+        } else {
+          const int rts = a.head_items / a.kv.kv_heads;
+          mu.h = item / rts;
+          mu.row0 = (item - mu.h * rts) * 16;
+        }
+        if (live) {
+          const int key = mu.tile * kTile;
+          mu.valid = min(kTile, n - key);
+          row = key & (a.kv.page_size - 1);
+          id = __ldg(pages + (key >> psh));
+          if ((unsigned)id >= (unsigned)a.kv.num_pages) {
+            if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
+            id = a.kv.num_pages;  // out of the map's range: reads as zeros
+          }
         }
       }
+      todo = __ballot_sync(0xffffffffu, live);
     }
-    const int id = __shfl_sync(0xffffffffu, ids, tile - (int)lids);
-    if (lane == 0) {
-      const int s = (int)((lu - u0) % C::kStages), row = (tile * kTile) & (a.kv.page_size - 1);
+    const int s = loaded % C::kStages;
+    if (lane == __ffs(todo) - 1) {
+      note[s] = mu;
       mbar_arrive_expect_tx(&bar[s], C::kStage);
-      tma_load_5d(mystage + s * C::kStage, &map_k, &bar[s], 0, row, 0, li.h, id);
-      tma_load_5d(mystage + s * C::kStage + C::kTileBytes, &map_v, &bar[s], 0, row, 0, li.h, id);
+      tma_load_5d(mystage + s * C::kStage, &map_k, &bar[s], 0, row, 0, mu.h, id);
+      tma_load_5d(mystage + s * C::kStage + C::kTileBytes, &map_v, &bar[s], 0, row, 0, mu.h, id);
     }
-    ++lu;
+    todo &= todo - 1;
+    ++loaded;
+    __syncwarp();
   };
 #pragma unroll 1
   for (int i = 0; i < C::kStages; ++i) load();
 
   bool ok = true;
-  int64_t u = u0;
-  while (u < u1 && ok) {
-    const Item it = find_item(a, base, nrows, t0, pre, u);
-    const int64_t stop = min(it.end, u1);
+  int used = 0;  // units
+  while (used < loaded && ok) {
+    const Unit it = note[used % C::kStages];  // the first unit of an item, or of this warp's part of it
+    const int rows = it.t < 0 ? min(16, a.T * a.group - it.row0) : min(16, a.group - it.row0);
     // ---- query fragments; rows beyond the last are zero
     uint32_t qf[D / 16][4];
     float qmul[2];  // what a score of rows g and g + 8 is multiplied by
@@ -245,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = g + 8 * e;
-        live[e] = i < it.rows;
+        live[e] = i < rows;
         const int r = it.row0 + (live[e] ? i : 0), tok = it.t < 0 ? row_token(a, r) : it.t;
         const int head = it.h * a.group + (it.t < 0 ? r - tok * a.group : r);
         qp[e] = a.q + (int64_t)tok * a.q_stride + head * D;
@@ -300,14 +319,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // by 2^8 (any base gives the same quotient), so the sums are seldom rescaled
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    for (; u < stop; ++u) {
-      const int n = (int)(u - u0), s = n % C::kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar[s], (n / C::kStages) & 1, abort_flag, a.err))) {
+    // until the item's last tile, or the run's
+    for (bool more = true; more;) {
+      const int s = used % C::kStages, tile = note[s].tile, valid = note[s].valid;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar[s], (used / C::kStages) & 1, abort_flag, a.err))) {
         ok = false;
         break;
       }
       const uint32_t ks = smem_u32(mystage + s * C::kStage), vs = ks + C::kTileBytes;
-      const int valid = it.keys - (int)(u - it.first) * kTile;
       if (valid < kTile) {
         // values beyond the last key may be anything, and 0 x NaN is NaN
         constexpr int CH = C::kTileBytes / kTile / 16;  // 16-byte chunks of a row
@@ -399,13 +418,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      __syncwarp();  // every lane has read the stage
+      __syncwarp();  // every lane has read the stage and its note
+      ++used;
       load();
+      more = tile + 1 < it.tiles && used < loaded;
     }
     if (!ok) break;
 
     // ---- the part
-    const int part = (int)(w - it.first / share) + (it.t < 0 ? 0 : a.prefix_parts);
+    const int64_t origin = it.t < 0 ? 0 : base[it.t - t0];
+    const int item = it.t < 0 ? it.row0 / 16 * a.kv.kv_heads + it.h : it.h * (a.head_items / a.kv.kv_heads) + it.row0 / 16;
+    const int part = (int)(w - first_unit(origin, item, it.tiles) / share) + (it.t < 0 ? 0 : a.prefix_parts);
     const float vscale = F8 ? a.kv.v_scale[it.h] : 1.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -429,10 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // copies in flight land before the CTA leaves, even after a wait that gave up
   if (!ok)
-    for (int64_t i = max(u, lu - C::kStages); i < lu; ++i) {
-      const int n = (int)(i - u0);
+    for (int i = used; i < loaded; ++i) {
       const long long c0 = clock64();
-      while (!mbar_try_wait(&bar[n % C::kStages], (n / C::kStages) & 1) && clock64() - c0 < kWaitLimit) {
+      while (!mbar_try_wait(&bar[i % C::kStages], (i / C::kStages) & 1) && clock64() - c0 < kWaitLimit) {
       }
     }
   pdl_wait();  // the combine kernel follows this one only: the tensor-core kernel is done then too
@@ -455,14 +477,14 @@ __global__ void __launch_bounds__(W * 32 < 128 ? 128 : W * 32) combine_kernel(co
   const int64_t* base = a.base + (int64_t)(t / kRowBlock) * (kRowBlock + 1);
   if (a.pre_tiles > 0) {
     const int64_t share = share_of(a, a.base[a.max_suffix > 0 ? min(kRowBlock, a.T) : 0]);
-    const int64_t f = ((int64_t)((t * a.group + r) / 16) * a.kv.kv_heads + h) * a.pre_tiles;
+    const int64_t f = first_unit(0, (t * a.group + r) / 16 * a.kv.kv_heads + h, a.pre_tiles);
     pre = (int)((f + a.pre_tiles - 1) / share - f / share) + 1;
   }
   if (a.max_suffix > 0) {
     const int nt = (suffix_keys(a, t) + kTile - 1) / kTile;
     if (nt > 0) {
       const int64_t share = share_of(a, base[min(kRowBlock, a.T - t / kRowBlock * kRowBlock)]);
-      const int64_t f = base[t % kRowBlock] + (int64_t)(h * (a.head_items / a.kv.kv_heads) + r / 16) * nt;
+      const int64_t f = first_unit(base[t % kRowBlock], h * (a.head_items / a.kv.kv_heads) + r / 16, nt);
       suf = (int)((f + nt - 1) / share - f / share) + 1;
     }
   }
@@ -654,7 +676,7 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
     if (pre_rts == 1 || traffic <= kStreamTraffic) {
       a->pre_tiles = (prefix_len + kTile - 1) / kTile;
       a->pre_items = (int)(pre_rts * kv->kv_heads);
-      const int64_t units = (int64_t)a->pre_tiles * a->pre_items;
+      const int64_t units = (int64_t)(a->pre_tiles + kHead) * a->pre_items;
       const int64_t share = std::max<int64_t>(a->min_share, (units + a->warps - 1) / a->warps);
       a->prefix_parts = (int)((a->pre_tiles - 1) / share + 2);
     } else {
