@@ -241,6 +241,20 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _scratch(nbytes, stream, like):
+    """(address, release) of nbytes of stream-ordered device memory from torch's caching
+    allocator. Releasing right after the launches is safe: whatever reuses the block on this
+    stream runs after them. (A tensor for it costs 8 us a call more, next to launches.)"""
+    import torch
+    alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+    if alloc is None:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream)):
+            held = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return held.data_ptr(), held.untyped_storage
+    p = alloc(nbytes, stream)
+    return p, lambda: torch._C._cuda_cudaCachingAllocator_raw_delete(p)
+
+
 def _kv_desc(k_cache, v_cache, k_scale, v_scale):
     """pmoe_kv_desc of a paged cache: CUDA bf16 or float8_e4m3fn [num_pages, kv_heads,
     page_size, head_dim] tensors of the same strides, contiguous but for the page stride."""
@@ -328,16 +342,23 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
     lib = load()
     if out is None:
         out = _empty((T, q_heads, dim), torch.bfloat16, q, stream)
-    if scratch is None:
+    raw = _raw_stream(stream, q)
+    release = None
+    if scratch is not None:
+        nbytes = scratch.numel()
+        work = _opt(scratch, torch.uint8, nbytes)
+    else:
         nbytes = lib.moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix)
-        if nbytes:
-            scratch = _empty(nbytes, torch.uint8, q, stream)
-    nbytes = 0 if scratch is None else scratch.numel()
-    _check(lib.moe_prefix_attention(desc, *_heads(q, T, q_heads, dim), T, q_heads, dim ** -0.5 if scale is None else scale,
-                                    pages, prefix_len, table, width, sequences, _opt(row_seq, i32, T), lens, max_suffix,
-                                    _opt(out, torch.bfloat16, T * q_heads * dim), _opt(lse_out, torch.float32, T * q_heads),
-                                    _opt(scratch, torch.uint8, nbytes), nbytes, _opt(err_out, i32, 1),
-                                    _raw_stream(stream, q)), "moe_prefix_attention")
+        work, release = _scratch(nbytes, raw, q) if nbytes else (None, None)
+    try:
+        _check(lib.moe_prefix_attention(desc, *_heads(q, T, q_heads, dim), T, q_heads,
+                                        dim ** -0.5 if scale is None else scale, pages, prefix_len, table, width, sequences,
+                                        _opt(row_seq, i32, T), lens, max_suffix, _opt(out, torch.bfloat16, T * q_heads * dim),
+                                        _opt(lse_out, torch.float32, T * q_heads), work, nbytes, _opt(err_out, i32, 1), raw),
+               "moe_prefix_attention")
+    finally:
+        if release is not None:
+            release()
     return out
 
 

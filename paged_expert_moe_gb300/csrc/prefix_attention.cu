@@ -25,7 +25,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 16;       // keys of a unit
-constexpr int kHead = 1;        // empty units at the start of an item
+constexpr int kHead = 2;        // empty units at the start of an item
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int64_t kStreamTraffic = 24 << 20;
@@ -68,8 +68,9 @@ template <int D, bool F8>
 struct StreamCfg {
   static constexpr int kTileBytes = kTile * D * (F8 ? 1 : 2);  // of K, and of V
   static constexpr int kStage = 2 * kTileBytes;
-  // 24 KB a warp and 192 KB an SM in flight; HBM's share of an SM over its latency is 50 KB
-  static constexpr int kFit = 24576 / kStage, kStages = kFit < 8 ? kFit : 8;
+  // 16 KB a warp and 128 KB an SM in flight; what HBM delivers an SM within its latency is 50
+  // KB, and 24 KB a warp is slower (52 against 50.6 us for 256 rows of 1..1,024 keys)
+  static constexpr int kFit = 16384 / kStage, kStages = kFit < 8 ? kFit : 8;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kSmem = 1024 /* alignment */ + kRing + kWarps * kStages * (8 + (int)sizeof(Unit)) +
                                (kRowBlock + 1) * 8 + kRowBlock * 4 + 64 * 8;
@@ -491,32 +492,41 @@ __global__ void __launch_bounds__(W * 32 < 128 ? 128 : W * 32) combine_kernel(co
   const int parts = pre + suf, skip = a.prefix_parts - pre;
   auto slot = [&](int p) { return (int64_t)(p < pre ? p : p + skip) * rh + i; };
 
+  // warp w takes parts w, w + W, ..: lane i looks at the i-th of them
+  __shared__ float tops[W];
+  float2 ml = make_float2(-INFINITY, 0.f);
   float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.ml_part[slot(p)].x);
+  for (int p = w + lane * W; p < parts; p += 32 * W) {
+    const float2 x = a.ml_part[slot(p)];
+    if (p < 32 * W) ml = x;
+    m = fmaxf(m, x.x);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if constexpr (W > 1) {
+    if (lane == 0) tops[w] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < W; ++k) m = fmaxf(m, tops[k]);
+  }
   const float top = m == -INFINITY ? 0.f : m;
   float l = 0.f, acc[V];
 #pragma unroll
   for (int d = 0; d < V; ++d) acc[d] = 0.f;
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    float f = 0.f;
-    if (p0 + lane < parts) {
-      const float2 ml = a.ml_part[slot(p0 + lane)];
-      f = ex2(ml.x - top);
-      l = fmaf(ml.y, f, l);
-    }
-    const int n = min(32, parts - p0);
-    constexpr int U = 4;  // parts in flight
-    for (int j0 = w; j0 < n; j0 += U * W) {
+  for (int p0 = 0; p0 < parts; p0 += 32 * W) {
+    if (p0 > 0) ml = p0 + w + lane * W < parts ? a.ml_part[slot(p0 + w + lane * W)] : make_float2(-INFINITY, 0.f);
+    const float f = ex2(ml.x - top);
+    l = fmaf(ml.y, f, l);
+    const int n = min(32, (parts - p0 - w + W - 1) / W);  // of this warp
+    constexpr int U = W == 16 ? 8 : 4;  // parts in flight
+    for (int j0 = 0; j0 < n; j0 += U) {
       float v[U][V];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int j = j0 + k * W;
 #pragma unroll
         for (int d = 0; d < V; ++d) v[k][d] = 0.f;
-        if (j < n) {
-          const float* src = a.o_part + slot(p0 + j) * D + lane * V;
+        if (j0 + k < n) {
+          const float* src = a.o_part + slot(p0 + w + (j0 + k) * W) * D + lane * V;
           if constexpr (V == 4) {
             const float4 x = *reinterpret_cast<const float4*>(src);
             v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
@@ -528,9 +538,8 @@ __global__ void __launch_bounds__(W * 32 < 128 ? 128 : W * 32) combine_kernel(co
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int j = j0 + k * W;
-        const float fj = __shfl_sync(0xffffffffu, f, j < n ? j : 0);
-        if (j < n) {
+        const float fj = __shfl_sync(0xffffffffu, f, j0 + k < n ? j0 + k : 0);
+        if (j0 + k < n) {
 #pragma unroll
           for (int d = 0; d < V; ++d) acc[d] = fmaf(v[k][d], fj, acc[d]);
         }
@@ -540,13 +549,15 @@ __global__ void __launch_bounds__(W * 32 < 128 ? 128 : W * 32) combine_kernel(co
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if constexpr (W > 1) {
-    const int set = (threadIdx.x >> 5) / W;  // 0 but for several row-heads a block
-    static_assert(kRowHeads == 1, "one row-head a block");
-    (void)set;
+    __syncthreads();  // tops is free
 #pragma unroll
     for (int d = 0; d < V; ++d) red[w][lane * V + d] = acc[d];
+    if (lane == 0) tops[w] = l;
     __syncthreads();
     if (w != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) l += tops[k];
 #pragma unroll
     for (int d = 0; d < V; ++d) {
       float x = 0.f;

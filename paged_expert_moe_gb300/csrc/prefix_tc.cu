@@ -38,10 +38,9 @@ struct TcCfg {
   static constexpr int kSlots = D == 128 ? 5 : 8;         // ring of K and V tiles
   static constexpr int kThreads = F8 ? 512 : 384;         // whole warpgroups
   // Registers a thread, by warpgroup: what the other roles give up the softmax takes. The
-  // launch has 168 x 384 = 64,512 (bf16) or 128 x 512 = 65,536 (e4m3) of them; the shares add
-  // up to 200 x 256 + 104 x 128 = 64,512 and 160 x 256 + 88 x 128 + 104 x 128 = 65,536.
-  static constexpr int kSoftmaxRegs = F8 ? 160 : 200, kMmaRegs = F8 ? 88 : 104;
-  static constexpr int kLoaderRegs = F8 ? 104 : 0;
+  // launch has 168 (bf16) or 128 (e4m3) of them for each of its threads.
+  static constexpr int kSoftmaxRegs = F8 ? 168 : 200, kMmaRegs = F8 ? 72 : 104, kLoaderRegs = F8 ? 104 : 0;
+  static_assert(kSoftmaxRegs * 256 + (kMmaRegs + kLoaderRegs) * 128 <= (F8 ? 128 : 168) * kThreads, "register shares");
   static constexpr int kRing = kSlots * kTileBytes;
   static constexpr int kSmem = kRing + 2 * kQBytes + 1024 /* alignment */ + 1024 /* row factors */ + 512;
   static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
@@ -144,17 +143,11 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       prefetch_map(&map_v);
     }
   }
-  if (warp == 8) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)),
-                 "r"(C::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   pdl_trigger();  // the stream kernel may take the SMs that this one is done with
-  fence_before();
   __syncthreads();
-  fence_after();
-  const uint32_t tmem = b.tmem;
+  // The issuing warp allocates all 512 columns: the base is column 0, lane 0. The other roles
+  // touch TMEM only after its first products.
+  constexpr uint32_t tmem = 0;
   const int64_t units = tc_units(a);
   int64_t u = (int64_t)blockIdx.x * units / a.tc_ctas;
   const int64_t end = (int64_t)(blockIdx.x + 1) * units / a.tc_ctas;
@@ -176,7 +169,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       // A negative scale goes into the sign of Q, so that the largest score stays the largest.
       const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
       const int c = row % LPR;
-      constexpr int kPasses = LPR, kAhead = F8 ? 8 : LPR;  // rows of a thread, and how many it has in flight
+      constexpr int kPasses = LPR, kAhead = LPR;  // rows of a thread, all in flight
 #pragma unroll
       for (int p0 = 0; p0 < kPasses; p0 += kAhead) {
         uint4 v[kAhead];
@@ -225,39 +218,19 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
           break;
         }
         fence_after();
-        // scores of 32 keys; -inf beyond the prefix. A bf16 cache's kernel has the registers
-        // to keep all 128, with the e4m3 loaders in the CTA they are read twice.
+        float s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+        tmem_wait_ld();
         const int valid = a.prefix_len - t * kTcKeys;
-        auto fetch = [&](int i, float* s) {
-          tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s));
-          tmem_wait_ld();
-          if (valid < kTcKeys) {
+        if (valid < kTcKeys) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (32 * i + k >= valid) s[k] = -INFINITY;
-          }
-        };
-        float s[F8 ? 32 : 128];
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if constexpr (!F8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
-          tmem_wait_ld();
-          if (valid < kTcKeys) {
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i >= valid) s[i] = -INFINITY;
-          }
-#pragma unroll
-          for (int i = 0; i < 128; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            fetch(i, s);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) x[(k >> 1) & 3] = max3(x[(k >> 1) & 3], s[k], s[k + 1]);
-          }
+          for (int i = 0; i < 128; ++i)
+            if (i >= valid) s[i] = -INFINITY;
         }
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
         const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
         if (t == sg.t0) {
           m = mx;
@@ -285,8 +258,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t p[16];
-          if constexpr (F8) fetch(i, s);
-          const float* sc = F8 ? s : s + 32 * i;
+          const float* sc = s + 32 * i;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float y, z;
@@ -353,6 +325,10 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
     if (warp == 8) {
     // ---------------- MMA issuer
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)),
+                 "r"(C::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     const uint32_t is = idesc_bf16(128, kTcKeys) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u);
     const uint32_t io = (idesc_bf16(128, D) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u)) | (1u << 16);  // B: N contiguous
     const uint32_t ring = smem_u32(smem), qa = smem_u32(qs);
@@ -475,54 +451,73 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoaderRegs));
     constexpr int CH = D / 16;  // 16-code chunks of a row
     constexpr int N = kTcKeys * CH / 128;
-    const int tid = threadIdx.x - 12 * 32, ch = tid % CH;
+    const int tid = threadIdx.x - 12 * 32, ch = tid % CH, r0 = tid / CH;
+    // page ids of a tile's rows of this thread, fetched a tile ahead of its values
+    auto fetch_ids = [&](int t, int (&ids)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int key = t * kTcKeys + r0 + i * (128 / CH);
+        ids[i] = key < a.prefix_len ? __ldg(a.prefix_pages + (key >> psh)) : -2;
+      }
+    };
+    auto fetch = [&](const void* cache, int t, int h, const int (&ids)[N], uint4 (&raw)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int key = t * kTcKeys + r0 + i * (128 / CH);
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if ((unsigned)ids[i] < (unsigned)a.kv.num_pages)
+          raw[i] = __ldg(reinterpret_cast<const uint4*>(
+              static_cast<const uint8_t*>(cache) + (int64_t)ids[i] * a.kv.page_stride +
+              ((int64_t)h * a.kv.page_size + (key & (a.kv.page_size - 1))) * D + ch * 16));
+        else if (ids[i] != -2 && a.err != nullptr)
+          atomicOr(a.err, kErrBadPage);
+      }
+    };
     uint32_t kv = 0;
     bool ok = true;
-    while (ok && segment(a, &u, end, &sg)) {
-      for (int t = sg.t0; t < sg.t1 && ok; ++t) {
-        int64_t off[N];
+    auto put = [&](const uint4 (&raw)[N]) {  // the tile to the ring
+      const uint32_t slot = kv % kSlots;
+      if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) {
+        ok = false;
+        return;
+      }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int key = t * kTcKeys + tid / CH + i * (128 / CH);
-          off[i] = -1;
-          if (key < a.prefix_len) {
-            const int id = __ldg(a.prefix_pages + (key >> psh));
-            if ((unsigned)id < (unsigned)a.kv.num_pages)
-              off[i] = (int64_t)id * a.kv.page_stride + ((int64_t)sg.h * a.kv.page_size + (key & (a.kv.page_size - 1))) * D + ch * 16;
-            else if (a.err != nullptr)
-              atomicOr(a.err, kErrBadPage);
-          }
+      for (int i = 0; i < N; ++i) {
+        const int r = r0 + i * (128 / CH);
+        uint8_t* dst = smem + slot * C::kTileBytes + (ch / 4) * (kTcKeys * 128) + r * 128;
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[2 * k] = e4m3x2(w[k] & 0xffffu), f[2 * k + 1] = e4m3x2(w[k] >> 16);
+        // 8 threads hold a row of 128: the upper four write their halves the other way
+        // round, so that the two 64-value blocks meet on different banks
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int kk = k ^ (ch / 4 & 1);
+          *reinterpret_cast<uint4*>(dst + (((2 * (ch % 4) + kk) ^ (r & 7)) << 4)) =
+              kk ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
         }
-        for (int v = 0; v < 2; ++v, ++kv) {
-          const uint8_t* src = static_cast<const uint8_t*>(v ? a.kv.v : a.kv.k);
-          uint4 raw[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            raw[i] = off[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + off[i])) : make_uint4(0, 0, 0, 0);
-          const uint32_t slot = kv % kSlots;
-          if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int r = tid / CH + i * (128 / CH);
-            uint8_t* dst = smem + slot * C::kTileBytes + (ch / 4) * (kTcKeys * 128) + r * 128;
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            uint32_t f[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[2 * k] = e4m3x2(w[k] & 0xffffu), f[2 * k + 1] = e4m3x2(w[k] >> 16);
-            // 8 threads hold a row of 128: the upper four write their halves the other way
-            // round, so that the two 64-value blocks meet on different banks
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int kk = k ^ (ch / 4 & 1);
-              *reinterpret_cast<uint4*>(dst + (((2 * (ch % 4) + kk) ^ (r & 7)) << 4)) =
-                  kk ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
-            }
-          }
-          fence_async();
-          warp_arrive(&b.full[slot]);
+      }
+      fence_async();
+      warp_arrive(&b.full[slot]);
+      ++kv;
+    };
+    while (ok && segment(a, &u, end, &sg)) {
+      // while one tile is converted, the next one's values are in flight
+      int ids[N], next[N];
+      uint4 rk[N], rv[N];
+      fetch_ids(sg.t0, ids);
+      fetch(a.kv.k, sg.t0, sg.h, ids, rk);
+      fetch(a.kv.v, sg.t0, sg.h, ids, rv);
+      fetch_ids(min(sg.t0 + 1, sg.t1 - 1), next);
+      for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+        put(rk);
+        if (!ok) break;
+        if (t + 1 < sg.t1) fetch(a.kv.k, t + 1, sg.h, next, rk);
+        put(rv);
+        if (t + 1 < sg.t1) {
+          fetch(a.kv.v, t + 1, sg.h, next, rv);
+          fetch_ids(min(t + 2, sg.t1 - 1), next);
         }
       }
     }
