@@ -241,18 +241,17 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _scratch(nbytes, stream, like):
-    """(address, release) of nbytes of stream-ordered device memory from torch's caching
-    allocator. Releasing right after the launches is safe: whatever reuses the block on this
-    stream runs after them. (A tensor for it costs 8 us a call more, next to launches.)"""
+def _scratch(nbytes, stream):
+    """The address of nbytes of device memory from torch's caching allocator, for `stream` (a
+    raw handle). Given back with _release right after the launches: whatever reuses the block
+    on this stream runs after them. (A tensor for it costs 8 us a call more.)"""
     import torch
-    alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
-    if alloc is None:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream)):
-            held = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-        return held.data_ptr(), held.untyped_storage
-    p = alloc(nbytes, stream)
-    return p, lambda: torch._C._cuda_cudaCachingAllocator_raw_delete(p)
+    return torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+
+
+def _release(address):
+    import torch
+    torch._C._cuda_cudaCachingAllocator_raw_delete(address)
 
 
 def _kv_desc(k_cache, v_cache, k_scale, v_scale):
@@ -343,13 +342,13 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
     if out is None:
         out = _empty((T, q_heads, dim), torch.bfloat16, q, stream)
     raw = _raw_stream(stream, q)
-    release = None
+    own = None
     if scratch is not None:
         nbytes = scratch.numel()
         work = _opt(scratch, torch.uint8, nbytes)
     else:
         nbytes = lib.moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix)
-        work, release = _scratch(nbytes, raw, q) if nbytes else (None, None)
+        work = own = _scratch(nbytes, raw) if nbytes else None
     try:
         _check(lib.moe_prefix_attention(desc, *_heads(q, T, q_heads, dim), T, q_heads,
                                         dim ** -0.5 if scale is None else scale, pages, prefix_len, table, width, sequences,
@@ -357,8 +356,8 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
                                         _opt(lse_out, torch.float32, T * q_heads), work, nbytes, _opt(err_out, i32, 1), raw),
                "moe_prefix_attention")
     finally:
-        if release is not None:
-            release()
+        if own is not None:
+            _release(own)
     return out
 
 

@@ -58,7 +58,8 @@ __host__ __device__ inline int tc_parts(const Args& a, int r, int h) {
   return tc_cta_of(u + a.tc_tiles - 1, units, a.tc_ctas) - tc_cta_of(u, units, a.tc_ctas) + 1;
 }
 
-void plan_prefix_tc(Args* a, int sms);
+double prefix_tc_cost(const Args& a, int ctas, int* used);
+void plan_prefix_tc(Args* a, int ctas);
 int launch_prefix_tc(const Args& a, cudaStream_t s);
 
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;

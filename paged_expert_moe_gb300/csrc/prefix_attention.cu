@@ -627,7 +627,7 @@ int launch_all(const Args& a, int sms, cudaStream_t s) {
     const int blocks = a.max_suffix > 0 ? (a.T + kRowBlock - 1) / kRowBlock : 1;
     for (int b = 0; b < blocks; ++b) {
       // a later block's launch may not overtake the one before it: only the first is early
-      r = launch_after(stream_kernel<D, F8>, sms, kThreads, C::kSmem, s, early && b == 0, mk, mv, a, b);
+      r = launch_after(stream_kernel<D, F8>, a.warps / kWarps, kThreads, C::kSmem, s, early && b == 0, mk, mv, a, b);
       if (r != PMOE_OK) return r;
     }
     early = true;
@@ -649,6 +649,29 @@ Layout scratch_layout(const Args& a) {
   l.base = l.ml + n * 8;
   l.bytes = l.base + (size_t)((a.T + kRowBlock - 1) / kRowBlock) * (kRowBlock + 1) * 8;
   return l;
+}
+
+// Plans the tensor-core prefix and returns the CTAs of the stream kernel. The one is bound by
+// the tensor cores (or its own latency), the other by HBM, and a CTA of either fills an SM:
+// side by side on shares of the SMs they end sooner than one after the other. Measured, in us
+// (prefix kernel on 116 SMs and stream kernel on 36, against 152 and then 152): 256 rows on
+// 32,768 + 1..1,024 keys 143 and 161. The stream's cost: 6 us, 8 tiles of 16 keys a us on an
+// SM, 6.2 TB/s in all. The lengths are known on the device only, half of max_suffix is taken
+// for their mean; with a quarter of the SMs at most the prefix loses a third at worst.
+int split_sms(Args* a, int sms, int64_t key_bytes) {
+  a->row_tiles = (a->T * a->group + kTcRows - 1) / kTcRows;
+  a->tc_tiles = (a->prefix_len + kTcKeys - 1) / kTcKeys;
+  const double keys = 0.5 * a->T * (double)a->max_suffix;
+  auto stream = [&](int n) { return 6 + std::max(keys / kTile * a->head_items / (8.0 * n), keys * key_bytes / 6.2e6); };
+  int prefix = 0, ctas = sms;
+  double best = 0.92 * (prefix_tc_cost(*a, sms, &prefix) + stream(sms) - 3);
+  for (int n = sms - sms / 4; n < sms && a->max_suffix > 0; ++n) {
+    int used;
+    const double t = std::max(prefix_tc_cost(*a, n, &used), stream(sms - n));
+    if (t < best) best = t, prefix = used, ctas = sms - used;
+  }
+  plan_prefix_tc(a, prefix);
+  return ctas;
 }
 
 // Checks shared by the call and its scratch size; fills the part plan.
@@ -673,26 +696,25 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
 
   const int rows = T * a->group, rts = (a->group + 15) / 16;
   a->head_items = kv->kv_heads * rts;
-  a->warps = *sms * kWarps;
+  int stream_ctas = *sms;
+  a->prefix_parts = 0;
+  const int64_t pre_rts = (rows + 15) / 16;
+  const int64_t key_bytes = (int64_t)kv->kv_heads * kv->head_dim * (kv->dtype == PMOE_KV_E4M3 ? 2 : 4);  // a key's and value's
+  const bool tc = prefix_len > 0 && pre_rts > 1 && pre_rts * prefix_len * key_bytes > kStreamTraffic;
+  if (tc) stream_ctas = split_sms(a, *sms, key_bytes);
+  a->warps = stream_ctas * kWarps;
   const int64_t tiles = ((int64_t)max_suffix + kTile - 1) / kTile;
   // A warp's run: 64 keys at least, and long enough that an item has few parts
   const int64_t items = (int64_t)T * a->head_items;
   const int64_t most = std::min<int64_t>(512, std::max<int64_t>(4, 4ll * a->warps / items));
   a->min_share = (int)std::max<int64_t>(4, (tiles + most - 1) / most);
   a->suffix_parts = tiles > 0 ? (int)((tiles - 1) / a->min_share + 2) : 0;
-  a->prefix_parts = 0;
-  if (prefix_len > 0) {
-    const int64_t pre_rts = (rows + 15) / 16;
-    const int64_t traffic = pre_rts * kv->kv_heads * prefix_len * kv->head_dim * (kv->dtype == PMOE_KV_E4M3 ? 2 : 4);
-    if (pre_rts == 1 || traffic <= kStreamTraffic) {
-      a->pre_tiles = (prefix_len + kTile - 1) / kTile;
-      a->pre_items = (int)(pre_rts * kv->kv_heads);
-      const int64_t units = (int64_t)(a->pre_tiles + kHead) * a->pre_items;
-      const int64_t share = std::max<int64_t>(a->min_share, (units + a->warps - 1) / a->warps);
-      a->prefix_parts = (int)((a->pre_tiles - 1) / share + 2);
-    } else {
-      plan_prefix_tc(a, *sms);
-    }
+  if (prefix_len > 0 && !tc) {
+    a->pre_tiles = (prefix_len + kTile - 1) / kTile;
+    a->pre_items = (int)(pre_rts * kv->kv_heads);
+    const int64_t units = (int64_t)(a->pre_tiles + kHead) * a->pre_items;
+    const int64_t share = std::max<int64_t>(a->min_share, (units + a->warps - 1) / a->warps);
+    a->prefix_parts = (int)((a->pre_tiles - 1) / share + 2);
   }
   return PMOE_OK;
 }
