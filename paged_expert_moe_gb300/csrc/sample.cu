@@ -71,7 +71,13 @@ struct Threshold {        // kept: key > this key, and the first `ties` ids that
   u64 total;              // weight of the kept tokens
 };
 
-struct Shared {
+struct Pick {             // a bin found by a scan, weight and count above it (bin kBins: all)
+  u64 above;
+  uint32_t cnt;
+  int bin;
+};
+
+struct alignas(16) Shared {
   Histogram hist;
   union {
     Histogram level;      // step 3's passes over the key's bits
@@ -88,9 +94,7 @@ struct Shared {
   u64 sel, sel_upto;      // and what it found
   u64 scan[kWarps];
   uint32_t scan_cnt[kWarps];
-  u64 pick_above;         // the bin found by a scan: weight above it,
-  uint32_t pick_cnt;      // count above it,
-  int pick_bin;           // and the bin
+  Pick pick;
   u64 seg_sum[kWarps];    // step 4: per warp segment, weight above the threshold
   uint32_t seg_tie[kWarps];
   u64 all_sum[kMaxCluster * kWarps];
@@ -161,6 +165,10 @@ template <bool BF16>
 struct Vec {
   static constexpr int N = BF16 ? 8 : 4;  // logits in 16 bytes
   float f[N];
+  static __device__ __forceinline__ uint4 none() {  // -inf
+    const uint32_t w = BF16 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
+  }
   __device__ __forceinline__ explicit Vec(const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -223,52 +231,66 @@ __device__ void sort_up(u64* buf, u64 (&c)[kEach]) {
   __syncthreads();  // buf is free
 }
 
+// Appends id of x to this CTA's list where `in`; all lanes of a warp call it. One atomic a
+// warp: one a candidate, all on the same word, would be done one after the other.
+__device__ __forceinline__ void append(Shared& sh, bool in, float x, int id) {
+  const uint32_t mask = __ballot_sync(0xffffffffu, in);
+  if (mask == 0) return;
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+  if (lane == __ffs(mask) - 1) at = atomicAdd(&sh.listed, __popc(mask));
+  at = __shfl_sync(0xffffffffu, at, __ffs(mask) - 1) + __popc(mask & ((1u << lane) - 1));
+  if (in && at < kList) sh.list[at] = ((u64)~key_of(x) << 32) | (uint32_t)id;
+}
+
 __device__ __forceinline__ int pow2_above(int n) { return n <= 64 ? 64 : 1 << (32 - __clz(n - 1)); }
 
-// Adds up bin `threadIdx.x` of all CTAs' histograms (`h`: this CTA's); finds the first bin,
-// ascending, at which the running count (by_count) or weight reaches `target` (> 0). Every
-// CTA of the cluster calls it; the result is in sh.pick_* (bin kBins where it is not
-// reached). Returns the total weight.
-__device__ u64 find_bin(cg::cluster_group& cluster, Shared& sh, Histogram* h, bool by_count, u64 target) {
+// The first CTA adds up bin `threadIdx.x` of all CTAs' histograms (`h`: this CTA's) and finds
+// the first bin, ascending, at which the running count (by_count) or weight reaches `target`
+// (> 0). Every CTA of the cluster calls it, and has the result in sh.pick (bin kBins where it
+// is not reached). Had each CTA read all histograms for itself, it would take 5,500 cycles.
+__device__ void find_bin(cg::cluster_group& cluster, Shared& sh, Histogram* h, bool by_count, bool weights, u64 target) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = (int)cluster.num_blocks();
   cluster.sync();
-  uint32_t v[kMaxCluster][3];  // all remote loads in flight at once
+  if (cluster.block_rank() == 0) {
+    uint32_t v[kMaxCluster][3];  // all remote loads in flight at once
 #pragma unroll
-  for (int i = 0; i < kMaxCluster; ++i) {
-    const Histogram* o = cluster.map_shared_rank(h, i < nb ? i : 0);
-    v[i][0] = o->cnt[tid], v[i][1] = o->lo[tid], v[i][2] = o->hi[tid];
-  }
-  uint32_t c = 0;
-  u64 w = 0;
+    for (int i = 0; i < kMaxCluster; ++i) {
+      const Histogram* o = cluster.map_shared_rank(h, i < nb ? i : 0);
+      v[i][0] = by_count ? o->cnt[tid] : 0;
+      v[i][1] = weights ? o->lo[tid] : 0, v[i][2] = weights ? o->hi[tid] : 0;
+    }
+    uint32_t c = 0;
+    u64 w = 0;
 #pragma unroll
-  for (int i = 0; i < kMaxCluster; ++i)
-    if (i < nb) c += v[i][0], w += ((u64)v[i][2] << 16) + v[i][1];
-  u64 wi = w;
-  uint32_t ci = c;
+    for (int i = 0; i < kMaxCluster; ++i)
+      if (i < nb) c += v[i][0], w += ((u64)v[i][2] << 16) + v[i][1];
+    u64 wi = w;
+    uint32_t ci = c;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const u64 a = __shfl_up_sync(0xffffffffu, wi, o);
-    const uint32_t d = __shfl_up_sync(0xffffffffu, ci, o);
-    if (lane >= o) wi += a, ci += d;
-  }
-  if (lane == 31) sh.scan[warp] = wi, sh.scan_cnt[warp] = ci;
-  if (tid == 0) sh.pick_bin = kBins;
-  __syncthreads();
-  u64 wb = 0, total = 0;
-  uint32_t cb = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 a = __shfl_up_sync(0xffffffffu, wi, o);
+      const uint32_t d = __shfl_up_sync(0xffffffffu, ci, o);
+      if (lane >= o) wi += a, ci += d;
+    }
+    if (lane == 31) sh.scan[warp] = wi, sh.scan_cnt[warp] = ci;
+    __syncthreads();
+    u64 wb = 0, total = 0;
+    uint32_t cb = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) wb += sh.scan[i], cb += sh.scan_cnt[i];
-    total += sh.scan[i];
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) wb += sh.scan[i], cb += sh.scan_cnt[i];
+      total += sh.scan[i];
+    }
+    wi += wb, ci += cb;
+    if (tid == 0) sh.pick = Pick{total, 0, kBins};
+    __syncthreads();
+    if (by_count ? (ci >= target && ci - c < target) : (wi >= target && wi - w < target))
+      sh.pick = Pick{wi - w, ci - c, tid};
+    __syncthreads();
+    if (tid > 0 && tid < nb) cluster.map_shared_rank(&sh, tid)->pick = sh.pick;
   }
-  wi += wb, ci += cb;
-  if (by_count ? (ci >= target && ci - c < target) : (wi >= target && wi - w < target)) {
-    sh.pick_bin = tid;
-    sh.pick_cnt = ci - c;
-    sh.pick_above = wi - w;
-  }
-  __syncthreads();
-  return total;
+  cluster.sync();
 }
 
 // What each CTA listed, read by one lane per CTA: whether all of it fits, and the sums.
@@ -315,6 +337,34 @@ __device__ __forceinline__ u64 group_sum(u64 v, int G) {
   return v;
 }
 
+// How many of a[0, n) are below x, and (WEIGHTS) the sum of their weights; the G threads that
+// share x take every G-th pair of elements each.
+template <bool WEIGHTS>
+__device__ __forceinline__ void count_below(const u64* a, const uint32_t* weights, int n, u64 x, int part, int G, u64* place,
+                                            u64* before) {
+  uint32_t p = 0;
+  u64 b = 0;
+  const int pairs = n >> 1;
+#pragma unroll 4
+  for (int j = part; j < pairs; j += G) {
+    const ulonglong2 v = reinterpret_cast<const ulonglong2*>(a)[j];
+    const bool f = v.x < x, g = v.y < x;
+    p += f;
+    p += g;
+    if (WEIGHTS) {
+      const uint2 w = reinterpret_cast<const uint2*>(weights)[j];
+      b += f ? w.x : 0u;
+      b += g ? w.y : 0u;
+    }
+  }
+  if ((n & 1) && part == 0 && a[n - 1] < x) {
+    ++p;
+    if (WEIGHTS) b += weights[n - 1];
+  }
+  *place = group_sum(p, G);
+  if (WEIGHTS) *before = group_sum(b, G);
+}
+
 // Step 2's end for up to kPairs candidates: sh.merged holds n of them (padded with ~0 to a
 // power of two from 64). A candidate's place and the weight before it come from comparing it
 // with all others, twice: in the order of the logits for the cuts, in the order of the ids
@@ -324,37 +374,33 @@ __device__ void compare_and_draw(Shared& sh, const SampleArgs& a, const Row& rw,
   const int tid = threadIdx.x, n2 = pow2_above(n), G = kThreads / n2, i = tid / G, part = tid % G;
   uint32_t* weights = reinterpret_cast<uint32_t*>(sh.list);  // the list is in sh.merged by now
   const u64 c = sh.merged[i];
-  const uint32_t id = (uint32_t)c;
   const float wt = rw.weight(of_key(~(uint32_t)(c >> 32)));
   const uint32_t w = i < n ? Row::units(wt) : 0;
-  if (part == 0) weights[i] = w;
-  __syncthreads();
-  u64 place = 0, before = 0;
-#pragma unroll 4
-  for (int j = part; j < n; j += G) {
-    const bool ahead = sh.merged[j] < c;
-    place += ahead;
-    before += ahead ? weights[j] : 0;
+  u64 place, before = 0, total = all_weights;
+  if (use_p) {
+    if (part == 0) weights[i] = w;
+    __syncthreads();
+    count_below<true>(sh.merged, weights, n, c, part, G, &place, &before);
+  } else {
+    count_below<false>(sh.merged, weights, n, c, part, G, &place, &before);
   }
-  place = group_sum(place, G);
-  before = group_sum(before, G);
   const bool in_k = i < n && (!use_k || place < (u64)top_k);
-  u64 total = all_weights;
-  if (use_k) block_scan(sh, in_k && part == 0 ? w : 0, &total);
+  if (use_k && use_p) block_scan(sh, in_k && part == 0 ? w : 0, &total);
   const u64 least = use_p ? least_weight(total, top_p) : ~0ull;
   const uint32_t kept = in_k && before < least && !(wt < min_p) ? w : 0;
   u64 S;
   block_scan(sh, part == 0 ? kept : 0, &S);
-  if (part == 0) weights[i] = kept;
+  // by id: what was cut goes behind every id, with no weight
+  const u64 by_id = kept > 0 ? c << 32 : ~0ull;
+  u64* ids = sh.merged + kPairs;
+  if (part == 0) ids[i] = by_id, weights[i] = kept;
   __syncthreads();
-  u64 run = 0;
-#pragma unroll 4
-  for (int j = part; j < n; j += G) run += (uint32_t)sh.merged[j] < id ? weights[j] : 0;
-  run = group_sum(run, G);
+  u64 run;
+  count_below<true>(ids, weights, n, by_id, part, G, &place, &run);
   const float uu = a.u[row];
   const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
-  if (part == 0 && run <= target && target < run + kept) {
-    a.ids[row] = (int32_t)id;
+  if (part == 0 && kept > 0 && run <= target && target < run + kept) {
+    a.ids[row] = (int32_t)(uint32_t)c;
     if (a.logprob != nullptr) a.logprob[row] = logf((float)kept / (float)S);
   }
 }
@@ -396,12 +442,10 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
   for (int i = 0; i < kWarps; ++i)
     if (i < warp) ci += sh.scan_cnt[i];
   if (by_count ? (ci >= target && ci - own_c < target) : (wi >= target && wi - own_w < target)) {
-    sh.pick_bin = tid;
-    sh.pick_cnt = ci - own_c;
-    sh.pick_above = wi - own_w;
+    sh.pick = Pick{wi - own_w, ci - own_c, tid};
   }
   __syncthreads();
-  const int pick = sh.pick_bin;
+  const int pick = sh.pick.bin;
 #pragma unroll
   for (int e = 0; e < kEach; ++e)
     if (c[e] != ~0ull && bin(c[e]) == pick) {
@@ -413,15 +457,10 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
   if (m <= kPairs) {
     const int n2 = pow2_above(m), G = kThreads / n2, i = tid / G, part = tid % G;
     const u64 x = i < m ? sh.merged[i] : ~0ull;
-    u64 place = 0, before = 0;
-#pragma unroll 4
-    for (int j = part; j < m; j += G) {
-      const bool ahead = sh.merged[j] < x;
-      place += ahead;
-      before += ahead ? weights[j] : 0;
-    }
-    place = group_sum(place, G) + sh.pick_cnt;
-    before = group_sum(before, G) + sh.pick_above;
+    u64 place, before;
+    count_below<true>(sh.merged, weights, m, x, part, G, &place, &before);
+    place += sh.pick.cnt;
+    before += sh.pick.above;
     const uint32_t w = i < m ? weights[i] : 0;
     if (part == 0 && i < m && (by_count ? place + 1 == target : before < target && target <= before + w)) {
       sh.sel = x;
@@ -606,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const uint32_t want = ((use_k ? top_k : kCutP) + nb - 1) / nb;
     const int mybin = Row{best, 1.f}.bin(mine);
     if (mine > -INFINITY) atomicAdd(&sh.hist.cnt[mybin], 1u);
-    if (tid == 0) sh.pick_bin = kBins, sh.bound_key = 0xffffffffu;
+    if (tid == 0) sh.pick.bin = kBins, sh.bound_key = 0xffffffffu;
     __syncthreads();
     uint32_t upto = sh.hist.cnt[tid];
     const uint32_t own = upto;
@@ -620,12 +659,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
     for (int i = 0; i < kWarps; ++i)
       if (i < warp) upto += sh.scan_cnt[i];
-    if (upto >= want && upto - own < want) sh.pick_bin = tid;
+    if (upto >= want && upto - own < want) sh.pick.bin = tid;
     __syncthreads();
-    if (mine > -INFINITY && mybin <= sh.pick_bin) atomicMin(&sh.bound_key, key_of(mine));
+    if (mine > -INFINITY && mybin <= sh.pick.bin) atomicMin(&sh.bound_key, key_of(mine));
     __syncthreads();
     // fewer threads with a logit than that: every logit is a candidate
-    if (tid == 0) sh.bound = sh.pick_bin == kBins ? -FLT_MAX : of_key(sh.bound_key);
+    if (tid == 0) sh.bound = sh.pick.bin == kBins ? -FLT_MAX : of_key(sh.bound_key);
   }
   cluster.sync();
   best = cluster.map_shared_rank(&sh, lane < nb ? lane : 0)->best;
@@ -660,11 +699,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
 
   // ---- 2. candidates
+  u64 total = 0;  // of all weights where only top-p cuts, then of what is kept
   if (listing) {
     u64 sum = 0, list_sum = 0;
     const bool totals = !use_k;
-    for (int i = tid; i < nv; i += kThreads) {
-      const V x(xs[i]);
+    for (int i0 = warp * 32; i0 < nv; i0 += kThreads) {
+      const int i = i0 + lane;
+      const V x(i < nv ? xs[i] : V::none());
       uint32_t w[N];
       if (totals) {
 #pragma unroll
@@ -672,17 +713,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
         for (int q = 0; q < N; ++q) sum += w[q];
       }
-      bool in[N], any = false;
+      bool any = false;
 #pragma unroll
-      for (int q = 0; q < N; ++q) any |= in[q] = x.f[q] >= bound;
-      if (any) {
+      for (int q = 0; q < N; ++q) any |= x.f[q] >= bound;
+      if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
-        for (int q = 0; q < N; ++q)
-          if (in[q]) {
-            if (totals) list_sum += w[q];
-            const int at = atomicAdd(&sh.listed, 1);
-            if (at < kList) sh.list[at] = ((u64)~key_of(x.f[q]) << 32) | (uint32_t)(first + i * N + q);
-          }
+        for (int q = 0; q < N; ++q) {
+          const bool in = x.f[q] >= bound;
+          if (totals && in) list_sum += w[q];
+          append(sh, in, x.f[q], first + i * N + q);
+        }
       }
     }
     if (totals) {
@@ -703,6 +743,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       return;
     }
+    total = l.sum;
     cluster.sync();  // every CTA has read the lists' sizes
   }
 
@@ -717,8 +758,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (x.f[q] > -INFINITY) f(x.f[q]);
     }
   };
-  auto add = [&](Histogram& h, int bin, float x, bool weigh) {
-    atomicAdd(&h.cnt[bin], 1u);
+  auto add = [&](Histogram& h, int bin, float x, bool count, bool weigh) {
+    if (count) atomicAdd(&h.cnt[bin], 1u);
     const uint32_t w = weigh ? rw.units_of(x) : 0;
     if (w) {
       atomicAdd(&h.lo[bin], w & 0xffffu);
@@ -728,38 +769,38 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (use_k || use_p) {
     sh.hist.cnt[tid] = sh.hist.lo[tid] = sh.hist.hi[tid] = 0;
     __syncthreads();
-    elements([&](float x) { add(sh.hist, rw.bin(x), x, use_p); });
-    u64 total = 0;
+    elements([&](float x) { add(sh.hist, rw.bin(x), x, use_k, use_p); });
     for (int mode = use_k ? 0 : 1; mode <= (use_p ? 1 : 0); ++mode) {
-      // mode 0: the top_k-th token; mode 1: the token at which the weight reaches top_p
-      if (mode == 1 && !use_k) total = find_bin(cluster, sh, &sh.hist, false, 1);
+      // mode 0: the top_k-th token; mode 1: the token at which the weight reaches top_p (the
+      // total is step 2's, or mode 0's)
       const u64 target = mode == 0 ? (u64)top_k : least_weight(total, top_p);
-      const u64 all = find_bin(cluster, sh, &sh.hist, mode == 0, target);
-      if (sh.pick_bin == kBins) {  // top_k exceeds the logits above -inf: none is cut
-        total = all;
+      find_bin(cluster, sh, &sh.hist, mode == 0, use_p, target);
+      const Pick pick = sh.pick;
+      if (pick.bin == kBins) {  // top_k exceeds the logits above -inf: none is cut
+        total = pick.above;
         continue;
       }
-      const int bin = sh.pick_bin;
-      const u64 above = sh.pick_above;
-      const uint32_t above_cnt = sh.pick_cnt;
-      const u64 inside = target - (mode == 0 ? above_cnt : above);
+      const int bin = pick.bin;
+      const u64 inside = target - (mode == 0 ? pick.cnt : pick.above);
       if (tid == 0) sh.listed = 0;
       __syncthreads();
-      for (int i = tid; i < nv; i += kThreads) {
-        const V x(xs[i]);
+      for (int i0 = warp * 32; i0 < nv; i0 += kThreads) {
+        const int i = i0 + lane;
+        const V x(i < nv ? xs[i] : V::none());
+        bool in[N], any = false;
 #pragma unroll
-        for (int q = 0; q < N; ++q)
-          if (x.f[q] > -INFINITY && rw.bin(x.f[q]) == bin) {
-            const int at = atomicAdd(&sh.listed, 1);
-            if (at < kList) sh.list[at] = ((u64)~key_of(x.f[q]) << 32) | (uint32_t)(first + i * N + q);
-          }
+        for (int q = 0; q < N; ++q) any |= in[q] = x.f[q] > -INFINITY && rw.bin(x.f[q]) == bin;
+        if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+          for (int q = 0; q < N; ++q) append(sh, in[q], x.f[q], first + i * N + q);
+        }
       }
       cluster.sync();
       const Listed l = read_listed(cluster, sh);
       if (l.fits) {
         if (rank == 0) {
           merge_lists(cluster, sh, l);
-          find_in_bin(sh, rw, l.total, bin, mode == 0, inside, above);
+          find_in_bin(sh, rw, l.total, bin, mode == 0, inside, pick.above);
           if (tid > 0 && tid < nb) cluster.map_shared_rank(&sh, tid)->thr = sh.thr;
         }
         cluster.sync();
@@ -769,8 +810,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       // inside the bin, 8 bits of the key at a time
       uint32_t prefix = 0;
-      u64 over = above;
-      uint32_t over_cnt = above_cnt;
+      u64 over = pick.above;
+      uint32_t over_cnt = pick.cnt;
       for (int level = 0; level < 4; ++level) {
         const int sft = 24 - 8 * level;
         cluster.sync();  // every CTA has read the list, or the level before
@@ -779,12 +820,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         elements([&](float x) {
           if (rw.bin(x) != bin) return;
           const uint32_t k = key_of(x);
-          if (level == 0 || (k >> (sft + 8)) == prefix) add(sh.level, 255 - ((k >> sft) & 255), x, use_p);  // descending
+          if (level == 0 || (k >> (sft + 8)) == prefix) add(sh.level, 255 - ((k >> sft) & 255), x, true, use_p);  // descending
         });
-        find_bin(cluster, sh, &sh.level, mode == 0, target - (mode == 0 ? over_cnt : over));
-        over += sh.pick_above;
-        over_cnt += sh.pick_cnt;
-        prefix = (prefix << 8) | (255 - sh.pick_bin);
+        find_bin(cluster, sh, &sh.level, mode == 0, use_p, target - (mode == 0 ? over_cnt : over));
+        over += sh.pick.above;
+        over_cnt += sh.pick.cnt;
+        prefix = (prefix << 8) | (255 - sh.pick.bin);
       }
       key_t = prefix;
       const u64 each = rw.units_of(of_key(key_t));
@@ -884,8 +925,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       u64 w[N], v = 0;
       uint32_t t = 0;
       const int i = i0 + lane;
-      const V x(i < s1 ? xs[i] : BF16 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
-                                      : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u));
+      const V x(i < s1 ? xs[i] : V::none());
 #pragma unroll
       for (int q = 0; q < N; ++q) t += x.f[q] == x_t;
       uint32_t ti = t;
