@@ -216,20 +216,27 @@ def moe_decode_forward_noalloc(experts, stride, E, top_k, H, I, fmt, x, ids, w, 
     return y
 
 
-# The calls of a decode step take a few microseconds on the GPU, so their binding is kept
-# lean: pointers go to ctypes as plain integers and the stream as its raw handle.
+# The calls of a decode step (below) go through _binding, which checks their tensors and calls
+# the library in C: their kernels take a few microseconds, less than the checks in Python.
 
-def _raw_stream(stream, like):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
+_BINDING = None
 
 
-def _opt(x, dtype, n):
-    """The address of a contiguous CUDA tensor of n elements, None for None."""
-    if x is None:
-        return None
-    assert x.dtype is dtype and x.is_cuda and x.numel() == n and x.is_contiguous(), (x.dtype, x.shape, dtype, n)
-    return x.data_ptr()
+def _binding():
+    global _BINDING
+    if _BINDING is None:
+        import torch
+        lib = load()
+        from . import _binding as b
+        fns = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "moe_kv_append", "moe_prefix_attention", "moe_prefix_attention_scratch_bytes", "moe_sample_tokens")]
+        # scratch comes from torch's caching allocator, by its raw calls (a tensor costs 8 us more)
+        c = torch._C
+        b.setup(tuple(fns), (torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32, torch.uint8),
+                c._cuda_getCurrentRawStream, c._cuda_cudaCachingAllocator_raw_alloc,
+                c._cuda_cudaCachingAllocator_raw_delete)
+        _BINDING = b
+    return _BINDING
 
 
 def _empty(shape, dtype, like, stream):
@@ -241,77 +248,33 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _scratch(nbytes, stream):
-    """The address of nbytes of device memory from torch's caching allocator, for `stream` (a
-    raw handle). Given back with _release right after the launches: whatever reuses the block
-    on this stream runs after them. (A tensor for it costs 8 us a call more.)"""
-    import torch
-    return torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
-
-
-def _release(address):
-    import torch
-    torch._C._cuda_cudaCachingAllocator_raw_delete(address)
-
-
-def _kv_desc(k_cache, v_cache, k_scale, v_scale):
-    """pmoe_kv_desc of a paged cache: CUDA bf16 or float8_e4m3fn [num_pages, kv_heads,
-    page_size, head_dim] tensors of the same strides, contiguous but for the page stride."""
-    import torch
-    pages, heads, page, dim = shape = k_cache.shape
-    stride = k_cache.stride()
-    dt = k_cache.dtype
-    assert k_cache.is_cuda and v_cache.is_cuda and v_cache.dtype is dt and v_cache.shape == shape
-    assert v_cache.stride() == stride and stride[1:] == (page * dim, dim, 1)
-    if dt is torch.bfloat16:
-        return pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride[0], None, None, pages, page, heads, dim,
-                            PMOE_KV_BF16)
-    assert dt is torch.float8_e4m3fn
-    return pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride[0], _opt(k_scale, torch.float32, heads),
-                        _opt(v_scale, torch.float32, heads), pages, page, heads, dim, PMOE_KV_E4M3)
-
-
-def _heads(x, T, heads, dim):
-    """(address, elements from token to token) of bf16 x [T, heads, dim] whose heads are
-    contiguous; one token or head has no stride of its own."""
-    import torch
-    st, sh, sd = x.stride()
-    assert x.dtype is torch.bfloat16 and x.is_cuda and x.shape == (T, heads, dim)
-    assert sd == 1 and (sh == dim or heads == 1)
-    return x.data_ptr(), st if T > 1 else heads * dim
-
-
 def moe_kv_append(k_cache, v_cache, q, k, v, positions, slots, inv_freq, pair_axis=None, interleaved=False, q_norm=None,
                   k_norm=None, eps=1e-6, k_scale=None, v_scale=None, q_out=None, err_out=None, stream=None):
     """Head norm, rotation and append of T tokens' keys and values to a paged cache.
-    k_cache, v_cache: bf16 or float8_e4m3fn [num_pages, kv_heads, page_size, head_dim];
-    q: bf16 [T, q_heads, head_dim], k, v: bf16 [T, kv_heads, head_dim] (views of one
-    projection will do); positions: int32 [axes, T] or [T]; slots: int32 [T], page *
+    k_cache, v_cache: bf16 or float8_e4m3fn [num_pages, kv_heads, page_size, head_dim], of one
+    page stride; q: bf16 [T, q_heads, head_dim], k, v: bf16 [T, kv_heads, head_dim] (views of
+    one projection will do); positions: int32 [axes, T] or [T]; slots: int32 [T], page *
     page_size + row, -1 = not stored; inv_freq: fp32 [rotary_dim / 2] or None; pair_axis:
     int32 [rotary_dim / 2]; q_norm, k_norm: bf16 [head_dim]. Returns the rotated q (q_out)."""
-    import torch
-    T, q_heads, dim = q.shape
-    desc = _kv_desc(k_cache, v_cache, k_scale, v_scale)
-    hk = desc.kv_heads
-    assert dim == desc.head_dim
-    i32, bf16 = torch.int32, torch.bfloat16
-    axes = positions.shape[0] if positions is not None and positions.dim() == 2 else 1
-    pairs = 0 if inv_freq is None else inv_freq.numel()
     if q_out is None:
-        q_out = _empty((T, q_heads, dim), bf16, q, stream)
-    _check(load().moe_kv_append(desc, *_heads(q, T, q_heads, dim), *_heads(k, T, hk, dim), *_heads(v, T, hk, dim), T,
-                                q_heads, _opt(positions, i32, axes * T), axes, _opt(pair_axis, i32, pairs),
-                                _opt(inv_freq, torch.float32, pairs), 2 * pairs, 1 if interleaved else 0,
-                                _opt(q_norm, bf16, dim), _opt(k_norm, bf16, dim), eps, _opt(slots, i32, T),
-                                _opt(q_out, bf16, T * q_heads * dim), _opt(err_out, i32, 1), _raw_stream(stream, q)),
-           "moe_kv_append")
+        q_out = _empty(q.shape, q.dtype, q, stream)
+    status = (_BINDING or _binding()).kv_append(
+        k_cache, v_cache, q, k, v, positions, slots, inv_freq, pair_axis, interleaved, q_norm, k_norm, eps, k_scale,
+        v_scale, q_out, err_out, stream)
+    if status:
+        raise PmoeError(status, "moe_kv_append")
     return q_out
 
 
-def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len, max_suffix, k_scale=None, v_scale=None):
+def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len, max_suffix):
     """Bytes of scratch a moe_prefix_attention call of these sizes needs."""
-    return int(load().moe_prefix_attention_scratch_bytes(_kv_desc(k_cache, v_cache, k_scale, v_scale), T, q_heads,
-                                                         prefix_len, max_suffix))
+    import torch
+    pages, heads, page, dim = k_cache.shape
+    kind = PMOE_KV_E4M3 if k_cache.dtype == torch.float8_e4m3fn else PMOE_KV_BF16
+    # the scales' values do not matter for the size, but that there are some does
+    desc = pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0), k_cache.data_ptr(), k_cache.data_ptr(),
+                        pages, page, heads, dim, kind)
+    return int(load().moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix))
 
 
 def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_table, suffix_len, max_suffix, scale=None,
@@ -321,43 +284,16 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
     Row t sees the first prefix_len keys of prefix_pages (int32), which all rows share, then
     the first suffix_len[t] (int32 [T], at most max_suffix) of page_table[row_seq[t]] (int32
     [sequences, pages]; row_seq int32 [T], default t). scale defaults to head_dim ** -0.5.
-    lse_out: fp32 [T, q_heads] or None; scratch: uint8, allocated here when not given.
-    Returns out (bf16 [T, q_heads, head_dim])."""
-    import torch
-    T, q_heads, dim = q.shape
-    desc = _kv_desc(k_cache, v_cache, k_scale, v_scale)
-    i32 = torch.int32
-    assert dim == desc.head_dim
-    pages = None
-    if prefix_len > 0:
-        n = prefix_pages.numel()
-        assert n * desc.page_size >= prefix_len
-        pages = _opt(prefix_pages, i32, n)
-    table = lens = None
-    sequences = width = 0
-    if max_suffix > 0:
-        sequences, width = page_table.shape
-        table, lens = _opt(page_table, i32, sequences * width), _opt(suffix_len, i32, T)
-    lib = load()
+    lse_out: fp32 [T, q_heads] or None; scratch: uint8, taken from torch's allocator for the
+    call when not given. Returns out (bf16 [T, q_heads, head_dim])."""
     if out is None:
-        out = _empty((T, q_heads, dim), torch.bfloat16, q, stream)
-    raw = _raw_stream(stream, q)
-    own = None
-    if scratch is not None:
-        nbytes = scratch.numel()
-        work = _opt(scratch, torch.uint8, nbytes)
-    else:
-        nbytes = lib.moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix)
-        work = own = _scratch(nbytes, raw) if nbytes else None
-    try:
-        _check(lib.moe_prefix_attention(desc, *_heads(q, T, q_heads, dim), T, q_heads,
-                                        dim ** -0.5 if scale is None else scale, pages, prefix_len, table, width, sequences,
-                                        _opt(row_seq, i32, T), lens, max_suffix, _opt(out, torch.bfloat16, T * q_heads * dim),
-                                        _opt(lse_out, torch.float32, T * q_heads), work, nbytes, _opt(err_out, i32, 1), raw),
-               "moe_prefix_attention")
-    finally:
-        if own is not None:
-            _release(own)
+        out = _empty(q.shape, q.dtype, q, stream)
+    status = (_BINDING or _binding()).prefix_attention(
+        k_cache, v_cache, q, prefix_pages, prefix_len, page_table, suffix_len, max_suffix,
+        k_cache.shape[3] ** -0.5 if scale is None else scale, row_seq, k_scale, v_scale, out, lse_out, scratch, err_out,
+        stream)
+    if status:
+        raise PmoeError(status, "moe_prefix_attention")
     return out
 
 
@@ -367,17 +303,12 @@ def moe_sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p
     u (fp32 [T], in [0, 1)). temperature, top_p, min_p: fp32 [T], top_k: int32 [T], or None
     (1, 1, 0 and 0: no cut); temperature 0 takes the largest logit. logprob_out: fp32 [T],
     the drawn token's log probability among the kept ones. Returns ids (int32 [T])."""
-    import torch
-    T, V = logits.shape
-    dt, f32 = logits.dtype, torch.float32
-    st, sv = logits.stride()
-    assert logits.is_cuda and (dt is f32 or dt is torch.bfloat16) and (V == 1 or sv == 1)
     if ids_out is None:
-        ids_out = _empty(T, torch.int32, logits, stream)
-    _check(load().moe_sample_tokens(logits.data_ptr(), 0 if dt is f32 else 1, T, V, st if T > 1 else V,
-                                    _opt(temperature, f32, T), _opt(top_k, torch.int32, T), _opt(top_p, f32, T),
-                                    _opt(min_p, f32, T), _opt(u, f32, T), _opt(ids_out, torch.int32, T),
-                                    _opt(logprob_out, f32, T), _raw_stream(stream, logits)), "moe_sample_tokens")
+        import torch
+        ids_out = _empty(logits.shape[0], torch.int32, logits, stream)
+    status = (_BINDING or _binding()).sample_tokens(logits, u, temperature, top_k, top_p, min_p, ids_out, logprob_out, stream)
+    if status:
+        raise PmoeError(status, "moe_sample_tokens")
     return ids_out
 
 

@@ -1,8 +1,8 @@
 """Builds libpagedmoe.so in-tree from the CUDA sources with nvcc (sm_103a only).
 
 Each translation unit is compiled in parallel, then linked into one shared library
-with a plain C ABI (include/pagedmoe.h). Rebuilds only when a source is newer than
-the library.
+with a plain C ABI (include/pagedmoe.h); gcc compiles the Python binding of the decode-step
+calls (csrc/binding.c) beside it. Rebuilds only when a source is newer than the libraries.
 """
 
 import concurrent.futures
@@ -10,11 +10,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedmoe.so")
+BINDING_SRC = os.path.join(CSRC, "binding.c")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -26,13 +29,13 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(HERE, "..", "include", "*.h"))
+    return [BINDING_SRC] + _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(HERE, "..", "include", "*.h"))
 
 
 def needs_build():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -47,13 +50,25 @@ def _compile(src, verbose_ptxas=False):
     return obj, r.stderr
 
 
+def _compile_binding():
+    tmp = BINDING + ".tmp"
+    cmd = ["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
+           BINDING_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for {BINDING_SRC}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force=False, verbose_ptxas=False, quiet=True):
     if not force and not needs_build():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)
