@@ -293,6 +293,10 @@ int cuda_status(cudaError_t e, const char* what) {
   return PMOE_ECUDA;
 }
 int launch_status(const char* what) { return cuda_status(cudaGetLastError(), what); }
+bool pdl_enabled() {
+  static const bool on = !env_flag("PMOE_NO_PDL");
+  return on;
+}
 int SmemLimit::set(const void* kernel, int bytes, const char* what) {
   int dev = 0;
   int r = cuda_status(cudaGetDevice(&dev), what);

@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a,
   constexpr int LPH = D / 16;              // threads of a head
   constexpr int UNITS = kThreads / LPH;    // heads at once
   __shared__ __align__(16) float cs[kMaxTok][2][kMaxPairs];
+  pdl_wait();  // the caches and inputs may come from the kernel ahead
+  pdl_trigger();
   const int t0 = blockIdx.x * tok;
   const int nt = min(tok, a.T - t0);
   const int hk = a.kv.kv_heads, heads = a.q_heads + 2 * hk;
@@ -278,9 +280,6 @@ extern "C" int moe_kv_append(const pmoe_kv_desc* kv, const void* q, int64_t q_st
   const int tok = std::min(kMaxTok, (T + 607) / 608);
   const int blocks = (T + tok - 1) / tok;
   cudaStream_t s = (cudaStream_t)stream;
-  if (D == 128)
-    kv_append_kernel<128><<<blocks, kThreads, 0, s>>>(a, tok);
-  else
-    kv_append_kernel<64><<<blocks, kThreads, 0, s>>>(a, tok);
-  return launch_status("moe_kv_append");
+  return launch("moe_kv_append", D == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, blocks, kThreads, 0, s, true, 1, a,
+                tok);
 }

@@ -7,6 +7,7 @@
 #include <stddef.h>
 
 #include <atomic>
+#include <utility>
 
 #include "../../include/pagedmoe.h"
 
@@ -159,6 +160,34 @@ ExpertLayout expert_layout(int fmt, int H, int I);
 // PMOE_OK, or PMOE_ECUDA with the launch's error text kept for pmoe_last_error.
 int launch_status(const char* what);
 int cuda_status(cudaError_t e, const char* what);
+// Whether kernels are launched with programmatic serialization (PMOE_NO_PDL=1: they are not).
+bool pdl_enabled();
+// Launches a kernel, with a cluster of `cluster` CTAs where that is above 1. pdl: it may be
+// scheduled before the kernel ahead of it has ended, and calls pdl_wait() itself.
+template <class... P, class... A>
+int launch(const char* what, void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s, bool pdl,
+           unsigned cluster, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (pdl && pdl_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...), what);
+}
 // A kernel's dynamic shared memory limit, raised once per device (the call costs more than
 // some launches).
 struct SmemLimit {

@@ -114,6 +114,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int t0 = block * kRowBlock, nrows = a.max_suffix > 0 ? min(kRowBlock, a.T - t0) : 0;
   const int64_t pre = block == 0 && a.pre_tiles > 0 ? (int64_t)a.pre_items * (a.pre_tiles + kHead) : 0;
+  // Behind the prefix kernel, which began after all that came before the call, this one starts
+  // at once and waits at its end; else it is the call's first and waits here.
+  if (a.tc_ctas == 0) pdl_wait();
   pdl_trigger();
 
   // ---- the first unit of every row: thread i sums 8 rows
@@ -470,6 +473,7 @@ __global__ void __launch_bounds__(W * 32 < 128 ? 128 : W * 32) combine_kernel(co
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % W;
   const int64_t i = (int64_t)blockIdx.x * kRowHeads + (threadIdx.x >> 5) / W;
   pdl_wait();
+  pdl_trigger();
   if (W == 1 && i >= rh) return;
   const int t = (int)(i / a.q_heads), hq = (int)(i % a.q_heads), h = hq / a.group, r = hq - h * a.group;
   // the row's parts of the prefix, then those of its own keys
@@ -596,47 +600,32 @@ int make_map(const Args& a, void* base, CUtensorMap* m) {
                        !f8 ? kTcMapBf16Sw128 : a.kv.head_dim == 128 ? kTcMapBytesSw128 : kTcMapBytesSw64);
 }
 
-template <class... P, class... A>
-int launch_after(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s, bool early, A&&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = early ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...), "moe_prefix_attention");
-}
-
 template <int D, bool F8>
 int launch_all(const Args& a, int sms, cudaStream_t s) {
   using C = StreamCfg<D, F8>;
   int r = a.tc_ctas > 0 ? launch_prefix_tc(a, s) : PMOE_OK;
   if (r != PMOE_OK) return r;
-  bool early = a.tc_ctas > 0;  // may start while the kernel before it, one of this call, still runs
+  const char* what = "moe_prefix_attention";
   if (a.pre_tiles > 0 || a.max_suffix > 0) {
     static SmemLimit limit;
     CUtensorMap mk, mv;
-    r = limit.set(reinterpret_cast<const void*>(stream_kernel<D, F8>), C::kSmem, "moe_prefix_attention");
+    r = limit.set(reinterpret_cast<const void*>(stream_kernel<D, F8>), C::kSmem, what);
     if (r == PMOE_OK) r = make_map(a, a.kv.k, &mk);
     if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
     if (r != PMOE_OK) return r;
     const int blocks = a.max_suffix > 0 ? (a.T + kRowBlock - 1) / kRowBlock : 1;
     for (int b = 0; b < blocks; ++b) {
-      // a later block's launch may not overtake the one before it: only the first is early
-      r = launch_after(stream_kernel<D, F8>, a.warps / kWarps, kThreads, C::kSmem, s, early && b == 0, mk, mv, a, b);
+      // a later block's launch does not overtake the one before it, which the combine kernel
+      // would not wait for
+      r = launch(what, stream_kernel<D, F8>, a.warps / kWarps, kThreads, C::kSmem, s, b == 0, 1, mk, mv, a, b);
       if (r != PMOE_OK) return r;
     }
-    early = true;
   }
   const int64_t rh = (int64_t)a.T * a.q_heads;
   const int parts = a.prefix_parts + a.suffix_parts;
-  if (parts <= 12 && rh >= 4096) return launch_after(combine_kernel<D, 1>, (unsigned)((rh + 3) / 4), 128, 0, s, early, a);
-  if (parts <= 64) return launch_after(combine_kernel<D, 4>, (unsigned)rh, 128, 0, s, early, a);
-  return launch_after(combine_kernel<D, 16>, (unsigned)rh, 512, 0, s, early, a);
+  if (parts <= 12 && rh >= 4096) return launch(what, combine_kernel<D, 1>, (unsigned)((rh + 3) / 4), 128, 0, s, true, 1, a);
+  if (parts <= 64) return launch(what, combine_kernel<D, 4>, (unsigned)rh, 128, 0, s, true, 1, a);
+  return launch(what, combine_kernel<D, 16>, (unsigned)rh, 512, 0, s, true, 1, a);
 }
 
 struct Layout {

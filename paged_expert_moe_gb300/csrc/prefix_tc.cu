@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       prefetch_map(&map_v);
     }
   }
+  pdl_wait();     // the cache and q may come from the kernel ahead
   pdl_trigger();  // the stream kernel may take the SMs that this one is done with
   __syncthreads();
   // The issuing warp allocates all 512 columns: the base is column 0, lane 0. The other roles
@@ -549,8 +550,7 @@ int launch(const Args& a, cudaStream_t s) {
   static SmemLimit limit;
   const int r = limit.set(reinterpret_cast<const void*>(prefix_tc_kernel<D, F8>), C::kSmem, "moe_prefix_attention");
   if (r != PMOE_OK) return r;
-  prefix_tc_kernel<D, F8><<<a.tc_ctas, C::kThreads, C::kSmem, s>>>(mk, mv, a);
-  return launch_status("moe_prefix_attention");
+  return pmoe::launch("moe_prefix_attention", prefix_tc_kernel<D, F8>, a.tc_ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, a);
 }
 
 }  // namespace

@@ -578,6 +578,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   extern __shared__ __align__(16) uint4 xs[];
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
+  pdl_wait();  // the logits may come from the kernel ahead
+  pdl_trigger();
   const int nb = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / nb;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1000,16 +1002,5 @@ extern "C" int moe_sample_tokens(const void* logits, int is_bf16, int T, int V, 
   static SmemLimit limit[2];
   const int r = limit[is_bf16 ? 1 : 0].set(reinterpret_cast<const void*>(kernel), kMaxSmem, "moe_sample_tokens");
   if (r != PMOE_OK) return r;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(T * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a), "moe_sample_tokens");
+  return launch("moe_sample_tokens", kernel, (unsigned)(T * cluster), kThreads, smem, (cudaStream_t)stream, true, cluster, a);
 }
