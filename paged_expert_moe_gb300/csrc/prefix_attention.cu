@@ -28,7 +28,6 @@ constexpr int kTile = 16;       // keys of a unit
 constexpr int kHead = 2;        // empty units at the start of an item
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int64_t kStreamTraffic = 24 << 20;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -689,7 +688,12 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   a->prefix_parts = 0;
   const int64_t pre_rts = (rows + 15) / 16;
   const int64_t key_bytes = (int64_t)kv->kv_heads * kv->head_dim * (kv->dtype == PMOE_KV_E4M3 ? 2 : 4);  // a key's and value's
-  const bool tc = prefix_len > 0 && pre_rts > 1 && pre_rts * prefix_len * key_bytes > kStreamTraffic;
+  // With few rows or keys the stream kernel takes the prefix along, 16 rows at a time, in one
+  // launch less; from 340 keys x heads x row tiles an SM on the tensor cores are faster. In us,
+  // prefix kernel / stream kernel, on 4 kv heads of 128 with 64 own keys a row: 64 rows of 32
+  // heads 18.0 / 16.6 on 400 keys, 18.7 / 22.2 on 1,600; 8 rows 13.3 / 13.5 on 1,600, 15.9 /
+  // 18.9 on 6,400; 3 rows 15.4 / 12.9 on 6,400, 23.3 / 22.9 on 25,600.
+  const bool tc = prefix_len > 0 && pre_rts > 1 && pre_rts * kv->kv_heads * prefix_len > 340ll * *sms;
   if (tc) stream_ctas = split_sms(a, *sms, key_bytes);
   a->warps = stream_ctas * kWarps;
   const int64_t tiles = ((int64_t)max_suffix + kTile - 1) / kTile;
