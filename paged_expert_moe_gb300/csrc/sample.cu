@@ -38,11 +38,12 @@ constexpr float kBinsPerUnit = 16.f;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxSmem = (kMaxVocab / kMaxCluster + 8) * 4;
-constexpr int kList = 1024;         // candidates of a CTA
-constexpr int kMerged = 2048;       // and of a row
+constexpr int kMerged = 2048;       // candidates of a row
 constexpr int kMaxK = 1200;         // top_k up to which rows are cut by their candidates
 constexpr int kCutP = 384;          // K for rows that only top-p cuts
 constexpr int kPairs = 256;         // elements up to which all pairs are compared
+constexpr int kGroups = 128;        // groups of 4 threads, whose largest logits give a bound
+constexpr int kSegs = kMaxCluster * kWarps;
 
 typedef unsigned long long u64;
 
@@ -79,26 +80,23 @@ struct Pick {             // a bin found by a scan, weight and count above it (b
 
 struct alignas(16) Shared {
   Histogram hist;
-  union {
-    Histogram level;      // step 3's passes over the key's bits
-    u64 list[kList];      // candidates of this CTA: ~key << 32 | id
-  };
-  u64 merged[kMerged];    // and, in the row's first CTA, of all
-  float best, bound;      // this CTA's largest logit, and its bound of the K-th
+  Histogram level;        // select's, and step 3's passes over the key's bits
+  u64 merged[kMerged];    // in the row's first CTA: ~key << 32 | id of the candidates
+  int listed;             // there: how many,
+  u64 sum, list_sum;      // all weights of the row, and the candidates'
+  int arg;                // and, of greedy rows, the lowest id that has the largest logit
+  float best[kMaxCluster], bound[kMaxCluster];  // every CTA's largest logit, its bound of the K-th
   uint32_t bound_key;
-  int arg;                // in the first CTA, of greedy rows: the lowest id that has it
-  int listed;             // candidates found
-  u64 sum, list_sum;      // all weights of the slice, and its candidates'
+  float top[kWarps];
+  alignas(16) float group_top[kGroups];
   Threshold thr;
   int members;            // select: elements of the bin it looks into
   u64 sel, sel_upto;      // and what it found
   u64 scan[kWarps];
   uint32_t scan_cnt[kWarps];
   Pick pick;
-  u64 seg_sum[kWarps];    // step 4: per warp segment, weight above the threshold
-  uint32_t seg_tie[kWarps];
-  u64 all_sum[kMaxCluster * kWarps];
-  u64 base_sum;
+  u64 seg_sum[kSegs];     // step 4: per warp segment of the row, weight above the threshold
+  uint32_t seg_tie[kSegs];
 };
 
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -231,16 +229,22 @@ __device__ void sort_up(u64* buf, u64 (&c)[kEach]) {
   __syncthreads();  // buf is free
 }
 
-// Appends id of x to this CTA's list where `in`; all lanes of a warp call it. One atomic a
-// warp: one a candidate, all on the same word, would be done one after the other.
-__device__ __forceinline__ void append(Shared& sh, bool in, float x, int id) {
-  const uint32_t mask = __ballot_sync(0xffffffffu, in);
-  if (mask == 0) return;
+// Room in the first CTA's list (`to`) for the `c` candidates of this thread: where they begin.
+// One remote atomic a warp; all lanes call it.
+__device__ __forceinline__ int reserve(Shared* to, int c) {
   const int lane = threadIdx.x & 31;
+  int upto = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int d = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += d;
+  }
   int at = 0;
-  if (lane == __ffs(mask) - 1) at = atomicAdd(&sh.listed, __popc(mask));
-  at = __shfl_sync(0xffffffffu, at, __ffs(mask) - 1) + __popc(mask & ((1u << lane) - 1));
-  if (in && at < kList) sh.list[at] = ((u64)~key_of(x) << 32) | (uint32_t)id;
+  if (lane == 31 && upto > 0) at = atomicAdd(&to->listed, upto);
+  return __shfl_sync(0xffffffffu, at, 31) + upto - c;
+}
+__device__ __forceinline__ void put(Shared* to, int at, float x, int id) {
+  if (at < kMerged) to->merged[at] = ((u64)~key_of(x) << 32) | (uint32_t)id;
 }
 
 __device__ __forceinline__ int pow2_above(int n) { return n <= 64 ? 64 : 1 << (32 - __clz(n - 1)); }
@@ -253,6 +257,7 @@ __device__ void find_bin(cg::cluster_group& cluster, Shared& sh, Histogram* h, b
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = (int)cluster.num_blocks();
   cluster.sync();
   if (cluster.block_rank() == 0) {
+    if (tid == 0) sh.listed = 0;  // every CTA has read it
     uint32_t v[kMaxCluster][3];  // all remote loads in flight at once
 #pragma unroll
     for (int i = 0; i < kMaxCluster; ++i) {
@@ -293,57 +298,19 @@ __device__ void find_bin(cg::cluster_group& cluster, Shared& sh, Histogram* h, b
   cluster.sync();
 }
 
-// What each CTA listed, read by one lane per CTA: whether all of it fits, and the sums.
-struct Listed {
-  int mine, before, total;  // lane's CTA: candidates, those of the CTAs before it; all
-  bool fits;
-  u64 sum, list_sum;        // of all CTAs
-};
-__device__ Listed read_listed(cg::cluster_group& cluster, Shared& sh) {
-  const int lane = threadIdx.x & 31, nb = (int)cluster.num_blocks();
-  const Shared* o = cluster.map_shared_rank(&sh, lane < nb ? lane : 0);
-  Listed l;
-  l.mine = lane < nb ? o->listed : 0;
-  l.sum = warp_sum(lane < nb ? o->sum : 0);
-  l.list_sum = warp_sum(lane < nb ? o->list_sum : 0);
-  int upto = l.mine;
-#pragma unroll
-  for (int d = 1; d < kMaxCluster; d <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += x;
-  }
-  l.before = upto - l.mine;
-  l.total = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
-  l.fits = l.total <= kMerged && __all_sync(0xffffffffu, l.mine <= kList);
-  return l;
-}
-// All CTAs' candidates to sh.merged, two warps to a CTA, padded with
-// ~0 to a power of two; ends with a barrier.
-__device__ void merge_lists(cg::cluster_group& cluster, Shared& sh, const Listed& l) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  static_assert(kWarps >= 2 * kMaxCluster, "two warps a CTA");
-  const int from = warp >> 1, n = __shfl_sync(0xffffffffu, l.mine, from), at = __shfl_sync(0xffffffffu, l.before, from);
-  if (from < (int)cluster.num_blocks()) {
-    const Shared* o = cluster.map_shared_rank(&sh, from);
-    for (int i = (warp & 1) * 32 + lane; i < n; i += 64) sh.merged[at + i] = o->list[i];
-  }
-  for (int i = l.total + threadIdx.x; i < pow2_above(l.total); i += kThreads) sh.merged[i] = ~0ull;
-  __syncthreads();
-}
-
 // Sum over the G consecutive lanes that share a candidate.
 __device__ __forceinline__ u64 group_sum(u64 v, int G) {
   for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// How many of a[0, n) are below x, and (WEIGHTS) the sum of their weights; the G threads that
-// share x take every G-th pair of elements each.
+// How many of a[0, n) are below x, and (WEIGHTS) the sums of their weights and of all; the G
+// threads that share x take every G-th pair of elements each.
 template <bool WEIGHTS>
 __device__ __forceinline__ void count_below(const u64* a, const uint32_t* weights, int n, u64 x, int part, int G, u64* place,
-                                            u64* before) {
+                                            u64* before, u64* all) {
   uint32_t p = 0;
-  u64 b = 0;
+  u64 b = 0, s = 0;
   const int pairs = n >> 1;
 #pragma unroll 4
   for (int j = part; j < pairs; j += G) {
@@ -355,51 +322,59 @@ __device__ __forceinline__ void count_below(const u64* a, const uint32_t* weight
       const uint2 w = reinterpret_cast<const uint2*>(weights)[j];
       b += f ? w.x : 0u;
       b += g ? w.y : 0u;
+      s += w.x;
+      s += w.y;
     }
   }
-  if ((n & 1) && part == 0 && a[n - 1] < x) {
-    ++p;
-    if (WEIGHTS) b += weights[n - 1];
+  if ((n & 1) && part == 0) {
+    const bool f = a[n - 1] < x;
+    const uint32_t w = WEIGHTS ? weights[n - 1] : 0u;
+    p += f;
+    b += f ? w : 0u;
+    s += w;
   }
-  *place = group_sum(p, G);
-  if (WEIGHTS) *before = group_sum(b, G);
+  for (int o = G / 2; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+  *place = p;
+  if (WEIGHTS) *before = group_sum(b, G), *all = group_sum(s, G);
 }
 
-// Step 2's end for up to kPairs candidates: sh.merged holds n of them (padded with ~0 to a
-// power of two from 64). A candidate's place and the weight before it come from comparing it
-// with all others, twice: in the order of the logits for the cuts, in the order of the ids
-// for the draw. kThreads / n2 threads share a candidate.
+// Step 2's end for up to kPairs candidates, the n of sh.merged. A candidate's place and the
+// weight before it come from comparing it with all others, twice: in the order of the logits
+// for the cuts, in the order of the ids for the draw. kThreads / n2 threads share a candidate.
 __device__ void compare_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, int row, int n, int top_k, bool use_k,
                                  float top_p, bool use_p, float min_p, u64 all_weights) {
   const int tid = threadIdx.x, n2 = pow2_above(n), G = kThreads / n2, i = tid / G, part = tid % G;
-  uint32_t* weights = reinterpret_cast<uint32_t*>(sh.list);  // the list is in sh.merged by now
-  const u64 c = sh.merged[i];
+  const bool own = part == 0 && i < n;
+  uint32_t *weights = sh.level.cnt, *kept_weights = sh.level.lo;
+  const u64 c = i < n ? sh.merged[i] : ~0ull;
   const float wt = rw.weight(of_key(~(uint32_t)(c >> 32)));
   const uint32_t w = i < n ? Row::units(wt) : 0;
-  u64 place, before = 0, total = all_weights;
+  const float uu = a.u[row];
+  u64 place, before = 0, total = all_weights, unused;
   if (use_p) {
-    if (part == 0) weights[i] = w;
+    if (own) weights[i] = w;
     __syncthreads();
-    count_below<true>(sh.merged, weights, n, c, part, G, &place, &before);
+    count_below<true>(sh.merged, weights, n, c, part, G, &place, &before, &unused);
   } else {
-    count_below<false>(sh.merged, weights, n, c, part, G, &place, &before);
+    count_below<false>(sh.merged, weights, n, c, part, G, &place, &before, &unused);
   }
   const bool in_k = i < n && (!use_k || place < (u64)top_k);
-  if (use_k && use_p) block_scan(sh, in_k && part == 0 ? w : 0, &total);
+  if (use_k && use_p) {
+    if (own && place + 1 == (u64)min(top_k, n)) sh.sel = before + w;  // the weight of the first top_k
+    __syncthreads();
+    total = sh.sel;
+  }
   const u64 least = use_p ? least_weight(total, top_p) : ~0ull;
   const uint32_t kept = in_k && before < least && !(wt < min_p) ? w : 0;
-  u64 S;
-  block_scan(sh, part == 0 ? kept : 0, &S);
   // by id: what was cut goes behind every id, with no weight
   const u64 by_id = kept > 0 ? c << 32 : ~0ull;
   u64* ids = sh.merged + kPairs;
-  if (part == 0) ids[i] = by_id, weights[i] = kept;
+  if (own) ids[i] = by_id, kept_weights[i] = kept;
   __syncthreads();
-  u64 run;
-  count_below<true>(ids, weights, n, by_id, part, G, &place, &run);
-  const float uu = a.u[row];
+  u64 run, S;
+  count_below<true>(ids, kept_weights, n, by_id, part, G, &place, &run, &S);
   const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
-  if (part == 0 && kept > 0 && run <= target && target < run + kept) {
+  if (own && kept > 0 && run <= target && target < run + kept) {
     a.ids[row] = (int32_t)(uint32_t)c;
     if (a.logprob != nullptr) a.logprob[row] = logf((float)kept / (float)S);
   }
@@ -457,8 +432,8 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
   if (m <= kPairs) {
     const int n2 = pow2_above(m), G = kThreads / n2, i = tid / G, part = tid % G;
     const u64 x = i < m ? sh.merged[i] : ~0ull;
-    u64 place, before;
-    count_below<true>(sh.merged, weights, m, x, part, G, &place, &before);
+    u64 place, before, unused;
+    count_below<true>(sh.merged, weights, m, x, part, G, &place, &before, &unused);
     place += sh.pick.cnt;
     before += sh.pick.above;
     const uint32_t w = i < m ? weights[i] : 0;
@@ -578,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   extern __shared__ __align__(16) uint4 xs[];
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before the first remote access
   pdl_wait();  // the logits may come from the kernel ahead
   pdl_trigger();
   const int nb = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -617,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       xs[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  sh.hist.cnt[tid] = sh.hist.lo[tid] = sh.hist.hi[tid] = 0;
-  if (tid == 0) sh.arg = INT_MAX, sh.listed = 0, sh.sum = 0, sh.list_sum = 0;
+  sh.hist.cnt[tid] = 0;
+  if (tid == 0) sh.bound_key = 0, sh.arg = INT_MAX, sh.listed = 0, sh.sum = 0, sh.list_sum = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");
   float mine = -INFINITY;  // of the vectors this thread loaded; fmaxf leaves NaN out
   for (int i = tid; i < nv; i += kThreads) {
@@ -629,22 +605,43 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   float best = mine;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if (lane == 0) sh.seg_tie[warp] = __float_as_uint(best);
+  if (lane == 0) sh.top[warp] = best;
   const float temp = a.temperature != nullptr ? a.temperature[row] : 1.f;
   const int top_k = a.top_k != nullptr ? a.top_k[row] : 0;
   const float top_p = a.top_p != nullptr ? a.top_p[row] : 1.f;
   const float min_p = a.min_p != nullptr ? fminf(a.min_p[row], 1.f) : 0.f;
   const bool use_k = top_k > 0 && top_k < a.V, use_p = top_p < 1.f;
   const bool listing = temp > 0.f && (use_k ? top_k <= kMaxK : use_p);
+  const uint32_t want = ((use_k ? top_k : kCutP) + nb - 1) / nb;  // of a CTA, if `listing`
+  const bool few = want <= kGroups * 2 / 3;
+  if (listing && few) {
+    float g = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+    if ((lane & 3) == 0) sh.group_top[tid >> 2] = g;
+  }
   __syncthreads();
-  best = __uint_as_float(sh.seg_tie[lane % kWarps]);
+  best = sh.top[lane % kWarps];
 #pragma unroll
   for (int o = kWarps / 2; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if (tid == 0) sh.best = best;
-  if (listing) {
+  const float cta_best = best;
+  float bound = -FLT_MAX;  // too few groups with a logit: every logit is a candidate
+  if (listing && few) {
+    // the want-th largest of the groups' largest: a warp ranks 8 of them
+    const float4 v = reinterpret_cast<const float4*>(sh.group_top)[lane];
+    float found = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kGroups / kWarps; ++i) {
+      const float x = sh.group_top[warp * (kGroups / kWarps) + i];
+      const int rank_x = __popc(__ballot_sync(0xffffffffu, v.x >= x)) + __popc(__ballot_sync(0xffffffffu, v.y >= x)) +
+                         __popc(__ballot_sync(0xffffffffu, v.z >= x)) + __popc(__ballot_sync(0xffffffffu, v.w >= x));
+      if (rank_x >= (int)want) found = fmaxf(found, x);
+    }
+    if (lane == 0 && found > -INFINITY) atomicMax(&sh.bound_key, key_of(found));
+    __syncthreads();
+    if (sh.bound_key != 0) bound = of_key(sh.bound_key);
+  } else if (listing) {
     // the bin of the threads' largest logits, by distance from the CTA's, that holds the
-    // K / nb-th; the bound is the least of those in it or above it
-    const uint32_t want = ((use_k ? top_k : kCutP) + nb - 1) / nb;
+    // want-th; the bound is the least of those in it or above it
     const int mybin = Row{best, 1.f}.bin(mine);
     if (mine > -INFINITY) atomicAdd(&sh.hist.cnt[mybin], 1u);
     if (tid == 0) sh.pick.bin = kBins, sh.bound_key = 0xffffffffu;
@@ -665,23 +662,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     __syncthreads();
     if (mine > -INFINITY && mybin <= sh.pick.bin) atomicMin(&sh.bound_key, key_of(mine));
     __syncthreads();
-    // fewer threads with a logit than that: every logit is a candidate
-    if (tid == 0) sh.bound = sh.pick.bin == kBins ? -FLT_MAX : of_key(sh.bound_key);
+    if (sh.pick.bin != kBins) bound = of_key(sh.bound_key);
+  }
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the row has started
+  if (tid < nb) {
+    Shared* o = cluster.map_shared_rank(&sh, tid);
+    o->best[rank] = cta_best, o->bound[rank] = bound;
   }
   cluster.sync();
-  best = cluster.map_shared_rank(&sh, lane < nb ? lane : 0)->best;
-  float bound = listing ? cluster.map_shared_rank(&sh, lane < nb ? lane : 0)->bound : 0.f;
 #pragma unroll
-  for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
-    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-    bound = fminf(bound, __shfl_xor_sync(0xffffffffu, bound, o));
-  }
-  best = __shfl_sync(0xffffffffu, best, 0);
-  bound = __shfl_sync(0xffffffffu, bound, 0);
+  for (int i = 0; i < kMaxCluster; ++i)
+    if (i < nb) best = fmaxf(best, sh.best[i]), bound = fminf(bound, sh.bound[i]);
+  Shared* const head = cluster.map_shared_rank(&sh, 0);  // the row's first CTA
 
   const Row rw{best, 1.f / temp};
   if (best == -INFINITY || !(temp > 0.f)) {  // the same for every CTA of the row
-    if (best != -INFINITY && sh.best == best) {
+    if (best != -INFINITY && cta_best == best) {
       int low = INT_MAX;
       for (int i = tid; i < nv; i += kThreads) {
         const V x(xs[i]);
@@ -690,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (x.f[q] == best) low = min(low, first + i * N + q);
       }
       low = __reduce_min_sync(0xffffffffu, low);
-      if (lane == 0 && low != INT_MAX) atomicMin(&cluster.map_shared_rank(&sh, 0)->arg, low);
+      if (lane == 0 && low != INT_MAX) atomicMin(&head->arg, low);
     }
     cluster.sync();
     if (rank == 0 && tid == 0) {
@@ -703,50 +699,56 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   // ---- 2. candidates
   u64 total = 0;  // of all weights where only top-p cuts, then of what is kept
   if (listing) {
-    u64 sum = 0, list_sum = 0;
-    const bool totals = !use_k;
-    for (int i0 = warp * 32; i0 < nv; i0 += kThreads) {
-      const int i = i0 + lane;
-      const V x(i < nv ? xs[i] : V::none());
-      uint32_t w[N];
-      if (totals) {
+    int found = 0;
+    if (use_k) {
+      if (mine >= bound)
+        for (int i = tid; i < nv; i += kThreads) {
+          const V x(xs[i]);
+#pragma unroll
+          for (int q = 0; q < N; ++q) found += x.f[q] >= bound;
+        }
+    } else {
+      u64 sum = 0, list_sum = 0;
+      for (int i = tid; i < nv; i += kThreads) {
+        const V x(xs[i]);
+        uint32_t w[N];
 #pragma unroll
         for (int q = 0; q < N; ++q) w[q] = rw.units_of(x.f[q]);
 #pragma unroll
-        for (int q = 0; q < N; ++q) sum += w[q];
-      }
-      bool any = false;
-#pragma unroll
-      for (int q = 0; q < N; ++q) any |= x.f[q] >= bound;
-      if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
         for (int q = 0; q < N; ++q) {
-          const bool in = x.f[q] >= bound;
-          if (totals && in) list_sum += w[q];
-          append(sh, in, x.f[q], first + i * N + q);
+          sum += w[q];
+          if (x.f[q] >= bound) list_sum += w[q], ++found;
         }
       }
-    }
-    if (totals) {
       sum = warp_sum(sum);
       list_sum = warp_sum(list_sum);
-      if (lane == 0) atomicAdd(&sh.sum, sum), atomicAdd(&sh.list_sum, list_sum);
+      if (lane == 0) atomicAdd(&head->sum, sum), atomicAdd(&head->list_sum, list_sum);
+    }
+    if (__any_sync(0xffffffffu, found > 0)) {
+      int at = reserve(head, found);
+      if (found > 0)
+        for (int i = tid; i < nv; i += kThreads) {
+          const V x(xs[i]);
+#pragma unroll
+          for (int q = 0; q < N; ++q)
+            if (x.f[q] >= bound) put(head, at++, x.f[q], first + i * N + q);
+        }
     }
     cluster.sync();
-    const Listed l = read_listed(cluster, sh);  // the same in every CTA
-    if (l.fits && (use_k || l.list_sum >= least_weight(l.sum, top_p))) {
-      if (rank == 0) merge_lists(cluster, sh, l);
-      cluster.sync();  // the other CTAs are done
+    const int listed = head->listed;  // the same in every CTA
+    total = head->sum;
+    if (listed <= kMerged && (use_k || head->list_sum >= least_weight(total, top_p))) {
+      asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA has read the first one's
       if (rank == 0) {
-        if (l.total <= kPairs)
-          compare_and_draw(sh, a, rw, row, l.total, top_k, use_k, top_p, use_p, min_p, l.sum);
+        if (listed <= kPairs)
+          compare_and_draw(sh, a, rw, row, listed, top_k, use_k, top_p, use_p, min_p, total);
         else
-          select_and_draw(sh, a, rw, row, l.total, top_k, use_k, top_p, use_p, min_p, l.sum);
+          select_and_draw(sh, a, rw, row, listed, top_k, use_k, top_p, use_p, min_p, total);
+        __syncthreads();
       }
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
       return;
     }
-    total = l.sum;
-    cluster.sync();  // every CTA has read the lists' sizes
   }
 
   // ---- 3. histogram over the distance from the largest
@@ -784,25 +786,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       const int bin = pick.bin;
       const u64 inside = target - (mode == 0 ? pick.cnt : pick.above);
-      if (tid == 0) sh.listed = 0;
-      __syncthreads();
-      for (int i0 = warp * 32; i0 < nv; i0 += kThreads) {
-        const int i = i0 + lane;
-        const V x(i < nv ? xs[i] : V::none());
-        bool in[N], any = false;
+      int found = 0;
+      auto inside_bin = [&](float x) { return x > -INFINITY && rw.bin(x) == bin; };
+      for (int i = tid; i < nv; i += kThreads) {
+        const V x(xs[i]);
 #pragma unroll
-        for (int q = 0; q < N; ++q) any |= in[q] = x.f[q] > -INFINITY && rw.bin(x.f[q]) == bin;
-        if (__any_sync(0xffffffffu, any)) {
+        for (int q = 0; q < N; ++q) found += inside_bin(x.f[q]);
+      }
+      if (__any_sync(0xffffffffu, found > 0)) {
+        int at = reserve(head, found);
+        if (found > 0)
+          for (int i = tid; i < nv; i += kThreads) {
+            const V x(xs[i]);
 #pragma unroll
-          for (int q = 0; q < N; ++q) append(sh, in[q], x.f[q], first + i * N + q);
-        }
+            for (int q = 0; q < N; ++q)
+              if (inside_bin(x.f[q])) put(head, at++, x.f[q], first + i * N + q);
+          }
       }
       cluster.sync();
-      const Listed l = read_listed(cluster, sh);
-      if (l.fits) {
+      const int listed = head->listed;
+      if (listed <= kMerged) {
         if (rank == 0) {
-          merge_lists(cluster, sh, l);
-          find_in_bin(sh, rw, l.total, bin, mode == 0, inside, pick.above);
+          find_in_bin(sh, rw, listed, bin, mode == 0, inside, pick.above);
           if (tid > 0 && tid < nb) cluster.map_shared_rank(&sh, tid)->thr = sh.thr;
         }
         cluster.sync();
@@ -816,7 +821,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       uint32_t over_cnt = pick.cnt;
       for (int level = 0; level < 4; ++level) {
         const int sft = 24 - 8 * level;
-        cluster.sync();  // every CTA has read the list, or the level before
         sh.level.cnt[tid] = sh.level.lo[tid] = sh.level.hi[tid] = 0;
         __syncthreads();
         elements([&](float x) {
@@ -833,7 +837,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const u64 each = rw.units_of(of_key(key_t));
       ties = (uint32_t)(mode == 0 ? target - over_cnt : (target - over + each - 1) / each);
       total = over + each * ties;
-      cluster.sync();  // before the list takes the level's place
     }
   }
 
@@ -880,49 +883,58 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   sum = warp_sum(sum);
   nt = (uint32_t)__reduce_add_sync(0xffffffffu, nt);
-  if (lane == 0) sh.seg_sum[warp] = sum, sh.seg_tie[warp] = nt;
-  cluster.sync();
-  const int segs = nb * kWarps;
-  if (warp == 0) {
-    // every CTA: running ties and sums over all segments
-    constexpr int R = kMaxCluster * kWarps / 32;
-    u64 sums[R], run = 0;
-    uint32_t tied[R], run_t = 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int s = i * 32 + lane;
-      const Shared* o = cluster.map_shared_rank(&sh, s < segs ? s / kWarps : 0);
-      sums[i] = s < segs ? o->seg_sum[s % kWarps] : 0;
-      tied[i] = s < segs ? o->seg_tie[s % kWarps] : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int s = i * 32 + lane;
-      uint32_t ti = tied[i];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t d = __shfl_up_sync(0xffffffffu, ti, o);
-        if (lane >= o) ti += d;
-      }
-      const uint32_t before = run_t + ti - tied[i];
-      run_t += __shfl_sync(0xffffffffu, ti, 31);
-      const uint32_t in = before >= ties ? 0 : min(tied[i], ties - before);
-      const u64 vi = warp_scan(sums[i] + (tie_ok ? (u64)in * unit_t : 0), lane) + run;
-      run = __shfl_sync(0xffffffffu, vi, 31);
-      if (s < segs) sh.all_sum[s] = vi;
-      if (s >= rank * kWarps && s < (rank + 1) * kWarps) sh.scan_cnt[s - rank * kWarps] = before;
-    }
-    if (lane == 0) sh.base_sum = run;
+  if (lane < nb) {  // to every CTA
+    Shared* o = cluster.map_shared_rank(&sh, lane);
+    o->seg_sum[rank * kWarps + warp] = sum, o->seg_tie[rank * kWarps + warp] = nt;
   }
-  __syncthreads();
-  const u64 S = sh.base_sum;
+  cluster.sync();  // the last one: no CTA reads another's memory from here on
+  // running ties and sums over the segments, kSegs / 32 in a row to a lane
+  constexpr int R = kSegs / 32;
+  const int segs = nb * kWarps, seg = rank * kWarps + warp;
+  u64 sums[R], run_s = 0;
+  uint32_t tied[R], run_t = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int s = lane * R + i;
+    sums[i] = s < segs ? sh.seg_sum[s] : 0;
+    tied[i] = s < segs ? sh.seg_tie[s] : 0;
+    run_t += tied[i];
+  }
+  {
+    const uint32_t own = run_t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t d = __shfl_up_sync(0xffffffffu, run_t, o);
+      if (lane >= o) run_t += d;
+    }
+    run_t -= own;
+  }
+  uint32_t ties_before[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    ties_before[i] = run_t;
+    const uint32_t in = run_t >= ties ? 0 : min(tied[i], ties - run_t);
+    run_t += tied[i];
+    if (tie_ok) sums[i] += (u64)in * unit_t;
+    run_s += sums[i];
+  }
+  const u64 upto = warp_scan(run_s, lane);
+  const u64 S = __shfl_sync(0xffffffffu, upto, 31);
+  u64 lo = upto - run_s, hi = lo;
+  uint32_t tb = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (i < seg % R) lo += sums[i];
+    if (i <= seg % R) hi += sums[i];
+    if (i == seg % R) tb = ties_before[i];
+  }
+  lo = __shfl_sync(0xffffffffu, lo, seg / R);
+  hi = __shfl_sync(0xffffffffu, hi, seg / R);
+  tb = __shfl_sync(0xffffffffu, tb, seg / R);
   const float uu = a.u[row];
   const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
-  const int seg = rank * kWarps + warp;
-  const u64 lo = seg == 0 ? 0 : sh.all_sum[seg - 1], hi = sh.all_sum[seg];
   if (target >= lo && target < hi) {  // exactly one warp of the cluster
     u64 run = lo;
-    uint32_t tb = sh.scan_cnt[warp];
     for (int i0 = s0; i0 < s1; i0 += 32) {
       u64 w[N], v = 0;
       uint32_t t = 0;
@@ -968,7 +980,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       run += __shfl_sync(0xffffffffu, vi, 31);
     }
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 }  // namespace
