@@ -112,6 +112,8 @@ __device__ __forceinline__ u64 share(u64 total, float part) {
   return (total >> 24) * n + (((total & 0xffffffull) * n) >> 24);
 }
 
+__device__ __forceinline__ u64 share_of(u64 total, float u) { return share(total, u > 0.f ? fminf(u, 0.99999994f) : 0.f); }
+
 __device__ __forceinline__ u64 least_weight(u64 total, float top_p) {
   return max((u64)1, share(total, top_p > 0.f ? top_p : 0.f));
 }
@@ -147,12 +149,21 @@ __device__ __forceinline__ u64 block_scan(Shared& sh, u64 v, u64* total) {
   return v + before;
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; what it flushes to 0 is below 2^-126
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 struct Row {
-  float m, r;  // largest logit, 1 / temperature
-  __device__ __forceinline__ float weight(float x) const { return x == m ? 1.f : expf((x - m) * r); }
+  float m, r;  // largest logit, log2(e) / temperature
+  // log2 of a weight: four roundings of an argument of at most 31, where the weight is not 0,
+  // change the weight by less than 2^-17 of it.
+  __device__ __forceinline__ float log2w(float x) const { return x == m ? 0.f : (x - m) * r; }
+  __device__ __forceinline__ float weight(float x) const { return exp2_approx(log2w(x)); }
   // NaN gives 0, as -inf does
   __device__ __forceinline__ static uint32_t units(float w) { return (uint32_t)(w * 2147483648.f); }
-  __device__ __forceinline__ uint32_t units_of(float x) const { return units(expf(x == m ? 0.f : (x - m) * r)); }
+  __device__ __forceinline__ uint32_t units_of(float x) const { return units(weight(x)); }
   __device__ __forceinline__ int bin(float x) const {
     const float d = (m - x) * kBinsPerUnit;
     return d < (float)(kBins - 1) ? (int)d : (x == m ? 0 : kBins - 1);
@@ -342,14 +353,13 @@ __device__ __forceinline__ void count_below(const u64* a, const uint32_t* weight
 // weight before it come from comparing it with all others, twice: in the order of the logits
 // for the cuts, in the order of the ids for the draw. kThreads / n2 threads share a candidate.
 __device__ void compare_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, int row, int n, int top_k, bool use_k,
-                                 float top_p, bool use_p, float min_p, u64 all_weights) {
+                                 float top_p, bool use_p, float min_p, float uu, u64 all_weights) {
   const int tid = threadIdx.x, n2 = pow2_above(n), G = kThreads / n2, i = tid / G, part = tid % G;
   const bool own = part == 0 && i < n;
   uint32_t *weights = sh.level.cnt, *kept_weights = sh.level.lo;
   const u64 c = i < n ? sh.merged[i] : ~0ull;
   const float wt = rw.weight(of_key(~(uint32_t)(c >> 32)));
   const uint32_t w = i < n ? Row::units(wt) : 0;
-  const float uu = a.u[row];
   u64 place, before = 0, total = all_weights, unused;
   if (use_p) {
     if (own) weights[i] = w;
@@ -373,7 +383,7 @@ __device__ void compare_and_draw(Shared& sh, const SampleArgs& a, const Row& rw,
   __syncthreads();
   u64 run, S;
   count_below<true>(ids, kept_weights, n, by_id, part, G, &place, &run, &S);
-  const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
+  const u64 target = share_of(S, uu);
   if (own && kept > 0 && run <= target && target < run + kept) {
     a.ids[row] = (int32_t)(uint32_t)c;
     if (a.logprob != nullptr) a.logprob[row] = logf((float)kept / (float)S);
@@ -381,42 +391,53 @@ __device__ void compare_and_draw(Shared& sh, const SampleArgs& a, const Row& rw,
 }
 
 // Of the block's elements c (kEach a thread, ~0 for none; ascending order), finds the one at
-// which the running count (by_count) or weight reaches `target`, into sh.sel; the running
-// weight up to it goes to sh.sel_upto. `bin` maps an element to 0 .. kBins - 1 without
-// disturbing the order, `weight` to its weight. One histogram finds the bin, comparing all
-// pairs inside it the element; a bin of more than kPairs elements is sorted instead.
-template <class Bin, class Weight>
-__device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool by_count, u64 target) {
+// which the running count (BY_COUNT) or weight reaches `target`, into sh.sel; the running
+// weight up to it goes to sh.sel_upto if `weigh`, or always without BY_COUNT. `bin` maps an
+// element to 0 .. kBins - 1 without disturbing the order, `weight` to its weight. One histogram
+// finds the bin, comparing all pairs inside it the element; a bin of more than kPairs elements
+// is sorted instead. sh.level and sh.members are zero on entry and on return.
+template <bool BY_COUNT, class Bin, class Weight>
+__device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool weigh, u64 target) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* weights = reinterpret_cast<uint32_t*>(sh.merged + kPairs);
-  sh.level.cnt[tid] = sh.level.lo[tid] = sh.level.hi[tid] = 0;
-  if (tid == 0) sh.members = 0;
-  __syncthreads();
+  weigh |= !BY_COUNT;
 #pragma unroll
   for (int e = 0; e < kEach; ++e)
     if (c[e] != ~0ull) {
       const int b = bin(c[e]);
-      const uint32_t w = weight(c[e]);
-      atomicAdd(&sh.level.cnt[b], 1u);
-      atomicAdd(&sh.level.lo[b], w & 0xffffu);
-      atomicAdd(&sh.level.hi[b], w >> 16);
+      if (BY_COUNT) atomicAdd(&sh.level.cnt[b], 1u);
+      if (weigh) {
+        const uint32_t w = weight(c[e]);
+        atomicAdd(&sh.level.lo[b], w & 0xffffu);
+        atomicAdd(&sh.level.hi[b], w >> 16);
+      }
     }
   __syncthreads();
   const uint32_t own_c = sh.level.cnt[tid];
   const u64 own_w = ((u64)sh.level.hi[tid] << 16) + sh.level.lo[tid];
   uint32_t ci = own_c;
+  u64 wi = own_w;
+  if (BY_COUNT) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t d = __shfl_up_sync(0xffffffffu, ci, o);
-    if (lane >= o) ci += d;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t d = __shfl_up_sync(0xffffffffu, ci, o);
+      if (lane >= o) ci += d;
+    }
+    if (lane == 31) sh.scan_cnt[warp] = ci;
   }
-  if (lane == 31) sh.scan_cnt[warp] = ci;
-  u64 total;
-  const u64 wi = block_scan(sh, own_w, &total);
+  if (weigh) {
+    wi = warp_scan(wi, lane);
+    if (lane == 31) sh.scan[warp] = wi;
+  }
+  __syncthreads();
+  sh.level.cnt[tid] = sh.level.lo[tid] = sh.level.hi[tid] = 0;
 #pragma unroll
   for (int i = 0; i < kWarps; ++i)
-    if (i < warp) ci += sh.scan_cnt[i];
-  if (by_count ? (ci >= target && ci - own_c < target) : (wi >= target && wi - own_w < target)) {
+    if (i < warp) {
+      if (BY_COUNT) ci += sh.scan_cnt[i];
+      if (weigh) wi += sh.scan[i];
+    }
+  if (BY_COUNT ? (ci >= target && ci - own_c < target) : (wi >= target && wi - own_w < target)) {
     sh.pick = Pick{wi - own_w, ci - own_c, tid};
   }
   __syncthreads();
@@ -437,11 +458,12 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
     place += sh.pick.cnt;
     before += sh.pick.above;
     const uint32_t w = i < m ? weights[i] : 0;
-    if (part == 0 && i < m && (by_count ? place + 1 == target : before < target && target <= before + w)) {
+    if (part == 0 && i < m && (BY_COUNT ? place + 1 == target : before < target && target <= before + w)) {
       sh.sel = x;
       sh.sel_upto = before + w;
     }
     __syncthreads();
+    if (tid == 0) sh.members = 0;
     return;
   }
   // every element of this or another bin may be sorted along; the caller keeps its own
@@ -454,11 +476,12 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
   u64 mine = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) mine += s[e] != ~0ull ? weight(s[e]) : 0;
-  u64 run = block_scan(sh, mine, &total) - mine;
+  u64 total, run = block_scan(sh, mine, &total) - mine;
+  if (tid == 0) sh.members = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const uint32_t w = s[e] != ~0ull ? weight(s[e]) : 0;
-    if (s[e] != ~0ull && (by_count ? (u64)(tid * kEach + e) + 1 == target : run < target && target <= run + w)) {
+    if (s[e] != ~0ull && (BY_COUNT ? (u64)(tid * kEach + e) + 1 == target : run < target && target <= run + w)) {
       sh.sel = s[e];
       sh.sel_upto = run + w;
     }
@@ -467,8 +490,10 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
   __syncthreads();
 }
 
-// sh.merged's n elements to registers, kEach a thread; ends with a barrier.
-__device__ void take_merged(const Shared& sh, int n, u64 (&c)[kEach]) {
+// sh.merged's n elements to registers, kEach a thread, and sh.level cleared; ends with a barrier.
+__device__ void take_merged(Shared& sh, int n, u64 (&c)[kEach]) {
+  sh.level.cnt[threadIdx.x] = sh.level.lo[threadIdx.x] = sh.level.hi[threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.members = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int i = e * kThreads + threadIdx.x;
@@ -479,7 +504,7 @@ __device__ void take_merged(const Shared& sh, int n, u64 (&c)[kEach]) {
 
 // The same for more candidates: the cuts and the draw are selections.
 __device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, int row, int n, int top_k, bool use_k,
-                                float top_p, bool use_p, float min_p, u64 all_weights) {
+                                float top_p, bool use_p, float min_p, float uu, u64 all_weights) {
   u64 c[kEach];
   take_merged(sh, n, c);
   const auto logit = [](u64 x) { return of_key(~(uint32_t)(x >> 32)); };
@@ -488,7 +513,7 @@ __device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, 
   u64 last = ~0ull - 1, total = all_weights;  // the last candidate that is kept
   if (use_k) {
     if (n > top_k) {
-      select(sh, c, by_logit, weight, true, (u64)top_k);
+      select<true>(sh, c, by_logit, weight, use_p, (u64)top_k);
       last = sh.sel, total = sh.sel_upto;
     } else {
       u64 mine = 0;
@@ -496,10 +521,9 @@ __device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, 
       for (int e = 0; e < kEach; ++e) mine += c[e] != ~0ull ? weight(c[e]) : 0;
       block_scan(sh, mine, &total);
     }
-    __syncthreads();
   }
   if (use_p) {
-    select(sh, c, by_logit, weight, false, least_weight(total, top_p));
+    select<false>(sh, c, by_logit, weight, true, least_weight(total, top_p));
     last = min(last, sh.sel);
   }
   // in the order of the ids: id << 32 | weight
@@ -513,10 +537,9 @@ __device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, 
   }
   u64 S;
   block_scan(sh, mine, &S);
-  const float uu = a.u[row];
-  const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
-  select(sh, c, [&](u64 x) { return (int)((x >> 32) * kBins / (uint32_t)a.V); }, [](u64 x) { return (uint32_t)x; }, false,
-         target + 1);
+  const u64 target = share_of(S, uu);
+  select<false>(sh, c, [&](u64 x) { return (int)((x >> 32) * kBins / (uint32_t)a.V); }, [](u64 x) { return (uint32_t)x; },
+                true, target + 1);
   if (threadIdx.x == 0) {
     a.ids[row] = (int32_t)(sh.sel >> 32);
     if (a.logprob != nullptr) a.logprob[row] = logf((float)(uint32_t)sh.sel / (float)S);
@@ -535,7 +558,11 @@ __device__ void find_in_bin(Shared& sh, const Row& rw, int n, int bin, bool by_c
     const float d = ((rw.m - logit(x)) * kBinsPerUnit - (float)bin) * (float)kBins;
     return d < (float)(kBins - 1) ? max((int)d, 0) : kBins - 1;
   };
-  select(sh, c, inner, [&](u64 x) { return rw.units_of(logit(x)); }, by_count, target);
+  const auto weight = [&](u64 x) { return rw.units_of(logit(x)); };
+  if (by_count)
+    select<true>(sh, c, inner, weight, true, target);
+  else
+    select<false>(sh, c, inner, weight, true, target);
   if (tid == 0) sh.thr.ties = 0;
   const u64 sel = sh.sel;
   __syncthreads();
@@ -560,6 +587,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const int row = blockIdx.x / nb;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  const float temp = a.temperature != nullptr ? a.temperature[row] : 1.f;
+  const int top_k = a.top_k != nullptr ? a.top_k[row] : 0;
+  const float top_p = a.top_p != nullptr ? a.top_p[row] : 1.f;
+  const float min_p = a.min_p != nullptr ? fminf(a.min_p[row], 1.f) : 0.f;
+  const float uu = a.u[row];
   // slices start where the row's 16-byte vectors do: `shift` elements before its first
   const uint8_t* base = static_cast<const uint8_t*>(a.logits) + (int64_t)row * a.row_stride * EB;
   const int shift = (int)((reinterpret_cast<uintptr_t>(base) & 15) / EB);
@@ -606,10 +638,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) sh.top[warp] = best;
-  const float temp = a.temperature != nullptr ? a.temperature[row] : 1.f;
-  const int top_k = a.top_k != nullptr ? a.top_k[row] : 0;
-  const float top_p = a.top_p != nullptr ? a.top_p[row] : 1.f;
-  const float min_p = a.min_p != nullptr ? fminf(a.min_p[row], 1.f) : 0.f;
   const bool use_k = top_k > 0 && top_k < a.V, use_p = top_p < 1.f;
   const bool listing = temp > 0.f && (use_k ? top_k <= kMaxK : use_p);
   const uint32_t want = ((use_k ? top_k : kCutP) + nb - 1) / nb;  // of a CTA, if `listing`
@@ -675,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (i < nb) best = fmaxf(best, sh.best[i]), bound = fminf(bound, sh.bound[i]);
   Shared* const head = cluster.map_shared_rank(&sh, 0);  // the row's first CTA
 
-  const Row rw{best, 1.f / temp};
+  const Row rw{best, 1.44269504f / temp};
   if (best == -INFINITY || !(temp > 0.f)) {  // the same for every CTA of the row
     if (best != -INFINITY && cta_best == best) {
       int low = INT_MAX;
@@ -735,15 +763,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
     }
     cluster.sync();
-    const int listed = head->listed;  // the same in every CTA
-    total = head->sum;
-    if (listed <= kMerged && (use_k || head->list_sum >= least_weight(total, top_p))) {
+    const Shared& of = rank == 0 ? sh : *head;
+    const int listed = of.listed;  // the same in every CTA
+    total = of.sum;
+    const u64 list_sum = of.list_sum;
+    if (listed <= kMerged && (use_k || list_sum >= least_weight(total, top_p))) {
       asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA has read the first one's
       if (rank == 0) {
         if (listed <= kPairs)
-          compare_and_draw(sh, a, rw, row, listed, top_k, use_k, top_p, use_p, min_p, total);
+          compare_and_draw(sh, a, rw, row, listed, top_k, use_k, top_p, use_p, min_p, uu, total);
         else
-          select_and_draw(sh, a, rw, row, listed, top_k, use_k, top_p, use_p, min_p, total);
+          select_and_draw(sh, a, rw, row, listed, top_k, use_k, top_p, use_p, min_p, uu, total);
         __syncthreads();
       }
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -849,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const bool tie_ok = !all_keys && !(rw.weight(x_t) < min_p);
   // an element's weight if it lies above the threshold (ties are counted apart)
   auto kept = [&](float x) -> uint32_t {
-    const float w = expf(x == rw.m ? 0.f : (x - rw.m) * rw.r);
+    const float w = rw.weight(x);
     return x > x_t && !(w < min_p) ? Row::units(w) : 0u;
   };
   u64 sum = 0;
@@ -865,14 +895,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   } else {
     // a vector whose elements are all cut needs no weights: none above the threshold, or all
-    // safely below min_p (z below log(min_p) by more than logf and expf can be off)
-    const float z_cut = min_p > 0.f ? logf(min_p) - 0.01f : -INFINITY;
+    // safely below min_p (by more than its logarithm and the weights can be off)
+    const float z_cut = min_p > 0.f ? log2f(min_p) - 0.01f : -INFINITY;
     for (int i = s0 + lane; i < s1; i += 32) {
       const V x(xs[i]);
       bool any = false;
 #pragma unroll
       for (int q = 0; q < N; ++q) {
-        any |= x.f[q] > x_t && ((x.f[q] - rw.m) * rw.r > z_cut || x.f[q] == rw.m);
+        any |= x.f[q] > x_t && rw.log2w(x.f[q]) > z_cut;
         nt += x.f[q] == x_t;  // -inf where nothing is cut: tie_ok is false then
       }
       if (any) {
@@ -931,8 +961,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   lo = __shfl_sync(0xffffffffu, lo, seg / R);
   hi = __shfl_sync(0xffffffffu, hi, seg / R);
   tb = __shfl_sync(0xffffffffu, tb, seg / R);
-  const float uu = a.u[row];
-  const u64 target = share(S, uu > 0.f ? fminf(uu, 0.99999994f) : 0.f);
+  const u64 target = share_of(S, uu);
   if (target >= lo && target < hi) {  // exactly one warp of the cluster
     u64 run = lo;
     for (int i0 = s0; i0 < s1; i0 += 32) {
