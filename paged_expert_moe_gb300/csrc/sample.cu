@@ -164,9 +164,11 @@ struct Row {
   // NaN gives 0, as -inf does
   __device__ __forceinline__ static uint32_t units(float w) { return (uint32_t)(w * 2147483648.f); }
   __device__ __forceinline__ uint32_t units_of(float x) const { return units(weight(x)); }
+  // Distance from the largest in bins; with an infinite largest one it is below 0.
+  __device__ __forceinline__ float distance(float x) const { return (fminf(m, FLT_MAX) - x) * kBinsPerUnit; }
   __device__ __forceinline__ int bin(float x) const {
-    const float d = (m - x) * kBinsPerUnit;
-    return d < (float)(kBins - 1) ? (int)d : (x == m ? 0 : kBins - 1);
+    const float d = distance(x);
+    return d < (float)(kBins - 1) ? (int)(uint32_t)d : kBins - 1;  // the conversion takes d < 0 to 0
   }
 };
 
@@ -803,7 +805,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (use_k || use_p) {
     sh.hist.cnt[tid] = sh.hist.lo[tid] = sh.hist.hi[tid] = 0;
     __syncthreads();
-    elements([&](float x) { add(sh.hist, rw.bin(x), x, use_k, use_p); });
+    if (use_k) {
+      elements([&](float x) { add(sh.hist, rw.bin(x), x, true, use_p); });
+    } else {
+      // what weighs at most (total - target) / V cannot be where the target is reached: all of
+      // it together weighs less than what may be cut. Half or more of the row's logits, as a rule.
+      const uint32_t least = (uint32_t)((total - least_weight(total, top_p)) / (uint32_t)a.V);
+      elements([&](float x) {
+        const uint32_t w = rw.units_of(x);
+        if (w > least) {
+          const int b = rw.bin(x);
+          atomicAdd(&sh.hist.lo[b], w & 0xffffu);
+          atomicAdd(&sh.hist.hi[b], w >> 16);
+        }
+      });
+    }
     for (int mode = use_k ? 0 : 1; mode <= (use_p ? 1 : 0); ++mode) {
       // mode 0: the top_k-th token; mode 1: the token at which the weight reaches top_p (the
       // total is step 2's, or mode 0's)
@@ -817,7 +833,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const int bin = pick.bin;
       const u64 inside = target - (mode == 0 ? pick.cnt : pick.above);
       int found = 0;
-      auto inside_bin = [&](float x) { return x > -INFINITY && rw.bin(x) == bin; };
+      const float d_lo = bin == 0 ? -INFINITY : (float)bin, d_hi = bin == kBins - 1 ? NAN : (float)(bin + 1);
+      auto inside_bin = [&](float x) {
+        const float d = rw.distance(x);
+        return d >= d_lo && !(d >= d_hi) && x > -INFINITY;
+      };
       for (int i = tid; i < nv; i += kThreads) {
         const V x(xs[i]);
 #pragma unroll
