@@ -290,7 +290,7 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
         out = _empty(q.shape, q.dtype, q, stream)
     status = (_BINDING or _binding()).prefix_attention(
         k_cache, v_cache, q, prefix_pages, prefix_len, page_table, suffix_len, max_suffix,
-        k_cache.shape[3] ** -0.5 if scale is None else scale, row_seq, k_scale, v_scale, out, lse_out, scratch, err_out,
+        k_cache.shape[-1] ** -0.5 if scale is None else scale, row_seq, k_scale, v_scale, out, lse_out, scratch, err_out,
         stream)
     if status:
         raise PmoeError(status, "moe_prefix_attention")
