@@ -292,7 +292,6 @@ int cuda_status(cudaError_t e, const char* what) {
   set_cuda_error(e, what);
   return PMOE_ECUDA;
 }
-int launch_status(const char* what) { return cuda_status(cudaGetLastError(), what); }
 bool pdl_enabled() {
   static const bool on = !env_flag("PMOE_NO_PDL");
   return on;

@@ -158,7 +158,6 @@ struct ExpertLayout {
 ExpertLayout expert_layout(int fmt, int H, int I);
 
 // PMOE_OK, or PMOE_ECUDA with the launch's error text kept for pmoe_last_error.
-int launch_status(const char* what);
 int cuda_status(cudaError_t e, const char* what);
 // Whether kernels are launched with programmatic serialization (PMOE_NO_PDL=1: they are not).
 bool pdl_enabled();
