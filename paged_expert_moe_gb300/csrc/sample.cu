@@ -61,7 +61,7 @@ struct SampleArgs {
   int slice;  // elements of a CTA's slice (a multiple of 8)
 };
 
-struct Histogram {        // weights as two 16-bit halves: a slice holds at most 32,776
+struct Histogram {        // weights as two 16-bit halves: a slice holds at most 40,968
   uint32_t cnt[kBins];    // elements, so that no half's sum leaves 32 bits
   uint32_t lo[kBins];
   uint32_t hi[kBins];
@@ -1047,12 +1047,16 @@ extern "C" int moe_sample_tokens(const void* logits, int is_bf16, int T, int V, 
       off(ids_out, 4) || off(logprob_out, 4))
     return PMOE_EINVAL;
   // CTAs of a row: slices of 4,096 logits and up. Once the rows fill the GPU (two CTAs an SM),
-  // a CTA's fixed steps cost more than its share of the row, and slices of 8,192 and up are
-  // faster: 256 rows of 50,001 take 61 us with 4 CTAs a row and 89 with 8, 32 rows of 64,000
-  // 33 and 27.
+  // a CTA's fixed steps cost more than its share of the row: slices of 6,144 and up, and of up
+  // to 80 KB (two still fit an SM) with four times that many CTAs. But a row that needs step 3
+  // takes the longer the fewer CTAs it has. In us, with settings of all kinds, 8 / 4 / 2 CTAs a
+  // row: 256 rows of 32,000 61.5 / 41.7 / 47.8, of 50,001 72.6 / 49.9; 100 bf16 rows of 32,000
+  // 28.7 / 23.1 / 37.9; bf16 rows of 131,072: 256 of them 90.2 / 75.2, 64 of them 29.5 / 33.1.
   int cluster = 1;
+  const int64_t resident = 304, bytes = (int64_t)V * (is_bf16 ? 2 : 4);
   while (cluster < kMaxCluster && V > cluster * 4096) cluster *= 2;
-  while (cluster > 1 && (int64_t)T * cluster > 304 && V <= cluster * 8192) cluster /= 2;
+  while (cluster > 1 && (int64_t)T * cluster > resident && V <= cluster * 6144) cluster /= 2;
+  while (cluster > 1 && (int64_t)T * cluster > 4 * resident && 2 * bytes <= (int64_t)cluster * 81920) cluster /= 2;
   if ((int64_t)T * cluster > INT32_MAX) return PMOE_EINVAL;
   SampleArgs a{logits, T, V, row_stride, temperature, top_k, top_p, min_p, u, ids_out, logprob_out, 0};
   // 7: the most elements by which a row can start after its first 16-byte vector

@@ -170,3 +170,21 @@ def test_sampling_refusals(pm):
         pm.moe_sample_tokens(torch.zeros((2, 262145), device="cuda"), u)
     assert e.value.status == pm.PMOE_EINVAL
     assert pm.moe_sample_tokens(torch.zeros((0, 8), device="cuda"), u[:0]).numel() == 0
+
+
+@pytest.mark.parametrize("T,V,bf16", [(640, 40000, True), (400, 17001, False), (320, 39999, False), (64, 131072, True)])
+def test_rows_do_not_depend_on_the_batch(pm, T, V, bf16):
+    """How many CTAs take a row depends on the rows and their length; what is drawn does not."""
+    rng = np.random.default_rng(T)
+    x = torch.from_numpy(rng.standard_normal((T, V)).astype(np.float32) * 2.5).cuda()
+    x = x.to(torch.bfloat16) if bf16 else x
+    u = torch.from_numpy(rng.random(T).astype(np.float32)).cuda()
+    dev = lambda v, dt: torch.from_numpy(np.asarray(v).astype(dt)).cuda()  # noqa: E731
+    args = dict(temperature=dev(rng.choice([0.0, 0.6, 1.0], T), np.float32), top_k=dev(rng.choice([0, 20, 1000, 2000], T), np.int32),
+                top_p=dev(rng.choice([1.0, 0.95, 0.8], T), np.float32), min_p=dev(rng.choice([0.0, 0.0, 0.05], T), np.float32))
+    lp = torch.empty(T, device="cuda")
+    ids = pm.moe_sample_tokens(x, u, logprob_out=lp, **args)
+    for i in range(0, T, 8):
+        few = torch.empty(8, device="cuda")
+        got = pm.moe_sample_tokens(x[i:i + 8], u[i:i + 8], logprob_out=few, **{k: v[i:i + 8] for k, v in args.items()})
+        assert torch.equal(got, ids[i:i + 8]) and torch.equal(few, lp[i:i + 8])
