@@ -392,26 +392,33 @@ __device__ void compare_and_draw(Shared& sh, const SampleArgs& a, const Row& rw,
   }
 }
 
-// Of the block's elements c (kEach a thread, ~0 for none; ascending order), finds the one at
-// which the running count (BY_COUNT) or weight reaches `target`, into sh.sel; the running
-// weight up to it goes to sh.sel_upto if `weigh`, or always without BY_COUNT. `bin` maps an
-// element to 0 .. kBins - 1 without disturbing the order, `weight` to its weight. One histogram
-// finds the bin, comparing all pairs inside it the element; a bin of more than kPairs elements
-// is sorted instead. sh.level and sh.members are zero on entry and on return.
-template <bool BY_COUNT, class Bin, class Weight>
-__device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool weigh, u64 target) {
+__device__ __forceinline__ float logit_of(u64 x) { return of_key(~(uint32_t)(x >> 32)); }
+
+// kEach elements of a thread, ~0 for none; their bins, which keep their order, and weights.
+struct Elements {
+  u64 c[kEach];
+  int bin[kEach];
+  uint32_t w[kEach];
+};
+
+// Of the block's elements, in ascending order, finds the one at which the running count
+// (by_count) or weight reaches `target`, into sh.sel; the running weight up to it goes to
+// sh.sel_upto if `weigh` (set without by_count). by_id: elements are id << 32 | weight, not
+// ~key << 32 | id. One histogram finds the bin, comparing all
+// pairs inside it the element; a bin of more than kPairs elements is sorted instead. sh.level
+// and sh.members are zero on entry and on return.
+__device__ void select(Shared& sh, const Row rw, const Elements& x, bool by_count, bool weigh, bool by_id,
+                                    u64 target) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* weights = reinterpret_cast<uint32_t*>(sh.merged + kPairs);
-  weigh |= !BY_COUNT;
 #pragma unroll
   for (int e = 0; e < kEach; ++e)
-    if (c[e] != ~0ull) {
-      const int b = bin(c[e]);
-      if (BY_COUNT) atomicAdd(&sh.level.cnt[b], 1u);
+    if (x.c[e] != ~0ull) {
+      const int b = x.bin[e];
+      if (by_count) atomicAdd(&sh.level.cnt[b], 1u);
       if (weigh) {
-        const uint32_t w = weight(c[e]);
-        atomicAdd(&sh.level.lo[b], w & 0xffffu);
-        atomicAdd(&sh.level.hi[b], w >> 16);
+        atomicAdd(&sh.level.lo[b], x.w[e] & 0xffffu);
+        atomicAdd(&sh.level.hi[b], x.w[e] >> 16);
       }
     }
   __syncthreads();
@@ -419,7 +426,7 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
   const u64 own_w = ((u64)sh.level.hi[tid] << 16) + sh.level.lo[tid];
   uint32_t ci = own_c;
   u64 wi = own_w;
-  if (BY_COUNT) {
+  if (by_count) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t d = __shfl_up_sync(0xffffffffu, ci, o);
@@ -433,115 +440,120 @@ __device__ void select(Shared& sh, u64 (&c)[kEach], Bin bin, Weight weight, bool
   }
   __syncthreads();
   sh.level.cnt[tid] = sh.level.lo[tid] = sh.level.hi[tid] = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i)
-    if (i < warp) {
-      if (BY_COUNT) ci += sh.scan_cnt[i];
-      if (weigh) wi += sh.scan[i];
-    }
-  if (BY_COUNT ? (ci >= target && ci - own_c < target) : (wi >= target && wi - own_w < target)) {
+#pragma unroll 4
+  for (int i = 0; i < warp; ++i) {
+    if (by_count) ci += sh.scan_cnt[i];
+    if (weigh) wi += sh.scan[i];
+  }
+  if (by_count ? (ci >= target && ci - own_c < target) : (wi >= target && wi - own_w < target)) {
     sh.pick = Pick{wi - own_w, ci - own_c, tid};
   }
   __syncthreads();
   const int pick = sh.pick.bin;
 #pragma unroll
   for (int e = 0; e < kEach; ++e)
-    if (c[e] != ~0ull && bin(c[e]) == pick) {
+    if (x.c[e] != ~0ull && x.bin[e] == pick) {
       const int at = atomicAdd(&sh.members, 1);
-      if (at < kPairs) sh.merged[at] = c[e], weights[at] = weight(c[e]);
+      if (at < kPairs) sh.merged[at] = x.c[e], weights[at] = x.w[e];
     }
   __syncthreads();
   const int m = sh.members;
   if (m <= kPairs) {
     const int n2 = pow2_above(m), G = kThreads / n2, i = tid / G, part = tid % G;
-    const u64 x = i < m ? sh.merged[i] : ~0ull;
+    const u64 one = i < m ? sh.merged[i] : ~0ull;
     u64 place, before, unused;
-    count_below<true>(sh.merged, weights, m, x, part, G, &place, &before, &unused);
+    count_below<true>(sh.merged, weights, m, one, part, G, &place, &before, &unused);
     place += sh.pick.cnt;
     before += sh.pick.above;
     const uint32_t w = i < m ? weights[i] : 0;
-    if (part == 0 && i < m && (BY_COUNT ? place + 1 == target : before < target && target <= before + w)) {
-      sh.sel = x;
+    if (part == 0 && i < m && (by_count ? place + 1 == target : before < target && target <= before + w)) {
+      sh.sel = one;
       sh.sel_upto = before + w;
     }
     __syncthreads();
     if (tid == 0) sh.members = 0;
     return;
   }
-  // every element of this or another bin may be sorted along; the caller keeps its own
+  // every element is sorted, those of other bins too
   u64 s[kEach];
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) sh.merged[tid * kEach + e] = c[e];
+  for (int e = 0; e < kEach; ++e) sh.merged[tid * kEach + e] = x.c[e];
   __syncthreads();
   sort_up(sh.merged, s);
+  uint32_t ws[kEach];
   u64 mine = 0;
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) mine += s[e] != ~0ull ? weight(s[e]) : 0;
+  for (int e = 0; e < kEach; ++e) {
+    ws[e] = s[e] == ~0ull ? 0 : by_id ? (uint32_t)s[e] : rw.units_of(logit_of(s[e]));
+    mine += ws[e];
+  }
   u64 total, run = block_scan(sh, mine, &total) - mine;
   if (tid == 0) sh.members = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const uint32_t w = s[e] != ~0ull ? weight(s[e]) : 0;
-    if (s[e] != ~0ull && (BY_COUNT ? (u64)(tid * kEach + e) + 1 == target : run < target && target <= run + w)) {
+    if (s[e] != ~0ull && (by_count ? (u64)(tid * kEach + e) + 1 == target : run < target && target <= run + ws[e])) {
       sh.sel = s[e];
-      sh.sel_upto = run + w;
+      sh.sel_upto = run + ws[e];
     }
-    run += w;
+    run += ws[e];
   }
   __syncthreads();
 }
 
-// sh.merged's n elements to registers, kEach a thread, and sh.level cleared; ends with a barrier.
-__device__ void take_merged(Shared& sh, int n, u64 (&c)[kEach]) {
+// sh.merged's n elements to registers, and sh.level cleared; ends with a barrier.
+__device__ __forceinline__ void take_merged(Shared& sh, int n, Elements& x) {
   sh.level.cnt[threadIdx.x] = sh.level.lo[threadIdx.x] = sh.level.hi[threadIdx.x] = 0;
   if (threadIdx.x == 0) sh.members = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int i = e * kThreads + threadIdx.x;
-    c[e] = i < n ? sh.merged[i] : ~0ull;
+    x.c[e] = i < n ? sh.merged[i] : ~0ull;
   }
   __syncthreads();
 }
 
 // The same for more candidates: the cuts and the draw are selections.
-__device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, int row, int n, int top_k, bool use_k,
-                                float top_p, bool use_p, float min_p, float uu, u64 all_weights) {
-  u64 c[kEach];
-  take_merged(sh, n, c);
-  const auto logit = [](u64 x) { return of_key(~(uint32_t)(x >> 32)); };
-  const auto by_logit = [&](u64 x) { return rw.bin(logit(x)); };
-  const auto weight = [&](u64 x) { return rw.units_of(logit(x)); };
+__device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row rw, int row, int n, int top_k,
+                                             bool use_k, float top_p, bool use_p, float min_p, float uu, u64 all_weights) {
+  Elements x;
+  take_merged(sh, n, x);
+  u64 mine = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const float logit = logit_of(x.c[e]);
+    x.bin[e] = rw.bin(logit);
+    x.w[e] = x.c[e] == ~0ull ? 0 : rw.units_of(logit);
+    mine += x.w[e];
+  }
   u64 last = ~0ull - 1, total = all_weights;  // the last candidate that is kept
   if (use_k) {
     if (n > top_k) {
-      select<true>(sh, c, by_logit, weight, use_p, (u64)top_k);
+      select(sh, rw, x, true, use_p, false, (u64)top_k);
       last = sh.sel, total = sh.sel_upto;
     } else {
-      u64 mine = 0;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) mine += c[e] != ~0ull ? weight(c[e]) : 0;
       block_scan(sh, mine, &total);
     }
   }
   if (use_p) {
-    select<false>(sh, c, by_logit, weight, true, least_weight(total, top_p));
+    select(sh, rw, x, false, true, false, least_weight(total, top_p));
     last = min(last, sh.sel);
   }
   // in the order of the ids: id << 32 | weight
-  u64 mine = 0;
+  const float bins_per_id = (float)kBins / (float)a.V;
+  mine = 0;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const float wt = c[e] <= last ? rw.weight(logit(c[e])) : 0.f;
-    const uint32_t w = wt < min_p ? 0 : Row::units(wt);
-    c[e] = w > 0 ? (c[e] << 32) | w : ~0ull;
+    const bool cut = x.c[e] > last || rw.weight(logit_of(x.c[e])) < min_p;
+    const uint32_t w = cut ? 0 : x.w[e], id = (uint32_t)x.c[e];
+    x.c[e] = w > 0 ? ((u64)id << 32) | w : ~0ull;
+    x.w[e] = w;
+    x.bin[e] = min((int)((float)id * bins_per_id), kBins - 1);
     mine += w;
   }
   u64 S;
   block_scan(sh, mine, &S);
-  const u64 target = share_of(S, uu);
-  select<false>(sh, c, [&](u64 x) { return (int)((x >> 32) * kBins / (uint32_t)a.V); }, [](u64 x) { return (uint32_t)x; },
-                true, target + 1);
+  select(sh, rw, x, false, true, true, share_of(S, uu) + 1);
   if (threadIdx.x == 0) {
     a.ids[row] = (int32_t)(sh.sel >> 32);
     if (a.logprob != nullptr) a.logprob[row] = logf((float)(uint32_t)sh.sel / (float)S);
@@ -550,27 +562,24 @@ __device__ void select_and_draw(Shared& sh, const SampleArgs& a, const Row& rw, 
 
 // Step 3's end, in the row's first CTA: sh.merged holds the n logits of bin `bin`; the one at
 // which their running count (by_count) or weight reaches `target` is the threshold.
-__device__ void find_in_bin(Shared& sh, const Row& rw, int n, int bin, bool by_count, u64 target, u64 above) {
+__device__ void find_in_bin(Shared& sh, const Row rw, int n, int bin, bool by_count, u64 target, u64 above) {
   const int tid = threadIdx.x;
-  u64 c[kEach];
-  take_merged(sh, n, c);
-  const auto logit = [](u64 x) { return of_key(~(uint32_t)(x >> 32)); };
-  // the bin, cut into kBins again (the last one reaches to -inf)
-  const auto inner = [&](u64 x) {
-    const float d = ((rw.m - logit(x)) * kBinsPerUnit - (float)bin) * (float)kBins;
-    return d < (float)(kBins - 1) ? max((int)d, 0) : kBins - 1;
-  };
-  const auto weight = [&](u64 x) { return rw.units_of(logit(x)); };
-  if (by_count)
-    select<true>(sh, c, inner, weight, true, target);
-  else
-    select<false>(sh, c, inner, weight, true, target);
+  Elements x;
+  take_merged(sh, n, x);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    // the bin, cut into kBins again (the last one reaches to -inf)
+    const float logit = logit_of(x.c[e]), d = (rw.distance(logit) - (float)bin) * (float)kBins;
+    x.bin[e] = d < (float)(kBins - 1) ? max((int)d, 0) : kBins - 1;
+    x.w[e] = rw.units_of(logit);
+  }
+  select(sh, rw, x, by_count, true, false, target);
   if (tid == 0) sh.thr.ties = 0;
   const u64 sel = sh.sel;
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < kEach; ++e)
-    if (c[e] <= sel && c[e] >> 32 == sel >> 32) atomicAdd(&sh.thr.ties, 1u);
+    if (x.c[e] <= sel && x.c[e] >> 32 == sel >> 32) atomicAdd(&sh.thr.ties, 1u);
   if (tid == 0) sh.thr.key = ~(uint32_t)(sel >> 32), sh.thr.total = above + sh.sel_upto;
   __syncthreads();
 }
