@@ -17,8 +17,15 @@
 // same quotient; weights up to 2^8 are far from overflow), so the accumulators in TMEM are
 // rarely rescaled. Sums are fp32 of the unrounded weights.
 //
-// Work is split into equal runs of (group, key tile) units, one run per SM: a group's parts
-// are joined by the combine kernel.
+// Work is split into equal runs of (group, key tile) units, one run per CTA and at most one CTA
+// an SM: a group's parts are joined by the combine kernel.
+//
+// Bound: the tensor cores, and beside them the softmax: a tile of 256 rows x 128 keys costs the
+// MMAs 1.4 us at the measured peak and the exponentials of its 32,768 scores 1.1 us at 16 a
+// cycle, and each query tile's weights have to be back before its own second product. Measured
+// with 256 rows of 32 heads on 32,768 keys (4 kv heads of 128): 103-106 us, 1,300-1,335 TFLOP/s,
+// 0.69-0.71 of a large matrix product; heads of 64 76 us; e4m3 152 and 87 us, where the
+// conversion to fp16 sets the pace. Few rows are bound by a run's start and end, 9 us.
 #include "attn.cuh"
 #include "tc_gemm.h"
 #include "tc_ptx.cuh"

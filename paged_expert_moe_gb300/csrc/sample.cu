@@ -19,6 +19,11 @@
 //   4. Sums of the kept tokens in id order (ties of the threshold in id order), the segment
 //      that holds floor(S * u), and its token.
 // Uncut rows take steps 1 and 4.
+//
+// Measured: a row of 32,000 fp32 logits with top_k 50 and top_p 0.9 7.3 us, uncut 5.1; 64 bf16
+// rows of 131,072 of all kinds 29.6 us; 256 fp32 rows of 160,001 104 us, 1.6 TB/s, where a read
+// alone would take 24. What holds them up is the chain of a row: its some ten exchanges between
+// the CTAs and passes of a few hundred cycles each, on the 36 clusters that find room at once.
 #include "pmoe_internal.h"
 
 #include <cooperative_groups.h>
@@ -404,11 +409,10 @@ struct Elements {
 // Of the block's elements, in ascending order, finds the one at which the running count
 // (by_count) or weight reaches `target`, into sh.sel; the running weight up to it goes to
 // sh.sel_upto if `weigh` (set without by_count). by_id: elements are id << 32 | weight, not
-// ~key << 32 | id. One histogram finds the bin, comparing all
-// pairs inside it the element; a bin of more than kPairs elements is sorted instead. sh.level
-// and sh.members are zero on entry and on return.
-__device__ void select(Shared& sh, const Row rw, const Elements& x, bool by_count, bool weigh, bool by_id,
-                                    u64 target) {
+// ~key << 32 | id. One histogram finds the bin, comparing all pairs inside it the element; a bin
+// of more than kPairs elements is sorted instead. sh.level and sh.members are zero on entry and
+// on return.
+__device__ void select(Shared& sh, const Row rw, const Elements& x, bool by_count, bool weigh, bool by_id, u64 target) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* weights = reinterpret_cast<uint32_t*>(sh.merged + kPairs);
 #pragma unroll
