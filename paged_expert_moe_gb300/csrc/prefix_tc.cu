@@ -20,12 +20,13 @@
 // Work is split into equal runs of (group, key tile) units, one run per CTA and at most one CTA
 // an SM: a group's parts are joined by the combine kernel.
 //
-// Bound: the tensor cores, and beside them the softmax: a tile of 256 rows x 128 keys costs the
-// MMAs 1.4 us at the measured peak and the exponentials of its 32,768 scores 1.1 us at 16 a
-// cycle, and each query tile's weights have to be back before its own second product. Measured
-// with 256 rows of 32 heads on 32,768 keys (4 kv heads of 128): 103-106 us, 1,300-1,335 TFLOP/s,
-// 0.69-0.71 of a large matrix product; heads of 64 76 us; e4m3 152 and 87 us, where the
-// conversion to fp16 sets the pace. Few rows are bound by a run's start and end, 9 us.
+// Bound: the tensor cores. Of the 3,050 cycles of a tile (256 rows x 128 keys, heads of 128) the
+// issuing warp spends 2,270 handing over its 32 MMAs, which run no faster, 480 until it sees
+// the next K and V, 370 until it sees P; the softmax of a query tile takes 1,370, under the other
+// one's products. Measured with 256 rows of 32 heads on 32,768 keys (4 kv heads of 128): 103-106
+// us, 1,300-1,335 TFLOP/s, 0.69-0.71 of a large matrix product; heads of 64 76 us (an MMA of 64
+// columns takes as long as one of 128); e4m3 152 and 87 us, where K and V wait for their
+// conversion to fp16. Few rows are bound by a run's start and end, 9 us.
 #include "attn.cuh"
 #include "tc_gemm.h"
 #include "tc_ptx.cuh"
