@@ -5,17 +5,18 @@
 //
 // Bound: HBM for many rows (each logit read once), the chain of dependent steps for few. A
 // cluster of up to 8 CTAs takes a row; each CTA keeps its slice in shared memory and the
-// CTAs exchange statistics through distributed shared memory.
-//   1. Load the slice; its largest logit, and each thread's. For rows that are cut by top-k
-//      or top-p a lower bound of the K-th largest logit (K = top_k, or 384): with K / CTAs
-//      of the threads' largest logits at or above a bound in every CTA, K logits are at or
-//      above the least of these bounds, and seldom many more.
+// CTAs exchange statistics through distributed shared memory, written to where they are read.
+//   1. Load the slice; its largest logit, and those of its threads. For rows that are cut by
+//      top-k or top-p a lower bound of the K-th largest logit (K = top_k, or 1,024): with K /
+//      CTAs of the threads' largest logits at or above a bound in every CTA, K logits are at
+//      or above the least of these bounds, and seldom many more.
 //   2. These candidates go to the row's first CTA, which orders them, cuts them and draws.
 //      Rows with more than 2,048 candidates, or whose candidates do not reach top_p, go on
 //      with step 3.
-//   3. A histogram of all logits by distance from the largest, count and weight; the bin that holds
-//      the top_k-th token or in which the weight reaches top_p. Its logits (again up to
-//      2,048; else four passes over 8 bits of the ordered logit) give the threshold itself.
+//   3. A histogram of the logits by distance from the largest, count and weight, without those
+//      that weigh too little to be at the top-p threshold; the bin that holds the top_k-th token
+//      or in which the weight reaches top_p. Its logits (again up to 2,048; else four passes
+//      over 8 bits of the ordered logit) give the threshold itself.
 //   4. Sums of the kept tokens in id order (ties of the threshold in id order), the segment
 //      that holds floor(S * u), and its token.
 // Uncut rows take steps 1 and 4.
@@ -44,10 +45,14 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxSmem = (kMaxVocab / kMaxCluster + 8) * 4;
 constexpr int kMerged = 2048;       // candidates of a row
-constexpr int kMaxK = 1200;         // top_k up to which rows are cut by their candidates
-constexpr int kCutP = 384;          // K for rows that only top-p cuts
+// Candidates: more of them decide more rows, but a list that overflows costs a pass for nothing.
+// top_k up to which rows are cut by theirs (16 rows of 131,072 with top_k 1,000 12.8 us, 25.2 by
+// step 3; 40 rows of 32,000 with 1,300 23.5 and 19.9), and, where only top-p cuts, K as a share
+// of each CTA (64 rows of 131,072 with top_p 0.8 37.9 us with 48, 26.9 with 128; 40 rows of
+// 32,000 11.9, 12.4, and 17.4 with 150).
+constexpr int kMaxK = 1200;
+constexpr int kCutP = 128;
 constexpr int kPairs = 256;         // elements up to which all pairs are compared
-constexpr int kGroups = 128;        // groups of 4 threads, whose largest logits give a bound
 constexpr int kSegs = kMaxCluster * kWarps;
 
 typedef unsigned long long u64;
@@ -93,7 +98,6 @@ struct alignas(16) Shared {
   float best[kMaxCluster], bound[kMaxCluster];  // every CTA's largest logit, its bound of the K-th
   uint32_t bound_key;
   float top[kWarps];
-  alignas(16) float group_top[kGroups];
   Threshold thr;
   int members;            // select: elements of the bin it looks into
   u64 sel, sel_upto;      // and what it found
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   }
   sh.hist.cnt[tid] = 0;
-  if (tid == 0) sh.bound_key = 0, sh.arg = INT_MAX, sh.listed = 0, sh.sum = 0, sh.list_sum = 0;
+  if (tid == 0) sh.arg = INT_MAX, sh.listed = 0, sh.sum = 0, sh.list_sum = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");
   float mine = -INFINITY;  // of the vectors this thread loaded; fmaxf leaves NaN out
   for (int i = tid; i < nv; i += kThreads) {
@@ -655,34 +659,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (lane == 0) sh.top[warp] = best;
   const bool use_k = top_k > 0 && top_k < a.V, use_p = top_p < 1.f;
   const bool listing = temp > 0.f && (use_k ? top_k <= kMaxK : use_p);
-  const uint32_t want = ((use_k ? top_k : kCutP) + nb - 1) / nb;  // of a CTA, if `listing`
-  const bool few = want <= kGroups * 2 / 3;
-  if (listing && few) {
-    float g = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
-    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((lane & 3) == 0) sh.group_top[tid >> 2] = g;
-  }
+  const uint32_t want = use_k ? (top_k + nb - 1) / nb : kCutP;  // of a CTA, if `listing`
   __syncthreads();
   best = sh.top[lane % kWarps];
 #pragma unroll
   for (int o = kWarps / 2; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
   const float cta_best = best;
-  float bound = -FLT_MAX;  // too few groups with a logit: every logit is a candidate
-  if (listing && few) {
-    // the want-th largest of the groups' largest: a warp ranks 8 of them
-    const float4 v = reinterpret_cast<const float4*>(sh.group_top)[lane];
-    float found = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kGroups / kWarps; ++i) {
-      const float x = sh.group_top[warp * (kGroups / kWarps) + i];
-      const int rank_x = __popc(__ballot_sync(0xffffffffu, v.x >= x)) + __popc(__ballot_sync(0xffffffffu, v.y >= x)) +
-                         __popc(__ballot_sync(0xffffffffu, v.z >= x)) + __popc(__ballot_sync(0xffffffffu, v.w >= x));
-      if (rank_x >= (int)want) found = fmaxf(found, x);
-    }
-    if (lane == 0 && found > -INFINITY) atomicMax(&sh.bound_key, key_of(found));
-    __syncthreads();
-    if (sh.bound_key != 0) bound = of_key(sh.bound_key);
-  } else if (listing) {
+  float bound = -FLT_MAX;  // fewer threads with a logit than that: every logit is a candidate
+  if (listing) {
     // the bin of the threads' largest logits, by distance from the CTA's, that holds the
     // want-th; the bound is the least of those in it or above it
     const int mybin = Row{best, 1.f}.bin(mine);
