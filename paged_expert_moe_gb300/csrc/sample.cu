@@ -910,6 +910,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
       for (int q = 0; q < N; ++q) sum += w[q];
     }
+  } else if (!(min_p > 0.f)) {
+    for (int i = s0 + lane; i < s1; i += 32) {
+      const V x(xs[i]);
+      uint32_t w[N];
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        w[q] = rw.units_of(x.f[q]);
+        nt += x.f[q] == x_t;
+      }
+#pragma unroll
+      for (int q = 0; q < N; ++q) sum += x.f[q] > x_t ? w[q] : 0u;
+    }
   } else {
     // a vector whose elements are all cut needs no weights: none above the threshold, or all
     // safely below min_p (by more than its logarithm and the weights can be off)
