@@ -165,16 +165,19 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; what it flush
 }
 
 struct Row {
-  float m, r;  // largest logit, log2(e) / temperature
+  float m, r;  // largest logit, log2(e) / temperature; both finite but for rows with +inf
+  // With a largest logit of +inf, r is too: +inf weighs the most there is, everything else 0.
+  __device__ __forceinline__ Row(float best, float temp)
+      : m(fminf(best, FLT_MAX)), r(best == INFINITY ? INFINITY : fminf(1.44269504f / temp, FLT_MAX)) {}
   // log2 of a weight: four roundings of an argument of at most 31, where the weight is not 0,
   // change the weight by less than 2^-17 of it.
-  __device__ __forceinline__ float log2w(float x) const { return x == m ? 0.f : (x - m) * r; }
+  __device__ __forceinline__ float log2w(float x) const { return (x - m) * r; }
   __device__ __forceinline__ float weight(float x) const { return exp2_approx(log2w(x)); }
   // NaN gives 0, as -inf does
   __device__ __forceinline__ static uint32_t units(float w) { return (uint32_t)(w * 2147483648.f); }
   __device__ __forceinline__ uint32_t units_of(float x) const { return units(weight(x)); }
   // Distance from the largest in bins; with an infinite largest one it is below 0.
-  __device__ __forceinline__ float distance(float x) const { return (fminf(m, FLT_MAX) - x) * kBinsPerUnit; }
+  __device__ __forceinline__ float distance(float x) const { return (m - x) * kBinsPerUnit; }
   __device__ __forceinline__ int bin(float x) const {
     const float d = distance(x);
     return d < (float)(kBins - 1) ? (int)(uint32_t)d : kBins - 1;  // the conversion takes d < 0 to 0
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (listing) {
     // the bin of the threads' largest logits, by distance from the CTA's, that holds the
     // want-th; the bound is the least of those in it or above it
-    const int mybin = Row{best, 1.f}.bin(mine);
+    const int mybin = Row(best, 1.f).bin(mine);
     if (mine > -INFINITY) atomicAdd(&sh.hist.cnt[mybin], 1u);
     if (tid == 0) sh.pick.bin = kBins, sh.bound_key = 0xffffffffu;
     __syncthreads();
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (i < nb) best = fmaxf(best, sh.best[i]), bound = fminf(bound, sh.bound[i]);
   Shared* const head = cluster.map_shared_rank(&sh, 0);  // the row's first CTA
 
-  const Row rw{best, 1.44269504f / temp};
+  const Row rw(best, temp);
   if (best == -INFINITY || !(temp > 0.f)) {  // the same for every CTA of the row
     if (best != -INFINITY && cta_best == best) {
       int low = INT_MAX;
@@ -923,20 +926,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       for (int q = 0; q < N; ++q) sum += x.f[q] > x_t ? w[q] : 0u;
     }
   } else {
-    // a vector whose elements are all cut needs no weights: none above the threshold, or all
-    // safely below min_p (by more than its logarithm and the weights can be off)
-    const float z_cut = min_p > 0.f ? log2f(min_p) - 0.01f : -INFINITY;
+    // A vector whose elements are all cut needs no weights: none at or above the threshold, or
+    // all safely below min_p (by more than its logarithm, the weights and x_lo can be off).
+    const float x_lo = fmaxf(x_t, rw.m + (log2f(min_p) - 0.01f) / rw.r - fabsf(rw.m) * 2.4e-7f);
     for (int i = s0 + lane; i < s1; i += 32) {
       const V x(xs[i]);
-      bool any = false;
+      float top = x.f[0];
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        any |= x.f[q] > x_t && rw.log2w(x.f[q]) > z_cut;
-        nt += x.f[q] == x_t;  // -inf where nothing is cut: tie_ok is false then
-      }
-      if (any) {
+      for (int q = 1; q < N; ++q) top = fmaxf(top, x.f[q]);
+      if (top >= x_lo) {
 #pragma unroll
-        for (int q = 0; q < N; ++q) sum += kept(x.f[q]);
+        for (int q = 0; q < N; ++q) {
+          nt += x.f[q] == x_t;
+          sum += kept(x.f[q]);
+        }
       }
     }
   }
