@@ -9,9 +9,9 @@
 // TMEM, weights back to TMEM in their place as the 16-bit A operand of the second product.
 // Warp 8 issues the MMAs, in the order O0 += P0 V, S0 of the next tile, O1 += P1 V, S1 of
 // the next tile, so that one query tile's softmax runs under the other's products. Warp 9
-// loads K and V tiles by TMA, one box a page and 64 columns, into a ring of five 128-key
-// tiles; with an e4m3 cache warps 12-15 read them, convert to fp16 (exact) and write the
-// same layout.
+// loads K and V tiles by TMA, one box a page and 64 columns, into a ring of 128-key tiles (five
+// of heads of 128, eight of 64); the bytes of an e4m3 cache land beside, and warps 12-15 convert
+// them to fp16 (exact) into the same layout.
 //
 // The running maximum of a row moves only when a score exceeds it by 2^8 (any base gives the
 // same quotient; weights up to 2^8 are far from overflow), so the accumulators in TMEM are
@@ -25,8 +25,8 @@
 // the next K and V, 370 until it sees P; the softmax of a query tile takes 1,370, under the other
 // one's products. Measured with 256 rows of 32 heads on 32,768 keys (4 kv heads of 128): 103-106
 // us, 1,300-1,335 TFLOP/s, 0.69-0.71 of a large matrix product; heads of 64 76 us (an MMA of 64
-// columns takes as long as one of 128); e4m3 152 and 87 us, where K and V wait for their
-// conversion to fp16. Few rows are bound by a run's start and end, 9 us.
+// columns takes as long as one of 128); e4m3 113 and 84 us (152 and 87 when the converting warps
+// read the cache themselves, a tile ahead in registers: too little in flight). Few rows are bound by a run's start and end, 9 us.
 #include "attn.cuh"
 #include "tc_gemm.h"
 #include "tc_ptx.cuh"
@@ -47,10 +47,17 @@ struct TcCfg {
   static constexpr int kThreads = F8 ? 512 : 384;         // whole warpgroups
   // Registers a thread, by warpgroup: what the other roles give up the softmax takes. The
   // launch has 168 (bf16) or 128 (e4m3) of them for each of its threads.
-  static constexpr int kSoftmaxRegs = F8 ? 168 : 200, kMmaRegs = F8 ? 72 : 104, kLoaderRegs = F8 ? 104 : 0;
+  static constexpr int kSoftmaxRegs = F8 ? 184 : 200, kMmaRegs = F8 ? 72 : 104, kLoaderRegs = F8 ? 72 : 0;
   static_assert(kSoftmaxRegs * 256 + (kMmaRegs + kLoaderRegs) * 128 <= (F8 ? 128 : 168) * kThreads, "register shares");
   static constexpr int kRing = kSlots * kTileBytes;
-  static constexpr int kSmem = kRing + 2 * kQBytes + 1024 /* alignment */ + 1024 /* row factors */ + 512;
+  // e4m3: where TMA puts a tile's bytes for the conversion. Heads of 128: the upper half of the
+  // tile's slot, whose line of row r also takes that row's upper 64 values, so that the warp that
+  // converts a row reads it before it writes. Heads of 64: a ring of their own.
+  static constexpr int kRawBytes = kTcKeys * D, kRawRing = F8 && D == 64 ? kSlots * kRawBytes : 0;
+  static __device__ __forceinline__ uint8_t* raw(uint8_t* smem, uint32_t slot) {
+    return D == 64 ? smem + kRing + slot * kRawBytes : smem + slot * kTileBytes + kRawBytes;
+  }
+  static constexpr int kSmem = kRing + kRawRing + 2 * kQBytes + 1024 /* alignment */ + 1024 /* row factors */ + 512;
   static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
 };
 
@@ -62,7 +69,7 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
 }
 
 struct Bars {
-  uint64_t full[8], empty[8];
+  uint64_t full[8], empty[8], raw[8];
   uint64_t sfull[2], pready[2], odone[2], qfull[2], staged[2], drain;
   uint32_t tmem;
   int abort;
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
   constexpr int kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qs = smem + C::kRing;
+  uint8_t* qs = smem + C::kRing + C::kRawRing;
   float* qmul = reinterpret_cast<float*>(qs + 2 * C::kQBytes);  // [256]
   Bars& b = *reinterpret_cast<Bars*>(qmul + 256);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,6 +142,7 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&b.full[i], F8 ? 4 : 1);
       mbar_init(&b.empty[i], 1);
+      mbar_init(&b.raw[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.sfull[i], 1);
@@ -146,10 +154,8 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     mbar_init(&b.drain, 1);
     b.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (!F8) {
-      prefetch_map(&map_k);
-      prefetch_map(&map_v);
-    }
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
   }
   pdl_wait();     // the cache and q may come from the kernel ahead
   pdl_trigger();  // the stream kernel may take the SMs that this one is done with
@@ -415,9 +421,10 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       }
     }
     __syncwarp();
-    } else if (!F8 && warp == 9) {
-    // ---------------- TMA loader: lane i issues box i % boxes of page box i / halves
-    constexpr int kHalves = D / 64;
+    } else if (warp == 9) {
+    // ---------------- TMA loader: lane i issues box i % halves of page box i / halves
+    constexpr int kHalves = F8 ? 1 : D / 64, kBytes = F8 ? 1 : 2;
+    uint64_t* arrive = F8 ? b.raw : b.full;
     const int box = min(a.kv.page_size, kTcKeys), boxes = kTcKeys / box;
     uint32_t kv = 0;
     bool ok = true;
@@ -440,94 +447,66 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&b.full[slot], used * box * D * 2);
+          if (lane == 0) mbar_arrive_expect_tx(&arrive[slot], used * box * D * kBytes);
           __syncwarp();
+          uint8_t* dst = F8 ? C::raw(smem, slot) + pb * box * D : smem + slot * C::kTileBytes + hf * (kTcKeys * 128) + pb * box * 128;
           if (pb < used)
-            tma_load_4d(smem + slot * C::kTileBytes + hf * (kTcKeys * 128) + pb * box * 128, v ? &map_v : &map_k,
-                        &b.full[slot], hf * 64, key & (a.kv.page_size - 1), sg.h, id);
+            tma_load_4d(dst, v ? &map_v : &map_k, &arrive[slot], hf * 64, key & (a.kv.page_size - 1), sg.h, id);
         }
       }
     }
     // copies in flight land before the CTA leaves, even where another role gave up
     for (uint32_t i = kv > kSlots ? kv - kSlots : 0; i < kv; ++i) {
       const long long t0 = clock64();
-      while (!mbar_try_wait(&b.full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kWaitLimit) {
+      while (!mbar_try_wait(&arrive[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kWaitLimit) {
       }
     }
     }
   } else if constexpr (F8) {
-    // ---------------- e4m3 loaders: 16 codes a thread and step, to fp16
+    // ---------------- e4m3 conversion: 16 codes a thread and step, to fp16
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoaderRegs));
     constexpr int CH = D / 16;  // 16-code chunks of a row
     constexpr int N = kTcKeys * CH / 128;
     const int tid = threadIdx.x - 12 * 32, ch = tid % CH, r0 = tid / CH;
-    // page ids of a tile's rows of this thread, fetched a tile ahead of its values
-    auto fetch_ids = [&](int t, int (&ids)[N]) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int key = t * kTcKeys + r0 + i * (128 / CH);
-        ids[i] = key < a.prefix_len ? __ldg(a.prefix_pages + (key >> psh)) : -2;
-      }
-    };
-    auto fetch = [&](const void* cache, int t, int h, const int (&ids)[N], uint4 (&raw)[N]) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int key = t * kTcKeys + r0 + i * (128 / CH);
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if ((unsigned)ids[i] < (unsigned)a.kv.num_pages)
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(
-              static_cast<const uint8_t*>(cache) + (int64_t)ids[i] * a.kv.page_stride +
-              ((int64_t)h * a.kv.page_size + (key & (a.kv.page_size - 1))) * D + ch * 16));
-        else if (ids[i] != -2 && a.err != nullptr)
-          atomicOr(a.err, kErrBadPage);
-      }
-    };
     uint32_t kv = 0;
     bool ok = true;
-    auto put = [&](const uint4 (&raw)[N]) {  // the tile to the ring
-      const uint32_t slot = kv % kSlots;
-      if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) {
-        ok = false;
-        return;
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int r = r0 + i * (128 / CH);
-        uint8_t* dst = smem + slot * C::kTileBytes + (ch / 4) * (kTcKeys * 128) + r * 128;
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t f[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f[2 * k] = e4m3x2(w[k] & 0xffffu), f[2 * k + 1] = e4m3x2(w[k] >> 16);
-        // 8 threads hold a row of 128: the upper four write their halves the other way
-        // round, so that the two 64-value blocks meet on different banks
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int kk = k ^ (ch / 4 & 1);
-          *reinterpret_cast<uint4*>(dst + (((2 * (ch % 4) + kk) ^ (r & 7)) << 4)) =
-              kk ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
-        }
-      }
-      fence_async();
-      warp_arrive(&b.full[slot]);
-      ++kv;
-    };
     while (ok && segment(a, &u, end, &sg)) {
-      // while one tile is converted, the next one's values are in flight
-      int ids[N], next[N];
-      uint4 rk[N], rv[N];
-      fetch_ids(sg.t0, ids);
-      fetch(a.kv.k, sg.t0, sg.h, ids, rk);
-      fetch(a.kv.v, sg.t0, sg.h, ids, rv);
-      fetch_ids(min(sg.t0 + 1, sg.t1 - 1), next);
-      for (int t = sg.t0; t < sg.t1 && ok; ++t) {
-        put(rk);
-        if (!ok) break;
-        if (t + 1 < sg.t1) fetch(a.kv.k, t + 1, sg.h, next, rk);
-        put(rv);
-        if (t + 1 < sg.t1) {
-          fetch(a.kv.v, t + 1, sg.h, next, rv);
-          fetch_ids(min(t + 2, sg.t1 - 1), next);
+      for (int i2 = 2 * sg.t0; i2 < 2 * sg.t1; ++i2, ++kv) {  // K and V of each tile
+        const uint32_t slot = kv % kSlots;
+        if (!warp_wait(&b.raw[slot], (kv / kSlots) & 1, abort_flag, a.err)) {
+          ok = false;
+          break;
         }
+        const uint8_t* src = C::raw(smem, slot);
+        const int valid = a.prefix_len - i2 / 2 * kTcKeys;
+        uint4 raw[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * (128 / CH);
+          const int at = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+          // values beyond the prefix may be anything, and 0 x NaN is NaN
+          raw[i] = r < valid ? *reinterpret_cast<const uint4*>(src + at) : make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * (128 / CH);
+          uint8_t* dst = smem + slot * C::kTileBytes + (ch / 4) * (kTcKeys * 128) + r * 128;
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[2 * k] = e4m3x2(w[k] & 0xffffu), f[2 * k + 1] = e4m3x2(w[k] >> 16);
+          // 8 threads hold a row of 128: the upper four write their halves the other way
+          // round, so that the two 64-value blocks meet on different banks
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int kk = k ^ (ch / 4 & 1);
+            *reinterpret_cast<uint4*>(dst + (((2 * (ch % 4) + kk) ^ (r & 7)) << 4)) =
+                kk ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
+          }
+        }
+        fence_async();
+        warp_arrive(&b.full[slot]);
       }
     }
   }
@@ -539,24 +518,23 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
 }
 
 int make_map(const Args& a, void* base, CUtensorMap* m) {
-  const uint64_t D = a.kv.head_dim, page = a.kv.page_size;
+  const bool f8 = a.kv.dtype == PMOE_KV_E4M3;
+  const uint64_t D = a.kv.head_dim, page = a.kv.page_size, eb = f8 ? 1 : 2;
   const uint64_t dims[4] = {D, page, (uint64_t)a.kv.kv_heads, (uint64_t)a.kv.num_pages};
-  const uint64_t strides[3] = {D * 2, page * D * 2, (uint64_t)a.kv.page_stride * 2};
-  const uint32_t box[4] = {64, (uint32_t)std::min<uint64_t>(page, kTcKeys), 1, 1};
-  return tc_encode_map(m, base, 4, dims, strides, box, kTcMapBf16Sw128);
+  const uint64_t strides[3] = {D * eb, page * D * eb, (uint64_t)a.kv.page_stride * eb};
+  const uint32_t box[4] = {f8 ? (uint32_t)D : 64u, (uint32_t)std::min<uint64_t>(page, kTcKeys), 1, 1};
+  return tc_encode_map(m, base, 4, dims, strides, box, !f8 ? kTcMapBf16Sw128 : D == 128 ? kTcMapBytesSw128 : kTcMapBytesSw64);
 }
 
 template <int D, bool F8>
 int launch(const Args& a, cudaStream_t s) {
   using C = TcCfg<D, F8>;
-  CUtensorMap mk{}, mv{};
-  if (!F8) {
-    int r = make_map(a, a.kv.k, &mk);
-    if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
-    if (r != PMOE_OK) return r;
-  }
+  CUtensorMap mk, mv;
   static SmemLimit limit;
-  const int r = limit.set(reinterpret_cast<const void*>(prefix_tc_kernel<D, F8>), C::kSmem, "moe_prefix_attention");
+  int r = make_map(a, a.kv.k, &mk);
+  if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
+  if (r != PMOE_OK) return r;
+  r = limit.set(reinterpret_cast<const void*>(prefix_tc_kernel<D, F8>), C::kSmem, "moe_prefix_attention");
   if (r != PMOE_OK) return r;
   return pmoe::launch("moe_prefix_attention", prefix_tc_kernel<D, F8>, a.tc_ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, a);
 }
@@ -564,13 +542,13 @@ int launch(const Args& a, cudaStream_t s) {
 }  // namespace
 
 // What the prefix takes on at most `ctas` CTAs, in us, and how many it then uses: 9 for a run,
-// 1.9 a tile of heads of 128 (1.4 of 64; 2.8 and 1.6 with e4m3) and 5.5 where a run crosses
+// 1.9 a tile of heads of 128 (1.4 of 64; 2.1 and 1.5 with e4m3) and 5.5 where a run crosses
 // from one group into the next (query rows to load, a part to write). Runs that divide the
 // groups evenly do not, and more runs than the tiles need only leave more parts: 64 rows on
 // 8,192 keys take 20.9 us with 128 CTAs of 4 tiles each, 22.3 with 152 of 3 or 4.
 double prefix_tc_cost(const Args& a, int ctas, int* used) {
   const bool f8 = a.kv.dtype == PMOE_KV_E4M3;
-  const double tile = a.kv.head_dim == 128 ? (f8 ? 2.8 : 1.9) : (f8 ? 1.6 : 1.4);
+  const double tile = a.kv.head_dim == 128 ? (f8 ? 2.1 : 1.9) : (f8 ? 1.5 : 1.4);
   const int64_t units = tc_units(a), groups = units / a.tc_tiles;
   const int64_t run = (units + ctas - 1) / ctas;
   int64_t n = (units + run - 1) / run;
