@@ -217,7 +217,7 @@ def moe_decode_forward_noalloc(experts, stride, E, top_k, H, I, fmt, x, ids, w, 
 
 
 # The calls of a decode step (below) go through _binding, which checks their tensors and calls
-# the library in C: their kernels take a few microseconds, less than the checks in Python.
+# the library in C++: their kernels take a few microseconds, less than the checks in Python.
 
 _BINDING = None
 
@@ -225,16 +225,11 @@ _BINDING = None
 def _binding():
     global _BINDING
     if _BINDING is None:
-        import torch
+        import torch  # noqa: F401  (the binding links to its libraries)
         lib = load()
         from . import _binding as b
-        fns = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-            "moe_kv_append", "moe_prefix_attention", "moe_prefix_attention_scratch_bytes", "moe_sample_tokens")]
-        # scratch comes from torch's caching allocator, by its raw calls (a tensor costs 8 us more)
-        c = torch._C
-        b.setup(tuple(fns), (torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32, torch.uint8),
-                c._cuda_getCurrentRawStream, c._cuda_cudaCachingAllocator_raw_alloc,
-                c._cuda_cudaCachingAllocator_raw_delete)
+        b.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "moe_kv_append", "moe_prefix_attention", "moe_prefix_attention_scratch_bytes", "moe_sample_tokens")))
         _BINDING = b
     return _BINDING
 
@@ -290,8 +285,7 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
         out = _empty(q.shape, q.dtype, q, stream)
     status = (_BINDING or _binding()).prefix_attention(
         k_cache, v_cache, q, prefix_pages, prefix_len, page_table, suffix_len, max_suffix,
-        k_cache.shape[-1] ** -0.5 if scale is None else scale, row_seq, k_scale, v_scale, out, lse_out, scratch, err_out,
-        stream)
+        scale, row_seq, k_scale, v_scale, out, lse_out, scratch, err_out, stream)
     if status:
         raise PmoeError(status, "moe_prefix_attention")
     return out

@@ -1,12 +1,13 @@
 """Builds libpagedmoe.so in-tree from the CUDA sources with nvcc (sm_103a only).
 
 Each translation unit is compiled in parallel, then linked into one shared library
-with a plain C ABI (include/pagedmoe.h); gcc compiles the Python binding of the decode-step
-calls (csrc/binding.c) beside it. Rebuilds only when a source is newer than the libraries.
+with a plain C ABI (include/pagedmoe.h); g++ compiles the Python binding of the decode-step
+calls (csrc/binding.cpp, against torch's headers) beside it. Rebuilds only when a source is newer than the libraries.
 """
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -16,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedmoe.so")
-BINDING_SRC = os.path.join(CSRC, "binding.c")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -52,11 +53,15 @@ def _compile(src, verbose_ptxas=False):
 
 def _compile_binding():
     tmp = BINDING + ".tmp"
-    cmd = ["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
-           BINDING_SRC, "-o", tmp]
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib = os.path.join(torch, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch, "include"), "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           BINDING_SRC, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for {BINDING_SRC}:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stderr}")
     os.replace(tmp, BINDING)
 
 
