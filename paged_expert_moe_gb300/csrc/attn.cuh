@@ -42,7 +42,7 @@ struct Args {
   // The stream kernel: units of one 16-key tile for one (up to 16 query rows, kv head) item;
   // see prefix_attention.cu. pre_tiles: its tiles of the prefix (0: the tensor-core kernel's),
   // pre_items its items.
-  int warps, min_share, pre_tiles, pre_items, head_items;
+  int warps, min_share, pre_tiles, pre_items, head_items, whole;
   int64_t* base;    // [row blocks][kRowBlock + 1] first unit of each row; last: all units
 };
 

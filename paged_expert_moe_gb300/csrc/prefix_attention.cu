@@ -10,7 +10,8 @@
 // one page; one box for K, one for V), mma.sync on 16 query rows, softmax in registers. The
 // (item, tile) units of all items, in order, are cut into equal runs, one a warp of every
 // SM, whatever the lengths; a warp whose run ends inside an item leaves a part of it. An item
-// counts for kHead units more than its tiles: short ones cost more than their keys. Measured: 256
+// counts for kHead units more than its tiles: short ones cost more than their keys. Calls of few
+// and short items take a CTA an item instead, which joins its warps' parts itself. Measured: 256
 // rows of 1..1,024 keys (4 kv heads of 128, bf16) 51 us; 2 rows on 100,003 shared and 256 own
 // keys 44.4 us with the combine, 4.6 TB/s; long suffixes 6.6 TB/s, 0.97 of a copy.
 #include "attn.cuh"
@@ -18,6 +19,7 @@
 #include "tc_ptx.cuh"
 
 #include <algorithm>
+#include <limits.h>
 #include <math.h>
 
 namespace pmoe {
@@ -99,7 +101,9 @@ __device__ __forceinline__ int64_t share_of(const Args& a, int64_t units) {
   return max((int64_t)a.min_share, (units + a.warps - 1) / a.warps);
 }
 
-template <int D, bool F8>
+// WHOLE: a CTA takes all keys of one item, shared and own, its warps a run of tiles each, and
+// writes the output itself.
+template <int D, bool F8, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a,
                   int block) {
@@ -112,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sums + kWarps);
   int32_t* keys = reinterpret_cast<int32_t*>(sums + 64);  // [nrows]
   Unit* notes = reinterpret_cast<Unit*>(keys + kRowBlock);
+  float2* ml = reinterpret_cast<float2*>(base);  // WHOLE, which has no rows to plan: [kWarps][16]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int t0 = block * kRowBlock, nrows = a.max_suffix > 0 ? min(kRowBlock, a.T - t0) : 0;
   const int64_t pre = block == 0 && a.pre_tiles > 0 ? (int64_t)a.pre_items * (a.pre_tiles + kHead) : 0;
@@ -120,61 +125,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.tc_ctas == 0) pdl_wait();
   pdl_trigger();
 
-  // ---- the first unit of every row: thread i sums 8 rows
-  int64_t mine[8], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = tid * 8 + i;
-    const int n = r < nrows ? suffix_keys(a, t0 + r) : 0;
-    if (r < nrows) keys[r] = n;
-    mine[i] = row_units(a, n);
-    sum += mine[i];
-  }
-  int64_t upto = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t d = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += d;
-  }
-  if (lane == 31) sums[warp] = upto;
   if (tid == 0) *abort_flag = 0;
   if (lane == 0) {
     for (int i = 0; i < C::kStages; ++i) mbar_init(&bars[warp * C::kStages + i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (warp == 0) prefetch_map(&map_k), prefetch_map(&map_v);
   }
-  __syncthreads();
-  int64_t at = pre + upto - sum, units = pre;
+  int64_t share = 0, w = 0, u0, u1;  // this warp's run of units; of a whole item: of its tiles
+  Unit mine_item{};                  // WHOLE: the CTA's item, its shared tiles and own keys
+  int shared_tiles = 0, own_keys = 0;
+  if constexpr (WHOLE) {
+    const int rts = a.head_items / a.kv.kv_heads, t = blockIdx.x / a.head_items, item = blockIdx.x - t * a.head_items;
+    mine_item.t = t, mine_item.h = item / rts, mine_item.row0 = (item - mine_item.h * rts) * 16;
+    mine_item.tiles = INT_MAX;  // the run ends it
+    shared_tiles = (a.prefix_len + kTile - 1) / kTile;
+    own_keys = a.max_suffix > 0 ? suffix_keys(a, t) : 0;
+    const int tiles = shared_tiles + (own_keys + kTile - 1) / kTile;
+    share = (tiles + kWarps - 1) / kWarps;
+    u0 = min((int64_t)tiles, warp * share), u1 = min((int64_t)tiles, u0 + share);
+    __syncthreads();
+  } else {
+    // ---- the first unit of every row: thread i sums 8 rows
+    int64_t mine[8], sum = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) at += sums[i];
-    units += sums[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = tid * 8 + i;
-    if (r < nrows) {
-      base[r] = at;
-      if (blockIdx.x == 0) a.base[(int64_t)block * (kRowBlock + 1) + r] = at;  // for the combine kernel
+    for (int i = 0; i < 8; ++i) {
+      const int r = tid * 8 + i;
+      const int n = r < nrows ? suffix_keys(a, t0 + r) : 0;
+      if (r < nrows) keys[r] = n;
+      mine[i] = row_units(a, n);
+      sum += mine[i];
     }
-    at += mine[i];
-  }
-  if (tid == 0) {
-    base[nrows] = units;
-    if (blockIdx.x == 0) a.base[(int64_t)block * (kRowBlock + 1) + nrows] = units;
-  }
-  __syncthreads();
+    int64_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t d = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += d;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int64_t at = pre + upto - sum, units = pre;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) at += sums[i];
+      units += sums[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = tid * 8 + i;
+      if (r < nrows) {
+        base[r] = at;
+        if (blockIdx.x == 0) a.base[(int64_t)block * (kRowBlock + 1) + r] = at;  // for the combine kernel
+      }
+      at += mine[i];
+    }
+    if (tid == 0) {
+      base[nrows] = units;
+      if (blockIdx.x == 0) a.base[(int64_t)block * (kRowBlock + 1) + nrows] = units;
+    }
+    __syncthreads();
 
-  // ---- this warp's run of units; neighbouring runs on different SMs
-  const int64_t share = share_of(a, units);
-  const int64_t w = (int64_t)warp * gridDim.x + blockIdx.x;
-  const int64_t u0 = w * share, u1 = min(units, u0 + share);
+    // ---- this warp's run of units; neighbouring runs on different SMs
+    share = share_of(a, units);
+    w = (int64_t)warp * gridDim.x + blockIdx.x;
+    u0 = w * share, u1 = min(units, u0 + share);
+  }
   const int psh = 31 - __clz(a.kv.page_size);
   uint8_t* mystage = ring + warp * C::kStages * C::kStage;
   uint64_t* bar = bars + warp * C::kStages;
 
   Unit* note = notes + warp * C::kStages;
 
+  auto own_pages = [&](int t) {
+    const int seq = a.row_seq != nullptr ? a.row_seq[t] : t;
+    const bool ok = (unsigned)seq < (unsigned)a.sequences;
+    if (!ok && a.err != nullptr) atomicOr(a.err, kErrBadPage);
+    // an invalid row reads row 0 of the table: in bounds, and its output is undefined
+    return a.page_table + (int64_t)(ok ? seq : 0) * a.table_stride;
+  };
   // ---- the loading side: lane i works out unit `batch` + i of the run, with its page id
   int64_t batch = u0 - 32;
   Unit mu{};
@@ -187,10 +214,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t v = batch + lane;
       bool live = v < u1;
       if (live) {
+        int whole_tile = 0;
         int64_t r;  // unit of its row, or of the prefix
         const int32_t* pages;
         int n;
-        if (v < pre) {
+        if constexpr (WHOLE) {
+          mu = mine_item;
+          const bool shared = v < shared_tiles;
+          r = v - (shared ? 0 : shared_tiles);
+          n = shared ? a.prefix_len : own_keys;
+          pages = shared ? a.prefix_pages : own_pages(mu.t);
+        } else if (v < pre) {
           r = v;
           n = a.prefix_len;
           pages = a.prefix_pages;
@@ -207,28 +241,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           r = v - base[lo];
           n = keys[lo];
           mu.t = t0 + lo;
-          const int seq = a.row_seq != nullptr ? a.row_seq[mu.t] : mu.t;
-          const bool ok = (unsigned)seq < (unsigned)a.sequences;
-          if (!ok && a.err != nullptr) atomicOr(a.err, kErrBadPage);
-          // an invalid row reads row 0 of the table: in bounds, and its output is undefined
-          pages = a.page_table + (int64_t)(ok ? seq : 0) * a.table_stride;
+          pages = own_pages(mu.t);
         }
-        mu.tiles = (n + kTile - 1) / kTile;
-        const int span = mu.tiles + kHead;
-        const int item = r >> 32 ? (int)(r / span) : (int)((uint32_t)r / (uint32_t)span);
-        mu.tile = (int)(r - (int64_t)item * span) - kHead;
-        live = mu.tile >= 0;
-        if (mu.t < 0) {
-          const int rt = item / a.kv.kv_heads;
-          mu.h = item - rt * a.kv.kv_heads;
-          mu.row0 = rt * 16;
+        if constexpr (WHOLE) {
+          whole_tile = (int)r;
         } else {
-          const int rts = a.head_items / a.kv.kv_heads;
-          mu.h = item / rts;
-          mu.row0 = (item - mu.h * rts) * 16;
+          mu.tiles = (n + kTile - 1) / kTile;
+          const int span = mu.tiles + kHead;
+          const int item = r >> 32 ? (int)(r / span) : (int)((uint32_t)r / (uint32_t)span);
+          mu.tile = (int)(r - (int64_t)item * span) - kHead;
+          live = mu.tile >= 0;
+          if (mu.t < 0) {
+            const int rt = item / a.kv.kv_heads;
+            mu.h = item - rt * a.kv.kv_heads;
+            mu.row0 = rt * 16;
+          } else {
+            const int rts = a.head_items / a.kv.kv_heads;
+            mu.h = item / rts;
+            mu.row0 = (item - mu.h * rts) * 16;
+          }
         }
         if (live) {
-          const int key = mu.tile * kTile;
+          const int key = (WHOLE ? whole_tile : mu.tile) * kTile;
           mu.valid = min(kTile, n - key);
           row = key & (a.kv.page_size - 1);
           id = __ldg(pages + (key >> psh));
@@ -430,6 +464,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) break;
 
+    if constexpr (WHOLE) {
+      // the warp's ring is done with: it takes the warp's part
+      float* mine_o = reinterpret_cast<float*>(mystage);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        float* dst = mine_o + (g + 8 * e) * D;
+        if constexpr (!F8) {
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) *reinterpret_cast<float2*>(dst + k * 8 + 2 * c) = make_float2(o[k][2 * e], o[k][2 * e + 1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            *reinterpret_cast<float4*>(dst + k * 16 + 4 * c) =
+                make_float4(o[2 * k][2 * e], o[2 * k + 1][2 * e], o[2 * k][2 * e + 1], o[2 * k + 1][2 * e + 1]);
+        }
+        if (c == 0) ml[warp * 16 + g + 8 * e] = make_float2(m[e], l[e]);
+      }
+      break;
+    }
     // ---- the part
     const int64_t origin = it.t < 0 ? 0 : base[it.t - t0];
     const int item = it.t < 0 ? it.row0 / 16 * a.kv.kv_heads + it.h : it.h * (a.head_items / a.kv.kv_heads) + it.row0 / 16;
@@ -462,6 +517,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (!mbar_try_wait(&bar[i % C::kStages], (i / C::kStages) & 1) && clock64() - c0 < kWaitLimit) {
       }
     }
+  if constexpr (WHOLE) {
+    __syncthreads();
+    // 16 threads a row, D / 16 columns each; what the warps hold counts from their own bases
+    const int i = tid >> 4, col = (tid & 15) * (D / 16);
+    const int parts = share > 0 ? (shared_tiles + (own_keys + kTile - 1) / kTile + (int)share - 1) / (int)share : 0;
+    float m = -INFINITY, l = 0.f, acc[D / 16];
+    for (int k = 0; k < parts; ++k) m = fmaxf(m, ml[k * 16 + i].x);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) acc[d] = 0.f;
+    for (int k = 0; k < parts; ++k) {
+      const float2 part = ml[k * 16 + i];
+      const float f = ex2(part.x - (m == -INFINITY ? 0.f : m));
+      l = fmaf(part.y, f, l);
+      const float4* src =
+          reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring + k * C::kStages * C::kStage) + i * D + col);
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) {
+        const float4 x = src[d];
+        acc[4 * d] = fmaf(x.x, f, acc[4 * d]), acc[4 * d + 1] = fmaf(x.y, f, acc[4 * d + 1]);
+        acc[4 * d + 2] = fmaf(x.z, f, acc[4 * d + 2]), acc[4 * d + 3] = fmaf(x.w, f, acc[4 * d + 3]);
+      }
+    }
+    if (mine_item.row0 + i < a.group) {
+      const int64_t rh = (int64_t)mine_item.t * a.q_heads + mine_item.h * a.group + mine_item.row0 + i;
+      const float inv = parts == 0 ? 0.f : (F8 ? a.kv.v_scale[mine_item.h] : 1.f) / l;
+#pragma unroll
+      for (int d = 0; d < D / 16; d += 2)
+        *reinterpret_cast<__nv_bfloat162*>(a.out + rh * D + col + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
+      if (a.lse != nullptr && (tid & 15) == 0) a.lse[rh] = parts == 0 ? -INFINITY : m * kLn2 + logf(l);
+    }
+  }
   pdl_wait();  // the combine kernel follows this one only: the tensor-core kernel is done then too
 }
 
@@ -607,18 +693,20 @@ int launch_all(const Args& a, int sms, cudaStream_t s) {
   int r = a.tc_ctas > 0 ? launch_prefix_tc(a, s) : PMOE_OK;
   if (r != PMOE_OK) return r;
   const char* what = "moe_prefix_attention";
-  if (a.pre_tiles > 0 || a.max_suffix > 0) {
-    static SmemLimit limit;
+  if (a.whole || a.pre_tiles > 0 || a.max_suffix > 0) {
+    static SmemLimit limit[2];
     CUtensorMap mk, mv;
-    r = limit.set(reinterpret_cast<const void*>(stream_kernel<D, F8>), C::kSmem, what);
+    const auto kernel = a.whole ? stream_kernel<D, F8, true> : stream_kernel<D, F8, false>;
+    r = limit[a.whole].set(reinterpret_cast<const void*>(kernel), C::kSmem, what);
     if (r == PMOE_OK) r = make_map(a, a.kv.k, &mk);
     if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
     if (r != PMOE_OK) return r;
+    if (a.whole) return launch(what, kernel, (unsigned)(a.T * a.head_items), kThreads, C::kSmem, s, true, 1, mk, mv, a, 0);
     const int blocks = a.max_suffix > 0 ? (a.T + kRowBlock - 1) / kRowBlock : 1;
     for (int b = 0; b < blocks; ++b) {
       // a later block's launch does not overtake the one before it, which the combine kernel
       // would not wait for
-      r = launch(what, stream_kernel<D, F8>, a.warps / kWarps, kThreads, C::kSmem, s, b == 0, 1, mk, mv, a, b);
+      r = launch(what, kernel, a.warps / kWarps, kThreads, C::kSmem, s, b == 0, 1, mk, mv, a, b);
       if (r != PMOE_OK) return r;
     }
   }
@@ -701,6 +789,18 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   // 18.9 on 6,400; 3 rows 15.4 / 12.9 on 6,400, 23.3 / 22.9 on 25,600.
   const bool tc = prefix_len > 0 && pre_rts > 1 && pre_rts * kv->kv_heads * prefix_len > 340ll * *sms;
   if (tc) stream_ctas = split_sms(a, *sms, key_bytes);
+  // Short calls: a CTA an item, without parts and their joining, as long as its warps' chains of
+  // tiles (and the waves of CTAs) are short. In us, in parts / whole, bf16 heads of 128, 4 kv
+  // heads: 1 row of 16 keys 9.3 / 3.8, of 564 9.8 / 7.7 (5 tiles a warp), of 1,300 10.2 / 11.5
+  // (11); 16 rows of 100 + 64 12.3 / 5.6; 76 rows (2 waves) of 300 13.4 / 12.4, of 564 16.1 / 15.9;
+  // 120 rows (4 waves) of 164 14.0 / 18.9.
+  const int64_t tiles_whole = ((int64_t)prefix_len + kTile - 1) / kTile + ((int64_t)max_suffix + kTile - 1) / kTile;
+  const int64_t waves = ((int64_t)T * a->head_items + *sms - 1) / *sms;
+  a->whole = !tc && waves * ((tiles_whole + kWarps - 1) / kWarps + 4) <= 14;
+  if (a->whole) {
+    a->suffix_parts = 0;
+    return PMOE_OK;
+  }
   a->warps = stream_ctas * kWarps;
   const int64_t tiles = ((int64_t)max_suffix + kTile - 1) / kTile;
   // A warp's run: 64 keys at least, and long enough that an item has few parts
