@@ -11,7 +11,8 @@
 // (item, tile) units of all items, in order, are cut into equal runs, one a warp of every
 // SM, whatever the lengths; a warp whose run ends inside an item leaves a part of it. An item
 // counts for kHead units more than its tiles: short ones cost more than their keys. Calls of few
-// and short items take a CTA an item instead, which joins its warps' parts itself. Measured: 256
+// and short items take a CTA or a cluster an item instead, which joins its warps' parts itself
+// (4 rows of 564 keys 7.7 us, 1 of 2,064 9.1). Measured: 256
 // rows of 1..1,024 keys (4 kv heads of 128, bf16) 51 us; 2 rows on 100,003 shared and 256 own
 // keys 44.4 us with the combine, 4.6 TB/s; long suffixes 6.6 TB/s, 0.97 of a copy.
 #include "attn.cuh"
@@ -19,6 +20,7 @@
 #include "tc_ptx.cuh"
 
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
 
@@ -101,8 +103,8 @@ __device__ __forceinline__ int64_t share_of(const Args& a, int64_t units) {
   return max((int64_t)a.min_share, (units + a.warps - 1) / a.warps);
 }
 
-// WHOLE: a CTA takes all keys of one item, shared and own, its warps a run of tiles each, and
-// writes the output itself.
+// WHOLE: a CTA, or a cluster of up to 8, takes all keys of one item, shared and own, its warps a
+// run of tiles each, and writes the output itself.
 template <int D, bool F8, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a,
@@ -133,16 +135,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   int64_t share = 0, w = 0, u0, u1;  // this warp's run of units; of a whole item: of its tiles
   Unit mine_item{};                  // WHOLE: the CTA's item, its shared tiles and own keys
-  int shared_tiles = 0, own_keys = 0;
+  int shared_tiles = 0, own_keys = 0, rank = 0;
   if constexpr (WHOLE) {
-    const int rts = a.head_items / a.kv.kv_heads, t = blockIdx.x / a.head_items, item = blockIdx.x - t * a.head_items;
+    const int block_item = blockIdx.x / a.whole, rts = a.head_items / a.kv.kv_heads;
+    const int t = block_item / a.head_items, item = block_item - t * a.head_items;
+    rank = blockIdx.x - block_item * a.whole;
     mine_item.t = t, mine_item.h = item / rts, mine_item.row0 = (item - mine_item.h * rts) * 16;
     mine_item.tiles = INT_MAX;  // the run ends it
     shared_tiles = (a.prefix_len + kTile - 1) / kTile;
     own_keys = a.max_suffix > 0 ? suffix_keys(a, t) : 0;
     const int tiles = shared_tiles + (own_keys + kTile - 1) / kTile;
-    share = (tiles + kWarps - 1) / kWarps;
-    u0 = min((int64_t)tiles, warp * share), u1 = min((int64_t)tiles, u0 + share);
+    share = (tiles + a.whole * kWarps - 1) / (a.whole * kWarps);
+    u0 = min((int64_t)tiles, (rank * kWarps + warp) * share), u1 = min((int64_t)tiles, u0 + share);
     __syncthreads();
   } else {
     // ---- the first unit of every row: thread i sums 8 rows
@@ -518,10 +522,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   if constexpr (WHOLE) {
-    __syncthreads();
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    if (a.whole > 1)
+      cluster.sync();  // the first CTA's rings are done with too
+    else
+      __syncthreads();
     // 16 threads a row, D / 16 columns each; what the warps hold counts from their own bases
     const int i = tid >> 4, col = (tid & 15) * (D / 16);
-    const int parts = share > 0 ? (shared_tiles + (own_keys + kTile - 1) / kTile + (int)share - 1) / (int)share : 0;
+    const int all = share > 0 ? (shared_tiles + (own_keys + kTile - 1) / kTile + (int)share - 1) / (int)share : 0;
+    const int parts = max(0, min(kWarps, all - rank * kWarps));  // warps with tiles: of this CTA, of all
     float m = -INFINITY, l = 0.f, acc[D / 16];
     for (int k = 0; k < parts; ++k) m = fmaxf(m, ml[k * 16 + i].x);
 #pragma unroll
@@ -539,13 +549,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc[4 * d + 2] = fmaf(x.z, f, acc[4 * d + 2]), acc[4 * d + 3] = fmaf(x.w, f, acc[4 * d + 3]);
       }
     }
-    if (mine_item.row0 + i < a.group) {
+    if (a.whole > 1) {
+      // the CTAs' parts meet in the first one's memory, in the halves of its rings that its own
+      // warps' parts leave free
+      constexpr int kHalf = C::kStages * C::kStage / 2;
+      static_assert(16 * D * 4 <= kHalf, "a part in half a ring");
+      if (rank > 0 && parts > 0) {
+        float4* dst = reinterpret_cast<float4*>(cluster.map_shared_rank(ring, 0) + rank * 2 * kHalf + kHalf + (i * D + col) * 4);
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) dst[d] = make_float4(acc[4 * d], acc[4 * d + 1], acc[4 * d + 2], acc[4 * d + 3]);
+        if ((tid & 15) == 0) cluster.map_shared_rank(ml, 0)[(kWarps + rank) * 16 + i] = make_float2(m, l);
+      }
+      cluster.sync();
+      const int ctas = (all + kWarps - 1) / kWarps;
+      float top = m;
+      for (int k = 1; k < ctas; ++k) top = fmaxf(top, ml[(kWarps + k) * 16 + i].x);
+      const float own = ex2(m - (top == -INFINITY ? 0.f : top));
+      l *= own;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) acc[d] *= own;
+      for (int k = 1; k < ctas && rank == 0; ++k) {
+        const float2 part = ml[(kWarps + k) * 16 + i];
+        const float f = ex2(part.x - (top == -INFINITY ? 0.f : top));
+        l = fmaf(part.y, f, l);
+        const float4* src = reinterpret_cast<const float4*>(ring + k * 2 * kHalf + kHalf + (i * D + col) * 4);
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) {
+          const float4 x = src[d];
+          acc[4 * d] = fmaf(x.x, f, acc[4 * d]), acc[4 * d + 1] = fmaf(x.y, f, acc[4 * d + 1]);
+          acc[4 * d + 2] = fmaf(x.z, f, acc[4 * d + 2]), acc[4 * d + 3] = fmaf(x.w, f, acc[4 * d + 3]);
+        }
+      }
+      m = top;
+    }
+    if (rank == 0 && mine_item.row0 + i < a.group) {
       const int64_t rh = (int64_t)mine_item.t * a.q_heads + mine_item.h * a.group + mine_item.row0 + i;
-      const float inv = parts == 0 ? 0.f : (F8 ? a.kv.v_scale[mine_item.h] : 1.f) / l;
+      const float inv = all == 0 ? 0.f : (F8 ? a.kv.v_scale[mine_item.h] : 1.f) / l;
 #pragma unroll
       for (int d = 0; d < D / 16; d += 2)
         *reinterpret_cast<__nv_bfloat162*>(a.out + rh * D + col + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
-      if (a.lse != nullptr && (tid & 15) == 0) a.lse[rh] = parts == 0 ? -INFINITY : m * kLn2 + logf(l);
+      if (a.lse != nullptr && (tid & 15) == 0) a.lse[rh] = all == 0 ? -INFINITY : m * kLn2 + logf(l);
     }
   }
   pdl_wait();  // the combine kernel follows this one only: the tensor-core kernel is done then too
@@ -697,11 +740,12 @@ int launch_all(const Args& a, int sms, cudaStream_t s) {
     static SmemLimit limit[2];
     CUtensorMap mk, mv;
     const auto kernel = a.whole ? stream_kernel<D, F8, true> : stream_kernel<D, F8, false>;
-    r = limit[a.whole].set(reinterpret_cast<const void*>(kernel), C::kSmem, what);
+    r = limit[a.whole > 0].set(reinterpret_cast<const void*>(kernel), C::kSmem, what);
     if (r == PMOE_OK) r = make_map(a, a.kv.k, &mk);
     if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
     if (r != PMOE_OK) return r;
-    if (a.whole) return launch(what, kernel, (unsigned)(a.T * a.head_items), kThreads, C::kSmem, s, true, 1, mk, mv, a, 0);
+    if (a.whole)
+      return launch(what, kernel, (unsigned)(a.T * a.head_items * a.whole), kThreads, C::kSmem, s, true, a.whole, mk, mv, a, 0);
     const int blocks = a.max_suffix > 0 ? (a.T + kRowBlock - 1) / kRowBlock : 1;
     for (int b = 0; b < blocks; ++b) {
       // a later block's launch does not overtake the one before it, which the combine kernel
@@ -789,14 +833,23 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   // 18.9 on 6,400; 3 rows 15.4 / 12.9 on 6,400, 23.3 / 22.9 on 25,600.
   const bool tc = prefix_len > 0 && pre_rts > 1 && pre_rts * kv->kv_heads * prefix_len > 340ll * *sms;
   if (tc) stream_ctas = split_sms(a, *sms, key_bytes);
-  // Short calls: a CTA an item, without parts and their joining, as long as its warps' chains of
-  // tiles (and the waves of CTAs) are short. In us, in parts / whole, bf16 heads of 128, 4 kv
-  // heads: 1 row of 16 keys 9.3 / 3.8, of 564 9.8 / 7.7 (5 tiles a warp), of 1,300 10.2 / 11.5
-  // (11); 16 rows of 100 + 64 12.3 / 5.6; 76 rows (2 waves) of 300 13.4 / 12.4, of 564 16.1 / 15.9;
-  // 120 rows (4 waves) of 164 14.0 / 18.9.
+  // Short calls: a CTA or a cluster an item, without the launch that joins parts, as long as the
+  // warps' chains of tiles are short. What is compared is a chain's tiles, 4 for start and end
+  // and 1 for the exchange in a cluster. In us, in parts / with 1 / 2 / 4 / 8 CTAs an item (bf16
+  // heads of 128, 4 kv heads): 1 row of 16 keys 9.3 / 3.8 / 4.7 / 4.7 / 4.6, of 564 9.4 / 7.6 / 7.6 /
+  // 7.4 / 7.3, of 2,064 10.6 / 15.2 / 11.2 / 9.2 / 9.1, of 12,500 13.1 and 15.6 with 8; 16 rows of
+  // 164 12.3 / 5.8 / 6.7, of 1,300 14.2 / 12.1 / 9.9; 76 rows (2 waves) of 300 13.4 / 12.4; 120 rows
+  // (4 waves) of 164 14.0 / 18.9. Clusters of 8 fill half of the SMs at most (4 rows of 564 with
+  // 16 of them: 13.4, with 16 clusters of 4 7.7).
   const int64_t tiles_whole = ((int64_t)prefix_len + kTile - 1) / kTile + ((int64_t)max_suffix + kTile - 1) / kTile;
-  const int64_t waves = ((int64_t)T * a->head_items + *sms - 1) / *sms;
-  a->whole = !tc && waves * ((tiles_whole + kWarps - 1) / kWarps + 4) <= 14;
+  a->whole = 0;
+  int64_t best = 14;
+  for (int n = 1; n <= 8 && !tc; n *= 2) {
+    const int64_t ctas = (int64_t)T * a->head_items * n, waves = (ctas + *sms - 1) / *sms;
+    if (n > 1 && ctas > (n == 8 ? 64 : 128)) break;
+    const int64_t cost = waves * ((tiles_whole + n * kWarps - 1) / (n * kWarps) + 4) + (n > 1 ? 1 : 0);
+    if (cost < best) best = cost, a->whole = n;
+  }
   if (a->whole) {
     a->suffix_parts = 0;
     return PMOE_OK;

@@ -294,3 +294,20 @@ def test_attention_refusals(pm):
     assert e.value.status == pm.PMOE_EINVAL
     out = pm.moe_prefix_attention(c["k"], c["v"], c["q"][:0], args[3], 40, args[5], args[6][:0], 20)
     assert out.shape == (0, 8, 64)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,page,e4m3,prefix,suffix", [
+    # one CTA an item; clusters of 2, 4 and 8, with less than a tile a warp and with several
+    (3, 32, 4, 128, 16, False, 0, 33), (20, 12, 4, 64, 32, True, 60, 60), (14, 8, 4, 128, 16, True, 500, 40),
+    (8, 40, 4, 64, 64, False, 1500, 70), (5, 64, 2, 128, 128, False, 700, 300), (1, 8, 1, 128, 16, False, 6000, 100),
+    (2, 16, 2, 64, 32, True, 3000, 200), (1, 48, 1, 128, 256, True, 250, 1)])
+def test_short_calls_without_parts(pm, T, Hq, Hkv, D, page, e4m3, prefix, suffix):
+    c = make(T + prefix, T, Hq, Hkv, D, page, e4m3, prefix, suffix)
+    c["lens"][0] = 0
+    c["lens"][-1] = suffix
+    poison_unseen(c)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = run(pm, c, err_out=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    check(c, out, lse)
