@@ -832,7 +832,6 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   // heads 18.0 / 16.6 on 400 keys, 18.7 / 22.2 on 1,600; 8 rows 13.3 / 13.5 on 1,600, 15.9 /
   // 18.9 on 6,400; 3 rows 15.4 / 12.9 on 6,400, 23.3 / 22.9 on 25,600.
   const bool tc = prefix_len > 0 && pre_rts > 1 && pre_rts * kv->kv_heads * prefix_len > 340ll * *sms;
-  if (tc) stream_ctas = split_sms(a, *sms, key_bytes);
   // Short calls: a CTA or a cluster an item, without the launch that joins parts, as long as the
   // warps' chains of tiles are short. What is compared is a chain's tiles, 4 for start and end
   // and 1 for the exchange in a cluster. In us, in parts / with 1 / 2 / 4 / 8 CTAs an item (bf16
@@ -840,11 +839,13 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   // 7.4 / 7.3, of 2,064 10.6 / 15.2 / 11.2 / 9.2 / 9.1, of 12,500 13.1 and 15.6 with 8; 16 rows of
   // 164 12.3 / 5.8 / 6.7, of 1,300 14.2 / 12.1 / 9.9; 76 rows (2 waves) of 300 13.4 / 12.4; 120 rows
   // (4 waves) of 164 14.0 / 18.9. Clusters of 8 fill half of the SMs at most (4 rows of 564 with
-  // 16 of them: 13.4, with 16 clusters of 4 7.7).
+  // 16 of them: 13.4, with 16 clusters of 4 7.7). The prefix kernel starts late: against it (tensor
+  // cores / whole) 32 rows of 1,300 keys take 15.6 / 12.3, of 1,664 15.6 / 13.6, 64 rows (2 waves)
+  // of 514 15.9 / 15.2, 76 of 764 16.1 / 17.6.
   const int64_t tiles_whole = ((int64_t)prefix_len + kTile - 1) / kTile + ((int64_t)max_suffix + kTile - 1) / kTile;
   a->whole = 0;
-  int64_t best = 14;
-  for (int n = 1; n <= 8 && !tc; n *= 2) {
+  int64_t best = tc ? 20 : 14;
+  for (int n = 1; n <= 8; n *= 2) {
     const int64_t ctas = (int64_t)T * a->head_items * n, waves = (ctas + *sms - 1) / *sms;
     if (n > 1 && ctas > (n == 8 ? 64 : 128)) break;
     const int64_t cost = waves * ((tiles_whole + n * kWarps - 1) / (n * kWarps) + 4) + (n > 1 ? 1 : 0);
@@ -854,6 +855,7 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
     a->suffix_parts = 0;
     return PMOE_OK;
   }
+  if (tc) stream_ctas = split_sms(a, *sms, key_bytes);
   a->warps = stream_ctas * kWarps;
   const int64_t tiles = ((int64_t)max_suffix + kTile - 1) / kTile;
   // A warp's run: 64 keys at least, and long enough that an item has few parts
