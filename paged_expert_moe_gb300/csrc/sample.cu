@@ -6,7 +6,8 @@
 // Bound: HBM for many rows (each logit read once), the chain of dependent steps for few. A
 // cluster of up to 8 CTAs takes a row; each CTA keeps its slice in shared memory and the
 // CTAs exchange statistics through distributed shared memory, written to where they are read.
-//   1. Load the slice; its largest logit, and those of its threads. For rows that are cut by
+//   1. Load the slice; its largest logit, and those of its threads (or of four groups of each
+//      thread's). For rows that are cut by
 //      top-k or top-p a lower bound of the K-th largest logit (K = top_k, or 1,024): with K /
 //      CTAs of the threads' largest logits at or above a bound in every CTA, K logits are at
 //      or above the least of these bounds, and seldom many more.
@@ -650,19 +651,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   sh.hist.cnt[tid] = 0;
   if (tid == 0) sh.arg = INT_MAX, sh.listed = 0, sh.sum = 0, sh.list_sum = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");
+  const bool use_k = top_k > 0 && top_k < a.V, use_p = top_p < 1.f;
+  const bool listing = temp > 0.f && (use_k ? top_k <= kMaxK : use_p);
+  const uint32_t want = use_k ? (top_k + nb - 1) / nb : kCutP;  // of a CTA, if `listing`
+  // A bound that a fourth of the threads' largest logits or more shall reach is found from
+  // those of four groups of each thread's instead: 256 bf16 rows of 8,000 with top_k 1,000 in
+  // one CTA each overflow their lists otherwise. Other rows need not tell the groups apart.
+  const bool fine = listing && want > kThreads / 4;
   float mine = -INFINITY;  // of the vectors this thread loaded; fmaxf leaves NaN out
-  for (int i = tid; i < nv; i += kThreads) {
-    const V x(xs[i]);
+  float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if (fine) {
+    for (int i = tid, k = 0; i < nv; i += kThreads, ++k) {
+      const V x(xs[i]);
+      float v[N / 4];
 #pragma unroll
-    for (int q = 0; q < N; ++q) mine = fmaxf(mine, x.f[q]);
+      for (int h = 0; h < N / 4; ++h) v[h] = fmaxf(fmaxf(x.f[4 * h], x.f[4 * h + 1]), fmaxf(x.f[4 * h + 2], x.f[4 * h + 3]));
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        constexpr int per = 16 / N;  // vectors until the groups come round again
+        top4[g] = g / (N / 4) == k % per ? fmaxf(top4[g], v[g % (N / 4)]) : top4[g];
+      }
+    }
+    mine = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+  } else {
+    for (int i = tid; i < nv; i += kThreads) {
+      const V x(xs[i]);
+#pragma unroll
+      for (int q = 0; q < N; ++q) mine = fmaxf(mine, x.f[q]);
+    }
   }
   float best = mine;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) sh.top[warp] = best;
-  const bool use_k = top_k > 0 && top_k < a.V, use_p = top_p < 1.f;
-  const bool listing = temp > 0.f && (use_k ? top_k <= kMaxK : use_p);
-  const uint32_t want = use_k ? (top_k + nb - 1) / nb : kCutP;  // of a CTA, if `listing`
   __syncthreads();
   best = sh.top[lane % kWarps];
 #pragma unroll
@@ -670,10 +691,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const float cta_best = best;
   float bound = -FLT_MAX;  // fewer threads with a logit than that: every logit is a candidate
   if (listing) {
-    // the bin of the threads' largest logits, by distance from the CTA's, that holds the
-    // want-th; the bound is the least of those in it or above it
-    const int mybin = Row(best, 1.f).bin(mine);
-    if (mine > -INFINITY) atomicAdd(&sh.hist.cnt[mybin], 1u);
+    // the bin of the largest logits, by distance from the CTA's, that holds the want-th; the
+    // bound is the least of those in it or above it
+    const Row by(best, 1.f);
+    if (fine) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (top4[g] > -INFINITY) atomicAdd(&sh.hist.cnt[by.bin(top4[g])], 1u);
+    } else if (mine > -INFINITY) {
+      atomicAdd(&sh.hist.cnt[by.bin(mine)], 1u);
+    }
     if (tid == 0) sh.pick.bin = kBins, sh.bound_key = 0xffffffffu;
     __syncthreads();
     uint32_t upto = sh.hist.cnt[tid];
@@ -690,7 +717,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       if (i < warp) upto += sh.scan_cnt[i];
     if (upto >= want && upto - own < want) sh.pick.bin = tid;
     __syncthreads();
-    if (mine > -INFINITY && mybin <= sh.pick.bin) atomicMin(&sh.bound_key, key_of(mine));
+    const int last = sh.pick.bin;
+    if (fine) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (top4[g] > -INFINITY && by.bin(top4[g]) <= last) atomicMin(&sh.bound_key, key_of(top4[g]));
+    } else if (mine > -INFINITY && by.bin(mine) <= last) {
+      atomicMin(&sh.bound_key, key_of(mine));
+    }
     __syncthreads();
     if (sh.pick.bin != kBins) bound = of_key(sh.bound_key);
   }
@@ -1058,17 +1092,19 @@ extern "C" int moe_sample_tokens(const void* logits, int is_bf16, int T, int V, 
   if (off(logits, is_bf16 ? 2 : 4) || off(temperature, 4) || off(top_k, 4) || off(top_p, 4) || off(min_p, 4) || off(u, 4) ||
       off(ids_out, 4) || off(logprob_out, 4))
     return PMOE_EINVAL;
-  // CTAs of a row: slices of 4,096 logits and up. Once the rows fill the GPU (two CTAs an SM),
-  // a CTA's fixed steps cost more than its share of the row: slices of 6,144 and up, and of up
-  // to 80 KB (two still fit an SM) with four times that many CTAs. But a row that needs step 3
-  // takes the longer the fewer CTAs it has. In us, with settings of all kinds, 8 / 4 / 2 CTAs a
-  // row: 256 rows of 32,000 61.5 / 41.7 / 47.8, of 50,001 72.6 / 49.9; 100 bf16 rows of 32,000
-  // 28.7 / 23.1 / 37.9; bf16 rows of 131,072: 256 of them 90.2 / 75.2, 64 of them 29.5 / 33.1.
+  // CTAs of a row: one up to 4,096 logits (a row of 3,000 8.5 us, 9.3 with 2), else slices of up
+  // to 2,048, 8 CTAs at most (a row of 8,000 6.4 with 4, 6.9 with 2). With more than 200 CTAs
+  // (clusters of 8 do not all find room) a CTA's fixed steps cost more than its share of the row:
+  // slices of up to 8,192, and beyond 608 CTAs of up to 80 KB (two fit an SM). But a row that
+  // needs step 3 takes the longer the fewer CTAs it has. In us, with settings of all kinds, 8 / 4 / 2 / 1 CTAs a row:
+  // 30 rows of 32,000 16.5 / 16.3 / 23.4 / 29.6; 60 of 8,000 16.8 / 11.9 / 10.3 / 10.8; 150 of 5,000
+  // 43.8 / 19.5 / 13.4 / 11.7; 256 of 32,000 62 / 43 / 36 / 40, of 50,001 72 / 51 / 56; bf16 rows of
+  // 131,072: 256 of them 90 / 75, 64 of them 29.5 / 33.1.
   int cluster = 1;
-  const int64_t resident = 304, bytes = (int64_t)V * (is_bf16 ? 2 : 4);
-  while (cluster < kMaxCluster && V > cluster * 4096) cluster *= 2;
-  while (cluster > 1 && (int64_t)T * cluster > resident && V <= cluster * 6144) cluster /= 2;
-  while (cluster > 1 && (int64_t)T * cluster > 4 * resident && 2 * bytes <= (int64_t)cluster * 81920) cluster /= 2;
+  const int64_t rows = T, bytes = (int64_t)V * (is_bf16 ? 2 : 4);
+  while (cluster < kMaxCluster && V > cluster * 2048 && V > 4096) cluster *= 2;
+  while (cluster > 1 && rows * cluster > 200 && 2 * V <= cluster * 8192) cluster /= 2;
+  while (cluster > 1 && rows * cluster > 608 && 2 * bytes <= (int64_t)cluster * 81920) cluster /= 2;
   if ((int64_t)T * cluster > INT32_MAX) return PMOE_EINVAL;
   SampleArgs a{logits, T, V, row_stride, temperature, top_k, top_p, min_p, u, ids_out, logprob_out, 0};
   // 7: the most elements by which a row can start after its first 16-byte vector
