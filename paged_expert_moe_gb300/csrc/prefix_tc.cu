@@ -181,8 +181,11 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
     while (ok && segment(a, &u, end, &sg)) {
       if (q >= sg.nq) continue;
       // the query tile, K-major with the 128-byte swizzle; rows beyond the last are zero.
-      // A negative scale goes into the sign of Q, so that the largest score stays the largest.
-      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+      // What a score is multiplied by, scale x key scale x the row's power of two, has to be above
+      // zero: then the largest score stays the largest, and a masked one -inf. So its sign goes
+      // into Q, and a row whose factor is 0 (or vanishes in fp32) has Q = 0 and factor 1.
+      const float ks = F8 ? a.kv.k_scale[sg.h] : 1.f;
+      const uint32_t flip = (a.scale < 0.f) != (ks < 0.f) ? 0x80008000u : 0u;
       const int c = row % LPR;
       constexpr int kPasses = LPR, kAhead = LPR;  // rows of a thread, all in flight
 #pragma unroll
@@ -210,11 +213,11 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const int e = row_exponent(mx);
-            const float down = pow2(-e);
+            const float factor = fabsf(a.scale) * fabsf(ks) * pow2(e), down = factor != 0.f ? pow2(-e) : 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-            if (c == 0) qmul[q * 128 + r] = fabsf(a.scale) * a.kv.k_scale[sg.h] * pow2(e);
+            if (c == 0) qmul[q * 128 + r] = factor != 0.f ? factor : 1.f;
           }
           *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
