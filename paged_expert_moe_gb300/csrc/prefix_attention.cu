@@ -913,7 +913,7 @@ extern "C" int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64
   if (scratch == nullptr || scratch_bytes < lay.bytes) return PMOE_EINVAL;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
-  a.scale = scale != 0.f ? scale * attn::kLog2e : 1e-30f;  // not 0: masked scores are -inf times it
+  a.scale = scale * attn::kLog2e;
   a.prefix_pages = prefix_pages;
   a.page_table = page_table;
   a.table_stride = table_stride;

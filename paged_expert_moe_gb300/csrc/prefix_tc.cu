@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       warp_arrive(&b.qfull[q]);
       // the row factors of all threads
       if (!warp_wait(&b.qfull[q], segs++ & 1, abort_flag, a.err)) break;
-      const float mul = F8 ? qmul[q * 128 + row] : fabsf(a.scale);
+      // (bf16, scale 0: times 2^-149 the largest score is below 2^-20)
+      const float mul = F8 ? qmul[q * 128 + row] : a.scale != 0.f ? fabsf(a.scale) : __uint_as_float(1);
 
       float m = -INFINITY, l = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++n) {

@@ -1,6 +1,7 @@
 """moe_prefix_attention where the factor of the scores is zero, negative or vanishes: e4m3 scales
-of any sign, queries so small that the factor leaves fp32's range. The answer is the formula's on every path, with prefixes that end inside a tile. Tolerances: those
-of test_gpu_prefix_attention, whose score error is proportional to the factor.
+of any sign, a softmax scale of zero, queries so small that the factor leaves fp32's range. The
+answer is the formula's on every path, with prefixes that end inside a tile. Tolerances: those of
+test_gpu_prefix_attention, whose score error is proportional to the factor.
 """
 
 import pytest
@@ -43,6 +44,16 @@ def test_value_scales_of_any_sign(pm, T, Hq, Hkv, D, prefix, suffix, v_scale):
     c["vs"] = torch.tensor(v_scale, device="cuda")
     out, lse = run(pm, c)
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,prefix,suffix", PATHS)
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("qscale", [2.0, 1e-30, 1e33])
+def test_a_softmax_scale_of_zero_weighs_all_keys_alike(pm, T, Hq, Hkv, D, prefix, suffix, e4m3, qscale):
+    c = make(T + prefix, T, Hq, Hkv, D, 16, e4m3, prefix, suffix, qscale=qscale)
+    for scale in (0.0, -0.0):
+        out, lse = run(pm, c, scale=scale)
+        check(c, out, lse, scale=scale)
 
 
 @pytest.mark.parametrize("T,Hq,Hkv,D,prefix,suffix", PATHS)
