@@ -478,8 +478,8 @@ PMOE_API int moe_kv_append(const pmoe_kv_desc* kv, const void* q, int64_t q_stri
  *   out          device bf16 [T][q_heads][head_dim], 16-byte aligned
  *   lse          device fp32 [T][q_heads], or NULL
  *   scratch      device, 16-byte aligned, moe_prefix_attention_scratch_bytes(...) bytes
- * A page outside [0, num_pages) or a row_seq outside [0, sequences) sets error bit 64; such
- * keys read as zeros. Error bit 16: a bounded wait expired, outputs are undefined.
+ * A page outside [0, num_pages), or a row_seq outside [0, sequences) of a row with keys of its
+ * own, sets error bit 64; such keys and values read as zeros. Error bit 16: a bounded wait expired, outputs are undefined.
  * T = 0 enqueues nothing. q_heads a multiple of kv_heads, at most 64 query heads to a kv
  * head (else PMOE_EUNSUPPORTED), T * q_heads < 2^24. PMOE_EINVAL on bad arguments.
  */

@@ -199,12 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Unit* note = notes + warp * C::kStages;
 
-  auto own_pages = [&](int t) {
+  // the pages of row t's own keys; none for a table row out of range, whose keys read as zeros
+  auto own_pages = [&](int t) -> const int32_t* {
     const int seq = a.row_seq != nullptr ? a.row_seq[t] : t;
-    const bool ok = (unsigned)seq < (unsigned)a.sequences;
-    if (!ok && a.err != nullptr) atomicOr(a.err, kErrBadPage);
-    // an invalid row reads row 0 of the table: in bounds, and its output is undefined
-    return a.page_table + (int64_t)(ok ? seq : 0) * a.table_stride;
+    if ((unsigned)seq < (unsigned)a.sequences) return a.page_table + (int64_t)seq * a.table_stride;
+    return nullptr;
   };
   // ---- the loading side: lane i works out unit `batch` + i of the run, with its page id
   int64_t batch = u0 - 32;
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key = (WHOLE ? whole_tile : mu.tile) * kTile;
           mu.valid = min(kTile, n - key);
           row = key & (a.kv.page_size - 1);
-          id = __ldg(pages + (key >> psh));
+          id = pages != nullptr ? __ldg(pages + (key >> psh)) : -1;
           if ((unsigned)id >= (unsigned)a.kv.num_pages) {
             if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
             id = a.kv.num_pages;  // out of the map's range: reads as zeros
