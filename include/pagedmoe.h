@@ -431,7 +431,8 @@ typedef struct {
  * p = positions[axis][t] * inv_freq[i]. Pair i of rotary_dim / 2 is (x[i], x[i +
  * rotary_dim / 2]), or (x[2i], x[2i + 1]) when interleaved != 0; elements from rotary_dim on
  * are not rotated. The rotated q goes to q_out, the rotated k and v as it is to cache row
- * slots[t]. fp32 throughout, one rounding (e4m3: of value / scale, to nearest even,
+ * slots[t]. fp32 throughout (the angle as two floats: any int32 position is exact), one
+ * rounding (e4m3: of value / scale, to nearest even,
  * saturating at 448).
  *   q, k, v    device bf16 [T][q_heads | kv_heads | kv_heads][head_dim], tokens q_stride,
  *              k_stride, v_stride elements apart (views of one projection's output), heads

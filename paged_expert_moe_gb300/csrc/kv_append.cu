@@ -7,9 +7,9 @@
 // then q -> q_out (bf16) and k, v -> the cache row that slots[t] names (bf16, or e4m3 of
 // x / scale[kv head]). All of it is fp32 with one rounding at the end.
 //
-// The angle keeps the rounding error of its product (one fma), since at position 10^5 that
-// error alone would be up to 4e-3 rad, more than a bf16 output's own rounding; the sine and
-// cosine of the rounded angle are corrected by it to second order.
+// The angle keeps what its floats round off, of the position (beyond 2^24) and of the product
+// (one fma): at position 10^5 the latter alone would be up to 4e-3 rad, more than a bf16 output's
+// own rounding. The sine and cosine of the rounded angle are turned by it.
 //
 // Bound: HBM (every input read once, every output written once); one token is launch
 // latency. A block takes a few tokens, computes their sines and cosines once into shared
@@ -17,9 +17,9 @@
 // 16 elements, arranged so that a thread holds both halves of its 8 pairs: no exchange
 // between threads but the norm's sum.
 //
-// Measured (32 + 4 + 4 heads of 128, bf16): 8,192 tokens 30.6 us, 5.5 TB/s of the 6.8 a copy
-// reaches, with the issue slots 70% busy; 4,099 tokens of 48 heads of 64 11.6 us, 4.3 TB/s; one
-// token 2.7 us, a launch.
+// Measured (32 + 4 + 4 heads of 128, bf16): 8,192 tokens 30.9 us, 5.4 TB/s of the 6.8 a copy
+// reaches, with the issue slots 70% busy; 4,099 tokens of 48 heads of 64 11.4 us, 4.4 TB/s; one
+// token 3.0 us, a launch.
 #include "pmoe_internal.h"
 
 #include <algorithm>
@@ -32,6 +32,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;    // tokens of a block
 constexpr int kMaxPairs = 64;  // R / 2 <= D / 2
+// Up to this angle its rounding is at most 2^-7, and the second-order correction off by 2^-23.5.
+constexpr float kFarAngle = 131072.f;
 
 struct AppendArgs {
   pmoe_kv_desc kv;
@@ -80,6 +82,19 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float* f, float s) {
     w[i] = lo | (hi << 16);
   }
   return make_uint2(w[0], w[1]);
+}
+
+// Sine and cosine of pos * f beyond kFarAngle, or of a position that a float does not hold (above
+// 2^24): by the sum of the rounded product and of what was rounded off, of both. Out of line
+// it costs 8,192 tokens at ordinary positions 0.2 us (30.9), in line 0.4.
+__device__ __noinline__ void far_angle(int pos, float f, float* s, float* c) {
+  const float p = (float)pos, rest = (float)((long long)pos - (long long)p);
+  const float hi = p * f, lo = fmaf(rest, f, fmaf(p, f, -hi));
+  float sh, ch, sl, cl;
+  sincosf(hi, &sh, &ch);
+  sincosf(lo, &sl, &cl);
+  *s = sh * cl + ch * sl;
+  *c = ch * cl - sh * sl;
 }
 
 template <int D>
@@ -136,13 +151,20 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a,
         ax = 0;
       }
     }
-    const float p = (float)a.positions[(size_t)ax * a.T + t0 + tt], f = a.inv_freq[pr];
+    const int pos = a.positions[(size_t)ax * a.T + t0 + tt];
+    const float p = (float)pos, f = a.inv_freq[pr];
     const float hi = p * f, lo = fmaf(p, f, -hi);
     float s, c;
-    sincosf(hi, &s, &c);
-    const float l2 = 0.5f * lo * lo;
-    cs[tt][0][pr] = c - lo * s - l2 * c;
-    cs[tt][1][pr] = s + lo * c - l2 * s;
+    if (fmaxf(fabsf(hi), fabsf(p) * 0.0078125f) > kFarAngle) {
+      far_angle(pos, f, &s, &c);
+      cs[tt][0][pr] = c;
+      cs[tt][1][pr] = s;
+    } else {
+      sincosf(hi, &s, &c);
+      const float l2 = 0.5f * lo * lo;
+      cs[tt][0][pr] = c - lo * s - l2 * c;
+      cs[tt][1][pr] = s + lo * c - l2 * s;
+    }
   }
   __syncthreads();
 
