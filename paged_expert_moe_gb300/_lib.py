@@ -269,7 +269,8 @@ def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len,
     # the scales' values do not matter for the size, but that there are some does
     desc = pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0), k_cache.data_ptr(), k_cache.data_ptr(),
                         pages, page, heads, dim, kind)
-    return int(load().moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix))
+    with torch.cuda.device(k_cache.device):
+        return int(load().moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix))
 
 
 def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_table, suffix_len, max_suffix, scale=None,

@@ -2,7 +2,7 @@
 // moe_sample_tokens): argument checks and marshalling only, as _lib.py does for the others
 // through ctypes. Their kernels take a few microseconds. A call of moe_kv_append, of which the
 // library's part is 1.7 us, issues in 11.5 us through ctypes, in 5.4 when a dozen tensors are
-// asked for their attributes one by one from C, in 2.0 here, where they are at::Tensors.
+// asked for their attributes one by one from C, in 2.15 here, where they are at::Tensors.
 //
 // The library's entry points come in through setup(). Refused arguments raise AssertionError;
 // what torch throws (an allocation that fails) is raised as its own Python exception.
@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cmath>
@@ -25,7 +26,7 @@ decltype(&moe_kv_append) f_append;
 decltype(&moe_prefix_attention) f_attention;
 decltype(&moe_prefix_attention_scratch_bytes) f_scratch;
 decltype(&moe_sample_tokens) f_sample;
-PyObject* n_cuda_stream;
+PyObject *n_cuda_stream, *n_device_index;
 
 struct Refused {};  // a Python error is set
 
@@ -49,13 +50,38 @@ PyObject* guarded(F&& f) {
   END_HANDLE_TH_ERRORS
 }
 
-// A CUDA tensor of one of two types.
+// The device of a call, which its first argument, a CUDA tensor, gives: every other tensor has
+// to be there too, and the stream (the last argument), since the kernels read all of them from
+// one device. Before anything else is asked of the tensors.
+c10::DeviceIndex place(PyObject* const* a, Py_ssize_t n, const char* const* names) {
+  if (!THPVariable_Check(a[0]) || !THPVariable_Unpack(a[0]).defined()) refuse("%s: not a tensor", names[0]);
+  const at::Device d = THPVariable_Unpack(a[0]).device();
+  if (!d.is_cuda()) refuse("%s: not a CUDA tensor", names[0]);
+  for (Py_ssize_t i = 1; i + 1 < n; ++i) {
+    // (the check of what is no tensor is slow, and most arguments that are none are these: with it,
+    // and a device guard that always asks twice, moe_kv_append issues in 2.65 us instead of 2.15)
+    if (a[i] == Py_None || PyLong_Check(a[i]) || PyFloat_Check(a[i])) continue;
+    if (!THPVariable_Check(a[i]) || !THPVariable_Unpack(a[i]).defined()) continue;
+    const at::Device o = THPVariable_Unpack(a[i]).device();
+    if (o != d) refuse("%s: on %s, %s on %s", names[i], o.str().c_str(), names[0], d.str().c_str());
+  }
+  if (a[n - 1] != Py_None) {
+    PyObject* v = PyObject_GetAttr(a[n - 1], n_device_index);
+    if (v == nullptr) throw Refused{};
+    const long long index = PyLong_AsLongLong(v);
+    Py_DECREF(v);
+    if (index == -1 && PyErr_Occurred()) throw Refused{};
+    if (index != d.index()) refuse("stream: of cuda:%lld, %s on %s", index, names[0], d.str().c_str());
+  }
+  return d.index();
+}
+
+// A tensor of one of two types.
 const at::Tensor& tensor(PyObject* x, const char* name, at::ScalarType type, at::ScalarType other) {
   if (!THPVariable_Check(x)) refuse("%s: not a tensor", name);
   const at::Tensor& t = THPVariable_Unpack(x);
   if (!t.defined()) refuse("%s: not a tensor", name);
   if (t.scalar_type() != type && t.scalar_type() != other) refuse("%s: dtype %s", name, c10::toString(t.scalar_type()));
-  if (!t.is_cuda()) refuse("%s: not a CUDA tensor", name);
   return t;
 }
 const at::Tensor& tensor(PyObject* x, const char* name, at::ScalarType type, at::ScalarType other, int64_t dims) {
@@ -112,9 +138,17 @@ struct Heads {
   }
 };
 
-// The raw handle of `stream`, or of the current stream of x's device for None.
-cudaStream_t raw_stream(PyObject* stream, PyObject* x) {
-  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(THPVariable_Unpack(x).get_device()).stream();
+// Makes the call's device the current one where it is not.
+struct OnDevice {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit OnDevice(c10::DeviceIndex device) {
+    if (c10::cuda::current_device() != device) guard.set_index(device);
+  }
+};
+
+// The raw handle of `stream`, or of the device's current one for None.
+cudaStream_t raw_stream(PyObject* stream, c10::DeviceIndex device) {
+  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(device).stream();
   PyObject* v = PyObject_GetAttr(stream, n_cuda_stream);
   if (v == nullptr) throw Refused{};
   const long long s = PyLong_AsLongLong(v);
@@ -145,6 +179,10 @@ void arity(Py_ssize_t have, Py_ssize_t need) {
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     arity(n, 18);
+    static const char* const names[18] = {"k_cache", "v_cache", "q", "k", "v", "positions", "slots", "inv_freq", "pair_axis",
+                                          "interleaved", "q_norm", "k_norm", "eps", "k_scale", "v_scale", "q_out", "err_out",
+                                          "stream"};
+    const c10::DeviceIndex device = place(a, n, names);
     const pmoe_kv_desc d = cache(a[0], a[1], a[13], a[14]);
     const at::Tensor& tq = tensor(a[2], "q", at::kBFloat16, at::kBFloat16, 3);
     const int64_t T = tq.size(0), q_heads = tq.size(1);
@@ -169,7 +207,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* kn = vec(a[11], at::kBFloat16, d.head_dim, "k_norm");
     auto* out = vec(a[15], at::kBFloat16, T * q_heads * d.head_dim, "q_out");
     auto* err = vec<int32_t>(a[16], at::kInt, 1, "err_out");
-    const cudaStream_t stream = raw_stream(a[17], a[2]);
+    const cudaStream_t stream = raw_stream(a[17], device);
+    const OnDevice on(device);
     int r;
     Py_BEGIN_ALLOW_THREADS
     r = f_append(&d, q.p, q.stride, k.p, k.stride, v.p, v.stride, (int)T, (int)q_heads, pos, (int)axes, axis, freq,
@@ -184,6 +223,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     arity(n, 17);
+    static const char* const names[17] = {"k_cache", "v_cache", "q", "prefix_pages", "prefix_len", "page_table", "suffix_len",
+                                          "max_suffix", "scale", "row_seq", "k_scale", "v_scale", "out", "lse_out", "scratch",
+                                          "err_out", "stream"};
+    const c10::DeviceIndex device = place(a, n, names);
     const pmoe_kv_desc d = cache(a[0], a[1], a[10], a[11]);
     const at::Tensor& tq = tensor(a[2], "q", at::kBFloat16, at::kBFloat16, 3);
     const int64_t T = tq.size(0), q_heads = tq.size(1);
@@ -209,7 +252,8 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     auto* out = vec(a[12], at::kBFloat16, T * q_heads * d.head_dim, "out");
     auto* lse = vec<float>(a[13], at::kFloat, T * q_heads, "lse_out");
     auto* err = vec<int32_t>(a[15], at::kInt, 1, "err_out");
-    const cudaStream_t stream = raw_stream(a[16], a[2]);
+    const cudaStream_t stream = raw_stream(a[16], device);
+    const OnDevice on(device);
     void *work = nullptr, *own = nullptr;  // scratch, and what of it was taken here
     int64_t bytes;
     if (a[14] != Py_None) {
@@ -234,6 +278,9 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* sample_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     arity(n, 9);
+    static const char* const names[9] = {"logits", "u", "temperature", "top_k", "top_p", "min_p", "ids_out", "logprob_out",
+                                         "stream"};
+    const c10::DeviceIndex device = place(a, n, names);
     const at::Tensor& x = tensor(a[0], "logits", at::kFloat, at::kBFloat16, 2);
     const int64_t T = x.size(0), V = x.size(1);
     if (T > INT32_MAX || V > INT32_MAX) refuse("logits: too large");
@@ -246,10 +293,11 @@ PyObject* sample_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* m = vec<float>(a[5], at::kFloat, T, "min_p");
     auto* ids = vec<int32_t>(a[6], at::kInt, T, "ids_out");
     auto* lp = vec<float>(a[7], at::kFloat, T, "logprob_out");
-    const cudaStream_t stream = raw_stream(a[8], a[0]);
+    const cudaStream_t stream = raw_stream(a[8], device);
     const int64_t row = T > 1 ? x.stride(0) : V;
     const void* logits = x.data_ptr();
     const int bf16 = x.scalar_type() == at::kBFloat16;
+    const OnDevice on(device);
     int r;
     Py_BEGIN_ALLOW_THREADS
     r = f_sample(logits, bf16, (int)T, (int)V, row, temp, k, p, m, u, ids, lp, stream);
@@ -284,5 +332,6 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "binding of the decode-
 
 PyMODINIT_FUNC PyInit__binding(void) {
   n_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-  return n_cuda_stream == nullptr ? nullptr : PyModule_Create(&module);
+  n_device_index = PyUnicode_InternFromString("device_index");
+  return n_cuda_stream == nullptr || n_device_index == nullptr ? nullptr : PyModule_Create(&module);
 }
