@@ -267,7 +267,8 @@ def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len,
     pages, heads, page, dim = k_cache.shape
     kind = PMOE_KV_E4M3 if k_cache.dtype == torch.float8_e4m3fn else PMOE_KV_BF16
     # the scales' values do not matter for the size, but that there are some does
-    desc = pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0), k_cache.data_ptr(), k_cache.data_ptr(),
+    stride = k_cache.stride(0) if pages > 1 else heads * page * dim  # a single page has no stride
+    desc = pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride, k_cache.data_ptr(), k_cache.data_ptr(),
                         pages, page, heads, dim, kind)
     with torch.cuda.device(k_cache.device):
         return int(load().moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix))

@@ -100,19 +100,27 @@ T* vec(PyObject* x, at::ScalarType type, int64_t n, const char* name) {
   return static_cast<T*>(t.data_ptr());
 }
 
-// A paged cache: two tensors [pages, kv_heads, page_size, head_dim] of one type and strides,
-// contiguous but for the page stride.
+// Elements from page to page of [pages, kv_heads, page_size, head_dim], contiguous but for that
+// stride. A dimension of size 1 has no stride of its own, whatever torch keeps there.
+int64_t page_stride(const at::Tensor& t) {
+  const auto a = t.sizes(), s = t.strides();
+  const int64_t page = a[1] * a[2] * a[3];
+  if ((a[3] > 1 && s[3] != 1) || (a[2] > 1 && s[2] != a[3]) || (a[1] > 1 && s[1] != a[2] * a[3]))
+    refuse("k_cache, v_cache: pages are not contiguous");
+  return a[0] > 1 ? s[0] : page;
+}
+
+// A paged cache: two such tensors of one type, size and page stride.
 pmoe_kv_desc cache(PyObject* k_cache, PyObject* v_cache, PyObject* k_scale, PyObject* v_scale) {
   const at::Tensor& k = tensor(k_cache, "k_cache", at::kBFloat16, at::kFloat8_e4m3fn, 4);
   const at::Tensor& v = tensor(v_cache, "v_cache", k.scalar_type(), k.scalar_type(), 4);
-  const auto a = k.sizes(), s = k.strides();
-  if (a != v.sizes() || s != v.strides()) refuse("k_cache and v_cache: different");
+  const auto a = k.sizes();
   for (const int64_t n : a)
     if (n > INT32_MAX) refuse("k_cache, v_cache: too large");
-  if (s[3] != 1 || s[2] != a[3] || s[1] != a[2] * a[3]) refuse("k_cache, v_cache: pages are not contiguous");
   pmoe_kv_desc d{};
+  d.page_stride = page_stride(k);
+  if (a != v.sizes() || d.page_stride != page_stride(v)) refuse("k_cache and v_cache: different");
   d.num_pages = (int32_t)a[0], d.kv_heads = (int32_t)a[1], d.page_size = (int32_t)a[2], d.head_dim = (int32_t)a[3];
-  d.page_stride = s[0];
   d.dtype = k.scalar_type() == at::kBFloat16 ? PMOE_KV_BF16 : PMOE_KV_E4M3;
   if (d.dtype == PMOE_KV_E4M3) {
     if (k_scale == Py_None || v_scale == Py_None) refuse("k_scale, v_scale: needed with an e4m3 cache");
