@@ -478,7 +478,8 @@ PMOE_API int moe_kv_append(const pmoe_kv_desc* kv, const void* q, int64_t q_stri
  *                nearer bound and sets error bit 128; NULL when max_suffix = 0)
  *   out          device bf16 [T][q_heads][head_dim], 16-byte aligned
  *   lse          device fp32 [T][q_heads], or NULL
- *   scratch      device, 16-byte aligned, moe_prefix_attention_scratch_bytes(...) bytes
+ *   scratch      device, 16-byte aligned, moe_prefix_attention_scratch_bytes(...) bytes, for
+ *                one call at a time
  * A page outside [0, num_pages), or a row_seq outside [0, sequences) of a row with keys of its
  * own, sets error bit 64; such keys and values read as zeros. Error bit 16: a bounded wait expired, outputs are undefined.
  * T = 0 enqueues nothing. q_heads a multiple of kv_heads, at most 64 query heads to a kv
@@ -489,7 +490,9 @@ PMOE_API int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64_t
                                   int table_stride, int sequences, const int32_t* row_seq, const int32_t* suffix_len,
                                   int max_suffix, void* out, float* lse, void* scratch, size_t scratch_bytes,
                                   int32_t* err_out, void* stream);
-/* Bytes of scratch moe_prefix_attention needs on the current device (0 for bad arguments). */
+/* Bytes of scratch that are enough on the current device for a call of these sizes and for every
+ * smaller one: the same kv_heads, head_dim and q_heads, no larger T, prefix_len and max_suffix.
+ * (0 for bad arguments.) */
 PMOE_API size_t moe_prefix_attention_scratch_bytes(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len,
                                                    int max_suffix);
 

@@ -229,7 +229,7 @@ def _binding():
         lib = load()
         from . import _binding as b
         b.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-            "moe_kv_append", "moe_prefix_attention", "moe_prefix_attention_scratch_bytes", "moe_sample_tokens")))
+            "moe_kv_append", "moe_prefix_attention", "pmoe_attention_plan", "moe_sample_tokens")))
         _BINDING = b
     return _BINDING
 
@@ -262,7 +262,8 @@ def moe_kv_append(k_cache, v_cache, q, k, v, positions, slots, inv_freq, pair_ax
 
 
 def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len, max_suffix):
-    """Bytes of scratch a moe_prefix_attention call of these sizes needs."""
+    """Bytes of scratch that are enough for a moe_prefix_attention call of these sizes, and for
+    every one with fewer rows, a shorter prefix or a smaller max_suffix."""
     import torch
     pages, heads, page, dim = k_cache.shape
     kind = PMOE_KV_E4M3 if k_cache.dtype == torch.float8_e4m3fn else PMOE_KV_BF16
@@ -281,7 +282,8 @@ def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_tab
     Row t sees the first prefix_len keys of prefix_pages (int32), which all rows share, then
     the first suffix_len[t] (int32 [T], at most max_suffix) of page_table[row_seq[t]] (int32
     [sequences, pages]; row_seq int32 [T], default t). scale defaults to head_dim ** -0.5.
-    lse_out: fp32 [T, q_heads] or None; scratch: uint8, taken from torch's allocator for the
+    lse_out: fp32 [T, q_heads] or None; scratch: uint8, of the size that
+    moe_prefix_attention_scratch_bytes gives for the largest of the calls it serves, taken from torch's allocator for the
     call when not given. Returns out (bf16 [T, q_heads, head_dim])."""
     if out is None:
         out = _empty(q.shape, q.dtype, q, stream)

@@ -18,13 +18,13 @@
 #include <cstdarg>
 #include <cstdint>
 
-#include "../../include/pagedmoe.h"
+#include "attn_plan.h"
 
 namespace {
 
 decltype(&moe_kv_append) f_append;
 decltype(&moe_prefix_attention) f_attention;
-decltype(&moe_prefix_attention_scratch_bytes) f_scratch;
+decltype(&pmoe_attention_plan) f_plan;
 decltype(&moe_sample_tokens) f_sample;
 PyObject *n_cuda_stream, *n_device_index;
 
@@ -268,7 +268,9 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       bytes = tensor(a[14], "scratch", at::kByte, at::kByte).numel();
       work = vec(a[14], at::kByte, bytes, "scratch");
     } else {
-      bytes = (int64_t)f_scratch(&d, (int)T, (int)q_heads, (int)prefix, (int)suffix);
+      pmoe_attention_plan_desc p;
+      f_plan(&d, (int)T, (int)q_heads, (int)prefix, (int)suffix, 0, &p);  // (0 bytes where the call refuses)
+      bytes = (int64_t)p.scratch_bytes;
       if (bytes > 0) work = own = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, stream);
     }
     int r;
@@ -314,13 +316,13 @@ PyObject* sample_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// setup((append, attention, scratch, sample addresses))
+// setup((append, attention, attention plan, sample addresses))
 PyObject* setup(PyObject*, PyObject* args) {
   unsigned long long f[4];
   if (!PyArg_ParseTuple(args, "(KKKK)", &f[0], &f[1], &f[2], &f[3])) return nullptr;
   f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)f[0]);
   f_attention = reinterpret_cast<decltype(f_attention)>((uintptr_t)f[1]);
-  f_scratch = reinterpret_cast<decltype(f_scratch)>((uintptr_t)f[2]);
+  f_plan = reinterpret_cast<decltype(f_plan)>((uintptr_t)f[2]);
   f_sample = reinterpret_cast<decltype(f_sample)>((uintptr_t)f[3]);
   Py_RETURN_NONE;
 }

@@ -16,6 +16,7 @@
 // rows of 1..1,024 keys (4 kv heads of 128, bf16) 51 us; 2 rows on 100,003 shared and 256 own
 // keys 44.4 us with the combine, 4.6 TB/s; long suffixes 6.6 TB/s, 0.97 of a copy.
 #include "attn.cuh"
+#include "attn_plan.h"
 #include "tc_gemm.h"
 #include "tc_ptx.cuh"
 
@@ -729,6 +730,16 @@ int make_map(const Args& a, void* base, CUtensorMap* m) {
                        !f8 ? kTcMapBf16Sw128 : a.kv.head_dim == 128 ? kTcMapBytesSw128 : kTcMapBytesSw64);
 }
 
+// Warps of a row-head in the combine kernel: one where there are enough of them to fill the GPU,
+// more where one would read many parts in turn. The whole call in us with 1 / 4 / 16: 128
+// row-heads of 11 parts 11.3 / 10.6 / 11.4, 64 of 304 72.0 / 49.5 / 44.7, 512 of 40 32.6 / 26.6 /
+// 34.7, 2,048 of 20 27.2 / 27.7 / 66, 8,192 of 5 23.6 / 37.4 / 174.
+int join_warps(const Args& a) {
+  const int parts = a.prefix_parts + a.suffix_parts;
+  if (parts <= 32 && (int64_t)a.T * a.q_heads >= 1536) return 1;
+  return parts <= 64 ? 4 : 16;
+}
+
 template <int D, bool F8>
 int launch_all(const Args& a, int sms, cudaStream_t s) {
   using C = StreamCfg<D, F8>;
@@ -753,15 +764,11 @@ int launch_all(const Args& a, int sms, cudaStream_t s) {
       if (r != PMOE_OK) return r;
     }
   }
-  const int64_t rh = (int64_t)a.T * a.q_heads;
-  const int parts = a.prefix_parts + a.suffix_parts;
-  // Warps of a row-head: one where there are enough of them to fill the GPU, more where one
-  // would read many parts in turn. The whole call in us with 1 / 4 / 16: 128 row-heads of 11
-  // parts 11.3 / 10.6 / 11.4, 64 of 304 72.0 / 49.5 / 44.7, 512 of 40 32.6 / 26.6 / 34.7, 2,048
-  // of 20 27.2 / 27.7 / 66, 8,192 of 5 23.6 / 37.4 / 174.
-  if (parts <= 32 && rh >= 1536) return launch(what, combine_kernel<D, 1>, (unsigned)((rh + 3) / 4), 128, 0, s, true, 1, a);
-  if (parts <= 64) return launch(what, combine_kernel<D, 4>, (unsigned)rh, 128, 0, s, true, 1, a);
-  return launch(what, combine_kernel<D, 16>, (unsigned)rh, 512, 0, s, true, 1, a);
+  const unsigned rh = (unsigned)(a.T * a.q_heads);
+  const int w = join_warps(a);
+  if (w == 1) return launch(what, combine_kernel<D, 1>, (rh + 3) / 4, 128, 0, s, true, 1, a);
+  if (w == 4) return launch(what, combine_kernel<D, 4>, rh, 128, 0, s, true, 1, a);
+  return launch(what, combine_kernel<D, 16>, rh, 512, 0, s, true, 1, a);
 }
 
 struct Layout {
@@ -774,6 +781,25 @@ Layout scratch_layout(const Args& a) {
   l.base = l.ml + n * 8;
   l.bytes = l.base + (size_t)((a.T + kRowBlock - 1) / kRowBlock) * (kRowBlock + 1) * 8;
   return l;
+}
+
+// What a call and every smaller one (in T, prefix_len and max_suffix) need at most: fewer rows
+// may be cut into more parts, so the size of a call itself is no bound. R row-heads have
+//   - of the prefix, in the stream kernel at most R (warps / items + 2) parts, where an item has
+//     16 row-heads or fewer: 16 x 8 x SMs + 2 R; in the tensor-core kernel R (CTAs / groups + 2),
+//     of groups of 256: 256 x SMs + 2 R;
+//   - of their own keys R (most + 1), most <= max(4, 4 x warps / items);
+//   - of neither more than one in 4 tiles of 16 keys, and 2.
+size_t scratch_bound(const Args& a, int sms) {
+  const int64_t R = (int64_t)a.T * a.q_heads;
+  auto by_keys = [&](int keys) { return R * (((int64_t)keys + kTile - 1) / kTile / 4 + 2); };
+  int64_t n = 0;
+  if (a.prefix_len > 0) n += std::min<int64_t>(by_keys(a.prefix_len), 2 * R + 256ll * sms);
+  if (a.max_suffix > 0) {
+    const int64_t split = (4ll * kWarps * sms * a.q_heads + a.head_items - 1) / a.head_items;
+    n += std::min<int64_t>(by_keys(a.max_suffix), R + std::max<int64_t>(4 * R, split));
+  }
+  return (size_t)n * (a.kv.head_dim * 4 + 8) + (size_t)((a.T + kRowBlock - 1) / kRowBlock) * (kRowBlock + 1) * 8;
 }
 
 // Plans the tensor-core prefix and returns the CTAs of the stream kernel. The one is bound by
@@ -799,7 +825,8 @@ int split_sms(Args* a, int sms, int64_t key_bytes) {
   return ctas;
 }
 
-// Checks shared by the call and its scratch size; fills the part plan.
+// Checks shared by the call and its scratch size; fills the part plan. *sms: 0 for the current
+// device's.
 int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suffix, Args* a, int* sms) {
   const int r = check_kv(kv);
   if (r != PMOE_OK) return r;
@@ -816,7 +843,7 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
   a->max_suffix = max_suffix;
   if (a->group > kMaxGroup) return PMOE_EUNSUPPORTED;
   if (T == 0) return PMOE_OK;
-  *sms = sm_count();
+  if (*sms == 0) *sms = sm_count();
   if (*sms == 0) return PMOE_ECUDA;
 
   const int rows = T * a->group, rts = (a->group + 15) / 16;
@@ -878,12 +905,27 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suf
 
 using namespace pmoe;
 
+extern "C" int pmoe_attention_plan(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len, int max_suffix, int sms,
+                                   pmoe_attention_plan_desc* out) {
+  *out = pmoe_attention_plan_desc{};
+  if (sms < 0) return PMOE_EINVAL;
+  attn::Args a{};
+  const int r = attn::plan(kv, T, q_heads, prefix_len, max_suffix, &a, &sms);
+  if (r != PMOE_OK || T == 0) return r;
+  out->scratch_bytes = attn::scratch_layout(a).bytes;
+  out->scratch_bound = attn::scratch_bound(a, sms);
+  out->cluster = a.whole;
+  out->tc_ctas = a.tc_ctas;
+  out->prefix_parts = a.prefix_parts;
+  out->suffix_parts = a.suffix_parts;
+  out->join_warps = a.whole ? 0 : attn::join_warps(a);
+  return PMOE_OK;
+}
+
 extern "C" size_t moe_prefix_attention_scratch_bytes(const pmoe_kv_desc* kv, int T, int q_heads, int prefix_len,
                                                      int max_suffix) {
-  attn::Args a{};
-  int sms = 0;
-  if (attn::plan(kv, T, q_heads, prefix_len, max_suffix, &a, &sms) != PMOE_OK || T == 0) return 0;
-  return attn::scratch_layout(a).bytes;
+  pmoe_attention_plan_desc p;
+  return pmoe_attention_plan(kv, T, q_heads, prefix_len, max_suffix, 0, &p) == PMOE_OK ? p.scratch_bound : 0;
 }
 
 extern "C" int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64_t q_stride, int T, int q_heads,
