@@ -1,8 +1,9 @@
 """Builds libpagedmoe.so in-tree from the CUDA sources with nvcc (sm_103a only).
 
 Each translation unit is compiled in parallel, then linked into one shared library
-with a plain C ABI (include/pagedmoe.h); g++ compiles the Python binding of the decode-step
-calls (csrc/binding.cpp, against torch's headers) beside it. Rebuilds only when a source is newer than the libraries.
+with a plain C ABI (include/pagedmoe.h), which needs nvcc alone. Where torch is installed, g++
+compiles the Python binding of the decode-step calls (csrc/binding.cpp, against torch's headers)
+beside it. Each is rebuilt when a source of its own is newer, the binding also when torch is another.
 """
 
 import concurrent.futures
@@ -30,14 +31,38 @@ def _sources():
 
 
 def _deps():
-    return [BINDING_SRC] + _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(HERE, "..", "include", "*.h"))
+    return _sources() + [p for d in (CSRC, os.path.join(HERE, "..", "include")) for e in ("*.h", "*.cuh")
+                         for p in glob.glob(os.path.join(d, e))]
+
+
+def _stale(lib, deps):
+    return not os.path.exists(lib) or any(os.path.getmtime(p) > os.path.getmtime(lib) for p in deps)
+
+
+def _torch():
+    """Where torch is installed, or None; without importing it."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None and spec.submodule_search_locations else None
+
+
+def _torch_id(torch):
+    """What the binding is built against."""
+    version = os.path.join(torch, "version.py")
+    return torch + "\n" + (open(version).read() if os.path.exists(version) else "")
+
+
+def _binding_stale():
+    torch = _torch()
+    if torch is None:
+        return False
+    stamp = os.path.join(BUILD, "binding.torch")
+    if not os.path.exists(stamp) or open(stamp).read() != _torch_id(torch):
+        return True
+    return _stale(BINDING, [BINDING_SRC] + [p for p in _deps() if p.endswith(".h")])
 
 
 def needs_build():
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    return _stale(LIB, _deps()) or _binding_stale()
 
 
 def _compile(src, verbose_ptxas=False):
@@ -53,7 +78,7 @@ def _compile(src, verbose_ptxas=False):
 
 def _compile_binding():
     tmp = BINDING + ".tmp"
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = _torch()
     lib = os.path.join(torch, "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(torch, "include"), "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
@@ -63,27 +88,35 @@ def _compile_binding():
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "binding.torch"), "w") as f:
+        f.write(_torch_id(torch))
 
 
-def build(force=False, verbose_ptxas=False, quiet=True):
-    if not force and not needs_build():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        binding = ex.submit(_compile_binding)
-        results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        binding.result()
-    if verbose_ptxas:
-        for _, log in results:
-            sys.stderr.write(log)
-    objs = [o for o, _ in results]
+def _link(objs):
     tmp = LIB + ".tmp"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-ldl", "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force=False, verbose_ptxas=False, quiet=True):
+    library, binding = force or _stale(LIB, _deps()), _torch() is not None and (force or _binding_stale())
+    if not library and not binding:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    srcs = _sources() if library else []
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        made = ex.submit(_compile_binding) if binding else None
+        results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        if made is not None:
+            made.result()
+    if verbose_ptxas:
+        for _, log in results:
+            sys.stderr.write(log)
+    if library:
+        _link([o for o, _ in results])
     if not quiet:
         print(f"built {LIB}")
     return LIB
