@@ -47,3 +47,36 @@ def test_every_batch_below_a_size_fits_its_bound():
                                        (0, 4096, 16, 1, 64), (30000, 0, 8, 8, 64), (5000, 5000, 48, 1, 128)):
         most = plan(512, Hq, Hkv, D, 16, False, prefix, suffix).scratch_bound
         assert all(plan(T, Hq, Hkv, D, 16, False, prefix, suffix).scratch_bytes <= most for T in range(1, 513))
+
+
+# T, Hq, Hkv, D, page, e4m3, prefix, suffix of test_gpu_attention_paths, by what they have to reach
+LARGE_GROUPS = [(3, 64, 2, 128, 128, False, 900, 5000), (70, 60, 1, 64, 16, True, 100, 300), (60, 40, 1, 128, 16, True, 300, 600)]
+MANY_PARTS = [(1, 16, 4, 128, 16, False, 30001, 100), (2, 32, 4, 64, 32, True, 30000, 256), (1, 1, 1, 64, 16, False, 0, 60000),
+              (2, 5, 1, 128, 64, False, 0, 33333), (3, 4, 4, 64, 16, True, 0, 9000)]
+TWO_ROUNDS = [(1, 8, 1, 64, 16, False, 100000, 40), (2, 8, 1, 128, 16, True, 40000, 0)]
+TC_MANY_PARTS = [(16, 16, 1, 128, 16, False, 20000, 30), (32, 8, 1, 64, 64, True, 20011, 0), (16, 16, 1, 64, 32, True, 12000, 300)]
+TC_LARGE_GROUP = [(5, 64, 1, 128, 16, False, 20000, 64)]
+TC_ROW_BLOCKS = [(2100, 2, 1, 64, 16, False, 700, 5), (2050, 4, 2, 128, 32, True, 600, 20), (4100, 1, 1, 64, 16, False, 2000, 3)]
+ALL_PATHS = LARGE_GROUPS + MANY_PARTS + TWO_ROUNDS + TC_MANY_PARTS + TC_LARGE_GROUP + TC_ROW_BLOCKS
+
+
+def parts(p):
+    return p.prefix_parts + p.suffix_parts
+
+
+def test_the_sizes_reach_their_paths():
+    for c in LARGE_GROUPS:  # several 16-row items of a token and kv head, in parts of the stream kernel
+        p = plan(*c)
+        assert p.cluster == 0 and p.tc_ctas == 0 and c[1] // c[2] > 16 and p.suffix_parts > 1 and p.prefix_parts > 1
+    for c in MANY_PARTS + TWO_ROUNDS:
+        p = plan(*c)
+        assert p.cluster == 0 and p.tc_ctas == 0 and parts(p) > 64 and p.join_warps == 16
+    for c in TWO_ROUNDS:  # a lane of the join looks at more than one part
+        assert parts(plan(*c)) > 32 * 16
+    for c in TC_MANY_PARTS:
+        p = plan(*c)
+        assert p.tc_ctas > 0 and parts(p) > 64 and p.join_warps == 16
+    for c in TC_LARGE_GROUP:
+        assert plan(*c).tc_ctas > 0 and c[1] // c[2] > 16
+    for c in TC_ROW_BLOCKS:  # more rows than one launch of the stream kernel takes
+        assert plan(*c).tc_ctas > 0 and c[0] > 2048 and c[7] > 0
