@@ -501,7 +501,8 @@ PMOE_API size_t moe_prefix_attention_scratch_bytes(const pmoe_kv_desc* kv, int T
  * With m the row's largest logit, token i weighs n_i = floor(exp((x_i - m) / temperature) *
  * 2^31), the exponential in fp32 as exp2((x_i - m) * (log2(e) / temperature)) and within 2^-17
  * of its value; from there on every sum and comparison is in whole numbers, so a draw depends
- * on no order of summation. The tokens in descending order of their logits, ties to the lower id, are cut to
+ * on no order of summation. The tokens in descending order of their logits, ties to the lower
+ * id, are cut to
  *   the first top_k                                          (top_k <= 0 or >= V: all),
  *   of these the shortest head whose weights reach floor(total * top_p)   (top_p >= 1: all;
  *   at least one token), and

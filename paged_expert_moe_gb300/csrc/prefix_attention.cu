@@ -741,7 +741,7 @@ int join_warps(const Args& a) {
 }
 
 template <int D, bool F8>
-int launch_all(const Args& a, int sms, cudaStream_t s) {
+int launch_all(const Args& a, cudaStream_t s) {
   using C = StreamCfg<D, F8>;
   int r = a.tc_ctas > 0 ? launch_prefix_tc(a, s) : PMOE_OK;
   if (r != PMOE_OK) return r;
@@ -969,6 +969,6 @@ extern "C" int moe_prefix_attention(const pmoe_kv_desc* kv, const void* q, int64
   a.base = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(scratch) + lay.base);
   cudaStream_t s = (cudaStream_t)stream;
   const bool f8 = kv->dtype == PMOE_KV_E4M3;
-  if (kv->head_dim == 128) return f8 ? attn::launch_all<128, true>(a, sms, s) : attn::launch_all<128, false>(a, sms, s);
-  return f8 ? attn::launch_all<64, true>(a, sms, s) : attn::launch_all<64, false>(a, sms, s);
+  if (kv->head_dim == 128) return f8 ? attn::launch_all<128, true>(a, s) : attn::launch_all<128, false>(a, s);
+  return f8 ? attn::launch_all<64, true>(a, s) : attn::launch_all<64, false>(a, s);
 }

@@ -187,41 +187,37 @@ __global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
       const float ks = F8 ? a.kv.k_scale[sg.h] : 1.f;
       const uint32_t flip = (a.scale < 0.f) != (ks < 0.f) ? 0x80008000u : 0u;
       const int c = row % LPR;
-      constexpr int kPasses = LPR, kAhead = LPR;  // rows of a thread, all in flight
+      uint4 v[LPR];  // LPR rows a thread, all in flight
 #pragma unroll
-      for (int p0 = 0; p0 < kPasses; p0 += kAhead) {
-        uint4 v[kAhead];
-#pragma unroll
-        for (int p = 0; p < kAhead; ++p) {
-          const int i = q * 128 + row / LPR + (p0 + p) * (128 / LPR);
-          v[p] = make_uint4(0, 0, 0, 0);
-          if (i < sg.rows) {
-            const int rr = sg.row0 + i, t = row_token(a, rr);
-            v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)t * a.q_stride +
-                                                        (sg.h * a.group + rr - t * a.group) * D + c * 8));
-          }
+      for (int p = 0; p < LPR; ++p) {
+        const int i = q * 128 + row / LPR + p * (128 / LPR);
+        v[p] = make_uint4(0, 0, 0, 0);
+        if (i < sg.rows) {
+          const int rr = sg.row0 + i, t = row_token(a, rr);
+          v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)t * a.q_stride +
+                                                      (sg.h * a.group + rr - t * a.group) * D + c * 8));
         }
+      }
 #pragma unroll
-        for (int p = 0; p < kAhead; ++p) {
-          const int r = row / LPR + (p0 + p) * (128 / LPR);
-          uint32_t w[4] = {v[p].x ^ flip, v[p].y ^ flip, v[p].z ^ flip, v[p].w ^ flip};
-          if (F8) {
-            float mx = 0.f;
+      for (int p = 0; p < LPR; ++p) {
+        const int r = row / LPR + p * (128 / LPR);
+        uint32_t w[4] = {v[p].x ^ flip, v[p].y ^ flip, v[p].z ^ flip, v[p].w ^ flip};
+        if (F8) {
+          float mx = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+          for (int k = 0; k < 4; ++k)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int e = row_exponent(mx);
-            const float factor = fabsf(a.scale) * fabsf(ks) * pow2(e), down = factor != 0.f ? pow2(-e) : 0.f;
+          for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int e = row_exponent(mx);
+          const float factor = fabsf(a.scale) * fabsf(ks) * pow2(e), down = factor != 0.f ? pow2(-e) : 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-            if (c == 0) qmul[q * 128 + r] = factor != 0.f ? factor : 1.f;
-          }
-          *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+          if (c == 0) qmul[q * 128 + r] = factor != 0.f ? factor : 1.f;
         }
+        *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_async();
       warp_arrive(&b.qfull[q]);
