@@ -475,7 +475,11 @@ PMOE_API int moe_kv_append(const pmoe_kv_desc* kv, const void* q, int64_t q_stri
  *   row_seq      device int32 [T], the table row of each query row, in [0, sequences), or
  *                NULL: row t. Several query rows may share one
  *   suffix_len   device int32 [T], each 0..max_suffix (a length outside counts as the
- *                nearer bound and sets error bit 128; NULL when max_suffix = 0)
+ *                nearer bound and sets error bit 128; NULL when max_suffix = 0).
+ *                The work is divided by max_suffix, since the lengths are on the device: a
+ *                bound within a few times the longest row costs little, one far above it much
+ *                (256 rows of up to 1,024 own keys 59 us with 1,024, 95 with 8,192, 1,250 with
+ *                131,072)
  *   out          device bf16 [T][q_heads][head_dim], 16-byte aligned
  *   lse          device fp32 [T][q_heads], or NULL
  *   scratch      device, 16-byte aligned, moe_prefix_attention_scratch_bytes(...) bytes, for

@@ -18,7 +18,7 @@
 // between threads but the norm's sum.
 //
 // Measured (32 + 4 + 4 heads of 128, bf16): 8,192 tokens 30.9 us, 5.4 TB/s of the 6.8 a copy
-// reaches, with the issue slots 70% busy; 4,099 tokens of 48 heads of 64 11.4 us, 4.4 TB/s; one
+// reaches, with the issue slots 67% busy; 4,099 tokens of 48 heads of 64 11.4 us, 4.4 TB/s; one
 // token 3.0 us, a launch.
 #include "pmoe_internal.h"
 

@@ -9,12 +9,15 @@
 // barrier of the block: a ring of 16-key tiles of its own that TMA fills (a tile lies inside
 // one page; one box for K, one for V), mma.sync on 16 query rows, softmax in registers. The
 // (item, tile) units of all items, in order, are cut into equal runs, one a warp of every
-// SM, whatever the lengths; a warp whose run ends inside an item leaves a part of it. An item
-// counts for kHead units more than its tiles: short ones cost more than their keys. Calls of few
-// and short items take a CTA or a cluster an item instead, which joins its warps' parts itself
-// (4 rows of 564 keys 7.7 us, 1 of 2,064 9.1). Measured: 256
-// rows of 1..1,024 keys (4 kv heads of 128, bf16) 51 us; 2 rows on 100,003 shared and 256 own
-// keys 44.4 us with the combine, 4.6 TB/s; long suffixes 6.6 TB/s, 0.97 of a copy.
+// SM; a warp whose run ends inside an item leaves a part of it. An item counts for kHead units
+// more than its tiles: short ones cost more than their keys. So that an item has few parts, whose
+// room is planned on the host, a run is at least a fraction of max_suffix: where that is far above
+// the lengths, few warps have work (256 rows of 1..1,024 own keys on 32,768 shared ones: 147 us with
+// a bound of 1,024, 206 with 8,192, 1,356 with 131,072). Calls of few and short items take a CTA or
+// a cluster an item instead, which joins its warps' parts itself (4 rows of 564 keys 7.8 us, 1 of
+// 2,064 9.1). Measured, with the combine: 256 rows of 1..1,024 keys (4 kv heads of 128, bf16) 59 us;
+// 64 rows of 1,000..16,000 172 us, 6.4 TB/s, 0.95 of a copy; 2 rows on 100,003 shared and 256 own
+// keys 45 us, 4.6 TB/s.
 #include "attn.cuh"
 #include "attn_plan.h"
 #include "tc_gemm.h"

@@ -23,8 +23,8 @@
 // Uncut rows take steps 1 and 4.
 //
 // Measured: a row of 32,000 fp32 logits with top_k 50 and top_p 0.9 7.2 us, uncut 5.0; 64 bf16
-// rows of 131,072 of all kinds 27.9 us; 256 fp32 rows of 160,001 100 us, 1.6 TB/s, where a read
-// alone would take 24. What holds them up is the chain of a row: its some ten exchanges between
+// rows of 131,072 of all kinds 28 to 36 us by what the slowest rows need; 256 fp32 rows of 160,001
+// 94 to 102 us, 1.6 TB/s, where a read alone would take 24. What holds them up is the chain of a row: its some ten exchanges between
 // the CTAs and passes of a few hundred cycles each, on the 36 clusters that find room at once.
 #include "pmoe_internal.h"
 
