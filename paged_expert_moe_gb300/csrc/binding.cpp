@@ -67,7 +67,11 @@ c10::DeviceIndex place(PyObject* const* a, Py_ssize_t n, const char* const* name
   }
   if (a[n - 1] != Py_None) {
     PyObject* v = PyObject_GetAttr(a[n - 1], n_device_index);
-    if (v == nullptr) throw Refused{};
+    if (v == nullptr) {  // another library's stream, which need not say
+      if (!PyErr_ExceptionMatches(PyExc_AttributeError)) throw Refused{};
+      PyErr_Clear();
+      return d.index();
+    }
     const long long index = PyLong_AsLongLong(v);
     Py_DECREF(v);
     if (index == -1 && PyErr_Occurred()) throw Refused{};
