@@ -529,6 +529,141 @@ PMOE_API int moe_sample_tokens(const void* logits, int is_bf16, int T, int V, in
                                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                                const float* u, int32_t* ids_out, float* logprob_out, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * A step over requests of different lengths: some generate one token each, others are still
+ * reading their prompts. The article's stack serves one batch of equal steps and has no
+ * counterpart of these calls. Conventions as above; err_out has further bits: 256 a request got
+ * no pages or rows, 512 a token id out of range. */
+
+/*
+ * moe_batch_tables - the pages, slots, positions and row ranges of a step's tokens, from the
+ * requests' lengths alone.
+ * Request r has lens[r] keys in the cache, in the pages page_table[r][0 .. ceil(lens[r] /
+ * page_size) - 1], and new_len[r] new tokens in this step; 0: it rests; -1: it has ended. First
+ * the ended requests' pages go onto the stack of free pages, in order of request and page. Then the
+ * others' new pages come off its top, in the same order: the k-th new page of the step is
+ * free_pages[n - 1 - k], n the stack's height. A request whose tokens do not all fit, its rows into T,
+ * its pages into its table row or the pages needed up to and with it into the stack, gets no
+ * page and stores nothing (its lens_out is lens; error bit 256).
+ *   page_table   device int32 [R][table_stride], entries of new pages are written
+ *   free_pages   device int32 [free_capacity], the lowest free_count of them free
+ *   free_count, free_count_out  device int32 [1]; may be the same
+ *   lens, new_len  device int32 [R]
+ *   lens_out     device int32 [R], keys after the step (0 for an ended request); may be lens
+ *   q_start      device int32 [R + 1]: request r's tokens are rows q_start[r] .. q_start[r + 1] - 1
+ *                of the step (ends beyond T count as T)
+ *   positions    device int32 [T], lens[r] + i for the i-th token of request r
+ *   slots        device int32 [T], the cache row of each token, -1 where it is not stored
+ *   row_seq      device int32 [T], the request of each row
+ *   row_len      device int32 [T] or NULL, position + 1 (0 where not stored): the keys that
+ *                moe_prefix_attention's row may see
+ * Rows from q_start[R] on: position 0, slot -1, row_seq -1, row_len 0, so that a step padded to a
+ * fixed T (a captured graph's) appends nothing for them. A length outside [0, table_stride *
+ * page_size], a new_len below -1 (taken as 0) or a count outside the stack counts as the nearer
+ * bound and sets error bit 128; so does a page that the full stack has no room for, which is lost. A page outside
+ * [0, num_pages) gives slot -1 and error bit 64. The buffers must not overlap but where said.
+ * R in 0..8192, T in 0..2^24, num_pages * page_size < 2^31. PMOE_EINVAL on bad arguments,
+ * PMOE_EUNSUPPORTED for another page size than moe_kv_append's.
+ */
+PMOE_API int moe_batch_tables(int32_t* page_table, int table_stride, int page_size, int num_pages, int32_t* free_pages,
+                              int free_capacity, const int32_t* free_count, const int32_t* lens, const int32_t* new_len,
+                              int R, int T, int32_t* lens_out, int32_t* free_count_out, int32_t* q_start,
+                              int32_t* positions, int32_t* slots, int32_t* row_seq, int32_t* row_len, int32_t* err_out,
+                              void* stream);
+
+/*
+ * moe_chunk_attention - attention of each request's new tokens over its own pages: pieces of
+ * prompts, single tokens and any mixture of them in one call.
+ * Request r's rows are t = q_start[r] .. q_start[r + 1] - 1, n of them, the last ones of its
+ * kv_len[r] keys: row q_start[r] + i stands at position p = kv_len[r] - n + i and sees the keys j
+ * <= p of the pages page_table[r][..]; with a window only those with j > p - window or j <
+ * sinks. out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j, lse[t][h] = log sum_j
+ * exp(scale * q[t][h] . k_j). A row that sees no key (p < 0) gets out = 0, lse = -inf. What the cache
+ * holds in rows that a query does not see is never used, whatever it is; rows of q outside all
+ * requests are not read, and left as they were in out and lse.
+ * Statistics and sums are fp32; the weights are rounded to 16 bits before they meet the
+ * values (bf16, or fp16 with an e4m3 cache).
+ *   q            device bf16 [T][q_heads][head_dim], tokens q_stride elements apart; 16-byte
+ *                aligned, q_stride a multiple of 8
+ *   q_start      device int32 [R + 1], ascending, in [0, T]
+ *   kv_len       device int32 [R], keys of each request, its new ones among them
+ *   page_table   device int32 [R][table_stride], table_stride * page_size <= 2^30
+ *   window       0: none; sinks: the first keys that stay visible beside it (without one: unused)
+ *   out          device bf16 [T][q_heads][head_dim], 16-byte aligned
+ *   lse          device fp32 [T][q_heads], or NULL
+ *   scratch      device, 16-byte aligned, moe_chunk_attention_scratch_bytes(...) bytes, for one
+ *                call at a time
+ * A start outside [0, T] and a length outside [0, table_stride * page_size] count as the nearer
+ * bound, a request whose start lies behind its end has no rows, one whose rows with those before it exceed T
+ * neither; each sets error bit 128. A page outside [0, num_pages) reads as zeros and sets error bit 64. Error bit 16: a
+ * bounded wait expired, outputs are undefined. T = 0 or R = 0 enqueues nothing. R up to 2^20,
+ * q_heads a multiple of kv_heads, at most 64 query heads to a kv head (else PMOE_EUNSUPPORTED), T *
+ * q_heads < 2^24. PMOE_EINVAL on bad arguments.
+ */
+PMOE_API int moe_chunk_attention(const pmoe_kv_desc* kv, const void* q, int64_t q_stride, int T, int q_heads, float scale,
+                                 const int32_t* q_start, const int32_t* kv_len, int R, const int32_t* page_table,
+                                 int table_stride, int window, int sinks, void* out, float* lse, void* scratch,
+                                 size_t scratch_bytes, int32_t* err_out, void* stream);
+/* Bytes of scratch that are enough on the current device for a call of these sizes and for every
+ * smaller one: the same kv_heads, head_dim and q_heads, no larger T and R. (0 for bad arguments.) */
+PMOE_API size_t moe_chunk_attention_scratch_bytes(const pmoe_kv_desc* kv, int T, int q_heads, int R);
+
+typedef enum { PMOE_SCORE_SOFTMAX = 0, PMOE_SCORE_SIGMOID = 1 } pmoe_scoring;
+
+/*
+ * moe_router_select - the choice of experts by scores, a balance bias and expert groups;
+ * moe_router_topk is the softmax without either.
+ * s_e = softmax over all E logits, or 1 / (1 + exp(-x_e)); c_e = s_e + bias[e]. The experts lie in
+ * `groups` equal groups of neighbours; a group's value is the sum of its group_top (1 or 2) largest c
+ * (of groups of one expert: its c), and the top_groups groups of the largest values are kept, ties
+ * to the lower group. In them the top_k largest c are selected, ordered by descending c, ties to the
+ * lower id. The order is that of c in exact arithmetic, as far as fp64 tells (without a bias: of the
+ * logits). w = s of the selected, divided by their sum when renormalize != 0 (0 where that is 0), times
+ * `scale`. A NaN logit counts as -inf, a NaN bias as -inf; of softmax rows with logits of +inf, or with
+ * none above -inf, the largest share the row.
+ *   logits   device, fp32 (is_bf16 = 0) or bf16 [T][E], rows row_stride elements apart; aligned to
+ *            its element
+ *   bias     device fp32 [E], or NULL
+ *   ids_out  device int32 [T][top_k]
+ *   w_out    device fp32 [T][top_k]
+ * T = 0 enqueues nothing. E in 1..1024, top_k in 1..min(E / groups * top_groups, 32), groups in 1..32
+ * that divide E, top_groups in 1..groups. PMOE_EINVAL on bad arguments.
+ */
+PMOE_API int moe_router_select(const void* logits, int is_bf16, int T, int E, int64_t row_stride, int top_k, int scoring,
+                               const float* bias, int groups, int top_groups, int group_top, int renormalize, float scale,
+                               int32_t* ids_out, float* w_out, void* stream);
+
+/*
+ * moe_adjust_logits - penalties for repeated tokens, biases and a grammar's mask, ahead of
+ * moe_sample_tokens. For token id v of row t, x its logit, in this order, in fp32:
+ *   in history[t]              x <- x / repetition if x > 0, else x * repetition
+ *   n > 0 times of its output  x <- x - frequency * n - presence
+ *   in bias_ids[t]             x <- x + bias (of several entries of one id the last one's)
+ *   not allowed by mask[t]     x <- -inf
+ * The first prompt_len[t] of the history_len[t] ids of history[t] are its prompt, the others its
+ * output.
+ *   logits   device, fp32 (is_bf16 = 0) or bf16 [T][V], rows row_stride elements apart; aligned to
+ *            its element
+ *   history  device int32 [T][max_history], rows history_stride apart; max_history 0: none. An id
+ *            outside [0, V) is left out and sets error bit 512. At most 2^19 - 1
+ *   prompt_len  device int32 [T], in [0, history_len], or NULL: 0; history_len device int32 [T], in
+ *            [0, max_history] (outside: the nearer bound, and error bit 128)
+ *   repetition  device fp32 [T], above 0; frequency, presence device fp32 [T]; NULL: 1, 0, 0
+ *   bias_ids device int32 [T][biases], -1: none (another id outside [0, V): the same, and error
+ *            bit 512); bias device fp32 [T][biases]; at most 4,095
+ *   mask     device uint32 [T][mask_stride], at least ceil(V / 32) words a row, bit v % 32 of word
+ *            v / 32 set: v is allowed; NULL: all are
+ *   out      device, fp32 or bf16 [T][V], rows out_stride apart; may be logits, of the same type and
+ *            stride (then only what changes is written), else must not overlap it
+ * V in 1..262144. T = 0 enqueues nothing. PMOE_EINVAL on bad arguments.
+ */
+PMOE_API int moe_adjust_logits(const void* logits, int is_bf16, int T, int V, int64_t row_stride, const int32_t* history,
+                               int64_t history_stride, int max_history, const int32_t* prompt_len,
+                               const int32_t* history_len, const float* repetition, const float* frequency,
+                               const float* presence, const int32_t* bias_ids, const float* bias, int biases,
+                               const uint32_t* mask, int64_t mask_stride, void* out, int out_is_bf16, int64_t out_stride,
+                               int32_t* err_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

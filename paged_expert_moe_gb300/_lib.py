@@ -8,6 +8,7 @@ fails with an error (there is no fallback path).
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -19,6 +20,7 @@ PMOE_OK, PMOE_EINVAL, PMOE_ENOMEM, PMOE_EHOSTALLOC, PMOE_ECUDA, PMOE_EUNSUPPORTE
 PMOE_BF16, PMOE_FP8_BLOCK128, PMOE_INT4_GPTQ_G128, PMOE_MXFP4, PMOE_NVFP4 = 0, 1, 2, 3, 4
 PMOE_PAGEIN_COPY_ENGINE, PMOE_PAGEIN_SM_PULL = 0, 1
 PMOE_KV_BF16, PMOE_KV_E4M3 = 0, 1
+PMOE_SCORE_SOFTMAX, PMOE_SCORE_SIGMOID = 0, 1
 
 
 class PmoeError(RuntimeError):
@@ -87,6 +89,12 @@ _SIGS = {
                               _I, _P, _P, _P, ctypes.c_size_t, _P, _P], _I),
     "moe_prefix_attention_scratch_bytes": ([ctypes.POINTER(pmoe_kv_desc), _I, _I, _I, _I], ctypes.c_size_t),
     "moe_sample_tokens": ([_P, _I, _I, _I, _L, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "moe_batch_tables": ([_P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "moe_chunk_attention": ([ctypes.POINTER(pmoe_kv_desc), _P, _L, _I, _I, ctypes.c_float, _P, _P, _I, _P, _I, _I, _I, _P,
+                             _P, _P, ctypes.c_size_t, _P, _P], _I),
+    "moe_chunk_attention_scratch_bytes": ([ctypes.POINTER(pmoe_kv_desc), _I, _I, _I], ctypes.c_size_t),
+    "moe_router_select": ([_P, _I, _I, _I, _L, _I, _I, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P], _I),
+    "moe_adjust_logits": ([_P, _I, _I, _I, _L, _P, _L, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _L, _P, _I, _L, _P, _P], _I),
     "moe_paged_stack_forward": ([_P, _P, _I, _P, _P, _P, _P, _P], _I),
 }
 EXPORTED = tuple(_SIGS)
@@ -216,7 +224,7 @@ def moe_decode_forward_noalloc(experts, stride, E, top_k, H, I, fmt, x, ids, w, 
     return y
 
 
-# The calls of a decode step (below) go through _binding, which checks their tensors and calls
+# The calls of a serving step (below) go through _binding, which checks their tensors and calls
 # the library in C++: their kernels take a few microseconds, less than the checks in Python.
 
 _BINDING = None
@@ -229,7 +237,8 @@ def _binding():
         lib = load()
         from . import _binding as b
         b.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-            "moe_kv_append", "moe_prefix_attention", "pmoe_attention_plan", "moe_sample_tokens")))
+            "moe_kv_append", "moe_prefix_attention", "pmoe_attention_plan", "moe_sample_tokens", "moe_batch_tables",
+            "moe_chunk_attention", "moe_chunk_attention_scratch_bytes", "moe_router_select", "moe_adjust_logits")))
         _BINDING = b
     return _BINDING
 
@@ -261,18 +270,23 @@ def moe_kv_append(k_cache, v_cache, q, k, v, positions, slots, inv_freq, pair_ax
     return q_out
 
 
-def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len, max_suffix):
-    """Bytes of scratch that are enough for a moe_prefix_attention call of these sizes, and for
-    every one with fewer rows, a shorter prefix or a smaller max_suffix."""
+def _desc(k_cache, v_cache):
+    """A cache's descriptor, for the sizes of scratch."""
     import torch
     pages, heads, page, dim = k_cache.shape
     kind = PMOE_KV_E4M3 if k_cache.dtype == torch.float8_e4m3fn else PMOE_KV_BF16
     # the scales' values do not matter for the size, but that there are some does
     stride = k_cache.stride(0) if pages > 1 else heads * page * dim  # a single page has no stride
-    desc = pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride, k_cache.data_ptr(), k_cache.data_ptr(),
+    return pmoe_kv_desc(k_cache.data_ptr(), v_cache.data_ptr(), stride, k_cache.data_ptr(), k_cache.data_ptr(),
                         pages, page, heads, dim, kind)
+
+
+def moe_prefix_attention_scratch_bytes(k_cache, v_cache, T, q_heads, prefix_len, max_suffix):
+    """Bytes of scratch that are enough for a moe_prefix_attention call of these sizes, and for
+    every one with fewer rows, a shorter prefix or a smaller max_suffix."""
+    import torch
     with torch.cuda.device(k_cache.device):
-        return int(load().moe_prefix_attention_scratch_bytes(desc, T, q_heads, prefix_len, max_suffix))
+        return int(load().moe_prefix_attention_scratch_bytes(_desc(k_cache, v_cache), T, q_heads, prefix_len, max_suffix))
 
 
 def moe_prefix_attention(k_cache, v_cache, q, prefix_pages, prefix_len, page_table, suffix_len, max_suffix, scale=None,
@@ -308,6 +322,108 @@ def moe_sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p
     if status:
         raise PmoeError(status, "moe_sample_tokens")
     return ids_out
+
+
+class BatchTables(NamedTuple):
+    """What moe_batch_tables gives: int32 tensors."""
+    lens: object        # [R] keys of each request after the step
+    free_count: object  # [1] free pages after it
+    q_start: object     # [R + 1] first row of each request
+    positions: object   # [T]
+    slots: object       # [T], -1: not stored
+    row_seq: object     # [T] request of each row, -1: none
+    row_len: object     # [T] keys up to each row's token, 0: not stored
+
+
+def moe_batch_tables(page_table, free_pages, free_count, lens, new_len, T, page_size, num_pages, lens_out=None,
+                     free_count_out=None, q_start=None, positions=None, slots=None, row_seq=None, row_len=None, err_out=None,
+                     stream=None):
+    """Pages, slots, positions and row ranges of a step of T rows, from the requests' lengths.
+    page_table: int32 [R, pages], new pages are written to it; free_pages: int32 [n], a stack of
+    which the lowest free_count (int32 [1]) are free; lens, new_len: int32 [R], keys in the cache and
+    new tokens (0: rests, -1: ended, its pages are given back). lens_out may be lens, free_count_out
+    may be free_count. Returns BatchTables."""
+    def out(x, n):
+        import torch
+        return _empty(n, torch.int32, page_table, stream) if x is None else x
+
+    R = page_table.shape[0]
+    r = BatchTables(out(lens_out, R), out(free_count_out, 1), out(q_start, R + 1), out(positions, T), out(slots, T),
+                    out(row_seq, T), out(row_len, T))
+    status = (_BINDING or _binding()).batch_tables(
+        page_table, free_pages, free_count, lens, new_len, T, page_size, num_pages, r.lens, r.free_count, r.q_start,
+        r.positions, r.slots, r.row_seq, r.row_len, err_out, stream)
+    if status:
+        raise PmoeError(status, "moe_batch_tables")
+    return r
+
+
+def moe_chunk_attention_scratch_bytes(k_cache, v_cache, T, q_heads, requests):
+    """Bytes of scratch that are enough for a moe_chunk_attention call of these sizes, and for every
+    one with fewer rows or requests."""
+    import torch
+    with torch.cuda.device(k_cache.device):
+        return int(load().moe_chunk_attention_scratch_bytes(_desc(k_cache, v_cache), T, q_heads, requests))
+
+
+def moe_chunk_attention(k_cache, v_cache, q, q_start, kv_len, page_table, window=0, sinks=0, scale=None, k_scale=None,
+                        v_scale=None, out=None, lse_out=None, scratch=None, err_out=None, stream=None):
+    """Attention of each request's new tokens over its own pages of a paged cache (as
+    moe_kv_append's). q: bf16 [T, q_heads, head_dim]; rows q_start[r] .. q_start[r + 1] - 1 (int32
+    [R + 1]) are the last of request r's kv_len[r] keys (int32 [R]), in the pages page_table[r] (int32
+    [R, pages]). A row sees the keys up to its own; with a window only the last `window` of these, and
+    the first `sinks`. scale defaults to head_dim ** -0.5. lse_out: fp32 [T, q_heads] or None;
+    scratch: uint8, of the size that moe_chunk_attention_scratch_bytes gives, taken from torch's
+    allocator for the call when not given. Returns out (bf16 [T, q_heads, head_dim]); rows of no
+    request are left as they were there."""
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+    status = (_BINDING or _binding()).chunk_attention(
+        k_cache, v_cache, q, q_start, kv_len, page_table, window, sinks, scale, k_scale, v_scale, out, lse_out, scratch,
+        err_out, stream)
+    if status:
+        raise PmoeError(status, "moe_chunk_attention")
+    return out
+
+
+def moe_router_select(logits, top_k, scoring="softmax", bias=None, groups=1, top_groups=1, group_top=1, renormalize=True,
+                      scale=1.0, ids_out=None, w_out=None, stream=None):
+    """Experts by scores: logits (CUDA fp32 or bf16 [T, E], rows contiguous) -> (ids int32 [T, top_k],
+    w fp32 [T, top_k]). scoring: "softmax" or "sigmoid"; bias (fp32 [E]) is added for the choice
+    alone; of `groups` groups of neighbouring experts the top_groups with the largest sums of their
+    group_top (1 or 2) best are kept; w is renormalised and multiplied by scale."""
+    import torch
+    if scoring not in ("softmax", "sigmoid"):
+        raise AssertionError(f"scoring: {scoring!r}")
+    T = logits.shape[0]
+    if ids_out is None:
+        ids_out = _empty((T, max(top_k, 0)), torch.int32, logits, stream)
+    if w_out is None:
+        w_out = _empty((T, max(top_k, 0)), torch.float32, logits, stream)
+    status = (_BINDING or _binding()).router_select(
+        logits, bias, top_k, PMOE_SCORE_SIGMOID if scoring == "sigmoid" else PMOE_SCORE_SOFTMAX, groups, top_groups,
+        group_top, renormalize, scale, ids_out, w_out, stream)
+    if status:
+        raise PmoeError(status, "moe_router_select")
+    return ids_out, w_out
+
+
+def moe_adjust_logits(logits, history=None, prompt_len=None, history_len=None, repetition=None, frequency=None,
+                      presence=None, bias_ids=None, bias=None, mask=None, out=None, err_out=None, stream=None):
+    """Penalties, biases and masks on logits (CUDA fp32 or bf16 [T, V], rows contiguous). history: int32
+    [T, n], of which the first history_len[t] ids count (int32 [T]), the first prompt_len[t] of these
+    as the prompt; repetition (of prompt and output), frequency and presence (of the output): fp32
+    [T]; bias_ids: int32 [T, B], -1 = none, with bias fp32 [T, B]; mask: int32 [T, words], bit v % 32 of
+    word v // 32 set where v is allowed. out: fp32 or bf16 [T, V], default fp32; logits itself for a
+    change in place. Returns out."""
+    if out is None:
+        import torch
+        out = _empty(logits.shape, torch.float32, logits, stream)
+    status = (_BINDING or _binding()).adjust_logits(
+        logits, history, prompt_len, history_len, repetition, frequency, presence, bias_ids, bias, mask, out, err_out, stream)
+    if status:
+        raise PmoeError(status, "moe_adjust_logits")
+    return out
 
 
 class ExpertCache:

@@ -1,6 +1,6 @@
-// Python binding of the calls of a decode step (moe_kv_append, moe_prefix_attention,
-// moe_sample_tokens): argument checks and marshalling only, as _lib.py does for the others
-// through ctypes. Their kernels take a few microseconds. A call of moe_kv_append, of which the
+// Python binding of the calls of a serving step (moe_kv_append, moe_prefix_attention,
+// moe_sample_tokens, moe_batch_tables, moe_chunk_attention, moe_router_select, moe_adjust_logits):
+// argument checks and marshalling only, as _lib.py does for the others through ctypes. Their kernels take a few microseconds. A call of moe_kv_append, of which the
 // library's part is 1.7 us, issues in 11.5 us through ctypes, in 5.4 when a dozen tensors are
 // asked for their attributes one by one from C, in 2.15 here, where they are at::Tensors.
 //
@@ -26,6 +26,11 @@ decltype(&moe_kv_append) f_append;
 decltype(&moe_prefix_attention) f_attention;
 decltype(&pmoe_attention_plan) f_plan;
 decltype(&moe_sample_tokens) f_sample;
+decltype(&moe_batch_tables) f_tables;
+decltype(&moe_chunk_attention) f_chunk;
+decltype(&moe_chunk_attention_scratch_bytes) f_chunk_bytes;
+decltype(&moe_router_select) f_select;
+decltype(&moe_adjust_logits) f_adjust;
 PyObject *n_cuda_stream, *n_device_index;
 
 struct Refused {};  // a Python error is set
@@ -320,14 +325,197 @@ PyObject* sample_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// setup((append, attention, attention plan, sample addresses))
+// [T][width] with contiguous rows, some stride apart.
+struct Rows {
+  void* p = nullptr;
+  int64_t width = 0, stride = 0;
+  Rows(PyObject* x, const char* name, at::ScalarType type, at::ScalarType other, int64_t T) {
+    if (x == Py_None) return;
+    const at::Tensor& t = tensor(x, name, type, other, 2);
+    if (T >= 0 && t.size(0) != T) refuse("%s: %lld rows, %lld are needed", name, (long long)t.size(0), (long long)T);
+    width = t.size(1);
+    if (width > INT32_MAX || t.size(0) > INT32_MAX) refuse("%s: too large", name);
+    if (width > 1 && t.stride(1) != 1) refuse("%s: rows are not contiguous", name);
+    stride = t.size(0) > 1 ? t.stride(0) : width;  // a single row has no stride
+    p = t.data_ptr();
+  }
+};
+
+int32_t* ints(PyObject* x, int64_t n, const char* name) {
+  if (x == Py_None) refuse("%s: needed", name);
+  return vec<int32_t>(x, at::kInt, n, name);
+}
+
+// (page_table, free_pages, free_count, lens, new_len, T, page_size, num_pages, lens_out, free_count_out,
+//  q_start, positions, slots, row_seq, row_len, err_out, stream) -> status
+PyObject* batch_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 17);
+    static const char* const names[17] = {"page_table", "free_pages", "free_count", "lens", "new_len", "T", "page_size",
+                                          "num_pages", "lens_out", "free_count_out", "q_start", "positions", "slots",
+                                          "row_seq", "row_len", "err_out", "stream"};
+    const c10::DeviceIndex device = place(a, n, names);
+    const at::Tensor& table = tensor(a[0], "page_table", at::kInt, at::kInt, 2);
+    const int64_t R = table.size(0), width = table.size(1);
+    if (R > INT32_MAX || width > INT32_MAX) refuse("page_table: too large");
+    auto* pt = ints(a[0], R * width, "page_table");
+    const int64_t capacity = tensor(a[1], "free_pages", at::kInt, at::kInt).numel();
+    if (capacity > INT32_MAX) refuse("free_pages: too large");
+    auto* free_pages = ints(a[1], capacity, "free_pages");
+    const auto *count = ints(a[2], 1, "free_count"), *lens = ints(a[3], R, "lens"), *new_len = ints(a[4], R, "new_len");
+    const long long T = integer(a[5], "T"), page = integer(a[6], "page_size"), pages = integer(a[7], "num_pages");
+    auto *lens_out = ints(a[8], R, "lens_out"), *count_out = ints(a[9], 1, "free_count_out"),
+         *start = ints(a[10], R + 1, "q_start"), *positions = ints(a[11], T, "positions"), *slots = ints(a[12], T, "slots"),
+         *row_seq = ints(a[13], T, "row_seq"), *row_len = vec<int32_t>(a[14], at::kInt, T, "row_len"),
+         *err = vec<int32_t>(a[15], at::kInt, 1, "err_out");
+    const cudaStream_t stream = raw_stream(a[16], device);
+    const OnDevice on(device);
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = f_tables(pt, (int)width, (int)page, (int)pages, free_pages, (int)capacity, count, lens, new_len, (int)R, (int)T,
+                 lens_out, count_out, start, positions, slots, row_seq, row_len, err, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(r);
+  });
+}
+
+// (k_cache, v_cache, q, q_start, kv_len, page_table, window, sinks, scale, k_scale, v_scale, out, lse_out,
+//  scratch, err_out, stream) -> status
+PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 16);
+    static const char* const names[16] = {"k_cache", "v_cache", "q", "q_start", "kv_len", "page_table", "window", "sinks",
+                                          "scale", "k_scale", "v_scale", "out", "lse_out", "scratch", "err_out", "stream"};
+    const c10::DeviceIndex device = place(a, n, names);
+    const pmoe_kv_desc d = cache(a[0], a[1], a[9], a[10]);
+    const at::Tensor& tq = tensor(a[2], "q", at::kBFloat16, at::kBFloat16, 3);
+    const int64_t T = tq.size(0), q_heads = tq.size(1);
+    if (T > INT32_MAX || q_heads > INT32_MAX) refuse("q: too large");
+    const Heads q(a[2], "q", T, q_heads, d.head_dim);
+    const at::Tensor& table = tensor(a[5], "page_table", at::kInt, at::kInt, 2);
+    const int64_t R = table.size(0), width = table.size(1);
+    if (R > INT32_MAX || width > INT32_MAX) refuse("page_table: too large");
+    const auto *pt = ints(a[5], R * width, "page_table"), *start = ints(a[3], R + 1, "q_start"), *lens = ints(a[4], R, "kv_len");
+    const long long window = integer(a[6], "window"), sinks = integer(a[7], "sinks");
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)d.head_dim) : real(a[8]);
+    auto* out = vec(a[11], at::kBFloat16, T * q_heads * d.head_dim, "out");
+    auto* lse = vec<float>(a[12], at::kFloat, T * q_heads, "lse_out");
+    auto* err = vec<int32_t>(a[14], at::kInt, 1, "err_out");
+    const cudaStream_t stream = raw_stream(a[15], device);
+    const OnDevice on(device);
+    void *work = nullptr, *own = nullptr;  // scratch, and what of it was taken here
+    int64_t bytes;
+    if (a[13] != Py_None) {
+      bytes = tensor(a[13], "scratch", at::kByte, at::kByte).numel();
+      work = vec(a[13], at::kByte, bytes, "scratch");
+    } else {
+      bytes = (int64_t)f_chunk_bytes(&d, (int)T, (int)q_heads, (int)R);  // (0 where the call refuses)
+      if (bytes > 0) work = own = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, stream);
+    }
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = f_chunk(&d, q.p, q.stride, (int)T, (int)q_heads, (float)scale, start, lens, (int)R, pt, (int)width, (int)window,
+                (int)sinks, out, lse, work, (size_t)bytes, err, stream);
+    Py_END_ALLOW_THREADS
+    // what reuses the block on this stream runs after the launches
+    if (own != nullptr) c10::cuda::CUDACachingAllocator::raw_delete(own);
+    return PyLong_FromLong(r);
+  });
+}
+
+// (logits, bias, top_k, scoring, groups, top_groups, group_top, renormalize, scale, ids_out, w_out, stream)
+// -> status
+PyObject* router_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 12);
+    static const char* const names[12] = {"logits", "bias", "top_k", "scoring", "groups", "top_groups", "group_top",
+                                          "renormalize", "scale", "ids_out", "w_out", "stream"};
+    const c10::DeviceIndex device = place(a, n, names);
+    const Rows x(a[0], "logits", at::kFloat, at::kBFloat16, -1);
+    const at::Tensor& t = THPVariable_Unpack(a[0]);
+    const int64_t T = t.size(0);
+    const auto* bias = vec<float>(a[1], at::kFloat, x.width, "bias");
+    const long long k = integer(a[2], "top_k"), scoring = integer(a[3], "scoring"), groups = integer(a[4], "groups"),
+                    top_groups = integer(a[5], "top_groups"), group_top = integer(a[6], "group_top");
+    const int renorm = PyObject_IsTrue(a[7]);
+    if (renorm < 0) throw Refused{};
+    const float scale = (float)real(a[8]);
+    auto* ids = ints(a[9], T * k, "ids_out");
+    if (a[10] == Py_None) refuse("w_out: needed");
+    auto* w = vec<float>(a[10], at::kFloat, T * k, "w_out");
+    const cudaStream_t stream = raw_stream(a[11], device);
+    const int bf16 = t.scalar_type() == at::kBFloat16;
+    const OnDevice on(device);
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = f_select(x.p, bf16, (int)T, (int)x.width, x.stride, (int)k, (int)scoring, bias, (int)groups, (int)top_groups,
+                 (int)group_top, renorm, scale, ids, w, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(r);
+  });
+}
+
+// (logits, history, prompt_len, history_len, repetition, frequency, presence, bias_ids, bias, mask, out,
+//  err_out, stream) -> status
+PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 13);
+    static const char* const names[13] = {"logits", "history", "prompt_len", "history_len", "repetition", "frequency",
+                                          "presence", "bias_ids", "bias", "mask", "out", "err_out", "stream"};
+    const c10::DeviceIndex device = place(a, n, names);
+    const Rows x(a[0], "logits", at::kFloat, at::kBFloat16, -1);
+    const at::Tensor& t = THPVariable_Unpack(a[0]);
+    const int64_t T = t.size(0);
+    const Rows history(a[1], "history", at::kInt, at::kInt, T);
+    if (a[1] != Py_None && a[3] == Py_None) refuse("history_len: needed with a history");
+    const auto *prompt = vec<int32_t>(a[2], at::kInt, T, "prompt_len"), *len = vec<int32_t>(a[3], at::kInt, T, "history_len");
+    const auto *rep = vec<float>(a[4], at::kFloat, T, "repetition"), *freq = vec<float>(a[5], at::kFloat, T, "frequency"),
+               *pres = vec<float>(a[6], at::kFloat, T, "presence");
+    int64_t biases = 0;
+    const int32_t* bias_ids = nullptr;
+    const float* bias = nullptr;
+    if (a[7] != Py_None || a[8] != Py_None) {
+      if (a[7] == Py_None || a[8] == Py_None) refuse("bias_ids, bias: one without the other");
+      const Rows ids(a[7], "bias_ids", at::kInt, at::kInt, T);
+      biases = ids.width;
+      bias_ids = vec<int32_t>(a[7], at::kInt, T * biases, "bias_ids");
+      const Rows values(a[8], "bias", at::kFloat, at::kFloat, T);
+      bias = vec<float>(a[8], at::kFloat, T * biases, "bias");
+    }
+    const Rows mask(a[9], "mask", at::kInt, at::kInt, T);
+    if (a[9] != Py_None && mask.width < (x.width + 31) / 32)
+      refuse("mask: %lld words a row for %lld tokens", (long long)mask.width, (long long)x.width);
+    if (a[10] == Py_None) refuse("out: needed");
+    const Rows out(a[10], "out", at::kFloat, at::kBFloat16, T);
+    if (out.width != x.width) refuse("out: %lld tokens, %lld are needed", (long long)out.width, (long long)x.width);
+    auto* err = vec<int32_t>(a[11], at::kInt, 1, "err_out");
+    const cudaStream_t stream = raw_stream(a[12], device);
+    const int bf16 = t.scalar_type() == at::kBFloat16, out_bf16 = THPVariable_Unpack(a[10]).scalar_type() == at::kBFloat16;
+    const int64_t mask_stride = T > 1 ? mask.stride : mask.width;
+    const OnDevice on(device);
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = f_adjust(x.p, bf16, (int)T, (int)x.width, x.stride, static_cast<const int32_t*>(history.p), history.stride,
+                 (int)history.width, prompt, len, rep, freq, pres, bias_ids, bias, (int)biases,
+                 static_cast<const uint32_t*>(mask.p), mask_stride, out.p, out_bf16, out.stride, err, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(r);
+  });
+}
+
+// setup(the library's entry points, in the order below)
 PyObject* setup(PyObject*, PyObject* args) {
-  unsigned long long f[4];
-  if (!PyArg_ParseTuple(args, "(KKKK)", &f[0], &f[1], &f[2], &f[3])) return nullptr;
+  unsigned long long f[9];
+  if (!PyArg_ParseTuple(args, "(KKKKKKKKK)", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8])) return nullptr;
   f_append = reinterpret_cast<decltype(f_append)>((uintptr_t)f[0]);
   f_attention = reinterpret_cast<decltype(f_attention)>((uintptr_t)f[1]);
   f_plan = reinterpret_cast<decltype(f_plan)>((uintptr_t)f[2]);
   f_sample = reinterpret_cast<decltype(f_sample)>((uintptr_t)f[3]);
+  f_tables = reinterpret_cast<decltype(f_tables)>((uintptr_t)f[4]);
+  f_chunk = reinterpret_cast<decltype(f_chunk)>((uintptr_t)f[5]);
+  f_chunk_bytes = reinterpret_cast<decltype(f_chunk_bytes)>((uintptr_t)f[6]);
+  f_select = reinterpret_cast<decltype(f_select)>((uintptr_t)f[7]);
+  f_adjust = reinterpret_cast<decltype(f_adjust)>((uintptr_t)f[8]);
   Py_RETURN_NONE;
 }
 
@@ -338,8 +526,12 @@ PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, "entry points"},
                          {"kv_append", fast(kv_append), METH_FASTCALL, "moe_kv_append"},
                          {"prefix_attention", fast(prefix_attention), METH_FASTCALL, "moe_prefix_attention"},
                          {"sample_tokens", fast(sample_tokens), METH_FASTCALL, "moe_sample_tokens"},
+                         {"batch_tables", fast(batch_tables), METH_FASTCALL, "moe_batch_tables"},
+                         {"chunk_attention", fast(chunk_attention), METH_FASTCALL, "moe_chunk_attention"},
+                         {"router_select", fast(router_select), METH_FASTCALL, "moe_router_select"},
+                         {"adjust_logits", fast(adjust_logits), METH_FASTCALL, "moe_adjust_logits"},
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "binding of the decode-step calls", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "binding of the serving-step calls", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

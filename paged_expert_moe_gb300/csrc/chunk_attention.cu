@@ -1,0 +1,897 @@
+// moe_chunk_attention: each request's new tokens over its own pages of a paged cache, with causal
+// limits and, where asked for, a sliding window and first keys that stay visible.
+//
+// A tile of query rows is up to 256 / group tokens of one request times the query heads of one kv
+// head, so that all its rows meet the same keys: S = Q K^T and O += P V on the tensor cores, 128
+// keys at a time, as two 128-row query tiles that share each K and V tile. Rows of a tile differ in
+// what they see only in its last key tiles and at a window's edge; all others take no masks.
+//
+// Work: the lengths are on the device, so a first kernel lists the tiles with the key tiles that each
+// needs, and cuts the sum into equal runs, one a CTA and one CTA an SM. What a run takes
+// of a tile without taking all of it is left as a part, and a last kernel joins the parts.
+//
+// Warps: 0-3 and 4-7 own one query tile each, a thread one row (a TMEM lane): scores from TMEM,
+// weights back to TMEM in their place as the 16-bit A operand of the second product. Warp 8 issues
+// the MMAs, warp 9 loads K and V tiles by TMA, one box a page and 64 columns. In partly visible
+// tiles a value that some row must not use may be anything, and 0 x NaN is NaN: with a bf16 cache
+// warps 10 and 11 look at those tiles before the MMAs do, clear the rows that no query row sees
+// and what is not finite in the others; with an e4m3 cache warps 12-15, which convert to fp16, do.
+// What was cleared is added to the rows that do see it at the end.
+#include "chunk.cuh"
+#include "tc_gemm.h"
+
+#include <algorithm>
+#include <math.h>
+
+namespace pmoe {
+namespace chunk {
+namespace {
+
+constexpr int kKeys = kTcKeys;  // of a tile
+constexpr int kRows = 256;      // of a query tile pair
+
+// ---------------------------------------------------------------- the plan
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive sums over the block; *total: of all.
+__device__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warps[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    warps[lane] = w;
+  }
+  __syncthreads();
+  *total = warps[31];
+  const int64_t r = (warp > 0 ? warps[warp - 1] : 0) + x - v;
+  __syncthreads();
+  return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
+  __shared__ int64_t warps[32];
+  __shared__ int upto[kPlanThreads + 1];  // tiles before each request of the block's turn
+  __shared__ int s_start[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t room = (int64_t)a.table_stride * a.kv.page_size;
+  int items = 0;
+  int64_t units = 0, rows = 0;
+  for (int r0 = 0; r0 < a.R; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    int start = 0, n = 0, len = 0;
+    bool bad = false;
+    if (r < a.R) {
+      const int s0 = a.q_start[r], s1 = a.q_start[r + 1];
+      start = min(max(s0, 0), a.T);
+      const int end = min(max(s1, 0), a.T);
+      n = max(end - start, 0);
+      len = a.kv_len[r];
+      bad = s0 != start || s1 != end || end < start;
+      if (len < 0 || len > room) bad = true, len = len < 0 ? 0 : (int)room;
+    }
+    // starts that go back may name more rows than there are
+    int64_t some;
+    const int64_t before = rows + block_scan(n, warps, &some);
+    rows += some;
+    if (before + n > a.T) bad = true, n = 0;
+    if (bad && a.err != nullptr) atomicOr(a.err, kErrBadLength);
+    const int tiles = (n + a.tile_tokens - 1) / a.tile_tokens;
+    int64_t all;
+    upto[tid] = (int)block_scan(tiles, warps, &all);
+    s_start[tid] = start, s_n[tid] = n, s_len[tid] = len;
+    if (tid == 0) upto[kPlanThreads] = (int)all;
+    __syncthreads();
+    for (int j0 = 0; j0 < all; j0 += kPlanThreads) {
+      const int j = j0 + tid;
+      Item it{};
+      if (j < all) {
+        int lo = 0, hi = kPlanThreads;  // upto[lo] <= j < upto[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (upto[mid] <= j)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        const int i0 = (j - upto[lo]) * a.tile_tokens;
+        it.req = r0 + lo;
+        it.tok0 = s_start[lo] + i0;
+        it.ntok = min(a.tile_tokens, s_n[lo] - i0);
+        it.p0 = s_len[lo] - s_n[lo] + i0;
+        const int p1 = it.p0 + it.ntok - 1;
+        it.lo = a.window > 0 ? max(it.p0 - a.window + 1, 0) / kKeys : 0;
+        const int st = a.window > 0 ? min((a.sinks + kKeys - 1) / kKeys, it.lo) : 0;
+        // a tile of rows before the first key has one tile of keys all the same, of which it sees none
+        it.nt = max((p1 >= 0 ? p1 / kKeys + 1 : 0) - it.lo, p1 < 0 ? 1 : 0) + st;
+      }
+      int64_t more;
+      it.base = units + block_scan((int64_t)it.nt * a.kv.kv_heads, warps, &more);
+      if (j < all) a.items[items + j] = it;
+      units += more;
+    }
+    items += (int)all;
+  }
+  __syncthreads();
+  // runs of two units at least; each run's first item
+  const int ctas = (int)min((int64_t)a.ctas, (units + 1) / 2);
+  if (tid == 0) a.plan[0] = units, a.plan[1] = ctas;
+  for (int j = tid; j < items; j += kPlanThreads) {
+    const int64_t b0 = a.items[j].base, b1 = b0 + (int64_t)a.items[j].nt * a.kv.kv_heads;
+    for (int c = (int)((b0 * ctas + units - 1) / units); c < ctas; ++c) {
+      const int64_t u = run_start(units, ctas, c);
+      if (u >= b1) break;
+      if (u >= b0) a.first[c] = j;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the tensor cores
+
+template <int D, bool F8>
+struct Cfg {
+  static constexpr int kTileBytes = kKeys * D * 2;        // one K or V tile, 16-bit operands
+  static constexpr int kQBytes = 128 * D * 2;             // one query tile
+  static constexpr int kSlots = D == 128 ? 5 : 8;         // ring of K and V tiles
+  static constexpr int kThreads = F8 ? 512 : 384;         // whole warpgroups
+  // Registers a thread, by warpgroup: what the other roles give up the softmax takes. The
+  // launch has 168 (bf16) or 128 (e4m3) of them for each of its threads.
+  static constexpr int kSoftmaxRegs = F8 ? 184 : 200, kMmaRegs = F8 ? 72 : 104, kLoaderRegs = F8 ? 72 : 0;
+  static_assert(kSoftmaxRegs * 256 + (kMmaRegs + kLoaderRegs) * 128 <= (F8 ? 128 : 168) * kThreads, "register shares");
+  static constexpr int kRing = kSlots * kTileBytes;
+  // e4m3: where TMA puts a tile's bytes for the conversion. Heads of 128: the upper half of the
+  // tile's slot, whose line of row r also takes that row's upper 64 values, so that the warp that
+  // converts a row reads it before it writes. Heads of 64: a ring of their own.
+  static constexpr int kRawBytes = kKeys * D, kRawRing = F8 && D == 64 ? kSlots * kRawBytes : 0;
+  static __device__ __forceinline__ uint8_t* raw(uint8_t* smem, uint32_t slot) {
+    return D == 64 ? smem + kRing + slot * kRawBytes : smem + slot * kTileBytes + kRawBytes;
+  }
+  static constexpr int kSmem = kRing + kRawRing + 2 * kQBytes + 1024 /* alignment */ + 1024 /* row factors */ + 512;
+  static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
+  static constexpr int kGuards = F8 ? 4 : 2;              // warps that look at partly visible values
+};
+
+struct Bars {
+  uint64_t full[8], empty[8], raw[8];
+  uint64_t vok[8];  // partly visible values are cleared
+  uint64_t sfull[2], pready[2], odone[2], qfull[2], staged[2], drain;
+  uint32_t tmem;
+  int abort;
+  // [guard warp][segment % 32]: cleared values that some row sees. A guard is at most four
+  // segments ahead of the MMAs, and these seldom more than one ahead of a query tile's end.
+  uint8_t poison[4][32];
+};
+static_assert(sizeof(Bars) <= 512, "room behind the row factors");
+
+// bf16 pairs with an element that is not finite: the top bits of the 16-bit halves say which
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+
+// What column d of the values adds to a row at position p beyond its finite values: the sum of
+// the infinities and NaNs among the values that it sees, in the segment's partly visible tiles.
+template <int D, bool F8>
+__device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p, int d) {
+  float sum = 0.f;
+  const int psh = 31 - __clz(a.kv.page_size);
+  for (int t = sg.t0; t < sg.t1; ++t) {
+    const int k0 = tile_key<kKeys>(a, sg.it, t);
+    if (all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys)) continue;
+    for (int j = k0; j < k0 + kKeys && j <= p; ++j) {
+      if (!sees(a, p, j)) continue;
+      const int page = a.page_table[(int64_t)sg.it.req * a.table_stride + (j >> psh)];
+      if ((unsigned)page >= (unsigned)a.kv.num_pages) continue;
+      const int64_t at = page * a.kv.page_stride + ((int64_t)sg.h * a.kv.page_size + (j & (a.kv.page_size - 1))) * D + d;
+      float v;
+      if (F8) {
+        const uint8_t c = static_cast<const uint8_t*>(a.kv.v)[at];
+        v = (c & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000) : 0.f;
+      } else {
+        v = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.kv.v)[at] << 16);
+      }
+      if (!(fabsf(v) < INFINITY)) sum += v;
+    }
+  }
+  return sum;
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a) {
+  using C = Cfg<D, F8>;
+  constexpr int kSlots = C::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = smem + C::kRing + C::kRawRing;
+  float* qmul = reinterpret_cast<float*>(qs + 2 * C::kQBytes);  // [256]
+  Bars& b = *reinterpret_cast<Bars*>(qmul + 256);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &b.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&b.full[i], F8 ? 4 : 1);
+      // the MMAs' commit, and the guards, which keep in step with the ring
+      mbar_init(&b.empty[i], F8 ? 1 : 1 + C::kGuards);
+      mbar_init(&b.raw[i], 1);
+      mbar_init(&b.vok[i], C::kGuards);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.sfull[i], 1);
+      mbar_init(&b.pready[i], 4);
+      mbar_init(&b.odone[i], 1);
+      mbar_init(&b.qfull[i], 4);
+      mbar_init(&b.staged[i], 4);
+    }
+    mbar_init(&b.drain, 1);
+    b.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
+  }
+  pdl_wait();  // the plan
+  pdl_trigger();
+  __syncthreads();
+  // The issuing warp allocates all 512 columns: the base is column 0, lane 0. The other roles
+  // touch TMEM only after its first products.
+  constexpr uint32_t tmem = 0;
+  const int64_t units = a.plan[0];
+  const int ctas = (int)a.plan[1];
+  Walk walk{0, 0, 0, 0};
+  if ((int)blockIdx.x < ctas) {
+    const int64_t u0 = run_start(units, ctas, blockIdx.x);
+    walk.item = a.first[blockIdx.x];
+    const int64_t in = u0 - a.items[walk.item].base;
+    const int nt = a.items[walk.item].nt;
+    walk.h = (int)(in / nt);
+    walk.t = (int)(in - (int64_t)walk.h * nt);
+    walk.left = run_start(units, ctas, blockIdx.x + 1) - u0;
+  }
+  const int psh = 31 - __clz(a.kv.page_size);
+  Segment sg;
+
+  if (warp < 8) {
+    // ---------------- softmax: one thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+    const int q = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + q * 128, to = lanes + 256 + q * 128;
+    constexpr int LPR = D / 8;  // threads of a row while Q is loaded
+    uint32_t n = 0, segs = 0;   // tiles and segments so far
+    uint32_t all = 0;           // segments of the CTA so far
+    bool ok = true;
+    for (; ok && walk.next(a, &sg); ++all) {
+      const int rows = sg.it.ntok * a.group;
+      if (q * 128 >= rows) continue;
+      // the query tile, K-major with the 128-byte swizzle; rows beyond the last are zero.
+      // What a score is multiplied by, scale x key scale x the row's power of two, has to be above
+      // zero: then the largest score stays the largest, and a masked one -inf. So its sign goes
+      // into Q, and a row whose factor is 0 (or vanishes in fp32) has Q = 0 and factor 1.
+      const float ks = F8 ? a.kv.k_scale[sg.h] : 1.f;
+      const uint32_t flip = (a.scale < 0.f) != (ks < 0.f) ? 0x80008000u : 0u;
+      const int c = row % LPR;
+      uint4 v[LPR];  // LPR rows a thread, all in flight
+#pragma unroll
+      for (int p = 0; p < LPR; ++p) {
+        const int i = q * 128 + row / LPR + p * (128 / LPR);
+        v[p] = make_uint4(0, 0, 0, 0);
+        if (i < rows) {
+          const int t = row_token(a, i);
+          v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(sg.it.tok0 + t) * a.q_stride +
+                                                      (sg.h * a.group + i - t * a.group) * D + c * 8));
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < LPR; ++p) {
+        const int r = row / LPR + p * (128 / LPR);
+        uint32_t w[4] = {v[p].x ^ flip, v[p].y ^ flip, v[p].z ^ flip, v[p].w ^ flip};
+        if (F8) {
+          float mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int e = row_exponent(mx);
+          const float factor = fabsf(a.scale) * fabsf(ks) * pow2(e), down = factor != 0.f ? pow2(-e) : 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+          if (c == 0) qmul[q * 128 + r] = factor != 0.f ? factor : 1.f;
+        }
+        *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_async();
+      warp_arrive(&b.qfull[q]);
+      // the row factors of all threads
+      if (!warp_wait(&b.qfull[q], segs++ & 1, abort_flag, a.err)) break;
+      // (bf16, scale 0: times 2^-149 the largest score is below 2^-20)
+      const float mul = F8 ? qmul[q * 128 + row] : a.scale != 0.f ? fabsf(a.scale) : __uint_as_float(1);
+      const int pos = sg.it.p0 + row_token(a, q * 128 + row);  // (of rows beyond the last: any)
+
+      float m = -INFINITY, l = 0.f;
+      for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+        if (!warp_wait(&b.sfull[q], n & 1, abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        float s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+        tmem_wait_ld();
+        const int k0 = tile_key<kKeys>(a, sg.it, t);
+        if (!all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys)) {
+          const int hi = pos - k0, lo = a.window > 0 ? hi - a.window : -1, sink = a.sinks - k0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > hi || (i <= lo && i >= sink)) s[i] = -INFINITY;
+        }
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
+        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
+        if (t == sg.t0) {
+          m = mx;
+        } else {
+          const bool grow = mx > m + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            // the products so far are done: these scores were issued after them
+            const float f = grow ? ex2(m - mx) : 1.f;
+            if (grow) m = mx;
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(to + i, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const uint64_t mul2 = pair(mul, mul), base2 = pair(-base, -base);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16];
+          const float* sc = s + 32 * i;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float y, z;
+            unpair(fma2(pair(sc[2 * k], sc[2 * k + 1]), mul2, base2), y, z);
+            y = ex2(y), z = ex2(z);
+            sum[k & 1] = add2(sum[k & 1], pair(y, z));
+            p[k] = pack2<F8>(y, z);
+          }
+          tmem_st16(ts + 16 * i, p);
+        }
+        tmem_wait_st();
+        fence_before();
+        warp_arrive(&b.pready[q]);
+        float y, z;
+        unpair(add2(sum[0], sum[1]), y, z);
+        l += y + z;
+      }
+      if (!ok) break;
+      if (!warp_wait(&b.odone[q], (segs - 1) & 1, abort_flag, a.err)) break;
+      fence_after();
+      bool poisoned = false;
+#pragma unroll
+      for (int i = 0; i < C::kGuards; ++i) poisoned |= *(volatile uint8_t*)&b.poison[i][all & 31] != 0;
+      if (poisoned) {
+#pragma unroll 1
+        for (int i = 0; i < D; i += 16) {
+          uint32_t o[16];
+          tmem_ld16(to + i, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            o[k] = __float_as_uint(__uint_as_float(o[k]) + (q * 128 + row < rows ? poison_of<D, F8>(a, sg, pos, i + k) : 0.f));
+          tmem_st16(to + i, o);
+          tmem_wait_st();
+        }
+      }
+      // 32 columns at a time through shared memory (the query tile's, which is done with), so
+      // that a store covers whole lines: 8 threads a row of 128 bytes (of 64 in bf16), whose
+      // 16-byte (8-byte) chunks are swizzled by the row
+      const bool whole = sg.whole();
+      const float vs = (F8 ? a.kv.v_scale[sg.h] : 1.f) * (!whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);
+      const int64_t part0 = ((int64_t)blockIdx.x * 2 + (sg.t0 == 0)) * a.part_rows;
+      uint8_t* stage = qs + q * C::kQBytes + (warp & 3) * (C::kQBytes / 4);
+      int64_t dst[8];  // elements into out or o_part
+      const int last = rows - q * 128 - (warp & 3) * 32;  // rows of this warp
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = 4 * k + (lane >> 3), i = q * 128 + (warp & 3) * 32 + r;
+        const int t = row_token(a, i);
+        dst[k] = whole ? ((int64_t)(sg.it.tok0 + t) * a.q_heads + sg.h * a.group + i - t * a.group) * D + (lane & 7) * 4
+                       : (part0 + i) * D + (lane & 7) * 4;
+      }
+#pragma unroll
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(to + d, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+              make_float4(__uint_as_float(o[4 * k]) * vs, __uint_as_float(o[4 * k + 1]) * vs,
+                          __uint_as_float(o[4 * k + 2]) * vs, __uint_as_float(o[4 * k + 3]) * vs);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3);
+          const float4 v4 = *reinterpret_cast<const float4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (r < last) {
+            if (whole)
+              *reinterpret_cast<uint2*>(a.out + dst[k] + d) = make_uint2(pack2<false>(v4.x, v4.y), pack2<false>(v4.z, v4.w));
+            else
+              *reinterpret_cast<float4*>(a.o_part + dst[k] + d) = v4;
+          }
+        }
+        __syncwarp();
+      }
+      const int i = q * 128 + row;
+      if (i < rows) {
+        if (!whole) {
+          a.ml_part[part0 + i] = make_float2(m, l);
+        } else if (a.lse != nullptr) {
+          const int t = row_token(a, i);
+          a.lse[(int64_t)(sg.it.tok0 + t) * a.q_heads + sg.h * a.group + i - t * a.group] =
+              m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+        }
+      }
+      // every warp is done with its stage before Q is written again
+      warp_arrive(&b.staged[q]);
+      if (!warp_wait(&b.staged[q], (segs - 1) & 1, abort_flag, a.err)) break;
+      fence_before();
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
+    if (warp == 8) {
+      // ---------------- MMA issuer
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)),
+                   "r"(C::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+      const uint32_t is = idesc_bf16(128, kKeys) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u);
+      const uint32_t io = (idesc_bf16(128, D) & (F8 ? ~((1u << 7) | (1u << 10)) : ~0u)) | (1u << 16);  // B: N contiguous
+      const uint32_t ring = smem_u32(smem), qa = smem_u32(qs);
+      uint32_t kv = 0;               // K and V tiles so far
+      uint32_t part = 0;             // by slot, whether an odd number of partly visible tiles was there
+      uint32_t seg[2] = {0, 0};      // segments of each query tile so far
+      uint32_t pn[2] = {0, 0};       // products with V of each query tile so far
+      bool ok = true;
+      auto wait_kv = [&](uint32_t i) {
+        return warp_wait(&b.full[i % kSlots], (i / kSlots) & 1, abort_flag, a.err);
+      };
+      auto scores = [&](int q, uint32_t slot, bool last) {  // last: of the query tiles on this slot
+        if (converged_lane()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
+            mma_bf16(tmem + q * 128, sw128_desc(qa + q * C::kQBytes + off), sw128_desc(ring + slot * C::kTileBytes + off), is,
+                     k > 0);
+          }
+          mma_commit(&b.sfull[q]);
+          if (last) mma_commit(&b.empty[slot]);
+        }
+        __syncwarp();
+      };
+      while (ok && walk.next(a, &sg)) {
+        const int nq = sg.it.ntok * a.group > 128 ? 2 : 1;
+        for (int q = 0; q < nq && ok; ++q) {
+          ok = warp_wait(&b.qfull[q], seg[q] & 1, abort_flag, a.err);
+          ++seg[q];
+        }
+        if (!ok || !wait_kv(kv)) break;
+        fence_after();
+        for (int q = 0; q < nq; ++q) scores(q, kv % kSlots, q + 1 == nq);
+        for (int t = sg.t0; t < sg.t1; ++t, kv += 2) {
+          const uint32_t vslot = (kv + 1) % kSlots;
+          const bool more = t + 1 < sg.t1;
+          if (!wait_kv(kv + 1) || (more && !wait_kv(kv + 2))) {
+            ok = false;
+            break;
+          }
+          if (!F8 && !all_see_tile(a, sg.it.p0, sg.p1(), tile_key<kKeys>(a, sg.it, t), kKeys)) {
+            if (!warp_wait(&b.vok[vslot], part >> vslot & 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            part ^= 1u << vslot;
+          }
+          for (int q = 0; q < nq; ++q) {
+            if (!warp_wait(&b.pready[q], pn[q] & 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            ++pn[q];
+            fence_after();
+            if (converged_lane()) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
+                           t > sg.t0 || k > 0);
+              if (!more) mma_commit(&b.odone[q]);
+              if (q + 1 == nq) mma_commit(&b.empty[vslot]);
+            }
+            __syncwarp();
+            if (more) scores(q, (kv + 2) % kSlots, q + 1 == nq);
+          }
+          if (!ok) break;
+        }
+      }
+      // every MMA and its arrival are done before the CTA leaves
+      if (converged_lane()) {
+        mma_commit(&b.drain);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&b.drain, 0) && clock64() - t0 < kWaitLimit) {
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---------------- TMA loader: lane i issues box i % halves of page box i / halves
+      constexpr int kHalves = F8 ? 1 : D / 64, kBytes = F8 ? 1 : 2;
+      uint64_t* arrive = F8 ? b.raw : b.full;
+      const int box = min(a.kv.page_size, kKeys), boxes = kKeys / box;
+      uint32_t kv = 0;
+      bool ok = true;
+      while (ok && walk.next(a, &sg)) {
+        const int32_t* table = a.page_table + (int64_t)sg.it.req * a.table_stride;
+        for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+          const int pb = lane / kHalves, hf = lane % kHalves;
+          const int key = tile_key<kKeys>(a, sg.it, t) + pb * box;
+          // pages with a key that some row sees
+          bool use = pb < boxes && key <= sg.p1();
+          if (use && a.window > 0) use = key + box - 1 > sg.it.p0 - a.window || key < a.sinks;
+          int id = 0;
+          if (use) {
+            id = __ldg(table + (key >> psh));
+            if ((unsigned)id >= (unsigned)a.kv.num_pages) {
+              if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
+              id = a.kv.num_pages;  // out of the map's range: reads as zeros
+            }
+          }
+          const int used = __popc(__ballot_sync(0xffffffffu, use));
+          for (int v = 0; v < 2; ++v, ++kv) {
+            const uint32_t slot = kv % kSlots;
+            if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&arrive[slot], used * box * (F8 ? D : 64) * kBytes);
+            __syncwarp();
+            uint8_t* dst = F8 ? C::raw(smem, slot) + pb * box * D : smem + slot * C::kTileBytes + hf * (kKeys * 128) + pb * box * 128;
+            if (use)
+              tma_load_4d(dst, v ? &map_v : &map_k, &arrive[slot], hf * 64, key & (a.kv.page_size - 1), sg.h, id);
+          }
+        }
+      }
+      // copies in flight land before the CTA leaves, even where another role gave up
+      for (uint32_t i = kv > kSlots ? kv - kSlots : 0; i < kv; ++i) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&arrive[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kWaitLimit) {
+        }
+      }
+    } else if (!F8) {
+      // ---------------- guards: warp 10 looks at keys 0-63 of partly visible tiles, 11 at the others
+      const int gw = warp - 10;
+      uint32_t kv = 0, segs = 0;
+      bool ok = true;
+      for (; ok && walk.next(a, &sg); ++segs) {
+        if (lane == 0) *(volatile uint8_t*)&b.poison[gw][segs & 31] = 0;
+        for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+          const int k0 = tile_key<kKeys>(a, sg.it, t);
+          for (int v = 0; v < 2; ++v, ++kv) {
+            const uint32_t slot = kv % kSlots;
+            if (!warp_wait(&b.full[slot], (kv / kSlots) & 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            if (v == 1 && !all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys)) {
+              bool found = false;
+#pragma unroll 4
+              for (int i = lane; i < 64 * (D / 8); i += 32) {
+                const int r = gw * 64 + i / (D / 8), c = i % (D / 8);
+                if (all_see(a, sg.it.p0, sg.p1(), k0 + r)) continue;
+                uint4* at = reinterpret_cast<uint4*>(smem + slot * C::kTileBytes + (c / 8) * (kKeys * 128) + r * 128 + (c & 7) * 16);
+                if (!any_sees(a, sg.it.p0, sg.p1(), k0 + r)) {
+                  *at = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                const uint4 x = *at;
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                if (not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3])) {
+                  found = true;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t bad = not_finite(w[k]);
+                    w[k] &= ~((bad & 0x8000u ? 0xffffu : 0u) | (bad & 0x80000000u ? 0xffff0000u : 0u));
+                  }
+                  *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+              if (found) *(volatile uint8_t*)&b.poison[gw][segs & 31] = 1;
+              fence_async();
+              warp_arrive(&b.vok[slot]);
+            }
+            warp_arrive(&b.empty[slot]);
+          }
+        }
+      }
+    }
+  } else if constexpr (F8) {
+    // ---------------- e4m3 conversion: 16 codes a thread and step, to fp16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoaderRegs));
+    constexpr int CH = D / 16;  // 16-code chunks of a row
+    constexpr int N = kKeys * CH / 128;
+    const int tid = threadIdx.x - 12 * 32, ch = tid % CH, r0 = tid / CH;
+    uint32_t kv = 0, segs = 0;
+    bool ok = true;
+    for (; ok && walk.next(a, &sg); ++segs) {
+      if (lane == 0) *(volatile uint8_t*)&b.poison[warp - 12][segs & 31] = 0;
+      __syncwarp();
+      for (int i2 = 2 * sg.t0; i2 < 2 * sg.t1; ++i2, ++kv) {  // K and V of each tile
+        const uint32_t slot = kv % kSlots;
+        if (!warp_wait(&b.raw[slot], (kv / kSlots) & 1, abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = C::raw(smem, slot);
+        const int k0 = tile_key<kKeys>(a, sg.it, i2 / 2);
+        const bool check = (i2 & 1) && !all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys);
+        uint4 raw[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * (128 / CH);
+          const int at = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+          raw[i] = *reinterpret_cast<const uint4*>(src + at);
+        }
+        if (check) {
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int j = k0 + r0 + i * (128 / CH);
+            if (all_see(a, sg.it.p0, sg.p1(), j)) continue;
+            const bool any = any_sees(a, sg.it.p0, sg.p1(), j);
+            uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // the code 0x7f of either sign
+              found |= any && nan != 0;
+              w[k] = any ? w[k] & ~((nan >> 7) * 0xffu) : 0u;
+            }
+            raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (found) *(volatile uint8_t*)&b.poison[warp - 12][segs & 31] = 1;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * (128 / CH);
+          uint8_t* dst = smem + slot * C::kTileBytes + (ch / 4) * (kKeys * 128) + r * 128;
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[2 * k] = e4m3x2(w[k] & 0xffffu), f[2 * k + 1] = e4m3x2(w[k] >> 16);
+          // 8 threads hold a row of 128: the upper four write their halves the other way
+          // round, so that the two 64-value blocks meet on different banks
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int kk = k ^ (ch / 4 & 1);
+            *reinterpret_cast<uint4*>(dst + (((2 * (ch % 4) + kk) ^ (r & 7)) << 4)) =
+                kk ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
+          }
+        }
+        fence_async();
+        warp_arrive(&b.full[slot]);
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
+}
+
+// ---------------------------------------------------------------- the join
+
+// Block (c, y): rows 8 y .. 8 y + 7 of the item that the boundary before CTA c cuts, a warp a row,
+// if that is the first boundary inside it. The parts are added in the order of the CTAs.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const int64_t units = a.plan[0];
+  const int ctas = (int)a.plan[1];
+  if (c >= ctas) return;
+  const Item it = a.items[a.first[c]];
+  const int64_t u = run_start(units, ctas, c), in = u - it.base;
+  const int h = (int)(in / it.nt);
+  const int64_t g0 = it.base + (int64_t)h * it.nt, g1 = g0 + it.nt;
+  if (u == g0 || run_start(units, ctas, c - 1) > g0) return;
+  const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (i >= it.ntok * a.group) return;
+  int n = 1;  // parts: CTA c - 1's slot 1, then slots 0
+  while (run_start(units, ctas, c + n - 1) < g1 && c + n - 1 < ctas) ++n;
+  auto at = [&](int p) { return ((int64_t)(c - 1 + p) * 2 + (p == 0)) * a.part_rows + i; };
+  float m = -INFINITY;
+  for (int p = lane; p < n; p += 32) m = fmaxf(m, a.ml_part[at(p)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float top = m == -INFINITY ? 0.f : m;
+  constexpr int V = D / 32;
+  float l = 0.f, acc[V];
+#pragma unroll
+  for (int d = 0; d < V; ++d) acc[d] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < n; ++p) {
+    const float2 ml = a.ml_part[at(p)];
+    const float f = ex2(ml.x - top);
+    const float* src = a.o_part + at(p) * D + lane * V;
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int d = 0; d < V; ++d) acc[d] = fmaf(src[d], f, acc[d]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int t = row_token(a, i);
+  const int64_t row = (int64_t)(it.tok0 + t) * a.q_heads + h * a.group + i - t * a.group;
+#pragma unroll
+  for (int d = 0; d < V; d += 2)
+    *reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * V + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+}
+
+// ---------------------------------------------------------------- host side
+
+int sm_count() {
+  static std::atomic<int> count[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = count[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) count[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+int make_map(const Args& a, void* base, CUtensorMap* m) {
+  const bool f8 = a.kv.dtype == PMOE_KV_E4M3;
+  const uint64_t D = a.kv.head_dim, page = a.kv.page_size, eb = f8 ? 1 : 2;
+  const uint64_t dims[4] = {D, page, (uint64_t)a.kv.kv_heads, (uint64_t)a.kv.num_pages};
+  const uint64_t strides[3] = {D * eb, page * D * eb, (uint64_t)a.kv.page_stride * eb};
+  const uint32_t box[4] = {f8 ? (uint32_t)D : 64u, (uint32_t)std::min<uint64_t>(page, kKeys), 1, 1};
+  return tc_encode_map(m, base, 4, dims, strides, box, !f8 ? kTcMapBf16Sw128 : D == 128 ? kTcMapBytesSw128 : kTcMapBytesSw64);
+}
+
+template <int D, bool F8>
+int launch_all(const Args& a, cudaStream_t s) {
+  using C = Cfg<D, F8>;
+  const char* what = "moe_chunk_attention";
+  static SmemLimit limit;
+  CUtensorMap mk, mv;
+  int r = make_map(a, a.kv.k, &mk);
+  if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
+  if (r == PMOE_OK) r = limit.set(reinterpret_cast<const void*>(chunk_kernel<D, F8>), C::kSmem, what);
+  if (r == PMOE_OK) r = launch(what, plan_kernel, 1, kPlanThreads, 0, s, true, 1, a);
+  if (r == PMOE_OK) r = launch(what, chunk_kernel<D, F8>, a.ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, a);
+  if (r != PMOE_OK || a.ctas == 1) return r;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(a.ctas - 1, (a.part_rows + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D>, a), what);
+}
+
+struct Layout {
+  size_t first, items, o, ml, bytes;
+};
+
+// Fills what follows from the sizes alone.
+int plan(const pmoe_kv_desc* kv, int T, int q_heads, int R, Args* a, Layout* l) {
+  const int r = check_kv(kv);
+  if (r != PMOE_OK) return r;
+  if (T < 0 || R < 0 || R > (1 << 20) || q_heads < 1 || q_heads % kv->kv_heads != 0) return PMOE_EINVAL;
+  if ((int64_t)T * q_heads >= (1 << 24)) return PMOE_EINVAL;
+  a->kv = *kv;
+  a->T = T;
+  a->R = R;
+  a->q_heads = q_heads;
+  a->group = q_heads / kv->kv_heads;
+  if (a->group > kMaxGroup) return PMOE_EUNSUPPORTED;
+  a->group_magic = (uint32_t)((1ull << 32) / a->group + 1);
+  if (T == 0 || R == 0) return PMOE_OK;
+  a->ctas = sm_count();
+  if (a->ctas == 0) return PMOE_ECUDA;
+  a->tile_tokens = kRows / a->group;
+  a->part_rows = std::min(kRows, T * a->group);
+  const size_t parts = (size_t)a->ctas * 2 * a->part_rows;
+  auto up = [](size_t n) { return (n + 15) / 16 * 16; };
+  l->first = 16;
+  l->items = up(l->first + (size_t)a->ctas * 4);
+  l->o = l->items + (size_t)(T / a->tile_tokens + std::min(R, T)) * sizeof(Item);  // a request's last tile may be short
+  l->ml = l->o + parts * kv->head_dim * 4;
+  l->bytes = up(l->ml + parts * 8);
+  return PMOE_OK;
+}
+
+}  // namespace
+}  // namespace chunk
+}  // namespace pmoe
+
+using namespace pmoe;
+
+extern "C" size_t moe_chunk_attention_scratch_bytes(const pmoe_kv_desc* kv, int T, int q_heads, int R) {
+  chunk::Args a{};
+  chunk::Layout l{};
+  return chunk::plan(kv, T, q_heads, R, &a, &l) == PMOE_OK ? l.bytes : 0;
+}
+
+extern "C" int moe_chunk_attention(const pmoe_kv_desc* kv, const void* q, int64_t q_stride, int T, int q_heads, float scale,
+                                   const int32_t* q_start, const int32_t* kv_len, int R, const int32_t* page_table,
+                                   int table_stride, int window, int sinks, void* out, float* lse, void* scratch,
+                                   size_t scratch_bytes, int32_t* err_out, void* stream) {
+  // arguments first: the plan asks the device for its size
+  if (check_kv(kv) == PMOE_OK && T > 0 && R > 0) {
+    auto off = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
+    if (q == nullptr || out == nullptr || off(q, 16) || off(out, 16) || q_stride % 8 != 0 ||
+        q_stride < (int64_t)q_heads * kv->head_dim || !(fabsf(scale) < INFINITY))
+      return PMOE_EINVAL;
+    if (q_start == nullptr || kv_len == nullptr || page_table == nullptr || off(q_start, 4) || off(kv_len, 4) ||
+        off(page_table, 4) || table_stride < 1 || (int64_t)table_stride * kv->page_size > (1 << 30))
+      return PMOE_EINVAL;
+    if (off(lse, 4) || off(err_out, 4) || off(scratch, 16)) return PMOE_EINVAL;
+  }
+  if (window < 0 || sinks < 0) return PMOE_EINVAL;
+  chunk::Args a{};
+  chunk::Layout lay{};
+  const int r = chunk::plan(kv, T, q_heads, R, &a, &lay);
+  if (r != PMOE_OK || T == 0 || R == 0) return r;
+  if (scratch == nullptr || scratch_bytes < lay.bytes) return PMOE_EINVAL;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.scale = scale * attn::kLog2e;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  // a request has 2^30 keys at most: a window or sinks of as many hide nothing
+  a.window = window >= (1 << 30) || sinks >= (1 << 30) ? 0 : window;
+  a.sinks = a.window > 0 ? sinks : 0;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.err = err_out;
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  a.plan = reinterpret_cast<int64_t*>(base);
+  a.first = reinterpret_cast<int32_t*>(base + lay.first);
+  a.items = reinterpret_cast<chunk::Item*>(base + lay.items);
+  a.o_part = reinterpret_cast<float*>(base + lay.o);
+  a.ml_part = reinterpret_cast<float2*>(base + lay.ml);
+  cudaStream_t s = (cudaStream_t)stream;
+  const bool f8 = kv->dtype == PMOE_KV_E4M3;
+  if (kv->head_dim == 128) return f8 ? chunk::launch_all<128, true>(a, s) : chunk::launch_all<128, false>(a, s);
+  return f8 ? chunk::launch_all<64, true>(a, s) : chunk::launch_all<64, false>(a, s);
+}

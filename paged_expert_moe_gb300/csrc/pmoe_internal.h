@@ -30,7 +30,7 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // Device error word bits.
 // (16: a bounded wait of a tensor-core kernel expired)
 enum : int32_t { kErrBadExpertId = 1, kErrPlanOverflow = 2, kErrBadSlot = 4, kErrPullTimeout = 8, kErrTcWait = 16,
-                 kErrBadAxis = 32, kErrBadPage = 64, kErrBadLength = 128 };
+                 kErrBadAxis = 32, kErrBadPage = 64, kErrBadLength = 128, kErrNoPages = 256, kErrBadToken = 512 };
 
 // Layout of a layer's residency plan (int32 words), written by the residency kernel
 // and mirrored to pinned host memory in copy-engine mode.
