@@ -8,6 +8,9 @@ namespace chunk {
 
 using namespace attn;
 
+// Empty units at the start of an item, for each kv head: what its start and end cost beside its tiles.
+constexpr int kHead = 2;
+
 // A tile of query rows: up to tile_tokens tokens of one request, times the query heads of a kv head.
 struct Item {
   int32_t req;    // request
@@ -16,7 +19,7 @@ struct Item {
   int32_t p0;     // the first one's position
   int32_t nt;     // key tiles that some row sees: first the sinks' (below lo), then from lo on
   int32_t lo;
-  int64_t base;   // units before it; its own: nt a kv head
+  int64_t base;   // units before it; its own: kHead + nt a kv head
 };
 
 struct Args {
@@ -34,7 +37,7 @@ struct Args {
   __nv_bfloat16* out;
   float* lse;
   int32_t* err;
-  int ctas, tile_tokens, part_rows;
+  int ctas, tile_tokens, few_tokens, part_rows;
   // scratch
   int64_t* plan;   // [2]: units, CTAs that have some
   int32_t* first;  // [ctas] the item of each CTA's first unit
@@ -68,35 +71,74 @@ __device__ __forceinline__ int row_token(const Args& a, int r) {
   return a.group == 1 ? r : (int)__umulhi((uint32_t)r, a.group_magic);
 }
 
-// One segment of a CTA's run: key tiles [t0, t1) of an item's nt, for one kv head.
-struct Segment {
-  Item it;
-  int h, t0, t1;
-  __device__ __forceinline__ int p1() const { return it.p0 + it.ntok - 1; }
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == it.nt; }
+// One segment of a CTA's run: key tiles [t0, t1) of an item, for one kv head. Items of up to 128 rows
+// take one query tile's warps and accumulators, in turn the first's and the second's (`lane`): one's
+// end then overlaps with the other's beginning.
+struct __align__(16) Segment {
+  int32_t req, tok0, p0, lo;  // as the item's
+  int32_t h, t0, t1;
+  int32_t bits;               // tokens, and from bit 16 on: two query tiles, lane, all of the item's tiles
+  __device__ __forceinline__ int ntok() const { return bits & 0xffff; }
+  __device__ __forceinline__ bool two() const { return bits >> 16 & 1; }
+  __device__ __forceinline__ int lane() const { return bits >> 17 & 1; }
+  __device__ __forceinline__ bool whole() const { return bits >> 18 & 1; }
+  __device__ __forceinline__ int p1() const { return p0 + ntok() - 1; }
+  __device__ __forceinline__ bool has(int q) const { return two() || lane() == q; }
 };
-// The first key of tile t of an item.
+// The first key of tile t.
 template <int KEYS>
-__device__ __forceinline__ int tile_key(const Args& a, const Item& it, int t) {
-  const int st = a.window > 0 ? min((a.sinks + KEYS - 1) / KEYS, it.lo) : 0;
-  return (t < st ? t : it.lo + t - st) * KEYS;
+__device__ __forceinline__ int tile_key(const Args& a, const Segment& s, int t) {
+  const int st = a.window > 0 ? min((a.sinks + KEYS - 1) / KEYS, s.lo) : 0;
+  return (t < st ? t : s.lo + t - st) * KEYS;
 }
+// A CTA's segments in order; the item after the present one is on its way.
 struct Walk {
-  int item, h, t;
+  int item, h, at;  // at: position in the item's units for this head, kHead empty ones first
   int64_t left;
+  int lane;
+  Item cur, ahead;
+  __device__ __forceinline__ void begin(const Args& a, int cta) {
+    const int64_t units = a.plan[0];
+    const int ctas = (int)a.plan[1];
+    left = 0;
+    if (cta >= ctas) return;
+    const int64_t u0 = run_start(units, ctas, cta);
+    left = run_start(units, ctas, cta + 1) - u0;
+    item = a.first[cta];
+    cur = a.items[item];
+    const int64_t in = u0 - cur.base;
+    const int n = cur.nt + kHead;
+    h = (int)(in / n);
+    at = (int)(in - (int64_t)h * n);
+    lane = 1;
+    if (left > (int64_t)(a.kv.kv_heads - h) * n - at) ahead = a.items[item + 1];
+  }
   __device__ __forceinline__ bool next(const Args& a, Segment* s) {
-    if (left <= 0) return false;
-    s->it = a.items[item];
-    s->h = h;
-    s->t0 = t;
-    s->t1 = (int)min((int64_t)s->it.nt, t + left);
-    left -= s->t1 - t;
-    t = s->t1;
-    if (t == s->it.nt) {
-      t = 0;
-      if (++h == a.kv.kv_heads) h = 0, ++item;
+    while (left > 0) {
+      const int n = cur.nt + kHead, to = (int)min((int64_t)n, at + left);
+      s->req = cur.req, s->tok0 = cur.tok0, s->p0 = cur.p0, s->lo = cur.lo;
+      s->h = h;
+      s->t0 = max(at - kHead, 0);
+      s->t1 = max(to - kHead, 0);
+      const bool two = cur.ntok * a.group > 128, whole = s->t0 == 0 && s->t1 == cur.nt;
+      if (!two && s->t1 > s->t0) lane ^= 1;
+      s->bits = cur.ntok | (two ? 1 << 16 : 0) | lane << 17 | (whole ? 1 << 18 : 0);
+      left -= to - at;
+      at = to;
+      if (at == n) {
+        at = 0;
+        if (++h == a.kv.kv_heads) {
+          h = 0;
+          ++item;
+          if (left > 0) {
+            cur = ahead;
+            if (left > (int64_t)(cur.nt + kHead) * a.kv.kv_heads) ahead = a.items[item + 1];
+          }
+        }
+      }
+      if (s->t1 > s->t0) return true;  // (else only empty units of it are in this run)
     }
-    return true;
+    return false;
   }
 };
 

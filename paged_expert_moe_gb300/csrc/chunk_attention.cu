@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
         it.nt = max((p1 >= 0 ? p1 / kKeys + 1 : 0) - it.lo, p1 < 0 ? 1 : 0) + st;
       }
       int64_t more;
-      it.base = units + block_scan((int64_t)it.nt * a.kv.kv_heads, warps, &more);
+      it.base = units + block_scan(j < all ? (int64_t)(it.nt + kHead) * a.kv.kv_heads : 0, warps, &more);
       if (j < all) a.items[items + j] = it;
       units += more;
     }
@@ -128,10 +128,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   }
   __syncthreads();
   // runs of two units at least; each run's first item
-  const int ctas = (int)min((int64_t)a.ctas, (units + 1) / 2);
+  const int ctas = (int)min((int64_t)a.ctas, (units + 1 + kHead) / (2 + kHead));
   if (tid == 0) a.plan[0] = units, a.plan[1] = ctas;
   for (int j = tid; j < items; j += kPlanThreads) {
-    const int64_t b0 = a.items[j].base, b1 = b0 + (int64_t)a.items[j].nt * a.kv.kv_heads;
+    const int64_t b0 = a.items[j].base, b1 = b0 + (int64_t)(a.items[j].nt + kHead) * a.kv.kv_heads;
     for (int c = (int)((b0 * ctas + units - 1) / units); c < ctas; ++c) {
       const int64_t u = run_start(units, ctas, c);
       if (u >= b1) break;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
 template <int D, bool F8>
 struct Cfg {
   static constexpr int kTileBytes = kKeys * D * 2;        // one K or V tile, 16-bit operands
-  static constexpr int kQBytes = 128 * D * 2;             // one query tile
+  static constexpr int kQBytes = kRows * D * 2;           // both query tiles: [D / 64][256 rows][128 bytes]
   static constexpr int kSlots = D == 128 ? 5 : 8;         // ring of K and V tiles
   static constexpr int kThreads = F8 ? 512 : 384;         // whole warpgroups
   // Registers a thread, by warpgroup: what the other roles give up the softmax takes. The
@@ -160,22 +160,41 @@ struct Cfg {
   static __device__ __forceinline__ uint8_t* raw(uint8_t* smem, uint32_t slot) {
     return D == 64 ? smem + kRing + slot * kRawBytes : smem + slot * kTileBytes + kRawBytes;
   }
-  static constexpr int kSmem = kRing + kRawRing + 2 * kQBytes + 1024 /* alignment */ + 1024 /* row factors */ + 512;
+  static constexpr int kSmem = kRing + kRawRing + kQBytes + 1024 /* alignment */ + 1024 /* row exponents */ + 1024;
   static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
   static constexpr int kGuards = F8 ? 4 : 2;              // warps that look at partly visible values
 };
 
+constexpr int kSegs = 12;
+
 struct Bars {
   uint64_t full[8], empty[8], raw[8];
   uint64_t vok[8];  // partly visible values are cleared
-  uint64_t sfull[2], pready[2], odone[2], qfull[2], staged[2], drain;
+  uint64_t sfull[2], pready[2], odone[2], ofree[2], qfull, qempty, drain;
   uint32_t tmem;
   int abort;
   // [guard warp][segment % 32]: cleared values that some row sees. A guard is at most four
   // segments ahead of the MMAs, and these seldom more than one ahead of a query tile's end.
   uint8_t poison[4][32];
+  // The segments, which the loader works out for all, in a ring that needs no way back: when it comes
+  // to segment s + 12, the tiles of s + 6 are done with (a ring of tiles holds four), hence
+  // both query tiles with a segment after s, as those of one query tile come in turn.
+  uint64_t segready[kSegs];
+  Segment segs[kSegs];
 };
-static_assert(sizeof(Bars) <= 512, "room behind the row factors");
+static_assert(sizeof(Bars) <= 1024, "room behind the row exponents");
+
+// Segment i; false after the last one, or where a wait gave up.
+__device__ __forceinline__ bool get_segment(Bars& b, uint32_t i, Segment* s, volatile int* abort_flag, int32_t* err) {
+  if (!warp_wait(&b.segready[i % kSegs], i / kSegs & 1, abort_flag, err)) return false;
+  const volatile int4* p = reinterpret_cast<const volatile int4*>(&b.segs[i % kSegs]);
+  s->req = p[0].x, s->tok0 = p[0].y, s->p0 = p[0].z, s->lo = p[0].w;
+  s->h = p[1].x, s->t0 = p[1].y, s->t1 = p[1].z, s->bits = p[1].w;
+  return s->bits != 0;
+}
+
+// the lowest n bits, n below 0 and above 32 as 0 and 32
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
 // bf16 pairs with an element that is not finite: the top bits of the 16-bit halves say which
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
@@ -187,11 +206,11 @@ __device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p,
   float sum = 0.f;
   const int psh = 31 - __clz(a.kv.page_size);
   for (int t = sg.t0; t < sg.t1; ++t) {
-    const int k0 = tile_key<kKeys>(a, sg.it, t);
-    if (all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys)) continue;
+    const int k0 = tile_key<kKeys>(a, sg, t);
+    if (all_see_tile(a, sg.p0, sg.p1(), k0, kKeys)) continue;
     for (int j = k0; j < k0 + kKeys && j <= p; ++j) {
       if (!sees(a, p, j)) continue;
-      const int page = a.page_table[(int64_t)sg.it.req * a.table_stride + (j >> psh)];
+      const int page = a.page_table[(int64_t)sg.req * a.table_stride + (j >> psh)];
       if ((unsigned)page >= (unsigned)a.kv.num_pages) continue;
       const int64_t at = page * a.kv.page_stride + ((int64_t)sg.h * a.kv.page_size + (j & (a.kv.page_size - 1))) * D + d;
       float v;
@@ -207,16 +226,19 @@ __device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p,
   return sum;
 }
 
+// q_many, q_few: boxes of tile_tokens and of few_tokens tokens of q, all heads of a kv head (bf16 caches)
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
-    chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a) {
+    chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ CUtensorMap q_many, const __grid_constant__ CUtensorMap q_few, const Args a) {
   using C = Cfg<D, F8>;
   constexpr int kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = smem + C::kRing + C::kRawRing;
-  float* qmul = reinterpret_cast<float*>(qs + 2 * C::kQBytes);  // [256]
-  Bars& b = *reinterpret_cast<Bars*>(qmul + 256);
+  // e4m3: the power of two that each row of q was divided by, of four segments in turn
+  volatile int8_t* qexp = reinterpret_cast<volatile int8_t*>(qs + C::kQBytes);  // [4][256]
+  Bars& b = *reinterpret_cast<Bars*>(qs + C::kQBytes + 1024);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &b.abort;
 
@@ -232,9 +254,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       mbar_init(&b.sfull[i], 1);
       mbar_init(&b.pready[i], 4);
       mbar_init(&b.odone[i], 1);
-      mbar_init(&b.qfull[i], 4);
-      mbar_init(&b.staged[i], 4);
+      mbar_init(&b.ofree[i], 4);
     }
+    mbar_init(&b.qfull, F8 ? 2 : 1);
+    mbar_init(&b.qempty, 1);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&b.segready[i], 1);
     mbar_init(&b.drain, 1);
     b.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -247,18 +271,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   // The issuing warp allocates all 512 columns: the base is column 0, lane 0. The other roles
   // touch TMEM only after its first products.
   constexpr uint32_t tmem = 0;
-  const int64_t units = a.plan[0];
-  const int ctas = (int)a.plan[1];
-  Walk walk{0, 0, 0, 0};
-  if ((int)blockIdx.x < ctas) {
-    const int64_t u0 = run_start(units, ctas, blockIdx.x);
-    walk.item = a.first[blockIdx.x];
-    const int64_t in = u0 - a.items[walk.item].base;
-    const int nt = a.items[walk.item].nt;
-    walk.h = (int)(in / nt);
-    walk.t = (int)(in - (int64_t)walk.h * nt);
-    walk.left = run_start(units, ctas, blockIdx.x + 1) - u0;
-  }
   const int psh = 31 - __clz(a.kv.page_size);
   Segment sg;
 
@@ -268,81 +280,66 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const int q = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + q * 128, to = lanes + 256 + q * 128;
-    constexpr int LPR = D / 8;  // threads of a row while Q is loaded
-    uint32_t n = 0, segs = 0;   // tiles and segments so far
-    uint32_t all = 0;           // segments of the CTA so far
+    uint32_t n = 0, segs = 0;   // tiles and segments of this query tile so far
     bool ok = true;
-    for (; ok && walk.next(a, &sg); ++all) {
-      const int rows = sg.it.ntok * a.group;
-      if (q * 128 >= rows) continue;
-      // the query tile, K-major with the 128-byte swizzle; rows beyond the last are zero.
+    for (uint32_t all = 0; ok && get_segment(b, all, &sg, abort_flag, a.err); ++all) {
+      if (!sg.has(q)) continue;
+      const int i = (sg.two() ? q * 128 : 0) + row;  // row of the item
+      const int rows = sg.ntok() * a.group;
+      const bool live = i - lane < rows;           // any row of this warp
+      const int tok = row_token(a, i), pos = sg.p0 + tok;  // (of rows beyond the last: any)
       // What a score is multiplied by, scale x key scale x the row's power of two, has to be above
-      // zero: then the largest score stays the largest, and a masked one -inf. So its sign goes
-      // into Q, and a row whose factor is 0 (or vanishes in fp32) has Q = 0 and factor 1.
+      // zero: then the largest score stays the largest, and a masked one -inf. So a sign goes
+      // to the scores, and where the factor is 0 (or vanishes in fp32) q is 0 and it is 1.
       const float ks = F8 ? a.kv.k_scale[sg.h] : 1.f;
-      const uint32_t flip = (a.scale < 0.f) != (ks < 0.f) ? 0x80008000u : 0u;
-      const int c = row % LPR;
-      uint4 v[LPR];  // LPR rows a thread, all in flight
-#pragma unroll
-      for (int p = 0; p < LPR; ++p) {
-        const int i = q * 128 + row / LPR + p * (128 / LPR);
-        v[p] = make_uint4(0, 0, 0, 0);
-        if (i < rows) {
-          const int t = row_token(a, i);
-          v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(sg.it.tok0 + t) * a.q_stride +
-                                                      (sg.h * a.group + i - t * a.group) * D + c * 8));
-        }
-      }
-#pragma unroll
-      for (int p = 0; p < LPR; ++p) {
-        const int r = row / LPR + p * (128 / LPR);
-        uint32_t w[4] = {v[p].x ^ flip, v[p].y ^ flip, v[p].z ^ flip, v[p].w ^ flip};
-        if (F8) {
-          float mx = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int e = row_exponent(mx);
-          const float factor = fabsf(a.scale) * fabsf(ks) * pow2(e), down = factor != 0.f ? pow2(-e) : 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-          if (c == 0) qmul[q * 128 + r] = factor != 0.f ? factor : 1.f;
-        }
-        *reinterpret_cast<uint4*>(qs + q * C::kQBytes + (c / 8) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      fence_async();
-      warp_arrive(&b.qfull[q]);
-      // the row factors of all threads
-      if (!warp_wait(&b.qfull[q], segs++ & 1, abort_flag, a.err)) break;
-      // (bf16, scale 0: times 2^-149 the largest score is below 2^-20)
-      const float mul = F8 ? qmul[q * 128 + row] : a.scale != 0.f ? fabsf(a.scale) : __uint_as_float(1);
-      const int pos = sg.it.p0 + row_token(a, q * 128 + row);  // (of rows beyond the last: any)
-
+      const bool negate = (a.scale < 0.f) != (ks < 0.f);
+      float mul = 1.f;
       float m = -INFINITY, l = 0.f;
       for (int t = sg.t0; t < sg.t1; ++t, ++n) {
         if (!warp_wait(&b.sfull[q], n & 1, abort_flag, a.err)) {
           ok = false;
           break;
         }
+        if (!live) {  // (whatever the scores are, as weights they reach their own rows only)
+          warp_arrive(&b.pready[q]);
+          continue;
+        }
         fence_after();
+        if (t == sg.t0) {
+          // (the scores are there, so q's rows were)
+          if (F8) {
+            const float factor = fabsf(a.scale) * fabsf(ks) * pow2(qexp[(all & 3) * 256 + i]);
+            mul = factor != 0.f ? factor : 1.f;
+          } else {
+            // (scale 0: times 2^-149 the largest score is below 2^-20)
+            mul = a.scale != 0.f ? fabsf(a.scale) : __uint_as_float(1);
+          }
+        }
+        const int k0 = tile_key<kKeys>(a, sg, t);
+        if (negate || !all_see_tile(a, sg.p0, sg.p1(), k0, kKeys)) {
+          // masked in TMEM: seldom needed code that does not displace the loop's from the cache
+          const int hi = pos - k0 + 1, lo = a.window > 0 ? hi - a.window : 0, sink = a.sinks - k0;
+          const uint32_t sign = negate ? 0x80000000u : 0u;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(ts + c, r);
+            const uint32_t see = low_bits(hi - c) & (~low_bits(lo - c) | low_bits(sink - c));
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) r[k] = see >> k & 1 ? r[k] ^ sign : 0xff800000u;
+            tmem_st16(ts + c, *reinterpret_cast<const uint32_t(*)[16]>(r));
+            tmem_st16(ts + c + 16, *reinterpret_cast<const uint32_t(*)[16]>(r + 16));
+          }
+          tmem_wait_st();
+        }
         float s[128];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
         tmem_wait_ld();
-        const int k0 = tile_key<kKeys>(a, sg.it, t);
-        if (!all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys)) {
-          const int hi = pos - k0, lo = a.window > 0 ? hi - a.window : -1, sink = a.sinks - k0;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > hi || (i <= lo && i >= sink)) s[i] = -INFINITY;
-        }
         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 128; i += 2) x[(i >> 1) & 3] = max3(x[(i >> 1) & 3], s[i], s[i + 1]);
+        for (int c = 0; c < 128; c += 2) x[(c >> 1) & 3] = max3(x[(c >> 1) & 3], s[c], s[c + 1]);
         const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
         if (t == sg.t0) {
           m = mx;
@@ -354,13 +351,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             if (grow) m = mx;
             l *= f;
 #pragma unroll 1
-            for (int i = 0; i < D; i += 16) {
+            for (int c = 0; c < D; c += 16) {
               uint32_t o[16];
-              tmem_ld16(to + i, o);
+              tmem_ld16(to + c, o);
               tmem_wait_ld();
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st16(to + i, o);
+              tmem_st16(to + c, o);
             }
           }
         }
@@ -368,9 +365,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         const uint64_t mul2 = pair(mul, mul), base2 = pair(-base, -base);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t p[16];
-          const float* sc = s + 32 * i;
+          const float* sc = s + 32 * c;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float y, z;
@@ -379,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             sum[k & 1] = add2(sum[k & 1], pair(y, z));
             p[k] = pack2<F8>(y, z);
           }
-          tmem_st16(ts + 16 * i, p);
+          tmem_st16(ts + 16 * c, p);
         }
         tmem_wait_st();
         fence_before();
@@ -388,79 +385,65 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         unpair(add2(sum[0], sum[1]), y, z);
         l += y + z;
       }
-      if (!ok) break;
-      if (!warp_wait(&b.odone[q], (segs - 1) & 1, abort_flag, a.err)) break;
-      fence_after();
-      bool poisoned = false;
+      if (!ok || !warp_wait(&b.odone[q], segs++ & 1, abort_flag, a.err)) break;
+      if (live) {
+        fence_after();
+        bool poisoned = false;
 #pragma unroll
-      for (int i = 0; i < C::kGuards; ++i) poisoned |= *(volatile uint8_t*)&b.poison[i][all & 31] != 0;
-      if (poisoned) {
+        for (int k = 0; k < C::kGuards; ++k) poisoned |= *(volatile uint8_t*)&b.poison[k][all & 31] != 0;
+        if (poisoned) {
 #pragma unroll 1
-        for (int i = 0; i < D; i += 16) {
-          uint32_t o[16];
-          tmem_ld16(to + i, o);
-          tmem_wait_ld();
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            o[k] = __float_as_uint(__uint_as_float(o[k]) + (q * 128 + row < rows ? poison_of<D, F8>(a, sg, pos, i + k) : 0.f));
-          tmem_st16(to + i, o);
-          tmem_wait_st();
-        }
-      }
-      // 32 columns at a time through shared memory (the query tile's, which is done with), so
-      // that a store covers whole lines: 8 threads a row of 128 bytes (of 64 in bf16), whose
-      // 16-byte (8-byte) chunks are swizzled by the row
-      const bool whole = sg.whole();
-      const float vs = (F8 ? a.kv.v_scale[sg.h] : 1.f) * (!whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);
-      const int64_t part0 = ((int64_t)blockIdx.x * 2 + (sg.t0 == 0)) * a.part_rows;
-      uint8_t* stage = qs + q * C::kQBytes + (warp & 3) * (C::kQBytes / 4);
-      int64_t dst[8];  // elements into out or o_part
-      const int last = rows - q * 128 - (warp & 3) * 32;  // rows of this warp
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = 4 * k + (lane >> 3), i = q * 128 + (warp & 3) * 32 + r;
-        const int t = row_token(a, i);
-        dst[k] = whole ? ((int64_t)(sg.it.tok0 + t) * a.q_heads + sg.h * a.group + i - t * a.group) * D + (lane & 7) * 4
-                       : (part0 + i) * D + (lane & 7) * 4;
-      }
-#pragma unroll
-      for (int d = 0; d < D; d += 32) {
-        uint32_t o[32];
-        tmem_ld32(to + d, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-              make_float4(__uint_as_float(o[4 * k]) * vs, __uint_as_float(o[4 * k + 1]) * vs,
-                          __uint_as_float(o[4 * k + 2]) * vs, __uint_as_float(o[4 * k + 3]) * vs);
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = 4 * k + (lane >> 3);
-          const float4 v4 = *reinterpret_cast<const float4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          if (r < last) {
-            if (whole)
-              *reinterpret_cast<uint2*>(a.out + dst[k] + d) = make_uint2(pack2<false>(v4.x, v4.y), pack2<false>(v4.z, v4.w));
-            else
-              *reinterpret_cast<float4*>(a.o_part + dst[k] + d) = v4;
+            for (int k = 0; k < 16; ++k)
+              o[k] = __float_as_uint(__uint_as_float(o[k]) + (i < rows ? poison_of<D, F8>(a, sg, pos, c + k) : 0.f));
+            tmem_st16(to + c, o);
+            tmem_wait_st();
           }
         }
-        __syncwarp();
-      }
-      const int i = q * 128 + row;
-      if (i < rows) {
-        if (!whole) {
-          a.ml_part[part0 + i] = make_float2(m, l);
-        } else if (a.lse != nullptr) {
-          const int t = row_token(a, i);
-          a.lse[(int64_t)(sg.it.tok0 + t) * a.q_heads + sg.h * a.group + i - t * a.group] =
-              m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+        // a thread its row, 32 columns at a time: whole sectors of out or of a part
+        const bool whole = sg.whole();
+        const float vs = (F8 ? a.kv.v_scale[sg.h] : 1.f) * (!whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);
+        const int64_t head = (int64_t)(sg.tok0 + tok) * a.q_heads + sg.h * a.group + i - tok * a.group;
+        const int64_t part = ((int64_t)blockIdx.x * 2 + (sg.t0 == 0)) * a.part_rows + i;
+        __nv_bfloat16* out = a.out + head * D;
+        float* o_part = a.o_part + part * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + c, o);
+          tmem_wait_ld();
+          if (i < rows) {
+            if (whole) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  w[j] = pack2<false>(__uint_as_float(o[k + 2 * j]) * vs, __uint_as_float(o[k + 2 * j + 1]) * vs);
+                *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<float4*>(o_part + c + k) =
+                    make_float4(__uint_as_float(o[k]) * vs, __uint_as_float(o[k + 1]) * vs, __uint_as_float(o[k + 2]) * vs,
+                                __uint_as_float(o[k + 3]) * vs);
+            }
+          }
         }
+        if (i < rows) {
+          if (!whole)
+            a.ml_part[part] = make_float2(m, l);
+          else if (a.lse != nullptr)
+            a.lse[head] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+        }
+        fence_before();
       }
-      // every warp is done with its stage before Q is written again
-      warp_arrive(&b.staged[q]);
-      if (!warp_wait(&b.staged[q], (segs - 1) & 1, abort_flag, a.err)) break;
-      fence_before();
+      warp_arrive(&b.ofree[q]);
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
@@ -475,68 +458,108 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       const uint32_t ring = smem_u32(smem), qa = smem_u32(qs);
       uint32_t kv = 0;               // K and V tiles so far
       uint32_t part = 0;             // by slot, whether an odd number of partly visible tiles was there
-      uint32_t seg[2] = {0, 0};      // segments of each query tile so far
-      uint32_t pn[2] = {0, 0};       // products with V of each query tile so far
-      bool ok = true;
-      auto wait_kv = [&](uint32_t i) {
-        return warp_wait(&b.full[i % kSlots], (i / kSlots) & 1, abort_flag, a.err);
-      };
-      auto scores = [&](int q, uint32_t slot, bool last) {  // last: of the query tiles on this slot
+      uint32_t segs = 0;
+      uint32_t pn[2] = {0, 0}, sn[2] = {0, 0};  // products with V, and segments, of each query tile so far
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity & 1, abort_flag, a.err); };
+      auto wait_kv = [&](uint32_t i) { return wait(&b.full[i % kSlots], i / kSlots); };
+      // scores of tile t of s by query tile q; the last query tile's are the last on this K tile, and
+      // with the last tile on this segment's q
+      auto scores = [&](const Segment& s, int t, int q, uint32_t slot) {
         if (converged_lane()) {
+          const uint32_t qq = qa + (s.two() && q ? 128 * 128 : 0);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
-            mma_bf16(tmem + q * 128, sw128_desc(qa + q * C::kQBytes + off), sw128_desc(ring + slot * C::kTileBytes + off), is,
-                     k > 0);
+            const uint32_t in = (k % 4) * 32;
+            mma_bf16(tmem + q * 128, sw128_desc(qq + (k / 4) * (kRows * 128) + in),
+                     sw128_desc(ring + slot * C::kTileBytes + (k / 4) * (kKeys * 128) + in), is, k > 0);
           }
           mma_commit(&b.sfull[q]);
-          if (last) mma_commit(&b.empty[slot]);
+          if (!s.two() || q == 1) {
+            mma_commit(&b.empty[slot]);
+            if (t + 1 == s.t1) mma_commit(&b.qempty);
+          }
         }
         __syncwarp();
       };
-      while (ok && walk.next(a, &sg)) {
-        const int nq = sg.it.ntok * a.group > 128 ? 2 : 1;
-        for (int q = 0; q < nq && ok; ++q) {
-          ok = warp_wait(&b.qfull[q], seg[q] & 1, abort_flag, a.err);
-          ++seg[q];
-        }
-        if (!ok || !wait_kv(kv)) break;
+      bool ok = true, have = get_segment(b, 0, &sg, abort_flag, a.err);
+      if (have) {
+        ok = wait(&b.qfull, segs) && wait_kv(kv);
         fence_after();
-        for (int q = 0; q < nq; ++q) scores(q, kv % kSlots, q + 1 == nq);
+        for (int q = 0; q < 2 && ok; ++q)
+          if (sg.has(q)) scores(sg, sg.t0, q, kv % kSlots);
+      }
+      while (ok && have) {
+        Segment nx;  // the next one; its first scores come among this one's last products
+        bool more = false;
         for (int t = sg.t0; t < sg.t1; ++t, kv += 2) {
-          const uint32_t vslot = (kv + 1) % kSlots;
-          const bool more = t + 1 < sg.t1;
-          if (!wait_kv(kv + 1) || (more && !wait_kv(kv + 2))) {
+          const uint32_t vslot = (kv + 1) % kSlots, kslot = (kv + 2) % kSlots;
+          const bool last = t + 1 == sg.t1;
+          if (last) {  // (the loader makes it known behind this tile)
+            more = get_segment(b, segs + 1, &nx, abort_flag, a.err);
+            if (__any_sync(0xffffffffu, *abort_flag)) {
+              ok = false;
+              break;
+            }
+          }
+          const Segment& s2 = last ? nx : sg;
+          const int t2 = last ? nx.t0 : t + 1;
+          const bool any = !last || more;
+          // the next scores come before and between this tile's products with V, but where q is late
+          const bool early = any && (!last || __all_sync(0xffffffffu, mbar_try_wait(&b.qfull, (segs + 1) & 1)));
+          const bool first = early && last && !sg.two() && !nx.two();  // the other query tile's turn: at once
+          if (early && !wait_kv(kv + 2)) {
             ok = false;
             break;
           }
-          if (!F8 && !all_see_tile(a, sg.it.p0, sg.p1(), tile_key<kKeys>(a, sg.it, t), kKeys)) {
-            if (!warp_wait(&b.vok[vslot], part >> vslot & 1, abort_flag, a.err)) {
+          fence_after();
+          if (first) scores(nx, t2, nx.lane(), kslot);
+          if (!wait_kv(kv + 1)) {
+            ok = false;
+            break;
+          }
+          if (!F8 && !all_see_tile(a, sg.p0, sg.p1(), tile_key<kKeys>(a, sg, t), kKeys)) {
+            if (!wait(&b.vok[vslot], part >> vslot)) {
               ok = false;
               break;
             }
             part ^= 1u << vslot;
           }
-          for (int q = 0; q < nq; ++q) {
-            if (!warp_wait(&b.pready[q], pn[q] & 1, abort_flag, a.err)) {
+          for (int q = 0; q < 2 && ok; ++q) {
+            if (sg.has(q)) {
+              // the weights, and at a segment's first tile the accumulators
+              if (!wait(&b.pready[q], pn[q]) || (t == sg.t0 && sn[q] > 0 && !wait(&b.ofree[q], sn[q] - 1))) {
+                ok = false;
+                break;
+              }
+              ++pn[q];
+              if (t == sg.t0) ++sn[q];
+              fence_after();
+              if (converged_lane()) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
+                             t > sg.t0 || k > 0);
+                if (last) mma_commit(&b.odone[q]);
+                if (!sg.two() || q == 1) mma_commit(&b.empty[vslot]);
+              }
+              __syncwarp();
+            }
+            if (early && !first && s2.has(q)) scores(s2, t2, q, kslot);
+          }
+          if (!ok) break;
+          if (any && !early) {
+            if (!wait(&b.qfull, segs + 1) || !wait_kv(kv + 2)) {
               ok = false;
               break;
             }
-            ++pn[q];
             fence_after();
-            if (converged_lane()) {
-#pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
-                           t > sg.t0 || k > 0);
-              if (!more) mma_commit(&b.odone[q]);
-              if (q + 1 == nq) mma_commit(&b.empty[vslot]);
-            }
-            __syncwarp();
-            if (more) scores(q, (kv + 2) % kSlots, q + 1 == nq);
+            for (int q = 0; q < 2; ++q)
+              if (nx.has(q)) scores(nx, t2, q, kslot);
           }
-          if (!ok) break;
         }
+        sg = nx;
+        have = more;
+        ++segs;
       }
       // every MMA and its arrival are done before the CTA leaves
       if (converged_lane()) {
@@ -553,14 +576,23 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       const int box = min(a.kv.page_size, kKeys), boxes = kKeys / box;
       uint32_t kv = 0;
       bool ok = true;
-      while (ok && walk.next(a, &sg)) {
-        const int32_t* table = a.page_table + (int64_t)sg.it.req * a.table_stride;
+      Walk walk;
+      walk.begin(a, blockIdx.x);
+      for (uint32_t i = 0; ok; ++i) {
+        if (!walk.next(a, &sg)) sg.bits = 0;
+        if (lane == 0) {
+          b.segs[i % kSegs] = sg;
+          mbar_arrive(&b.segready[i % kSegs]);
+        }
+        __syncwarp();
+        if (sg.bits == 0) break;
+        const int32_t* table = a.page_table + (int64_t)sg.req * a.table_stride;
         for (int t = sg.t0; t < sg.t1 && ok; ++t) {
           const int pb = lane / kHalves, hf = lane % kHalves;
-          const int key = tile_key<kKeys>(a, sg.it, t) + pb * box;
+          const int key = tile_key<kKeys>(a, sg, t) + pb * box;
           // pages with a key that some row sees
           bool use = pb < boxes && key <= sg.p1();
-          if (use && a.window > 0) use = key + box - 1 > sg.it.p0 - a.window || key < a.sinks;
+          if (use && a.window > 0) use = key + box - 1 > sg.p0 - a.window || key < a.sinks;
           int id = 0;
           if (use) {
             id = __ldg(table + (key >> psh));
@@ -590,29 +622,56 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         while (!mbar_try_wait(&arrive[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kWaitLimit) {
         }
       }
-    } else if (!F8) {
-      // ---------------- guards: warp 10 looks at keys 0-63 of partly visible tiles, 11 at the others
+    } else if constexpr (!F8) {
+      // ---------------- guards: warp 10 looks at keys 0-63 of partly visible tiles, 11 at the others;
+      // warp 10 also loads q. A box holds whole tokens, so rows beyond the item's are the next tokens' or zero.
       const int gw = warp - 10;
-      uint32_t kv = 0, segs = 0;
-      bool ok = true;
-      for (; ok && walk.next(a, &sg); ++segs) {
+      uint32_t kv = 0, segs = 0, loads = 0;
+      bool ok = get_segment(b, 0, &sg, abort_flag, a.err);
+      auto load_q = [&](const Segment& s) {
+        if (lane == 0) {
+          const bool few = s.ntok() <= a.few_tokens;
+          mbar_arrive_expect_tx(&b.qfull, (few ? a.few_tokens : a.tile_tokens) * a.group * D * 2);
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, &b.qfull, hf * 64, s.h * a.group, s.tok0);
+        }
+        __syncwarp();
+        ++loads;
+      };
+      if (gw == 0 && ok) load_q(sg);
+      while (ok) {
+        Segment nx;
+        bool more = false;
         if (lane == 0) *(volatile uint8_t*)&b.poison[gw][segs & 31] = 0;
+        __syncwarp();
         for (int t = sg.t0; t < sg.t1 && ok; ++t) {
-          const int k0 = tile_key<kKeys>(a, sg.it, t);
+          const int k0 = tile_key<kKeys>(a, sg, t);
           for (int v = 0; v < 2; ++v, ++kv) {
             const uint32_t slot = kv % kSlots;
             if (!warp_wait(&b.full[slot], (kv / kSlots) & 1, abort_flag, a.err)) {
               ok = false;
               break;
             }
-            if (v == 1 && !all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys)) {
+            if (v == 1 && t + 1 == sg.t1) {
+              // the next segment's q, once this one's last scores are there
+              more = get_segment(b, segs + 1, &nx, abort_flag, a.err);
+              if (more && gw == 0) {
+                if (!warp_wait(&b.qempty, segs & 1, abort_flag, a.err)) {
+                  ok = false;
+                  break;
+                }
+                load_q(nx);
+              }
+            }
+            if (v == 1 && !all_see_tile(a, sg.p0, sg.p1(), k0, kKeys)) {
               bool found = false;
 #pragma unroll 4
               for (int i = lane; i < 64 * (D / 8); i += 32) {
                 const int r = gw * 64 + i / (D / 8), c = i % (D / 8);
-                if (all_see(a, sg.it.p0, sg.p1(), k0 + r)) continue;
+                if (all_see(a, sg.p0, sg.p1(), k0 + r)) continue;
                 uint4* at = reinterpret_cast<uint4*>(smem + slot * C::kTileBytes + (c / 8) * (kKeys * 128) + r * 128 + (c & 7) * 16);
-                if (!any_sees(a, sg.it.p0, sg.p1(), k0 + r)) {
+                if (!any_sees(a, sg.p0, sg.p1(), k0 + r)) {
                   *at = make_uint4(0, 0, 0, 0);
                   continue;
                 }
@@ -635,6 +694,63 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             warp_arrive(&b.empty[slot]);
           }
         }
+        ok = ok && more;
+        sg = nx;
+        ++segs;
+      }
+      // q's copy in flight lands before the CTA leaves
+      if (loads > 0) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&b.qfull, (loads - 1) & 1) && clock64() - t0 < kWaitLimit) {
+        }
+      }
+    } else {
+      // ---------------- e4m3: warps 10 and 11 bring q, in fp16 divided by each row's power of two, into
+      // the K-major layout with the 128-byte swizzle. Rows beyond the item's stay what they were.
+      constexpr int LPR = D / 8, N = 8, kStep = 64 / LPR;  // threads of a row, loads in flight, rows at a time
+      const int tid = threadIdx.x - 10 * 32, c = tid % LPR;
+      uint32_t segs = 0;
+      for (; get_segment(b, segs, &sg, abort_flag, a.err); ++segs) {
+        const int rows = sg.ntok() * a.group;
+        const float ks = a.kv.k_scale[sg.h];
+        for (int r0 = tid / LPR; r0 - tid / LPR < rows; r0 += N * kStep) {
+          uint4 v[N];
+#pragma unroll
+          for (int p = 0; p < N; ++p) {
+            const int i = r0 + p * kStep;
+            v[p] = make_uint4(0, 0, 0, 0);
+            if (i < rows) {
+              const int t = row_token(a, i);
+              v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(sg.tok0 + t) * a.q_stride +
+                                                          (sg.h * a.group + i - t * a.group) * D + c * 8));
+            }
+          }
+          if (r0 < kStep && segs > 0 && !warp_wait(&b.qempty, (segs - 1) & 1, abort_flag, a.err)) break;
+#pragma unroll
+          for (int p = 0; p < N; ++p) {
+            const int r = r0 + p * kStep;
+            uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+            float mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e = row_exponent(mx);
+            const float down = fabsf(a.scale) * fabsf(ks) * pow2(e) != 0.f ? pow2(-e) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+            if (r < rows) {
+              if (c == 0) qexp[(segs & 3) * 256 + r] = (int8_t)e;
+              *reinterpret_cast<uint4*>(qs + (c / 8) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        fence_async();
+        warp_arrive(&b.qfull);
       }
     }
   } else if constexpr (F8) {
@@ -645,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     const int tid = threadIdx.x - 12 * 32, ch = tid % CH, r0 = tid / CH;
     uint32_t kv = 0, segs = 0;
     bool ok = true;
-    for (; ok && walk.next(a, &sg); ++segs) {
+    for (; ok && get_segment(b, segs, &sg, abort_flag, a.err); ++segs) {
       if (lane == 0) *(volatile uint8_t*)&b.poison[warp - 12][segs & 31] = 0;
       __syncwarp();
       for (int i2 = 2 * sg.t0; i2 < 2 * sg.t1; ++i2, ++kv) {  // K and V of each tile
@@ -655,8 +771,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           break;
         }
         const uint8_t* src = C::raw(smem, slot);
-        const int k0 = tile_key<kKeys>(a, sg.it, i2 / 2);
-        const bool check = (i2 & 1) && !all_see_tile(a, sg.it.p0, sg.p1(), k0, kKeys);
+        const int k0 = tile_key<kKeys>(a, sg, i2 / 2);
+        const bool check = (i2 & 1) && !all_see_tile(a, sg.p0, sg.p1(), k0, kKeys);
         uint4 raw[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -669,8 +785,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int j = k0 + r0 + i * (128 / CH);
-            if (all_see(a, sg.it.p0, sg.p1(), j)) continue;
-            const bool any = any_sees(a, sg.it.p0, sg.p1(), j);
+            if (all_see(a, sg.p0, sg.p1(), j)) continue;
+            const bool any = any_sees(a, sg.p0, sg.p1(), j);
             uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -726,9 +842,9 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   if (c >= ctas) return;
   const Item it = a.items[a.first[c]];
   const int64_t u = run_start(units, ctas, c), in = u - it.base;
-  const int h = (int)(in / it.nt);
-  const int64_t g0 = it.base + (int64_t)h * it.nt, g1 = g0 + it.nt;
-  if (u == g0 || run_start(units, ctas, c - 1) > g0) return;
+  const int h = (int)(in / (it.nt + kHead));
+  const int64_t g0 = it.base + (int64_t)h * (it.nt + kHead) + kHead, g1 = g0 + it.nt;  // its tiles
+  if (u <= g0 || run_start(units, ctas, c - 1) > g0) return;
   const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (i >= it.ntok * a.group) return;
   int n = 1;  // parts: CTA c - 1's slot 1, then slots 0
@@ -782,17 +898,27 @@ int make_map(const Args& a, void* base, CUtensorMap* m) {
   return tc_encode_map(m, base, 4, dims, strides, box, !f8 ? kTcMapBf16Sw128 : D == 128 ? kTcMapBytesSw128 : kTcMapBytesSw64);
 }
 
+int make_q_map(const Args& a, int tokens, CUtensorMap* m) {
+  const uint64_t D = a.kv.head_dim;
+  const uint64_t dims[3] = {D, (uint64_t)a.q_heads, (uint64_t)a.T};
+  const uint64_t strides[2] = {D * 2, (uint64_t)a.q_stride * 2};
+  const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)tokens};
+  return tc_encode_map(m, const_cast<__nv_bfloat16*>(a.q), 3, dims, strides, box, kTcMapBf16Sw128);
+}
+
 template <int D, bool F8>
 int launch_all(const Args& a, cudaStream_t s) {
   using C = Cfg<D, F8>;
   const char* what = "moe_chunk_attention";
   static SmemLimit limit;
-  CUtensorMap mk, mv;
+  CUtensorMap mk, mv, many, few;
   int r = make_map(a, a.kv.k, &mk);
   if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
+  if (r == PMOE_OK) r = make_q_map(a, a.tile_tokens, &many);
+  if (r == PMOE_OK) r = make_q_map(a, a.few_tokens, &few);
   if (r == PMOE_OK) r = limit.set(reinterpret_cast<const void*>(chunk_kernel<D, F8>), C::kSmem, what);
   if (r == PMOE_OK) r = launch(what, plan_kernel, 1, kPlanThreads, 0, s, true, 1, a);
-  if (r == PMOE_OK) r = launch(what, chunk_kernel<D, F8>, a.ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, a);
+  if (r == PMOE_OK) r = launch(what, chunk_kernel<D, F8>, a.ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, many, few, a);
   if (r != PMOE_OK || a.ctas == 1) return r;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
@@ -827,6 +953,7 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int R, Args* a, Layout* l) 
   a->ctas = sm_count();
   if (a->ctas == 0) return PMOE_ECUDA;
   a->tile_tokens = kRows / a->group;
+  a->few_tokens = std::max(1, 16 / a->group);
   a->part_rows = std::min(kRows, T * a->group);
   const size_t parts = (size_t)a->ctas * 2 * a->part_rows;
   auto up = [](size_t n) { return (n + 15) / 16 * 16; };
