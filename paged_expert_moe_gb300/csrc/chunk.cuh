@@ -1,4 +1,4 @@
-// Shared by the kernels of moe_chunk_attention: arguments, the plan in scratch, what a row sees.
+// moe_chunk_attention: its arguments, what a row sees, and a CTA's share of the work.
 #pragma once
 
 #include "attn_tc.cuh"
@@ -10,17 +10,6 @@ using namespace attn;
 
 // Empty units at the start of an item, for each kv head: what its start and end cost beside its tiles.
 constexpr int kHead = 2;
-
-// A tile of query rows: up to tile_tokens tokens of one request, times the query heads of a kv head.
-struct Item {
-  int32_t req;    // request
-  int32_t tok0;   // its first token's row of q
-  int32_t ntok;   // tokens
-  int32_t p0;     // the first one's position
-  int32_t nt;     // key tiles that some row sees: first the sinks' (below lo), then from lo on
-  int32_t lo;
-  int64_t base;   // units before it; its own: kHead + nt a kv head
-};
 
 struct Args {
   pmoe_kv_desc kv;
@@ -39,13 +28,11 @@ struct Args {
   int32_t* err;
   int ctas, tile_tokens, few_tokens, part_rows;
   // scratch
-  int64_t* plan;   // [2]: units, CTAs that have some
-  int32_t* first;  // [ctas] the item of each CTA's first unit
-  Item* items;
   // Parts of items that a CTA does not take whole: slot 0 where it continues one, slot 1 where it
   // begins one. o: sum of weights x values, ml: (base of the weights' exponents, sum of weights).
   float* o_part;    // [ctas][2][part_rows][head_dim]
   float2* ml_part;  // [ctas][2][part_rows]
+  uint32_t* done;   // [ctas][8] parts written of the item that begins in a CTA and ends in another, by 32 rows
 };
 
 // Visible keys of a row at position p: j <= p, and with a window j > p - window or j < sinks.
@@ -71,17 +58,51 @@ __device__ __forceinline__ int row_token(const Args& a, int r) {
   return a.group == 1 ? r : (int)__umulhi((uint32_t)r, a.group_magic);
 }
 
+// The CTA that takes unit u: the largest c with run_start(c) <= u.
+__device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) { return (int)(((u + 1) * ctas - 1) / units); }
+
+// A request's rows of this step.
+struct Request {
+  int start, n, len;
+  bool bad;
+};
+// `r`'s, before what the rows of the ones ahead of it leave of T.
+__device__ __forceinline__ Request request(const Args& a, int r) {
+  Request q{0, 0, 0, false};
+  if (r >= a.R) return q;
+  const int s0 = a.q_start[r], s1 = a.q_start[r + 1], len = a.kv_len[r];
+  q.start = min(max(s0, 0), a.T);
+  const int end = min(max(s1, 0), a.T);
+  q.n = max(end - q.start, 0);
+  const int64_t room = (int64_t)a.table_stride * a.kv.page_size;
+  q.len = (int)min((int64_t)max(len, 0), room);
+  q.bad = s0 != q.start || s1 != end || end < q.start || len != q.len;
+  return q;
+}
+
+// A tile of query rows (an item): up to tile_tokens tokens of one request, times the query heads of
+// a kv head. lo: the first of its key tiles beside the sinks'. Returns how many it has.
+__device__ __forceinline__ int key_tiles(const Args& a, int p0, int ntok, int* lo) {
+  const int p1 = p0 + ntok - 1;
+  *lo = a.window > 0 ? max(p0 - a.window + 1, 0) / kTcKeys : 0;
+  if (p1 < 0) return 1;  // rows before the first key: a tile of which they see nothing
+  const int st = a.window > 0 ? min((a.sinks + kTcKeys - 1) / kTcKeys, *lo) : 0;
+  return p1 / kTcKeys + 1 - *lo + st;
+}
+
 // One segment of a CTA's run: key tiles [t0, t1) of an item, for one kv head. Items of up to 128 rows
 // take one query tile's warps and accumulators, in turn the first's and the second's (`lane`): one's
 // end then overlaps with the other's beginning.
 struct __align__(16) Segment {
-  int32_t req, tok0, p0, lo;  // as the item's
-  int32_t h, t0, t1;
-  int32_t bits;               // tokens, and from bit 16 on: two query tiles, lane, all of the item's tiles
-  __device__ __forceinline__ int ntok() const { return bits & 0xffff; }
-  __device__ __forceinline__ bool two() const { return bits >> 16 & 1; }
-  __device__ __forceinline__ int lane() const { return bits >> 17 & 1; }
-  __device__ __forceinline__ bool whole() const { return bits >> 18 & 1; }
+  int32_t req, tok0, p0, lo;  // request, first row of q, its position, first key tile beside the sinks'
+  int32_t t0, t1;
+  int32_t join;  // of a part: the CTA with the item's first tile, and from bit 16 on the number of parts
+  int32_t bits;  // tokens, and from bit 10 on: two query tiles, lane, all of the item's tiles; 13: kv head
+  __device__ __forceinline__ int ntok() const { return bits & 1023; }
+  __device__ __forceinline__ bool two() const { return bits >> 10 & 1; }
+  __device__ __forceinline__ int lane() const { return bits >> 11 & 1; }
+  __device__ __forceinline__ bool whole() const { return bits >> 12 & 1; }
+  __device__ __forceinline__ int h() const { return bits >> 13; }
   __device__ __forceinline__ int p1() const { return p0 + ntok() - 1; }
   __device__ __forceinline__ bool has(int q) const { return two() || lane() == q; }
 };
@@ -91,49 +112,85 @@ __device__ __forceinline__ int tile_key(const Args& a, const Segment& s, int t) 
   const int st = a.window > 0 ? min((a.sinks + KEYS - 1) / KEYS, s.lo) : 0;
   return (t < st ? t : s.lo + t - st) * KEYS;
 }
-// A CTA's segments in order; the item after the present one is on its way.
+
+// Where a CTA's run of units begins. An item has kHead + its key tiles units a kv head, items come
+// request by request.
+struct Run {
+  int64_t units, left, u, before;  // all units, the run's, its first one's; rows of the requests ahead
+  int ctas, req, tile, h, at;      // request, tile of its rows, kv head, unit of the item
+};
+
+// A CTA's segments in order, by a whole warp: lane i holds request `batch` + i.
 struct Walk {
-  int item, h, at;  // at: position in the item's units for this head, kHead empty ones first
-  int64_t left;
-  int lane;
-  Item cur, ahead;
-  __device__ __forceinline__ void begin(const Args& a, int cta) {
-    const int64_t units = a.plan[0];
-    const int ctas = (int)a.plan[1];
-    left = 0;
-    if (cta >= ctas) return;
-    const int64_t u0 = run_start(units, ctas, cta);
-    left = run_start(units, ctas, cta + 1) - u0;
-    item = a.first[cta];
-    cur = a.items[item];
-    const int64_t in = u0 - cur.base;
-    const int n = cur.nt + kHead;
-    h = (int)(in / n);
-    at = (int)(in - (int64_t)h * n);
-    lane = 1;
-    if (left > (int64_t)(a.kv.kv_heads - h) * n - at) ahead = a.items[item + 1];
+  Run run;
+  int64_t first;  // unit of the item's first tile, for this head
+  int batch, k, lane, p0, ntok, tok0, nt, lo;
+  Request mine;
+  uint32_t some;  // lanes whose requests have rows
+
+  __device__ __forceinline__ void load(const Args& a, int from) {
+    const int l = threadIdx.x & 31;
+    batch = from;
+    mine = request(a, from + l);
+    int64_t upto = mine.n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t d = __shfl_up_sync(0xffffffffu, upto, o);
+      if (l >= o) upto += d;
+    }
+    if (run.before + upto > a.T) mine.n = 0;
+    run.before += __shfl_sync(0xffffffffu, upto, 31);
+    some = __ballot_sync(0xffffffffu, mine.n > 0);
+  }
+  __device__ __forceinline__ void item(const Args& a) {
+    const int start = __shfl_sync(0xffffffffu, mine.start, k), n = __shfl_sync(0xffffffffu, mine.n, k),
+              len = __shfl_sync(0xffffffffu, mine.len, k), i0 = run.tile * a.tile_tokens;
+    tok0 = start + i0;
+    ntok = min(a.tile_tokens, n - i0);
+    p0 = len - n + i0;
+    nt = key_tiles(a, p0, ntok, &lo);
+  }
+  __device__ __forceinline__ void begin(const Args& a, const Run& r) {
+    run = r;
+    if (run.left <= 0) return;
+    load(a, run.req);
+    k = 0, lane = 1;
+    item(a);
+    first = run.u - run.at + kHead;
   }
   __device__ __forceinline__ bool next(const Args& a, Segment* s) {
-    while (left > 0) {
-      const int n = cur.nt + kHead, to = (int)min((int64_t)n, at + left);
-      s->req = cur.req, s->tok0 = cur.tok0, s->p0 = cur.p0, s->lo = cur.lo;
-      s->h = h;
-      s->t0 = max(at - kHead, 0);
+    while (run.left > 0) {
+      const int n = nt + kHead, to = (int)min((int64_t)n, run.at + run.left);
+      s->req = batch + k, s->tok0 = tok0, s->p0 = p0, s->lo = lo;
+      s->t0 = max(run.at - kHead, 0);
       s->t1 = max(to - kHead, 0);
-      const bool two = cur.ntok * a.group > 128, whole = s->t0 == 0 && s->t1 == cur.nt;
+      const bool two = ntok * a.group > 128, whole = s->t0 == 0 && s->t1 == nt;
       if (!two && s->t1 > s->t0) lane ^= 1;
-      s->bits = cur.ntok | (two ? 1 << 16 : 0) | lane << 17 | (whole ? 1 << 18 : 0);
-      left -= to - at;
-      at = to;
-      if (at == n) {
-        at = 0;
-        if (++h == a.kv.kv_heads) {
-          h = 0;
-          ++item;
-          if (left > 0) {
-            cur = ahead;
-            if (left > (int64_t)(cur.nt + kHead) * a.kv.kv_heads) ahead = a.items[item + 1];
+      s->bits = ntok | (two ? 1 << 10 : 0) | lane << 11 | (whole ? 1 << 12 : 0) | run.h << 13;
+      s->join = 0;
+      if (!whole) {
+        const int c0 = cta_of(run.units, run.ctas, first);
+        s->join = c0 | (cta_of(run.units, run.ctas, first + nt - 1) - c0 + 1) << 16;
+      }
+      run.left -= to - run.at;
+      run.at = to;
+      if (to == n && run.left > 0) {
+        run.at = 0;
+        first += n;
+        if (++run.h == a.kv.kv_heads) {
+          run.h = 0;
+          ++run.tile;
+          if (run.tile * a.tile_tokens >= __shfl_sync(0xffffffffu, mine.n, k)) {
+            run.tile = 0;
+            uint32_t rest = k < 31 ? some >> (k + 1) << (k + 1) : 0;
+            while (rest == 0 && batch + 32 < a.R) load(a, batch + 32), rest = some;
+            if (rest == 0) {  // (some units are left, so some request has rows; if its numbers are still the same)
+              run.left = 0;
+              return s->t1 > s->t0;
+            }
+            k = __ffs(rest) - 1;
           }
+          item(a);
         }
       }
       if (s->t1 > s->t0) return true;  // (else only empty units of it are in this run)

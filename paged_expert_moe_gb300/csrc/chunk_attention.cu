@@ -6,9 +6,9 @@
 // keys at a time, as two 128-row query tiles that share each K and V tile. Rows of a tile differ in
 // what they see only in its last key tiles and at a window's edge; all others take no masks.
 //
-// Work: the lengths are on the device, so a first kernel lists the tiles with the key tiles that each
-// needs, and cuts the sum into equal runs, one a CTA and one CTA an SM. What a run takes
-// of a tile without taking all of it is left as a part, and a last kernel joins the parts.
+// Work: the lengths are on the device, so each CTA adds up the key tiles that all tiles of rows need
+// and takes its share, one of equal runs, one CTA an SM. What a run has of a tile of rows without having
+// all of it is left as a part in scratch; whoever writes the last part of a tile joins them, in order.
 //
 // Warps: 0-3 and 4-7 own one query tile each, a thread one row (a TMEM lane): scores from TMEM,
 // weights back to TMEM in their place as the 16-bit A operand of the second product. Warp 8 issues
@@ -32,10 +32,9 @@ constexpr int kRows = 256;      // of a query tile pair
 
 // ---------------------------------------------------------------- the plan
 
-constexpr int kPlanThreads = 1024;
-
-// Exclusive sums over the block; *total: of all.
-__device__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* total) {
+// Sums over the threads before this one; *total: over all of them. warps: [2][32].
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
 #pragma unroll
@@ -45,99 +44,95 @@ __device__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* total) {
   }
   if (lane == 31) warps[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int64_t w = warps[lane];
+  // every warp adds up the warps' sums for itself
+  int64_t w = lane < NT / 32 ? warps[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    warps[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int64_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
   __syncthreads();
-  *total = warps[31];
-  const int64_t r = (warp > 0 ? warps[warp - 1] : 0) + x - v;
-  __syncthreads();
-  return r;
+  return (warp > 0 ? before : 0) + x - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
-  __shared__ int64_t warps[32];
-  __shared__ int upto[kPlanThreads + 1];  // tiles before each request of the block's turn
-  __shared__ int s_start[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
+template <int NT>
+struct PlanSmem {
+  int64_t warps[32], rows[NT];  // rows of the requests ahead
+  int upto[NT + 1];             // tiles before each request of the turn
+  int n[NT], len[NT];
+};
+
+// The start of this CTA's run, by all NT threads: the units of all items are added up, NT requests and NT
+// items at a time, and the item with the run's first unit is looked for; where one turn has them all it is
+// at hand, else in a second pass.
+template <int NT>
+__device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
   const int tid = threadIdx.x;
+  int64_t units = 0;
+  int ctas = 0;
+  if (tid == 0) run->left = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t sum = 0, rows = 0;
+    for (int r0 = 0; r0 < a.R; r0 += NT) {
+      Request q = request(a, r0 + tid);
+      // starts that go back may name more rows than there are
+      int64_t some, all;
+      const int64_t before = rows + block_scan<NT>(q.n, m.warps, &some);
+      if (before + q.n > a.T) q.bad = true, q.n = 0;
+      if (q.bad && pass == 0 && blockIdx.x == 0 && a.err != nullptr) atomicOr(a.err, kErrBadLength);
+      rows += some;
+      m.upto[tid] = (int)block_scan<NT>((q.n + a.tile_tokens - 1) / a.tile_tokens, m.warps, &all);
+      m.n[tid] = q.n, m.len[tid] = q.len, m.rows[tid] = before;
+      if (tid == 0) m.upto[NT] = (int)all;
+      __syncthreads();
+      for (int j0 = 0; j0 < all; j0 += NT) {
+        const int j = j0 + tid;
+        int lo = 0, hi = NT, len = 0, i = 0;  // upto[lo] <= j < upto[hi]
+        if (j < all) {
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (m.upto[mid] <= j)
+              lo = mid;
+            else
+              hi = mid;
+          }
+          i = j - m.upto[lo];
+          const int i0 = i * a.tile_tokens;
+          int first;
+          len = kHead + key_tiles(a, m.len[lo] - m.n[lo] + i0, min(a.tile_tokens, m.n[lo] - i0), &first);
+        }
+        int64_t more;
+        const int64_t base = sum + block_scan<NT>((int64_t)len * a.kv.kv_heads, m.warps, &more);
+        sum += more;
+        const bool single = a.R <= NT && all <= NT;
+        if (single) units = sum;
+        if (pass == 1 || single) {
+          // runs of two tiles' units at least
+          ctas = (int)min((int64_t)a.ctas, (units + kHead + 1) / (kHead + 2));
+          const int64_t u = run_start(units, ctas, blockIdx.x), in = u - base;
+          if ((int)blockIdx.x < ctas && in >= 0 && in < (int64_t)len * a.kv.kv_heads) {
+            run->units = units, run->left = run_start(units, ctas, blockIdx.x + 1) - u, run->u = u, run->before = m.rows[lo];
+            run->ctas = ctas, run->req = r0 + lo, run->tile = i;
+            run->h = (int)(in / len), run->at = (int)(in - in / len * len);
+          }
+        }
+        if (single) pass = 2;
+      }
+    }
+    if (sum == 0) break;
+    units = sum;
+  }
+  fence_async();  // what this wrote, TMA will write again
+  __syncthreads();
+}
+
+// Clears the counts of an item's parts.
+__global__ void __launch_bounds__(256) clear_kernel(uint32_t* done, int n) {
   pdl_wait();
   pdl_trigger();
-  const int64_t room = (int64_t)a.table_stride * a.kv.page_size;
-  int items = 0;
-  int64_t units = 0, rows = 0;
-  for (int r0 = 0; r0 < a.R; r0 += kPlanThreads) {
-    const int r = r0 + tid;
-    int start = 0, n = 0, len = 0;
-    bool bad = false;
-    if (r < a.R) {
-      const int s0 = a.q_start[r], s1 = a.q_start[r + 1];
-      start = min(max(s0, 0), a.T);
-      const int end = min(max(s1, 0), a.T);
-      n = max(end - start, 0);
-      len = a.kv_len[r];
-      bad = s0 != start || s1 != end || end < start;
-      if (len < 0 || len > room) bad = true, len = len < 0 ? 0 : (int)room;
-    }
-    // starts that go back may name more rows than there are
-    int64_t some;
-    const int64_t before = rows + block_scan(n, warps, &some);
-    rows += some;
-    if (before + n > a.T) bad = true, n = 0;
-    if (bad && a.err != nullptr) atomicOr(a.err, kErrBadLength);
-    const int tiles = (n + a.tile_tokens - 1) / a.tile_tokens;
-    int64_t all;
-    upto[tid] = (int)block_scan(tiles, warps, &all);
-    s_start[tid] = start, s_n[tid] = n, s_len[tid] = len;
-    if (tid == 0) upto[kPlanThreads] = (int)all;
-    __syncthreads();
-    for (int j0 = 0; j0 < all; j0 += kPlanThreads) {
-      const int j = j0 + tid;
-      Item it{};
-      if (j < all) {
-        int lo = 0, hi = kPlanThreads;  // upto[lo] <= j < upto[hi]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (upto[mid] <= j)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        const int i0 = (j - upto[lo]) * a.tile_tokens;
-        it.req = r0 + lo;
-        it.tok0 = s_start[lo] + i0;
-        it.ntok = min(a.tile_tokens, s_n[lo] - i0);
-        it.p0 = s_len[lo] - s_n[lo] + i0;
-        const int p1 = it.p0 + it.ntok - 1;
-        it.lo = a.window > 0 ? max(it.p0 - a.window + 1, 0) / kKeys : 0;
-        const int st = a.window > 0 ? min((a.sinks + kKeys - 1) / kKeys, it.lo) : 0;
-        // a tile of rows before the first key has one tile of keys all the same, of which it sees none
-        it.nt = max((p1 >= 0 ? p1 / kKeys + 1 : 0) - it.lo, p1 < 0 ? 1 : 0) + st;
-      }
-      int64_t more;
-      it.base = units + block_scan(j < all ? (int64_t)(it.nt + kHead) * a.kv.kv_heads : 0, warps, &more);
-      if (j < all) a.items[items + j] = it;
-      units += more;
-    }
-    items += (int)all;
-  }
-  __syncthreads();
-  // runs of two units at least; each run's first item
-  const int ctas = (int)min((int64_t)a.ctas, (units + 1 + kHead) / (2 + kHead));
-  if (tid == 0) a.plan[0] = units, a.plan[1] = ctas;
-  for (int j = tid; j < items; j += kPlanThreads) {
-    const int64_t b0 = a.items[j].base, b1 = b0 + (int64_t)(a.items[j].nt + kHead) * a.kv.kv_heads;
-    for (int c = (int)((b0 * ctas + units - 1) / units); c < ctas; ++c) {
-      const int64_t u = run_start(units, ctas, c);
-      if (u >= b1) break;
-      if (u >= b0) a.first[c] = j;
-    }
-  }
+  for (int i = threadIdx.x; i < n; i += 256) done[i] = 0;
 }
 
 // ---------------------------------------------------------------- the tensor cores
@@ -170,15 +165,15 @@ constexpr int kSegs = 12;
 struct Bars {
   uint64_t full[8], empty[8], raw[8];
   uint64_t vok[8];  // partly visible values are cleared
-  uint64_t sfull[2], pready[2], odone[2], ofree[2], qfull, qempty, drain;
+  uint64_t sfull[2], pready[2], odone[2], ofree[2], qfull, qraw, qempty, drain;
   uint32_t tmem;
   int abort;
-  // [guard warp][segment % 32]: cleared values that some row sees. A guard is at most four
-  // segments ahead of the MMAs, and these seldom more than one ahead of a query tile's end.
-  uint8_t poison[4][32];
+  Run run;
+  uint8_t poison[4][16];  // [guard warp][segment % 16]: cleared values that some row sees
   // The segments, which the loader works out for all, in a ring that needs no way back: when it comes
   // to segment s + 12, the tiles of s + 6 are done with (a ring of tiles holds four), hence
-  // both query tiles with a segment after s, as those of one query tile come in turn.
+  // both query tiles with a segment after s, as those of one query tile come in turn (so are `poison`,
+  // of 16, and the e4m3 row exponents, of 4, whose writers wait for the segment before).
   uint64_t segready[kSegs];
   Segment segs[kSegs];
 };
@@ -189,7 +184,7 @@ __device__ __forceinline__ bool get_segment(Bars& b, uint32_t i, Segment* s, vol
   if (!warp_wait(&b.segready[i % kSegs], i / kSegs & 1, abort_flag, err)) return false;
   const volatile int4* p = reinterpret_cast<const volatile int4*>(&b.segs[i % kSegs]);
   s->req = p[0].x, s->tok0 = p[0].y, s->p0 = p[0].z, s->lo = p[0].w;
-  s->h = p[1].x, s->t0 = p[1].y, s->t1 = p[1].z, s->bits = p[1].w;
+  s->t0 = p[1].x, s->t1 = p[1].y, s->join = p[1].z, s->bits = p[1].w;
   return s->bits != 0;
 }
 
@@ -212,7 +207,7 @@ __device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p,
       if (!sees(a, p, j)) continue;
       const int page = a.page_table[(int64_t)sg.req * a.table_stride + (j >> psh)];
       if ((unsigned)page >= (unsigned)a.kv.num_pages) continue;
-      const int64_t at = page * a.kv.page_stride + ((int64_t)sg.h * a.kv.page_size + (j & (a.kv.page_size - 1))) * D + d;
+      const int64_t at = page * a.kv.page_stride + ((int64_t)sg.h() * a.kv.page_size + (j & (a.kv.page_size - 1))) * D + d;
       float v;
       if (F8) {
         const uint8_t c = static_cast<const uint8_t*>(a.kv.v)[at];
@@ -224,6 +219,64 @@ __device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p,
     }
   }
   return sum;
+}
+
+// A warp that has written its rows of a part: whether all parts of those rows are there now. (The same
+// rows are the same warp's of a query tile in every CTA.)
+__device__ __forceinline__ bool last_part(const Args& a, const Segment& sg, int i0) {
+  __threadfence();
+  __syncwarp();
+  uint32_t before = 0;
+  if ((threadIdx.x & 31) == 0) before = atomicAdd(&a.done[(sg.join & 0xffff) * (kRows / 32) + i0 / 32], 1u);
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (before + 1 != (uint32_t)(sg.join >> 16)) return false;
+  __threadfence();
+  return true;
+}
+
+// Joins the parts of `rows` rows from row i0 of an item on, in the order of the CTAs, by a warp; 4
+// columns a lane.
+template <int D>
+__device__ __noinline__ void join(const Args& a, const Segment& sg, int i0, int rows) {
+  constexpr int L = D / 4, S = 32 / L, U = 8;  // lanes of a row, rows at a time, of these in flight
+  const int lane = threadIdx.x & 31, c = lane % L * 4;
+  const int c0 = sg.join & 0xffff, parts = sg.join >> 16;
+  for (int r0 = lane / L; r0 < rows; r0 += U * S) {
+    float m[U], l[U], acc[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) m[k] = -INFINITY, l[k] = acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p) {
+      const int64_t at = ((int64_t)(c0 + p) * 2 + (p == 0)) * a.part_rows + i0;
+      float2 ml[U];
+      float4 o[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int r = min(r0 + k * S, rows - 1);
+        ml[k] = __ldcg(a.ml_part + at + r);
+        o[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (at + r) * D + c));
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float top = fmaxf(m[k], ml[k].x), base = top == -INFINITY ? 0.f : top, f = ex2(m[k] - base), g = ex2(ml[k].x - base);
+        m[k] = top;
+        l[k] = l[k] * f + ml[k].y * g;
+        acc[k][0] = acc[k][0] * f + o[k].x * g, acc[k][1] = acc[k][1] * f + o[k].y * g;
+        acc[k][2] = acc[k][2] * f + o[k].z * g, acc[k][3] = acc[k][3] * f + o[k].w * g;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int r = r0 + k * S, i = i0 + r;
+      if (r >= rows) continue;
+      const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+      const int t = row_token(a, i);
+      const int64_t row = (int64_t)(sg.tok0 + t) * a.q_heads + sg.h() * a.group + i - t * a.group;
+      *reinterpret_cast<uint2*>(a.out + row * D + c) =
+          make_uint2(pack2<false>(acc[k][0] * inv, acc[k][1] * inv), pack2<false>(acc[k][2] * inv, acc[k][3] * inv));
+      if (a.lse != nullptr && c == 0) a.lse[row] = m[k] == -INFINITY ? -INFINITY : m[k] * kLn2 + logf(l[k]);
+    }
+  }
 }
 
 // q_many, q_few: boxes of tile_tokens and of few_tokens tokens of q, all heads of a kv head (bf16 caches)
@@ -257,6 +310,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       mbar_init(&b.ofree[i], 4);
     }
     mbar_init(&b.qfull, F8 ? 2 : 1);
+    mbar_init(&b.qraw, 1);
     mbar_init(&b.qempty, 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&b.segready[i], 1);
     mbar_init(&b.drain, 1);
@@ -265,9 +319,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     prefetch_map(&map_k);
     prefetch_map(&map_v);
   }
-  pdl_wait();  // the plan
+  pdl_wait();
   pdl_trigger();
-  __syncthreads();
+  // (the ring is not in use yet)
+  find_run<C::kThreads>(a, *reinterpret_cast<PlanSmem<C::kThreads>*>(smem), &b.run);
   // The issuing warp allocates all 512 columns: the base is column 0, lane 0. The other roles
   // touch TMEM only after its first products.
   constexpr uint32_t tmem = 0;
@@ -291,7 +346,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       // What a score is multiplied by, scale x key scale x the row's power of two, has to be above
       // zero: then the largest score stays the largest, and a masked one -inf. So a sign goes
       // to the scores, and where the factor is 0 (or vanishes in fp32) q is 0 and it is 1.
-      const float ks = F8 ? a.kv.k_scale[sg.h] : 1.f;
+      const float ks = F8 ? a.kv.k_scale[sg.h()] : 1.f;
       const bool negate = (a.scale < 0.f) != (ks < 0.f);
       float mul = 1.f;
       float m = -INFINITY, l = 0.f;
@@ -390,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         fence_after();
         bool poisoned = false;
 #pragma unroll
-        for (int k = 0; k < C::kGuards; ++k) poisoned |= *(volatile uint8_t*)&b.poison[k][all & 31] != 0;
+        for (int k = 0; k < C::kGuards; ++k) poisoned |= *(volatile uint8_t*)&b.poison[k][all & 15] != 0;
         if (poisoned) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -406,8 +461,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         // a thread its row, 32 columns at a time: whole sectors of out or of a part
         const bool whole = sg.whole();
-        const float vs = (F8 ? a.kv.v_scale[sg.h] : 1.f) * (!whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);
-        const int64_t head = (int64_t)(sg.tok0 + tok) * a.q_heads + sg.h * a.group + i - tok * a.group;
+        const float vs = (F8 ? a.kv.v_scale[sg.h()] : 1.f) * (!whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);
+        const int64_t head = (int64_t)(sg.tok0 + tok) * a.q_heads + sg.h() * a.group + i - tok * a.group;
         const int64_t part = ((int64_t)blockIdx.x * 2 + (sg.t0 == 0)) * a.part_rows + i;
         __nv_bfloat16* out = a.out + head * D;
         float* o_part = a.o_part + part * D;
@@ -444,6 +499,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         fence_before();
       }
       warp_arrive(&b.ofree[q]);
+      if (live && !sg.whole() && last_part(a, sg, i - lane)) join<D>(a, sg, i - lane, min(32, rows - (i - lane)));
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
@@ -577,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       uint32_t kv = 0;
       bool ok = true;
       Walk walk;
-      walk.begin(a, blockIdx.x);
+      walk.begin(a, b.run);
       for (uint32_t i = 0; ok; ++i) {
         if (!walk.next(a, &sg)) sg.bits = 0;
         if (lane == 0) {
@@ -612,7 +668,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             __syncwarp();
             uint8_t* dst = F8 ? C::raw(smem, slot) + pb * box * D : smem + slot * C::kTileBytes + hf * (kKeys * 128) + pb * box * 128;
             if (use)
-              tma_load_4d(dst, v ? &map_v : &map_k, &arrive[slot], hf * 64, key & (a.kv.page_size - 1), sg.h, id);
+              tma_load_4d(dst, v ? &map_v : &map_k, &arrive[slot], hf * 64, key & (a.kv.page_size - 1), sg.h(), id);
           }
         }
       }
@@ -634,7 +690,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           mbar_arrive_expect_tx(&b.qfull, (few ? a.few_tokens : a.tile_tokens) * a.group * D * 2);
 #pragma unroll
           for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, &b.qfull, hf * 64, s.h * a.group, s.tok0);
+            tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, &b.qfull, hf * 64, s.h() * a.group, s.tok0);
         }
         __syncwarp();
         ++loads;
@@ -643,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       while (ok) {
         Segment nx;
         bool more = false;
-        if (lane == 0) *(volatile uint8_t*)&b.poison[gw][segs & 31] = 0;
+        if (lane == 0) *(volatile uint8_t*)&b.poison[gw][segs & 15] = 0;
         __syncwarp();
         for (int t = sg.t0; t < sg.t1 && ok; ++t) {
           const int k0 = tile_key<kKeys>(a, sg, t);
@@ -687,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                   *at = make_uint4(w[0], w[1], w[2], w[3]);
                 }
               }
-              if (found) *(volatile uint8_t*)&b.poison[gw][segs & 31] = 1;
+              if (found) *(volatile uint8_t*)&b.poison[gw][segs & 15] = 1;
               fence_async();
               warp_arrive(&b.vok[slot]);
             }
@@ -705,27 +761,34 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
       }
     } else {
-      // ---------------- e4m3: warps 10 and 11 bring q, in fp16 divided by each row's power of two, into
-      // the K-major layout with the 128-byte swizzle. Rows beyond the item's stay what they were.
-      constexpr int LPR = D / 8, N = 8, kStep = 64 / LPR;  // threads of a row, loads in flight, rows at a time
+      // ---------------- e4m3: warp 10 loads q as for a bf16 cache; 10 and 11 turn it in place into fp16
+      // divided by each row's power of two. Rows beyond the item's stay what they were.
+      constexpr int LPR = D / 8, N = 8, kStep = 64 / LPR;  // threads of a row, chunks at once, rows at a time
       const int tid = threadIdx.x - 10 * 32, c = tid % LPR;
-      uint32_t segs = 0;
+      uint32_t segs = 0, loads = 0;
       for (; get_segment(b, segs, &sg, abort_flag, a.err); ++segs) {
         const int rows = sg.ntok() * a.group;
-        const float ks = a.kv.k_scale[sg.h];
+        const float ks = a.kv.k_scale[sg.h()];
+        if (segs > 0 && !warp_wait(&b.qempty, (segs - 1) & 1, abort_flag, a.err)) break;
+        if (warp == 10) {
+          if (lane == 0) {
+            const bool few = sg.ntok() <= a.few_tokens;
+            mbar_arrive_expect_tx(&b.qraw, (few ? a.few_tokens : a.tile_tokens) * a.group * D * 2);
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, &b.qraw, hf * 64, sg.h() * a.group, sg.tok0);
+          }
+          ++loads;
+          __syncwarp();
+        }
+        if (!warp_wait(&b.qraw, segs & 1, abort_flag, a.err)) break;
         for (int r0 = tid / LPR; r0 - tid / LPR < rows; r0 += N * kStep) {
           uint4 v[N];
 #pragma unroll
           for (int p = 0; p < N; ++p) {
-            const int i = r0 + p * kStep;
-            v[p] = make_uint4(0, 0, 0, 0);
-            if (i < rows) {
-              const int t = row_token(a, i);
-              v[p] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(sg.tok0 + t) * a.q_stride +
-                                                          (sg.h * a.group + i - t * a.group) * D + c * 8));
-            }
+            const int r = min(r0 + p * kStep, kRows - 1);
+            v[p] = *reinterpret_cast<const uint4*>(qs + (c / 8) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
           }
-          if (r0 < kStep && segs > 0 && !warp_wait(&b.qempty, (segs - 1) & 1, abort_flag, a.err)) break;
 #pragma unroll
           for (int p = 0; p < N; ++p) {
             const int r = r0 + p * kStep;
@@ -748,9 +811,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
           }
         }
-        if (__any_sync(0xffffffffu, *abort_flag)) break;
         fence_async();
         warp_arrive(&b.qfull);
+      }
+      // q's copy in flight lands before the CTA leaves
+      if (loads > 0) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&b.qraw, (loads - 1) & 1) && clock64() - t0 < kWaitLimit) {
+        }
       }
     }
   } else if constexpr (F8) {
@@ -762,7 +830,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     uint32_t kv = 0, segs = 0;
     bool ok = true;
     for (; ok && get_segment(b, segs, &sg, abort_flag, a.err); ++segs) {
-      if (lane == 0) *(volatile uint8_t*)&b.poison[warp - 12][segs & 31] = 0;
+      if (lane == 0) *(volatile uint8_t*)&b.poison[warp - 12][segs & 15] = 0;
       __syncwarp();
       for (int i2 = 2 * sg.t0; i2 < 2 * sg.t1; ++i2, ++kv) {  // K and V of each tile
         const uint32_t slot = kv % kSlots;
@@ -796,7 +864,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (found) *(volatile uint8_t*)&b.poison[warp - 12][segs & 31] = 1;
+          if (found) *(volatile uint8_t*)&b.poison[warp - 12][segs & 15] = 1;
         }
         __syncwarp();
 #pragma unroll
@@ -826,55 +894,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   fence_after();
   if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
-}
-
-// ---------------------------------------------------------------- the join
-
-// Block (c, y): rows 8 y .. 8 y + 7 of the item that the boundary before CTA c cuts, a warp a row,
-// if that is the first boundary inside it. The parts are added in the order of the CTAs.
-template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const Args a) {
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
-  const int64_t units = a.plan[0];
-  const int ctas = (int)a.plan[1];
-  if (c >= ctas) return;
-  const Item it = a.items[a.first[c]];
-  const int64_t u = run_start(units, ctas, c), in = u - it.base;
-  const int h = (int)(in / (it.nt + kHead));
-  const int64_t g0 = it.base + (int64_t)h * (it.nt + kHead) + kHead, g1 = g0 + it.nt;  // its tiles
-  if (u <= g0 || run_start(units, ctas, c - 1) > g0) return;
-  const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (i >= it.ntok * a.group) return;
-  int n = 1;  // parts: CTA c - 1's slot 1, then slots 0
-  while (run_start(units, ctas, c + n - 1) < g1 && c + n - 1 < ctas) ++n;
-  auto at = [&](int p) { return ((int64_t)(c - 1 + p) * 2 + (p == 0)) * a.part_rows + i; };
-  float m = -INFINITY;
-  for (int p = lane; p < n; p += 32) m = fmaxf(m, a.ml_part[at(p)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float top = m == -INFINITY ? 0.f : m;
-  constexpr int V = D / 32;
-  float l = 0.f, acc[V];
-#pragma unroll
-  for (int d = 0; d < V; ++d) acc[d] = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < n; ++p) {
-    const float2 ml = a.ml_part[at(p)];
-    const float f = ex2(ml.x - top);
-    const float* src = a.o_part + at(p) * D + lane * V;
-    l = fmaf(ml.y, f, l);
-#pragma unroll
-    for (int d = 0; d < V; ++d) acc[d] = fmaf(src[d], f, acc[d]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int t = row_token(a, i);
-  const int64_t row = (int64_t)(it.tok0 + t) * a.q_heads + h * a.group + i - t * a.group;
-#pragma unroll
-  for (int d = 0; d < V; d += 2)
-    *reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * V + d) = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
-  if (a.lse != nullptr && lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // ---------------------------------------------------------------- host side
@@ -917,23 +936,13 @@ int launch_all(const Args& a, cudaStream_t s) {
   if (r == PMOE_OK) r = make_q_map(a, a.tile_tokens, &many);
   if (r == PMOE_OK) r = make_q_map(a, a.few_tokens, &few);
   if (r == PMOE_OK) r = limit.set(reinterpret_cast<const void*>(chunk_kernel<D, F8>), C::kSmem, what);
-  if (r == PMOE_OK) r = launch(what, plan_kernel, 1, kPlanThreads, 0, s, true, 1, a);
+  if (r == PMOE_OK) r = launch(what, clear_kernel, 1, 256, 0, s, true, 1, a.done, kRows / 32 * a.ctas);
   if (r == PMOE_OK) r = launch(what, chunk_kernel<D, F8>, a.ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, many, few, a);
-  if (r != PMOE_OK || a.ctas == 1) return r;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(a.ctas - 1, (a.part_rows + 7) / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D>, a), what);
+  return r;
 }
 
 struct Layout {
-  size_t first, items, o, ml, bytes;
+  size_t ml, done, bytes;
 };
 
 // Fills what follows from the sizes alone.
@@ -956,12 +965,9 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int R, Args* a, Layout* l) 
   a->few_tokens = std::max(1, 16 / a->group);
   a->part_rows = std::min(kRows, T * a->group);
   const size_t parts = (size_t)a->ctas * 2 * a->part_rows;
-  auto up = [](size_t n) { return (n + 15) / 16 * 16; };
-  l->first = 16;
-  l->items = up(l->first + (size_t)a->ctas * 4);
-  l->o = l->items + (size_t)(T / a->tile_tokens + std::min(R, T)) * sizeof(Item);  // a request's last tile may be short
-  l->ml = l->o + parts * kv->head_dim * 4;
-  l->bytes = up(l->ml + parts * 8);
+  l->ml = parts * kv->head_dim * 4;
+  l->done = l->ml + parts * 8;
+  l->bytes = l->done + (size_t)a->ctas * (kRows / 32) * 4;
   return PMOE_OK;
 }
 
@@ -1012,11 +1018,9 @@ extern "C" int moe_chunk_attention(const pmoe_kv_desc* kv, const void* q, int64_
   a.lse = lse;
   a.err = err_out;
   uint8_t* base = static_cast<uint8_t*>(scratch);
-  a.plan = reinterpret_cast<int64_t*>(base);
-  a.first = reinterpret_cast<int32_t*>(base + lay.first);
-  a.items = reinterpret_cast<chunk::Item*>(base + lay.items);
-  a.o_part = reinterpret_cast<float*>(base + lay.o);
+  a.o_part = reinterpret_cast<float*>(base);
   a.ml_part = reinterpret_cast<float2*>(base + lay.ml);
+  a.done = reinterpret_cast<uint32_t*>(base + lay.done);
   cudaStream_t s = (cudaStream_t)stream;
   const bool f8 = kv->dtype == PMOE_KV_E4M3;
   if (kv->head_dim == 128) return f8 ? chunk::launch_all<128, true>(a, s) : chunk::launch_all<128, false>(a, s);
