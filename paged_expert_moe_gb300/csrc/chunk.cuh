@@ -26,13 +26,13 @@ struct Args {
   __nv_bfloat16* out;
   float* lse;
   int32_t* err;
-  int ctas, tile_tokens, few_tokens, part_rows;
+  int ctas, tile_tokens, few_tokens, part_rows, few;
   // scratch
   // Parts of items that a CTA does not take whole: slot 0 where it continues one, slot 1 where it
   // begins one. o: sum of weights x values, ml: (base of the weights' exponents, sum of weights).
   float* o_part;    // [ctas][2][part_rows][head_dim]
   float2* ml_part;  // [ctas][2][part_rows]
-  uint32_t* done;   // [ctas][8] parts written of the item that begins in a CTA and ends in another, by 32 rows
+  uint32_t* done;   // [ctas][2] parts written of the item that begins in a CTA and ends in another, by query tile
 };
 
 // Visible keys of a row at position p: j <= p, and with a window j > p - window or j < sinks.
@@ -51,7 +51,11 @@ __device__ __forceinline__ bool all_see_tile(const Args& a, int p0, int p1, int 
   return k0 + n - 1 <= p0 && (a.window == 0 || k0 > p1 - a.window || k0 + n <= a.sinks);
 }
 
-__device__ __forceinline__ int64_t run_start(int64_t units, int ctas, int c) { return units * c / ctas; }
+// The first unit of CTA c's run. (A 64-bit division takes some 500 cycles, one of 32 bits a tenth.)
+__device__ __forceinline__ int64_t run_start(int64_t units, int ctas, int c) {
+  const int64_t x = units * c;
+  return x >> 32 ? x / ctas : (int64_t)((uint32_t)x / (uint32_t)ctas);
+}
 
 // r / group for r < 2^24 and group <= 64
 __device__ __forceinline__ int row_token(const Args& a, int r) {
@@ -59,7 +63,10 @@ __device__ __forceinline__ int row_token(const Args& a, int r) {
 }
 
 // The CTA that takes unit u: the largest c with run_start(c) <= u.
-__device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) { return (int)(((u + 1) * ctas - 1) / units); }
+__device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) {
+  const int64_t x = (u + 1) * ctas - 1;  // (of at least units)
+  return x >> 32 ? (int)(x / units) : (int)((uint32_t)x / (uint32_t)units);
+}
 
 // A request's rows of this step.
 struct Request {
@@ -116,22 +123,23 @@ __device__ __forceinline__ int tile_key(const Args& a, const Segment& s, int t) 
 // Where a CTA's run of units begins. An item has kHead + its key tiles units a kv head, items come
 // request by request.
 struct Run {
-  int64_t units, left, u, before;  // all units, the run's, its first one's; rows of the requests ahead
+  int64_t units, left, u, before;  // all units, the run's, its first one's; rows of the requests up to its first
   int ctas, req, tile, h, at;      // request, tile of its rows, kv head, unit of the item
+  int start, n, len;               // of the request
 };
 
-// A CTA's segments in order, by a whole warp: lane i holds request `batch` + i.
+// A CTA's segments in order, by a whole warp.
 struct Walk {
   Run run;
   int64_t first;  // unit of the item's first tile, for this head
-  int batch, k, lane, p0, ntok, tok0, nt, lo;
+  int lane, p0, ntok, tok0, nt, lo;
+  int batch;      // the requests from this one on, one a lane, once the first request is through
   Request mine;
-  uint32_t some;  // lanes whose requests have rows
+  uint32_t some;  // lanes whose requests have rows and are still to come
 
-  __device__ __forceinline__ void load(const Args& a, int from) {
+  __device__ __forceinline__ void load(const Args& a) {
     const int l = threadIdx.x & 31;
-    batch = from;
-    mine = request(a, from + l);
+    mine = request(a, batch + l);
     int64_t upto = mine.n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -143,25 +151,40 @@ struct Walk {
     some = __ballot_sync(0xffffffffu, mine.n > 0);
   }
   __device__ __forceinline__ void item(const Args& a) {
-    const int start = __shfl_sync(0xffffffffu, mine.start, k), n = __shfl_sync(0xffffffffu, mine.n, k),
-              len = __shfl_sync(0xffffffffu, mine.len, k), i0 = run.tile * a.tile_tokens;
-    tok0 = start + i0;
-    ntok = min(a.tile_tokens, n - i0);
-    p0 = len - n + i0;
+    const int i0 = run.tile * a.tile_tokens;
+    tok0 = run.start + i0;
+    ntok = min(a.tile_tokens, run.n - i0);
+    p0 = run.len - run.n + i0;
     nt = key_tiles(a, p0, ntok, &lo);
+  }
+  // The next request with rows; false: there is none.
+  __device__ __forceinline__ bool request_after(const Args& a) {
+    while (some == 0) {
+      if (batch + 32 >= a.R) return false;
+      batch += 32;
+      load(a);
+    }
+    const int k = __ffs(some) - 1;
+    some &= some - 1;
+    run.req = batch + k;
+    run.start = __shfl_sync(0xffffffffu, mine.start, k);
+    run.n = __shfl_sync(0xffffffffu, mine.n, k);
+    run.len = __shfl_sync(0xffffffffu, mine.len, k);
+    return true;
   }
   __device__ __forceinline__ void begin(const Args& a, const Run& r) {
     run = r;
     if (run.left <= 0) return;
-    load(a, run.req);
-    k = 0, lane = 1;
+    lane = 1;
+    batch = run.req + 1 - 32;
+    some = 0;
     item(a);
     first = run.u - run.at + kHead;
   }
   __device__ __forceinline__ bool next(const Args& a, Segment* s) {
     while (run.left > 0) {
       const int n = nt + kHead, to = (int)min((int64_t)n, run.at + run.left);
-      s->req = batch + k, s->tok0 = tok0, s->p0 = p0, s->lo = lo;
+      s->req = run.req, s->tok0 = tok0, s->p0 = p0, s->lo = lo;
       s->t0 = max(run.at - kHead, 0);
       s->t1 = max(to - kHead, 0);
       const bool two = ntok * a.group > 128, whole = s->t0 == 0 && s->t1 == nt;
@@ -180,15 +203,10 @@ struct Walk {
         if (++run.h == a.kv.kv_heads) {
           run.h = 0;
           ++run.tile;
-          if (run.tile * a.tile_tokens >= __shfl_sync(0xffffffffu, mine.n, k)) {
+          if (run.tile * a.tile_tokens >= run.n) {
             run.tile = 0;
-            uint32_t rest = k < 31 ? some >> (k + 1) << (k + 1) : 0;
-            while (rest == 0 && batch + 32 < a.R) load(a, batch + 32), rest = some;
-            if (rest == 0) {  // (some units are left, so some request has rows; if its numbers are still the same)
-              run.left = 0;
-              return s->t1 > s->t0;
-            }
-            k = __ffs(rest) - 1;
+            // (some units are left, so some request has rows; if its numbers are still the same)
+            if (!request_after(a)) run.left = 0;
           }
           item(a);
         }

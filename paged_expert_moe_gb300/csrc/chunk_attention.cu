@@ -59,9 +59,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t
 
 template <int NT>
 struct PlanSmem {
-  int64_t warps[32], rows[NT];  // rows of the requests ahead
+  int64_t warps[32], rows[NT];  // rows of the requests up to each
   int upto[NT + 1];             // tiles before each request of the turn
-  int n[NT], len[NT];
+  int start[NT], n[NT], len[NT];
 };
 
 // The start of this CTA's run, by all NT threads: the units of all items are added up, NT requests and NT
@@ -79,12 +79,13 @@ __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
       Request q = request(a, r0 + tid);
       // starts that go back may name more rows than there are
       int64_t some, all;
-      const int64_t before = rows + block_scan<NT>(q.n, m.warps, &some);
+      const int n = q.n;
+      const int64_t before = rows + block_scan<NT>(n, m.warps, &some);
       if (before + q.n > a.T) q.bad = true, q.n = 0;
       if (q.bad && pass == 0 && blockIdx.x == 0 && a.err != nullptr) atomicOr(a.err, kErrBadLength);
       rows += some;
       m.upto[tid] = (int)block_scan<NT>((q.n + a.tile_tokens - 1) / a.tile_tokens, m.warps, &all);
-      m.n[tid] = q.n, m.len[tid] = q.len, m.rows[tid] = before;
+      m.start[tid] = q.start, m.n[tid] = q.n, m.len[tid] = q.len, m.rows[tid] = before + n;
       if (tid == 0) m.upto[NT] = (int)all;
       __syncthreads();
       for (int j0 = 0; j0 < all; j0 += NT) {
@@ -113,9 +114,10 @@ __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
           ctas = (int)min((int64_t)a.ctas, (units + kHead + 1) / (kHead + 2));
           const int64_t u = run_start(units, ctas, blockIdx.x), in = u - base;
           if ((int)blockIdx.x < ctas && in >= 0 && in < (int64_t)len * a.kv.kv_heads) {
-            run->units = units, run->left = run_start(units, ctas, blockIdx.x + 1) - u, run->u = u, run->before = m.rows[lo];
-            run->ctas = ctas, run->req = r0 + lo, run->tile = i;
-            run->h = (int)(in / len), run->at = (int)(in - in / len * len);
+            const int h = in >> 32 ? (int)(in / len) : (int)((uint32_t)in / (uint32_t)len);
+            run->units = units, run->left = run_start(units, ctas, blockIdx.x + 1) - u, run->u = u;
+            run->ctas = ctas, run->req = r0 + lo, run->tile = i, run->h = h, run->at = (int)(in - (int64_t)h * len);
+            run->start = m.start[lo], run->n = m.n[lo], run->len = m.len[lo], run->before = m.rows[lo];
           }
         }
         if (single) pass = 2;
@@ -126,6 +128,57 @@ __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
   }
   fence_async();  // what this wrote, TMA will write again
   __syncthreads();
+}
+
+// The same by one warp, where neither requests nor items can be more than 32.
+__device__ __forceinline__ void find_run_of_few(const Args& a, Run* run) {
+  const int lane = threadIdx.x & 31;
+  auto scan = [&](int v) {  // up to and with each lane
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  Request q = request(a, lane);
+  const int rows = scan(q.n);  // (below 32 x 2^24)
+  if (rows > a.T) q.bad = true, q.n = 0;
+  if (q.bad && blockIdx.x == 0 && a.err != nullptr) atomicOr(a.err, kErrBadLength);
+  const int tiles = (q.n + a.tile_tokens - 1) / a.tile_tokens, upto = scan(tiles);
+  // lane j: item j, of the request r with upto[r] - tiles[r] <= j < upto[r]
+  int r = 0;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) r += __shfl_sync(0xffffffffu, upto, k) <= lane;
+  r = min(r, 31);
+  const int i = lane - __shfl_sync(0xffffffffu, upto - tiles, r), start = __shfl_sync(0xffffffffu, q.start, r),
+            n = __shfl_sync(0xffffffffu, q.n, r), len = __shfl_sync(0xffffffffu, q.len, r), before = __shfl_sync(0xffffffffu, rows, r);
+  int span = 0;
+  if (lane < __shfl_sync(0xffffffffu, upto, 31)) {
+    int lo;
+    span = kHead + key_tiles(a, len - n + i * a.tile_tokens, min(a.tile_tokens, n - i * a.tile_tokens), &lo);
+  }
+  int64_t end = (int64_t)span * a.kv.kv_heads;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += y;
+  }
+  const int64_t units = __shfl_sync(0xffffffffu, end, 31);
+  const int ctas = (int)min((int64_t)a.ctas, (units + kHead + 1) / (kHead + 2));
+  int64_t u = 0, left = 0;
+  if ((int)blockIdx.x < ctas) u = run_start(units, ctas, blockIdx.x), left = run_start(units, ctas, blockIdx.x + 1) - u;
+  const int64_t in = u - (end - (int64_t)span * a.kv.kv_heads);
+  const uint32_t has = __ballot_sync(0xffffffffu, left > 0 && in >= 0 && u < end);
+  run->left = has != 0 ? left : 0;
+  if (has == 0) return;
+  const int k = __ffs(has) - 1, n_units = __shfl_sync(0xffffffffu, span, k);
+  const int64_t at = __shfl_sync(0xffffffffu, in, k);
+  const int h = at >> 32 ? (int)(at / n_units) : (int)((uint32_t)at / (uint32_t)n_units);
+  run->units = units, run->u = u, run->ctas = ctas, run->h = h, run->at = (int)(at - (int64_t)h * n_units);
+  run->req = __shfl_sync(0xffffffffu, r, k), run->tile = __shfl_sync(0xffffffffu, i, k);
+  run->start = __shfl_sync(0xffffffffu, start, k), run->n = __shfl_sync(0xffffffffu, n, k);
+  run->len = __shfl_sync(0xffffffffu, len, k), run->before = __shfl_sync(0xffffffffu, before, k);
 }
 
 // Clears the counts of an item's parts.
@@ -165,9 +218,10 @@ constexpr int kSegs = 12;
 struct Bars {
   uint64_t full[8], empty[8], raw[8];
   uint64_t vok[8];  // partly visible values are cleared
-  uint64_t sfull[2], pready[2], odone[2], ofree[2], qfull, qraw, qempty, drain;
+  uint64_t sfull[2], pready[2], odone[2], ofree[2], joined[2], qfull, qraw, qempty, drain;
   uint32_t tmem;
   int abort;
+  int last[2];  // whether a query tile's last part was the item's
   Run run;
   uint8_t poison[4][16];  // [guard warp][segment % 16]: cleared values that some row sees
   // The segments, which the loader works out for all, in a ring that needs no way back: when it comes
@@ -221,60 +275,93 @@ __device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p,
   return sum;
 }
 
-// A warp that has written its rows of a part: whether all parts of those rows are there now. (The same
-// rows are the same warp's of a query tile in every CTA.)
-__device__ __forceinline__ bool last_part(const Args& a, const Segment& sg, int i0) {
-  __threadfence();
-  __syncwarp();
-  uint32_t before = 0;
-  if ((threadIdx.x & 31) == 0) before = atomicAdd(&a.done[(sg.join & 0xffff) * (kRows / 32) + i0 / 32], 1u);
-  before = __shfl_sync(0xffffffffu, before, 0);
-  if (before + 1 != (uint32_t)(sg.join >> 16)) return false;
-  __threadfence();
-  return true;
-}
+// log of a sum of weights to base m of their exponents, in units of log 2
+__device__ __forceinline__ float lse_of(float m, float l) { return m == -INFINITY ? -INFINITY : (m + __log2f(l)) * kLn2; }
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }
 
-// Joins the parts of `rows` rows from row i0 of an item on, in the order of the CTAs, by a warp; 4
-// columns a lane.
-template <int D>
-__device__ __noinline__ void join(const Args& a, const Segment& sg, int i0, int rows) {
-  constexpr int L = D / 4, S = 32 / L, U = 8;  // lanes of a row, rows at a time, of these in flight
+// The parts of rows i0 + r0, i0 + r0 + step, .. (U of them, below `rows`) of an item, added in the order of the
+// CTAs by a warp; 4 columns a lane, P parts at a time. Little code: it runs once in a while, and what is not in
+// the instruction cache costs more than what it does.
+template <int D, int U, int P>
+__device__ __forceinline__ void join_rows(const Args& a, const Segment& sg, int i0, int rows, int r0, int step) {
+  constexpr int L = D / 4;  // lanes of a row; 32 / L rows of the U are a lane's
   const int lane = threadIdx.x & 31, c = lane % L * 4;
   const int c0 = sg.join & 0xffff, parts = sg.join >> 16;
-  for (int r0 = lane / L; r0 < rows; r0 += U * S) {
-    float m[U], l[U], acc[U][4];
+  float m[U], l[U], acc[U][4];
 #pragma unroll
-    for (int k = 0; k < U; ++k) m[k] = -INFINITY, l[k] = acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-#pragma unroll 2
-    for (int p = 0; p < parts; ++p) {
-      const int64_t at = ((int64_t)(c0 + p) * 2 + (p == 0)) * a.part_rows + i0;
-      float2 ml[U];
-      float4 o[U];
+  for (int k = 0; k < U; ++k) m[k] = -INFINITY, l[k] = acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+  for (int p0 = 0; p0 < parts; p0 += P) {
+    float2 ml[P][U];
+    float4 o[P][U];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int r = min(r0 + k * S, rows - 1);
-        ml[k] = __ldcg(a.ml_part + at + r);
-        o[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (at + r) * D + c));
-      }
+    for (int p = 0; p < P; ++p) {
+      const int pp = min(p0 + p, parts - 1);
+      const int64_t at = ((int64_t)(c0 + pp) * 2 + (pp == 0)) * a.part_rows + i0;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const float top = fmaxf(m[k], ml[k].x), base = top == -INFINITY ? 0.f : top, f = ex2(m[k] - base), g = ex2(ml[k].x - base);
-        m[k] = top;
-        l[k] = l[k] * f + ml[k].y * g;
-        acc[k][0] = acc[k][0] * f + o[k].x * g, acc[k][1] = acc[k][1] * f + o[k].y * g;
-        acc[k][2] = acc[k][2] * f + o[k].z * g, acc[k][3] = acc[k][3] * f + o[k].w * g;
+        const int r = min(r0 + k * step, rows - 1);
+        ml[p][k] = __ldcg(a.ml_part + at + r);
+        if (p0 + p >= parts) ml[p][k] = make_float2(-INFINITY, 0.f);
+        o[p][k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (at + r) * D + c));
       }
     }
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int r = r0 + k * S, i = i0 + r;
-      if (r >= rows) continue;
-      const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
-      const int t = row_token(a, i);
-      const int64_t row = (int64_t)(sg.tok0 + t) * a.q_heads + sg.h() * a.group + i - t * a.group;
-      *reinterpret_cast<uint2*>(a.out + row * D + c) =
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float top = fmaxf(m[k], ml[p][k].x), base = top == -INFINITY ? 0.f : top, f = ex2(m[k] - base),
+                    g = ex2(ml[p][k].x - base);
+        m[k] = top;
+        l[k] = fmaf(l[k], f, ml[p][k].y * g);
+        const float v[4] = {o[p][k].x, o[p][k].y, o[p][k].z, o[p][k].w};
+        // (a part that is none is another one again, times 0: it may hold infinities)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[k][d] = p0 + p < parts ? fmaf(acc[k][d], f, v[d] * g) : acc[k][d];
+      }
+  }
+  const uint32_t row0 = (uint32_t)sg.tok0 * a.q_heads + sg.h() * a.group;
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int r = r0 + k * step, i = i0 + r;
+    const uint32_t row = row0 + i + row_token(a, i) * (a.q_heads - a.group);
+    const float inv = inverse(l[k]);
+    if (r < rows) {
+      *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + c) =
           make_uint2(pack2<false>(acc[k][0] * inv, acc[k][1] * inv), pack2<false>(acc[k][2] * inv, acc[k][3] * inv));
-      if (a.lse != nullptr && c == 0) a.lse[row] = m[k] == -INFINITY ? -INFINITY : m[k] * kLn2 + logf(l[k]);
+      if (a.lse != nullptr && c == 0) a.lse[row] = lse_of(m[k], l[k]);
+    }
+  }
+}
+// `rows` rows from i0 on by the four warps of a query tile, w this one.
+template <int D>
+__device__ __noinline__ void join(const Args& a, const Segment& sg, int i0, int rows, int w) {
+  constexpr int S = 128 / D;  // rows at a time
+  const int first = (threadIdx.x & 31) / (D / 4);
+  if (rows <= 8) {
+    join_rows<D, 2 / S, 8>(a, sg, i0, rows, w * 2 + first, S);
+  } else {
+    for (int r0 = w * 8; r0 < rows; r0 += 32) join_rows<D, 8 / S, 2>(a, sg, i0, rows, r0 + first, S);
+  }
+}
+
+// 4 x 4 units of 32 bytes turned over among four lanes: lane j of the four leaves with unit j of each.
+__device__ __forceinline__ void turn_units(uint32_t (&r)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (u & bit) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t give = up ? r[u * 8 + k] : r[(u + bit) * 8 + k];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, bit);
+        if (up)
+          r[u * 8 + k] = got;
+        else
+          r[(u + bit) * 8 + k] = got;
+      }
     }
   }
 }
@@ -308,6 +395,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       mbar_init(&b.pready[i], 4);
       mbar_init(&b.odone[i], 1);
       mbar_init(&b.ofree[i], 4);
+      mbar_init(&b.joined[i], 4);
     }
     mbar_init(&b.qfull, F8 ? 2 : 1);
     mbar_init(&b.qraw, 1);
@@ -318,11 +406,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_map(&map_k);
     prefetch_map(&map_v);
+    prefetch_map(&q_few);
+    prefetch_map(&q_many);
   }
   pdl_wait();
   pdl_trigger();
   // (the ring is not in use yet)
-  find_run<C::kThreads>(a, *reinterpret_cast<PlanSmem<C::kThreads>*>(smem), &b.run);
+  if (a.few)
+    __syncthreads();
+  else
+    find_run<C::kThreads>(a, *reinterpret_cast<PlanSmem<C::kThreads>*>(smem), &b.run);
   // The issuing warp allocates all 512 columns: the base is column 0, lane 0. The other roles
   // touch TMEM only after its first products.
   constexpr uint32_t tmem = 0;
@@ -459,47 +552,74 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             tmem_wait_st();
           }
         }
-        // a thread its row, 32 columns at a time: whole sectors of out or of a part
+        // 128 bytes of each row at a time, turned over among four lanes, so that a store covers half of each
+        // of 8 lines (a row a lane covers 16 bytes of 32 lines: 5,000 cycles for an item, 1,900 so)
         const bool whole = sg.whole();
-        const float vs = (F8 ? a.kv.v_scale[sg.h()] : 1.f) * (!whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l);
-        const int64_t head = (int64_t)(sg.tok0 + tok) * a.q_heads + sg.h() * a.group + i - tok * a.group;
-        const int64_t part = ((int64_t)blockIdx.x * 2 + (sg.t0 == 0)) * a.part_rows + i;
-        __nv_bfloat16* out = a.out + head * D;
-        float* o_part = a.o_part + part * D;
+        const float vs = (F8 ? a.kv.v_scale[sg.h()] : 1.f) * (whole ? inverse(l) : 1.f);
+        const uint32_t head = (uint32_t)(sg.tok0 + tok) * a.q_heads + sg.h() * a.group + i - tok * a.group;
+        const uint32_t part = (blockIdx.x * 2 + (sg.t0 == 0)) * a.part_rows + i;
+        uint8_t* dst[4];  // of rows (lane & ~3) + k, from this lane's unit on
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t of = __shfl_sync(0xffffffffu, whole ? head : part, (lane & ~3) + k);
+          dst[k] = (whole ? reinterpret_cast<uint8_t*>(a.out + (int64_t)of * D) : reinterpret_cast<uint8_t*>(a.o_part + (int64_t)of * D)) +
+                   (lane & 3) * 32;
+        }
+        const int mine = rows - (i - lane) - (lane & ~3);  // rows of the four that are there
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D; c += whole ? 64 : 32) {
           uint32_t o[32];
           tmem_ld32(to + c, o);
           tmem_wait_ld();
-          if (i < rows) {
-            if (whole) {
+          if (whole) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                uint32_t w[4];
+            for (int k = 0; k < 16; ++k) o[k] = pack2<false>(__uint_as_float(o[2 * k]) * vs, __uint_as_float(o[2 * k + 1]) * vs);
+            uint32_t o2[32];
+            tmem_ld32(to + c + 32, o2);
+            tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  w[j] = pack2<false>(__uint_as_float(o[k + 2 * j]) * vs, __uint_as_float(o[k + 2 * j + 1]) * vs);
-                *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            } else {
+            for (int k = 0; k < 16; ++k)
+              o[16 + k] = pack2<false>(__uint_as_float(o2[2 * k]) * vs, __uint_as_float(o2[2 * k + 1]) * vs);
+          } else {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(o_part + c + k) =
-                    make_float4(__uint_as_float(o[k]) * vs, __uint_as_float(o[k + 1]) * vs, __uint_as_float(o[k + 2]) * vs,
-                                __uint_as_float(o[k + 3]) * vs);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * vs);
+          }
+          turn_units(o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k < mine) {
+              reinterpret_cast<uint4*>(dst[k])[0] = make_uint4(o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3]);
+              reinterpret_cast<uint4*>(dst[k])[1] = make_uint4(o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]);
             }
+            dst[k] += 128;
           }
         }
         if (i < rows) {
           if (!whole)
             a.ml_part[part] = make_float2(m, l);
           else if (a.lse != nullptr)
-            a.lse[head] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+            a.lse[head] = lse_of(m, l);
         }
         fence_before();
       }
       warp_arrive(&b.ofree[q]);
-      if (live && !sg.whole() && last_part(a, sg, i - lane)) join<D>(a, sg, i - lane, min(32, rows - (i - lane)));
+      if (!sg.whole()) {
+        // the query tile's four warps, the ones without rows too, and one of them counts the part
+        __threadfence();
+        warp_arrive(&b.joined[q]);
+        if (!warp_wait(&b.joined[q], 0, abort_flag, a.err)) break;
+        if ((warp & 3) == 0 && lane == 0) {
+          const int half = sg.two() ? q : 0;
+          *(volatile int*)&b.last[q] = atomicAdd(&a.done[(sg.join & 0xffff) * 2 + half], 1u) + 1 == (uint32_t)(sg.join >> 16);
+        }
+        warp_arrive(&b.joined[q]);
+        if (!warp_wait(&b.joined[q], 1, abort_flag, a.err)) break;
+        if (*(volatile int*)&b.last[q]) {
+          __threadfence();
+          const int i0 = i - row;
+          join<D>(a, sg, i0, min(128, rows - i0), warp & 3);
+        }
+      }
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
@@ -633,7 +753,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       uint32_t kv = 0;
       bool ok = true;
       Walk walk;
-      walk.begin(a, b.run);
+      if (a.few) {
+        Run run;
+        find_run_of_few(a, &run);
+        walk.begin(a, run);
+      } else {
+        walk.begin(a, b.run);
+      }
       for (uint32_t i = 0; ok; ++i) {
         if (!walk.next(a, &sg)) sg.bits = 0;
         if (lane == 0) {
@@ -936,7 +1062,7 @@ int launch_all(const Args& a, cudaStream_t s) {
   if (r == PMOE_OK) r = make_q_map(a, a.tile_tokens, &many);
   if (r == PMOE_OK) r = make_q_map(a, a.few_tokens, &few);
   if (r == PMOE_OK) r = limit.set(reinterpret_cast<const void*>(chunk_kernel<D, F8>), C::kSmem, what);
-  if (r == PMOE_OK) r = launch(what, clear_kernel, 1, 256, 0, s, true, 1, a.done, kRows / 32 * a.ctas);
+  if (r == PMOE_OK) r = launch(what, clear_kernel, 1, 256, 0, s, true, 1, a.done, 2 * a.ctas);
   if (r == PMOE_OK) r = launch(what, chunk_kernel<D, F8>, a.ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, many, few, a);
   return r;
 }
@@ -963,11 +1089,12 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int R, Args* a, Layout* l) 
   if (a->ctas == 0) return PMOE_ECUDA;
   a->tile_tokens = kRows / a->group;
   a->few_tokens = std::max(1, 16 / a->group);
+  a->few = R <= 32 && T / a->tile_tokens + std::min(R, T) <= 32;
   a->part_rows = std::min(kRows, T * a->group);
   const size_t parts = (size_t)a->ctas * 2 * a->part_rows;
   l->ml = parts * kv->head_dim * 4;
   l->done = l->ml + parts * 8;
-  l->bytes = l->done + (size_t)a->ctas * (kRows / 32) * 4;
+  l->bytes = l->done + (size_t)a->ctas * 8;
   return PMOE_OK;
 }
 
