@@ -46,11 +46,6 @@ __device__ __forceinline__ bool any_sees(const Args& a, int p0, int p1, int j) {
 __device__ __forceinline__ bool all_see(const Args& a, int p0, int p1, int j) {
   return j <= p0 && (a.window == 0 || j > p1 - a.window || j < a.sinks);
 }
-// whether all see the n keys from k0 on
-__device__ __forceinline__ bool all_see_tile(const Args& a, int p0, int p1, int k0, int n) {
-  return k0 + n - 1 <= p0 && (a.window == 0 || k0 > p1 - a.window || k0 + n <= a.sinks);
-}
-
 // The first unit of CTA c's run. (A 64-bit division takes some 500 cycles, one of 32 bits a tenth.)
 __device__ __forceinline__ int64_t run_start(int64_t units, int ctas, int c) {
   const int64_t x = units * c;
@@ -105,6 +100,8 @@ struct __align__(16) Segment {
   int32_t t0, t1;
   int32_t join;  // of a part: the CTA with the item's first tile, and from bit 16 on the number of parts
   int32_t bits;  // tokens, and from bit 10 on: two query tiles, lane, all of the item's tiles; 13: kv head
+  int32_t part0, part1, part2;  // tiles that some row does not see in full: [part0, part1), and from part2 on
+  int32_t pad;
   __device__ __forceinline__ int ntok() const { return bits & 1023; }
   __device__ __forceinline__ bool two() const { return bits >> 10 & 1; }
   __device__ __forceinline__ int lane() const { return bits >> 11 & 1; }
@@ -112,6 +109,7 @@ struct __align__(16) Segment {
   __device__ __forceinline__ int h() const { return bits >> 13; }
   __device__ __forceinline__ int p1() const { return p0 + ntok() - 1; }
   __device__ __forceinline__ bool has(int q) const { return two() || lane() == q; }
+  __device__ __forceinline__ bool partly(int t) const { return t >= part2 || (t >= part0 && t < part1); }
 };
 // The first key of tile t.
 template <int KEYS>
@@ -127,6 +125,39 @@ struct Run {
   int ctas, req, tile, h, at;      // request, tile of its rows, kv head, unit of the item
   int start, n, len;               // of the request
 };
+
+// Of a partly visible tile from key k0 on: keys that some row sees lie in [first, end), by steps of
+// 16 (the K of an MMA), and of these all rows see those in [low, high), but for sinks.
+struct Span {
+  int first, end, low, high;
+};
+template <int KEYS>
+__device__ __forceinline__ Span seen_span(const Args& a, const Segment& s, int k0) {
+  Span p{0, 0, 0, 0};
+  const int p1 = s.p1();
+  if (a.window > 0 && a.sinks <= k0) p.first = min(max(s.p0 - a.window + 1 - k0, 0), KEYS - 1) & ~15;
+  p.end = min((max(p1 - k0 + 1, 1) + 15) & ~15, KEYS);
+  if (p.end <= p.first) p.end = p.first + 16;  // (no row sees a key: one step of zeros all the same)
+  p.low = a.window > 0 ? min(max(p1 - a.window + 1 - k0, p.first), p.end) : p.first;
+  p.high = min(max(s.p0 + 1 - k0, p.low), p.end);
+  return p;
+}
+
+// Which tiles are partly visible: a tile from key k0 on is seen by all rows if its last key is by the
+// first row (k0 + KEYS - 1 <= p0), and with a window if its first key is by the last row (k0 > p1 -
+// window) or all of it is sinks. (Where sinks reach into the window's own tiles some of these count as
+// partly visible although all rows see them.)
+template <int KEYS>
+__device__ __forceinline__ void mark_parts(const Args& a, Segment* s) {
+  const int st = a.window > 0 ? min((a.sinks + KEYS - 1) / KEYS, s->lo) : 0, p1 = s->p1();
+  const int full = max(s->p0 + 1, 0) / KEYS;  // key tiles that the first row is past
+  s->part0 = s->part1 = 0;
+  if (a.window > 0) {
+    s->part0 = min(a.sinks / KEYS, st);
+    s->part1 = st + max((max(p1 - a.window + 1, 0) + KEYS - 1) / KEYS - s->lo, 0);
+  }
+  s->part2 = full > s->lo ? st + full - s->lo : min(full, st);
+}
 
 // A CTA's segments in order, by a whole warp.
 struct Walk {
@@ -211,6 +242,7 @@ struct Walk {
           item(a);
         }
       }
+      mark_parts<kTcKeys>(a, s);
       if (s->t1 > s->t0) return true;  // (else only empty units of it are in this run)
     }
     return false;

@@ -131,54 +131,44 @@ __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
 }
 
 // The same by one warp, where neither requests nor items can be more than 32.
-__device__ __forceinline__ void find_run_of_few(const Args& a, Run* run) {
+__device__ __forceinline__ void find_run_of_few(const Args& a, int8_t* list, Run* run) {
   const int lane = threadIdx.x & 31;
-  auto scan = [&](int v) {  // up to and with each lane
-#pragma unroll
+  auto scan = [&](int64_t v) {  // up to and with each lane
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += y;
     }
     return v;
   };
   Request q = request(a, lane);
-  const int rows = scan(q.n);  // (below 32 x 2^24)
+  const int64_t rows = scan(q.n);
   if (rows > a.T) q.bad = true, q.n = 0;
   if (q.bad && blockIdx.x == 0 && a.err != nullptr) atomicOr(a.err, kErrBadLength);
-  const int tiles = (q.n + a.tile_tokens - 1) / a.tile_tokens, upto = scan(tiles);
-  // lane j: item j, of the request r with upto[r] - tiles[r] <= j < upto[r]
-  int r = 0;
-#pragma unroll
-  for (int k = 0; k < 32; ++k) r += __shfl_sync(0xffffffffu, upto, k) <= lane;
-  r = min(r, 31);
+  // the items, request by request; lane j then takes the j-th
+  const int tiles = (q.n + a.tile_tokens - 1) / a.tile_tokens, upto = (int)scan(tiles);
+#pragma unroll 1
+  for (int i = 0; i < tiles; ++i) list[upto - tiles + i] = (int8_t)lane;
+  __syncwarp();
+  const bool live = lane < __shfl_sync(0xffffffffu, upto, 31);
+  const int r = live ? list[lane] : 0;
   const int i = lane - __shfl_sync(0xffffffffu, upto - tiles, r), start = __shfl_sync(0xffffffffu, q.start, r),
-            n = __shfl_sync(0xffffffffu, q.n, r), len = __shfl_sync(0xffffffffu, q.len, r), before = __shfl_sync(0xffffffffu, rows, r);
-  int span = 0;
-  if (lane < __shfl_sync(0xffffffffu, upto, 31)) {
-    int lo;
-    span = kHead + key_tiles(a, len - n + i * a.tile_tokens, min(a.tile_tokens, n - i * a.tile_tokens), &lo);
-  }
-  int64_t end = (int64_t)span * a.kv.kv_heads;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
-    if (lane >= o) end += y;
-  }
-  const int64_t units = __shfl_sync(0xffffffffu, end, 31);
+            n = __shfl_sync(0xffffffffu, q.n, r), len = __shfl_sync(0xffffffffu, q.len, r);
+  const int64_t before = __shfl_sync(0xffffffffu, rows, r);
+  int span = 0, lo;
+  if (live) span = kHead + key_tiles(a, len - n + i * a.tile_tokens, min(a.tile_tokens, n - i * a.tile_tokens), &lo);
+  const int64_t mine = (int64_t)span * a.kv.kv_heads, end = scan(mine), units = __shfl_sync(0xffffffffu, end, 31);
   const int ctas = (int)min((int64_t)a.ctas, (units + kHead + 1) / (kHead + 2));
   int64_t u = 0, left = 0;
   if ((int)blockIdx.x < ctas) u = run_start(units, ctas, blockIdx.x), left = run_start(units, ctas, blockIdx.x + 1) - u;
-  const int64_t in = u - (end - (int64_t)span * a.kv.kv_heads);
-  const uint32_t has = __ballot_sync(0xffffffffu, left > 0 && in >= 0 && u < end);
-  run->left = has != 0 ? left : 0;
-  if (has == 0) return;
-  const int k = __ffs(has) - 1, n_units = __shfl_sync(0xffffffffu, span, k);
-  const int64_t at = __shfl_sync(0xffffffffu, in, k);
-  const int h = at >> 32 ? (int)(at / n_units) : (int)((uint32_t)at / (uint32_t)n_units);
-  run->units = units, run->u = u, run->ctas = ctas, run->h = h, run->at = (int)(at - (int64_t)h * n_units);
-  run->req = __shfl_sync(0xffffffffu, r, k), run->tile = __shfl_sync(0xffffffffu, i, k);
-  run->start = __shfl_sync(0xffffffffu, start, k), run->n = __shfl_sync(0xffffffffu, n, k);
-  run->len = __shfl_sync(0xffffffffu, len, k), run->before = __shfl_sync(0xffffffffu, before, k);
+  if (lane == 0) run->left = left;
+  if (left > 0 && u < end && u >= end - mine) {
+    const int64_t at = u - (end - mine);
+    const int h = at >> 32 ? (int)(at / span) : (int)((uint32_t)at / (uint32_t)span);
+    run->units = units, run->u = u, run->ctas = ctas, run->h = h, run->at = (int)(at - (int64_t)h * span);
+    run->req = r, run->tile = i, run->start = start, run->n = n, run->len = len, run->before = before;
+  }
+  __syncwarp();
 }
 
 // Clears the counts of an item's parts.
@@ -213,19 +203,19 @@ struct Cfg {
   static constexpr int kGuards = F8 ? 4 : 2;              // warps that look at partly visible values
 };
 
-constexpr int kSegs = 12;
+constexpr int kSegs = 8;
 
 struct Bars {
   uint64_t full[8], empty[8], raw[8];
   uint64_t vok[8];  // partly visible values are cleared
-  uint64_t sfull[2], pready[2], odone[2], ofree[2], joined[2], qfull, qraw, qempty, drain;
+  uint64_t sfull[2], pready[2], odone[2], joined[2], qfull, qraw, qempty, drain;
   uint32_t tmem;
   int abort;
   int last[2];  // whether a query tile's last part was the item's
   Run run;
   uint8_t poison[4][16];  // [guard warp][segment % 16]: cleared values that some row sees
-  // The segments, which the loader works out for all, in a ring that needs no way back: when it comes
-  // to segment s + 12, the tiles of s + 6 are done with (a ring of tiles holds four), hence
+  // The segments, which the loader works out for all, in a ring that needs no way back: when it writes
+  // segment s + 8, the tiles of s + 3 are done with (a ring of tiles holds four), hence
   // both query tiles with a segment after s, as those of one query tile come in turn (so are `poison`,
   // of 16, and the e4m3 row exponents, of 4, whose writers wait for the segment before).
   uint64_t segready[kSegs];
@@ -239,7 +229,14 @@ __device__ __forceinline__ bool get_segment(Bars& b, uint32_t i, Segment* s, vol
   const volatile int4* p = reinterpret_cast<const volatile int4*>(&b.segs[i % kSegs]);
   s->req = p[0].x, s->tok0 = p[0].y, s->p0 = p[0].z, s->lo = p[0].w;
   s->t0 = p[1].x, s->t1 = p[1].y, s->join = p[1].z, s->bits = p[1].w;
+  s->part0 = p[2].x, s->part1 = p[2].y, s->part2 = p[2].z;
   return s->bits != 0;
+}
+
+// the larger of two pairs of bf16
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // the lowest n bits, n below 0 and above 32 as 0 and 32
@@ -256,7 +253,7 @@ __device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p,
   const int psh = 31 - __clz(a.kv.page_size);
   for (int t = sg.t0; t < sg.t1; ++t) {
     const int k0 = tile_key<kKeys>(a, sg, t);
-    if (all_see_tile(a, sg.p0, sg.p1(), k0, kKeys)) continue;
+    if (!sg.partly(t)) continue;
     for (int j = k0; j < k0 + kKeys && j <= p; ++j) {
       if (!sees(a, p, j)) continue;
       const int page = a.page_table[(int64_t)sg.req * a.table_stride + (j >> psh)];
@@ -279,68 +276,113 @@ __device__ __noinline__ float poison_of(const Args& a, const Segment& sg, int p,
 __device__ __forceinline__ float lse_of(float m, float l) { return m == -INFINITY ? -INFINITY : (m + __log2f(l)) * kLn2; }
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }
 
-// The parts of rows i0 + r0, i0 + r0 + step, .. (U of them, below `rows`) of an item, added in the order of the
-// CTAs by a warp; 4 columns a lane, P parts at a time. Little code: it runs once in a while, and what is not in
-// the instruction cache costs more than what it does.
-template <int D, int U, int P>
-__device__ __forceinline__ void join_rows(const Args& a, const Segment& sg, int i0, int rows, int r0, int step) {
-  constexpr int L = D / 4;  // lanes of a row; 32 / L rows of the U are a lane's
-  const int lane = threadIdx.x & 31, c = lane % L * 4;
-  const int c0 = sg.join & 0xffff, parts = sg.join >> 16;
-  float m[U], l[U], acc[U][4];
-#pragma unroll
-  for (int k = 0; k < U; ++k) m[k] = -INFINITY, l[k] = acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-  for (int p0 = 0; p0 < parts; p0 += P) {
-    float2 ml[P][U];
-    float4 o[P][U];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int pp = min(p0 + p, parts - 1);
-      const int64_t at = ((int64_t)(c0 + pp) * 2 + (pp == 0)) * a.part_rows + i0;
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int r = min(r0 + k * step, rows - 1);
-        ml[p][k] = __ldcg(a.ml_part + at + r);
-        if (p0 + p >= parts) ml[p][k] = make_float2(-INFINITY, 0.f);
-        o[p][k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (at + r) * D + c));
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const float top = fmaxf(m[k], ml[p][k].x), base = top == -INFINITY ? 0.f : top, f = ex2(m[k] - base),
-                    g = ex2(ml[p][k].x - base);
-        m[k] = top;
-        l[k] = fmaf(l[k], f, ml[p][k].y * g);
-        const float v[4] = {o[p][k].x, o[p][k].y, o[p][k].z, o[p][k].w};
-        // (a part that is none is another one again, times 0: it may hold infinities)
-#pragma unroll
-        for (int d = 0; d < 4; ++d) acc[k][d] = p0 + p < parts ? fmaf(acc[k][d], f, v[d] * g) : acc[k][d];
-      }
-  }
-  const uint32_t row0 = (uint32_t)sg.tok0 * a.q_heads + sg.h() * a.group;
-#pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const int r = r0 + k * step, i = i0 + r;
-    const uint32_t row = row0 + i + row_token(a, i) * (a.q_heads - a.group);
-    const float inv = inverse(l[k]);
-    if (r < rows) {
-      *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + c) =
-          make_uint2(pack2<false>(acc[k][0] * inv, acc[k][1] * inv), pack2<false>(acc[k][2] * inv, acc[k][3] * inv));
-      if (a.lse != nullptr && c == 0) a.lse[row] = lse_of(m[k], l[k]);
-    }
-  }
-}
-// `rows` rows from i0 on by the four warps of a query tile, w this one.
+// Joins the parts of `rows` rows from row i0 of an item on, in the order of the CTAs, by the four warps
+// of a query tile, w this one. Little code: it runs once in a while, and what is not in the instruction
+// cache costs more than what it does. First a row's base and sum, then its weighted sums, 16 bytes a lane.
 template <int D>
 __device__ __noinline__ void join(const Args& a, const Segment& sg, int i0, int rows, int w) {
-  constexpr int S = 128 / D;  // rows at a time
-  const int first = (threadIdx.x & 31) / (D / 4);
+  constexpr int L = D / 4, S = 32 / L;  // lanes of a row, rows at a time
+  const int lane = threadIdx.x & 31, sub = lane / L, c = lane % L * 4;
+  const int c0 = sg.join & 0xffff, parts = sg.join >> 16;
+  const int64_t stride = 2 * a.part_rows;
+  const int64_t at0 = (int64_t)c0 * stride + i0;  // of part p: + p stride, and one slot further for p = 0
+  const uint32_t row0 = (uint32_t)sg.tok0 * a.q_heads + sg.h() * a.group;
+  auto part_at = [&](int p) { return at0 + p * stride + (p == 0 ? a.part_rows : 0); };
+  auto put = [&](int r, const float (&acc)[4], float inv) {
+    const int i = i0 + r;
+    const uint32_t row = row0 + i + row_token(a, i) * (a.q_heads - a.group);
+    *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + c) =
+        make_uint2(pack2<false>(acc[0] * inv, acc[1] * inv), pack2<false>(acc[2] * inv, acc[3] * inv));
+  };
   if (rows <= 8) {
-    join_rows<D, 2 / S, 8>(a, sg, i0, rows, w * 2 + first, S);
-  } else {
-    for (int r0 = w * 8; r0 < rows; r0 += 32) join_rows<D, 8 / S, 2>(a, sg, i0, rows, r0 + first, S);
+    // a warp two rows, 8 parts of them at a time
+    constexpr int U = 2 / S, P = 8;
+    const int r0 = w * 2 + sub;
+    float m[U], l[U], acc[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) m[k] = -INFINITY, l[k] = acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+#pragma unroll 1
+    for (int p0 = 0; p0 < parts; p0 += P) {
+      float2 ml[P][U];
+      float4 o[P][U];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int64_t at = part_at(min(p0 + p, parts - 1));
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int r = min(r0 + k, rows - 1);
+          ml[p][k] = __ldcg(a.ml_part + at + r);
+          o[p][k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (at + r) * D + c));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        float top = m[k];
+#pragma unroll
+        for (int p = 0; p < P; ++p) top = fmaxf(top, ml[p][k].x);
+        const float base = top == -INFINITY ? 0.f : top, f = ex2(m[k] - base);
+        m[k] = top;
+        l[k] *= f, acc[k][0] *= f, acc[k][1] *= f, acc[k][2] *= f, acc[k][3] *= f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          if (p0 + p < parts) {
+            const float g = ex2(ml[p][k].x - base);
+            l[k] = fmaf(ml[p][k].y, g, l[k]);
+            acc[k][0] = fmaf(o[p][k].x, g, acc[k][0]), acc[k][1] = fmaf(o[p][k].y, g, acc[k][1]);
+            acc[k][2] = fmaf(o[p][k].z, g, acc[k][2]), acc[k][3] = fmaf(o[p][k].w, g, acc[k][3]);
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (r0 + k < rows) {
+        put(r0 + k, acc[k], inverse(l[k]));
+        if (a.lse != nullptr && c == 0)
+          a.lse[row0 + i0 + r0 + k + row_token(a, i0 + r0 + k) * (a.q_heads - a.group)] = lse_of(m[k], l[k]);
+      }
+    return;
+  }
+  // a warp 32 rows: a lane a row, for the base and the sum; then 8 rows at a time
+  const int b0 = w * 32;
+  if (b0 >= rows) return;
+  const int mine = min(b0 + lane, rows - 1);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = __ldcg(a.ml_part + part_at(p) + mine);
+    const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+    l = l * ex2(m - base) + ml.y * ex2(ml.x - base);
+    m = top;
+  }
+  const float base = m == -INFINITY ? 0.f : m, inv = inverse(l);
+  if (a.lse != nullptr && b0 + lane < rows) a.lse[row0 + i0 + mine + row_token(a, i0 + mine) * (a.q_heads - a.group)] = lse_of(m, l);
+  constexpr int U = 8;
+#pragma unroll 1
+  for (int g0 = 0; g0 < min(32, rows - b0); g0 += U * S) {
+    float acc[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p) {
+      const float f = ex2(__ldcg(a.ml_part + part_at(p) + mine).x - base);
+      const float* src = a.o_part + (part_at(p) + b0) * D + c;
+      float4 o[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k)  // (rows beyond the last: the last, of the item's part all the same)
+        o[k] = __ldcg(reinterpret_cast<const float4*>(src + min(g0 + k * S + sub, rows - 1 - b0) * D));
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float g = __shfl_sync(0xffffffffu, f, (g0 + k * S + sub) & 31);
+        acc[k][0] = fmaf(o[k].x, g, acc[k][0]), acc[k][1] = fmaf(o[k].y, g, acc[k][1]);
+        acc[k][2] = fmaf(o[k].z, g, acc[k][2]), acc[k][3] = fmaf(o[k].w, g, acc[k][3]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int r = g0 + k * S + sub;
+      const float v = __shfl_sync(0xffffffffu, inv, r & 31);
+      if (b0 + r < rows) put(b0 + r, acc[k], v);
+    }
   }
 }
 
@@ -394,10 +436,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       mbar_init(&b.sfull[i], 1);
       mbar_init(&b.pready[i], 4);
       mbar_init(&b.odone[i], 1);
-      mbar_init(&b.ofree[i], 4);
       mbar_init(&b.joined[i], 4);
     }
-    mbar_init(&b.qfull, F8 ? 2 : 1);
+    mbar_init(&b.qfull, F8 ? 4 : 1);
     mbar_init(&b.qraw, 1);
     mbar_init(&b.qempty, 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&b.segready[i], 1);
@@ -421,6 +462,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   constexpr uint32_t tmem = 0;
   const int psh = 31 - __clz(a.kv.page_size);
   Segment sg;
+  auto load_q = [&](const Segment& s, uint64_t* bar) {
+    if (lane == 0) {
+      const bool few = s.ntok() <= a.few_tokens;
+      mbar_arrive_expect_tx(bar, (few ? a.few_tokens : a.tile_tokens) * a.group * D * 2);
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+        tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, bar, hf * 64, s.h() * a.group, s.tok0);
+    }
+    __syncwarp();
+  };
 
   if (warp < 8) {
     // ---------------- softmax: one thread a row
@@ -464,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           }
         }
         const int k0 = tile_key<kKeys>(a, sg, t);
-        if (negate || !all_see_tile(a, sg.p0, sg.p1(), k0, kKeys)) {
+        if (negate || sg.partly(t)) {
           // masked in TMEM: seldom needed code that does not displace the loop's from the cache
           const int hi = pos - k0 + 1, lo = a.window > 0 ? hi - a.window : 0, sink = a.sinks - k0;
           const uint32_t sign = negate ? 0x80000000u : 0u;
@@ -561,11 +612,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         uint8_t* dst[4];  // of rows (lane & ~3) + k, from this lane's unit on
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t of = __shfl_sync(0xffffffffu, whole ? head : part, (lane & ~3) + k);
+          const uint32_t of = __shfl_sync(0xffffffffu, whole ? head : part, rows > 32 ? (lane & ~3) + k : lane);
           dst[k] = (whole ? reinterpret_cast<uint8_t*>(a.out + (int64_t)of * D) : reinterpret_cast<uint8_t*>(a.o_part + (int64_t)of * D)) +
-                   (lane & 3) * 32;
+                   (rows > 32 ? lane & 3 : k) * 32;
         }
-        const int mine = rows - (i - lane) - (lane & ~3);  // rows of the four that are there
+        // of the four stores' rows these are there; few rows stay a lane each
+        const int mine = rows > 32 ? rows - (i - lane) - (lane & ~3) : i < rows ? 4 : 0;
 #pragma unroll 1
         for (int c = 0; c < D; c += whole ? 64 : 32) {
           uint32_t o[32];
@@ -584,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * vs);
           }
-          turn_units(o);
+          if (rows > 32) turn_units(o);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (k < mine) {
@@ -602,7 +654,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         fence_before();
       }
-      warp_arrive(&b.ofree[q]);
       if (!sg.whole()) {
         // the query tile's four warps, the ones without rows too, and one of them counts the part
         __threadfence();
@@ -635,14 +686,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       uint32_t kv = 0;               // K and V tiles so far
       uint32_t part = 0;             // by slot, whether an odd number of partly visible tiles was there
       uint32_t segs = 0;
-      uint32_t pn[2] = {0, 0}, sn[2] = {0, 0};  // products with V, and segments, of each query tile so far
+      uint32_t pn[2] = {0, 0};       // products with V of each query tile so far
       auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity & 1, abort_flag, a.err); };
       auto wait_kv = [&](uint32_t i) { return wait(&b.full[i % kSlots], i / kSlots); };
-      // scores of tile t of s by query tile q; the last query tile's are the last on this K tile, and
-      // with the last tile on this segment's q
-      auto scores = [&](const Segment& s, int t, int q, uint32_t slot) {
+      // scores by query tile q, whose rows are at qq; the last query tile's are the last on this K tile,
+      // and with a segment's last tile on its q
+      auto scores = [&](int q, uint32_t qq, uint32_t slot, bool last, bool end) {
         if (converged_lane()) {
-          const uint32_t qq = qa + (s.two() && q ? 128 * 128 : 0);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t in = (k % 4) * 32;
@@ -650,89 +700,142 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                      sw128_desc(ring + slot * C::kTileBytes + (k / 4) * (kKeys * 128) + in), is, k > 0);
           }
           mma_commit(&b.sfull[q]);
-          if (!s.two() || q == 1) {
-            mma_commit(&b.empty[slot]);
-            if (t + 1 == s.t1) mma_commit(&b.qempty);
-          }
+          if (last) mma_commit(&b.empty[slot]);
+          if (end) mma_commit(&b.qempty);
         }
         __syncwarp();
+      };
+      // weights x values of tile t of sg by query tile q
+      auto products = [&](int t, int q, uint32_t slot, bool last) {
+        const uint32_t o = tmem + 256 + q * 128, p = tmem + q * 128, v = ring + slot * C::kTileBytes;
+        if (converged_lane()) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k) mma_f16_ts(o, p + k * 8, v_desc(v + k * 2048), io, t > sg.t0 || k > 0);
+          if (last) mma_commit(&b.empty[slot]);
+        }
+        __syncwarp();
+      };
+      // the same of any tile: of a partly visible one only the steps of 16 keys that some row sees
+      auto any_products = [&](int t, int q, uint32_t slot, bool last) {
+        const uint32_t o = tmem + 256 + q * 128, p = tmem + q * 128, v = ring + slot * C::kTileBytes;
+        int step0 = 0, step1 = kKeys / 16;
+        if (sg.partly(t)) {
+          const Span pt = seen_span<kKeys>(a, sg, tile_key<kKeys>(a, sg, t));
+          step0 = pt.first / 16, step1 = pt.end / 16;
+        }
+#pragma unroll 1
+        for (int k = step0; k < step1; ++k)
+          if (converged_lane()) mma_f16_ts(o, p + k * 8, v_desc(v + k * 2048), io, t > sg.t0 || k > step0);
+        if (converged_lane()) {
+          if (t + 1 == sg.t1) mma_commit(&b.odone[q]);
+          if (last) mma_commit(&b.empty[slot]);
+        }
+        __syncwarp();
+      };
+      auto wait_v = [&](int t, uint32_t i) {
+        if (!wait_kv(i)) return false;
+        if (F8 || !sg.partly(t)) return true;
+        const uint32_t slot = i % kSlots;
+        if (!wait(&b.vok[slot], part >> slot)) return false;
+        part ^= 1u << slot;
+        return true;
+      };
+      auto q_rows = [&](const Segment& s, int q) { return qa + (s.two() && q ? 128 * 128 : 0); };
+      // all scores of a segment's first tile
+      auto first_scores = [&](const Segment& s, uint32_t slot) {
+        const bool end = s.t0 + 1 == s.t1;
+        for (int q = s.two() ? 0 : s.lane(); q < (s.two() ? 2 : s.lane() + 1); ++q) {
+          const bool last = !s.two() || q == 1;
+          scores(q, q_rows(s, q), slot, last, last && end);
+        }
       };
       bool ok = true, have = get_segment(b, 0, &sg, abort_flag, a.err);
       if (have) {
         ok = wait(&b.qfull, segs) && wait_kv(kv);
         fence_after();
-        for (int q = 0; q < 2 && ok; ++q)
-          if (sg.has(q)) scores(sg, sg.t0, q, kv % kSlots);
+        if (ok) first_scores(sg, kv % kSlots);
       }
       while (ok && have) {
-        Segment nx;  // the next one; its first scores come among this one's last products
-        bool more = false;
-        for (int t = sg.t0; t < sg.t1; ++t, kv += 2) {
-          const uint32_t vslot = (kv + 1) % kSlots, kslot = (kv + 2) % kSlots;
-          const bool last = t + 1 == sg.t1;
-          if (last) {  // (the loader makes it known behind this tile)
-            more = get_segment(b, segs + 1, &nx, abort_flag, a.err);
-            if (__any_sync(0xffffffffu, *abort_flag)) {
+        const int qb = sg.two() ? 0 : sg.lane(), qe = sg.two() ? 2 : sg.lane() + 1;
+        int t = sg.t0;
+        // (a query tile's weights come after it has read its accumulators of the segment before)
+        while (t + 1 < sg.t1) {
+          // a run of tiles that all rows see, in as few instructions as can be: this warp's are what the
+          // tensor cores wait for (with the other tiles' case in the loop 60,000 keys take 7% longer)
+          const int stop = min(t < sg.part0 ? sg.part0 : t < sg.part1 ? t : sg.part2, sg.t1 - 1);
+          for (; t < stop; ++t, kv += 2) {
+            if (!wait_kv(kv + 2) || !wait_kv(kv + 1)) {
               ok = false;
               break;
             }
-          }
-          const Segment& s2 = last ? nx : sg;
-          const int t2 = last ? nx.t0 : t + 1;
-          const bool any = !last || more;
-          // the next scores come before and between this tile's products with V, but where q is late
-          const bool early = any && (!last || __all_sync(0xffffffffu, mbar_try_wait(&b.qfull, (segs + 1) & 1)));
-          const bool first = early && last && !sg.two() && !nx.two();  // the other query tile's turn: at once
-          if (early && !wait_kv(kv + 2)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          if (first) scores(nx, t2, nx.lane(), kslot);
-          if (!wait_kv(kv + 1)) {
-            ok = false;
-            break;
-          }
-          if (!F8 && !all_see_tile(a, sg.p0, sg.p1(), tile_key<kKeys>(a, sg, t), kKeys)) {
-            if (!wait(&b.vok[vslot], part >> vslot)) {
-              ok = false;
-              break;
-            }
-            part ^= 1u << vslot;
-          }
-          for (int q = 0; q < 2 && ok; ++q) {
-            if (sg.has(q)) {
-              // the weights, and at a segment's first tile the accumulators
-              if (!wait(&b.pready[q], pn[q]) || (t == sg.t0 && sn[q] > 0 && !wait(&b.ofree[q], sn[q] - 1))) {
+            const uint32_t vslot = (kv + 1) % kSlots, kslot = (kv + 2) % kSlots;
+            const bool end = t + 2 == sg.t1;
+            for (int q = qb; q < qe; ++q) {
+              if (!wait(&b.pready[q], pn[q])) {
                 ok = false;
                 break;
               }
               ++pn[q];
-              if (t == sg.t0) ++sn[q];
               fence_after();
-              if (converged_lane()) {
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_f16_ts(tmem + 256 + q * 128, tmem + q * 128 + k * 8, v_desc(ring + vslot * C::kTileBytes + k * 2048), io,
-                             t > sg.t0 || k > 0);
-                if (last) mma_commit(&b.odone[q]);
-                if (!sg.two() || q == 1) mma_commit(&b.empty[vslot]);
-              }
-              __syncwarp();
+              products(t, q, vslot, q + 1 == qe);
+              scores(q, q_rows(sg, q), kslot, q + 1 == qe, end && q + 1 == qe);
             }
-            if (early && !first && s2.has(q)) scores(s2, t2, q, kslot);
+            if (!ok) break;
           }
           if (!ok) break;
-          if (any && !early) {
-            if (!wait(&b.qfull, segs + 1) || !wait_kv(kv + 2)) {
+          if (t + 1 == sg.t1) break;
+          if (!wait_kv(kv + 2) || !wait_v(t, kv + 1)) {
+            ok = false;
+            break;
+          }
+          for (int q = qb; q < qe; ++q) {
+            if (!wait(&b.pready[q], pn[q])) {
               ok = false;
               break;
             }
+            ++pn[q];
             fence_after();
-            for (int q = 0; q < 2; ++q)
-              if (nx.has(q)) scores(nx, t2, q, kslot);
+            any_products(t, q, (kv + 1) % kSlots, q + 1 == qe);
+            scores(q, q_rows(sg, q), (kv + 2) % kSlots, q + 1 == qe, t + 2 == sg.t1 && q + 1 == qe);
+          }
+          if (!ok) break;
+          ++t, kv += 2;
+        }
+        if (!ok) break;
+        // the last tile: the next segment's scores come before and between its products with V, but where q
+        // is late
+        Segment nx;
+        const bool more = get_segment(b, segs + 1, &nx, abort_flag, a.err);  // (made known behind this tile)
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        const uint32_t vslot = (kv + 1) % kSlots, kslot = (kv + 2) % kSlots;
+        const bool early = more && __all_sync(0xffffffffu, mbar_try_wait(&b.qfull, (segs + 1) & 1));
+        const bool first = early && !sg.two() && !nx.two();  // the other query tile's turn: at once
+        if (early && !wait_kv(kv + 2)) break;
+        fence_after();
+        if (first) first_scores(nx, kslot);
+        if (!wait_v(t, kv + 1)) break;
+        for (int q = 0; q < 2; ++q) {
+          if (sg.has(q)) {
+            if (!wait(&b.pready[q], pn[q])) {
+              ok = false;
+              break;
+            }
+            ++pn[q];
+            fence_after();
+            any_products(t, q, vslot, q + 1 == qe);
+          }
+          if (early && !first && nx.has(q)) {
+            const bool last = !nx.two() || q == 1;
+            scores(q, q_rows(nx, q), kslot, last, last && nx.t0 + 1 == nx.t1);
           }
         }
+        if (!ok) break;
+        if (more && !early) {
+          if (!wait(&b.qfull, segs + 1) || !wait_kv(kv + 2)) break;
+          fence_after();
+          first_scores(nx, kslot);
+        }
+        kv += 2;
         sg = nx;
         have = more;
         ++segs;
@@ -753,13 +856,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       uint32_t kv = 0;
       bool ok = true;
       Walk walk;
-      if (a.few) {
-        Run run;
-        find_run_of_few(a, &run);
-        walk.begin(a, run);
-      } else {
-        walk.begin(a, b.run);
-      }
+      if (a.few) find_run_of_few(a, reinterpret_cast<int8_t*>(&b.segs[kSegs - 1]), &b.run);  // (a place not yet in use)
+      walk.begin(a, b.run);
       for (uint32_t i = 0; ok; ++i) {
         if (!walk.next(a, &sg)) sg.bits = 0;
         if (lane == 0) {
@@ -805,23 +903,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
       }
     } else if constexpr (!F8) {
-      // ---------------- guards: warp 10 looks at keys 0-63 of partly visible tiles, 11 at the others;
+      // ---------------- guards: warps 10 and 11 look at the values of partly visible tiles;
       // warp 10 also loads q. A box holds whole tokens, so rows beyond the item's are the next tokens' or zero.
       const int gw = warp - 10;
       uint32_t kv = 0, segs = 0, loads = 0;
       bool ok = get_segment(b, 0, &sg, abort_flag, a.err);
-      auto load_q = [&](const Segment& s) {
-        if (lane == 0) {
-          const bool few = s.ntok() <= a.few_tokens;
-          mbar_arrive_expect_tx(&b.qfull, (few ? a.few_tokens : a.tile_tokens) * a.group * D * 2);
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, &b.qfull, hf * 64, s.h() * a.group, s.tok0);
-        }
-        __syncwarp();
-        ++loads;
-      };
-      if (gw == 0 && ok) load_q(sg);
+      if (gw == 0 && ok) load_q(sg, &b.qfull), ++loads;
       while (ok) {
         Segment nx;
         bool more = false;
@@ -843,14 +930,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
                   ok = false;
                   break;
                 }
-                load_q(nx);
+                load_q(nx, &b.qfull);
+                ++loads;
               }
             }
-            if (v == 1 && !all_see_tile(a, sg.p0, sg.p1(), k0, kKeys)) {
+            if (v == 1 && sg.partly(t)) {
               bool found = false;
-#pragma unroll 4
-              for (int i = lane; i < 64 * (D / 8); i += 32) {
-                const int r = gw * 64 + i / (D / 8), c = i % (D / 8);
+              const Span pt = seen_span<kKeys>(a, sg, k0);
+              const int below = pt.low - pt.first, rows = below + pt.end - pt.high;
+#pragma unroll 1
+              for (int i = gw * 32 + lane; i < rows * (D / 8); i += 64) {
+                const int n = i / (D / 8), c = i % (D / 8), r = n < below ? pt.first + n : pt.high + n - below;
                 if (all_see(a, sg.p0, sg.p1(), k0 + r)) continue;
                 uint4* at = reinterpret_cast<uint4*>(smem + slot * C::kTileBytes + (c / 8) * (kKeys * 128) + r * 128 + (c & 7) * 16);
                 if (!any_sees(a, sg.p0, sg.p1(), k0 + r)) {
@@ -887,59 +977,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
       }
     } else {
-      // ---------------- e4m3: warp 10 loads q as for a bf16 cache; 10 and 11 turn it in place into fp16
-      // divided by each row's power of two. Rows beyond the item's stay what they were.
-      constexpr int LPR = D / 8, N = 8, kStep = 64 / LPR;  // threads of a row, chunks at once, rows at a time
-      const int tid = threadIdx.x - 10 * 32, c = tid % LPR;
-      uint32_t segs = 0, loads = 0;
-      for (; get_segment(b, segs, &sg, abort_flag, a.err); ++segs) {
-        const int rows = sg.ntok() * a.group;
-        const float ks = a.kv.k_scale[sg.h()];
-        if (segs > 0 && !warp_wait(&b.qempty, (segs - 1) & 1, abort_flag, a.err)) break;
-        if (warp == 10) {
-          if (lane == 0) {
-            const bool few = sg.ntok() <= a.few_tokens;
-            mbar_arrive_expect_tx(&b.qraw, (few ? a.few_tokens : a.tile_tokens) * a.group * D * 2);
-#pragma unroll
-            for (int hf = 0; hf < D / 64; ++hf)
-              tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, &b.qraw, hf * 64, sg.h() * a.group, sg.tok0);
-          }
-          ++loads;
-          __syncwarp();
+      // ---------------- e4m3: warp 10 loads q
+      uint32_t loads = 0;
+      if (warp == 10)
+        for (; get_segment(b, loads, &sg, abort_flag, a.err); ++loads) {
+          if (loads > 0 && !warp_wait(&b.qempty, (loads - 1) & 1, abort_flag, a.err)) break;
+          load_q(sg, &b.qraw);
         }
-        if (!warp_wait(&b.qraw, segs & 1, abort_flag, a.err)) break;
-        for (int r0 = tid / LPR; r0 - tid / LPR < rows; r0 += N * kStep) {
-          uint4 v[N];
-#pragma unroll
-          for (int p = 0; p < N; ++p) {
-            const int r = min(r0 + p * kStep, kRows - 1);
-            v[p] = *reinterpret_cast<const uint4*>(qs + (c / 8) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-          }
-#pragma unroll
-          for (int p = 0; p < N; ++p) {
-            const int r = r0 + p * kStep;
-            uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-            float mx = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int e = row_exponent(mx);
-            const float down = fabsf(a.scale) * fabsf(ks) * pow2(e) != 0.f ? pow2(-e) : 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-            if (r < rows) {
-              if (c == 0) qexp[(segs & 3) * 256 + r] = (int8_t)e;
-              *reinterpret_cast<uint4*>(qs + (c / 8) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
-        fence_async();
-        warp_arrive(&b.qfull);
-      }
       // q's copy in flight lands before the CTA leaves
       if (loads > 0) {
         const long long t0 = clock64();
@@ -958,40 +1002,77 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     for (; ok && get_segment(b, segs, &sg, abort_flag, a.err); ++segs) {
       if (lane == 0) *(volatile uint8_t*)&b.poison[warp - 12][segs & 15] = 0;
       __syncwarp();
+      {  // q in place, divided by each row's power of two; rows beyond the item's stay what they were
+        constexpr int LPR = D / 8, U = 4, kStep = 128 / LPR;  // threads of a row, chunks at once, rows at a time
+        const int rows = sg.ntok() * a.group, c = tid % LPR;
+        const float factor = fabsf(a.scale) * fabsf(a.kv.k_scale[sg.h()]);
+        if (!warp_wait(&b.qraw, segs & 1, abort_flag, a.err)) break;
+        uint8_t* q0 = qs + (c / 8) * (kRows * 128);
+#pragma unroll 1
+        for (int i0 = 0; i0 < rows; i0 += U * kStep) {
+          const int ra = i0 + tid / LPR;
+          uint4 v[U];
+          uint32_t mx[U];
+#pragma unroll
+          for (int p = 0; p < U; ++p) {
+            const int r = min(ra + p * kStep, kRows - 1);
+            v[p] = *reinterpret_cast<const uint4*>(q0 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            mx[p] = max2(max2(v[p].x & 0x7fff7fffu, v[p].y & 0x7fff7fffu), max2(v[p].z & 0x7fff7fffu, v[p].w & 0x7fff7fffu));
+            mx[p] = max2(mx[p], mx[p] >> 16);
+          }
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int p = 0; p < U; ++p) mx[p] = max2(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
+#pragma unroll
+          for (int p = 0; p < U; ++p) {
+            const int r = ra + p * kStep;
+            const int e = row_exponent(__uint_as_float(mx[p] << 16));
+            const float down = factor * pow2(e) != 0.f ? pow2(-e) : 0.f;
+            uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+            if (r < rows) {
+              if (c == 0) qexp[(segs & 3) * 256 + r] = (int8_t)e;
+              *reinterpret_cast<uint4*>(q0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        fence_async();
+        warp_arrive(&b.qfull);
+      }
       for (int i2 = 2 * sg.t0; i2 < 2 * sg.t1; ++i2, ++kv) {  // K and V of each tile
         const uint32_t slot = kv % kSlots;
         if (!warp_wait(&b.raw[slot], (kv / kSlots) & 1, abort_flag, a.err)) {
           ok = false;
           break;
         }
-        const uint8_t* src = C::raw(smem, slot);
+        uint8_t* src = C::raw(smem, slot);
         const int k0 = tile_key<kKeys>(a, sg, i2 / 2);
-        const bool check = (i2 & 1) && !all_see_tile(a, sg.p0, sg.p1(), k0, kKeys);
-        uint4 raw[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = r0 + i * (128 / CH);
-          const int at = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
-          raw[i] = *reinterpret_cast<const uint4*>(src + at);
-        }
-        if (check) {
+        auto at = [&](int r) { return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4); };
+        if ((i2 & 1) && sg.partly(i2 / 2)) {
           bool found = false;
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < N; ++i) {
-            const int j = k0 + r0 + i * (128 / CH);
+            const int r = r0 + i * (128 / CH), j = k0 + r;
             if (all_see(a, sg.p0, sg.p1(), j)) continue;
-            const bool any = any_sees(a, sg.p0, sg.p1(), j);
-            uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            const uint32_t any = any_sees(a, sg.p0, sg.p1(), j) ? ~0u : 0u;
+            uint4 x = *reinterpret_cast<const uint4*>(src + at(r));
+            uint32_t* w = &x.x;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // the code 0x7f of either sign
-              found |= any && nan != 0;
-              w[k] = any ? w[k] & ~((nan >> 7) * 0xffu) : 0u;
+              const uint32_t nan = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u & any;  // the code 0x7f of either sign
+              found |= nan != 0;
+              w[k] = w[k] & ~((nan >> 7) * 0xffu) & any;
             }
-            raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(src + at(r)) = x;
           }
           if (found) *(volatile uint8_t*)&b.poison[warp - 12][segs & 15] = 1;
         }
+        uint4 raw[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + at(r0 + i * (128 / CH)));
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
