@@ -76,7 +76,7 @@ __device__ __forceinline__ void store4(void* p, int64_t i, const float (&v)[4]) 
 // BI, BO: logits, out in bf16
 template <bool BI, bool BO>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
-  extern __shared__ uint32_t table[];  // [slice]
+  extern __shared__ __align__(16) uint32_t table[];  // [slice]
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x / a.slices, part = blockIdx.x - t * a.slices, tid = threadIdx.x;
@@ -86,38 +86,6 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   auto complain = [&](int32_t what) {
     if (a.err != nullptr && part == 0) atomicOr(a.err, what);
   };
-  const bool sparse = a.max_history > 0 || a.biases > 0;
-  if (sparse) {
-    for (int i = tid; i < n; i += kThreads) table[i] = 0;
-    __syncthreads();
-    for (int j = tid; j < a.biases; j += kThreads) {
-      const int id = a.bias_ids[(int64_t)t * a.biases + j];
-      if ((unsigned)(id - v0) < (unsigned)n)
-        atomicMax(&table[id - v0], (uint32_t)(j + 1) << kBiasShift);
-      else if (id < -1 || id >= a.V)
-        complain(kErrBadToken);
-    }
-    __syncthreads();
-    if (a.max_history > 0) {
-      const int len = a.history_len[t], all = min(max(len, 0), a.max_history);
-      const int prompt = a.prompt_len != nullptr ? a.prompt_len[t] : 0, made = min(max(prompt, 0), all);
-      if (tid == 0 && (len != all || prompt != made)) complain(kErrBadLength);
-      const int32_t* history = a.history + t * a.history_stride;
-#pragma unroll 4
-      for (int j = tid; j < all; j += kThreads) {
-        const int id = history[j];
-        if ((unsigned)(id - v0) < (unsigned)n) {
-          if (j < made)
-            atomicOr(&table[id - v0], kPrompt);
-          else
-            atomicAdd(&table[id - v0], 1u);
-        } else if (id < 0 || id >= a.V) {
-          complain(kErrBadToken);
-        }
-      }
-    }
-  }
-
   // ---- all of them as they are, or -inf
   const float kOff = -INFINITY;
   if (!a.in_place || mask != nullptr) {
@@ -133,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
       const int b0 = min(v1, v0 + (int)((4 - ((ai + v0) & 3)) & 3)), quads = (v1 - b0) >> 2, b1 = b0 + 4 * quads;
       if (tid < b0 - v0) one(v0 + tid);
       if (tid < v1 - b1) one(b1 + tid);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = tid; i < quads; i += kThreads) {
         const int v = b0 + 4 * i;
         uint32_t on = 15;
@@ -153,18 +121,57 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
         store4<BO>(a.out, out + v, x);
       }
     } else {
-#pragma unroll 4
+#pragma unroll 8
       for (int v = v0 + tid; v < v1; v += kThreads) one(v);
     }
   }
+  // ---- the touched ones: first which
+  const bool sparse = a.max_history > 0 || a.biases > 0;
   if (!sparse) return;
+  {
+    for (int i = tid; i < (n + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int j = tid; j < a.biases; j += kThreads) {
+      const int id = a.bias_ids[(int64_t)t * a.biases + j];
+      if ((unsigned)(id - v0) < (unsigned)n)
+        atomicMax(&table[id - v0], (uint32_t)(j + 1) << kBiasShift);
+      else if (id < -1 || id >= a.V)
+        complain(kErrBadToken);
+    }
+    __syncthreads();
+    if (a.max_history > 0) {
+      const int len = a.history_len[t], all = min(max(len, 0), a.max_history);
+      const int prompt = a.prompt_len != nullptr ? a.prompt_len[t] : 0, made = min(max(prompt, 0), all);
+      if (tid == 0 && (len != all || prompt != made)) complain(kErrBadLength);
+      const int32_t* history = a.history + t * a.history_stride;
+#pragma unroll 8
+      for (int j = tid; j < all; j += kThreads) {
+        const int id = history[j];
+        if ((unsigned)(id - v0) < (unsigned)n) {
+          if (j < made)
+            atomicOr(&table[id - v0], kPrompt);
+          else
+            atomicAdd(&table[id - v0], 1u);
+        } else if (id < 0 || id >= a.V) {
+          complain(kErrBadToken);
+        }
+      }
+    }
+  }
+
   __syncthreads();
 
-  // ---- the touched ones
+  // ---- then what they become
   const float rep = a.repetition != nullptr ? a.repetition[t] : 1.f, freq = a.frequency != nullptr ? a.frequency[t] : 0.f,
               pres = a.presence != nullptr ? a.presence[t] : 0.f;
-  for (int i = tid; i < n; i += kThreads) {
-    const uint32_t e = table[i];
+  for (int i4 = tid; i4 < (n + 3) / 4; i4 += kThreads) {
+    const uint4 four = reinterpret_cast<const uint4*>(table)[i4];
+    if ((four.x | four.y | four.z | four.w) == 0) continue;
+    const uint32_t es[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+    const int i = 4 * i4 + k;
+    const uint32_t e = k == 0 ? es[0] : k == 1 ? es[1] : k == 2 ? es[2] : es[3];
     if (e == 0) continue;
     const int v = v0 + i;
     if (mask != nullptr && !(mask[v >> 5] >> (v & 31) & 1)) continue;
@@ -174,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
     if (times > 0) x = x - freq * (float)times - pres;
     if (e >> kBiasShift) x += a.bias[(int64_t)t * a.biases + (e >> kBiasShift) - 1];
     store1<BO>(a.out, out + v, x);
+    }
   }
 }
 

@@ -8,9 +8,6 @@ namespace chunk {
 
 using namespace attn;
 
-// Empty units at the start of an item, for each kv head: what its start and end cost beside its tiles.
-constexpr int kHead = 2;
-
 struct Args {
   pmoe_kv_desc kv;
   const __nv_bfloat16* q;
@@ -27,6 +24,8 @@ struct Args {
   float* lse;
   int32_t* err;
   int ctas, tile_tokens, few_tokens, part_rows, few;
+  // Empty units at the start of an item, for each kv head: what its start and end cost beside its tiles.
+  int head;
   // scratch
   // Parts of items that a CTA does not take whole: slot 0 where it continues one, slot 1 where it
   // begins one. o: sum of weights x values, ml: (base of the weights' exponents, sum of weights).
@@ -118,7 +117,7 @@ __device__ __forceinline__ int tile_key(const Args& a, const Segment& s, int t) 
   return (t < st ? t : s.lo + t - st) * KEYS;
 }
 
-// Where a CTA's run of units begins. An item has kHead + its key tiles units a kv head, items come
+// Where a CTA's run of units begins. An item has a.head + its key tiles units a kv head, items come
 // request by request.
 struct Run {
   int64_t units, left, u, before;  // all units, the run's, its first one's; rows of the requests up to its first
@@ -210,14 +209,14 @@ struct Walk {
     batch = run.req + 1 - 32;
     some = 0;
     item(a);
-    first = run.u - run.at + kHead;
+    first = run.u - run.at + a.head;
   }
   __device__ __forceinline__ bool next(const Args& a, Segment* s) {
     while (run.left > 0) {
-      const int n = nt + kHead, to = (int)min((int64_t)n, run.at + run.left);
+      const int n = nt + a.head, to = (int)min((int64_t)n, run.at + run.left);
       s->req = run.req, s->tok0 = tok0, s->p0 = p0, s->lo = lo;
-      s->t0 = max(run.at - kHead, 0);
-      s->t1 = max(to - kHead, 0);
+      s->t0 = max(run.at - a.head, 0);
+      s->t1 = max(to - a.head, 0);
       const bool two = ntok * a.group > 128, whole = s->t0 == 0 && s->t1 == nt;
       if (!two && s->t1 > s->t0) lane ^= 1;
       s->bits = ntok | (two ? 1 << 10 : 0) | lane << 11 | (whole ? 1 << 12 : 0) | run.h << 13;

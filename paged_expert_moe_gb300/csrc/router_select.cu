@@ -9,10 +9,13 @@
 // apart lie closer than that, the token is done again in fp64. Where there is no bias the order is
 // the logits' own.
 //
-// Bound: issue slots; a warp a token, its logits in registers, lane l experts l + 32 i. The largest
-// of the warp is found by integer maxima over keys that order like the floats.
+// Bound: issue slots. A warp a token, lane l with the logits l N .. l N + N - 1, so that a group of whole
+// lanes is compared by shuffles, that of equal values the lowest lane's is the lowest id's, and a row is read
+// in whole vectors; the bias stays in registers from token to token. The largest value of the warp is an
+// integer maximum over keys that order like the floats.
 #include "pmoe_internal.h"
 
+#include <algorithm>
 #include <math.h>
 
 namespace pmoe {
@@ -29,6 +32,7 @@ struct SelectArgs {
   float scale;
   int32_t* ids;
   float* w;
+  int lanes;  // of a group, where it is a power of two of whole lanes; else 0
 };
 
 // Keys that order like the values; 0 stands below all of them.
@@ -48,30 +52,6 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
   return (uint64_t)hi << 32 | lo;
 }
 
-// e^x within 2^-21 of its value, x <= 88; below -87: 0
-__device__ __forceinline__ float exp_of(float x) {
-  constexpr float kL = 1.44269504088896f, kRest = 1.92596299e-8f;  // log2(e) and what its float leaves
-  const float y = x * kL, rest = fmaf(x, kRest, fmaf(x, kL, -y));
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-  return x < -87.f ? 0.f : fmaf(r, rest * 0.693147181f, r);
-}
-__device__ __forceinline__ double exp_of(double x) { return exp(x); }
-
-__device__ __forceinline__ float sigmoid(float x) { return x < -87.f ? 0.f : 1.f / (1.f + exp_of(fmaxf(-x, -88.f))); }
-__device__ __forceinline__ double sigmoid(double x) { return 1. / (1. + exp(-x)); }
-
-template <class F>
-struct KeyOf;
-template <>
-struct KeyOf<float> {
-  using T = uint32_t;
-};
-template <>
-struct KeyOf<double> {
-  using T = uint64_t;
-};
-
 // A row's logit: NaN counts as -inf.
 template <bool BF16>
 __device__ __forceinline__ float logit(const SelectArgs& a, int64_t row, int e) {
@@ -83,200 +63,325 @@ __device__ __forceinline__ float logit(const SelectArgs& a, int64_t row, int e) 
   return x != x ? -INFINITY : x;
 }
 
-// Whether c, of score s, may be no larger than d, of score t, given what both may be off by in fp32:
-// sigmoid: 2^-20 of the scores (the exponential 2^-21.5, its sum with 1 and the division 2^-24 each);
-// softmax: 2^-18 (a sum of up to 32 values a lane and 5 exchanges, 2^-24 each); and the sum with the
-// bias, 2^-24 of c and of d.
-__device__ __forceinline__ bool unsure(const SelectArgs& a, float c, float s, float d, float t) {
-  return !(c - d > (a.sigmoid ? 9.5367432e-7f : 3.8146973e-6f) * (s + t) + 1.1920929e-7f * (fabsf(c) + fabsf(d)));
-}
-
-// One token by one warp, in arithmetic F. False: done again in fp64. choice: E values of this warp's
-// in shared memory (groups > 1 only).
-template <class F, int NPL, bool BF16>
-__device__ __forceinline__ bool select_token(const SelectArgs& a, int t, F* choice) {
-  using Key = typename KeyOf<F>::T;
+// One token in fp64, by one warp. choice: E values of this warp's in shared memory (where there are groups).
+template <bool BF16>
+__device__ __noinline__ void select_in_64_bits(const SelectArgs& a, int t, double* choice) {
   const int lane = threadIdx.x & 31;
   const int64_t row = t * a.row_stride;
-  float x[NPL];
+  // lane l takes experts l + 32 i; their keys are worked out again for every pass, which is seldom
   float top = -INFINITY;
+  for (int e = lane; e < a.E; e += 32) top = fmaxf(top, logit<BF16>(a, row, e));
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = lane + 32 * i;
-    x[i] = e < a.E ? logit<BF16>(a, row, e) : -INFINITY;
-    top = fmaxf(top, x[i]);
-  }
-  F inv = 1;  // softmax: 1 / sum
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  double sum = 0;
   if (!a.sigmoid) {
-    top = value_of(warp_max(key_of(top)));
-    F sum = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)  // (logits of +inf, or all of -inf, share the row)
-      if (lane + 32 * i < a.E) sum += x[i] == top ? (F)1 : exp_of((F)x[i] - (F)top);
+    for (int e = lane; e < a.E; e += 32) {
+      const float x = logit<BF16>(a, row, e);
+      sum += x == top ? 1. : exp((double)x - top);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    inv = (F)1 / sum;
   }
-  auto score = [&](float v) -> F {
-    if (a.sigmoid) return sigmoid((F)v);
-    return v == top ? inv : exp_of((F)v - (F)top) * inv;
-  };
-
-  // ---- what decides: c, or the logits themselves
-  const bool by_logits = a.bias == nullptr;
-  Key key[NPL];
-  if (!by_logits || (a.groups > 1 && a.group_top > 1)) {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      key[i] = 0;
-      if (e < a.E) {
-        F c = score(x[i]);
-        if (!by_logits) {
-          const float bias = __ldg(a.bias + e);
-          c += bias;
-          if (c != c) c = -INFINITY;
-        }
-        key[i] = key_of(by_logits ? (F)x[i] : c);
-        if (a.groups > 1) choice[e] = c;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      key[i] = e < a.E ? key_of((F)x[i]) : 0;
-      if (a.groups > 1 && e < a.E) choice[e] = x[i];
-    }
+  auto score = [&](float x) { return a.sigmoid ? 1. / (1. + exp(-(double)x)) : (x == top ? 1. : exp((double)x - top)) / sum; };
+  for (int e = lane; e < a.E; e += 32) {
+    const float x = logit<BF16>(a, row, e);
+    double c = a.bias == nullptr && a.group_top == 1 ? x : score(x);
+    if (a.bias != nullptr) c += a.bias[e];
+    choice[e] = c != c ? -INFINITY : c;
   }
-
-  // ---- the groups: 32 / 2^ceil(log2 groups) lanes each
+  __syncwarp();
+  uint32_t kept = ~0u;
+  const int size = a.E / a.groups;
   if (a.groups > 1) {
-    __syncwarp();
-    int per = 32;
-    while (per * a.groups > 32) per >>= 1;
-    const int g = lane / per, size = a.E / a.groups;
-    F m1 = -INFINITY, m2 = -INFINITY;  // the group's largest two
-    bool one = false;
-    if (g < a.groups) {
-      one = size == 1;
-      for (int i = lane % per; i < size; i += per) {
-        const F c = choice[g * size + i];
+    double value = -INFINITY;  // lane g: of group g
+    if (lane < a.groups) {
+      double m1 = -INFINITY, m2 = -INFINITY;
+      for (int i = 0; i < size; ++i) {
+        const double c = choice[lane * size + i];
         if (c > m1)
           m2 = m1, m1 = c;
         else if (c > m2)
           m2 = c;
       }
+      value = a.group_top > 1 && size > 1 ? m1 + m2 : m1;
+      if (value != value) value = -INFINITY;  // infinities of both signs
     }
-    for (int o = 1; o < per; o <<= 1) {
-      const F n1 = __shfl_xor_sync(0xffffffffu, m1, o), n2 = __shfl_xor_sync(0xffffffffu, m2, o);
-      m2 = fmax(fmin(m1, n1), fmax(m2, n2));
-      m1 = fmax(m1, n1);
-    }
-    F value = a.group_top > 1 && !one ? m1 + m2 : m1;
-    if (value != value) value = -INFINITY;  // infinities of both signs
-    // its rank among the groups; of equal ones the first is better
     int rank = 0;
     for (int k = 0; k < a.groups; ++k) {
-      const F other = __shfl_sync(0xffffffffu, value, k * per);
-      if (other > value || (other == value && k < g)) ++rank;
+      const double other = __shfl_sync(0xffffffffu, value, k);
+      if (other > value || (other == value && k < lane)) ++rank;
     }
-    const bool in = g < a.groups && rank < a.top_groups;
-    if (sizeof(F) == 4 && !(by_logits && a.group_top == 1)) {
-      // the worst that is kept against the best that is not, as sums of two scores of at most 1
-      const uint32_t worst = ~warp_max(in ? ~key_of((float)value) : 0u);
-      const uint32_t best = warp_max(g < a.groups && !in ? key_of((float)value) : 0u);
-      if (best != 0) {
-        if (unsure(a, value_of(worst), 2.f, value_of(best), 2.f)) return false;
-      }
-    }
-    const uint32_t kept = __ballot_sync(0xffffffffu, in);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E && !(kept >> (e / size * per) & 1)) key[i] = 0;
-    }
-    __syncwarp();  // choice may be written for the next token
+    kept = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
   }
-
-  // ---- the top_k largest, one more to see how sure the last is; lane r keeps the r-th
-  Key mine = 0;
-  int id = 0;
-  const bool check = sizeof(F) == 4 && !by_logits;
-  const int rounds = a.top_k + (check ? 1 : 0);
-  Key last = 0;
-  for (int r = 0; r < rounds; ++r) {
-    Key best = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) best = key[i] > best ? key[i] : best;
-    const Key all = warp_max(best);
-    int e = 0x7fffffff;
-    if (best == all) {
-#pragma unroll
-      for (int i = NPL - 1; i >= 0; --i)
-        if (key[i] == all) e = lane + 32 * i;
+  // (the logits themselves decide where there is no bias)
+  auto key = [&](int e) -> uint64_t {
+    if (a.groups > 1 && !(kept >> (e / size) & 1)) return 0;
+    return key_of(a.bias != nullptr ? choice[e] : (double)logit<BF16>(a, row, e));
+  };
+  uint64_t bound = ~0ull;  // the last one taken: key and id
+  int bound_id = -1, id = 0;
+  for (int r = 0; r < a.top_k; ++r) {
+    uint64_t best = 0;
+    int at = 0x7fffffff;
+    for (int e = lane; e < a.E; e += 32) {
+      const uint64_t k = key(e);
+      if (k > best && (k < bound || (k == bound && e > bound_id))) best = k, at = e;
     }
-    e = (int)__reduce_min_sync(0xffffffffu, (uint32_t)e);
-    if ((e & 31) == lane) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (e == lane + 32 * i) key[i] = 0;
-    }
-    if (lane == r) mine = all, id = e;
-    last = all;
+    const uint64_t all = warp_max(best);
+    at = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(best == all ? at : 0x7fffffff));
+    bound = all, bound_id = at;
+    if (lane == r) id = at;
   }
-  const F s = lane < rounds && mine != 0 ? score(logit<BF16>(a, row, id)) : (F)0;
-  if (check) {
-    // neighbours in the order, the last against the one after it
-    const float c = value_of((uint32_t)mine);
-    float d = __shfl_down_sync(0xffffffffu, c, 1), u = __shfl_down_sync(0xffffffffu, (float)s, 1);
-    if (lane == 31) d = value_of((uint32_t)last), u = 1.f;  // (of 33; some score)
-    const bool pair = lane + 1 < a.top_k || (lane + 1 == a.top_k && last != 0);
-    if (__any_sync(0xffffffffu, pair && unsure(a, c, (float)s, d, u))) return false;
-  }
-  F w = s;
+  const double s = lane < a.top_k ? score(logit<BF16>(a, row, id)) : 0.;
+  double w = s;
   if (a.renorm) {
-    F sum = lane < a.top_k ? s : (F)0;
+    double total = s;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (sizeof(F) == 4 && sum < 1e-30f) return false;  // scores that fp32 does not hold
-    w = sum > 0 ? s / sum : (F)0;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    w = total > 0 ? s / total : 0.;
   }
   if (lane < a.top_k) {
     a.ids[(int64_t)t * a.top_k + lane] = id;
-    a.w[(int64_t)t * a.top_k + lane] = (float)(w * (F)a.scale);
+    a.w[(int64_t)t * a.top_k + lane] = (float)(w * a.scale);
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// N values of a row from element i on; beyond `n` and NaN: -inf. VEC: whole vectors.
+template <int N, bool BF16, bool VEC>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int i, int n, float (&x)[N]) {
+  if constexpr (VEC && BF16 && N % 2 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + row + i);
+    uint32_t v[N / 2];
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+      for (int k = 0; k < N / 8; ++k) *reinterpret_cast<uint4*>(v + 4 * k) = __ldg(reinterpret_cast<const uint4*>(w) + k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) v[k] = __ldg(w + k);
+    }
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) x[2 * k] = __uint_as_float(v[k] << 16), x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+  } else if constexpr (VEC && !BF16 && N % 4 == 0) {
+    const float4* w = reinterpret_cast<const float4*>(static_cast<const float*>(p) + row + i);
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      const float4 f = __ldg(w + k);
+      x[4 * k] = f.x, x[4 * k + 1] = f.y, x[4 * k + 2] = f.z, x[4 * k + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      x[k] = -INFINITY;
+      if (i + k < n) {
+        if constexpr (BF16)
+          x[k] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + row + i + k) << 16);
+        else
+          x[k] = __ldg(static_cast<const float*>(p) + row + i + k);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = fmaxf(x[k], -INFINITY);  // (NaN: the other operand)
+}
+
+// One token in fp32 by one warp; false: not sure. bias: this lane's. choice, list: of this warp, in shared memory.
+template <int N, bool BF16, bool VEC>
+__device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const float (&bias)[N], float* choice, uint2* list) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = t * a.row_stride;
+  float x[N];
+  load_row<N, BF16, VEC>(a.logits, row, lane * N, a.E, x);
+  // softmax: the largest logit and 1 / the sum of the exponentials. Logits of +inf, or all of -inf, share the row.
+  float top = 0.f, inv = 1.f;
+  if (!a.sigmoid) {
+    top = x[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) top = fmaxf(top, x[k]);
+    top = value_of(warp_max(key_of(top)));
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (lane * N + k < a.E) sum += x[k] == top ? 1.f : ex2((x[k] - top) * kLog2e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    inv = 1.f / sum;
+  }
+  auto score = [&](float v) {
+    if (a.sigmoid) return rcp(1.f + ex2(fmaxf(v, -200.f) * -kLog2e));
+    return v == top ? inv : ex2((v - top) * kLog2e) * inv;
+  };
+  // What two values of scores s and t, c and d with the bias, may be off by together. Sigmoid: a score 2^-22
+  // (the exponential's argument |x| 2^-23.7 of it and it itself 2^-22, times s (1 - s) <= 1/4 and |x| s (1 - s) <=
+  // 0.23; sum and reciprocal 2^-22.4). Softmax: the sum and its reciprocal 2^-18.8 of a score (up to 32 terms a lane and 5
+  // exchanges, 2^-24 each, and the exponentials), the exponential's argument |x - top| 2^-23.3 of it, of which
+  // |x - top| exp(x - top) <= 0.37. And 2^-24 of c and of d.
+  auto unsure = [&](float c, float s, float d, float u) {
+    const float tol = a.sigmoid ? 7e-7f : 3.8146973e-6f * (s + u) + 2.3841858e-7f * inv;
+    return !(c - d > tol + 1.1920929e-7f * (fabsf(c) + fabsf(d)));
+  };
+
+  // ---- what decides: c, or without a bias the logits themselves
+  const bool by_logits = a.bias == nullptr, scored = !by_logits || (a.groups > 1 && a.group_top > 1);
+  uint32_t key[N], group_key[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float c = scored ? fmaxf(score(x[k]) + bias[k], -INFINITY) : x[k] + 0.f;
+    group_key[k] = lane * N + k < a.E ? key_of(c) : 0;
+    key[k] = by_logits && scored && group_key[k] != 0 ? key_of(x[k] + 0.f) : group_key[k];
+  }
+
+  // ---- the groups
+  if (a.groups > 1) {
+    const int size = a.E / a.groups;
+    uint32_t m1 = 0, m2 = 0;  // the two largest of a group
+    int g, per;               // this lane's group, lanes of a group
+    if (a.lanes > 0) {        // groups of whole lanes, a power of two of them
+      g = lane / a.lanes, per = a.lanes;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        m2 = max(m2, min(m1, group_key[k]));
+        m1 = max(m1, group_key[k]);
+      }
+    } else {  // by way of shared memory
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (lane * N + k < a.E) choice[lane * N + k] = value_of(group_key[k]);
+      __syncwarp();
+      per = 32;
+      while (per * a.groups > 32) per >>= 1;
+      g = lane / per;
+      if (g < a.groups)
+        for (int i = lane % per; i < size; i += per) {
+          const uint32_t c = key_of(choice[g * size + i]);
+          m2 = max(m2, min(m1, c));
+          m1 = max(m1, c);
+        }
+      __syncwarp();
+    }
+    for (int o = 1; o < per; o <<= 1) {
+      const uint32_t n1 = __shfl_xor_sync(0xffffffffu, m1, o), n2 = __shfl_xor_sync(0xffffffffu, m2, o);
+      m2 = max(min(m1, n1), max(m2, n2));
+      m1 = max(m1, n1);
+    }
+    float value = a.group_top > 1 && size > 1 ? value_of(m1) + value_of(m2) : value_of(m1);
+    value = fmaxf(value, -INFINITY);  // (infinities of both signs)
+    int rank = 0;  // of equal groups the first is better
+    for (int k = 0; k < a.groups; ++k) {
+      const float other = __shfl_sync(0xffffffffu, value, k * per);
+      rank += other > value || (other == value && k < g);
+    }
+    const bool in = g < a.groups && rank < a.top_groups;
+    if (scored) {
+      // the worst that is kept against the best that is not: sums of two scores of at most 1 each
+      const uint32_t worst = ~warp_max(in ? ~key_of(value) : 0u), best = warp_max(g < a.groups && !in ? key_of(value) : 0u);
+      if (unsure(value_of(worst) - (a.sigmoid ? 7e-7f : 0.f), 2.f, value_of(best), 2.f)) return false;
+    }
+    const uint32_t kept = __ballot_sync(0xffffffffu, in);
+    if (a.lanes > 0) {
+      if (!in) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) key[k] = 0;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (lane * N + k < a.E && !(kept >> ((lane * N + k) / size * per) & 1)) key[k] = 0;
+    }
+  }
+
+  // ---- the top_k largest, and with scores one more to see how sure the last is
+  const bool check = !by_logits;
+  const int rounds = a.top_k + (check ? 1 : 0);
+  uint32_t best = key[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k) best = max(best, key[k]);
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    const uint32_t all = warp_max(best);
+    const int from = __ffs(__ballot_sync(0xffffffffu, best == all)) - 1;  // (of equal ones the lowest lane, and below its first)
+    if (lane == from) {
+      int at = -1;
+      best = 0;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (at < 0 && key[k] == all)
+          at = k, key[k] = 0;
+        best = max(best, key[k]);
+      }
+      list[r] = make_uint2(all, lane * N + at);
+    }
+  }
+  __syncwarp();
+  const uint2 mine = lane < rounds ? list[lane] : make_uint2(0, 0);
+  const float s = mine.x != 0 ? score(logit<BF16>(a, row, mine.y)) : 0.f;
+  if (check) {
+    // neighbours in the order, the last against the one after it
+    const float c = value_of(mine.x);
+    const uint32_t last = list[a.top_k].x;
+    float d = __shfl_down_sync(0xffffffffu, c, 1), u = __shfl_down_sync(0xffffffffu, s, 1);
+    if (lane == 31) d = value_of(last), u = 1.f;  // (of 33; some score)
+    const bool pair = lane + 1 < a.top_k || (lane + 1 == a.top_k && last != 0);
+    if (__any_sync(0xffffffffu, pair && unsure(c, s, d, u))) return false;
+  }
+  __syncwarp();  // list may be written for the next token
+  float w = s;
+  if (a.renorm) {
+    float sum = lane < a.top_k ? s : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (sum < 1e-30f) return false;  // scores that fp32 does not hold
+    w = __fdividef(s, sum);
+  }
+  if (lane < a.top_k) {
+    a.ids[(int64_t)t * a.top_k + lane] = mine.y;
+    a.w[(int64_t)t * a.top_k + lane] = w * a.scale;
   }
   return true;
 }
 
-template <int NPL, bool BF16>
-__device__ __noinline__ void select_in_64_bits(const SelectArgs& a, int t, double* choice) {
-  select_token<double, NPL, BF16>(a, t, choice);
-}
-
-template <int NPL, bool BF16>
+template <int N, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a) {
-  extern __shared__ double choices[];  // [kWarps][E] where there are groups
+  extern __shared__ double choices[];  // [kWarps][E]
+  __shared__ uint2 lists[kWarps][kMaxTopK + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kWarps + warp;
-  if (t >= a.T) return;
+  float bias[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) bias[k] = a.bias != nullptr && lane * N + k < a.E ? __ldg(a.bias + lane * N + k) : 0.f;
   double* mine = choices + (size_t)warp * a.E;
-  if (!select_token<float, NPL, BF16>(a, t, reinterpret_cast<float*>(mine))) select_in_64_bits<NPL, BF16>(a, t, mine);
+  for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps)
+    if (!select_token<N, BF16, VEC>(a, t, bias, reinterpret_cast<float*>(mine), lists[warp])) select_in_64_bits<BF16>(a, t, mine);
 }
 
 template <bool BF16>
-int launch_select(const SelectArgs& a, cudaStream_t s) {
+int launch_select(SelectArgs a, cudaStream_t s) {
   const int npl = (a.E + 31) / 32;
-  const unsigned blocks = (unsigned)((a.T + kWarps - 1) / kWarps);
-  const size_t smem = a.groups > 1 ? (size_t)kWarps * a.E * 8 : 0;
-#define PMOE_SELECT_CASE(N)                                                                                             \
-  do {                                                                                                                  \
-    static SmemLimit limit;                                                                                             \
-    const int r = limit.set(reinterpret_cast<const void*>(select_kernel<N, BF16>), kWarps * N * 32 * 8, "moe_router_select"); \
-    return r != PMOE_OK ? r                                                                                             \
-                        : launch("moe_router_select", select_kernel<N, BF16>, blocks, kWarps * 32, smem, s, true, 1, a); \
+  const size_t smem = (size_t)kWarps * a.E * 8;
+  const char* what = "moe_router_select";
+#define PMOE_SELECT_CASE(N)                                                                                               \
+  do {                                                                                                                    \
+    static SmemLimit limits[2];                                                                                           \
+    const bool vec = a.E == 32 * N && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * (BF16 ? 2 : 4) % 16 == 0; \
+    const int size = a.E / a.groups;                                                                                      \
+    a.lanes = size % N == 0 && (size / N & (size / N - 1)) == 0 ? size / N : 0;                                           \
+    const auto kernel = vec ? select_kernel<N, BF16, true> : select_kernel<N, BF16, false>;                               \
+    const int r = limits[vec].set(reinterpret_cast<const void*>(kernel), kWarps * N * 32 * 8, what);                      \
+    const unsigned blocks = (unsigned)std::min((a.T + kWarps - 1) / kWarps, 152 * 6);                                     \
+    return r != PMOE_OK ? r : launch(what, kernel, blocks, kWarps * 32, smem, s, true, 1, a);                             \
   } while (0)
   if (npl <= 1) PMOE_SELECT_CASE(1);
   if (npl <= 2) PMOE_SELECT_CASE(2);
@@ -305,6 +410,6 @@ extern "C" int moe_router_select(const void* logits, int is_bf16, int T, int E, 
   if (off(logits, is_bf16 ? 2 : 4) || (bias != nullptr && off(bias, 4)) || off(ids_out, 4) || off(w_out, 4)) return PMOE_EINVAL;
   const bool grouped = groups > 1 && top_groups < groups;  // all groups kept: no choice among them
   const SelectArgs a{logits, row_stride, T, E, top_k, scoring == PMOE_SCORE_SIGMOID, bias, grouped ? groups : 1,
-                     grouped ? top_groups : 1, group_top, renormalize != 0, scale, ids_out, w_out};
+                     grouped ? top_groups : 1, group_top, renormalize != 0, scale, ids_out, w_out, 0};
   return is_bf16 ? launch_select<true>(a, (cudaStream_t)stream) : launch_select<false>(a, (cudaStream_t)stream);
 }
