@@ -51,16 +51,28 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
   else
     static_cast<float*>(p)[i] = v;
 }
+// Four values as they lie in memory.
 template <bool BF16>
-__device__ __forceinline__ void load4(const void* p, int64_t i, float (&v)[4]) {
-  if constexpr (BF16) {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+struct Quad;
+template <>
+struct Quad<true> {
+  uint2 u;
+  __device__ __forceinline__ void get(float (&v)[4]) const {
     v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
     v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xffff0000u);
-  } else {
-    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
   }
+};
+template <>
+struct Quad<false> {
+  float4 f;
+  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w; }
+};
+template <bool BF16>
+__device__ __forceinline__ Quad<BF16> load4(const void* p, int64_t i) {
+  if constexpr (BF16)
+    return {*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i)};
+  else
+    return {*reinterpret_cast<const float4*>(static_cast<const float*>(p) + i)};
 }
 template <bool BF16>
 __device__ __forceinline__ void store4(void* p, int64_t i, const float (&v)[4]) {
@@ -101,24 +113,36 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
       const int b0 = min(v1, v0 + (int)((4 - ((ai + v0) & 3)) & 3)), quads = (v1 - b0) >> 2, b1 = b0 + 4 * quads;
       if (tid < b0 - v0) one(v0 + tid);
       if (tid < v1 - b1) one(b1 + tid);
-#pragma unroll 8
-      for (int i = tid; i < quads; i += kThreads) {
-        const int v = b0 + 4 * i;
-        uint32_t on = 15;
-        if (mask != nullptr) {
-          // 4 bits from v on, of one word or two
-          const int w = v >> 5, s = v & 31;
-          on = mask[w] >> s;
-          if (s > 28) on |= mask[w + 1] << (32 - s);
-          on &= 15;
-        }
-        if (on == 15 && a.in_place) continue;
-        float x[4] = {kOff, kOff, kOff, kOff};
-        if (on != 0) load4<BI>(a.logits, in + v, x);
+      constexpr int U = 8;  // in flight
+      for (int i0 = tid; i0 < quads; i0 += U * kThreads) {
+        uint32_t on[U];
+        Quad<BI> x[U];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (!(on >> k & 1)) x[k] = kOff;
-        store4<BO>(a.out, out + v, x);
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * kThreads, v = b0 + 4 * i;
+          on[u] = 15;
+          if (mask != nullptr && i < quads) {
+            // 4 bits from v on, of one word or two
+            const int w = v >> 5, s = v & 31;
+            on[u] = mask[w] >> s;
+            if (s > 28) on[u] |= mask[w + 1] << (32 - s);
+            on[u] &= 15;
+          }
+          if (i >= quads) on[u] = 16;  // none
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (on[u] - 1 < (a.in_place ? 14u : 15u)) x[u] = load4<BI>(a.logits, in + b0 + 4 * (i0 + u * kThreads));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (on[u] == 16 || (on[u] == 15 && a.in_place)) continue;
+          float f[4] = {kOff, kOff, kOff, kOff};
+          if (on[u] != 0) x[u].get(f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!(on[u] >> k & 1)) f[k] = kOff;
+          store4<BO>(a.out, out + b0 + 4 * (i0 + u * kThreads), f);
+        }
       }
     } else {
 #pragma unroll 8
@@ -128,37 +152,34 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   // ---- the touched ones: first which
   const bool sparse = a.max_history > 0 || a.biases > 0;
   if (!sparse) return;
-  {
-    for (int i = tid; i < (n + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    for (int j = tid; j < a.biases; j += kThreads) {
-      const int id = a.bias_ids[(int64_t)t * a.biases + j];
-      if ((unsigned)(id - v0) < (unsigned)n)
-        atomicMax(&table[id - v0], (uint32_t)(j + 1) << kBiasShift);
-      else if (id < -1 || id >= a.V)
-        complain(kErrBadToken);
-    }
-    __syncthreads();
-    if (a.max_history > 0) {
-      const int len = a.history_len[t], all = min(max(len, 0), a.max_history);
-      const int prompt = a.prompt_len != nullptr ? a.prompt_len[t] : 0, made = min(max(prompt, 0), all);
-      if (tid == 0 && (len != all || prompt != made)) complain(kErrBadLength);
-      const int32_t* history = a.history + t * a.history_stride;
+  for (int i = tid; i < (n + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  for (int j = tid; j < a.biases; j += kThreads) {
+    const int id = a.bias_ids[(int64_t)t * a.biases + j];
+    if ((unsigned)(id - v0) < (unsigned)n)
+      atomicMax(&table[id - v0], (uint32_t)(j + 1) << kBiasShift);
+    else if (id < -1 || id >= a.V)
+      complain(kErrBadToken);
+  }
+  __syncthreads();
+  if (a.max_history > 0) {
+    const int len = a.history_len[t], all = min(max(len, 0), a.max_history);
+    const int prompt = a.prompt_len != nullptr ? a.prompt_len[t] : 0, made = min(max(prompt, 0), all);
+    if (tid == 0 && (len != all || prompt != made)) complain(kErrBadLength);
+    const int32_t* history = a.history + t * a.history_stride;
 #pragma unroll 8
-      for (int j = tid; j < all; j += kThreads) {
-        const int id = history[j];
-        if ((unsigned)(id - v0) < (unsigned)n) {
-          if (j < made)
-            atomicOr(&table[id - v0], kPrompt);
-          else
-            atomicAdd(&table[id - v0], 1u);
-        } else if (id < 0 || id >= a.V) {
-          complain(kErrBadToken);
-        }
+    for (int j = tid; j < all; j += kThreads) {
+      const int id = history[j];
+      if ((unsigned)(id - v0) < (unsigned)n) {
+        if (j < made)
+          atomicOr(&table[id - v0], kPrompt);
+        else
+          atomicAdd(&table[id - v0], 1u);
+      } else if (id < 0 || id >= a.V) {
+        complain(kErrBadToken);
       }
     }
   }
-
   __syncthreads();
 
   // ---- then what they become
@@ -168,19 +189,23 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
     const uint4 four = reinterpret_cast<const uint4*>(table)[i4];
     if ((four.x | four.y | four.z | four.w) == 0) continue;
     const uint32_t es[4] = {four.x, four.y, four.z, four.w};
-#pragma unroll 1
+    const int v = v0 + 4 * i4;
+    bool on[4];
+    float x[4];
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-    const int i = 4 * i4 + k;
-    const uint32_t e = k == 0 ? es[0] : k == 1 ? es[1] : k == 2 ? es[2] : es[3];
-    if (e == 0) continue;
-    const int v = v0 + i;
-    if (mask != nullptr && !(mask[v >> 5] >> (v & 31) & 1)) continue;
-    float x = load1<BI>(a.logits, in + v);
-    const uint32_t times = e & kCount;
-    if (e & (kCount | kPrompt)) x = x > 0.f ? x / rep : x * rep;
-    if (times > 0) x = x - freq * (float)times - pres;
-    if (e >> kBiasShift) x += a.bias[(int64_t)t * a.biases + (e >> kBiasShift) - 1];
-    store1<BO>(a.out, out + v, x);
+      on[k] = es[k] != 0 && (mask == nullptr || (mask[(v + k) >> 5] >> ((v + k) & 31) & 1));
+      if (on[k]) x[k] = load1<BI>(a.logits, in + v + k);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!on[k]) continue;
+      const uint32_t times = es[k] & kCount;
+      float y = x[k];
+      if (es[k] & (kCount | kPrompt)) y = y > 0.f ? y / rep : y * rep;
+      if (times > 0) y = y - freq * (float)times - pres;
+      if (es[k] >> kBiasShift) y += a.bias[(int64_t)t * a.biases + (es[k] >> kBiasShift) - 1];
+      store1<BO>(a.out, out + v + k, y);
     }
   }
 }

@@ -147,6 +147,32 @@ __device__ __noinline__ void select_in_64_bits(const SelectArgs& a, int t, doubl
   __syncwarp();
 }
 
+// c of expert e in fp64, with sigmoid scores.
+template <bool BF16>
+__device__ __forceinline__ double exact_choice(const SelectArgs& a, int64_t row, int e) {
+  double c = 1. / (1. + exp(-(double)logit<BF16>(a, row, e)));
+  if (a.bias != nullptr) c += a.bias[e];
+  return c != c ? -INFINITY : c;
+}
+
+// Batcher's odd-even merge sort.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t x = v[i + j], y = v[i + j + k];
+            v[i + j] = max(x, y);
+            v[i + j + k] = min(x, y);
+          }
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -197,9 +223,11 @@ __device__ __forceinline__ void load_row(const void* p, int64_t row, int i, int 
   for (int k = 0; k < N; ++k) x[k] = fmaxf(x[k], -INFINITY);  // (NaN: the other operand)
 }
 
-// One token in fp32 by one warp; false: not sure. bias: this lane's. choice, list: of this warp, in shared memory.
+// One token in fp32 by one warp; false: not sure. bias: this lane's. choice [E] and lane_keys [32 N], one after the
+// other in the same place, and list [33]: of this warp, in shared memory.
 template <int N, bool BF16, bool VEC>
-__device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const float (&bias)[N], float* choice, uint2* list) {
+__device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const float (&bias)[N], float* choice, uint32_t* lane_keys,
+                                             uint2* list) {
   const int lane = threadIdx.x & 31;
   const int64_t row = t * a.row_stride;
   float x[N];
@@ -283,11 +311,57 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
       const float other = __shfl_sync(0xffffffffu, value, k * per);
       rank += other > value || (other == value && k < g);
     }
-    const bool in = g < a.groups && rank < a.top_groups;
+    bool in = g < a.groups && rank < a.top_groups;
     if (scored) {
       // the worst that is kept against the best that is not: sums of two scores of at most 1 each
       const uint32_t worst = ~warp_max(in ? ~key_of(value) : 0u), best = warp_max(g < a.groups && !in ? key_of(value) : 0u);
-      if (unsure(value_of(worst) - (a.sigmoid ? 7e-7f : 0.f), 2.f, value_of(best), 2.f)) return false;
+      if (unsure(value_of(worst) - (a.sigmoid ? 7e-7f : 0.f), 2.f, value_of(best), 2.f)) {
+        if (!a.sigmoid) return false;
+        // each group's two largest in fp64: those that come near its second, one a lane
+        const float near = value_of(m2) - 1.5e-6f - 2.5e-7f * fabsf(value_of(m2));
+        int n = 0;
+#pragma unroll 1
+        for (int k = 0; k < N; ++k) {
+          float c = 0.f;
+          int group = -1;
+          const int e = lane * N + k;
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (j == k) c = value_of(group_key[j]);
+          if (e < a.E) group = e / size;
+          const float bound = __shfl_sync(0xffffffffu, near, max(group, 0) * per);
+          const uint32_t takes = __ballot_sync(0xffffffffu, group >= 0 && !(c < bound));
+          const int at = n + __popc(takes & ((1u << lane) - 1));
+          if (takes >> lane & 1 && at < 32) list[at].y = e;
+          n += __popc(takes);
+        }
+        __syncwarp();
+        if (n > 32) return false;
+        const int e = lane < n ? list[lane].y : 0, group = lane < n ? e / size : -1;
+        const double c = exact_choice<BF16>(a, row, e);
+        double d1 = -INFINITY, d2 = -INFINITY;  // lane i: of group i
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+          const double other = __shfl_sync(0xffffffffu, c, k);
+          if (__shfl_sync(0xffffffffu, group, k) == lane) {
+            if (other > d1)
+              d2 = d1, d1 = other;
+            else if (other > d2)
+              d2 = other;
+          }
+        }
+        double sum = a.group_top > 1 && size > 1 ? d1 + d2 : d1;
+        if (sum != sum) sum = -INFINITY;
+        int place = 0;
+#pragma unroll 1
+        for (int k = 0; k < a.groups; ++k) {
+          const double other = __shfl_sync(0xffffffffu, sum, k);
+          place += other > sum || (other == sum && k < lane);
+        }
+        const uint32_t best_groups = __ballot_sync(0xffffffffu, lane < a.groups && place < a.top_groups);
+        in = g < a.groups && (best_groups >> g & 1);
+        __syncwarp();
+      }
     }
     const uint32_t kept = __ballot_sync(0xffffffffu, in);
     if (a.lanes > 0) {
@@ -305,36 +379,73 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
   // ---- the top_k largest, and with scores one more to see how sure the last is
   const bool check = !by_logits;
   const int rounds = a.top_k + (check ? 1 : 0);
-  uint32_t best = key[0];
+  // a lane's keys in descending order, its largest against the other lanes'; which expert a key is of is
+  // looked up at the end
 #pragma unroll
-  for (int k = 1; k < N; ++k) best = max(best, key[k]);
-#pragma unroll 1
-  for (int r = 0; r < rounds; ++r) {
-    const uint32_t all = warp_max(best);
-    const int from = __ffs(__ballot_sync(0xffffffffu, best == all)) - 1;  // (of equal ones the lowest lane, and below its first)
+  for (int k = 0; k < N; ++k) lane_keys[lane * N + k] = key[k];
+  sort_descending<N>(key);
+  uint32_t last = 0;
+  int n = 0;  // of the list
+  auto take = [&]() {
+    last = warp_max(key[0]);
+    const int from = __ffs(__ballot_sync(0xffffffffu, key[0] == last)) - 1;  // (of equal ones the lowest lane)
     if (lane == from) {
-      int at = -1;
-      best = 0;
+      list[n] = make_uint2(last, lane);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (at < 0 && key[k] == all)
-          at = k, key[k] = 0;
-        best = max(best, key[k]);
-      }
-      list[r] = make_uint2(all, lane * N + at);
+      for (int k = 0; k + 1 < N; ++k) key[k] = key[k + 1];
+      key[N - 1] = 0;
     }
-  }
-  __syncwarp();
-  const uint2 mine = lane < rounds ? list[lane] : make_uint2(0, 0);
-  const float s = mine.x != 0 ? score(logit<BF16>(a, row, mine.y)) : 0.f;
+    ++n;
+  };
+#pragma unroll 1
+  while (n < rounds) take();
+  uint2 mine;
+  float s, c;
+  int id;
+  auto look = [&]() {  // lane i: the i-th of the list
+    __syncwarp();
+    mine = lane < n ? list[lane] : make_uint2(0, lane);
+    // of equal keys of one lane the first is the lower id's
+    const uint32_t same = __match_any_sync(0xffffffffu, (uint64_t)mine.y << 32 | mine.x);
+    int skip = __popc(same & ((1u << lane) - 1));
+    id = 0;
+    const uint32_t* keys = lane_keys + mine.y * N;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const bool hit = keys[k] == mine.x;
+      if (hit && skip-- == 0) id = mine.y * N + k;
+    }
+    s = mine.x != 0 ? score(logit<BF16>(a, row, id)) : 0.f;
+    c = value_of(mine.x);
+  };
+  look();
   if (check) {
     // neighbours in the order, the last against the one after it
-    const float c = value_of(mine.x);
-    const uint32_t last = list[a.top_k].x;
     float d = __shfl_down_sync(0xffffffffu, c, 1), u = __shfl_down_sync(0xffffffffu, s, 1);
     if (lane == 31) d = value_of(last), u = 1.f;  // (of 33; some score)
     const bool pair = lane + 1 < a.top_k || (lane + 1 == a.top_k && last != 0);
-    if (__any_sync(0xffffffffu, pair && unsure(c, s, d, u))) return false;
+    if (__any_sync(0xffffffffu, pair && unsure(c, s, d, u))) {
+      if (!a.sigmoid || a.top_k > 30) return false;
+      // the list in fp64, and with it all that come near its end; one a lane, sorted by rank
+      float end = __shfl_sync(0xffffffffu, c, a.top_k - 1);
+      end -= 1.5e-6f + 2.5e-7f * fabsf(end);
+      while (n < 32 && last != 0 && !(value_of(last) < end)) take();
+      if (n == 32) return false;
+      look();
+      const bool there = mine.x != 0;
+      const double exact = there ? exact_choice<BF16>(a, row, id) : 0.;
+      int place = 0;
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
+        const double other = __shfl_sync(0xffffffffu, exact, k);
+        const int other_id = __shfl_sync(0xffffffffu, id, k), other_there = __shfl_sync(0xffffffffu, (int)there, k);
+        place += other_there && (other > exact || (other == exact && other_id < id));
+      }
+      __syncwarp();
+      if (there && place < a.top_k) list[place] = make_uint2(__float_as_uint(s), id);
+      __syncwarp();
+      if (lane < a.top_k) s = __uint_as_float(list[lane].x), id = list[lane].y;
+    }
   }
   __syncwarp();  // list may be written for the next token
   float w = s;
@@ -346,7 +457,7 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
     w = __fdividef(s, sum);
   }
   if (lane < a.top_k) {
-    a.ids[(int64_t)t * a.top_k + lane] = mine.y;
+    a.ids[(int64_t)t * a.top_k + lane] = id;
     a.w[(int64_t)t * a.top_k + lane] = w * a.scale;
   }
   return true;
@@ -354,7 +465,7 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
 
 template <int N, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a) {
-  extern __shared__ double choices[];  // [kWarps][E]
+  extern __shared__ double choices[];  // [kWarps][32 N]
   __shared__ uint2 lists[kWarps][kMaxTopK + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
@@ -362,15 +473,15 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a)
   float bias[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) bias[k] = a.bias != nullptr && lane * N + k < a.E ? __ldg(a.bias + lane * N + k) : 0.f;
-  double* mine = choices + (size_t)warp * a.E;
+  double* mine = choices + (size_t)warp * 32 * N;
   for (int t = blockIdx.x * kWarps + warp; t < a.T; t += gridDim.x * kWarps)
-    if (!select_token<N, BF16, VEC>(a, t, bias, reinterpret_cast<float*>(mine), lists[warp])) select_in_64_bits<BF16>(a, t, mine);
+    if (!select_token<N, BF16, VEC>(a, t, bias, reinterpret_cast<float*>(mine), reinterpret_cast<uint32_t*>(mine),
+                                     lists[warp])) select_in_64_bits<BF16>(a, t, mine);
 }
 
 template <bool BF16>
 int launch_select(SelectArgs a, cudaStream_t s) {
   const int npl = (a.E + 31) / 32;
-  const size_t smem = (size_t)kWarps * a.E * 8;
   const char* what = "moe_router_select";
 #define PMOE_SELECT_CASE(N)                                                                                               \
   do {                                                                                                                    \
@@ -381,7 +492,7 @@ int launch_select(SelectArgs a, cudaStream_t s) {
     const auto kernel = vec ? select_kernel<N, BF16, true> : select_kernel<N, BF16, false>;                               \
     const int r = limits[vec].set(reinterpret_cast<const void*>(kernel), kWarps * N * 32 * 8, what);                      \
     const unsigned blocks = (unsigned)std::min((a.T + kWarps - 1) / kWarps, 152 * 6);                                     \
-    return r != PMOE_OK ? r : launch(what, kernel, blocks, kWarps * 32, smem, s, true, 1, a);                             \
+    return r != PMOE_OK ? r : launch(what, kernel, blocks, kWarps * 32, kWarps * N * 32 * 8, s, true, 1, a);                            \
   } while (0)
   if (npl <= 1) PMOE_SELECT_CASE(1);
   if (npl <= 2) PMOE_SELECT_CASE(2);
