@@ -1,12 +1,12 @@
 // moe_adjust_logits: penalties for repeated tokens, biases and grammar masks on logits.
 //
-// A row's history touches few of its V logits, so the row is copied as it is (or left in place) with
-// the masked ones set to -inf, and the touched ones are worked out after that. Which those are, and
-// how often each occurs, is counted in shared memory: a CTA takes a slice of the ids of one row, one
-// word an id, and reads the row's whole history, of which it counts what falls into its slice. The
-// counts are whole numbers, so their order does not matter.
+// A row's history touches few of its V logits. Which, and how often each occurs, is counted in shared
+// memory: a CTA takes a slice of the ids of one row, one word an id, and looks at the row's whole history,
+// of which it counts what falls into its slice. Then the slice's logits go by once, four a thread with their
+// four words. The counts are whole numbers, so their order does not matter.
 //
-// Bound: HBM, the logits read and written once.
+// Bound: HBM, the logits read and written once. The first logits are on their way while the history is
+// counted.
 #include "pmoe_internal.h"
 
 #include <math.h>
@@ -15,7 +15,7 @@ namespace pmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxSlice = 8192;
+constexpr int kMaxSlice = 16384;
 // A word of the table: times in the output (19 bits), in the prompt (1 bit), 1 + index of the bias (12 bits).
 constexpr uint32_t kPrompt = 1u << 19, kCount = kPrompt - 1;
 constexpr int kBiasShift = 20, kMaxBiases = 4095;
@@ -98,114 +98,123 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   auto complain = [&](int32_t what) {
     if (a.err != nullptr && part == 0) atomicOr(a.err, what);
   };
-  // ---- all of them as they are, or -inf
   const float kOff = -INFINITY;
-  if (!a.in_place || mask != nullptr) {
-    auto one = [&](int v) {
-      const bool on = mask == nullptr || (mask[v >> 5] >> (v & 31) & 1);
-      if (on && a.in_place) return;
-      store1<BO>(a.out, out + v, on ? load1<BI>(a.logits, in + v) : kOff);
-    };
-    // 4 at a time from where both rows are aligned
-    const int ai = (int)((reinterpret_cast<uintptr_t>(a.logits) / (BI ? 2 : 4) + in) & 3);
-    const int ao = (int)((reinterpret_cast<uintptr_t>(a.out) / (BO ? 2 : 4) + out) & 3);
-    if (ai == ao) {
-      const int b0 = min(v1, v0 + (int)((4 - ((ai + v0) & 3)) & 3)), quads = (v1 - b0) >> 2, b1 = b0 + 4 * quads;
-      if (tid < b0 - v0) one(v0 + tid);
-      if (tid < v1 - b1) one(b1 + tid);
-      constexpr int U = 8;  // in flight
-      for (int i0 = tid; i0 < quads; i0 += U * kThreads) {
-        uint32_t on[U];
-        Quad<BI> x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * kThreads, v = b0 + 4 * i;
-          on[u] = 15;
-          if (mask != nullptr && i < quads) {
-            // 4 bits from v on, of one word or two
-            const int w = v >> 5, s = v & 31;
-            on[u] = mask[w] >> s;
-            if (s > 28) on[u] |= mask[w + 1] << (32 - s);
-            on[u] &= 15;
-          }
-          if (i >= quads) on[u] = 16;  // none
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (on[u] - 1 < (a.in_place ? 14u : 15u)) x[u] = load4<BI>(a.logits, in + b0 + 4 * (i0 + u * kThreads));
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (on[u] == 16 || (on[u] == 15 && a.in_place)) continue;
-          float f[4] = {kOff, kOff, kOff, kOff};
-          if (on[u] != 0) x[u].get(f);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (!(on[u] >> k & 1)) f[k] = kOff;
-          store4<BO>(a.out, out + b0 + 4 * (i0 + u * kThreads), f);
-        }
-      }
-    } else {
-#pragma unroll 8
-      for (int v = v0 + tid; v < v1; v += kThreads) one(v);
-    }
-  }
-  // ---- the touched ones: first which
   const bool sparse = a.max_history > 0 || a.biases > 0;
-  if (!sparse) return;
-  for (int i = tid; i < (n + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  for (int j = tid; j < a.biases; j += kThreads) {
-    const int id = a.bias_ids[(int64_t)t * a.biases + j];
-    if ((unsigned)(id - v0) < (unsigned)n)
-      atomicMax(&table[id - v0], (uint32_t)(j + 1) << kBiasShift);
-    else if (id < -1 || id >= a.V)
-      complain(kErrBadToken);
-  }
-  __syncthreads();
-  if (a.max_history > 0) {
-    const int len = a.history_len[t], all = min(max(len, 0), a.max_history);
-    const int prompt = a.prompt_len != nullptr ? a.prompt_len[t] : 0, made = min(max(prompt, 0), all);
-    if (tid == 0 && (len != all || prompt != made)) complain(kErrBadLength);
-    const int32_t* history = a.history + t * a.history_stride;
-#pragma unroll 8
-    for (int j = tid; j < all; j += kThreads) {
-      const int id = history[j];
-      if ((unsigned)(id - v0) < (unsigned)n) {
-        if (j < made)
-          atomicOr(&table[id - v0], kPrompt);
-        else
-          atomicAdd(&table[id - v0], 1u);
-      } else if (id < 0 || id >= a.V) {
-        complain(kErrBadToken);
-      }
-    }
-  }
-  __syncthreads();
-
-  // ---- then what they become
   const float rep = a.repetition != nullptr ? a.repetition[t] : 1.f, freq = a.frequency != nullptr ? a.frequency[t] : 0.f,
               pres = a.presence != nullptr ? a.presence[t] : 0.f;
-  for (int i4 = tid; i4 < (n + 3) / 4; i4 += kThreads) {
-    const uint4 four = reinterpret_cast<const uint4*>(table)[i4];
-    if ((four.x | four.y | four.z | four.w) == 0) continue;
-    const uint32_t es[4] = {four.x, four.y, four.z, four.w};
-    const int v = v0 + 4 * i4;
-    bool on[4];
-    float x[4];
+  auto adjusted = [&](float x, uint32_t e) {
+    const uint32_t times = e & kCount;
+    if (e & (kCount | kPrompt)) x = x > 0.f ? x / rep : x * rep;
+    if (times > 0) x = x - freq * (float)times - pres;
+    if (e >> kBiasShift) x += a.bias[(int64_t)t * a.biases + (e >> kBiasShift) - 1];
+    return x;
+  };
+  // 4 logits at a time from where both rows are aligned; one by one where they are not alike
+  const int ai = (int)((reinterpret_cast<uintptr_t>(a.logits) / (BI ? 2 : 4) + in) & 3);
+  const int ao = (int)((reinterpret_cast<uintptr_t>(a.out) / (BO ? 2 : 4) + out) & 3);
+  const int b0 = ai == ao ? min(v1, v0 + (int)((4 - ((ai + v0) & 3)) & 3)) : v1, quads = (v1 - b0) >> 2, b1 = b0 + 4 * quads;
+  const int word0 = (4 - (b0 - v0)) & 3;  // of the slice's first id in the table, so that the four's words are aligned
+  constexpr int U = 8;                    // in flight
+  Quad<BI> x[U];
+  auto load = [&](int i0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      on[k] = es[k] != 0 && (mask == nullptr || (mask[(v + k) >> 5] >> ((v + k) & 31) & 1));
-      if (on[k]) x[k] = load1<BI>(a.logits, in + v + k);
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kThreads < quads) x[u] = load4<BI>(a.logits, in + b0 + 4 * (i0 + u * kThreads));
+  };
+  if (!a.in_place) load(tid);
+
+  // ---- the table
+  if (sparse) {
+    for (int i = tid; i < (n + word0 + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int j = tid; j < a.biases; j += kThreads) {
+      const int id = a.bias_ids[(int64_t)t * a.biases + j];
+      if ((unsigned)(id - v0) < (unsigned)n)
+        atomicMax(&table[id - v0 + word0], (uint32_t)(j + 1) << kBiasShift);
+      else if (id < -1 || id >= a.V)
+        complain(kErrBadToken);
     }
+    __syncthreads();
+    if (a.max_history > 0) {
+      const int len = a.history_len[t], all = min(max(len, 0), a.max_history);
+      const int prompt = a.prompt_len != nullptr ? a.prompt_len[t] : 0, made = min(max(prompt, 0), all);
+      if (tid == 0 && (len != all || prompt != made)) complain(kErrBadLength);
+      const int32_t* history = a.history + t * a.history_stride;
+      uint32_t* mine = table + word0;
+      auto count = [&](int j, int id) {
+        if ((unsigned)(id - v0) < (unsigned)n) {
+          if (j < made)
+            atomicOr(&mine[id - v0], kPrompt);
+          else
+            atomicAdd(&mine[id - v0], 1u);
+        }
+      };
+      // 4 at a time from where the row is aligned, in as few instructions an id as can be: every slice looks
+      // at them all
+      const int j0 = min(all, (int)((4 - (reinterpret_cast<uintptr_t>(history) >> 2)) & 3)), fours = (all - j0) >> 2;
+      if (tid < j0) count(tid, history[tid]);
+      if (tid < all - j0 - 4 * fours) count(j0 + 4 * fours + tid, history[j0 + 4 * fours + tid]);
+#pragma unroll 2
+      for (int i = tid; i < fours; i += kThreads) {
+        const int4 id = *reinterpret_cast<const int4*>(history + j0 + 4 * i);
+        count(j0 + 4 * i, id.x), count(j0 + 4 * i + 1, id.y), count(j0 + 4 * i + 2, id.z), count(j0 + 4 * i + 3, id.w);
+      }
+      if (part == 0) {
+        bool bad = false;
+        for (int j = tid; j < all; j += kThreads) bad |= (unsigned)history[j] >= (unsigned)a.V;
+        if (bad) complain(kErrBadToken);
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- the logits
+  auto one = [&](int v) {
+    const bool on = mask == nullptr || (mask[v >> 5] >> (v & 31) & 1);
+    const uint32_t e = sparse ? table[v - v0 + word0] : 0;
+    if (on && a.in_place && e == 0) return;
+    store1<BO>(a.out, out + v, on ? adjusted(load1<BI>(a.logits, in + v), e) : kOff);
+  };
+  if (ai != ao) {
+#pragma unroll 4
+    for (int v = v0 + tid; v < v1; v += kThreads) one(v);
+    return;
+  }
+  if (tid < b0 - v0) one(v0 + tid);
+  if (tid < v1 - b1) one(b1 + tid);
+  const uint4* words = reinterpret_cast<const uint4*>(table + word0 + b0 - v0);
+  for (int i0 = tid; i0 < quads; i0 += U * kThreads) {
+    if (!a.in_place && i0 != tid) load(i0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!on[k]) continue;
-      const uint32_t times = es[k] & kCount;
-      float y = x[k];
-      if (es[k] & (kCount | kPrompt)) y = y > 0.f ? y / rep : y * rep;
-      if (times > 0) y = y - freq * (float)times - pres;
-      if (es[k] >> kBiasShift) y += a.bias[(int64_t)t * a.biases + (es[k] >> kBiasShift) - 1];
-      store1<BO>(a.out, out + v + k, y);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads, v = b0 + 4 * i;
+      if (i >= quads) break;
+      uint32_t on = 15;
+      if (mask != nullptr) {
+        // 4 bits from v on, of one word or two
+        const int w = v >> 5, s = v & 31;
+        on = mask[w] >> s;
+        if (s > 28) on |= mask[w + 1] << (32 - s);
+        on &= 15;
+      }
+      const uint4 e = sparse ? words[i] : make_uint4(0, 0, 0, 0);
+      const bool touched = (e.x | e.y | e.z | e.w) != 0;
+      if (a.in_place) {
+        if (on == 15 && !touched) continue;
+        x[u] = load4<BI>(a.logits, in + v);
+      }
+      float f[4];
+      x[u].get(f);
+      if (touched) {
+        if (e.x) f[0] = adjusted(f[0], e.x);
+        if (e.y) f[1] = adjusted(f[1], e.y);
+        if (e.z) f[2] = adjusted(f[2], e.z);
+        if (e.w) f[3] = adjusted(f[3], e.w);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (!(on >> k & 1)) f[k] = kOff;
+      store4<BO>(a.out, out + v, f);
     }
   }
 }
@@ -238,18 +247,18 @@ extern "C" int moe_adjust_logits(const void* logits, int is_bf16, int T, int V, 
   AdjustArgs a{logits,    out,        row_stride, out_stride, T,      V,    in_place, history, history_stride, max_history,
                prompt_len, history_len, repetition, frequency,  presence, bias_ids, bias,     biases,  mask,           mask_stride,
                err_out,   0,          0};
-  // a slice an SM four times over, where the rows give that much
+  // slices as large as leaves four an SM: each looks at the row's whole history
   a.slice = kMaxSlice;
   while (a.slice > 1024 && (int64_t)T * ((V + a.slice - 1) / a.slice) < 608) a.slice /= 2;
   a.slices = (V + a.slice - 1) / a.slice;
   if ((int64_t)T * a.slices > INT32_MAX) return PMOE_EINVAL;
-  const size_t smem = max_history > 0 || biases > 0 ? (size_t)a.slice * 4 : 0;
+  static SmemLimit limits[4];
+  const size_t smem = max_history > 0 || biases > 0 ? (size_t)a.slice * 4 + 16 : 0;
   cudaStream_t s = (cudaStream_t)stream;
   const char* what = "moe_adjust_logits";
   const unsigned blocks = (unsigned)(T * a.slices);
-  if (is_bf16)
-    return out_is_bf16 ? launch(what, adjust_kernel<true, true>, blocks, kThreads, smem, s, true, 1, a)
-                       : launch(what, adjust_kernel<true, false>, blocks, kThreads, smem, s, true, 1, a);
-  return out_is_bf16 ? launch(what, adjust_kernel<false, true>, blocks, kThreads, smem, s, true, 1, a)
-                     : launch(what, adjust_kernel<false, false>, blocks, kThreads, smem, s, true, 1, a);
+  const auto kernel = is_bf16 ? (out_is_bf16 ? adjust_kernel<true, true> : adjust_kernel<true, false>)
+                              : (out_is_bf16 ? adjust_kernel<false, true> : adjust_kernel<false, false>);
+  const int r = limits[(is_bf16 ? 2 : 0) + (out_is_bf16 ? 1 : 0)].set(reinterpret_cast<const void*>(kernel), kMaxSlice * 4 + 16, what);
+  return r != PMOE_OK ? r : launch(what, kernel, blocks, kThreads, smem, s, true, 1, a);
 }
