@@ -23,7 +23,7 @@ struct Args {
   __nv_bfloat16* out;
   float* lse;
   int32_t* err;
-  int ctas, tile_tokens, half_tokens, few_tokens, part_rows, few;
+  int ctas, tile_tokens, few_tokens, part_rows, few;
   // Empty units at the start of an item, for each kv head: what its start and end cost beside its tiles.
   int head;
   // scratch
@@ -92,23 +92,20 @@ __device__ __forceinline__ int key_tiles(const Args& a, int p0, int ntok, int* l
 }
 
 // One segment of a CTA's run: key tiles [t0, t1) of an item, for one kv head. Items of up to 128 rows
-// take one query tile's warps and accumulators (`lane`). Two such segments after one another make a pair,
-// whose tiles come in turn, so that one's softmax runs under the other's products and loads; what has no
-// second one takes the two query tiles in turn: one's end then overlaps with the other's beginning.
+// take one query tile's warps and accumulators, in turn the first's and the second's (`lane`): one's
+// end then overlaps with the other's beginning.
 struct __align__(16) Segment {
   int32_t req, tok0, p0, lo;  // request, first row of q, its position, first key tile beside the sinks'
   int32_t t0, t1;
   int32_t join;  // of a part: the CTA with the item's first tile, and from bit 16 on the number of parts
-  // tokens, and from bit 10 on: two query tiles, lane, all of the item's tiles; 13: kv head; 23: first of a pair
-  int32_t bits;
+  int32_t bits;  // tokens, and from bit 10 on: two query tiles, lane, all of the item's tiles; 13: kv head
   int32_t part0, part1, part2;  // tiles that some row does not see in full: [part0, part1), and from part2 on
   int32_t pad;
   __device__ __forceinline__ int ntok() const { return bits & 1023; }
   __device__ __forceinline__ bool two() const { return bits >> 10 & 1; }
   __device__ __forceinline__ int lane() const { return bits >> 11 & 1; }
   __device__ __forceinline__ bool whole() const { return bits >> 12 & 1; }
-  __device__ __forceinline__ int h() const { return bits >> 13 & 1023; }
-  __device__ __forceinline__ bool pair() const { return bits >> 23 & 1; }
+  __device__ __forceinline__ int h() const { return bits >> 13; }
   __device__ __forceinline__ int p1() const { return p0 + ntok() - 1; }
   __device__ __forceinline__ bool has(int q) const { return two() || lane() == q; }
   __device__ __forceinline__ bool partly(int t) const { return t >= part2 || (t >= part0 && t < part1); }

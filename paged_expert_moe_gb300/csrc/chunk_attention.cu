@@ -21,7 +21,6 @@
 #include "tc_gemm.h"
 
 #include <algorithm>
-#include <limits.h>
 #include <math.h>
 
 namespace pmoe {
@@ -201,7 +200,6 @@ struct Cfg {
   }
   static constexpr int kSmem = kRing + kRawRing + kQBytes + 1024 /* alignment */ + 1024 /* row exponents */ + 1024;
   static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
-  static constexpr bool kPairs = true;
   static constexpr int kGuards = F8 ? 4 : 2;              // warps that look at partly visible values
 };
 
@@ -410,12 +408,11 @@ __device__ __forceinline__ void turn_units(uint32_t (&r)[32]) {
   }
 }
 
-// q_many, q_half, q_few: boxes of tile_tokens, half_tokens and few_tokens tokens of q, all heads of a kv head
+// q_many, q_few: boxes of tile_tokens and of few_tokens tokens of q, all heads of a kv head (bf16 caches)
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                 const __grid_constant__ CUtensorMap q_many, const __grid_constant__ CUtensorMap q_half,
-                 const __grid_constant__ CUtensorMap q_few, const Args a) {
+                 const __grid_constant__ CUtensorMap q_many, const __grid_constant__ CUtensorMap q_few, const Args a) {
   using C = Cfg<D, F8>;
   constexpr int kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -451,7 +448,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     prefetch_map(&map_k);
     prefetch_map(&map_v);
     prefetch_map(&q_few);
-    prefetch_map(&q_half);
     prefetch_map(&q_many);
   }
   pdl_wait();
@@ -466,25 +462,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
   constexpr uint32_t tmem = 0;
   const int psh = 31 - __clz(a.kv.page_size);
   Segment sg;
-  auto paired = [&](const Segment& s) { return C::kPairs && s.pair(); };
-  // q of a segment, or of both of a pair, the second one's from row 128 on. A box holds whole tokens, so
-  // rows beyond the item's are the next tokens' or zero.
-  auto load_q = [&](const Segment& s, const Segment& s2, uint64_t* bar) {
+  auto load_q = [&](const Segment& s, uint64_t* bar) {
     if (lane == 0) {
-      auto tokens = [&](const Segment& x) { return x.ntok() <= a.few_tokens ? a.few_tokens : x.two() ? a.tile_tokens : a.half_tokens; };
-      auto box = [&](const Segment& x, uint8_t* to) {
-        const CUtensorMap* map = x.ntok() <= a.few_tokens ? &q_few : x.two() ? &q_many : &q_half;
+      const bool few = s.ntok() <= a.few_tokens;
+      mbar_arrive_expect_tx(bar, (few ? a.few_tokens : a.tile_tokens) * a.group * D * 2);
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf)
-          tma_load_3d(to + hf * (kRows * 128), map, bar, hf * 64, x.h() * a.group, x.tok0);
-      };
-      mbar_arrive_expect_tx(bar, (tokens(s) + (paired(s) ? tokens(s2) : 0)) * a.group * D * 2);
-      box(s, qs);
-      if (paired(s)) box(s2, qs + 128 * 128);
+        tma_load_3d(qs + hf * (kRows * 128), few ? &q_few : &q_many, bar, hf * 64, s.h() * a.group, s.tok0);
     }
     __syncwarp();
   };
-  auto segment = [&](uint32_t i, Segment* s) { return get_segment(b, i, s, abort_flag, a.err); };
 
   if (warp < 8) {
     // ---------------- softmax: one thread a row
@@ -719,18 +706,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         __syncwarp();
       };
       // weights x values of tile t of sg by query tile q
-      auto products = [&](bool add, int q, uint32_t slot, bool last, bool end) {
+      auto products = [&](int t, int q, uint32_t slot, bool last) {
         const uint32_t o = tmem + 256 + q * 128, p = tmem + q * 128, v = ring + slot * C::kTileBytes;
         if (converged_lane()) {
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k) mma_f16_ts(o, p + k * 8, v_desc(v + k * 2048), io, add || k > 0);
+          for (int k = 0; k < kKeys / 16; ++k) mma_f16_ts(o, p + k * 8, v_desc(v + k * 2048), io, t > sg.t0 || k > 0);
           if (last) mma_commit(&b.empty[slot]);
-          if (end) mma_commit(&b.odone[q]);
         }
         __syncwarp();
       };
       // the same of any tile: of a partly visible one only the steps of 16 keys that some row sees
-      auto any_products = [&](const Segment& sg, int t, int q, uint32_t slot, bool last) {
+      auto any_products = [&](int t, int q, uint32_t slot, bool last) {
         const uint32_t o = tmem + 256 + q * 128, p = tmem + q * 128, v = ring + slot * C::kTileBytes;
         int step0 = 0, step1 = kKeys / 16;
         if (sg.partly(t)) {
@@ -754,93 +740,22 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         part ^= 1u << slot;
         return true;
       };
-      auto q_rows = [&](const Segment& s, int q) { return qa + ((s.two() || paired(s)) && q ? 128 * 128 : 0); };
-      // all scores of a segment's first tile, whose K is ring tile i, or of a pair's
-      Segment sb{};  // of a pair the second
-      auto first_scores = [&](const Segment& s, uint32_t i) {
-        if (paired(s)) {
-          const bool end = s.t0 + 1 == s.t1 && sb.t0 + 1 == sb.t1;
-          scores(0, qa, i % kSlots, true, false);
-          if (!wait_kv(i + 2)) return false;
-          fence_after();
-          scores(1, qa + 128 * 128, (i + 2) % kSlots, true, end);
-          return true;
-        }
+      auto q_rows = [&](const Segment& s, int q) { return qa + (s.two() && q ? 128 * 128 : 0); };
+      // all scores of a segment's first tile
+      auto first_scores = [&](const Segment& s, uint32_t slot) {
         const bool end = s.t0 + 1 == s.t1;
         for (int q = s.two() ? 0 : s.lane(); q < (s.two() ? 2 : s.lane() + 1); ++q) {
           const bool last = !s.two() || q == 1;
-          scores(q, q_rows(s, q), i % kSlots, last, last && end);
+          scores(q, q_rows(s, q), slot, last, last && end);
         }
-        return true;
       };
-      // the segment or pair from i on
-      auto group = [&](uint32_t i, Segment* s) {
-        if (!segment(i, s)) return false;
-        return !paired(*s) || segment(i + 1, &sb);
-      };
-      uint32_t groups = 0;  // so far
-      bool ok = true, have = group(0, &sg);
+      bool ok = true, have = get_segment(b, 0, &sg, abort_flag, a.err);
       if (have) {
-        ok = wait(&b.qfull, groups) && wait_kv(kv);
+        ok = wait(&b.qfull, segs) && wait_kv(kv);
         fence_after();
-        if (ok) ok = first_scores(sg, kv);
+        if (ok) first_scores(sg, kv % kSlots);
       }
       while (ok && have) {
-        if (paired(sg)) {
-          // each query tile its own segment: their tiles in turn, as long as both have some
-          int t[2] = {sg.t0, sb.t0};
-          uint32_t cur[2] = {kv, kv + 2}, next = kv + 4;  // ring tiles: K of the present ones, of the next one
-          while (ok && (t[0] < sg.t1 || t[1] < sb.t1)) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const Segment& s = q ? sb : sg;
-              const Segment& other = q ? sg : sb;
-              if (t[q] >= s.t1) continue;
-              const bool more = t[q] + 1 < s.t1;
-              const uint32_t vslot = (cur[q] + 1) % kSlots;
-              const bool part_of = s.partly(t[q]);
-              // (all of them at once, where they are through: one after the other they are 100 cycles each)
-              const uint32_t kk = more ? next : cur[q];
-              const bool there = mbar_try_wait(&b.full[kk % kSlots], kk / kSlots & 1) &
-                                 mbar_try_wait(&b.full[vslot], (cur[q] + 1) / kSlots & 1) & mbar_try_wait(&b.pready[q], pn[q] & 1);
-              if (!__all_sync(0xffffffffu, there) &&
-                  ((more && !wait_kv(next)) || !wait_kv(cur[q] + 1) || !wait(&b.pready[q], pn[q]))) {
-                ok = false;
-                break;
-              }
-              if (!F8 && part_of && !wait(&b.vok[vslot], part >> vslot)) {
-                ok = false;
-                break;
-              }
-              if (!F8 && part_of) part ^= 1u << vslot;
-              ++pn[q];
-              fence_after();
-              if (part_of)
-                any_products(s, t[q], q, vslot, true);
-              else
-                products(t[q] > s.t0, q, vslot, true, !more);
-              ++t[q];
-              if (more) {
-                // the group's last scores: no other ones come, of this segment or of the other
-                const bool end = t[q] + 1 == s.t1 && t[q ^ 1] + 1 >= other.t1;
-                scores(q, qa + q * 128 * 128, next % kSlots, true, end);
-                cur[q] = next;
-                next += 2;
-              }
-            }
-          }
-          if (!ok) break;
-          kv = next;
-          segs += 2, ++groups;
-          have = group(segs, &sg);
-          if (__any_sync(0xffffffffu, *abort_flag)) break;
-          if (have) {
-            ok = wait(&b.qfull, groups) && wait_kv(kv);
-            fence_after();
-            if (ok) ok = first_scores(sg, kv);
-          }
-          continue;
-        }
         const int qb = sg.two() ? 0 : sg.lane(), qe = sg.two() ? 2 : sg.lane() + 1;
         int t = sg.t0;
         // (a query tile's weights come after it has read its accumulators of the segment before)
@@ -862,7 +777,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               }
               ++pn[q];
               fence_after();
-              products(t > sg.t0, q, vslot, q + 1 == qe, false);
+              products(t, q, vslot, q + 1 == qe);
               scores(q, q_rows(sg, q), kslot, q + 1 == qe, end && q + 1 == qe);
             }
             if (!ok) break;
@@ -880,7 +795,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             ++pn[q];
             fence_after();
-            any_products(sg, t, q, (kv + 1) % kSlots, q + 1 == qe);
+            any_products(t, q, (kv + 1) % kSlots, q + 1 == qe);
             scores(q, q_rows(sg, q), (kv + 2) % kSlots, q + 1 == qe, t + 2 == sg.t1 && q + 1 == qe);
           }
           if (!ok) break;
@@ -890,14 +805,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         // the last tile: the next segment's scores come before and between its products with V, but where q
         // is late
         Segment nx;
-        const bool more = group(segs + 1, &nx);  // (made known behind this tile)
+        const bool more = get_segment(b, segs + 1, &nx, abort_flag, a.err);  // (made known behind this tile)
         if (__any_sync(0xffffffffu, *abort_flag)) break;
         const uint32_t vslot = (kv + 1) % kSlots, kslot = (kv + 2) % kSlots;
-        const bool early = more && !paired(nx) && __all_sync(0xffffffffu, mbar_try_wait(&b.qfull, (groups + 1) & 1));
-        const bool first = early && !sg.two() && !nx.two() && sg.lane() != nx.lane();  // the other query tile's turn: at once
+        const bool early = more && __all_sync(0xffffffffu, mbar_try_wait(&b.qfull, (segs + 1) & 1));
+        const bool first = early && !sg.two() && !nx.two();  // the other query tile's turn: at once
         if (early && !wait_kv(kv + 2)) break;
         fence_after();
-        if (first) first_scores(nx, kv + 2);
+        if (first) first_scores(nx, kslot);
         if (!wait_v(t, kv + 1)) break;
         for (int q = 0; q < 2; ++q) {
           if (sg.has(q)) {
@@ -907,7 +822,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             ++pn[q];
             fence_after();
-            any_products(sg, t, q, vslot, q + 1 == qe);
+            any_products(t, q, vslot, q + 1 == qe);
           }
           if (early && !first && nx.has(q)) {
             const bool last = !nx.two() || q == 1;
@@ -916,14 +831,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         if (!ok) break;
         if (more && !early) {
-          if (!wait(&b.qfull, groups + 1) || !wait_kv(kv + 2)) break;
+          if (!wait(&b.qfull, segs + 1) || !wait_kv(kv + 2)) break;
           fence_after();
-          if (!first_scores(nx, kv + 2)) break;
+          first_scores(nx, kslot);
         }
         kv += 2;
         sg = nx;
         have = more;
-        ++segs, ++groups;
+        ++segs;
       }
       // every MMA and its arrival are done before the CTA leaves
       if (converged_lane()) {
@@ -942,76 +857,43 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       bool ok = true;
       Walk walk;
       if (a.few) find_run_of_few(a, reinterpret_cast<int8_t*>(&b.segs[kSegs - 1]), &b.run);  // (a place not yet in use)
-      walk.begin(a, b.run);       // the ids of 32 pages, one a lane: a tile's own would cost it the latency of a load
-      struct Pages {
-        int first, ids;
-      };
-      auto load_tile = [&](const Segment& s, int t, Pages& pages) {
-        const int pb = lane / kHalves, hf = lane % kHalves;
-        const int key0 = tile_key<kKeys>(a, s, t), key = key0 + pb * box, page0 = key0 >> psh;
-        if (page0 < pages.first || page0 + boxes > pages.first + 32) {
-          pages.first = page0;
-          pages.ids = 0;
-          if (page0 + lane <= max(s.p1(), 0) >> psh)
-            pages.ids = __ldg(a.page_table + (int64_t)s.req * a.table_stride + page0 + lane);
+      walk.begin(a, b.run);
+      for (uint32_t i = 0; ok; ++i) {
+        if (!walk.next(a, &sg)) sg.bits = 0;
+        if (lane == 0) {
+          b.segs[i % kSegs] = sg;
+          mbar_arrive(&b.segready[i % kSegs]);
         }
-        int id = __shfl_sync(0xffffffffu, pages.ids, ((key >> psh) - pages.first) & 31);
+        __syncwarp();
+        if (sg.bits == 0) break;
+        const int32_t* table = a.page_table + (int64_t)sg.req * a.table_stride;
+        for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+          const int pb = lane / kHalves, hf = lane % kHalves;
+          const int key = tile_key<kKeys>(a, sg, t) + pb * box;
           // pages with a key that some row sees
-        bool use = pb < boxes && key <= s.p1();
-        if (use && a.window > 0) use = key + box - 1 > s.p0 - a.window || key < a.sinks;
-        if (use && (unsigned)id >= (unsigned)a.kv.num_pages) {
+          bool use = pb < boxes && key <= sg.p1();
+          if (use && a.window > 0) use = key + box - 1 > sg.p0 - a.window || key < a.sinks;
+          int id = 0;
+          if (use) {
+            id = __ldg(table + (key >> psh));
+            if ((unsigned)id >= (unsigned)a.kv.num_pages) {
               if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
               id = a.kv.num_pages;  // out of the map's range: reads as zeros
+            }
           }
           const int used = __popc(__ballot_sync(0xffffffffu, use));
           for (int v = 0; v < 2; ++v, ++kv) {
             const uint32_t slot = kv % kSlots;
-          if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) return false;
+            if (!warp_wait(&b.empty[slot], ((kv / kSlots) & 1) ^ 1, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
             if (lane == 0) mbar_arrive_expect_tx(&arrive[slot], used * box * (F8 ? D : 64) * kBytes);
             __syncwarp();
             uint8_t* dst = F8 ? C::raw(smem, slot) + pb * box * D : smem + slot * C::kTileBytes + hf * (kKeys * 128) + pb * box * 128;
             if (use)
-            tma_load_4d(dst, v ? &map_v : &map_k, &arrive[slot], hf * 64, key & (a.kv.page_size - 1), s.h(), id);
+              tma_load_4d(dst, v ? &map_v : &map_k, &arrive[slot], hf * 64, key & (a.kv.page_size - 1), sg.h(), id);
           }
-        return true;
-      };
-      Segment sb{};  // the one after, where it is known already: of a pair the second
-      bool ahead = false;
-      for (uint32_t i = 0; ok;) {
-        if (ahead)
-          sg = sb;
-        else if (!walk.next(a, &sg))
-          sg.bits = 0;
-        ahead = false;
-        if (C::kPairs && sg.bits != 0 && !sg.two()) {
-          ahead = walk.next(a, &sb);
-          if (ahead && !sb.two()) {
-            sg.bits = (sg.bits & ~(1 << 11)) | 1 << 23;
-            sb.bits |= 1 << 11;
-          }
-        }
-        const bool pair = sg.bits != 0 && paired(sg);
-        if (lane == 0) {
-          b.segs[i % kSegs] = sg;
-          mbar_arrive(&b.segready[i % kSegs]);
-          if (pair) {
-            b.segs[(i + 1) % kSegs] = sb;
-            mbar_arrive(&b.segready[(i + 1) % kSegs]);
-          }
-        }
-        __syncwarp();
-        if (sg.bits == 0) break;
-        Pages pa{INT_MAX, 0}, pb{INT_MAX, 0};
-        if (pair) {
-          ahead = false;
-          for (int ta = sg.t0, tb = sb.t0; ok && (ta < sg.t1 || tb < sb.t1); ++ta, ++tb) {
-            if (ta < sg.t1) ok = load_tile(sg, ta, pa);
-            if (ok && tb < sb.t1) ok = load_tile(sb, tb, pb);
-          }
-          i += 2;
-        } else {
-          for (int t = sg.t0; t < sg.t1 && ok; ++t) ok = load_tile(sg, t, pa);
-          ++i;
         }
       }
       // copies in flight land before the CTA leaves, even where another role gave up
@@ -1022,75 +904,71 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       }
     } else if constexpr (!F8) {
       // ---------------- guards: warps 10 and 11 look at the values of partly visible tiles;
-      // warp 10 also loads q
+      // warp 10 also loads q. A box holds whole tokens, so rows beyond the item's are the next tokens' or zero.
       const int gw = warp - 10;
-      uint32_t kv = 0, segs = 0, groups = 0;
-      Segment sb{}, nx, nb{};
-      // tile t of segment i; last: of its group
-      auto guard = [&](const Segment& s, uint32_t i, int t, bool last, bool* more) {
-        const int k0 = tile_key<kKeys>(a, s, t);
+      uint32_t kv = 0, segs = 0, loads = 0;
+      bool ok = get_segment(b, 0, &sg, abort_flag, a.err);
+      if (gw == 0 && ok) load_q(sg, &b.qfull), ++loads;
+      while (ok) {
+        Segment nx;
+        bool more = false;
+        if (lane == 0) *(volatile uint8_t*)&b.poison[gw][segs & 15] = 0;
+        __syncwarp();
+        for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+          const int k0 = tile_key<kKeys>(a, sg, t);
           for (int v = 0; v < 2; ++v, ++kv) {
             const uint32_t slot = kv % kSlots;
-          if (!warp_wait(&b.full[slot], (kv / kSlots) & 1, abort_flag, a.err)) return false;
-          if (v == 1 && last) {
-            // the next group's q, once this one's last scores are there
-            const uint32_t n = segs + (paired(sg) ? 2 : 1);
-            *more = segment(n, &nx) && (!paired(nx) || segment(n + 1, &nb));
-            if (*more && gw == 0) {
-              if (!warp_wait(&b.qempty, groups & 1, abort_flag, a.err)) return false;
-              load_q(nx, nb, &b.qfull);
-              }
+            if (!warp_wait(&b.full[slot], (kv / kSlots) & 1, abort_flag, a.err)) {
+              ok = false;
+              break;
             }
-          if (v == 1 && s.partly(t)) {
-            bool found = false;
-            const Span pt = seen_span<kKeys>(a, s, k0);
-            const int below = pt.low - pt.first, rows = below + pt.end - pt.high;
-#pragma unroll 1
-            for (int k = gw * 32 + lane; k < rows * (D / 8); k += 64) {
-              const int n = k / (D / 8), c = k % (D / 8), r = n < below ? pt.first + n : pt.high + n - below;
-              if (all_see(a, s.p0, s.p1(), k0 + r)) continue;
-              uint4* at = reinterpret_cast<uint4*>(smem + slot * C::kTileBytes + (c / 8) * (kKeys * 128) + r * 128 + (c & 7) * 16);
-              if (!any_sees(a, s.p0, s.p1(), k0 + r)) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 x = *at;
-              uint32_t w[4] = {x.x, x.y, x.z, x.w};
-              if (not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3])) {
-                found = true;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint32_t bad = not_finite(w[j]);
-                  w[j] &= ~((bad & 0x8000u ? 0xffffu : 0u) | (bad & 0x80000000u ? 0xffff0000u : 0u));
+            if (v == 1 && t + 1 == sg.t1) {
+              // the next segment's q, once this one's last scores are there
+              more = get_segment(b, segs + 1, &nx, abort_flag, a.err);
+              if (more && gw == 0) {
+                if (!warp_wait(&b.qempty, segs & 1, abort_flag, a.err)) {
+                  ok = false;
+                  break;
                 }
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                load_q(nx, &b.qfull);
+                ++loads;
               }
             }
-            if (found) *(volatile uint8_t*)&b.poison[gw][i & 15] = 1;
-            fence_async();
-            warp_arrive(&b.vok[slot]);
-          }
+            if (v == 1 && sg.partly(t)) {
+              bool found = false;
+              const Span pt = seen_span<kKeys>(a, sg, k0);
+              const int below = pt.low - pt.first, rows = below + pt.end - pt.high;
+#pragma unroll 1
+              for (int i = gw * 32 + lane; i < rows * (D / 8); i += 64) {
+                const int n = i / (D / 8), c = i % (D / 8), r = n < below ? pt.first + n : pt.high + n - below;
+                if (all_see(a, sg.p0, sg.p1(), k0 + r)) continue;
+                uint4* at = reinterpret_cast<uint4*>(smem + slot * C::kTileBytes + (c / 8) * (kKeys * 128) + r * 128 + (c & 7) * 16);
+                if (!any_sees(a, sg.p0, sg.p1(), k0 + r)) {
+                  *at = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                const uint4 x = *at;
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                if (not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3])) {
+                  found = true;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t bad = not_finite(w[k]);
+                    w[k] &= ~((bad & 0x8000u ? 0xffffu : 0u) | (bad & 0x80000000u ? 0xffff0000u : 0u));
+                  }
+                  *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+              if (found) *(volatile uint8_t*)&b.poison[gw][segs & 15] = 1;
+              fence_async();
+              warp_arrive(&b.vok[slot]);
+            }
             warp_arrive(&b.empty[slot]);
           }
-        return true;
-      };
-      bool ok = segment(0, &sg) && (!paired(sg) || segment(1, &sb));
-      uint32_t loads = 0;
-      if (gw == 0 && ok) load_q(sg, sb, &b.qfull), ++loads;
-      while (ok) {
-        bool more = false;
-        const int nseg = paired(sg) ? 2 : 1;
-        if (lane < nseg) *(volatile uint8_t*)&b.poison[gw][(segs + lane) & 15] = 0;
-        __syncwarp();
-        const int tb1 = paired(sg) ? sb.t1 : 0;
-        for (int ta = sg.t0, tb = paired(sg) ? sb.t0 : 0; ok && (ta < sg.t1 || tb < tb1); ++ta, ++tb) {
-          if (ta < sg.t1) ok = guard(sg, segs, ta, ta + 1 == sg.t1 && tb >= tb1, &more);
-          if (ok && tb < tb1) ok = guard(sb, segs + 1, tb, tb + 1 == tb1 && ta + 1 >= sg.t1, &more);
         }
         ok = ok && more;
-        if (gw == 0 && more) ++loads;
-        segs += nseg, ++groups;
-        sg = nx, sb = nb;
+        sg = nx;
+        ++segs;
       }
       // q's copy in flight lands before the CTA leaves
       if (loads > 0) {
@@ -1102,12 +980,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       // ---------------- e4m3: warp 10 loads q
       uint32_t loads = 0;
       if (warp == 10)
-        for (uint32_t segs = 0; segment(segs, &sg); ++loads) {
-          Segment sb{};
-          if (paired(sg) && !segment(segs + 1, &sb)) break;
-          segs += paired(sg) ? 2 : 1;
+        for (; get_segment(b, loads, &sg, abort_flag, a.err); ++loads) {
           if (loads > 0 && !warp_wait(&b.qempty, (loads - 1) & 1, abort_flag, a.err)) break;
-          load_q(sg, sb, &b.qraw);
+          load_q(sg, &b.qraw);
         }
       // q's copy in flight lands before the CTA leaves
       if (loads > 0) {
@@ -1122,13 +997,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     constexpr int CH = D / 16;  // 16-code chunks of a row
     constexpr int N = kKeys * CH / 128;
     const int tid = threadIdx.x - 12 * 32, ch = tid % CH, r0 = tid / CH;
-    uint32_t kv = 0, segs = 0, groups = 0;
-    // q of segment i in place, divided by each row's power of two; rows beyond the item's stay what they were
-    auto convert_q = [&](const Segment& s, uint32_t i, int row0) {
+    uint32_t kv = 0, segs = 0;
+    bool ok = true;
+    for (; ok && get_segment(b, segs, &sg, abort_flag, a.err); ++segs) {
+      if (lane == 0) *(volatile uint8_t*)&b.poison[warp - 12][segs & 15] = 0;
+      __syncwarp();
+      {  // q in place, divided by each row's power of two; rows beyond the item's stay what they were
         constexpr int LPR = D / 8, U = 4, kStep = 128 / LPR;  // threads of a row, chunks at once, rows at a time
-      const int rows = s.ntok() * a.group, c = tid % LPR;
-      const float factor = fabsf(a.scale) * fabsf(a.kv.k_scale[s.h()]);
-      uint8_t* q0 = qs + (c / 8) * (kRows * 128) + row0 * 128;
+        const int rows = sg.ntok() * a.group, c = tid % LPR;
+        const float factor = fabsf(a.scale) * fabsf(a.kv.k_scale[sg.h()]);
+        if (!warp_wait(&b.qraw, segs & 1, abort_flag, a.err)) break;
+        uint8_t* q0 = qs + (c / 8) * (kRows * 128);
 #pragma unroll 1
         for (int i0 = 0; i0 < rows; i0 += U * kStep) {
           const int ra = i0 + tid / LPR;
@@ -1136,7 +1015,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
           uint32_t mx[U];
 #pragma unroll
           for (int p = 0; p < U; ++p) {
-          const int r = min(ra + p * kStep, kRows - 1 - row0);
+            const int r = min(ra + p * kStep, kRows - 1);
             v[p] = *reinterpret_cast<const uint4*>(q0 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
             mx[p] = max2(max2(v[p].x & 0x7fff7fffu, v[p].y & 0x7fff7fffu), max2(v[p].z & 0x7fff7fffu, v[p].w & 0x7fff7fffu));
             mx[p] = max2(mx[p], mx[p] >> 16);
@@ -1155,27 +1034,30 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             for (int k = 0; k < 4; ++k)
               w[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
             if (r < rows) {
-            if (c == 0) qexp[(i & 3) * 256 + r] = (int8_t)e;
+              if (c == 0) qexp[(segs & 3) * 256 + r] = (int8_t)e;
               *reinterpret_cast<uint4*>(q0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
-    };
-    // K and V of tile t of segment `seg`
-    auto convert_tile = [&](const Segment& s, uint32_t seg, int t) {
-      for (int kind = 0; kind < 2; ++kind, ++kv) {
+        fence_async();
+        warp_arrive(&b.qfull);
+      }
+      for (int i2 = 2 * sg.t0; i2 < 2 * sg.t1; ++i2, ++kv) {  // K and V of each tile
         const uint32_t slot = kv % kSlots;
-        if (!warp_wait(&b.raw[slot], (kv / kSlots) & 1, abort_flag, a.err)) return false;
+        if (!warp_wait(&b.raw[slot], (kv / kSlots) & 1, abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
         uint8_t* src = C::raw(smem, slot);
-        const int k0 = tile_key<kKeys>(a, s, t);
+        const int k0 = tile_key<kKeys>(a, sg, i2 / 2);
         auto at = [&](int r) { return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4); };
-        if (kind == 1 && s.partly(t)) {
+        if ((i2 & 1) && sg.partly(i2 / 2)) {
           bool found = false;
 #pragma unroll 1
           for (int i = 0; i < N; ++i) {
             const int r = r0 + i * (128 / CH), j = k0 + r;
-            if (all_see(a, s.p0, s.p1(), j)) continue;
-            const uint32_t any = any_sees(a, s.p0, s.p1(), j) ? ~0u : 0u;
+            if (all_see(a, sg.p0, sg.p1(), j)) continue;
+            const uint32_t any = any_sees(a, sg.p0, sg.p1(), j) ? ~0u : 0u;
             uint4 x = *reinterpret_cast<const uint4*>(src + at(r));
             uint32_t* w = &x.x;
 #pragma unroll
@@ -1186,7 +1068,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             *reinterpret_cast<uint4*>(src + at(r)) = x;
           }
-          if (found) *(volatile uint8_t*)&b.poison[warp - 12][seg & 15] = 1;
+          if (found) *(volatile uint8_t*)&b.poison[warp - 12][segs & 15] = 1;
         }
         uint4 raw[N];
 #pragma unroll
@@ -1211,23 +1093,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         fence_async();
         warp_arrive(&b.full[slot]);
-      }
-      return true;
-    };
-    bool ok = true;
-    Segment sb{};
-    for (; ok && segment(segs, &sg) && (!paired(sg) || segment(segs + 1, &sb)); segs += paired(sg) ? 2 : 1, ++groups) {
-      if (lane < (paired(sg) ? 2 : 1)) *(volatile uint8_t*)&b.poison[warp - 12][(segs + lane) & 15] = 0;
-      __syncwarp();
-      if (!warp_wait(&b.qraw, groups & 1, abort_flag, a.err)) break;
-      convert_q(sg, segs, 0);
-      if (paired(sg)) convert_q(sb, segs + 1, 128);
-      fence_async();
-      warp_arrive(&b.qfull);
-      const int tb1 = paired(sg) ? sb.t1 : 0;
-      for (int ta = sg.t0, tb = paired(sg) ? sb.t0 : 0; ok && (ta < sg.t1 || tb < tb1); ++ta, ++tb) {
-        if (ta < sg.t1) ok = convert_tile(sg, segs, ta);
-        if (ok && tb < tb1) ok = convert_tile(sb, segs + 1, tb);
       }
     }
   }
@@ -1272,15 +1137,14 @@ int launch_all(const Args& a, cudaStream_t s) {
   using C = Cfg<D, F8>;
   const char* what = "moe_chunk_attention";
   static SmemLimit limit;
-  CUtensorMap mk, mv, many, half, few;
+  CUtensorMap mk, mv, many, few;
   int r = make_map(a, a.kv.k, &mk);
   if (r == PMOE_OK) r = make_map(a, a.kv.v, &mv);
   if (r == PMOE_OK) r = make_q_map(a, a.tile_tokens, &many);
-  if (r == PMOE_OK) r = make_q_map(a, a.half_tokens, &half);
   if (r == PMOE_OK) r = make_q_map(a, a.few_tokens, &few);
   if (r == PMOE_OK) r = limit.set(reinterpret_cast<const void*>(chunk_kernel<D, F8>), C::kSmem, what);
   if (r == PMOE_OK) r = launch(what, clear_kernel, 1, 256, 0, s, true, 1, a.done, 2 * a.ctas);
-  if (r == PMOE_OK) r = launch(what, chunk_kernel<D, F8>, a.ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, many, half, few, a);
+  if (r == PMOE_OK) r = launch(what, chunk_kernel<D, F8>, a.ctas, C::kThreads, C::kSmem, s, true, 1, mk, mv, many, few, a);
   return r;
 }
 
@@ -1305,7 +1169,6 @@ int plan(const pmoe_kv_desc* kv, int T, int q_heads, int R, Args* a, Layout* l) 
   a->ctas = sm_count();
   if (a->ctas == 0) return PMOE_ECUDA;
   a->tile_tokens = kRows / a->group;
-  a->half_tokens = 128 / a->group;
   a->few_tokens = std::max(1, 16 / a->group);
   // in us with 2 / 3 / 4 / 6: a prompt of 8,192 tokens (32 / 4 heads of 128) 427 / 411 / 412 / 423, with e4m3
   // 691 / 589 / 508 / 478; 256 single tokens with a window of 4,096 314 / 316 / 318 / 319
