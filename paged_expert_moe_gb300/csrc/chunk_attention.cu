@@ -21,6 +21,7 @@
 #include "tc_gemm.h"
 
 #include <algorithm>
+#include <limits.h>
 #include <math.h>
 
 namespace pmoe {
@@ -867,19 +868,23 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         __syncwarp();
         if (sg.bits == 0) break;
         const int32_t* table = a.page_table + (int64_t)sg.req * a.table_stride;
+        // the ids of 32 pages from `first` on, one a lane: a tile's own would cost it the latency of a load
+        int first = INT_MAX, ids = 0;
         for (int t = sg.t0; t < sg.t1 && ok; ++t) {
           const int pb = lane / kHalves, hf = lane % kHalves;
-          const int key = tile_key<kKeys>(a, sg, t) + pb * box;
+          const int key0 = tile_key<kKeys>(a, sg, t), key = key0 + pb * box, page0 = key0 >> psh;
+          if (page0 < first || page0 + boxes > first + 32) {
+            first = page0;
+            ids = 0;
+            if (page0 + lane <= max(sg.p1(), 0) >> psh) ids = __ldg(table + page0 + lane);
+          }
+          int id = __shfl_sync(0xffffffffu, ids, ((key >> psh) - first) & 31);
           // pages with a key that some row sees
           bool use = pb < boxes && key <= sg.p1();
           if (use && a.window > 0) use = key + box - 1 > sg.p0 - a.window || key < a.sinks;
-          int id = 0;
-          if (use) {
-            id = __ldg(table + (key >> psh));
-            if ((unsigned)id >= (unsigned)a.kv.num_pages) {
-              if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
-              id = a.kv.num_pages;  // out of the map's range: reads as zeros
-            }
+          if (use && (unsigned)id >= (unsigned)a.kv.num_pages) {
+            if (a.err != nullptr) atomicOr(a.err, kErrBadPage);
+            id = a.kv.num_pages;  // out of the map's range: reads as zeros
           }
           const int used = __popc(__ballot_sync(0xffffffffu, use));
           for (int v = 0; v < 2; ++v, ++kv) {
