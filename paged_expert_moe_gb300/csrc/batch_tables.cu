@@ -32,41 +32,27 @@ struct TableArgs {
   int32_t* err;
 };
 
-struct Sums {
-  int64_t rows, back, need;
-};
-__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
-  return {a.rows + b.rows, a.back + b.back, a.need + b.need};
-}
-
-// Sums over the threads before this one; *total: over all.
-__device__ Sums block_scan(Sums v, Sums* warps, Sums* total) {
+// The sum over the threads before this one; *total: over all.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto up = [](const Sums& s, int o) -> Sums {
-    return {__shfl_up_sync(0xffffffffu, s.rows, o), __shfl_up_sync(0xffffffffu, s.back, o), __shfl_up_sync(0xffffffffu, s.need, o)};
-  };
-  Sums x = v;
+  int64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Sums y = up(x, o);
-    if (lane >= o) x = x + y;
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
   if (lane == 31) warps[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    Sums w = warps[lane];
+  // every warp adds up the warps' sums for itself
+  int64_t w = warps[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const Sums y = up(w, o);
-      if (lane >= o) w = w + y;
-    }
-    warps[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  __syncthreads();
-  *total = warps[31];
-  const Sums before = warp > 0 ? warps[warp - 1] : Sums{0, 0, 0};
-  __syncthreads();
-  return {before.rows + x.rows - v.rows, before.back + x.back - v.back, before.need + x.need - v.need};
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int64_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return (warp > 0 ? before : 0) + x - v;
 }
 
 __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TableArgs a) {
@@ -74,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TableArgs 
   int32_t* start = smem;                 // [R + 1] first row
   int32_t* len = start + a.R + 1;        // [R] keys before the step
   int32_t* got = len + a.R;              // [R] new pages before its own; -1: the request gets none
-  __shared__ Sums warps[32];
+  __shared__ int64_t warps[3][32];  // of three sums in turn, so that none waits for the one before to be read
   __shared__ int s_taken;
   const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x, all = kThreads * ctas, me = cta * kThreads + tid;
   const int psh = 31 - __clz(a.page_size), round = a.page_size - 1;
@@ -91,12 +77,11 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TableArgs 
     count = count < 0 ? 0 : a.free_capacity;
   }
 
-  // ---- what each request needs, and where its rows lie; pages given back
-  Sums sum{0, 0, 0};
+  // ---- where each request's rows lie; pages given back
+  int64_t sum = 0, back = 0;
   for (int r0 = 0; r0 < a.R; r0 += kThreads) {
     const int r = r0 + tid;
     int have = 0, n = 0, old = 0;
-    Sums mine{0, 0, 0};
     if (r < a.R) {
       old = a.lens[r], n = a.new_len[r];
       if (old < 0 || old > room || n < -1) {
@@ -104,50 +89,53 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TableArgs 
         old = old < 0 ? 0 : (int)min((int64_t)old, room);
       }
       have = (int)(((int64_t)old + round) >> psh);
-      mine.rows = max(n, 0);
-      if (n == -1) mine.back = have;
     }
-    Sums total;
-    const Sums at = block_scan(mine, warps, &total);
+    const int ended = __syncthreads_or(n == -1);
+    int64_t total;
+    const int64_t at = sum + block_scan(max(n, 0), warps[0], &total);
     if (r < a.R) {
-      const int64_t end = sum.rows + at.rows + max(n, 0);
-      start[r] = (int)min(sum.rows + at.rows, (int64_t)a.T);
+      start[r] = (int)min(at, (int64_t)a.T);
       // the row's end and the table's width decide first: what does not fit there takes no pages
-      const bool fits = end <= a.T && (int64_t)old + max(n, 0) <= room;
+      const bool fits = at + max(n, 0) <= a.T && (int64_t)old + max(n, 0) <= room;
       len[r] = old;
       got[r] = n > 0 && !fits ? -1 : 0;
       if (cta == 0) a.q_start[r] = start[r];
     }
-    if (total.back > 0) {  // a warp a request of the block's turn, the cluster's warps in turn
-      __syncthreads();
-      for (int i = cta * 32 + (tid >> 5); i < kThreads && r0 + i < a.R; i += ctas * 32) {
-        if (a.new_len[r0 + i] != -1) continue;
-        // (how many pages lie before this request's: summed up again, few requests end in a step)
-        int64_t before = 0;
-        for (int k = tid & 31; k < i; k += 32)
-          if (a.new_len[r0 + k] == -1) before += (len[r0 + k] + (int64_t)round) >> psh;
+    sum += total;
+    if (ended) {
+      const int64_t first = count + back + block_scan(n == -1 ? have : 0, warps[1], &total);
+      back += total;
+      // a warp hands back the pages of its lanes' requests, one request after another, each over
+      // the whole cluster; eight loads of a lane are under way at a time
+      const int lane = tid & 31, step = 32 * ctas;
+      for (unsigned m = __ballot_sync(0xffffffffu, n == -1 && have > 0); m != 0; m &= m - 1) {
+        const int k = __ffs(m) - 1, pages = __shfl_sync(0xffffffffu, have, k);
+        const int64_t to = __shfl_sync(0xffffffffu, first, k);
+        const int32_t* from = a.page_table + (int64_t)(r - lane + k) * a.table_stride;
+        for (int i0 = cta * 32 + lane; i0 < pages; i0 += 8 * step) {
+          int32_t page[8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-        const int pages = (int)(((int64_t)len[r0 + i] + round) >> psh);
-        const int64_t to = count + sum.back + before;
-        for (int k = tid & 31; k < pages; k += 32) {
-          const int page = a.page_table[(int64_t)(r0 + i) * a.table_stride + k];
-          if (to + k < a.free_capacity)
-            a.free_pages[to + k] = page;
-          else if (a.err != nullptr)
-            atomicOr(a.err, kErrBadLength);
+          for (int u = 0; u < 8; ++u) page[u] = i0 + u * step < pages ? __ldcg(from + i0 + u * step) : 0;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * step;
+            if (i >= pages) break;
+            if (to + i < a.free_capacity)
+              a.free_pages[to + i] = page[u];
+            else if (a.err != nullptr)
+              atomicOr(a.err, kErrBadLength);
+          }
         }
       }
+      __syncthreads();
     }
-    sum = sum + total;
-    __syncthreads();
   }
-  const int rows = (int)min(sum.rows, (int64_t)a.T);
+  const int rows = (int)min(sum, (int64_t)a.T);
   if (tid == 0) {
     start[a.R] = rows;
     if (cta == 0) a.q_start[a.R] = rows;
   }
-  const int64_t stack = min(count + sum.back, (int64_t)a.free_capacity);
+  const int64_t stack = min(count + back, (int64_t)a.free_capacity);
   cooperative_groups::this_cluster().sync();
 
   // ---- new pages, in order, off the top of the stack
@@ -155,24 +143,24 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TableArgs 
   for (int r0 = 0; r0 < a.R; r0 += kThreads) {
     const int r = r0 + tid;
     int old = 0, n = 0, have = 0;
-    Sums mine{0, 0, 0};
+    int64_t mine = 0;
     bool denied = false;
     if (r < a.R) {
       old = len[r], n = a.new_len[r];
       have = (int)(((int64_t)old + round) >> psh);
       denied = got[r] < 0;
-      if (n > 0 && !denied) mine.need = (((int64_t)old + n + round) >> psh) - have;
+      if (n > 0 && !denied) mine = (((int64_t)old + n + round) >> psh) - have;
     }
-    Sums total;
-    const Sums at = block_scan(mine, warps, &total);
+    int64_t total;
+    const int64_t first = need_before + block_scan(mine, warps[2], &total);
     if (r < a.R) {
-      const int64_t first = need_before + at.need;
-      if (mine.need > 0 && first + mine.need > stack) denied = true;
+      if (mine > 0 && first + mine > stack) denied = true;
       if (denied) complain(kErrNoPages);
       got[r] = denied ? -1 : (int)min(first, stack);
-      if (mine.need > 0 && !denied) atomicMax(&s_taken, (int)(first + mine.need));
+      if (mine > 0 && !denied) atomicMax(&s_taken, (int)(first + mine));
     }
-    need_before += total.need;
+    need_before += total;
+    if (r0 + kThreads < a.R) __syncthreads();
   }
   __syncthreads();
   if (me == 0) *a.free_count_out = (int)stack - s_taken;
