@@ -15,7 +15,9 @@ namespace pmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxSlice = 16384;
+constexpr int kPerSM = 5;
+constexpr int kInFlight = 4;  // fours of logits of a thread
+constexpr int kMaxSlice = 2 * 4 * kInFlight * kThreads;
 // A word of the table: times in the output (19 bits), in the prompt (1 bit), 1 + index of the bias (12 bits).
 constexpr uint32_t kPrompt = 1u << 19, kCount = kPrompt - 1;
 constexpr int kBiasShift = 20, kMaxBiases = 4095;
@@ -87,7 +89,7 @@ __device__ __forceinline__ void store4(void* p, int64_t i, const float (&v)[4]) 
 
 // BI, BO: logits, out in bf16
 template <bool BI, bool BO>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSM) adjust_kernel(const AdjustArgs a) {
   extern __shared__ __align__(16) uint32_t table[];  // [slice]
   pdl_wait();
   pdl_trigger();
@@ -114,14 +116,21 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   const int ao = (int)((reinterpret_cast<uintptr_t>(a.out) / (BO ? 2 : 4) + out) & 3);
   const int b0 = ai == ao ? min(v1, v0 + (int)((4 - ((ai + v0) & 3)) & 3)) : v1, quads = (v1 - b0) >> 2, b1 = b0 + 4 * quads;
   const int word0 = (4 - (b0 - v0)) & 3;  // of the slice's first id in the table, so that the four's words are aligned
-  constexpr int U = 8;                    // in flight
+  constexpr int U = kInFlight;
   Quad<BI> x[U];
+  uint32_t bits[U];
+  const bool whole = (b0 & 3) == 0;  // four logits' bits lie in one word
   auto load = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u * kThreads < quads) x[u] = load4<BI>(a.logits, in + b0 + 4 * (i0 + u * kThreads));
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads, v = b0 + 4 * i;
+      bits[u] = ~0u;
+      if (i >= quads) continue;
+      if (!a.in_place) x[u] = load4<BI>(a.logits, in + v);
+      if (mask != nullptr) bits[u] = mask[v >> 5];
+    }
   };
-  if (!a.in_place) load(tid);
+  load(tid);
 
   // ---- the table
   if (sparse) {
@@ -159,11 +168,10 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
         const int4 id = *reinterpret_cast<const int4*>(history + j0 + 4 * i);
         count(j0 + 4 * i, id.x), count(j0 + 4 * i + 1, id.y), count(j0 + 4 * i + 2, id.z), count(j0 + 4 * i + 3, id.w);
       }
-      if (part == 0) {
-        bool bad = false;
-        for (int j = tid; j < all; j += kThreads) bad |= (unsigned)history[j] >= (unsigned)a.V;
-        if (bad) complain(kErrBadToken);
-      }
+      // ids outside the vocabulary: each slice looks through a part of them
+      bool bad = false;
+      for (int j = part * kThreads + tid; j < all; j += a.slices * kThreads) bad |= (unsigned)history[j] >= (unsigned)a.V;
+      if (bad && a.err != nullptr) atomicOr(a.err, kErrBadToken);
     }
     __syncthreads();
   }
@@ -184,19 +192,14 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustArgs a) {
   if (tid < v1 - b1) one(b1 + tid);
   const uint4* words = reinterpret_cast<const uint4*>(table + word0 + b0 - v0);
   for (int i0 = tid; i0 < quads; i0 += U * kThreads) {
-    if (!a.in_place && i0 != tid) load(i0);
+    if (i0 != tid) load(i0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kThreads, v = b0 + 4 * i;
       if (i >= quads) break;
-      uint32_t on = 15;
-      if (mask != nullptr) {
-        // 4 bits from v on, of one word or two
-        const int w = v >> 5, s = v & 31;
-        on = mask[w] >> s;
-        if (s > 28) on |= mask[w + 1] << (32 - s);
-        on &= 15;
-      }
+      uint32_t on = __funnelshift_r(bits[u], bits[u], v);  // (by v mod 32)
+      if (!whole && mask != nullptr && (v & 31) > 28) on = __funnelshift_r(bits[u], mask[(v >> 5) + 1], v);
+      on &= 15;
       const uint4 e = sparse ? words[i] : make_uint4(0, 0, 0, 0);
       const bool touched = (e.x | e.y | e.z | e.w) != 0;
       if (a.in_place) {
@@ -247,10 +250,12 @@ extern "C" int moe_adjust_logits(const void* logits, int is_bf16, int T, int V, 
   AdjustArgs a{logits,    out,        row_stride, out_stride, T,      V,    in_place, history, history_stride, max_history,
                prompt_len, history_len, repetition, frequency,  presence, bias_ids, bias,     biases,  mask,           mask_stride,
                err_out,   0,          0};
-  // slices as large as leaves four an SM: each looks at the row's whole history
+  // Each slice looks at its row's whole history, so they are as large as leaves every SM its share, and no
+  // larger than two turns of the logits in flight: 256 rows of 160,001 in slices of 16,384, 8,192, 4,096 89, 76, 97 us.
   a.slice = kMaxSlice;
-  while (a.slice > 1024 && (int64_t)T * ((V + a.slice - 1) / a.slice) < 608) a.slice /= 2;
+  while (a.slice > 1024 && (int64_t)T * ((V + a.slice - 1) / a.slice) < 152 * kPerSM) a.slice /= 2;
   a.slices = (V + a.slice - 1) / a.slice;
+  a.slice = ((V + a.slices - 1) / a.slices + 3) / 4 * 4;  // all alike
   if ((int64_t)T * a.slices > INT32_MAX) return PMOE_EINVAL;
   static SmemLimit limits[4];
   const size_t smem = max_history > 0 || biases > 0 ? (size_t)a.slice * 4 + 16 : 0;
