@@ -32,7 +32,9 @@ struct SelectArgs {
   float scale;
   int32_t* ids;
   float* w;
+  int size;   // experts of a group
   int lanes;  // of a group, where it is a power of two of whole lanes; else 0
+  int shift;  // log2 of the lanes that work on a group
 };
 
 // Keys that order like the values; 0 stands below all of them.
@@ -264,20 +266,24 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
   // ---- what decides: c, or without a bias the logits themselves
   const bool by_logits = a.bias == nullptr, scored = !by_logits || (a.groups > 1 && a.group_top > 1);
   uint32_t key[N], group_key[N];
+  auto there = [&](int k) { return VEC || lane * N + k < a.E; };
+  if (!scored) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float c = scored ? fmaxf(score(x[k]) + bias[k], -INFINITY) : x[k] + 0.f;
-    group_key[k] = lane * N + k < a.E ? key_of(c) : 0;
-    key[k] = by_logits && scored && group_key[k] != 0 ? key_of(x[k] + 0.f) : group_key[k];
+    for (int k = 0; k < N; ++k) key[k] = group_key[k] = there(k) ? key_of(x[k]) : 0;
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) key[k] = group_key[k] = there(k) ? key_of(fmaxf(score(x[k]) + bias[k], -INFINITY)) : 0;
+    if (by_logits) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) key[k] = there(k) ? key_of(x[k]) : 0;
+    }
   }
 
   // ---- the groups
   if (a.groups > 1) {
-    const int size = a.E / a.groups;
-    uint32_t m1 = 0, m2 = 0;  // the two largest of a group
-    int g, per;               // this lane's group, lanes of a group
-    if (a.lanes > 0) {        // groups of whole lanes, a power of two of them
-      g = lane / a.lanes, per = a.lanes;
+    const int size = a.size, per = 1 << a.shift, g = lane >> a.shift;  // this lane's group, lanes of a group
+    uint32_t m1 = 0, m2 = 0;                                           // the two largest of a group
+    if (a.lanes > 0) {  // groups of whole lanes, a power of two of them
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         m2 = max(m2, min(m1, group_key[k]));
@@ -288,11 +294,8 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
       for (int k = 0; k < N; ++k)
         if (lane * N + k < a.E) choice[lane * N + k] = value_of(group_key[k]);
       __syncwarp();
-      per = 32;
-      while (per * a.groups > 32) per >>= 1;
-      g = lane / per;
       if (g < a.groups)
-        for (int i = lane % per; i < size; i += per) {
+        for (int i = lane & (per - 1); i < size; i += per) {
           const uint32_t c = key_of(choice[g * size + i]);
           m2 = max(m2, min(m1, c));
           m1 = max(m1, c);
@@ -307,14 +310,16 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
     float value = a.group_top > 1 && size > 1 ? value_of(m1) + value_of(m2) : value_of(m1);
     value = fmaxf(value, -INFINITY);  // (infinities of both signs)
     int rank = 0;  // of equal groups the first is better
+    const uint32_t mark = key_of(value);
+#pragma unroll 4
     for (int k = 0; k < a.groups; ++k) {
-      const float other = __shfl_sync(0xffffffffu, value, k * per);
-      rank += other > value || (other == value && k < g);
+      const uint32_t other = __shfl_sync(0xffffffffu, mark, k << a.shift);
+      rank += other >= mark + (k < g ? 0 : 1);
     }
     bool in = g < a.groups && rank < a.top_groups;
     if (scored) {
       // the worst that is kept against the best that is not: sums of two scores of at most 1 each
-      const uint32_t worst = ~warp_max(in ? ~key_of(value) : 0u), best = warp_max(g < a.groups && !in ? key_of(value) : 0u);
+      const uint32_t worst = ~warp_max(in ? ~mark : 0u), best = warp_max(g < a.groups && !in ? mark : 0u);
       if (unsure(value_of(worst) - (a.sigmoid ? 7e-7f : 0.f), 2.f, value_of(best), 2.f)) {
         if (!a.sigmoid) return false;
         // each group's two largest in fp64: those that come near its second, one a lane
@@ -329,7 +334,7 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
           for (int j = 0; j < N; ++j)
             if (j == k) c = value_of(group_key[j]);
           if (e < a.E) group = e / size;
-          const float bound = __shfl_sync(0xffffffffu, near, max(group, 0) * per);
+          const float bound = __shfl_sync(0xffffffffu, near, max(group, 0) << a.shift);
           const uint32_t takes = __ballot_sync(0xffffffffu, group >= 0 && !(c < bound));
           const int at = n + __popc(takes & ((1u << lane) - 1));
           if (takes >> lane & 1 && at < 32) list[at].y = e;
@@ -487,11 +492,13 @@ int launch_select(SelectArgs a, cudaStream_t s) {
   do {                                                                                                                    \
     static SmemLimit limits[2];                                                                                           \
     const bool vec = a.E == 32 * N && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * (BF16 ? 2 : 4) % 16 == 0; \
-    const int size = a.E / a.groups;                                                                                      \
-    a.lanes = size % N == 0 && (size / N & (size / N - 1)) == 0 ? size / N : 0;                                           \
+    a.size = a.E / a.groups;                                                                                              \
+    a.lanes = a.size % N == 0 && (a.size / N & (a.size / N - 1)) == 0 ? a.size / N : 0;                                   \
+    a.shift = 0;                                                                                                          \
+    while (a.lanes > 0 ? 1 << a.shift < a.lanes : a.groups << (a.shift + 1) <= 32) ++a.shift;                             \
     const auto kernel = vec ? select_kernel<N, BF16, true> : select_kernel<N, BF16, false>;                               \
     const int r = limits[vec].set(reinterpret_cast<const void*>(kernel), kWarps * N * 32 * 8, what);                      \
-    const unsigned blocks = (unsigned)std::min((a.T + kWarps - 1) / kWarps, 152 * 6);                                     \
+    const unsigned blocks = (unsigned)std::min((a.T + kWarps - 1) / kWarps, 152 * 4);                                     \
     return r != PMOE_OK ? r : launch(what, kernel, blocks, kWarps * 32, kWarps * N * 32 * 8, s, true, 1, a);                            \
   } while (0)
   if (npl <= 1) PMOE_SELECT_CASE(1);
@@ -521,6 +528,6 @@ extern "C" int moe_router_select(const void* logits, int is_bf16, int T, int E, 
   if (off(logits, is_bf16 ? 2 : 4) || (bias != nullptr && off(bias, 4)) || off(ids_out, 4) || off(w_out, 4)) return PMOE_EINVAL;
   const bool grouped = groups > 1 && top_groups < groups;  // all groups kept: no choice among them
   const SelectArgs a{logits, row_stride, T, E, top_k, scoring == PMOE_SCORE_SIGMOID, bias, grouped ? groups : 1,
-                     grouped ? top_groups : 1, group_top, renormalize != 0, scale, ids_out, w_out, 0};
+                     grouped ? top_groups : 1, group_top, renormalize != 0, scale, ids_out, w_out, 0, 0, 0};
   return is_bf16 ? launch_select<true>(a, (cudaStream_t)stream) : launch_select<false>(a, (cudaStream_t)stream);
 }
