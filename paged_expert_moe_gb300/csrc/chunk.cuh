@@ -108,6 +108,8 @@ struct __align__(16) Segment {
   __device__ __forceinline__ int h() const { return bits >> 13; }
   __device__ __forceinline__ int p1() const { return p0 + ntok() - 1; }
   __device__ __forceinline__ bool has(int q) const { return two() || lane() == q; }
+  // Whose scores' place tile t of a segment of one query tile takes: in turn both query tiles', its own last.
+  __device__ __forceinline__ int place(int t) const { return ((t1 - 1 - t) & 1) ^ lane(); }
   __device__ __forceinline__ bool partly(int t) const { return t >= part2 || (t >= part0 && t < part1); }
 };
 // The first key of tile t.

@@ -201,6 +201,11 @@ struct Cfg {
   }
   static constexpr int kSmem = kRing + kRawRing + kQBytes + 1024 /* alignment */ + 1024 /* row exponents */ + 1024;
   static constexpr int kTmemCols = 512;                   // S0 S1 at 0 and 128, O0 O1 at 256 and 384
+  // Whether segments of one query tile have their scores made two tiles ahead, in both query tiles' places: a chain
+  // of few rows' tiles then has no wait for scores in it. 64 single tokens on 16,000 keys at most: heads of 64
+  // 199 us (without 245), prompt of 8,192 tokens 331 (318). Not with e4m3 (225 / 267, but 377 / 359), whose softmax
+  // has no registers left for it, and not with heads of 128 (189 / 172), whose ring is too short.
+  static constexpr bool kAhead = D == 64 && !F8;
   static constexpr int kGuards = F8 ? 4 : 2;              // warps that look at partly visible values
 };
 
@@ -209,7 +214,7 @@ constexpr int kSegs = 8;
 struct Bars {
   uint64_t full[8], empty[8], raw[8];
   uint64_t vok[8];  // partly visible values are cleared
-  uint64_t sfull[2], pready[2], odone[2], joined[2], qfull, qraw, qempty, drain;
+  uint64_t sfull[4] /* by query tile and place */, pready[2] /* by place */, odone[2], joined[2], qfull, qraw, qempty, drain;
   uint32_t tmem;
   int abort;
   int last[2];  // whether a query tile's last part was the item's
@@ -434,7 +439,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       mbar_init(&b.vok[i], C::kGuards);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b.sfull[i], 1);
+      mbar_init(&b.sfull[2 * i], 1);
+      mbar_init(&b.sfull[2 * i + 1], 1);
       mbar_init(&b.pready[i], 4);
       mbar_init(&b.odone[i], 1);
       mbar_init(&b.joined[i], 4);
@@ -479,11 +485,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     const int q = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lanes + q * 128, to = lanes + 256 + q * 128;
-    uint32_t n = 0, segs = 0;   // tiles and segments of this query tile so far
+    const uint32_t to = lanes + 256 + q * 128;
+    uint32_t segs = 0;         // segments of this query tile so far
+    uint32_t n = 0, other = 0;  // its tiles with the scores in its place, in the other's
+    uint32_t tiles = 0;        // key tiles so far
     bool ok = true;
-    for (uint32_t all = 0; ok && get_segment(b, all, &sg, abort_flag, a.err); ++all) {
+    for (uint32_t all = 0; ok && get_segment(b, all, &sg, abort_flag, a.err); tiles += sg.t1 - sg.t0, ++all) {
       if (!sg.has(q)) continue;
+      const bool ahead = C::kAhead && !sg.two();
       const int i = (sg.two() ? q * 128 : 0) + row;  // row of the item
       const int rows = sg.ntok() * a.group;
       const bool live = i - lane < rows;           // any row of this warp
@@ -495,13 +504,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       const bool negate = (a.scale < 0.f) != (ks < 0.f);
       float mul = 1.f;
       float m = -INFINITY, l = 0.f;
-      for (int t = sg.t0; t < sg.t1; ++t, ++n) {
-        if (!warp_wait(&b.sfull[q], n & 1, abort_flag, a.err)) {
+      for (int t = sg.t0; t < sg.t1; ++t) {
+        const int place = ahead ? sg.place(t) : q;
+        const uint32_t turn = place == q ? n++ : other++;
+        const uint32_t ts = lanes + place * 128;
+        if (!warp_wait(&b.sfull[q * 2 + place], turn & 1, abort_flag, a.err)) {
           ok = false;
           break;
         }
         if (!live) {  // (whatever the scores are, as weights they reach their own rows only)
-          warp_arrive(&b.pready[q]);
+          warp_arrive(&b.pready[place]);
           continue;
         }
         fence_after();
@@ -546,7 +558,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         } else {
           const bool grow = mx > m + 8.f;
           if (__any_sync(0xffffffffu, grow)) {
-            // the products so far are done: these scores were issued after them
+            // the products so far are done: these scores were issued after them, or the last one's values are
+            // released
+            if (ahead) {
+              const uint32_t i = 2 * (tiles + t - sg.t0) - 1;
+              if (!warp_wait(&b.empty[i % kSlots], i / kSlots & 1, abort_flag, a.err)) {
+                ok = false;
+                break;
+              }
+              fence_after();
+            }
             const float f = grow ? ex2(m - mx) : 1.f;
             if (grow) m = mx;
             l *= f;
@@ -580,7 +601,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         }
         tmem_wait_st();
         fence_before();
-        warp_arrive(&b.pready[q]);
+        warp_arrive(&b.pready[place]);
         float y, z;
         unpair(add2(sum[0], sum[1]), y, z);
         l += y + z;
@@ -696,25 +717,25 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         return __all_sync(0xffffffffu, rx && ry && rz) != 0;
       };
       auto wait_kv = [&](uint32_t i) { return wait(&b.full[i % kSlots], i / kSlots); };
-      // scores by query tile q, whose rows are at qq; the last query tile's are the last on this K tile,
+      // scores by query tile q, whose rows are at qq, to a place in TMEM; the last query tile's are the last on this K tile,
       // and with a segment's last tile on its q
-      auto scores = [&](int q, uint32_t qq, uint32_t slot, bool last, bool end) {
+      auto scores = [&](int q, int place, uint32_t qq, uint32_t slot, bool last, bool end) {
         if (converged_lane()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t in = (k % 4) * 32;
-            mma_bf16(tmem + q * 128, sw128_desc(qq + (k / 4) * (kRows * 128) + in),
+            mma_bf16(tmem + place * 128, sw128_desc(qq + (k / 4) * (kRows * 128) + in),
                      sw128_desc(ring + slot * C::kTileBytes + (k / 4) * (kKeys * 128) + in), is, k > 0);
           }
-          mma_commit(&b.sfull[q]);
+          mma_commit(&b.sfull[q * 2 + place]);
           if (last) mma_commit(&b.empty[slot]);
           if (end) mma_commit(&b.qempty);
         }
         __syncwarp();
       };
       // weights x values of tile t of sg by query tile q
-      auto products = [&](int t, int q, uint32_t slot, bool last) {
-        const uint32_t o = tmem + 256 + q * 128, p = tmem + q * 128, v = ring + slot * C::kTileBytes;
+      auto products = [&](int t, int q, int place, uint32_t slot, bool last) {
+        const uint32_t o = tmem + 256 + q * 128, p = tmem + place * 128, v = ring + slot * C::kTileBytes;
         if (converged_lane()) {
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k) mma_f16_ts(o, p + k * 8, v_desc(v + k * 2048), io, t > sg.t0 || k > 0);
@@ -723,8 +744,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         __syncwarp();
       };
       // the same of any tile: of a partly visible one only the steps of 16 keys that some row sees
-      auto any_products = [&](int t, int q, uint32_t slot, bool last) {
-        const uint32_t o = tmem + 256 + q * 128, p = tmem + q * 128, v = ring + slot * C::kTileBytes;
+      auto any_products = [&](int t, int q, int place, uint32_t slot, bool last) {
+        const uint32_t o = tmem + 256 + q * 128, p = tmem + place * 128, v = ring + slot * C::kTileBytes;
         int step0 = 0, step1 = kKeys / 16;
         if (sg.partly(t)) {
           const Span pt = seen_span<kKeys>(a, sg, tile_key<kKeys>(a, sg, t));
@@ -752,7 +773,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         const bool end = s.t0 + 1 == s.t1;
         for (int q = s.two() ? 0 : s.lane(); q < (s.two() ? 2 : s.lane() + 1); ++q) {
           const bool last = !s.two() || q == 1;
-          scores(q, q_rows(s, q), slot, last, last && end);
+          scores(q, C::kAhead && !s.two() ? s.place(s.t0) : q, q_rows(s, q), slot, last, last && end);
         }
       };
       bool ok = true, have = get_segment(b, 0, &sg, abort_flag, a.err);
@@ -764,6 +785,35 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
       while (ok && have) {
         const int qb = sg.two() ? 0 : sg.lane(), qe = sg.two() ? 2 : sg.lane() + 1;
         int t = sg.t0;
+        if (C::kAhead && !sg.two()) {
+          // scores two tiles ahead, in turn in both query tiles' places: the second tile's now, the others' with the
+          // products of the tile whose place they take
+          auto next = [&](int u, uint32_t i) {
+            if (!wait_kv(i)) return false;
+            fence_after();
+            scores(qb, sg.place(u), qa, i % kSlots, true, u + 1 == sg.t1);
+            return true;
+          };
+          if (t + 1 < sg.t1) ok = next(t + 1, kv + 2);
+          for (; ok && t + 1 < sg.t1; ++t, kv += 2) {
+            const int place = sg.place(t);
+            const bool plain = t + 2 < sg.t1 && !sg.partly(t);
+            const bool all = plain && there(&b.full[(kv + 1) % kSlots], (kv + 1) / kSlots, &b.pready[place], pn[place],
+                                            &b.full[(kv + 4) % kSlots], (kv + 4) / kSlots);
+            if (!all && !(wait_v(t, kv + 1) && wait(&b.pready[place], pn[place]))) {
+              ok = false;
+              break;
+            }
+            ++pn[place];
+            fence_after();
+            if (plain)
+              products(t, qb, place, (kv + 1) % kSlots, true);
+            else
+              any_products(t, qb, place, (kv + 1) % kSlots, true);
+            if (t + 2 < sg.t1) ok = next(t + 2, kv + 4);
+          }
+          if (!ok) break;
+        }
         // (a query tile's weights come after it has read its accumulators of the segment before)
         while (t + 1 < sg.t1) {
           // a run of tiles that all rows see, in as few instructions as can be: this warp's are what the
@@ -784,8 +834,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               }
               ++pn[q];
               fence_after();
-              products(t, q, vslot, q + 1 == qe);
-              scores(q, q_rows(sg, q), kslot, q + 1 == qe, end && q + 1 == qe);
+              products(t, q, q, vslot, q + 1 == qe);
+              scores(q, q, q_rows(sg, q), kslot, q + 1 == qe, end && q + 1 == qe);
             }
             if (!ok) break;
           }
@@ -802,8 +852,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             ++pn[q];
             fence_after();
-            any_products(t, q, (kv + 1) % kSlots, q + 1 == qe);
-            scores(q, q_rows(sg, q), (kv + 2) % kSlots, q + 1 == qe, t + 2 == sg.t1 && q + 1 == qe);
+            any_products(t, q, q, (kv + 1) % kSlots, q + 1 == qe);
+            scores(q, q, q_rows(sg, q), (kv + 2) % kSlots, q + 1 == qe, t + 2 == sg.t1 && q + 1 == qe);
           }
           if (!ok) break;
           ++t, kv += 2;
@@ -816,7 +866,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         if (__any_sync(0xffffffffu, *abort_flag)) break;
         const uint32_t vslot = (kv + 1) % kSlots, kslot = (kv + 2) % kSlots;
         const bool early = more && __all_sync(0xffffffffu, mbar_try_wait(&b.qfull, (segs + 1) & 1));
-        const bool first = early && !sg.two() && !nx.two();  // the other query tile's turn: at once
+        // the other query tile's turn: at once, where the place of its scores is not still to be read
+        const bool first = early && !sg.two() && !nx.two() && (!C::kAhead || nx.place(nx.t0) != sg.lane());
+        const bool late = !early || (C::kAhead && !nx.two() && !first);
         if (early && !wait_kv(kv + 2)) break;
         fence_after();
         if (first) first_scores(nx, kslot);
@@ -829,16 +881,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
             }
             ++pn[q];
             fence_after();
-            any_products(t, q, vslot, q + 1 == qe);
+            any_products(t, q, q, vslot, q + 1 == qe);
           }
-          if (early && !first && nx.has(q)) {
+          if (!late && !first && nx.has(q)) {
             const bool last = !nx.two() || q == 1;
-            scores(q, q_rows(nx, q), kslot, last, last && nx.t0 + 1 == nx.t1);
+            scores(q, q, q_rows(nx, q), kslot, last, last && nx.t0 + 1 == nx.t1);
           }
         }
         if (!ok) break;
-        if (more && !early) {
-          if (!wait(&b.qfull, segs + 1) || !wait_kv(kv + 2)) break;
+        if (more && late) {
+          if (!early && (!wait(&b.qfull, segs + 1) || !wait_kv(kv + 2))) break;
           fence_after();
           first_scores(nx, kslot);
         }
