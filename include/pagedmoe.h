@@ -579,8 +579,8 @@ PMOE_API int moe_batch_tables(int32_t* page_table, int table_stride, int page_si
  * <= p of the pages page_table[r][..]; with a window only those with j > p - window or j <
  * sinks. out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j, lse[t][h] = log sum_j
  * exp(scale * q[t][h] . k_j). A row that sees no key (p < 0) gets out = 0, lse = -inf. What the cache
- * holds in rows that a query does not see is never used, whatever it is; rows of q outside all
- * requests are not read, and left as they were in out and lse.
+ * holds in rows that a query does not see is never used, whatever it is; rows outside all requests
+ * are left as they were in out and lse, and what q holds there is not used.
  * Statistics and sums are fp32; the weights are rounded to 16 bits before they meet the
  * values (bf16, or fp16 with an e4m3 cache).
  *   q            device bf16 [T][q_heads][head_dim], tokens q_stride elements apart; 16-byte

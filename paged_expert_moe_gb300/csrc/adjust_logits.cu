@@ -5,8 +5,10 @@
 // of which it counts what falls into its slice. Then the slice's logits go by once, four a thread with their
 // four words. The counts are whole numbers, so their order does not matter.
 //
-// Bound: HBM, the logits read and written once. The first logits are on their way while the history is
-// counted.
+// Bound: HBM, the logits read and written once, and the history's counting, in which a CTA waits for its
+// atomics. The first logits and mask words are on their way meanwhile. 256 fp32 rows of 160,001 with 2,000 ids of
+// history at most 70 us (50 without; a plain copy 56), 64 bf16 rows of 131,072 to fp32 with 4,000 20 us (10
+// without; a copy 17, cold caches 27), one row 3.5 us.
 #include "pmoe_internal.h"
 
 #include <math.h>

@@ -9,6 +9,9 @@
 // bytes) and keeps what tokens look up in shared memory; the cluster's barrier stands between the
 // ended requests' pages arriving on the stack and the new pages leaving it, and between the last
 // read of the lengths and their update in place. Tokens are then spread over the cluster's threads.
+// 256 requests of a token each take 6.5 us, 1,000 with 32,768 rows 11 us: three block-wide sums, two
+// cluster barriers and two rounds of loads. Four tokens of a thread at a time, so that their searches
+// overlap, cost the small call 0.6 us and gave the large one 0.3: not kept.
 #include "pmoe_internal.h"
 
 #include <cooperative_groups.h>
