@@ -589,7 +589,8 @@ PMOE_API int moe_batch_tables(int32_t* page_table, int table_stride, int page_si
  *   kv_len       device int32 [R], keys of each request, its new ones among them
  *   page_table   device int32 [R][table_stride], table_stride * page_size <= 2^30
  *   window       0: none; sinks: the first keys that stay visible beside it (without one: unused)
- *   out          device bf16 [T][q_heads][head_dim], 16-byte aligned
+ *   out          device bf16 [T][q_heads][head_dim], 16-byte aligned; neither it nor lse nor
+ *                scratch may overlap what the call reads (out = q is refused)
  *   lse          device fp32 [T][q_heads], or NULL
  *   scratch      device, 16-byte aligned, moe_chunk_attention_scratch_bytes(...) bytes, for one
  *                call at a time

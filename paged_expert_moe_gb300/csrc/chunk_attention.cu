@@ -1276,7 +1276,7 @@ extern "C" int moe_chunk_attention(const pmoe_kv_desc* kv, const void* q, int64_
   // arguments first: the plan asks the device for its size
   if (check_kv(kv) == PMOE_OK && T > 0 && R > 0) {
     auto off = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
-    if (q == nullptr || out == nullptr || off(q, 16) || off(out, 16) || q_stride % 8 != 0 ||
+    if (q == nullptr || out == nullptr || q == out || off(q, 16) || off(out, 16) || q_stride % 8 != 0 ||
         q_stride < (int64_t)q_heads * kv->head_dim || !(fabsf(scale) < INFINITY))
       return PMOE_EINVAL;
     if (q_start == nullptr || kv_len == nullptr || page_table == nullptr || off(q_start, 4) || off(kv_len, 4) ||

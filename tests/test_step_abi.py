@@ -76,6 +76,10 @@ def test_attention_refuses(pm, change):
     assert attend(pm, desc(pm), **change) == EINVAL
 
 
+def test_attention_refuses_its_queries_as_outputs(pm):
+    assert attend(pm, desc(pm), out=0x40000) == EINVAL
+
+
 def test_attention_refuses_large_groups(pm):
     assert attend(pm, desc(pm), hq=130, qs=130 * 64) == EUNSUPPORTED
 
