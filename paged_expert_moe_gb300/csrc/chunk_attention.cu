@@ -7,7 +7,7 @@
 // what they see only in its last key tiles and at a window's edge; all others take no masks.
 //
 // Work: the lengths are on the device, so each CTA adds up the key tiles that all tiles of rows need
-// and takes its share, one of equal runs, one CTA an SM. What a run has of a tile of rows without having
+// and takes its share, one of (nearly) equal runs, one CTA an SM. What a run has of a tile of rows without having
 // all of it is left as a part in scratch; whoever writes the last part of a tile joins them, in order.
 //
 // Warps: 0-3 and 4-7 own one query tile each, a thread one row (a TMEM lane): scores from TMEM,
@@ -77,15 +77,15 @@ struct PlanSmem {
   int start[NT], n[NT], len[NT];
 };
 
-// The start of this CTA's run, by all NT threads: the units of all items are added up, NT requests and NT
-// items at a time, and the item with the run's first unit is looked for; where one turn has them all it is
-// at hand, else in a second pass.
+// The start and end of this CTA's run, by all NT threads: the units of all items are added up, NT requests and
+// NT items at a time, and the items that its boundaries lie in are looked for; where one turn has them all
+// they are at hand, else in a second pass.
 template <int NT>
 __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
   const int tid = threadIdx.x;
   int64_t units = 0;
   int ctas = 0;
-  if (tid == 0) run->left = 0;
+  if (tid == 0) run->u = run->end = 0;
   for (int pass = 0; pass < 2; ++pass) {
     int64_t sum = 0, rows = 0;
     for (int r0 = 0; r0 < a.R; r0 += NT) {
@@ -103,7 +103,7 @@ __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
       __syncthreads();
       for (int j0 = 0; j0 < all; j0 += NT) {
         const int j = j0 + tid;
-        int lo = 0, hi = NT, len = 0, i = 0;  // upto[lo] <= j < upto[hi]
+        int lo = 0, hi = NT, len = 0, i = 0, ntok = 0;  // upto[lo] <= j < upto[hi]
         if (j < all) {
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -115,7 +115,8 @@ __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
           i = j - m.upto[lo];
           const int i0 = i * a.tile_tokens;
           int first;
-          len = a.head + key_tiles(a, m.len[lo] - m.n[lo] + i0, min(a.tile_tokens, m.n[lo] - i0), &first);
+          ntok = min(a.tile_tokens, m.n[lo] - i0);
+          len = a.head + key_tiles(a, m.len[lo] - m.n[lo] + i0, ntok, &first);
         }
         int64_t more;
         const int64_t base = sum + block_scan<NT>((int64_t)len * a.kv.kv_heads, m.warps, &more);
@@ -125,13 +126,21 @@ __device__ void find_run(const Args& a, PlanSmem<NT>& m, Run* run) {
         if (pass == 1 || single) {
           // runs of four units at least
           ctas = (int)min((int64_t)a.ctas, (units + 3) / 4);
-          const int64_t u = run_start(units, ctas, blockIdx.x), in = u - base;
-          if ((int)blockIdx.x < ctas && in >= 0 && in < (int64_t)len * a.kv.kv_heads) {
-            const int h = in >> 32 ? (int)(in / len) : (int)((uint32_t)in / (uint32_t)len);
-            run->units = units, run->left = run_start(units, ctas, blockIdx.x + 1) - u, run->u = u;
-            run->ctas = ctas, run->req = r0 + lo, run->tile = i, run->h = h, run->at = (int)(in - (int64_t)h * len);
-            run->start = m.start[lo], run->n = m.n[lo], run->len = m.len[lo], run->before = m.rows[lo];
-          }
+          if ((int)blockIdx.x < ctas)
+            for (int side = 0; side < 2; ++side) {
+              const int64_t in = run_start(units, ctas, blockIdx.x + side) - base;
+              if (in < 0 || in >= (int64_t)len * a.kv.kv_heads) continue;
+              const int h = in >> 32 ? (int)(in / len) : (int)((uint32_t)in / (uint32_t)len);
+              const int at = moved(a, units, ctas, (int)(in - (int64_t)h * len), len, ntok);
+              const int64_t u = base + (int64_t)h * len + at;
+              if (side == 1) {
+                run->end = u;
+              } else {
+                run->u = u, run->units = units, run->ctas = ctas, run->req = r0 + lo, run->tile = i, run->h = h, run->at = at;
+                run->start = m.start[lo], run->n = m.n[lo], run->len = m.len[lo], run->before = m.rows[lo];
+              }
+            }
+          if (tid == 0 && (int)blockIdx.x + 1 == ctas) run->end = units;
         }
         if (single) pass = 2;
       }
@@ -168,19 +177,28 @@ __device__ __forceinline__ void find_run_of_few(const Args& a, int8_t* list, Run
   const int i = lane - __shfl_sync(0xffffffffu, upto - tiles, r), start = __shfl_sync(0xffffffffu, q.start, r),
             n = __shfl_sync(0xffffffffu, q.n, r), len = __shfl_sync(0xffffffffu, q.len, r);
   const int64_t before = __shfl_sync(0xffffffffu, rows, r);
+  const int ntok = min(a.tile_tokens, n - i * a.tile_tokens);
   int span = 0, lo;
-  if (live) span = a.head + key_tiles(a, len - n + i * a.tile_tokens, min(a.tile_tokens, n - i * a.tile_tokens), &lo);
+  if (live) span = a.head + key_tiles(a, len - n + i * a.tile_tokens, ntok, &lo);
   const int64_t mine = (int64_t)span * a.kv.kv_heads, end = scan(mine), units = __shfl_sync(0xffffffffu, end, 31);
   const int ctas = (int)min((int64_t)a.ctas, (units + 3) / 4);
-  int64_t u = 0, left = 0;
-  if ((int)blockIdx.x < ctas) u = run_start(units, ctas, blockIdx.x), left = run_start(units, ctas, blockIdx.x + 1) - u;
-  if (lane == 0) run->left = left;
-  if (left > 0 && u < end && u >= end - mine) {
-    const int64_t at = u - (end - mine);
-    const int h = at >> 32 ? (int)(at / span) : (int)((uint32_t)at / (uint32_t)span);
-    run->units = units, run->u = u, run->ctas = ctas, run->h = h, run->at = (int)(at - (int64_t)h * span);
-    run->req = r, run->tile = i, run->start = start, run->n = n, run->len = len, run->before = before;
-  }
+  if (lane == 0) run->u = 0, run->end = (int)blockIdx.x + 1 == ctas ? units : 0;
+  __syncwarp();
+  if ((int)blockIdx.x < ctas)
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const int64_t in = run_start(units, ctas, blockIdx.x + side) - (end - mine);
+      if (in < 0 || in >= mine) continue;
+      const int h = in >> 32 ? (int)(in / span) : (int)((uint32_t)in / (uint32_t)span);
+      const int at = moved(a, units, ctas, (int)(in - (int64_t)h * span), span, ntok);
+      const int64_t u = end - mine + (int64_t)h * span + at;
+      if (side == 1) {
+        run->end = u;
+      } else {
+        run->units = units, run->u = u, run->ctas = ctas, run->h = h, run->at = at;
+        run->req = r, run->tile = i, run->start = start, run->n = n, run->len = len, run->before = before;
+      }
+    }
   __syncwarp();
 }
 
