@@ -62,17 +62,24 @@ __device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) {
   return x >> 32 ? (int)(x / units) : (int)((uint32_t)x / (uint32_t)units);
 }
 
-// A run's boundary moves to the start or the end of an item that it would cut this many tiles from there, or fewer:
-// of many rows a part and its join cost more than two tiles (a prompt of 512 tokens 17.8 us instead of 29.6, of 1,024
-// 33.7 / 48.0, 8 of 300 25.5 / 37.3), of few they do not (4 single tokens with 0, 1, 2 18.6, 19.4, 20.9). In longer runs
-// there is little to win, and the unevenness costs (61 tokens and 3 pieces of 1,500, runs of 50 units: 243 / 223).
+// Cutting an item costs a part and a join, some four tiles of few rows and more of many. So where runs are
+// short a run's boundary moves to the start or the end of its item, whichever is nearer, if the item is
+// short too, and else if it lies within `slack` tiles of it. Measured with 14 / 0 tiles as short for more than 32
+// rows: prompts of 512 tokens 17.8 / 29.6 us, 1,024 24.7 / 48, 1,600 41 / 49, 4 of 1,000 55 / 69, 400 on 900 keys 28.6 / 36
+// (16: 2,048 tokens, heads of 64, 53 / 47); with 6 / 0 for few: one token on 500 keys 14.2 / 16.8, 16 on 600 17.3 / 20.6. In runs of
+// 50 units slack of 2 costs more unevenness than it saves (61 tokens and 3 pieces of 1,500 243 / 223), and for few
+// rows it never pays (4 tokens on 2,000 keys with 0, 1, 2 18.6, 19.4, 20.9).
+__device__ __forceinline__ bool short_run(int64_t units, int ctas, int limit) { return units < (int64_t)limit * ctas; }
 __device__ __forceinline__ int slack(const Args& a, int64_t units, int ctas, int ntok) {
-  return ntok * a.group > 32 && units < 12ll * ctas ? 2 : 0;
+  return ntok * a.group > 32 && short_run(units, ctas, 12) ? 2 : 0;
+}
+__device__ __forceinline__ bool never_cut(const Args& a, int64_t units, int ctas, int tiles, int ntok) {
+  return ntok * a.group > 32 ? tiles <= 14 && short_run(units, ctas, 48) : tiles <= 6 && short_run(units, ctas, 12);
 }
 // Where a boundary at unit `at` of an item's n goes.
 __device__ __forceinline__ int moved(const Args& a, int64_t units, int ctas, int at, int n, int ntok) {
-  const int behind = max(at - a.head, 0), ahead = n - at, s = slack(a, units, ctas, ntok);
-  if (min(behind, ahead) > s) return at;
+  const int behind = max(at - a.head, 0), ahead = n - at;
+  if (min(behind, ahead) > slack(a, units, ctas, ntok) && !never_cut(a, units, ctas, n - a.head, ntok)) return at;
   return behind <= ahead ? 0 : n;
 }
 
