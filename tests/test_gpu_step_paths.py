@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 from tests import test_gpu_batch_tables as tables
+from tests import test_gpu_router_select as selection
 from tests.test_gpu_chunk_attention import check, make, poison_unseen, run, up
 
 torch = pytest.importorskip("torch")
@@ -181,3 +182,17 @@ def test_a_stack_without_room_for_what_comes_back(pm):
     back = np.concatenate([c["table"][r, :have[r]] for r in range(30)])
     assert err == 128 and int(got[3]) == whole // 2
     assert np.array_equal(got[1].cpu().numpy(), back[:whole // 2])
+
+
+@pytest.mark.parametrize("E,groups,top_groups,k", [(96, 1, 1, 5), (96, 8, 3, 7), (160, 8, 3, 8), (160, 4, 2, 6), (192, 6, 2, 10),
+                                                   (192, 32, 9, 8), (384, 1, 1, 32), (384, 12, 4, 6), (512, 16, 4, 8), (1024, 32, 8, 32)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_selection_with_any_share_of_a_lane(pm, E, groups, top_groups, k, bf16):
+    """Experts a lane 3, 5, 6, 12, 16 and 32, in groups of whole lanes and of others; rows aligned or not."""
+    g = torch.Generator(device="cuda").manual_seed(E + groups)
+    T = 700
+    wide = torch.randn((T, E + 8), generator=g, device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1
+    for logits in (wide[:, :E].contiguous(), wide[:, 1:E + 1]):
+        for scoring in ("sigmoid", "softmax"):
+            selection.check(pm, logits, k, scoring, bias, groups, top_groups, 2)
