@@ -312,7 +312,8 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
       m2 = max(min(m1, n1), max(m2, n2));
       m1 = max(m1, n1);
     }
-    float value = a.group_top > 1 && size > 1 ? value_of(m1) + value_of(m2) : value_of(m1);
+    const bool pairs = a.group_top > 1 && size > 1;
+    float value = pairs ? value_of(m1) + value_of(m2) : value_of(m1);
     value = fmaxf(value, -INFINITY);  // (infinities of both signs)
     int rank = 0;  // of equal groups the first is better
     const uint32_t mark = key_of(value);
@@ -323,9 +324,14 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
     }
     bool in = g < a.groups && rank < a.top_groups;
     if (scored) {
-      // the worst that is kept against the best that is not: sums of two scores of at most 1 each
-      const uint32_t worst = ~warp_max(in ? ~mark : 0u), best = warp_max(g < a.groups && !in ? mark : 0u);
-      if (unsure(value_of(worst) - (a.sigmoid ? 7e-7f : 0.f), 2.f, value_of(best), 2.f)) {
+      // What each value may be off by: two scores, of at most 1 each, and 2^-24 of either c, of their sum and of
+      // the bounds. The c of a group may cancel, so the sum says nothing of their own errors. All that is
+      // kept has to lie above all that is not. (-inf is exact or below what fp32 holds.)
+      const float spread = (a.sigmoid ? 7e-7f : 7.6293945e-6f + 2.3841858e-7f * inv) +
+                           2.3841858e-7f * (fabsf(value_of(m1)) + (pairs ? fabsf(value_of(m2)) : 0.f));
+      const float low = fmaxf(value - spread, -INFINITY), high = value == -INFINITY ? value : value + spread;
+      const uint32_t worst = ~warp_max(in ? ~key_of(low) : 0u), best = warp_max(g < a.groups && !in ? key_of(high) : 0u);
+      if (!(value_of(worst) > value_of(best))) {
         if (!a.sigmoid) return false;
         // each group's two largest in fp64: those that come near its second, one a lane
         const float near = value_of(m2) - 1.5e-6f - 2.5e-7f * fabsf(value_of(m2));
@@ -360,7 +366,7 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
               d2 = other;
           }
         }
-        double sum = a.group_top > 1 && size > 1 ? d1 + d2 : d1;
+        double sum = pairs ? d1 + d2 : d1;
         if (sum != sum) sum = -INFINITY;
         int place = 0;
 #pragma unroll 1

@@ -1,0 +1,75 @@
+"""moe_router_select where fp32 has the order of two values wrong by more than their difference.
+
+float64 computes each c = score + bias within 2^-53 of c and a few 2^-53 of the score: with biases of up
+to 1,000 within 2^-43, a sum of two within 2^-41. All differences that decide something here are above
+2^-38 (2^-48 with biases of up to 1: asserted), so that the ids have to be the oracle's.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import steps
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import paged_expert_moe_gb300 as pm
+    pm.load()
+    return pm
+
+
+def same_ids(pm, x, top_k, scoring, bias, least, **how):
+    """least: what every margin has to be above, or the case says nothing."""
+    x, bias = np.asarray(x, np.float32), np.asarray(bias, np.float32)
+    want, _, margin = steps.router_select(x, top_k, scoring, bias, **how)
+    assert margin.min() > least
+    ids, _ = pm.moe_router_select(torch.from_numpy(x).cuda(), top_k, scoring=scoring, bias=torch.from_numpy(bias).cuda(), **how)
+    assert np.array_equal(ids.cpu().numpy(), want)
+
+
+def test_a_group_whose_two_best_cancel(pm):
+    """fp32 has 1.000061 and 1 for the groups' sums, which are 1.000032 and 1.000044."""
+    s = np.array([[3.2e-5, 0, 2.9e-5, 1.5e-5]])
+    same_ids(pm, 4 * s, 1, "sigmoid", [1000, -1000, 1000, -1000], 1e-6, groups=2, top_groups=1, group_top=2)
+
+
+@pytest.mark.parametrize("scoring,spread", [("sigmoid", 2e-4), ("softmax", 2e-2)])
+@pytest.mark.parametrize("E,groups,top_groups", [(16, 4, 1), (64, 8, 3), (256, 8, 4), (160, 8, 2), (60, 4, 2), (1024, 32, 5)])
+def test_groups_of_large_biases_of_both_signs(pm, scoring, spread, E, groups, top_groups):
+    """Two experts of each group have biases B and -B, the others less: a group's sum is that of two
+    scores, and fp32 has lost up to 2^-15 of each on the way."""
+    rng = np.random.default_rng(E + groups)
+    size = E // groups
+    bias = np.full((groups, size), -3000.0)
+    for g in range(groups):
+        a, b = rng.permutation(size)[:2]
+        bias[g, a] = 2.0 ** rng.uniform(4, 9.95)
+        bias[g, b] = -np.float32(bias[g, a])
+    x = rng.standard_normal((200, E)) * spread
+    same_ids(pm, x, 2 * top_groups, scoring, bias.ravel(), 2.0 ** -38, groups=groups, top_groups=top_groups, group_top=2)
+
+
+@pytest.mark.parametrize("E", [64, 256, 60])
+def test_groups_of_the_lowest_and_infinite_biases(pm, E):
+    """Experts that a bias of the type's lowest value or -inf takes out, with groups of nothing else."""
+    rng = np.random.default_rng(E)
+    lowest = float(np.finfo(np.float32).min)
+    x = rng.standard_normal((50, E)) * 2
+    for out in (lowest, -1e30, -np.inf):
+        bias = rng.standard_normal(E) * 0.1
+        bias.reshape(4, -1)[1] = out      # a group of none
+        bias.reshape(4, -1)[2, 1:] = out  # of one
+        bias[rng.integers(0, E // 4, 5)] = out
+        x32, b32 = x.astype(np.float32), bias.astype(np.float32)
+        for scoring in ("sigmoid", "softmax"):
+            want, _, margin = steps.router_select(x32, 6, scoring, b32, 4, 2, 2)
+            sure = margin > 2.0 ** -48
+            assert sure.mean() > 0.9
+            ids, _ = pm.moe_router_select(torch.from_numpy(x32).cuda(), 6, scoring=scoring, bias=torch.from_numpy(b32).cuda(),
+                                          groups=4, top_groups=2, group_top=2)
+            assert np.array_equal(ids.cpu().numpy()[sure], want[sure])
