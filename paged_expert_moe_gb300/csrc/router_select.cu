@@ -191,6 +191,14 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 constexpr float kLog2e = 1.44269504f;
+// Sum in a tree, so that no term takes more than log2 N roundings.
+template <int I, int N, int M>
+__device__ __forceinline__ float sum_of(const float (&t)[M]) {
+  if constexpr (N == 1)
+    return t[I];
+  else
+    return sum_of<I, N / 2>(t) + sum_of<I + N / 2, N - N / 2>(t);
+}
 
 // N values of a row from element i on; beyond `n` and NaN: -inf. VEC: whole vectors.
 template <int N, bool BF16, bool VEC>
@@ -246,10 +254,10 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
 #pragma unroll
     for (int k = 1; k < N; ++k) top = fmaxf(top, x[k]);
     top = value_of(warp_max(key_of(top)));
-    float sum = 0.f;
+    float term[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (lane * N + k < a.E) sum += x[k] == top ? 1.f : ex2((x[k] - top) * kLog2e);
+    for (int k = 0; k < N; ++k) term[k] = lane * N + k >= a.E ? 0.f : x[k] == top ? 1.f : ex2((x[k] - top) * kLog2e);
+    float sum = sum_of<0, N>(term);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     inv = 1.f / sum;
@@ -258,15 +266,14 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
     if (a.sigmoid) return rcp(1.f + ex2(fmaxf(v, -200.f) * -kLog2e));
     return v == top ? inv : ex2((v - top) * kLog2e) * inv;
   };
-  // What two values of scores s and t, c and d with the bias, may be off by together. Sigmoid: a score 2^-22
-  // (the exponential's argument |x| 2^-23.7 of it and it itself 2^-22, times s (1 - s) <= 1/4 and |x| s (1 - s) <=
-  // 0.23; sum and reciprocal 2^-22.4). Softmax: the sum and its reciprocal 2^-18.8 of a score (up to 32 terms a lane and 5
-  // exchanges, 2^-24 each, and the exponentials), the exponential's argument |x - top| 2^-23.3 of it, of which
-  // |x - top| exp(x - top) <= 0.37. And 2^-24 of c and of d.
-  auto unsure = [&](float c, float s, float d, float u) {
-    const float tol = a.sigmoid ? 7e-7f : 3.8146973e-6f * (s + u) + 2.3841858e-7f * inv;
-    return !(c - d > tol + 1.1920929e-7f * (fabsf(c) + fabsf(d)));
-  };
+  // What a score may be off by, with u = 2^-24. Sigmoid: the exponential 4 u, its argument |x| 1.23 u, of which s (1 - s)
+  // <= 1/4 and |x| s (1 - s) <= 0.23 reach s; sum and reciprocal 3 u: 5 u. Softmax: of the row's sum the terms 4 u, their
+  // arguments 2.23 u times a mean of |x - top|, which is at most log(1024) = 7, and 10 u of adding in a tree; division, own
+  // exponential and product 6 u: 36 u of the score, which is at most the largest one's, inv. It is the row's largest
+  // that counts for all: an expert of a large score may stand among ones of small scores by its bias.
+  const float score_error = a.sigmoid ? 3.5e-7f : 2.2e-6f * inv;
+  // c and d, which two scores are in, may be the other way round (2^-24 of each by its own rounding)
+  auto unsure = [&](float c, float d) { return !(c - d > 2.f * score_error + 1.1920929e-7f * (fabsf(c) + fabsf(d))); };
 
   // ---- what decides: c, or without a bias the logits themselves
   const bool by_logits = a.bias == nullptr, scored = !by_logits || (a.groups > 1 && a.group_top > 1);
@@ -324,11 +331,10 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
     }
     bool in = g < a.groups && rank < a.top_groups;
     if (scored) {
-      // What each value may be off by: two scores, of at most 1 each, and 2^-24 of either c, of their sum and of
+      // What each value may be off by: two scores, and 2^-24 of either c, of their sum and of
       // the bounds. The c of a group may cancel, so the sum says nothing of their own errors. All that is
       // kept has to lie above all that is not. (-inf is exact or below what fp32 holds.)
-      const float spread = (a.sigmoid ? 7e-7f : 7.6293945e-6f + 2.3841858e-7f * inv) +
-                           2.3841858e-7f * (fabsf(value_of(m1)) + (pairs ? fabsf(value_of(m2)) : 0.f));
+      const float spread = 2.f * score_error + 2.3841858e-7f * (fabsf(value_of(m1)) + (pairs ? fabsf(value_of(m2)) : 0.f));
       const float low = fmaxf(value - spread, -INFINITY), high = value == -INFINITY ? value : value + spread;
       const uint32_t worst = ~warp_max(in ? ~key_of(low) : 0u), best = warp_max(g < a.groups && !in ? key_of(high) : 0u);
       if (!(value_of(worst) > value_of(best))) {
@@ -437,10 +443,10 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
   look();
   if (check) {
     // neighbours in the order, the last against the one after it
-    float d = __shfl_down_sync(0xffffffffu, c, 1), u = __shfl_down_sync(0xffffffffu, s, 1);
-    if (lane == 31) d = value_of(last), u = 1.f;  // (of 33; some score)
+    float d = __shfl_down_sync(0xffffffffu, c, 1);
+    if (lane == 31) d = value_of(last);  // (of 33)
     const bool pair = lane + 1 < a.top_k || (lane + 1 == a.top_k && last != 0);
-    if (__any_sync(0xffffffffu, pair && unsure(c, s, d, u))) {
+    if (__any_sync(0xffffffffu, pair && unsure(c, d))) {
       if (!a.sigmoid || a.top_k > 30) return false;
       // the list in fp64, and with it all that come near its end; one a lane, sorted by rank
       float end = __shfl_sync(0xffffffffu, c, a.top_k - 1);

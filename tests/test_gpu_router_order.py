@@ -73,3 +73,25 @@ def test_groups_of_the_lowest_and_infinite_biases(pm, E):
             ids, _ = pm.moe_router_select(torch.from_numpy(x32).cuda(), 6, scoring=scoring, bias=torch.from_numpy(b32).cuda(),
                                           groups=4, top_groups=2, group_top=2)
             assert np.array_equal(ids.cpu().numpy()[sure], want[sure])
+
+
+@pytest.mark.parametrize("top_k", [1, 3, 8])
+@pytest.mark.parametrize("E,at", [(512, 256), (512, 0), (1024, 512), (1024, 992), (256, 128), (1000, 640)])
+def test_an_expert_of_a_large_score_and_a_negative_bias(pm, E, at, top_k):
+    """Softmax rows with nearly all of the sum at one expert, whose own c is off by more in fp32 than the c of
+    the experts of small scores around it: it is told apart from each of them, not from its neighbours alone."""
+    low = np.float32(-11.2463)  # its exponential is 109.5 times 2^-23: added to 1, each one is off by half of that
+    x = np.full((3, E), low)
+    x[:, at] = 0
+    e = np.exp(x[0].astype(np.float64))
+    score = e / e.sum()
+    first, second = (2, 1) if at == 0 else (1, E - 1)
+    for gap in (3e-7, 5e-7, 7e-7, 1e-6, 2e-6):
+        for ahead in (2e-7, 5e-7, 8e-7, -2e-7, -5e-7, -8e-7):
+            bias = np.full(E, -1.0)
+            others = [i for i in range(3, 200) if i not in (at, first, second)][:top_k - 1]
+            bias[others] = np.linspace(1, 0.5, len(others))
+            bias[first] = 0.01
+            bias[second] = 0.01 - gap
+            bias[at] = np.float32(0.01) + score[first] + ahead - score[at]
+            same_ids(pm, x, top_k, "softmax", bias, 2.0 ** -48)
