@@ -620,8 +620,9 @@ typedef enum { PMOE_SCORE_SOFTMAX = 0, PMOE_SCORE_SIGMOID = 1 } pmoe_scoring;
  * to the lower group. In them the top_k largest c are selected, ordered by descending c, ties to the
  * lower id. The order is that of c in exact arithmetic, as far as fp64 tells (without a bias: of the
  * logits). w = s of the selected, divided by their sum when renormalize != 0 (0 where that is 0), times
- * `scale`. A NaN logit counts as -inf, a NaN bias as -inf; of softmax rows with logits of +inf, or with
- * none above -inf, the largest share the row.
+ * `scale`: within 2^-18 of its value where s is 2^-126 or more. A NaN logit counts as -inf, a NaN
+ * bias as -inf; of softmax rows with logits of +inf, or with none above -inf, the largest share the
+ * row.
  *   logits   device, fp32 (is_bf16 = 0) or bf16 [T][E], rows row_stride elements apart; aligned to
  *            its element
  *   bias     device fp32 [E], or NULL

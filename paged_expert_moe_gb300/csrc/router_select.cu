@@ -266,6 +266,16 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
     if (a.sigmoid) return rcp(1.f + ex2(fmaxf(v, -200.f) * -kLog2e));
     return v == top ? inv : ex2((v - top) * kLog2e) * inv;
   };
+  // The same for the weights, to within a few units in the last place of the exponential (and the sum's error):
+  // `score` is off by 2^-23 |argument| of itself, 2^-17 where all logits of a row's choice are as low as -60.
+  auto fine_score = [&](float v) {
+    if (a.sigmoid) return __fdividef(1.f, 1.f + expf(-v));
+    if (v == top) return inv;
+    const float d = v - top, back = d - v, rest = (v - (d - back)) - (top + back);  // v - top = d + rest
+    if (!(d > -104.f)) return 0.f;
+    const float e = expf(d);
+    return fmaf(e, rest, e) * inv;
+  };
   // What a score may be off by, with u = 2^-24. Sigmoid: the exponential 4 u, its argument |x| 1.23 u, of which s (1 - s)
   // <= 1/4 and |x| s (1 - s) <= 0.23 reach s; sum and reciprocal 3 u: 5 u. Softmax: of the row's sum the terms 4 u, their
   // arguments 2.23 u times a mean of |x - top|, which is at most log(1024) = 7, and 10 u of adding in a tree; division, own
@@ -437,7 +447,7 @@ __device__ __forceinline__ bool select_token(const SelectArgs& a, int t, const f
       const bool hit = keys[k] == mine.x;
       if (hit && skip-- == 0) id = mine.y * N + k;
     }
-    s = mine.x != 0 ? score(logit<BF16>(a, row, id)) : 0.f;
+    s = mine.x != 0 ? fine_score(logit<BF16>(a, row, id)) : 0.f;
     c = value_of(mine.x);
   };
   look();
