@@ -582,7 +582,8 @@ PMOE_API int moe_batch_tables(int32_t* page_table, int table_stride, int page_si
  * holds in rows that a query does not see is never used, whatever it is; rows outside all requests
  * are left as they were in out and lse, and what q holds there is not used.
  * Statistics and sums are fp32; the weights are rounded to 16 bits before they meet the
- * values (bf16, or fp16 with an e4m3 cache).
+ * values (bf16, or fp16 with an e4m3 cache: by at most 2^-11 of a weight or 2^-32 of the row's
+ * largest, whichever is more).
  *   q            device bf16 [T][q_heads][head_dim], tokens q_stride elements apart; 16-byte
  *                aligned, q_stride a multiple of 8
  *   q_start      device int32 [R + 1], ascending, in [0, T]

@@ -28,7 +28,7 @@
 // such item at a time; 64 with e4m3 186 us, with heads of 64 and 40 / 8 of them 199 us (5.3 TB/s), with
 // both 267 us. Few calls' worth of work: start and end, 17 us for four tokens on up to 2,000 keys.
 // Sixteen bits for the weights, as the second product takes them: at most half a unit of bf16's or fp16's last
-// place each, while their sum and the products' stay fp32.
+// place each, or with fp16 2^-32 of the row's largest, while their sum and the products' stay fp32.
 #include "chunk.cuh"
 #include "tc_gemm.h"
 
@@ -237,6 +237,11 @@ struct Cfg {
   // has no registers left for it, and not with heads of 128 (189 / 172), whose ring is too short.
   static constexpr bool kAhead = D == 64 && !F8;
   static constexpr int kGuards = F8 ? 4 : 2;              // warps that look at partly visible values
+  // The base of the weights' exponents lies so far below the largest score, which may outgrow it by 8 more before
+  // the base moves. So fp16 weights reach 2^15 at most and the largest one is 2^7 or more: the rounding to fp16's smallest
+  // step, 2^-24, is by 2^-32 of the largest at most. (With the base at the largest score it was 2^-25, and a million
+  // keys of 2^-25.5 each were lost while the weights' sum held them.) bf16 has fp32's range.
+  static constexpr float kLift = F8 ? 7.f : 0.f;
 };
 
 constexpr int kSegs = 8;
@@ -520,6 +525,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
     uint32_t n = 0, other = 0;  // its tiles with the scores in its place, in the other's
     uint32_t tiles = 0;        // key tiles so far
     bool ok = true;
+    auto lifted = [](float top) {  // the base for a largest score
+      if constexpr (F8) return top - C::kLift;
+      return top;
+    };
     for (uint32_t all = 0; ok && get_segment(b, all, &sg, abort_flag, a.err); tiles += sg.t1 - sg.t0, ++all) {
       if (!sg.has(q)) continue;
       const bool ahead = C::kAhead && !sg.two();
@@ -584,9 +593,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
         for (int c = 0; c < 128; c += 2) x[(c >> 1) & 3] = max3(x[(c >> 1) & 3], s[c], s[c + 1]);
         const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * mul;
         if (t == sg.t0) {
-          m = mx;
+          m = lifted(mx);
         } else {
-          const bool grow = mx > m + 8.f;
+          const bool grow = mx > m + (8.f + C::kLift);
           if (__any_sync(0xffffffffu, grow)) {
             // the products so far are done: these scores were issued after them, or the last one's values are
             // released
@@ -598,8 +607,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::kThreads, 1)
               }
               fence_after();
             }
-            const float f = grow ? ex2(m - mx) : 1.f;
-            if (grow) m = mx;
+            const float f = grow ? ex2(m - lifted(mx)) : 1.f;
+            if (grow) m = lifted(mx);
             l *= f;
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
