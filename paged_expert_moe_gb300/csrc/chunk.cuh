@@ -2,6 +2,7 @@
 #pragma once
 
 #include "attn_tc.cuh"
+#include "runs.h"
 
 namespace pmoe {
 namespace chunk {
@@ -45,21 +46,9 @@ __device__ __forceinline__ bool any_sees(const Args& a, int p0, int p1, int j) {
 __device__ __forceinline__ bool all_see(const Args& a, int p0, int p1, int j) {
   return j <= p0 && (a.window == 0 || j > p1 - a.window || j < a.sinks);
 }
-// The first unit of CTA c's run. (A 64-bit division takes some 500 cycles, one of 32 bits a tenth.)
-__device__ __forceinline__ int64_t run_start(int64_t units, int ctas, int c) {
-  const int64_t x = units * c;
-  return x >> 32 ? x / ctas : (int64_t)((uint32_t)x / (uint32_t)ctas);
-}
-
 // r / group for r < 2^24 and group <= 64
 __device__ __forceinline__ int row_token(const Args& a, int r) {
   return a.group == 1 ? r : (int)__umulhi((uint32_t)r, a.group_magic);
-}
-
-// The CTA that takes unit u: the largest c with run_start(c) <= u.
-__device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) {
-  const int64_t x = (u + 1) * ctas - 1;  // (of at least units)
-  return x >> 32 ? (int)(x / units) : (int)((uint32_t)x / (uint32_t)units);
 }
 
 // Cutting an item costs a part and a join, some four tiles of few rows and more of many. So where runs are
