@@ -101,10 +101,29 @@ class Server:
                 self.routes.append((ids, w))
         return x
 
+    def check(self, r):
+        """Refuses what would index beyond the model's tensors or the server's buffers."""
+        def refuse(what):
+            raise AssertionError(f"request: {what}")
+
+        if not r.prompt or r.tokens < 1 or r.output:
+            refuse("a prompt, at least one token to generate and no output so far are needed")
+        if len(r.prompt) + r.tokens > self.longest:
+            refuse(f"{len(r.prompt)} + {r.tokens} tokens, {self.longest} at most")
+        if len(r.biases) > self.max_biases:
+            refuse(f"{len(r.biases)} biases, {self.max_biases} at most")
+        if r.allowed is not None and len(r.allowed) == 0:
+            refuse("no token is allowed")
+        for name, ids in (("prompt", r.prompt), ("biases", r.biases), ("allowed", () if r.allowed is None else r.allowed)):
+            for v in ids:
+                if not 0 <= v < self.shape.vocab:
+                    refuse(f"{name}: token {v} of {self.shape.vocab}")
+
     def plan(self, waiting):
         """Seats requests, and gives each seat its tokens of this step: (seat, token ids)."""
         for seat in range(self.seats):
             if self.seated[seat] is None and seat not in self.ended and waiting:
+                self.check(waiting[0])
                 self.seated[seat], self.read[seat] = waiting.pop(0), 0
         room, work = self.rows, {}
         # generating requests first, one token each; then pieces of prompts
@@ -157,6 +176,8 @@ class Server:
                                        top_p=full(top_p, torch.float32)).tolist()
             for seat, token in zip(draws, ids):
                 r = self.seated[seat]
+                if token < 0:
+                    raise RuntimeError(f"seat {seat}: no token's logit is above -inf")
                 r.output.append(token)
                 if r.done():
                     self.seated[seat] = None
@@ -194,7 +215,7 @@ class Server:
     def run(self, requests, **how):
         """Serves the requests; their outputs are filled in. Returns the number of steps."""
         for r in requests:
-            assert r.prompt and r.tokens > 0 and len(r.prompt) + r.tokens <= self.longest and len(r.biases) <= self.max_biases
+            self.check(r)
         waiting, steps = list(requests), 0
         while self.step(waiting, **how):
             steps += 1
