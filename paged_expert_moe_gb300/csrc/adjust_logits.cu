@@ -8,7 +8,8 @@
 // Bound: HBM, the logits read and written once, and the history's counting, in which a CTA waits for its
 // atomics. The first logits and mask words are on their way meanwhile. 256 fp32 rows of 160,001 with 2,000 ids of
 // history at most 70 us (50 without; a plain copy 56), 64 bf16 rows of 131,072 to fp32 with 4,000 20 us (10
-// without; a copy 17, cold caches 27), one row 3.5 us.
+// without; a copy 17, cold caches 27), one row 3.5 us. In place 62, 23 (a four that changes is read and written where it
+// lies, after its counts are known, so nothing is on its way before) and 3.5 us.
 #include "pmoe_internal.h"
 
 #include <math.h>
@@ -252,7 +253,7 @@ extern "C" int moe_adjust_logits(const void* logits, int is_bf16, int T, int V, 
   AdjustArgs a{logits,    out,        row_stride, out_stride, T,      V,    in_place, history, history_stride, max_history,
                prompt_len, history_len, repetition, frequency,  presence, bias_ids, bias,     biases,  mask,           mask_stride,
                err_out,   0,          0};
-  // Each slice looks at its row's whole history, so they are as large as leaves every SM its share, and no
+  // Each slice looks at its row's whole history, so they are as large as leaves every SM (of 152) its share, and no
   // larger than two turns of the logits in flight: 256 rows of 160,001 in slices of 16,384, 8,192, 4,096 89, 76, 97 us.
   a.slice = kMaxSlice;
   while (a.slice > 1024 && (int64_t)T * ((V + a.slice - 1) / a.slice) < 152 * kPerSM) a.slice /= 2;

@@ -19,14 +19,15 @@
 // warps 12-15, which convert keys, values and q to fp16, do. What was cleared is added to the rows that
 // do see it at the end.
 //
-// Bounds, and what it measures (heads 32 / 4 x 128, bf16, a GPU of 152 SMs). Prompts: the tensor cores.
-// 8,192 tokens 380 us (1,450 TFLOP/s; 1,920 is what a library product reaches), 4,096 tokens on 60,001
-// keys 2.5-2.7 ms by power (1,530-1,650). The issuing warp is what they wait for: it sees keys, values and weights
-// in one look, and its inner loop holds nothing but tiles that all rows see. Many single tokens: HBM; 64
-// on up to 16,000 keys 172 us (6.0 TB/s), 256 with a window of 4,096 314 us (6.1 TB/s). Single tokens with
-// an 8-bit cache or heads of 64: the chain of a tile (scores, softmax, products), as one CTA an SM has one
-// such item at a time; 64 with e4m3 186 us, with heads of 64 and 40 / 8 of them 199 us (5.3 TB/s), with
-// both 267 us. Few calls' worth of work: start and end, 17 us for four tokens on up to 2,000 keys.
+// Bounds, and what it measures (heads 32 / 4 x 128, bf16, a GPU of 152 SMs; in a loop, pages of 64, but where said).
+// Prompts: the tensor cores. 8,192 tokens 380 us (1,450 TFLOP/s; 1,920 is what a library product reaches), in pages of
+// 16 404, and 418-425 with cold caches; 4,096 tokens on 60,001 keys 2.5-2.7 ms by power (1,530-1,650), cold 2.8-2.9. The
+// issuing warp is what they wait for: it sees keys, values and weights in one look, and its inner loop holds nothing but tiles that
+// all rows see. Many single tokens: HBM; 64 on up to 16,000 keys 172 us (6.0 TB/s), 256 with a window of 4,096 314 us
+// (6.1 TB/s). Single tokens with an 8-bit cache or heads of 64: the chain of a tile (scores, softmax, products), as one CTA
+// an SM has one such item at a time; 64 with e4m3 187 us, with heads of 64 and 40 / 8 of them 204 us (5.1 TB/s), with both
+// 267 us. Few calls' worth of work: start and end, 18 us for four tokens on up to 2,000 keys. A negative scale (or key
+// scale) takes every tile through the masks' pass in TMEM: a prompt of 8,192 tokens 516 us, with e4m3 626 (465), 64 single tokens 217.
 // Sixteen bits for the weights, as the second product takes them: at most half a unit of bf16's or fp16's last
 // place each, or with fp16 2^-32 of the row's largest, while their sum and the products' stay fp32.
 #include "chunk.cuh"

@@ -9,8 +9,10 @@
 // apart lie closer than that, the token is done again in fp64. Where there is no bias the order is
 // the logits' own.
 //
-// Bound: issue slots, 0.65 of them in use: 16,384 tokens of 256 experts in 8 groups 21.8 us (their logits take
-// 2.7 us to read), 4 tokens 3.4 us. A warp a token, lane l with the logits l N .. l N + N - 1, so that a group of whole
+// Bound: issue slots, 0.65 of them in use: 16,384 tokens of 256 experts in 8 groups 21.9 us (sigmoid and bias, 852 instructions a
+// token; their logits take 2.7 us to read), 4 tokens 3.4 us. Softmax with a bias 51 us, 56 with the groups: one token in some
+// hundreds is done in fp64, which takes 30 us. Where many c are equal, as with bf16 logits and no other bias than 0, every third token
+// is: sigmoid 34 us, softmax 304 to 324. A warp a token, lane l with the logits l N .. l N + N - 1, so that a group of whole
 // lanes is compared by shuffles, that of equal values the lowest lane's is the lowest id's, and a row is read
 // in whole vectors; the bias stays in registers from token to token. The largest value of the warp is an
 // integer maximum over keys that order like the floats.
@@ -160,7 +162,7 @@ __device__ __forceinline__ double exact_choice(const SelectArgs& a, int64_t row,
 
 // Batcher's odd-even merge sort: runs of P are merged, first by comparisons K apart. (By templates: nested
 // loops are not unrolled for 16 values and more, and the keys then lie in local memory: 16,384 tokens of 512 experts
-// 53.8 us, so 44.6.)
+// 53.8 us, so 44.6; with the sums in a tree 32.8.)
 template <int N, int P, int K>
 __device__ __forceinline__ void merge_descending(uint32_t (&v)[N]) {
 #pragma unroll
@@ -521,14 +523,15 @@ int launch_one(SelectArgs a, cudaStream_t s) {
   while (a.lanes > 0 ? 1 << a.shift < a.lanes : a.groups << (a.shift + 1) <= 32) ++a.shift;
   const auto kernel = select_kernel<N, BF16, VEC>;
   const int r = limit.set(reinterpret_cast<const void*>(kernel), kWarps * N * 32 * 8, what);
-  // one wave of blocks: four an SM by registers, two with 16 keys a lane (512 experts 41.6 us, 44.6 with four)
+  // one wave of blocks on the GB300's 152 SMs: four an SM by registers, two with 16 keys a lane (16,384 tokens of 512
+  // experts 32.8 us, 35.6 with four)
   const unsigned blocks = (unsigned)std::min((a.T + kWarps - 1) / kWarps, 152 * (N < 16 ? 4 : 2));
   return r != PMOE_OK ? r : launch(what, kernel, blocks, kWarps * 32, kWarps * N * 32 * 8, s, true, 1, a);
 }
 
-// A lane takes 2^n experts, or where E is 32 times another number that many: fewer keys to sort, and of 160 experts in
-// 8 groups four lanes hold a group, while of 8 a lane no whole ones do. 16,384 tokens, so and with 2^n: 160 experts 20.9 and
-// 30.5 us, 192 17.6 and 20.1, 384 24.4 and 56.5.
+// A lane takes 2^n experts; of 96, 160, 192 and 384 experts, in rows that are aligned for it, exactly E / 32: fewer keys to
+// sort, and of 160 experts in 8 groups four lanes hold a group, while of 8 a lane no whole ones do. 16,384 tokens, so and with
+// 2^n: 96 experts 15.2 and 16.3 us, 160 21.2 and 29.3, 192 18.2 and 18.3, 384 20.5 and 33.4. Other multiples of 32 take 2^n.
 template <bool BF16>
 int launch_select(SelectArgs a, cudaStream_t s) {
   if (reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * (BF16 ? 2 : 4) % 16 == 0) {
