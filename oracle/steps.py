@@ -103,7 +103,7 @@ def router_select(logits, top_k, scoring, bias=None, groups=1, top_groups=1, gro
         alive = list(range(E))
         if groups > 1 and top_groups < groups:
             size = E // groups
-            best = order if bias is None and group_top == 1 else c
+            best = order if bias is None and min(group_top, size) == 1 else c  # (a sum needs the scores)
             value = [sum(sorted(best[g * size:(g + 1) * size], reverse=True)[:group_top]) for g in range(groups)]
             rank = sorted(range(groups), key=lambda g: (-value[g], g))
             margin[t] = min(margin[t], value[rank[top_groups - 1]] - value[rank[top_groups]])

@@ -575,6 +575,6 @@ extern "C" int moe_router_select(const void* logits, int is_bf16, int T, int E, 
   if (off(logits, is_bf16 ? 2 : 4) || (bias != nullptr && off(bias, 4)) || off(ids_out, 4) || off(w_out, 4)) return PMOE_EINVAL;
   const bool grouped = groups > 1 && top_groups < groups;  // all groups kept: no choice among them
   const SelectArgs a{logits, row_stride, T, E, top_k, scoring == PMOE_SCORE_SIGMOID, bias, grouped ? groups : 1,
-                     grouped ? top_groups : 1, group_top, renormalize != 0, scale, ids_out, w_out, 0, 0, 0};
+                     grouped ? top_groups : 1, E / groups > 1 ? group_top : 1, renormalize != 0, scale, ids_out, w_out, 0, 0, 0};
   return is_bf16 ? launch_select<true>(a, (cudaStream_t)stream) : launch_select<false>(a, (cudaStream_t)stream);
 }

@@ -95,3 +95,12 @@ def test_an_expert_of_a_large_score_and_a_negative_bias(pm, E, at, top_k):
             bias[second] = 0.01 - gap
             bias[at] = np.float32(0.01) + score[first] + ahead - score[at]
             same_ids(pm, x, top_k, "softmax", bias, 2.0 ** -48)
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_groups_of_one_expert_whose_scores_are_equal_in_64_bits(pm, group_top):
+    """Without a bias the logits decide, also where a group's value is a single score: 1 for 45 as for 50."""
+    x = torch.tensor([[0.0, 45.0, 50.0, 48.0, -3.0, 60.0, 47.0, 44.0]], device="cuda")
+    ids, _ = pm.moe_router_select(x, 2, scoring="sigmoid", groups=8, top_groups=3, group_top=group_top)
+    assert ids.tolist() == [[5, 2]]
+    assert steps.router_select(x.cpu().numpy(), 2, "sigmoid", None, 8, 3, group_top)[0].tolist() == [[5, 2]]
