@@ -46,6 +46,7 @@ __device__ __forceinline__ bool any_sees(const Args& a, int p0, int p1, int j) {
 __device__ __forceinline__ bool all_see(const Args& a, int p0, int p1, int j) {
   return j <= p0 && (a.window == 0 || j > p1 - a.window || j < a.sinks);
 }
+
 // r / group for r < 2^24 and group <= 64
 __device__ __forceinline__ int row_token(const Args& a, int r) {
   return a.group == 1 ? r : (int)__umulhi((uint32_t)r, a.group_magic);

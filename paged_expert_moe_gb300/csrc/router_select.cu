@@ -10,8 +10,8 @@
 // the logits' own.
 //
 // Bound: issue slots, 0.65 of them in use: 16,384 tokens of 256 experts in 8 groups 21.9 us (sigmoid and bias, 852 instructions a
-// token; their logits take 2.7 us to read), 4 tokens 3.4 us. Softmax with a bias 51 us, 56 with the groups: one token in some
-// hundreds is done in fp64, which takes 30 us. Where many c are equal, as with bf16 logits and no other bias than 0, every third token
+// token; their logits take 2.7 us to read), 4 tokens 3.4 us. Softmax with a bias 51 us, 56 with the groups: one token in a
+// thousand is done in fp64, which takes 30 us. Where many c are equal, as with bf16 logits and no other bias than 0, every third token
 // is: sigmoid 34 us, softmax 304 to 324. A warp a token, lane l with the logits l N .. l N + N - 1, so that a group of whole
 // lanes is compared by shuffles, that of equal values the lowest lane's is the lowest id's, and a row is read
 // in whole vectors; the bias stays in registers from token to token. The largest value of the warp is an
